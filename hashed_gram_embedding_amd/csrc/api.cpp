@@ -312,7 +312,7 @@ size_t forward_ws_bytes(int64_t n_tok, const engram_layer* L) {
 }
 
 // Steps 6-8 once the gate statistics are in `stats`: conv (+ residual), then
-// the decode-state commit.
+// the decode-state commit (commit = false: st is only read).
 // next: a hashed gather of another batch to run with this conv (in the same
 // launch where a fused form exists, else right after it), or null.
 engram_status run_conv_commit(void* H, const void* v, int64_t v_stride, int vdtype, const float4* stats, int qv,
@@ -320,7 +320,7 @@ engram_status run_conv_commit(void* H, const void* v, int64_t v_stride, int vdty
                               const int32_t* tokens, const int32_t* proj, int32_t max_n, int32_t vocab,
                               float* alpha_out, float* gamma, float* y_out, hipStream_t s,
                               const engram::GatherJob* next = nullptr,
-                              bool state_folded = false) {
+                              bool state_folded = false, bool commit = true) {
   engram::ConvArgs ca{};
   ca.H = H;
   ca.v = v;
@@ -365,7 +365,7 @@ engram_status run_conv_commit(void* H, const void* v, int64_t v_stride, int vdty
       if (r != ENGRAM_OK) return r;
     }
   }
-  if (st != nullptr && !state_folded) {
+  if (st != nullptr && !state_folded && commit) {
     engram::StateArgs sa{tokens != nullptr ? st->ids : nullptr, st->conv, st->pos};
     prof_mark(s, "state_commit_kernel");
     r = hip_status(engram::launch_state_commit(v, v_stride, vdtype, B, T, g, gamma, sa, tokens, proj, max_n, vocab,
@@ -579,17 +579,60 @@ engram_status run_retrieve(const int32_t* tokens, int64_t B, int64_t T, const en
                     "hash+gather launch");
 }
 
-// Steps 5-8 on gathered rows e.
+// The 8-bit integer product; float rows are quantised into codes / scale first.
+engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, const int8_t* w, const float* w_scale,
+                             int64_t n_tok, int64_t d_mem, int64_t n_out, int out_dtype, void* out, int8_t* codes,
+                             float* scale, hipStream_t stream) {
+  const int8_t* q = static_cast<const int8_t*>(e);
+  int64_t ldq = d_mem;
+  const bool tailed = e_dtype != ENGRAM_I8;
+  if (tailed) {
+    ldq = engram::i8_row_stride(d_mem);
+    prof_mark(stream, "quantize_i8_kernel");
+    const engram_status r = hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, codes, ldq, true, scale, stream),
+                                       "quantize_i8 launch");
+    if (r != ENGRAM_OK) return r;
+    q = codes;
+    e_scale = scale;
+  }
+  prof_mark(stream, "project_i8_kernel");
+  return hip_status(engram::launch_project_i8(q, ldq, tailed, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out,
+                                              stream),
+                    "project_i8 launch");
+}
+
+// Codes and scales of quantised rows in a workspace.
+struct CodeSpace {
+  int8_t* codes;
+  float* scale;
+};
+
+CodeSpace carve_codes(Carve& c, int64_t n_tok, int64_t d_mem) {
+  CodeSpace s;
+  s.codes = c.take<int8_t>(static_cast<size_t>(n_tok) * engram::i8_row_stride(d_mem));
+  s.scale = c.take<float>(static_cast<size_t>(n_tok));
+  return s;
+}
+
+// Step 5 in 8-bit integers: W and where the gathered rows' codes go.
+struct Int8Step {
+  const engram_i8_weights* w;
+  int8_t* codes;
+  float* scale;
+};
+
+// Steps 5-8 on gathered rows e.  i8: Step 5 as the 8-bit integer product, or
+// null.  commit = false leaves st as it is.
 engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t B, int64_t T,
                           const engram_layer* L, engram::GateConvArgs g, engram_decode_state* st,
                           float* alpha_out, float* y_out, const ComputeWorkspace& f, hipStream_t stream,
-                          const engram::GatherJob* next = nullptr) {
+                          const engram::GatherJob* next = nullptr, const Int8Step* i8 = nullptr, bool commit = true) {
   const int64_t n_tok = B * T;
   const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim;
   const int M = g.branches, d = g.d;
   const int64_t n_out = static_cast<int64_t>(1 + M) * d;
   engram_status r;
-  if (use_fused(L)) {
+  if (i8 == nullptr && use_fused(L)) {
     // Step 5 with the gate's sums folded into the product's epilogue; only v is stored
     engram::ProjGateArgs pa{};
     const bool mx = L->w_mx != nullptr;
@@ -613,7 +656,7 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
     // Decode step (T = 1, the strip conv): the state's ids and pos advance in
     // this launch and the conv writes the new ring row, so no commit kernel
     bool fold = false;
-    if (st != nullptr && T == 1 && tokens != nullptr && st->ids != nullptr) {
+    if (commit && st != nullptr && T == 1 && tokens != nullptr && st->ids != nullptr) {
       engram::ConvArgs probe{};
       probe.g = g;
       probe.qv = pl.qv;
@@ -638,19 +681,25 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
     r = hip_status(engram::launch_proj_gate(pa, stream), "projection launch");
     if (r != ENGRAM_OK) return r;
     return run_conv_commit(H, f.kv, d, ENGRAM_F32, f.stats, pl.qv, pl.qk, pl.mixed, B, T, g, st, tokens, L->hash.proj,
-                           L->hash.max_n, static_cast<int32_t>(L->hash.vocab), alpha_out, f.gamma, y_out, stream, next, fold);
+                           L->hash.max_n, static_cast<int32_t>(L->hash.vocab), alpha_out, f.gamma, y_out, stream, next, fold,
+                           commit);
   }
   // Step 5 into float32 projections, then whole-row gate statistics
-  prof_mark(stream, "gemm_kernel");
-  r = hip_status(engram::launch_project_kv(e, L->w, n_tok, d_mem, n_out, g.hdtype, ENGRAM_F32, f.kv, stream),
-                 "project_kv launch");
+  if (i8 != nullptr) {
+    r = run_project_i8(e, g.hdtype, nullptr, i8->w->w, i8->w->scale, n_tok, d_mem, n_out, ENGRAM_F32, f.kv, i8->codes,
+                       i8->scale, stream);
+  } else {
+    prof_mark(stream, "gemm_kernel");
+    r = hip_status(engram::launch_project_kv(e, L->w, n_tok, d_mem, n_out, g.hdtype, ENGRAM_F32, f.kv, stream),
+                   "project_kv launch");
+  }
   if (r != ENGRAM_OK) return r;
   g.kvdtype = ENGRAM_F32;
   prof_mark(stream, "gate_stats_kernel");
   r = hip_status(engram::launch_gate_stats(H, f.kv, n_tok, g, f.stats, stream), "gate statistics launch");
   if (r != ENGRAM_OK) return r;
   return run_conv_commit(H, f.kv, n_out, ENGRAM_F32, f.stats, 1, 1, false, B, T, g, st, tokens, L->hash.proj,
-                         L->hash.max_n, static_cast<int32_t>(L->hash.vocab), alpha_out, f.gamma, y_out, stream, next);
+                         L->hash.max_n, static_cast<int32_t>(L->hash.vocab), alpha_out, f.gamma, y_out, stream, next, false, commit);
 }
 
 }  // namespace
@@ -1193,6 +1242,268 @@ ENGRAM_API engram_status engram_cache_update(const engram_tables* tab, int64_t c
                                                 tab->dtype == ENGRAM_I8 ? cache_scale : nullptr, counts, decay_shift,
                                                 ws, stream),
                     "cache update launch");
+}
+
+ENGRAM_API engram_status engram_quantize_i8(const void* x, engram_dtype dtype, int64_t rows, int64_t cols, int8_t* q,
+                                            float* scale, hipStream_t stream) {
+  if (dtype != ENGRAM_F32 && dtype != ENGRAM_BF16)
+    return fail(ENGRAM_EUNSUPPORTED, "quantize_i8: dtype must be F32 or BF16");
+  if (rows < 0 || cols < 1) return fail(ENGRAM_EINVAL, "quantize_i8: need rows >= 0 and cols >= 1");
+  if (rows > INT32_MAX || cols > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "quantize_i8: rows and cols must be below 2^31");
+  if (rows == 0) return ENGRAM_OK;
+  if (x == nullptr || q == nullptr || scale == nullptr)
+    return fail(ENGRAM_EINVAL, "quantize_i8: x, q and scale must be non-NULL");
+  if (!aligned(x, dtype_size(dtype)) || !aligned(scale, 4))
+    return fail(ENGRAM_EINVAL, "quantize_i8: x and scale must be aligned to their elements");
+  prof_begin();
+  prof_mark(stream, "quantize_i8_kernel");
+  return hip_status(engram::launch_quantize_i8(x, dtype, rows, cols, q, cols, false, scale, stream), "quantize_i8 launch");
+}
+
+ENGRAM_API size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, engram_dtype e_dtype) {
+  if (n_tok < 1 || d_mem < 1 || e_dtype == ENGRAM_I8) return 0;
+  Carve c{nullptr};
+  carve_codes(c, n_tok, d_mem);
+  return c.used;
+}
+
+ENGRAM_API engram_status engram_project_i8(const void* e, engram_dtype e_dtype, const float* e_scale, const int8_t* w,
+                                           const float* w_scale, int64_t n_tok, int64_t d_mem, int64_t n_out,
+                                           engram_dtype out_dtype, void* out, void* ws, size_t ws_bytes,
+                                           hipStream_t stream) {
+  if (e_dtype != ENGRAM_F32 && e_dtype != ENGRAM_BF16 && e_dtype != ENGRAM_I8)
+    return fail(ENGRAM_EUNSUPPORTED, "project_i8: e_dtype must be F32, BF16 or I8");
+  if (out_dtype != ENGRAM_F32 && out_dtype != ENGRAM_BF16)
+    return fail(ENGRAM_EUNSUPPORTED, "project_i8: out_dtype must be F32 or BF16");
+  if (n_tok < 0 || d_mem < 1 || n_out < 1)
+    return fail(ENGRAM_EINVAL, "project_i8: need n_tok >= 0, d_mem >= 1, n_out >= 1");
+  if (d_mem > 131071) return fail(ENGRAM_EUNSUPPORTED, "project_i8: d_mem above 131071 could leave the int32 sum");
+  if (n_tok > INT32_MAX || n_out > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "project_i8: n_tok and n_out must be below 2^31");
+  if (n_tok == 0) return ENGRAM_OK;
+  if (e == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
+    return fail(ENGRAM_EINVAL, "project_i8: e, w, w_scale and out must be non-NULL");
+  if ((e_dtype == ENGRAM_I8) != (e_scale != nullptr))
+    return fail(ENGRAM_EINVAL, "project_i8: e_scale goes with int8 codes, and only with them");
+  if (!aligned(e, dtype_size(e_dtype)) || !aligned(out, dtype_size(out_dtype)) || !aligned(e_scale, 4) || !aligned(w_scale, 4))
+    return fail(ENGRAM_EINVAL, "project_i8: e, out and the scales must be aligned to their elements");
+  const size_t need = engram_project_i8_workspace(n_tok, d_mem, e_dtype);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
+    return fail(ENGRAM_EINVAL, "project_i8: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  CodeSpace cs{};
+  if (need > 0) {
+    Carve c{static_cast<char*>(ws)};
+    cs = carve_codes(c, n_tok, d_mem);
+  }
+  prof_begin();
+  const engram_status r = run_project_i8(e, e_dtype, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out, cs.codes,
+                                         cs.scale, stream);
+  prof_mark(stream, nullptr);
+  return r;
+}
+
+namespace {
+
+// Workspace of a layer call with Step 5 in 8-bit integers or over a draft
+// (then v and gamma are the caller's): rows, projections, statistics, codes.
+struct DraftWorkspace {
+  void* e;
+  ComputeWorkspace f;
+  CodeSpace codes;
+};
+
+DraftWorkspace carve_draft(Carve& c, int64_t n_tok, const engram_layer* L, bool i8, bool own_v) {
+  const int M = L->gc.branches, d = L->gc.d;
+  DraftWorkspace w{};
+  w.e = c.take<char>(rows_bytes(n_tok, L));
+  if (own_v && !i8) {
+    w.f = carve_compute(c, n_tok, L);
+  } else {
+    const bool fused = !i8 && use_fused(L);
+    if (own_v) w.f.kv = c.take<float>(static_cast<size_t>(n_tok) * (1 + M) * d);
+    w.f.stats = c.take<float4>(fused ? static_cast<size_t>(n_tok) * (1 + M) * d / engram::kProjGateTileF
+                                     : static_cast<size_t>(n_tok) * (1 + M));
+    if (own_v) w.f.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
+  }
+  if (i8) w.codes = carve_codes(c, n_tok, static_cast<int64_t>(L->tables.n_tables) * L->tables.dim);
+  return w;
+}
+
+size_t draft_ws_bytes(int64_t B, int64_t T, const engram_layer* L, bool i8, bool own_v) {
+  if (L == nullptr || B < 0 || T < 0 || L->gc.branches < 1 || L->tables.n_tables < 1) return 0;
+  Carve c{nullptr};
+  carve_draft(c, B * T, L, i8, own_v);
+  return c.used;
+}
+
+engram_status check_i8(const char* who, const engram_i8_weights* w) {
+  if (w->w == nullptr || w->scale == nullptr) return fail(ENGRAM_EINVAL, "%s: int8 w and scale must be non-NULL", who);
+  if (!aligned(w->scale, 4)) return fail(ENGRAM_EINVAL, "%s: the int8 scales must be 4-byte aligned", who);
+  return ENGRAM_OK;
+}
+
+engram_status check_draft(const char* who, const engram_draft* draft) {
+  if (draft == nullptr || draft->v == nullptr || draft->gamma == nullptr)
+    return fail(ENGRAM_EINVAL, "%s: the draft's v and gamma must be non-NULL", who);
+  if (!aligned(draft->v, 16) || !aligned(draft->gamma, 4))
+    return fail(ENGRAM_EINVAL, "%s: the draft's v must be 16-byte and gamma 4-byte aligned", who);
+  return ENGRAM_OK;
+}
+
+// engram_forward_i8 (draft NULL) and engram_forward_draft.
+engram_status forward_draft(const char* who, const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                            const engram_i8_weights* w8, engram_decode_state* st, const engram_draft* draft,
+                            float* alpha_out, float* y_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  engram::HashArgs ha;
+  engram::TableArgs ta;
+  engram::GateConvArgs g;
+  engram_status r = check_call(who, L, st, true, B, T, &ha, &ta, &g);
+  if (r != ENGRAM_OK) return r;
+  if (w8 != nullptr && (r = check_i8(who, w8)) != ENGRAM_OK) return r;
+  const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim;
+  if (w8 != nullptr && d_mem > 131071) return fail(ENGRAM_EUNSUPPORTED, "%s: d_mem above 131071 for the int8 product", who);
+  const int64_t n_tok = B * T;
+  if (n_tok == 0) return ENGRAM_OK;
+  if (n_tok > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "%s: B*T above 2^31-1 tokens per call", who);
+  if (tokens == nullptr || H == nullptr) return fail(ENGRAM_EINVAL, "%s: tokens and H must be non-NULL", who);
+  if (!aligned(H, 16)) return fail(ENGRAM_EINVAL, "%s: H must be 16-byte aligned", who);
+  if (y_out != nullptr && !aligned(y_out, 16)) return fail(ENGRAM_EINVAL, "%s: y_out must be 16-byte aligned", who);
+  const size_t need = draft_ws_bytes(B, T, L, w8 != nullptr, draft == nullptr);
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+    return fail(ENGRAM_EINVAL, "%s: workspace needs %zu bytes, 256-byte aligned (got %zu)", who, need, ws_bytes);
+  Carve c{static_cast<char*>(ws)};
+  DraftWorkspace w = carve_draft(c, n_tok, L, w8 != nullptr, draft == nullptr);
+  if (draft != nullptr) {
+    w.f.kv = draft->v;
+    w.f.gamma = draft->gamma;
+  }
+  prof_begin();
+  // the int8 product reads the rows in hdtype, also where the layer has MXFP8 weights
+  r = run_retrieve(tokens, B, T, L, ha, ta, g.hdtype, st, w.e, stream, w8 != nullptr ? static_cast<int>(g.hdtype) : -1);
+  if (r != ENGRAM_OK) return r;
+  const Int8Step i8{w8, w.codes.codes, w.codes.scale};
+  return run_compute(tokens, w.e, H, B, T, L, g, st, alpha_out, y_out, w.f, stream, nullptr, w8 != nullptr ? &i8 : nullptr,
+                     draft == nullptr);
+}
+
+}  // namespace
+
+ENGRAM_API size_t engram_forward_i8_workspace(int64_t B, int64_t T, const engram_layer* L) {
+  return draft_ws_bytes(B, T, L, true, true);
+}
+
+ENGRAM_API engram_status engram_forward_i8(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                                           const engram_i8_weights* w, engram_decode_state* st, float* alpha_out,
+                                           float* y_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (w == nullptr) return fail(ENGRAM_EINVAL, "forward_i8: the int8 weights are NULL");
+  return forward_draft("forward_i8", tokens, H, B, T, L, w, st, nullptr, alpha_out, y_out, ws, ws_bytes, stream);
+}
+
+ENGRAM_API int64_t engram_draft_stride(const engram_layer* L, const engram_i8_weights* w) {
+  if (L == nullptr || L->gc.branches < 1) return 0;
+  return w == nullptr && use_fused(L) ? L->gc.d : static_cast<int64_t>(1 + L->gc.branches) * L->gc.d;
+}
+
+ENGRAM_API size_t engram_forward_draft_workspace(int64_t B, int64_t T, const engram_layer* L, const engram_i8_weights* w) {
+  return draft_ws_bytes(B, T, L, w != nullptr, false);
+}
+
+ENGRAM_API engram_status engram_forward_draft(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                                              const engram_i8_weights* w, const engram_decode_state* st,
+                                              const engram_draft* draft, float* alpha_out, float* y_out, void* ws,
+                                              size_t ws_bytes, hipStream_t stream) {
+  if (st == nullptr) return fail(ENGRAM_EINVAL, "forward_draft: the decode state is NULL");
+  if (L == nullptr) return fail(ENGRAM_EINVAL, "layer is NULL");
+  const engram_status r = check_draft("forward_draft", draft);
+  if (r != ENGRAM_OK) return r;
+  if (draft->v_stride != engram_draft_stride(L, w))
+    return fail(ENGRAM_EINVAL, "forward_draft: v_stride must be engram_draft_stride() = %lld",
+                static_cast<long long>(engram_draft_stride(L, w)));
+  engram_decode_state view = *st;   // read only: no commit follows
+  return forward_draft("forward_draft", tokens, H, B, T, L, w, &view, draft, alpha_out, y_out, ws, ws_bytes, stream);
+}
+
+ENGRAM_API engram_status engram_commit_draft(const int32_t* tokens, int64_t B, int64_t T, const engram_layer* L,
+                                             const engram_draft* draft, const int32_t* n_accepted, engram_decode_state* st,
+                                             hipStream_t stream) {
+  if (st == nullptr) return fail(ENGRAM_EINVAL, "commit_draft: the decode state is NULL");
+  engram::HashArgs ha;
+  engram::TableArgs ta;
+  engram::GateConvArgs g;
+  engram_status r = check_call("commit_draft", L, st, true, B, T, &ha, &ta, &g);
+  if (r != ENGRAM_OK) return r;
+  if ((r = check_draft("commit_draft", draft)) != ENGRAM_OK) return r;
+  if (draft->v_stride < g.d || draft->v_stride % 4 != 0)
+    return fail(ENGRAM_EINVAL, "commit_draft: v_stride must be a multiple of 4, at least d");
+  if (B * T == 0) return ENGRAM_OK;
+  if (tokens == nullptr || n_accepted == nullptr)
+    return fail(ENGRAM_EINVAL, "commit_draft: tokens and n_accepted must be non-NULL");
+  prof_begin();
+  prof_mark(stream, "commit_draft_kernel");
+  return hip_status(engram::launch_commit_draft(draft->v, draft->v_stride, draft->gamma, B, T, g,
+                                                engram::StateArgs{st->ids, st->conv, st->pos}, tokens, L->hash.proj,
+                                                L->hash.max_n, static_cast<int32_t>(L->hash.vocab), n_accepted,
+                                                g_err_word.load(), stream),
+                    "commit_draft launch");
+}
+
+ENGRAM_API size_t engram_token_probs_workspace(int64_t rows, int64_t V) {
+  if (rows < 1 || V < 1) return 0;
+  return engram::probs_workspace(rows, V);
+}
+
+ENGRAM_API engram_status engram_token_probs(const void* logits, engram_dtype dtype, int64_t rows, int64_t V, int64_t ld,
+                                            const float* temperature, int64_t per, float* probs, void* ws,
+                                            size_t ws_bytes, hipStream_t stream) {
+  if (dtype != ENGRAM_F32 && dtype != ENGRAM_BF16)
+    return fail(ENGRAM_EUNSUPPORTED, "token_probs: dtype must be F32 or BF16");
+  if (rows < 0 || V < 1 || ld < V || per < 1)
+    return fail(ENGRAM_EINVAL, "token_probs: need rows >= 0, V >= 1, ld >= V and per >= 1");
+  if (rows > INT32_MAX || V > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "token_probs: rows and V must be below 2^31");
+  if (rows == 0) return ENGRAM_OK;
+  if (logits == nullptr || probs == nullptr) return fail(ENGRAM_EINVAL, "token_probs: logits and probs must be non-NULL");
+  if (!aligned(logits, dtype_size(dtype)) || !aligned(probs, 4) || !aligned(temperature, 4))
+    return fail(ENGRAM_EINVAL, "token_probs: logits, temperature and probs must be aligned to their elements");
+  const size_t need = engram_token_probs_workspace(rows, V);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
+    return fail(ENGRAM_EINVAL, "token_probs: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  prof_begin();
+  prof_mark(stream, "token_probs_kernel");
+  return hip_status(engram::launch_token_probs(logits, dtype, rows, V, ld, temperature, per, probs, ws, stream),
+                    "token_probs launch");
+}
+
+ENGRAM_API size_t engram_verify_drafts_workspace(int64_t S, int64_t V) {
+  if (S < 1 || V < 1) return 0;
+  return align_up(engram::verify_workspace(S, V));
+}
+
+ENGRAM_API engram_status engram_verify_drafts(const void* target, const void* draft, engram_dtype dtype,
+                                              const int32_t* drafted, const int32_t* n_draft, const float* u_accept,
+                                              const float* u_sample, int64_t S, int32_t G, int64_t V, int32_t* tokens,
+                                              int32_t* n_accepted, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (dtype != ENGRAM_F32 && dtype != ENGRAM_BF16)
+    return fail(ENGRAM_EUNSUPPORTED, "verify_drafts: dtype must be F32 or BF16");
+  if (S < 0 || G < 0 || V < 1) return fail(ENGRAM_EINVAL, "verify_drafts: need S >= 0, G >= 0 and V >= 1");
+  if (S > 65535 || G > ENGRAM_MAX_DRAFTS || V > INT32_MAX)
+    return fail(ENGRAM_EUNSUPPORTED, "verify_drafts: S above 65535, G above %d or V above 2^31-1", ENGRAM_MAX_DRAFTS);
+  if (S == 0) return ENGRAM_OK;
+  if (target == nullptr || u_sample == nullptr || tokens == nullptr || n_accepted == nullptr)
+    return fail(ENGRAM_EINVAL, "verify_drafts: target, u_sample, tokens and n_accepted must be non-NULL");
+  if (G > 0 && (drafted == nullptr || u_accept == nullptr))
+    return fail(ENGRAM_EINVAL, "verify_drafts: drafted and u_accept must be non-NULL when G > 0");
+  if (!aligned(target, dtype_size(dtype)) || !aligned(draft, dtype_size(dtype)) || !aligned(drafted, 4) ||
+      !aligned(n_draft, 4) || !aligned(u_accept, 4) || !aligned(u_sample, 4) || !aligned(tokens, 4) || !aligned(n_accepted, 4))
+    return fail(ENGRAM_EINVAL, "verify_drafts: every buffer must be aligned to its elements");
+  const size_t need = engram_verify_drafts_workspace(S, V);
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+    return fail(ENGRAM_EINVAL, "verify_drafts: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  prof_begin();
+  prof_mark(stream, "verify_sums_kernel");
+  const engram_status r = hip_status(engram::launch_verify(target, draft, dtype, drafted, n_draft, u_accept, u_sample, S, G, V, tokens,
+                                                           n_accepted, ws, stream),
+                                     "verify_drafts launch");
+  prof_mark(stream, nullptr);
+  return r;
 }
 
 ENGRAM_API engram_status engram_quantize_mxfp8(const void* x, engram_dtype dtype, int64_t rows, int64_t cols,

@@ -323,6 +323,30 @@ hipError_t launch_state_commit(const void* v, int64_t v_stride, int vdtype, int6
                                const int32_t* tokens, const int32_t* proj, int32_t max_n, int32_t vocab,
                                uint32_t* err, hipStream_t s);
 
+// ---- speculative decode (int8.hip, verify.hip, draft.hip) ----
+
+// Bytes of a quantised row in the product's own layout: whole 16-byte runs.
+int64_t i8_row_stride(int64_t cols);
+// Rows to int8 codes [rows][ldq] and scales.  tail: a last run of 16 columns
+// that is not whole is stored right-aligned in its 16 bytes, zeros before it
+// (ldq = i8_row_stride(cols)); otherwise the rows are plain.
+hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail,
+                              float* scale, hipStream_t s);
+// Product of int8 codes q [n_tok][ldq] (tailed: in the layout above) with W.
+hipError_t launch_project_i8(const int8_t* q, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
+                             const float* w_scale, int64_t n_tok, int64_t K, int64_t n_out, int out_dtype, void* out,
+                             hipStream_t s);
+hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
+                              int64_t per, float* probs, void* ws, hipStream_t s);
+size_t probs_workspace(int64_t rows, int64_t V);
+size_t verify_workspace(int64_t S, int64_t V);
+hipError_t launch_verify(const void* target, const void* draft, int dtype, const int32_t* drafted, const int32_t* n_draft,
+                         const float* u_accept, const float* u_sample, int64_t S, int32_t G, int64_t V, int32_t* tokens,
+                         int32_t* n_accepted, void* ws, hipStream_t s);
+hipError_t launch_commit_draft(const float* v, int64_t v_stride, const float* gamma, int64_t B, int64_t T,
+                               const GateConvArgs& g, const StateArgs& st, const int32_t* tokens, const int32_t* proj,
+                               int32_t max_n, int32_t vocab, const int32_t* n_accepted, uint32_t* err, hipStream_t s);
+
 size_t cache_build_workspace(int64_t total_rows);
 size_t cache_update_workspace(int64_t total_rows, int64_t cache_n);
 hipError_t launch_cache_update(const TableArgs& ta, int64_t total_rows, int row_bytes, int64_t cache_n,

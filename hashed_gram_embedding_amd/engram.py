@@ -24,9 +24,11 @@ OK, EINVAL, EUNSUPPORTED, EHIP = 0, -1, -2, -3
 F32, BF16, I8 = 0, 1, 2
 MAX_TABLES, MAX_ORDER = 32, 4
 MAX_D, MAX_BRANCHES = 65536, 64
+MAX_DRAFTS = 64
 
 _DT = {"f32": F32, "bf16": BF16, "i8": I8}
 _TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16, I8: torch.int8}
+_DT_OF = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
 
 c_i32p = ctypes.POINTER(ctypes.c_int32)
 
@@ -65,6 +67,14 @@ class LayerStruct(ctypes.Structure):
 
 class DecodeStateStruct(ctypes.Structure):
     _fields_ = [("ids", ctypes.c_void_p), ("conv", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class I8WeightsStruct(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class DraftStruct(ctypes.Structure):
+    _fields_ = [("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64), ("gamma", ctypes.c_void_p)]
 
 
 _lib = None
@@ -141,6 +151,24 @@ def load_library(path: str) -> ctypes.CDLL:
         "engram_debug_set_error_word": (i32, [vp]),
         "engram_debug_read_errors": (i32, [ctypes.POINTER(ctypes.c_uint32)]),
         "engram_host_free": (i32, [vp]),
+        "engram_quantize_i8": (i32, [vp, i32, i64, i64, vp, vp, vp]),
+        "engram_project_i8_workspace": (sz, [i64, i64, i32]),
+        "engram_project_i8": (i32, [vp, i32, vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]),
+        "engram_forward_i8_workspace": (sz, [i64, i64, ctypes.POINTER(LayerStruct)]),
+        "engram_forward_i8": (i32, [vp, vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct),
+                                    ctypes.POINTER(DecodeStateStruct), vp, vp, vp, sz, vp]),
+        "engram_draft_stride": (i64, [ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct)]),
+        "engram_forward_draft_workspace": (sz, [i64, i64, ctypes.POINTER(LayerStruct),
+                                                ctypes.POINTER(I8WeightsStruct)]),
+        "engram_forward_draft": (i32, [vp, vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct),
+                                       ctypes.POINTER(DecodeStateStruct), ctypes.POINTER(DraftStruct), vp, vp, vp, sz,
+                                       vp]),
+        "engram_commit_draft": (i32, [vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(DraftStruct), vp,
+                                      ctypes.POINTER(DecodeStateStruct), vp]),
+        "engram_token_probs_workspace": (sz, [i64, i64]),
+        "engram_token_probs": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, sz, vp]),
+        "engram_verify_drafts_workspace": (sz, [i64, i64]),
+        "engram_verify_drafts": (i32, [vp, vp, i32, vp, vp, vp, vp, i64, i32, i64, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -161,7 +189,11 @@ def exported_names():
             "engram_hot_buckets", "engram_hot_build", "engram_hot_lookup", "engram_forward_retrieved_prefetch",
             "engram_profile_enable", "engram_profile_read",
             "engram_host_alloc", "engram_host_free", "engram_debug_checks", "engram_debug_set_error_word",
-            "engram_debug_read_errors"]
+            "engram_debug_read_errors",
+            "engram_quantize_i8", "engram_project_i8_workspace", "engram_project_i8", "engram_forward_i8_workspace",
+            "engram_forward_i8", "engram_draft_stride", "engram_forward_draft_workspace", "engram_forward_draft",
+            "engram_commit_draft", "engram_token_probs_workspace", "engram_token_probs",
+            "engram_verify_drafts_workspace", "engram_verify_drafts"]
 
 
 def last_error() -> str:
@@ -181,6 +213,44 @@ def _stream(stream=None):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+# The entry points of the speculative decode step check what they marshal
+# (device, dtype, shape, contiguity) and launch on the tensors' own device.
+
+def _check_tensor(name: str, t: torch.Tensor, dtypes, shape, device, strided: bool = False):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(fn, device: torch.device, stream, *args, ws=None):
+    """fn(*args, stream) with `device` current, on `stream` (default: the
+    device's current one); ws is scratch allocated for this call."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, not on {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
+    if torch.cuda.current_device() == device.index:
+        cur = torch.cuda.current_stream()
+        s = cur if stream is None else stream
+        _check(fn(*args, s.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            cur = torch.cuda.current_stream()
+            s = cur if stream is None else stream
+            _check(fn(*args, s.cuda_stream))
+    if ws is not None and s.cuda_stream != cur.cuda_stream:
+        ws.record_stream(s)   # allocated on the current stream, used on another
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_I32, _I8, _F32 = (torch.int32,), (torch.int8,), (torch.float32,)
 
 
 def to_device(a: np.ndarray, kind: str, device) -> torch.Tensor:
@@ -608,6 +678,213 @@ def pack_bf16(w: torch.Tensor, packed: torch.Tensor, stream=None):
     """The bf16 W [rows, cols] in the matrix cores' operand order (same size)."""
     rows, cols = w.shape
     _check(lib().engram_pack_bf16(_ptr(w), rows, cols, _ptr(packed), _stream(stream)))
+
+
+def quantize_i8(x: torch.Tensor, stream=None):
+    """Rows of x (float32 or bfloat16 [rows, cols]) as 8-bit integers: (codes
+    int8 [rows, cols], scales float32 [rows]), x about codes * scale."""
+    rows, cols = x.shape
+    _check_tensor("x", x, _FLOATS, (rows, cols), x.device)
+    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _launch(lib().engram_quantize_i8, x.device, stream, x.data_ptr(), _DT_OF[x.dtype], rows, cols, q.data_ptr(),
+            scale.data_ptr())
+    return q, scale
+
+
+def project_i8(e: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, e_scale: Optional[torch.Tensor] = None,
+               out_dtype: str = "bf16", out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """e [..., d_mem] times W^T in 8-bit integers (engram_project_i8): w int8
+    [n_out, d_mem] with one scale per row, e int8 codes with e_scale [...] or
+    float32 / bfloat16 rows, quantised on the way.  Returns [..., n_out]."""
+    dev, d_mem, n_out = e.device, e.shape[-1], w.shape[0]
+    lead = e.shape[:-1]
+    n_tok = e.numel() // max(d_mem, 1)
+    dt = _DT_OF.get(e.dtype)
+    _check_tensor("e", e, _FLOATS if e_scale is None else _I8, e.shape, dev)
+    _check_tensor("w", w, _I8, (n_out, d_mem), dev)
+    _check_tensor("w_scale", w_scale, _F32, (n_out,), dev)
+    if e_scale is not None:
+        _check_tensor("e_scale", e_scale, _F32, lead, dev)
+    odt = _DT[out_dtype]
+    if out is None:
+        out = torch.empty((*lead, n_out), dtype=_TORCH_DT[odt], device=dev)
+    else:
+        _check_tensor("out", out, (_TORCH_DT[odt],), (*lead, n_out), dev)
+    own = None
+    nbytes = lib().engram_project_i8_workspace(n_tok, d_mem, dt)
+    if ws is None and nbytes:
+        ws = own = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _launch(lib().engram_project_i8, dev, stream, e.data_ptr(), dt, None if e_scale is None else e_scale.data_ptr(),
+            w.data_ptr(), w_scale.data_ptr(), n_tok, d_mem, n_out, odt, out.data_ptr(),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), ws=own)
+    return out
+
+
+class Int8Weights:
+    """A layer's stacked W [(1+M)d, d_mem] in 8-bit integers (engram_i8_weights):
+    quantised from the layer's own, or the given codes and scales."""
+
+    def __init__(self, layer: Layer, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+        if q is None:
+            q, scale = quantize_i8(layer.w)
+        n, k = layer.w.shape
+        _check_tensor("q", q, _I8, (n, k), layer.w.device)
+        _check_tensor("scale", scale, _F32, (n,), layer.w.device)
+        self.q, self.scale = q, scale
+        self.s = I8WeightsStruct(q.data_ptr(), scale.data_ptr())
+
+
+class Draft:
+    """The buffers that forward_draft fills and commit_draft reads (engram_draft):
+    v float32 [B*T, stride] and gamma float32 [B*T, M], allocated unless given."""
+
+    def __init__(self, B: int, T: int, layer: Layer, device="cuda", w8: Optional[Int8Weights] = None,
+                 v: Optional[torch.Tensor] = None, gamma: Optional[torch.Tensor] = None):
+        stride = int(lib().engram_draft_stride(ctypes.byref(layer.s), None if w8 is None else ctypes.byref(w8.s)))
+        self.B, self.T = B, T
+        self.v = torch.empty((B * T, stride), dtype=torch.float32, device=device) if v is None else v
+        self.gamma = torch.empty((B * T, layer.M), dtype=torch.float32, device=device) if gamma is None else gamma
+        dev = self.v.device
+        if self.v.dim() != 2 or self.v.shape[1] < layer.d:
+            raise ValueError(f"v must be [B*T, at least d={layer.d}]")
+        _check_tensor("v", self.v, _F32, (B * T, self.v.shape[1]), dev)
+        _check_tensor("gamma", self.gamma, _F32, (B * T, layer.M), dev)
+        self.s = DraftStruct(self.v.data_ptr(), self.v.shape[1], self.gamma.data_ptr())
+
+
+def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, state: Optional["DecodeState"]):
+    dev = tokens.device
+    B, T = tokens.shape
+    _check_tensor("tokens", tokens, _I32, (B, T), dev)
+    if H is not None:
+        _check_tensor("H", H, (_TORCH_DT[layer.hdtype],), H.shape, dev)
+        if H.numel() != B * T * layer.M * layer.d:
+            raise ValueError(f"H has {H.numel()} values, expected B*T*M*d = {B * T * layer.M * layer.d}")
+    if state is not None:
+        g, n1 = layer.li, layer.li.hash.max_n - 1
+        _check_tensor("state.ids", state.ids, _I32, (B, n1), dev)
+        _check_tensor("state.conv", state.conv, _F32, (B, layer.M, (g.kernel_w - 1) * g.dilation, layer.d), dev)
+        _check_tensor("state.pos", state.pos, _I32, (B,), dev)
+    return dev, B, T
+
+
+def _layer_outputs(B, T, layer, dev, want_alpha, want_y):
+    alpha = torch.empty((B, T, layer.M), dtype=torch.float32, device=dev) if want_alpha else None
+    y = torch.empty((B, T, layer.M, layer.d), dtype=torch.float32, device=dev) if want_y else None
+    return alpha, y
+
+
+def forward_i8(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, w8: Int8Weights,
+               state: Optional[DecodeState] = None, want_alpha: bool = False, want_y: bool = False,
+               ws: Optional[torch.Tensor] = None, stream=None):
+    """forward() with Step 5 as the 8-bit integer product.  Returns (alpha, y)
+    when asked."""
+    dev, B, T = _check_chunk(tokens, H, layer, state)
+    alpha, y = _layer_outputs(B, T, layer, dev, want_alpha, want_y)
+    own = None
+    if ws is None:
+        ws = own = torch.empty(max(lib().engram_forward_i8_workspace(B, T, ctypes.byref(layer.s)), 256),
+                               dtype=torch.uint8, device=dev)
+    _launch(lib().engram_forward_i8, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s),
+            ctypes.byref(w8.s), None if state is None else ctypes.byref(state.s), _ptr(alpha), _ptr(y), ws.data_ptr(),
+            ws.numel(), ws=own)
+    return alpha, y
+
+
+def forward_draft(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, state: DecodeState, draft: Draft,
+                  w8: Optional[Int8Weights] = None, want_alpha: bool = False, want_y: bool = False,
+                  ws: Optional[torch.Tensor] = None, stream=None):
+    """One layer over a drafted chunk: H as forward() (or forward_i8() with w8)
+    would leave it, `state` only read, the chunk's conv inputs in `draft`."""
+    dev, B, T = _check_chunk(tokens, H, layer, state)
+    if (draft.B, draft.T) != (B, T):
+        raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
+    alpha, y = _layer_outputs(B, T, layer, dev, want_alpha, want_y)
+    p8 = None if w8 is None else ctypes.byref(w8.s)
+    own = None
+    if ws is None:
+        ws = own = torch.empty(max(lib().engram_forward_draft_workspace(B, T, ctypes.byref(layer.s), p8), 256),
+                               dtype=torch.uint8, device=dev)
+    _launch(lib().engram_forward_draft, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s), p8,
+            ctypes.byref(state.s), ctypes.byref(draft.s), _ptr(alpha), _ptr(y), ws.data_ptr(), ws.numel(), ws=own)
+    return alpha, y
+
+
+def commit_draft(tokens: torch.Tensor, layer: Layer, draft: Draft, n_accepted: torch.Tensor, state: DecodeState,
+                 stream=None):
+    """Advance `state` by the first n_accepted + 1 tokens of each sequence's
+    chunk (n_accepted int32 [B] from verify_drafts; -1 keeps none)."""
+    dev, B, T = _check_chunk(tokens, None, layer, state)
+    if (draft.B, draft.T) != (B, T):
+        raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
+    _check_tensor("n_accepted", n_accepted, _I32, (B,), dev)
+    _launch(lib().engram_commit_draft, dev, stream, tokens.data_ptr(), B, T, ctypes.byref(layer.s),
+            ctypes.byref(draft.s), n_accepted.data_ptr(), ctypes.byref(state.s))
+
+
+def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Probabilities float32 [S, R, V] of logits [S, R, V] (or [S, V]; float32
+    or bfloat16, rows may be padded: any uniform row stride) at a temperature
+    float32 [S] (default 1; 0 = all on the largest logit)."""
+    if logits.dim() not in (2, 3):
+        raise ValueError("logits must be [S, R, V] or [S, V]")
+    dev, V, S = logits.device, logits.shape[-1], logits.shape[0]
+    per = logits.shape[1] if logits.dim() == 3 else 1
+    _check_tensor("logits", logits, _FLOATS, logits.shape, dev, strided=True)
+    ld = logits.stride(-2)
+    if S * per <= 1:
+        ld = V
+    elif per == 1:
+        ld = logits.stride(0)
+    if (V > 1 and logits.stride(-1) != 1) or ld < V or (logits.dim() == 3 and S > 1 and per > 1 and logits.stride(0) != per * ld):
+        raise ValueError("logits must have contiguous rows at one row stride")
+    if temperature is not None:
+        _check_tensor("temperature", temperature, _F32, (S,), dev)
+    if probs is None:
+        probs = torch.empty(logits.shape, dtype=torch.float32, device=dev)
+    else:
+        _check_tensor("probs", probs, _F32, logits.shape, dev)
+    own = None
+    nbytes = lib().engram_token_probs_workspace(S * per, V)
+    if ws is None and nbytes:
+        ws = own = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _launch(lib().engram_token_probs, dev, stream, logits.data_ptr(), _DT_OF[logits.dtype], S * per, V, ld,
+            None if temperature is None else temperature.data_ptr(), max(per, 1), probs.data_ptr(),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), ws=own)
+    return probs
+
+
+def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], drafted: torch.Tensor, u_accept: torch.Tensor,
+                  u_sample: torch.Tensor, n_draft: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Verify drafted tokens int32 [S, G] against the target's probabilities
+    [S, G+1, V] (engram_verify_drafts); draft: the probabilities [S, G, V] the
+    drafts were drawn with, or None.  Returns (tokens int32 [S, G+1]: accepted
+    drafts, next token, -1; n_accepted int32 [S])."""
+    dev = target.device
+    S, G = drafted.shape
+    V = target.shape[-1]
+    _check_tensor("target", target, _FLOATS, (S, G + 1, V), dev)
+    if draft is not None:
+        _check_tensor("draft", draft, (target.dtype,), (S, G, V), dev)
+    _check_tensor("drafted", drafted, _I32, (S, G), dev)
+    _check_tensor("u_accept", u_accept, _F32, (S, G), dev)
+    _check_tensor("u_sample", u_sample, _F32, (S,), dev)
+    if n_draft is not None:
+        _check_tensor("n_draft", n_draft, _I32, (S,), dev)
+    tokens = torch.empty((S, G + 1), dtype=torch.int32, device=dev)
+    n_accepted = torch.empty(S, dtype=torch.int32, device=dev)
+    own = None
+    if ws is None:
+        ws = own = torch.empty(max(lib().engram_verify_drafts_workspace(S, V), 256), dtype=torch.uint8, device=dev)
+    _launch(lib().engram_verify_drafts, dev, stream, target.data_ptr(), None if draft is None else draft.data_ptr(),
+            _DT_OF[target.dtype], drafted.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
+            u_accept.data_ptr(), u_sample.data_ptr(), S, G, V, tokens.data_ptr(), n_accepted.data_ptr(), ws.data_ptr(),
+            ws.numel(), ws=own)
+    return tokens, n_accepted
 
 
 def hot_lookup(tokens: torch.Tensor, spec, hot: HotTier, hist: Optional[torch.Tensor] = None,

@@ -460,6 +460,142 @@ engram_status engram_pack_mxfp8(const uint8_t* q, const uint8_t* scale, int64_t 
  * of 32, cols of 16 (EINVAL otherwise); rows*cols = 0 is a no-op. */
 engram_status engram_pack_bf16(const void* w, int64_t rows, int64_t cols, void* packed, hipStream_t stream);
 
+/* ---- Speculative decode next to the layer ----
+ * A speculative step runs the layers over a chunk of T = G + 1 tokens per
+ * sequence (the last sampled token and G drafted ones), multiplies the final
+ * hidden states with the vocabulary, verifies the drafts against the
+ * resulting probabilities and keeps the accepted tokens:
+ *   engram_forward_draft    the layer over the chunk, the state left alone
+ *   engram_project_i8       logits (and Step 5) as a product in 8-bit integers
+ *   engram_token_probs      probabilities of the logits
+ *   engram_verify_drafts    accepted drafts and the next token
+ *   engram_commit_draft     the state takes in the kept tokens
+ * None of these calls synchronises or allocates; all of them can be captured
+ * into a HIP graph. */
+
+/* Rows as 8-bit integers: scale[r] = max_c |x[r][c]| / 127 and q[r][c] =
+ * 127 x[r][c] / max_c |x[r][c]| rounded to nearest, ties to even (of the
+ * exact quotient).  A row of zeros gets scale 0 and codes 0; a row holding an
+ * infinity or a NaN gets codes 0 and scale NaN, so its products are NaN.
+ * x: device [rows][cols], F32 or BF16; q: device [rows][cols]; scale: device
+ * [rows].  rows < 2^31, 1 <= cols < 2^31.  rows = 0 is a no-op. */
+engram_status engram_quantize_i8(const void* x, engram_dtype dtype, int64_t rows, int64_t cols, int8_t* q,
+                                 float* scale, hipStream_t stream);
+
+/* out[t][o] = (sum_c q[t][c] w[o][c]) * e_scale[t] * w_scale[o]: the product
+ * of W in 8-bit integers with one scale per token and one per output channel.
+ * The sum is exact (int32); the two multiplications are in float32, and BF16
+ * output rounds once more.
+ *   e        device [n_tok][d_mem]: int8 codes with e_scale [n_tok] (e_dtype
+ *            I8), or F32 or BF16 rows, quantised on the way as
+ *            engram_quantize_i8 does (e_scale NULL)
+ *   w        device int8 [n_out][d_mem], w_scale device [n_out] (the rows of W
+ *            from engram_quantize_i8, or a checkpoint's)
+ *   out      device [n_tok][n_out], F32 or BF16, aligned to its elements
+ *   ws       engram_project_i8_workspace() bytes, 256-byte aligned (NULL where
+ *            that is 0)
+ * 1 <= d_mem <= 131071 (so that the sum cannot leave int32), n_out < 2^31,
+ * n_tok < 2^31 (EUNSUPPORTED otherwise).  Any d_mem, n_out and n_tok; 16-byte
+ * aligned e and w with d_mem a multiple of 16 run fastest.  n_tok = 0 is a
+ * no-op. */
+size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, engram_dtype e_dtype);
+engram_status engram_project_i8(const void* e, engram_dtype e_dtype, const float* e_scale, const int8_t* w,
+                                const float* w_scale, int64_t n_tok, int64_t d_mem, int64_t n_out,
+                                engram_dtype out_dtype, void* out, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* A layer's W in 8-bit integers: engram_quantize_i8 of engram_layer.w. */
+typedef struct engram_i8_weights {
+  const int8_t* w;      /* device [(1+M)*d][n_tables*dim] */
+  const float* scale;   /* device [(1+M)*d]               */
+} engram_i8_weights;
+
+/* engram_forward with Step 5 as the 8-bit integer product: the gathered rows
+ * (in the layer's hdtype) are quantised per token, the projections are
+ * float32.  Arguments otherwise as engram_forward; L's own w, w_mx and
+ * w_packed are not read.  ws: engram_forward_i8_workspace() bytes, 256-byte
+ * aligned. */
+size_t engram_forward_i8_workspace(int64_t B, int64_t T, const engram_layer* L);
+engram_status engram_forward_i8(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                                const engram_i8_weights* w, engram_decode_state* st, float* alpha_out,
+                                float* y_out, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* What engram_forward_draft leaves for engram_commit_draft: the conv inputs
+ * u^(m) = RMSNorm(alpha^(m) v) = gamma^(m) v of the chunk's tokens in two
+ * factors.  The caller owns both buffers. */
+typedef struct engram_draft {
+  float* v;           /* device [B*T][v_stride], 16-byte aligned; v in the first d columns */
+  int64_t v_stride;   /* engram_draft_stride()                                             */
+  float* gamma;       /* device [B*T][M]                                                   */
+} engram_draft;
+
+/* engram_forward (w NULL) or engram_forward_i8 (w set) over a drafted chunk:
+ * the sequences continue from st, which is only read.  H, alpha_out and y_out
+ * are those of the forward call, bit for bit.  engram_commit_draft then
+ * advances st by the tokens that are kept.
+ * engram_draft_stride: columns of a row of draft->v (w NULL or not).
+ * ws: engram_forward_draft_workspace() bytes, 256-byte aligned; it need not
+ * outlive the call's kernels. */
+int64_t engram_draft_stride(const engram_layer* L, const engram_i8_weights* w);
+size_t engram_forward_draft_workspace(int64_t B, int64_t T, const engram_layer* L, const engram_i8_weights* w);
+engram_status engram_forward_draft(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                                   const engram_i8_weights* w, const engram_decode_state* st,
+                                   const engram_draft* draft, float* alpha_out, float* y_out, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
+/* Advances st by the first k_b = min(max(n_accepted[b] + 1, 0), T) tokens of
+ * sequence b's chunk: afterwards it is the state that engram_forward would
+ * have left after those k_b tokens.  n_accepted: device int32 [B], as
+ * engram_verify_drafts writes it (the chunk's first token is always kept, and
+ * the token drawn at the end starts the next chunk); -1 keeps none.  tokens,
+ * B, T, L, draft: as in the engram_forward_draft call (v_stride may be any
+ * multiple of 4 from d up). */
+engram_status engram_commit_draft(const int32_t* tokens, int64_t B, int64_t T, const engram_layer* L,
+                                  const engram_draft* draft, const int32_t* n_accepted, engram_decode_state* st,
+                                  hipStream_t stream);
+
+/* probs[r][v] = e^((l[r][v] - max_v l[r][v]) / T) / sum, float32 [rows][V].
+ * logits: device, F32 or BF16, row r at element r * ld (ld >= V), aligned to
+ * its elements.  temperature: device [ceil(rows / per)], T of rows i*per ..
+ * i*per + per - 1 (per = the rows of one sequence), or NULL for 1.  T <= 0
+ * puts probability 1 on the lowest index of the largest logit.  A logit of
+ * -inf has probability 0 and a row of nothing else has none at all (zeros); a
+ * row with a NaN, or with +inf at T > 0, is NaN throughout.  rows and V below
+ * 2^31; rows = 0 is a no-op.  ws: engram_token_probs_workspace() bytes,
+ * 256-byte aligned. */
+size_t engram_token_probs_workspace(int64_t rows, int64_t V);
+engram_status engram_token_probs(const void* logits, engram_dtype dtype, int64_t rows, int64_t V, int64_t ld,
+                                 const float* temperature, int64_t per, float* probs, void* ws, size_t ws_bytes,
+                                 hipStream_t stream);
+
+/* Verification of up to G drafted tokens for each of S sequences against the
+ * target's probabilities p [S][G+1][V] (row i: after the chunk's token i), so
+ * that the kept tokens are distributed as if each had been drawn from p.
+ * Draft i (x_i, drawn with probabilities q_i) is accepted while
+ * u_accept_i * q_i(x_i) < p_i(x_i).  The next token is drawn from max(p_i -
+ * q_i, 0) of the first refused draft, or from the row behind the last draft
+ * when all were accepted (and from p_i where p_i - q_i leaves nothing): the
+ * lowest index whose cumulative sum exceeds u_sample * total, sums in double.
+ *   target    device [S][G+1][V], F32 or BF16, need not be normalised
+ *   draft     device [S][G][V] of the same dtype, or NULL: every draft was
+ *             chosen outright (q_i(x_i) = 1)
+ *   drafted   device int32 [S][G]; an id outside [0, V) is refused
+ *   n_draft   device int32 [S], drafts of each sequence, clamped to [0, G]; or
+ *             NULL for G each
+ *   u_accept  device [S][G], u_sample device [S]: random numbers in [0, 1)
+ *   tokens    device int32 [S][G+1]: the accepted drafts, the next token, then
+ *             -1; the next token is -1 where its row holds nothing (zeros, or
+ *             a sum that is not finite; a NaN entry counts as 0)
+ *   n_accepted device int32 [S]
+ *   ws        engram_verify_drafts_workspace() bytes, 256-byte aligned
+ * 1 <= S <= 65535, 0 <= G <= ENGRAM_MAX_DRAFTS, 1 <= V < 2^31 (EUNSUPPORTED
+ * otherwise); S = 0 is a no-op. */
+#define ENGRAM_MAX_DRAFTS 64
+size_t engram_verify_drafts_workspace(int64_t S, int64_t V);
+engram_status engram_verify_drafts(const void* target, const void* draft, engram_dtype dtype, const int32_t* drafted,
+                                   const int32_t* n_draft, const float* u_accept, const float* u_sample, int64_t S,
+                                   int32_t G, int64_t V, int32_t* tokens, int32_t* n_accepted, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
 /* Engram-Nine hot tier set-up and lookup (see engram_hot_tier).
  *
  * engram_hot_buckets: pilots of a hot set of n_hot n-grams, ceil(n_hot / 4)
@@ -489,11 +625,13 @@ engram_status engram_hot_lookup(const int32_t* tokens, int64_t B, int64_t T, con
                                 int32_t* hot_row, hipStream_t stream);
 
 /* Stage timing, for benchmarks.  While profiling is on, calls of
- * engram_forward (and engram_forward_noalloc), engram_retrieve,
- * engram_forward_retrieved(_prefetch), engram_gate_conv_forward and
- * engram_hot_lookup on the calling thread time each kernel they launch: the start and stop events are recorded by the kernel's own
- * dispatch (hipExtLaunchKernel), so a stage is the kernel's execution
- * interval (events owned by the library and reused).
+ * engram_forward (and engram_forward_noalloc, engram_forward_i8,
+ * engram_forward_draft), engram_retrieve, engram_forward_retrieved(_prefetch),
+ * engram_gate_conv_forward, engram_hot_lookup, engram_project_i8,
+ * engram_token_probs, engram_verify_drafts and engram_commit_draft on the
+ * calling thread time each kernel they launch: the start and stop events are
+ * recorded by the kernel's own dispatch (hipExtLaunchKernel), so a stage is
+ * the kernel's execution interval (events owned by the library and reused).
  *   on = 1: engram_profile_read returns the stages of the most recent call
  *           (at most 12).
  *   on = 2: stages accumulate over calls until engram_profile_read, which

@@ -482,6 +482,99 @@ def project_kv_mxfp8(e: np.ndarray, w: np.ndarray) -> np.ndarray:
     return dequantize_mxfp8(eq, es) @ dequantize_mxfp8(wq, ws).T
 
 
+# --------------------------------------------------------------------------
+# speculative decode: 8-bit integer product, probabilities, verification
+# --------------------------------------------------------------------------
+
+def quantize_i8(x: np.ndarray):
+    """Rows of x (float64 values of float32 or bfloat16 numbers) as (codes,
+    float32 scales): 127 x / max|x| to nearest, ties to even; a row of zeros
+    has scale 0, a row with an infinity or a NaN codes 0 and scale NaN.  (The
+    quotient in float64 rounds as the exact one does: it is a ratio of a
+    31-bit and a 24-bit number, a tie or at least 2^-26 away from one.)"""
+    top = np.max(np.abs(x), axis=1)
+    ok = np.isfinite(top) & (top > 0)
+    codes = np.zeros(x.shape, dtype=np.int8)
+    codes[ok] = np.rint(x[ok] * 127.0 / top[ok, None]).astype(np.int8)
+    scale = np.where(np.isfinite(top), top.astype(np.float32) / np.float32(127.0), np.float32(np.nan))
+    return codes, scale.astype(np.float32)
+
+
+def project_i8(q: np.ndarray, q_scale: np.ndarray, w: np.ndarray, w_scale: np.ndarray) -> np.ndarray:
+    acc = q.astype(np.float64) @ w.astype(np.float64).T      # whole numbers below 2^31: exact
+    return acc * q_scale.astype(np.float64)[:, None] * w_scale.astype(np.float64)[None, :]
+
+
+def project_kv_i8(e: np.ndarray, w: np.ndarray) -> np.ndarray:
+    """Step 5 with the rows of e and W in 8-bit integers."""
+    q, s = quantize_i8(e.reshape(-1, e.shape[-1]))
+    wq, ws = quantize_i8(w)
+    return project_i8(q, s, wq, ws).reshape(*e.shape[:-1], w.shape[0])
+
+
+def token_probs(logits: np.ndarray, temperature: float = 1.0) -> np.ndarray:
+    """Probabilities of one row of logits [V] (see engram_token_probs)."""
+    out = np.zeros(logits.shape, dtype=np.float64)
+    top = np.nan if np.any(np.isnan(logits)) else np.max(logits)
+    if np.isnan(top) or (top == np.inf and temperature > 0):
+        out[:] = np.nan
+    elif top == -np.inf:
+        pass
+    elif temperature > 0:
+        x = np.exp((logits - top) / temperature)
+        out[:] = x / np.sum(x)
+    else:
+        out[int(np.argmax(logits == top))] = 1.0
+    return out
+
+
+def verify_drafts(target: np.ndarray, draft, drafted, u_accept, u_sample: float, n: int):
+    """One sequence: target [G+1, V] and draft [G, V] (or None) float64 values,
+    drafted [G], n drafts.  Returns (tokens [G+1], n_accepted)."""
+    G, V = len(drafted), target.shape[1]
+    n = min(max(int(n), 0), G)
+    out = np.full(G + 1, -1, dtype=np.int32)
+    a = 0
+    while a < n:
+        x = int(drafted[a])
+        if not 0 <= x < V:
+            break
+        q = 1.0 if draft is None else draft[a, x]
+        if not float(u_accept[a]) * q < target[a, x]:
+            break
+        out[a] = x
+        a += 1
+    row = np.where(target[a] > 0, target[a], 0.0)
+    left = row
+    if a < n:
+        if draft is None:
+            left = row.copy()
+            if 0 <= int(drafted[a]) < V:
+                left[int(drafted[a])] = 0.0
+        else:
+            d = target[a] - draft[a]
+            left = np.where(d > 0, d, 0.0)
+        if not np.sum(left) > 0:
+            left = row
+    below = np.cumsum(left)
+    if below[-1] > 0 and np.isfinite(below[-1]):
+        over = np.nonzero(below > float(u_sample) * below[-1])[0]
+        out[a] = over[0] if over.size else np.nonzero(left > 0)[0][-1]
+    return out, a
+
+
+def commit_draft(state: dict, tokens: np.ndarray, proj: np.ndarray, u: np.ndarray, kept: np.ndarray) -> dict:
+    """The state (see new_state) after the first kept[b] tokens of each chunk
+    [B, T], whose conv inputs are u [B, T, M, d]: token by token."""
+    out = {"ids": state["ids"].copy(), "u": state["u"].copy(), "pos": state["pos"] + kept}
+    xc = compress(tokens, proj)
+    for b in range(tokens.shape[0]):
+        for t in range(int(kept[b])):
+            out["ids"][b] = np.append(out["ids"][b][1:], xc[b, t])
+            out["u"][b] = np.concatenate([out["u"][b][:, 1:], u[b, t][:, None]], axis=1)
+    return out
+
+
 def forward(tokens: np.ndarray, H: np.ndarray, layer, h_dtype: str, state=None,
             e_dtype=None, gemm: str = "exact", hot=None) -> dict:
     """One Engram layer over tokens [B, T] and hidden states H [B, T, M, d].
@@ -491,7 +584,8 @@ def forward(tokens: np.ndarray, H: np.ndarray, layer, h_dtype: str, state=None,
     the gathered rows ("f32" or "bf16").  With `state` (see new_state) the
     chunk continues earlier tokens and a new state is returned.
     Returns float64 arrays: z, e, kv, alpha [B,T,M], vt, u, c, Y [B,T,M,d],
-    H_out, and `state`.  gemm="mxfp8" takes Step 5 in MXFP8 (project_kv_mxfp8).
+    H_out, and `state`.  gemm="mxfp8" takes Step 5 in MXFP8 (project_kv_mxfp8),
+    gemm="int8" in 8-bit integers (project_kv_i8).
     hot = {"keys": {n: n-tuples}, "rows": {n: [n_hot, K*dim] rows}} adds the
     Engram-Nine hot tier (gather_two_tier); the result then also holds hot_idx.
     """
@@ -509,7 +603,7 @@ def forward(tokens: np.ndarray, H: np.ndarray, layer, h_dtype: str, state=None,
         e = gather_two_tier(z, hot_idx, tab.rows, tab.dtype, tab.row_offset, tab.dim, hp.heads, hot["rows"],
                             tab.scale, e_dtype)
     w64 = storage_to_f64(layer.w, h_dtype)
-    kv = project_kv_mxfp8(e, w64) if gemm == "mxfp8" else project_kv(e, w64)       # Step 5
+    kv = {"mxfp8": project_kv_mxfp8, "int8": project_kv_i8}.get(gemm, project_kv)(e, w64)   # Step 5
     out = gate_conv(storage_to_f64(H, h_dtype), kv, layer.conv_w, layer.dilation, layer.eps,
                     None if state is None else state["u"])                           # Steps 6-8
     out.update({"z": z, "e": e, "kv": kv})

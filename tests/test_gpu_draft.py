@@ -1,0 +1,208 @@
+"""GPU: the layer over a drafted chunk with the state only read, the commit of
+the kept tokens, and a speculative decode loop of all the operators together
+against decoding token by token."""
+import numpy as np
+import pytest
+import torch
+
+from hashed_gram_embedding_amd import engram as eg
+from hashed_gram_embedding_amd import inputs
+from oracle import engram_oracle as orc
+
+from parity import log
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def _same(a, b):
+    return torch.equal(a.contiguous().view(torch.int32 if a.element_size() == 4 else torch.int16),
+                       b.contiguous().view(torch.int32 if b.element_size() == 4 else torch.int16))
+
+
+def _state_like(st, S, max_n, M, span, d):
+    c = eg.DecodeState(S, max_n, M, span, d, DEV)
+    c.ids.copy_(st.ids)
+    c.conv.copy_(st.conv)
+    c.pos.copy_(st.pos)
+    return c
+
+
+def _chunk_inputs(config, S, T, M=1):
+    w = inputs.make_config(config, B=S, T=T + 12, rows_per_table=997)
+    lay = w.layers[0]
+    return w, lay
+
+
+CASES = [(1, "bf16", 3, 1), (1, "bf16", 2, 5), (1, "bf16", 3, 9), (1, "bf16", 2, 14), (2, "bf16", 2, 4), (0, "f32", 1, 6)]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("config,hdtype,S,T", CASES)
+def test_draft_then_commit_equals_forward(config, hdtype, S, T, int8):
+    """forward_draft gives forward's H, alpha and Y bit for bit and leaves the
+    state alone; committing every token leaves forward's state bit for bit, and
+    committing k tokens the state of the oracle after k tokens."""
+    log(f"draft config {config} S={S} T={T} int8={int8}")
+    kw = {} if config == 0 else dict(rows_per_table=997)
+    w = inputs.make_config(config, B=S, T=T + 12, **kw)
+    lay = w.layers[0]
+    L = eg.Layer(lay, hdtype, DEV)
+    w8 = eg.Int8Weights(L) if int8 else None
+    span, max_n = (lay.kernel_w - 1) * lay.dilation, lay.hash.max_n
+    tok = torch.from_numpy(w.tokens).to(DEV)
+    H = eg.to_device(w.H, hdtype, DEV)
+    run = (lambda t, h, st, **k: eg.forward_i8(t, h, L, w8, state=st, **k)) if int8 else \
+        (lambda t, h, st, **k: eg.forward(t, h, L, state=st, **k))
+    st = eg.DecodeState(S, max_n, lay.branches, span, lay.d, DEV)
+    run(tok[:, :12].contiguous(), H[:, :12].contiguous(), st)
+    before = _state_like(st, S, max_n, lay.branches, span, lay.d)
+    chunk = tok[:, 12:].contiguous()
+    ref_st = _state_like(st, S, max_n, lay.branches, span, lay.d)
+    h_ref = H[:, 12:].clone(memory_format=torch.contiguous_format)
+    a_ref, y_ref = run(chunk, h_ref, ref_st, want_alpha=True, want_y=True)
+
+    draft = eg.Draft(S, T, L, DEV, w8=w8)
+    h = H[:, 12:].clone(memory_format=torch.contiguous_format)
+    a, y = eg.forward_draft(chunk, h, L, st, draft, w8=w8, want_alpha=True, want_y=True)
+    assert _same(h, h_ref) and _same(a, a_ref) and _same(y, y_ref)
+    assert torch.equal(st.ids, before.ids) and torch.equal(st.pos, before.pos) and _same(st.conv, before.conv)
+
+    full = _state_like(st, S, max_n, lay.branches, span, lay.d)
+    eg.commit_draft(chunk, L, draft, torch.full((S,), T - 1, dtype=torch.int32, device=DEV), full)
+    assert torch.equal(full.ids, ref_st.ids) and torch.equal(full.pos, ref_st.pos) and _same(full.conv, ref_st.conv)
+
+    u = (draft.v[:, :lay.d].double().view(S, T, 1, lay.d) * draft.gamma.double().view(S, T, lay.branches, 1)).cpu().numpy()
+    state = {"ids": before.ids.cpu().numpy(), "pos": before.pos.cpu().numpy(),
+             "u": np.zeros((S, lay.branches, span, lay.d))}
+    for r in range(span):                    # the ring as the last `span` inputs, oldest first
+        state["u"][:, :, r] = before.conv[:, :, (12 + r) % span].double().cpu().numpy()
+    for k in range(-1, T + 1):
+        part = _state_like(st, S, max_n, lay.branches, span, lay.d)
+        acc = torch.full((S,), k, dtype=torch.int32, device=DEV)
+        acc[0] = T - 1 - max(k, 0)
+        eg.commit_draft(chunk, L, draft, acc, part)
+        kept = np.clip(acc.cpu().numpy() + 1, 0, T)
+        ref = orc.commit_draft(state, chunk.cpu().numpy(), lay.hash.proj, u, kept)
+        assert np.array_equal(part.ids.cpu().numpy(), ref["ids"]) and np.array_equal(part.pos.cpu().numpy(), ref["pos"])
+        for s in range(S):
+            at = [(int(ref["pos"][s]) + r) % span for r in range(span)]
+            got = part.conv[s][:, at].double().cpu().numpy()
+            assert np.all(np.abs(got - ref["u"][s]) <= 2.0 ** -24 * np.abs(ref["u"][s]) + 2.0 ** -149), (k, s)
+
+
+def test_commit_in_a_graph():
+    log("commit graph")
+    S, T = 6, 5
+    w = inputs.make_config(3, B=S, T=T, layers=1, rows_per_table=997)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV)
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    h0 = eg.to_device(w.H, "bf16", DEV)
+    h = h0.clone()
+    st, ref = (eg.DecodeState(S, 3, 1, 9, lay.d, DEV) for _ in range(2))
+    draft, dr = eg.Draft(S, T, L, DEV), eg.Draft(S, T, L, DEV)
+    acc = torch.tensor([-1, 0, 1, 2, 3, 4], dtype=torch.int32, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    eg.forward_draft(tok, h, L, st, draft)   # loads the code; the state is only read
+    with torch.cuda.graph(g):
+        eg.forward_draft(tok, h, L, st, draft)
+        eg.commit_draft(tok, L, draft, acc, st)
+    for i in range(4):
+        acc.copy_(acc.roll(1))
+        h.copy_(h0)
+        g.replay()
+        torch.cuda.synchronize()
+        hr = h0.clone()
+        eg.forward_draft(tok, hr, L, ref, dr)
+        eg.commit_draft(tok, L, dr, acc, ref)
+        assert _same(h, hr) and torch.equal(st.ids, ref.ids) and torch.equal(st.pos, ref.pos) and _same(st.conv, ref.conv), i
+
+
+class _Decoder:
+    """A stand-in model: a token embedding, two Engram layers and the product
+    with the vocabulary, all products in 8-bit integers."""
+
+    def __init__(self, S, vocab=1500):
+        w = inputs.make_config(3, B=S, T=1, rows_per_table=997)
+        self.S, self.vocab, self.d = S, vocab, w.layers[0].d
+        self.layers = [eg.Layer(lay, "bf16", DEV) for lay in w.layers]
+        self.w8 = [eg.Int8Weights(L) for L in self.layers]
+        g = torch.Generator(device=DEV).manual_seed(5)
+        self.emb = torch.randn(vocab, self.d, generator=g, device=DEV).to(torch.bfloat16)
+        self.head = eg.quantize_i8(torch.randn(vocab, self.d, generator=g, device=DEV))
+
+    def states(self):
+        return [eg.DecodeState(self.S, 3, 1, 9, self.d, DEV) for _ in self.layers]
+
+    def logits(self, H):
+        return eg.project_i8(H.view(self.S, -1, self.d), *self.head, out_dtype="f32")
+
+    def step(self, tok, states):
+        H = self.emb[tok.long()].view(self.S, tok.shape[1], 1, self.d).contiguous()
+        for L, w8, st in zip(self.layers, self.w8, states):
+            eg.forward_i8(tok, H, L, w8, state=st)
+        return self.logits(H)
+
+    def chunk(self, tok, states):
+        H = self.emb[tok.long()].view(self.S, tok.shape[1], 1, self.d).contiguous()
+        drafts = []
+        for L, w8, st in zip(self.layers, self.w8, states):
+            drafts.append(eg.Draft(self.S, tok.shape[1], L, DEV, w8=w8))
+            eg.forward_draft(tok, H, L, st, drafts[-1], w8=w8)
+        return self.logits(H), drafts
+
+
+def test_speculative_decode_loop():
+    """Greedy decoding in chunks of drafts of mixed quality, verified and
+    committed, gives the tokens and states of decoding token by token."""
+    log("speculative loop")
+    S, G, new = 5, 4, 16
+    m = _Decoder(S)
+    greedy = torch.zeros(S, device=DEV)
+    rng = torch.Generator(device=DEV).manual_seed(1)
+    start = torch.randint(0, m.vocab, (S, 1), generator=rng, device=DEV, dtype=torch.int32)
+    no_draft, no_u, half = torch.empty((S, 0), dtype=torch.int32, device=DEV), torch.empty((S, 0), device=DEV), \
+        torch.full((S,), 0.5, device=DEV)
+    plain, st = [start], m.states()
+    for _ in range(new + G + 1):             # without drafts the next token comes from the one row there is
+        tok, _ = eg.verify_drafts(eg.token_probs(m.step(plain[-1], st), greedy), None, no_draft, no_u, half)
+        plain.append(tok)
+    plain = torch.cat(plain, 1)
+
+    st = m.states()
+    seqs = [[int(t)] for t in start[:, 0]]
+    accepted = steps = 0
+    while max(len(s) for s in seqs) < new:
+        known = torch.tensor([len(s) for s in seqs], device=DEV)
+        d = plain.gather(1, known[:, None] + torch.arange(G, device=DEV))
+        good = (torch.arange(S, device=DEV) + steps) % (G + 1)          # right for so many tokens, then not
+        d = torch.where(torch.arange(G, device=DEV) < good[:, None], d, (d + 1) % m.vocab).to(torch.int32)
+        last = torch.tensor([[s[-1]] for s in seqs], dtype=torch.int32, device=DEV)
+        chunk = torch.cat([last, d], 1)
+        logits, drafts = m.chunk(chunk, st)
+        tok, acc = eg.verify_drafts(eg.token_probs(logits, greedy), None, d, torch.rand(S, G, device=DEV), half)
+        assert torch.equal(acc.long(), good)
+        for L, s_, dr in zip(m.layers, st, drafts):
+            eg.commit_draft(chunk, L, dr, acc, s_)
+        for s in range(S):
+            seqs[s] += tok[s, :int(acc[s]) + 1].tolist()
+        accepted += int(acc.sum())
+        steps += 1
+    assert accepted > 0
+    for s in range(S):
+        assert seqs[s] == plain[s, :len(seqs[s])].tolist(), s
+
+    # each state has consumed all but the last known token of its sequence
+    ref = m.states()
+    for i in range(max(len(s) for s in seqs) - 1):
+        m.step(plain[:, i:i + 1].contiguous(), ref)
+        for s in range(S):
+            if len(seqs[s]) == i + 2:
+                for a, b in zip(st, ref):
+                    assert int(a.pos[s]) == int(b.pos[s]) == i + 1 and torch.equal(a.ids[s], b.ids[s])
+                # layer 0 sees the same hidden states: v is exact, gamma's sums over d = 1024 run in another
+                # order in a one-token launch (up to 4 * 1024 roundings through the gate and the norm)
+                a, b = st[0].conv[s], ref[0].conv[s]
+                assert torch.all((a - b).abs() <= 4096 * 2.0 ** -24 * b.abs() + 2.0 ** -126), s

@@ -1,0 +1,226 @@
+"""GPU: rows and products in 8-bit integers.  Codes and scales are exact; the
+product's sum is exact, so an output is off by the float32 conversion of the
+sum and two multiplications (3 * 2^-24, second-order terms within a fourth),
+and by half a bf16 step (2^-8) more where it is stored in bf16."""
+import numpy as np
+import pytest
+import torch
+
+from hashed_gram_embedding_amd import engram as eg
+from hashed_gram_embedding_amd import inputs
+from oracle import engram_oracle as orc
+
+from parity import check_bf16_layer, check_f32_layer, log, to_f64
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+TINY = 2.0 ** -126
+
+
+def _bound(ref, out_dtype):
+    rel = 4 * 2.0 ** -24 + (2.0 ** -8 if out_dtype == "bf16" else 0.0)
+    return rel * np.abs(ref) + 2 * TINY
+
+
+def _rows(rng, n, k, dtype):
+    x = (rng.standard_normal((n, k)) * np.exp2(rng.integers(-20, 20, (n, 1)))).astype(np.float32)
+    t = torch.from_numpy(x).to(DEV).to(TYPES[dtype])
+    return t, t.double().cpu().numpy()
+
+
+def _check_rows(q, s, x64):
+    rq, rs = orc.quantize_i8(x64)
+    assert np.array_equal(s.cpu().numpy(), rs, equal_nan=True)
+    assert np.array_equal(q.cpu().numpy(), rq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1), (3, 7), (5, 64), (70, 256), (9, 1000), (33, 1024), (2, 2048), (3, 2049),
+                                   (4, 5003), (1, 16384)])
+def test_quantize_exact(dtype, shape):
+    log(f"quantize_i8 {dtype} {shape}")
+    rng = np.random.default_rng(1)
+    x, x64 = _rows(rng, *shape, dtype)
+    _check_rows(*eg.quantize_i8(x), x64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_borders(dtype):
+    """Ties, equal magnitudes, subnormal rows, zeros, infinities and NaN."""
+    log(f"quantize_i8 borders {dtype}")
+    rng = np.random.default_rng(2)
+    x = rng.standard_normal((12, 130)).astype(np.float32)
+    for r in range(3):                       # x = max / 2 is the tie 63.5 for every max
+        x[r, :] = np.float32(1.0 + r * 0.375) * 0.5
+        x[r, 5] = np.float32(1.0 + r * 0.375)
+        x[r, 6] = -x[r, 5]
+    x[3, :] = np.arange(130) * 0.5           # max 64.5: many near borders
+    x[4, :] = 0.0
+    x[5, :] = 2.0 ** -133 * np.arange(130)   # subnormal in both types
+    x[6, :] = 0.0
+    x[6, 9] = 2.0 ** -149 if dtype == "f32" else 2.0 ** -133
+    x[7, 3] = np.inf
+    x[8, 4] = np.nan
+    x[9, 5] = -np.inf
+    x[9, 6] = np.nan
+    x[10, :] = 3.0e38
+    x[11, :] = np.arange(130) + 125.0        # 254 = 2 * 127: whole and half codes
+    t = torch.from_numpy(x).to(DEV).to(TYPES[dtype])
+    x64 = t.double().cpu().numpy()
+    q, s = eg.quantize_i8(t)
+    _check_rows(q, s, x64)
+    assert torch.isnan(s[7:10]).all() and (q[7:10] == 0).all() and s[4] == 0
+
+
+SIZES = [(1, 16, 1), (1, 1024, 2000), (2, 64, 64), (3, 48, 65), (5, 17, 33), (16, 1024, 4100), (31, 15, 7), (33, 1, 5),
+         (64, 1024, 256), (65, 128, 129), (130, 1000, 515), (200, 2823, 103), (257, 1024, 512), (300, 4096, 192),
+         (1000, 320, 1031), (513, 2048, 2048)]
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("source", ["i8", "bf16", "f32"])
+@pytest.mark.parametrize("size", SIZES)
+def test_product(size, source, out_dtype):
+    n, k, o = size
+    log(f"project_i8 {size} {source} -> {out_dtype}")
+    rng = np.random.default_rng(n * 7 + k * 3 + o)
+    w = rng.integers(-128, 128, (o, k), dtype=np.int8)
+    ws = np.exp2(rng.uniform(-9, 3, o)).astype(np.float32)
+    if source == "i8":
+        q = rng.integers(-128, 128, (n, k), dtype=np.int8)
+        s = np.exp2(rng.uniform(-9, 3, n)).astype(np.float32)
+        e, e_scale = torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)
+    else:
+        e, x64 = _rows(rng, n, k, source)
+        e_scale = None
+        q, s = orc.quantize_i8(x64)
+    out = eg.project_i8(e, torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV), e_scale=e_scale,
+                        out_dtype=out_dtype)
+    ref = orc.project_i8(q, s, w, ws)
+    assert out.dtype == TYPES[out_dtype] and tuple(out.shape) == (n, o)
+    err = np.abs(to_f64(out) - ref)
+    assert np.all(err <= _bound(ref, out_dtype)), float(np.max(err - _bound(ref, out_dtype)))
+
+
+@pytest.mark.parametrize("n", [1, 20, 300])
+def test_product_full_sums(n):
+    """All codes at -128 with the most columns that fit: the sum is 2^31 - 2^14."""
+    log(f"project_i8 full sums n={n}")
+    k, o = 131071, 40
+    e = torch.full((n, k), -128, dtype=torch.int8, device=DEV)
+    w = torch.full((o, k), -128, dtype=torch.int8, device=DEV)
+    one = torch.ones(max(n, o), device=DEV)
+    out = eg.project_i8(e, w, one[:o], e_scale=one[:n], out_dtype="f32")
+    assert (out.double() == float(np.float32(131071 * 16384))).all()
+
+
+@pytest.mark.parametrize("k", [64, 1024, 1000])
+def test_product_of_unaligned_views(k):
+    """Operands that start at any byte: views into larger buffers."""
+    log(f"project_i8 unaligned views k={k}")
+    rng = np.random.default_rng(5)
+    for n, o, off in ((1, 70, 1), (40, 70, 3), (300, 130, 8)):
+        q = rng.integers(-128, 128, (n, k), dtype=np.int8)
+        w = rng.integers(-128, 128, (o, k), dtype=np.int8)
+        bq = torch.zeros(n * k + 16, dtype=torch.int8, device=DEV)
+        bw = torch.zeros(o * k + 16, dtype=torch.int8, device=DEV)
+        e, wt = bq[off:off + n * k].view(n, k), bw[off:off + o * k].view(o, k)
+        e.copy_(torch.from_numpy(q))
+        wt.copy_(torch.from_numpy(w))
+        buf = torch.full((n * o + 2,), 7.0, device=DEV)
+        out = buf[1:1 + n * o].view(n, o)
+        eg.project_i8(e, wt, torch.ones(o, device=DEV), e_scale=torch.ones(n, device=DEV), out_dtype="f32", out=out)
+        assert np.array_equal(to_f64(out), (q.astype(np.int64) @ w.astype(np.int64).T).astype(np.float32))
+        assert buf[0] == 7.0 and buf[-1] == 7.0      # nothing outside the output
+
+
+@pytest.mark.parametrize("n", [1, 2, 40, 300])
+def test_product_of_bad_rows(n):
+    """A row with an infinity or a NaN gives NaN in its outputs and in no other row; a row of zeros gives zeros."""
+    log(f"project_i8 bad rows n={n}")
+    x = torch.randn(n + 3, 256, device=DEV)
+    x[0, 3] = float("inf")
+    x[1, 255] = float("nan")
+    x[2] = 0
+    w = torch.randint(-127, 128, (90, 256), dtype=torch.int8, device=DEV)
+    out = eg.project_i8(x, w, torch.ones(90, device=DEV), out_dtype="f32")
+    assert torch.isnan(out[:2]).all() and (out[2] == 0).all() and torch.isfinite(out[2:]).all()
+    if n == 1:
+        solo = eg.project_i8(x[:1].contiguous(), w, torch.ones(90, device=DEV), out_dtype="bf16")
+        assert torch.isnan(solo).all()
+
+
+def test_empty_products():
+    log("project_i8 empty")
+    w, s = torch.ones((8, 32), dtype=torch.int8, device=DEV), torch.ones(8, device=DEV)
+    assert eg.project_i8(torch.empty((0, 32), device=DEV), w, s).shape == (0, 8)
+    q, sc = eg.quantize_i8(torch.empty((0, 32), device=DEV))
+    assert q.shape == (0, 32) and sc.shape == (0,)
+
+
+def _layer_case(config, hdtype, **kw):
+    w = inputs.make_config(config, rows_per_table=None if config == 0 else 997, **kw)
+    lay = w.layers[0]
+    L = eg.Layer(lay, hdtype, DEV)
+    return w, lay, L, eg.Int8Weights(L)
+
+
+@pytest.mark.parametrize("config,hdtype,kw", [(0, "f32", {}), (1, "bf16", dict(B=2, T=90)), (1, "bf16", dict(B=1, T=1)),
+                                              (2, "bf16", dict(B=2, T=33)), (3, "bf16", dict(B=16, T=1, layers=1))])
+def test_layer_matches_oracle(config, hdtype, kw):
+    """The layer with Step 5 in 8-bit integers against the oracle's."""
+    log(f"forward_i8 config {config} {kw}")
+    w, lay, L, w8 = _layer_case(config, hdtype, **kw)
+    H = eg.to_device(w.H, hdtype, DEV)
+    alpha, y = eg.forward_i8(torch.from_numpy(w.tokens).to(DEV), H, L, w8, want_alpha=True, want_y=True)
+    ref = orc.forward(w.tokens, w.H, lay, hdtype, gemm="int8")
+    check, h_in = (check_bf16_layer, orc.bf16_to_f64(w.H)) if hdtype == "bf16" else (check_f32_layer, w.H.astype(np.float64))
+    check(to_f64(alpha), ref["alpha"], to_f64(y), ref["Y"], to_f64(H), h_in, tag=f"int8 config {config}")
+
+
+def test_layer_decode_state():
+    """A prefill and single-token steps with the int8 layer against the oracle run over the same chunks."""
+    log("forward_i8 decode")
+    w = inputs.make_config(3, B=8, T=3, layers=1, context_len=12, rows_per_table=997)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    st = eg.DecodeState(8, 3, 1, 9, lay.d, DEV)
+    ref = orc.new_state(8, 3, 1, 9, lay.d)
+    chunks = [(w.context, w.H_context)] + [(w.tokens[:, t:t + 1], w.H[:, t:t + 1]) for t in range(3)]
+    for i, (tk, Hn) in enumerate(chunks):
+        H = eg.to_device(Hn, "bf16", DEV)
+        alpha, y = eg.forward_i8(torch.from_numpy(np.ascontiguousarray(tk)).to(DEV), H, L, w8, state=st,
+                                 want_alpha=True, want_y=True)
+        r = orc.forward(tk, Hn, lay, "bf16", state=ref, gemm="int8")
+        ref = r["state"]
+        check_bf16_layer(to_f64(alpha), r["alpha"], to_f64(y), r["Y"], to_f64(H), orc.bf16_to_f64(Hn), tag=f"chunk {i}")
+    assert np.array_equal(st.ids.cpu().numpy(), ref["ids"]) and np.array_equal(st.pos.cpu().numpy(), ref["pos"])
+
+
+def test_product_in_a_graph_and_on_another_stream():
+    """Captured and replayed between eager calls; then on a stream of its own."""
+    log("project_i8 graph")
+    for n in (1, 24, 300):
+        x = torch.randn(n, 1000, device=DEV).to(torch.bfloat16)
+        w = torch.randint(-127, 128, (515, 1000), dtype=torch.int8, device=DEV)
+        s = torch.rand(515, device=DEV)
+        out = torch.empty((n, 515), device=DEV)
+        ws = torch.empty(max(eg.lib().engram_project_i8_workspace(n, 1000, eg.BF16), 256), dtype=torch.uint8, device=DEV)
+        call = lambda: eg.project_i8(x, w, s, out_dtype="f32", out=out, ws=ws)   # noqa: E731
+        call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        for i in range(3):
+            x.copy_(torch.randn(n, 1000, device=DEV))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, eg.project_i8(x, w, s, out_dtype="f32")), i
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = eg.project_i8(x, w, s, out_dtype="f32", stream=side)
+        side.synchronize()
+        assert torch.equal(got, out)

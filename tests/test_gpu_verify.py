@@ -1,0 +1,209 @@
+"""GPU: token probabilities and the verification of drafted tokens.
+
+Probabilities: the exponent (l - max) log2(e) / T is formed with four
+roundings (difference, the factor's constant, division and product), so the
+exponential is off by ln 2 * 4 * 2^-24 * |exponent| and by the two units of
+the hardware's exp2; the sum by the length of its longest chain of additions
+(at most V / 64 + 32 of them); reciprocal and product by 2 * 2^-24.  Results
+below the smallest normal number may be flushed.
+
+Verification is exact: accepted counts and tokens are equal."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from hashed_gram_embedding_amd import engram as eg
+from oracle import engram_oracle as orc
+
+from parity import log
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+INF, NAN = float("inf"), float("nan")
+
+
+def _check_probs(p, logits, temps):
+    x, got = logits.double().cpu().numpy(), p.double().cpu().numpy()
+    S, R, V = x.shape
+    for s in range(S):
+        t = 1.0 if temps is None else float(temps[s])
+        for r in range(R):
+            ref = orc.token_probs(x[s, r], t)
+            assert np.array_equal(np.isnan(ref), np.isnan(got[s, r])), (s, r)
+            if np.isnan(ref).any():
+                continue
+            if t > 0 and np.isfinite(x[s, r].max()):
+                arg = np.where(np.isfinite(x[s, r]), (x[s, r].max() - x[s, r]) / t / math.log(2), 0.0)
+                # the exponentials' error enters each term, and through the sum the weighted mean of it
+                own = 2.0 ** -24 * (4 * math.log(2) * arg + 4)
+                rel = own + np.sum(ref * own) + 2.0 ** -24 * (V / 64 + 32 + 2)
+            else:
+                rel = 0.0
+            err = np.abs(got[s, r] - ref)
+            assert np.all(err <= rel * ref + 2.0 ** -125), (s, r, float(np.max(err - rel * ref)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 3, 5), (1, 5, 1000), (3, 2, 4096), (2, 2, 4097), (1, 4, 32001),
+                                   (40, 8, 2049), (1, 1, 128000), (300, 1, 515), (2, 1, 300001)])
+def test_probs(dtype, shape):
+    log(f"token_probs {dtype} {shape}")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = (4 * torch.randn(shape, generator=g, device=DEV)).to(TYPES[dtype])
+    t = 0.3 + torch.rand(shape[0], generator=g, device=DEV)
+    if shape[0] > 1:
+        t[0] = 0.0
+    _check_probs(eg.token_probs(x, t), x, t)
+    if x.numel() < 1 << 18:
+        _check_probs(eg.token_probs(x), x, None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [3, 700, 9000, 40000])
+def test_probs_of_masked_and_bad_rows(dtype, V):
+    """Rows that a mask leaves empty or with one entry, the type's lowest value as a mask, infinities, NaN, ties."""
+    log(f"token_probs masked {dtype} V={V}")
+    x = torch.randn(2, 9, V, device=DEV).to(TYPES[dtype])
+    x[:, 0] = -INF
+    x[:, 1] = -INF
+    x[:, 1, V - 1] = -5.0
+    x[:, 2] = torch.finfo(TYPES[dtype]).min
+    x[:, 3, V // 2:] = torch.finfo(TYPES[dtype]).min
+    x[:, 4, 1] = INF
+    x[:, 5, V - 1] = NAN
+    x[:, 6] = 2.5                            # all tied
+    x[:, 7, 2] = 1000.0
+    x[:, 8, 0] = -INF
+    t = torch.tensor([0.7, 0.0], device=DEV)
+    p = eg.token_probs(x, t)
+    _check_probs(p, x, t)
+    assert (p[:, 0] == 0).all() and torch.isnan(p[:, 5]).all() and torch.isnan(p[0, 4]).all()
+    assert p[1, 4, 1] == 1 and p[1, 6, 0] == 1 and p[0, 1, V - 1] == 1
+
+
+def test_probs_of_padded_rows():
+    """Rows of a padded vocabulary: the padding is not read, whatever it holds."""
+    log("token_probs padded")
+    for V, ld in ((515, 520), (4099, 4100), (32001, 32064)):
+        x = torch.full((2, 3, ld), NAN, device=DEV)
+        x[..., :V] = torch.randn(2, 3, V, device=DEV)
+        t = torch.tensor([0.8, 0.0], device=DEV)
+        assert torch.equal(eg.token_probs(x[..., :V], t), eg.token_probs(x[..., :V].contiguous(), t))
+
+
+def _verify_both(p, q, drafted, ua, us, n=None):
+    tok, acc = eg.verify_drafts(p, q, drafted, ua, us, n_draft=n)
+    p64 = p.double().cpu().numpy()
+    q64 = None if q is None else q.double().cpu().numpy()
+    S, G = drafted.shape
+    d, a64, s64 = drafted.cpu().numpy(), ua.double().cpu().numpy(), us.double().cpu().numpy()
+    for s in range(S):
+        rt, ra = orc.verify_drafts(p64[s], None if q64 is None else q64[s], d[s], a64[s], s64[s],
+                                   G if n is None else int(n[s]))
+        assert int(acc[s]) == ra, s
+        assert np.array_equal(tok[s].cpu().numpy(), rt), (s, tok[s], rt)
+    return tok, acc
+
+
+def _case(S, G, V, dtype, sampled, seed=0, sharp=2.5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = sharp * torch.randn(S, G + 1, V, generator=g, device=DEV)
+    p = torch.softmax(x, -1).to(TYPES[dtype])
+    q = torch.softmax(x[:, :G] + 0.5 * torch.randn(S, G, V, generator=g, device=DEV), -1).to(TYPES[dtype])
+    drafted = torch.multinomial(q.float().view(S * G, V), 1, generator=g).view(S, G).to(torch.int32) if G else \
+        torch.empty((S, 0), dtype=torch.int32, device=DEV)
+    ua = torch.rand(S, G, generator=g, device=DEV)
+    if not sampled:
+        ua = ua * 0.02
+    return p, (q if sampled else None), drafted, ua, torch.rand(S, generator=g, device=DEV)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sampled", [True, False])
+@pytest.mark.parametrize("size", [(1, 1, 1), (3, 2, 5), (1, 4, 32001), (7, 7, 4095), (5, 3, 4096), (5, 3, 4097), (64, 5, 1000),
+                                  (300, 2, 777), (2, 64, 130), (2, 1, 128000), (3, 0, 900), (1, 2, 600011)])
+def test_verify(size, sampled, dtype):
+    log(f"verify {size} sampled={sampled} {dtype}")
+    S, G, V = size
+    p, q, d, ua, us = _case(S, G, V, dtype, sampled, seed=S + G)
+    _verify_both(p, q, d, ua, us)
+    n = torch.randint(-1, G + 3, (S,), device=DEV, dtype=torch.int32)
+    _verify_both(p, q, d, ua, us, n)
+
+
+@pytest.mark.parametrize("V", [6, 5000, 70000])
+@pytest.mark.parametrize("S", [4, 200])
+def test_verify_borders(V, S):
+    """Random numbers at both ends, one-hot and dyadic rows, drafts outside the vocabulary, rows that leave nothing."""
+    log(f"verify borders V={V} S={S}")
+    top = 1.0 - 2.0 ** -24
+    for us_v in (0.0, 0.5, top):
+        us = torch.full((S,), us_v, device=DEV)
+        p = torch.zeros(S, 3, V, device=DEV)
+        p[:, 0, V - 1] = 0.5                                   # two equal halves at both ends
+        p[:, 0, 0] = 0.5
+        p[:, 1, V // 2] = 1.0
+        p[:, 2, V // 3] = 0.25
+        p[:, 2, V - 2] = 0.75
+        q = torch.zeros(S, 2, V, device=DEV)
+        q[:, :, 0] = 1.0
+        d = torch.zeros(S, 2, dtype=torch.int32, device=DEV)
+        d[1, 0], d[2, 0], d[3, 0] = V, -1, V - 1
+        for ua_v in (0.0, 0.5, top):
+            ua = torch.full((S, 2), ua_v, device=DEV)
+            _verify_both(p, q, d, ua, us)
+            _verify_both(p, None, d, ua, us)
+            _verify_both(p, 2 * p[:, :2].contiguous(), torch.full_like(d, V // 2), ua, us)   # p - q leaves nothing
+        z = torch.zeros_like(p)
+        tok, acc = _verify_both(z, q, d, ua, us)               # rows of zeros: no token
+        assert (tok == -1).all() and (acc == 0).all()
+        z[:, :, 2] = NAN
+        z[:, :, 4] = 0.125
+        tok, _ = _verify_both(z, None, d, ua, us)              # a NaN counts as nothing
+        assert (tok[:, 0] == 4).all()
+        z[:, :, 3] = INF
+        assert (eg.verify_drafts(z, None, d, ua, us)[0][:, 0] == -1).all()
+
+
+def test_verify_in_a_graph_and_on_another_stream():
+    log("verify graph")
+    for S, V in ((1, 32001), (300, 4000)):
+        p, q, d, ua, us = _case(S, 4, V, "f32", True)
+        x = torch.randn(S, 5, V, device=DEV)
+        t = torch.rand(S, device=DEV) + 0.5
+        eg.verify_drafts(p, q, d, ua, us)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            probs = eg.token_probs(x, t)
+            tok, acc = eg.verify_drafts(probs, q, d, ua, us)
+        for i in range(4):
+            x.copy_(torch.log(p) + 0.3 * torch.randn(S, 5, V, device=DEV))
+            us.copy_(torch.rand(S, device=DEV))
+            g.replay()
+            torch.cuda.synchronize()
+            et, ea = eg.verify_drafts(eg.token_probs(x, t), q, d, ua, us)
+            assert torch.equal(tok, et) and torch.equal(acc, ea), i
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        st, sa = eg.verify_drafts(eg.token_probs(x, t, stream=side), q, d, ua, us, stream=side)
+        side.synchronize()
+        assert torch.equal(st, et) and torch.equal(sa, ea)
+
+
+def test_verified_tokens_follow_the_target():
+    """Over many random numbers the next token is distributed as the target says, accepted or not."""
+    log("verify distribution")
+    V, n = 7, 60000
+    g = torch.Generator(device=DEV).manual_seed(9)
+    p1 = torch.softmax(torch.randn(2, V, generator=g, device=DEV), -1)
+    q1 = torch.softmax(torch.randn(1, V, generator=g, device=DEV), -1)
+    p, q = p1.expand(n, 2, V).contiguous(), q1.expand(n, 1, V).contiguous()
+    d = torch.multinomial(q1.expand(n, V), 1, generator=g).to(torch.int32)
+    tok, _ = eg.verify_drafts(p, q, d, torch.rand(n, 1, generator=g, device=DEV), torch.rand(n, generator=g, device=DEV))
+    got = torch.bincount(tok[:, 0].long(), minlength=V).double().cpu() / n
+    # six standard deviations of each share
+    assert (got - p1[0].double().cpu()).abs().max() < 6 * math.sqrt(0.25 / n)
