@@ -8,6 +8,9 @@
 // The sum is exact in int32 (|q|, |w| <= 128 and at most 131071 columns), so
 // its order is free: the kernels permute and split the columns as it suits
 // them and results do not depend on it.
+#include <algorithm>
+#include <atomic>
+
 #include "device_util.h"
 #include "engram_internal.h"
 
@@ -15,6 +18,8 @@ namespace engram {
 namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
@@ -174,6 +179,270 @@ project_i8_kernel(ProjectI8Args a) {
   }
 }
 
+
+// Tiled product for the sizes that fill the chip.  A workgroup of WF x WT
+// wavefronts forms TF outputs x TT tokens; W rows are the A operand of
+// v_mfma_i32_32x32x32_i8 and token rows the B operand, so a lane ends with
+// runs of four consecutive outputs of one token.  Columns come in slices of
+// 128 through two LDS buffers: while one is multiplied the next is in flight.
+// Chunk c (16 bytes) of a slice's row r lies at c ^ ((r >> 1) & 7), so that
+// the operand reads of 16 lanes (16 rows, one chunk) spread over all banks.
+//
+// Workgroups are persistent: each walks its share of the tiles, and the first
+// slice of the next tile is on its way while the last one of this tile is
+// multiplied and its outputs are scaled and stored.  (One workgroup per tile
+// left the matrix cores idle at both ends of every tile: with 1024 columns a
+// tile has 8 slices, and 32763 x 1024 x 5120 took 227 us instead of 195.)
+// Tiles go to the XCDs in contiguous shares, the operand with fewer bytes
+// fastest within a share, so that it is re-read from the XCD's L2 and the
+// larger one is read once.
+//
+// DIRECT: slices go from memory straight into LDS (both operands 16-byte
+// aligned, whole chunks).  Otherwise through registers, at any alignment.
+template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
+__global__ void __launch_bounds__(64 * WF * WT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t, int f_fastest) {
+  constexpr int NT = 64 * WF * WT;
+  constexpr int I = TF / WF / 32, J = TT / WT / 32;   // 32 x 32 blocks of a wavefront
+  constexpr int WC = TF * 8, QC = TT * 8;             // chunks of a slice
+  constexpr int NW = WC / NT, NQ = QC / NT;           // chunks a thread loads
+  constexpr int RC = TF / WF * static_cast<int>(sizeof(OutT)) / 16;   // chunks of a wavefront's output row
+  static_assert(RC >= 8 && (RC & (RC - 1)) == 0 && WF * WT * 32 * RC <= WC + QC, "outputs turn around in one buffer");
+  static_assert((TF + TT) % NT == 0 || NT % (TF + TT) == 0, "scales per thread");
+  extern __shared__ u32x4_t lds[];
+  float* const sc = reinterpret_cast<float*>(lds + 2 * (WC + QC));   // [2][TF + TT] scales: outputs, then tokens
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wf = wave % WF, wt = wave / WF, lr = lane & 31, lh = lane >> 5;
+  const int K = a.K, chunks = (K + 15) / 16, ksteps = (chunks + 7) / 8;
+  const int n_tiles = tiles_f * tiles_t, share = (n_tiles + 7) / 8;
+  const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+
+  struct Tile {
+    int64_t f0, t0;
+  };
+  auto tile_of = [&](int local, Tile* t) {
+    const int id = xcd * share + local;
+    if (local >= share || id >= n_tiles) return false;
+    t->f0 = static_cast<int64_t>(f_fastest ? id % tiles_f : id / tiles_t) * TF;
+    t->t0 = static_cast<int64_t>(f_fastest ? id / tiles_f : id % tiles_t) * TT;
+    return true;
+  };
+
+  // This thread's chunk of a slice: row r0 (and every NT / 8 rows from there),
+  // source chunk ch, into LDS slot tid.  The rows of one thread are 16 n
+  // apart, so one source chunk serves all of them.
+  static_assert(NT / 8 % 16 == 0, "the swizzle repeats every 16 rows");
+  const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
+  const int ldq = static_cast<int>(a.ldq);
+
+  // Direct: rows past the operand's end and chunks past the last one are out
+  // of the buffer's range and read as zeros (a W chunk past the row's end may
+  // read the next row instead: the tokens' zeros leave it out).
+  auto issue = [&](const Tile& t, int kt, int buf) {
+    const int w_bytes = static_cast<int>(min(static_cast<int64_t>(TF), a.n_out - t.f0)) * K;
+    const int q_bytes = static_cast<int>(min(static_cast<int64_t>(TT), a.n_tok - t.t0)) * ldq;
+    const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.w + t.f0 * K), 0, w_bytes, 0x00020000);
+    const auto rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q + t.t0 * ldq), 0, q_bytes, 0x00020000);
+    u32x4_t* dst = lds + buf * (WC + QC) + wave * 64;
+    const bool in = kt * 8 + ch < chunks;
+    const int wo = r0 * K + ch * 16, qo = in ? r0 * ldq + ch * 16 : 0x7fff0000;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(dst + i * NT), 16,
+                                               wo + i * (NT / 8) * K, kt * 128, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (__attribute__((address_space(3))) void*)(dst + WC + i * NT), 16,
+                                               in ? qo + i * (NT / 8) * ldq : qo, kt * 128, 0, 0);
+  };
+  // Through registers: load() early, store() once the buffer is free.
+  u32x4_t vw[DIRECT ? 1 : NW], vq[DIRECT ? 1 : NQ];
+  auto load = [&](const Tile& t, int kt) {
+    const int c = kt * 8 + ch;
+#pragma unroll
+    for (int i = 0; i < (DIRECT ? 0 : NW); ++i)
+      vw[i] = load_chunk(a.w + min(t.f0 + r0 + i * (NT / 8), a.n_out - 1) * K, min(c, chunks - 1), K);
+#pragma unroll
+    for (int i = 0; i < (DIRECT ? 0 : NQ); ++i) {
+      const int8_t* row = a.q + min(t.t0 + r0 + i * (NT / 8), a.n_tok - 1) * a.ldq;
+      vq[i] = u32x4_t{0, 0, 0, 0};
+      if (c < chunks) vq[i] = a.tailed ? *reinterpret_cast<const u32x4_t*>(row + c * 16) : load_chunk_once(row, c, K);
+    }
+  };
+  auto store = [&](int buf) {
+    u32x4_t* dst = lds + buf * (WC + QC) + tid;
+#pragma unroll
+    for (int i = 0; i < (DIRECT ? 0 : NW); ++i) dst[i * NT] = vw[i];
+#pragma unroll
+    for (int i = 0; i < (DIRECT ? 0 : NQ); ++i) dst[WC + i * NT] = vq[i];
+  };
+  auto scales = [&](const Tile& t, int par) {
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (int b = 0; b < (TF + TT) / 64; b += WF * WT) {
+        const int seg = b + wave;   // 64 scales per wavefront instruction
+        if (seg < (TF + TT) / 64) {
+          const int r = seg * 64 + lane;
+          const float* src = seg < TF / 64 ? a.w_scale + min(t.f0 + r, a.n_out - 1) : a.q_scale + min(t.t0 + (r - TF), a.n_tok - 1);
+          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                           (__attribute__((address_space(3))) void*)(sc + par * (TF + TT) + seg * 64), 4, 0, 0);
+        }
+      }
+    } else {
+      for (int r = tid; r < TF + TT; r += NT)
+        sc[par * (TF + TT) + r] = r < TF ? a.w_scale[min(t.f0 + r, a.n_out - 1)] : a.q_scale[min(t.t0 + (r - TF), a.n_tok - 1)];
+    }
+  };
+
+  Tile cur, next{0, 0};
+  int local = blockIdx.x >> 3;
+  if (!tile_of(local, &cur)) return;
+  int buf = 0, par = 0;
+  scales(cur, 0);
+  if constexpr (DIRECT) {
+    issue(cur, 0, 0);
+  } else {
+    load(cur, 0);
+    store(0);
+  }
+  for (;;) {
+    i32x16_t acc[I][J];
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    local += stride;
+    const bool more = tile_of(local, &next);
+    for (int kt = 0; kt < ksteps; ++kt) {
+      // this lane's part of the slice has landed and its reads of the other
+      // buffer are done; after the barrier, every lane's
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const bool same = kt + 1 < ksteps;
+      if constexpr (DIRECT) {
+        if (same) {
+          issue(cur, kt + 1, buf ^ 1);
+        } else if (more) {
+          issue(next, 0, buf ^ 1);
+          scales(next, par ^ 1);
+        }
+      } else {
+        if (same || more) load(same ? cur : next, same ? kt + 1 : 0);
+        if (!same && more) scales(next, par ^ 1);
+      }
+      const u32x4_t* Ws = lds + buf * (WC + QC);
+      const u32x4_t* Qs = Ws + WC;
+      if constexpr (DIRECT) __builtin_amdgcn_iglp_opt(0);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const int kc = (ks * 2 + lh) ^ ((lr >> 1) & 7);
+        i32x4_t fa[I], fb[J];
+#pragma unroll
+        for (int i = 0; i < I; ++i) fa[i] = __builtin_bit_cast(i32x4_t, Ws[(wf * (TF / WF) + i * 32 + lr) * 8 + kc]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) fb[j] = __builtin_bit_cast(i32x4_t, Qs[(wt * (TT / WT) + j * 32 + lr) * 8 + kc]);
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int j = 0; j < J; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      }
+      if constexpr (!DIRECT) {
+        if (same || more) store(buf ^ 1);
+      }
+      buf ^= 1;
+    }
+    // Outputs: every wavefront turns a block of 32 tokens around in its part
+    // of the buffer that was multiplied last, so that it stores runs of
+    // TF / WF outputs of one token.  acc[i][j][4g + e] is output 32i + 8g +
+    // 4 lh + e of token 32j + lr.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the buffer's last reads are done
+    u32x4_t* E = lds + (buf ^ 1) * (WC + QC) + wave * 32 * RC;
+    const float* sw = sc + par * (TF + TT) + wf * (TF / WF);
+    const float* sq = sc + par * (TF + TT) + TF + wt * (TT / WT);
+    constexpr int EPC = 16 / static_cast<int>(sizeof(OutT));   // outputs of a chunk
+    const int64_t fw = cur.f0 + wf * (TF / WF);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float st = sq[j * 32 + lr];
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t s4 = *reinterpret_cast<const f32x4_t*>(sw + i * 32 + g * 8 + lh * 4);
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(acc[i][j][4 * g + e]) * st * s4[e];
+          if constexpr (sizeof(OutT) == 2)
+            reinterpret_cast<u32x2_t*>(E + lr * RC + ((i * 4 + g) ^ (lr & 7)))[lh] = u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+          else
+            E[lr * RC + ((i * 8 + g * 2 + lh) ^ (lr & 7))] = __builtin_bit_cast(u32x4_t, f32x4_t{x[0], x[1], x[2], x[3]});
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wavefront's block is in LDS
+      constexpr int NIT = 32 * RC / 64;
+      u32x4_t v[NIT];
+#pragma unroll
+      for (int it = 0; it < NIT; ++it) {
+        const int rr = (it * 64 + lane) / RC, c = (it * 64 + lane) % RC;
+        v[it] = E[rr * RC + (c ^ (rr & 7))];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and read, before the next block's writes
+#pragma unroll
+      for (int it = 0; it < NIT; ++it) {
+        const int rr = (it * 64 + lane) / RC, c = (it * 64 + lane) % RC;
+        const int64_t tok = cur.t0 + wt * (TT / WT) + j * 32 + rr, o = fw + c * EPC;
+        if (tok < a.n_tok && o < a.n_out) {
+          OutT* dst = static_cast<OutT*>(a.out) + tok * a.n_out + o;
+          if (o + EPC <= a.n_out) {
+            __builtin_memcpy(dst, &v[it], 16);
+          } else {
+            const int left = static_cast<int>(a.n_out - o);
+#pragma unroll
+            for (int e = 0; e < EPC - 1; ++e) {
+              OutT x;
+              if constexpr (sizeof(OutT) == 2) x = static_cast<uint16_t>(v[it][e >> 1] >> (16 * (e & 1)));
+              else x = __uint_as_float(v[it][e]);
+              if (e < left) dst[e] = x;
+            }
+          }
+        }
+      }
+    }
+    if (!more) break;
+    cur = next;
+    par ^= 1;
+  }
+}
+
+template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
+hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
+  constexpr int kLds = 2 * (TF + TT) * 128 + 2 * (TF + TT) * 4;
+  auto* const fn = project_i8_tile_kernel<OutT, TF, TT, WF, WT, DIRECT>;
+  static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((attr_set.load() & bit) == 0) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+    attr_set.fetch_or(bit);
+  }
+  const int64_t tf = (a.n_out + TF - 1) / TF, tt = (a.n_tok + TT - 1) / TT;
+  if (tf * tt > (1 << 30)) return hipErrorInvalidValue;
+  // one workgroup of 8 wavefronts per CU, or two of 4
+  const int grid = static_cast<int>(std::min<int64_t>(256 * 8 / (WF * WT), (tf * tt + 7) / 8 * 8));
+  launch_k(fn, dim3(grid), dim3(64 * WF * WT), kLds, s, a, static_cast<int>(tf), static_cast<int>(tt), a.n_out <= a.n_tok ? 1 : 0);
+  return hipGetLastError();
+}
+
+template <typename OutT, bool DIRECT>
+hipError_t launch_tiles(const ProjectI8Args& a, hipStream_t s) {
+  if (((a.n_out + 255) / 256) * ((a.n_tok + 255) / 256) >= 256) return launch_tile<OutT, 256, 256, 4, 2, DIRECT>(a, s);
+  return launch_tile<OutT, 128, 128, 2, 2, DIRECT>(a, s);
+}
+
 }  // namespace
 
 int64_t i8_row_stride(int64_t cols) { return (cols + 15) / 16 * 16; }
@@ -196,6 +465,11 @@ hipError_t launch_project_i8(const int8_t* q, int64_t ldq, bool tailed, const fl
                              hipStream_t s) {
   if (n_tok == 0) return hipSuccess;
   const ProjectI8Args a{q, q_scale, w, w_scale, out, n_tok, ldq, n_out, static_cast<int>(K), tailed ? 1 : 0};
+  const bool direct = K % 16 == 0 && ldq % 16 == 0 && (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(w)) % 16 == 0;
+  if (n_tok > 64 && n_out > 64) {
+    if (out_dtype == ENGRAM_BF16) return direct ? launch_tiles<uint16_t, true>(a, s) : launch_tiles<uint16_t, false>(a, s);
+    return direct ? launch_tiles<float, true>(a, s) : launch_tiles<float, false>(a, s);
+  }
   const int64_t tiles = ((n_out + 63) / 64) * ((n_tok + 63) / 64);
   if (tiles > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(tiles));
