@@ -583,20 +583,20 @@ engram_status run_retrieve(const int32_t* tokens, int64_t B, int64_t T, const en
 engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, const int8_t* w, const float* w_scale,
                              int64_t n_tok, int64_t d_mem, int64_t n_out, int out_dtype, void* out, int8_t* codes,
                              float* scale, hipStream_t stream) {
-  const int8_t* q = static_cast<const int8_t*>(e);
   int64_t ldq = d_mem;
-  const bool tailed = e_dtype != ENGRAM_I8;
+  const bool tailed = e_dtype != ENGRAM_I8 && !engram::project_i8_quantizes(n_tok, d_mem);
   if (tailed) {
     ldq = engram::i8_row_stride(d_mem);
     prof_mark(stream, "quantize_i8_kernel");
     const engram_status r = hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, codes, ldq, true, scale, stream),
                                        "quantize_i8 launch");
     if (r != ENGRAM_OK) return r;
-    q = codes;
+    e = codes;
+    e_dtype = ENGRAM_I8;
     e_scale = scale;
   }
   prof_mark(stream, "project_i8_kernel");
-  return hip_status(engram::launch_project_i8(q, ldq, tailed, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out,
+  return hip_status(engram::launch_project_i8(e, e_dtype, ldq, tailed, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out,
                                               stream),
                     "project_i8 launch");
 }
@@ -1261,7 +1261,7 @@ ENGRAM_API engram_status engram_quantize_i8(const void* x, engram_dtype dtype, i
 }
 
 ENGRAM_API size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, engram_dtype e_dtype) {
-  if (n_tok < 1 || d_mem < 1 || e_dtype == ENGRAM_I8) return 0;
+  if (n_tok < 1 || d_mem < 1 || e_dtype == ENGRAM_I8 || engram::project_i8_quantizes(n_tok, d_mem)) return 0;
   Carve c{nullptr};
   carve_codes(c, n_tok, d_mem);
   return c.used;
@@ -1495,10 +1495,10 @@ ENGRAM_API engram_status engram_verify_drafts(const void* target, const void* dr
       !aligned(n_draft, 4) || !aligned(u_accept, 4) || !aligned(u_sample, 4) || !aligned(tokens, 4) || !aligned(n_accepted, 4))
     return fail(ENGRAM_EINVAL, "verify_drafts: every buffer must be aligned to its elements");
   const size_t need = engram_verify_drafts_workspace(S, V);
-  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
     return fail(ENGRAM_EINVAL, "verify_drafts: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
   prof_begin();
-  prof_mark(stream, "verify_sums_kernel");
+  prof_mark(stream, "verify_drafts_kernel");
   const engram_status r = hip_status(engram::launch_verify(target, draft, dtype, drafted, n_draft, u_accept, u_sample, S, G, V, tokens,
                                                            n_accepted, ws, stream),
                                      "verify_drafts launch");

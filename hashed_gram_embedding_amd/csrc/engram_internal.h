@@ -332,8 +332,12 @@ int64_t i8_row_stride(int64_t cols);
 // (ldq = i8_row_stride(cols)); otherwise the rows are plain.
 hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail,
                               float* scale, hipStream_t s);
-// Product of int8 codes q [n_tok][ldq] (tailed: in the layout above) with W.
-hipError_t launch_project_i8(const int8_t* q, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
+// Whether the product of float rows quantises them itself (few rows that fit
+// in LDS); otherwise launch_quantize_i8 comes first.
+bool project_i8_quantizes(int64_t n_tok, int64_t K);
+// Product with W of int8 codes [n_tok][ldq] (tailed: in the layout above; with
+// q_scale) or, where project_i8_quantizes, of float rows [n_tok][K].
+hipError_t launch_project_i8(const void* e, int e_dtype, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
                              const float* w_scale, int64_t n_tok, int64_t K, int64_t n_out, int out_dtype, void* out,
                              hipStream_t s);
 hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,

@@ -29,56 +29,136 @@ __device__ __forceinline__ float load_f32(const void* x, int64_t i, int dtype) {
   return dtype == ENGRAM_BF16 ? bf16_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
 }
 
-// rne(127 x / top) of exact arithmetic, for |x| <= top.  x * (127 / top) in
-// float is off by less than 2^-15; only where that could change the rounding
-// (or 127 / top overflows: top below 2^-120) is the quotient formed in
-// double, whose error of 2^-53 cannot: 127 x / top is a ratio of numbers of
-// 31 and 24 bits, so it is a tie or at least 2^-26 away from one.
-__device__ __forceinline__ int quantize(float x, float top, float inv) {
-  const float y = x * inv;
-  float r = rintf(y);
-  if (!(fabsf(y - r) < 0.5f - 1.0f / 8192.0f)) r = static_cast<float>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(top)));
-  return static_cast<int>(r);
+// What quantising a row needs: its largest magnitude, and 127 over it.  Both
+// and the values are scaled by g, a power of two that keeps 127 / top finite
+// for rows of the smallest numbers (exact: nothing is rounded by it).
+struct RowScale {
+  float top, inv, g;
+};
+
+__device__ __forceinline__ RowScale row_factors(float top) {
+  const float g = top < 0x1p-60f ? 0x1p80f : 1.0f;
+  return RowScale{top * g, 127.0f / (top * g), g};
 }
 
-// One row per group of THREADS lanes.  Codes go to q [rows][ldq].  With
-// `tail` the last, incomplete run of 16 columns is stored right-aligned in
-// its 16 bytes (zeros before it): the product reads W's last 16 columns there
-// (load_chunk) and the zeros leave out those already counted.  A row of zeros
-// has scale 0; one holding an infinity or a NaN has codes 0 and scale NaN, so
-// its products are NaN.
-template <int THREADS>
-__global__ void __launch_bounds__(256)
-quantize_kernel(const void* __restrict__ x, int dtype, int64_t rows, int cols, int8_t* __restrict__ q, int64_t ldq,
-                int tail, float* __restrict__ scale) {
-  __shared__ uint32_t part[4];
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / THREADS;
-  const int t = threadIdx.x % THREADS;
-  if (row >= rows) return;   // whole groups leave together
-  const int64_t base = row * cols;
-  // largest magnitude by its bits: an infinity and a NaN order above every
-  // finite value
-  uint32_t top = 0;
-  for (int c = t; c < cols; c += THREADS) top = max(top, __float_as_uint(load_f32(x, base + c, dtype)) & 0x7fffffffu);
+// rne(127 x / top) of exact arithmetic, for |x| <= top.  In float y = x *
+// (127 / top) is off by less than 2^-15.  Only within 2^-13 of the middle m
+// of two whole numbers could that change the rounding; there 127 x is
+// compared with m top, both exact in double (31 and 32 bits).
+__device__ __forceinline__ int quantize(float x, const RowScale& r) {
+  const float v = x * r.g, y = v * r.inv, n = floorf(y);
+  float q = rintf(y);
+  if (fabsf(y - n - 0.5f) < 0x1p-13f) {
+    const double d = 127.0 * static_cast<double>(v) - (static_cast<double>(n) + 0.5) * static_cast<double>(r.top);
+    const float even = 2.0f * rintf(0.5f * (n + 0.5f));   // n or n + 1
+    q = d > 0.0 ? n + 1.0f : (d < 0.0 ? n : even);
+  }
+  return static_cast<int>(q);
+}
+
+// Largest magnitude of values held by a group of wavefronts, by its bits: an
+// infinity and a NaN order above every finite value.
+__device__ __forceinline__ uint32_t wave_top(uint32_t top) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off, 64)));
-  if constexpr (THREADS > 64) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = max(max(part[0], part[1]), max(part[2], part[3]));
+  return top;
+}
+
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  return top < 0x7f800000u ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7fc00000u);
+}
+
+// Codes of a row whose largest magnitude is `top` (its bits): none where the
+// row is zero or holds an infinity or a NaN.
+__device__ __forceinline__ bool row_has_codes(uint32_t top) { return top != 0u && top < 0x7f800000u; }
+
+// Eight values of a row, 16-byte aligned.
+template <int DT>
+__device__ __forceinline__ void load8(const void* x, int64_t i, float* f) {
+  if constexpr (DT == ENGRAM_BF16) {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i), f);
+  } else {
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(x) + i);
+    const f32x4_t a = p[0], b = p[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[k] = a[k];
+      f[4 + k] = b[k];
+    }
   }
-  const bool finite = top < 0x7f800000u;
-  const float ft = __uint_as_float(top);
-  const float inv = 127.0f / ft;
-  if (t == 0) scale[row] = finite ? ft / 127.0f : __uint_as_float(0x7fc00000u);
+}
+
+__device__ __forceinline__ u32x2_t quantize8(const float* f, const RowScale& r) {
+  u32x2_t w{0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k >> 2] |= (static_cast<uint32_t>(quantize(f[k], r)) & 0xffu) << (8 * (k & 3));
+  return w;
+}
+
+// Rows of up to 512 N columns in runs of 8 (aligned): one wavefront a row,
+// every value read once, all loads in flight together.  Zero rows have scale
+// 0, rows with an infinity or a NaN scale NaN and codes 0.
+template <int DT, int N>
+__global__ void __launch_bounds__(256)
+quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ q, int64_t ldq,
+                     float* __restrict__ scale) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= rows) return;
+  float f[N][8];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * 64 + lane) * 8;
+    if (c < cols) {
+      load8<DT>(x, row * cols + c, f[n]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[n][k] = 0.f;
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[n][k]) & 0x7fffffffu);
+  top = wave_top(top);
+  if (lane == 0) scale[row] = row_scale(top);
+  const bool codes = row_has_codes(top);
+  const RowScale rs = row_factors(__uint_as_float(top));
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int c = (n * 64 + lane) * 8;
+    if (c < cols) *reinterpret_cast<u32x2_t*>(q + row * ldq + c) = codes ? quantize8(f[n], rs) : u32x2_t{0, 0};
+  }
+}
+
+// Any columns and alignment, one row per workgroup, read twice (the second
+// time from the L2).  With `tail` the last, incomplete run of 16 columns is
+// stored right-aligned in its 16 bytes (zeros before it): the product reads
+// W's last 16 columns there (load_chunk) and the zeros leave out those
+// already counted.
+__global__ void __launch_bounds__(256)
+quantize_any_kernel(const void* __restrict__ x, int dtype, int cols, int8_t* __restrict__ q, int64_t ldq, int tail,
+                    float* __restrict__ scale) {
+  __shared__ uint32_t part[4];
+  const int64_t row = blockIdx.x, base = row * cols;
+  const int t = threadIdx.x;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int c = t; c < cols; c += 256) top = max(top, __float_as_uint(load_f32(x, base + c, dtype)) & 0x7fffffffu);
+  top = wave_top(top);
+  if ((t & 63) == 0) part[t >> 6] = top;
+  __syncthreads();
+  top = max(max(part[0], part[1]), max(part[2], part[3]));
+  if (t == 0) scale[row] = row_scale(top);
+  const bool codes = row_has_codes(top);
+  const RowScale rs = row_factors(__uint_as_float(top));
   const int whole = tail ? cols / 16 * 16 : cols;
   const int shift = tail && whole < cols ? 16 - (cols - whole) : 0;
   int8_t* dst = q + row * ldq;
-  for (int c = t; c < cols; c += THREADS) {
-    const float v = load_f32(x, base + c, dtype);
-    const int code = top != 0 && finite ? quantize(v, ft, inv) : 0;
-    dst[c < whole ? c : c + shift] = static_cast<int8_t>(code);
-  }
+#pragma unroll 4
+  for (int c = t; c < cols; c += 256)
+    dst[c < whole ? c : c + shift] = static_cast<int8_t>(codes ? quantize(load_f32(x, base + c, dtype), rs) : 0);
   if (t < shift) dst[whole + t] = 0;
 }
 
@@ -415,6 +495,160 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t, int f_fastest)
   }
 }
 
+// Few tokens: bound by reading W once.  Every wavefront streams 16 rows of W
+// from memory straight into the operand registers of v_mfma_i32_16x16x64_i8
+// (lane l: row l & 15, bytes 16 (l >> 4) of each run of 64), 16 loads (1024
+// columns) in flight, while the tokens' codes sit in LDS.  A row of codes
+// starts 16 bytes further round the banks than the one before (stride 16
+// modulo 256), so the 16 rows of an operand read are free of conflicts.
+// E_DT: type of e; up to kFewQuantized float rows are quantised here, one per
+// wavefront, which saves a launch, more are quantised beforehand.
+// NB: blocks of 16 tokens.
+constexpr int kFewWaves = 8;
+constexpr int kFewQuantized = 8;
+constexpr int kFewTokens = 64;
+constexpr int kFewLds = 150 << 10;
+
+__host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 + 16; }
+
+template <typename OutT, int E_DT, int NB>
+__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(NB == 1 ? 4 : 2, NB == 1 ? 4 : 2)))
+project_i8_few_kernel(ProjectI8Args a, const void* __restrict__ e) {
+  extern __shared__ u32x4_t lds[];
+  __shared__ float sq[16 * NB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int K = a.K, chunks = (K + 15) / 16, steps = (chunks + 3) / 4;
+  const int n_tok = static_cast<int>(a.n_tok), stride = few_stride(K) / 16;   // in chunks
+  const int r = lane & 15, h = lane >> 4;
+  const int64_t groups = (a.n_out + 15) / 16, all = static_cast<int64_t>(gridDim.x) * kFewWaves;
+  int64_t g = static_cast<int64_t>(blockIdx.x) * kFewWaves + wave;
+
+  u32x4_t w[16];
+  auto load = [&](int64_t grp, int s0) {
+    const int8_t* row = a.w + min(grp * 16 + r, a.n_out - 1) * K;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) __builtin_memcpy(&w[i], row + min(((s0 + i) * 4 + h) * 16, K - 16), 16);
+  };
+  if (g < groups) load(g, 0);
+
+  // codes into LDS, in the layout of a chunked row with the tail right-aligned
+  if constexpr (E_DT == ENGRAM_I8) {
+    for (int i = threadIdx.x; i < n_tok * steps * 4; i += 64 * kFewWaves) {
+      const int t = i / (steps * 4), c = i % (steps * 4);
+      const int8_t* row = a.q + t * a.ldq;
+      u32x4_t v{0, 0, 0, 0};
+      if (c < chunks) v = a.tailed ? *reinterpret_cast<const u32x4_t*>(row + c * 16) : load_chunk_once(row, c, K);
+      lds[t * stride + c] = v;
+    }
+    if (threadIdx.x < 16 * NB) sq[threadIdx.x] = a.q_scale[min(static_cast<int>(threadIdx.x), n_tok - 1)];
+  } else {
+    for (int t = wave; t < n_tok; t += kFewWaves) {
+      const int64_t base = static_cast<int64_t>(t) * K;
+      int8_t* dst = reinterpret_cast<int8_t*>(lds + t * stride);
+      const bool runs = K % 16 == 0 && reinterpret_cast<uintptr_t>(e) % 16 == 0;
+      uint32_t top = 0;
+      if (runs) {
+        for (int c = lane * 8; c < K; c += 512) {
+          float f[8];
+          load8<E_DT>(e, base + c, f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
+        }
+      } else {
+        for (int c = lane; c < K; c += 64) top = max(top, __float_as_uint(load_f32(e, base + c, E_DT)) & 0x7fffffffu);
+      }
+      top = wave_top(top);
+      if (lane == 0) sq[t] = row_scale(top);
+      const bool codes = row_has_codes(top);
+      const RowScale rs = row_factors(__uint_as_float(top));
+      if (runs) {
+        for (int c = lane * 8; c < K; c += 512) {
+          float f[8];
+          load8<E_DT>(e, base + c, f);
+          *reinterpret_cast<u32x2_t*>(dst + c) = codes ? quantize8(f, rs) : u32x2_t{0, 0};
+        }
+      } else {
+        const int whole = K / 16 * 16, shift = whole < K ? 16 - (K - whole) : 0;
+        for (int c = lane; c < K; c += 64)
+          dst[c < whole ? c : c + shift] = static_cast<int8_t>(codes ? quantize(load_f32(e, base + c, E_DT), rs) : 0);
+        if (lane < shift) dst[whole + lane] = 0;
+      }
+      for (int c = chunks + lane; c < steps * 4; c += 64) lds[t * stride + c] = u32x4_t{0, 0, 0, 0};
+    }
+  }
+  __syncthreads();
+
+  for (; g < groups; g += all) {
+    const int64_t o = g * 16 + h * 4;   // acc[b][k]: output o + k of token 16 b + r
+    float so[4];                        // read before the next group's rows: loads return in order
+#pragma unroll
+    for (int k = 0; k < 4; ++k) so[k] = a.w_scale[min(o + k, a.n_out - 1)];
+    i32x4_t acc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = i32x4_t{0, 0, 0, 0};
+    for (int s0 = 0; s0 < steps; s0 += 16) {
+      if (s0 > 0) load(g, s0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (s0 + i < steps) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)   // tokens past the last read the first one's codes; not stored
+            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                __builtin_bit_cast(i32x4_t, w[i]),
+                __builtin_bit_cast(i32x4_t, lds[(b * 16 + r < n_tok ? b * 16 + r : 0) * stride + (s0 + i) * 4 + h]), acc[b], 0, 0, 0);
+        }
+      }
+    }
+    if (g + all < groups) load(g + all, 0);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (b * 16 + r >= n_tok) continue;
+      const float st = sq[b * 16 + r];
+      OutT x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = to_out<OutT>(static_cast<float>(acc[b][k]) * st * so[k]);
+      OutT* dst = static_cast<OutT*>(a.out) + static_cast<int64_t>(b * 16 + r) * a.n_out + o;
+      if (o + 4 <= a.n_out) {
+        __builtin_memcpy(dst, x, sizeof(x));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (o + k < a.n_out) dst[k] = x[k];
+      }
+    }
+  }
+}
+
+template <typename OutT, int E_DT, int NB>
+hipError_t launch_few(const ProjectI8Args& a, const void* e, hipStream_t s) {
+  auto* const fn = project_i8_few_kernel<OutT, E_DT, NB>;
+  const int bytes = static_cast<int>(a.n_tok) * few_stride(a.K);
+  static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((attr_set.load() & bit) == 0) {
+    err = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kFewLds);
+    if (err != hipSuccess) return err;
+    attr_set.fetch_or(bit);
+  }
+  const int64_t groups = (a.n_out + 15) / 16;
+  const int64_t most = NB == 1 && bytes <= kFewLds / 2 ? 512 : 256;   // workgroups that are on the chip together
+  launch_k(fn, dim3(static_cast<unsigned>(std::min(most, (groups + kFewWaves - 1) / kFewWaves))), dim3(64 * kFewWaves), bytes, s, a, e);
+  return hipGetLastError();
+}
+
+template <typename OutT, int E_DT>
+hipError_t launch_few_blocks(const ProjectI8Args& a, const void* e, hipStream_t s) {
+  if (a.n_tok <= 16) return launch_few<OutT, E_DT, 1>(a, e, s);
+  if constexpr (E_DT == ENGRAM_I8) {
+    if (a.n_tok <= 32) return launch_few<OutT, E_DT, 2>(a, e, s);
+    return launch_few<OutT, E_DT, 4>(a, e, s);
+  }
+  return hipErrorInvalidValue;
+}
+
 template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
 hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
   constexpr int kLds = 2 * (TF + TT) * 128 + 2 * (TF + TT) * 4;
@@ -447,35 +681,61 @@ hipError_t launch_tiles(const ProjectI8Args& a, hipStream_t s) {
 
 int64_t i8_row_stride(int64_t cols) { return (cols + 15) / 16 * 16; }
 
+template <int DT>
+void launch_quantize_rows(const void* x, int64_t rows, int cols, int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  if (cols <= 512) launch_k((quantize_rows_kernel<DT, 1>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
+  else if (cols <= 1024) launch_k((quantize_rows_kernel<DT, 2>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
+  else if (cols <= 2048) launch_k((quantize_rows_kernel<DT, 4>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
+  else launch_k((quantize_rows_kernel<DT, 8>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
+}
+
 hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail,
                               float* scale, hipStream_t s) {
   if (rows == 0) return hipSuccess;
   const int c = static_cast<int>(cols);
-  if (cols <= 2048)
-    launch_k(quantize_kernel<64>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, s, x, dtype, rows, c, q, ldq,
-             tail ? 1 : 0, scale);
-  else
-    launch_k(quantize_kernel<256>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, x, dtype, rows, c, q, ldq,
-             tail ? 1 : 0, scale);
+  // runs of 8 with 16-byte loads (f32: two) and 8-byte stores; a whole number
+  // of 16-column runs has no tail to shift
+  const bool runs = c % 8 == 0 && c <= 4096 && ldq % 8 == 0 && (!tail || c % 16 == 0) && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(q) % 8 == 0;
+  if (runs && dtype == ENGRAM_BF16) launch_quantize_rows<ENGRAM_BF16>(x, rows, c, q, ldq, scale, s);
+  else if (runs) launch_quantize_rows<ENGRAM_F32>(x, rows, c, q, ldq, scale, s);
+  else launch_k(quantize_any_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, x, dtype, c, q, ldq, tail ? 1 : 0, scale);
   return hipGetLastError();
 }
 
-hipError_t launch_project_i8(const int8_t* q, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
+bool project_i8_few(int64_t n_tok, int64_t K) {
+  return n_tok <= kFewTokens && K >= 16 && n_tok * few_stride(static_cast<int>(K)) <= kFewLds;
+}
+
+bool project_i8_quantizes(int64_t n_tok, int64_t K) { return n_tok <= kFewQuantized && project_i8_few(n_tok, K); }
+
+namespace {
+
+template <typename OutT>
+hipError_t launch_product(const ProjectI8Args& a, const void* e, int e_dtype, hipStream_t s) {
+  if (e_dtype == ENGRAM_BF16) return launch_few_blocks<OutT, ENGRAM_BF16>(a, e, s);
+  if (e_dtype == ENGRAM_F32) return launch_few_blocks<OutT, ENGRAM_F32>(a, e, s);
+  if (project_i8_few(a.n_tok, a.K)) return launch_few_blocks<OutT, ENGRAM_I8>(a, nullptr, s);
+  if (a.n_tok > 64 && a.n_out > 64) {
+    const bool direct = a.K % 16 == 0 && a.ldq % 16 == 0 &&
+                        (reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.w)) % 16 == 0;
+    return direct ? launch_tiles<OutT, true>(a, s) : launch_tiles<OutT, false>(a, s);
+  }
+  const int64_t tiles = ((a.n_out + 63) / 64) * ((a.n_tok + 63) / 64);
+  if (tiles > INT32_MAX) return hipErrorInvalidValue;
+  launch_k(project_i8_kernel<OutT>, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_project_i8(const void* e, int e_dtype, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
                              const float* w_scale, int64_t n_tok, int64_t K, int64_t n_out, int out_dtype, void* out,
                              hipStream_t s) {
   if (n_tok == 0) return hipSuccess;
-  const ProjectI8Args a{q, q_scale, w, w_scale, out, n_tok, ldq, n_out, static_cast<int>(K), tailed ? 1 : 0};
-  const bool direct = K % 16 == 0 && ldq % 16 == 0 && (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(w)) % 16 == 0;
-  if (n_tok > 64 && n_out > 64) {
-    if (out_dtype == ENGRAM_BF16) return direct ? launch_tiles<uint16_t, true>(a, s) : launch_tiles<uint16_t, false>(a, s);
-    return direct ? launch_tiles<float, true>(a, s) : launch_tiles<float, false>(a, s);
-  }
-  const int64_t tiles = ((n_out + 63) / 64) * ((n_tok + 63) / 64);
-  if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(tiles));
-  if (out_dtype == ENGRAM_BF16) launch_k(project_i8_kernel<uint16_t>, grid, dim3(256), 0, s, a);
-  else launch_k(project_i8_kernel<float>, grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  const ProjectI8Args a{static_cast<const int8_t*>(e), q_scale, w, w_scale, out, n_tok, ldq, n_out, static_cast<int>(K), tailed ? 1 : 0};
+  return out_dtype == ENGRAM_BF16 ? launch_product<uint16_t>(a, e, e_dtype, s) : launch_product<float>(a, e, e_dtype, s);
 }
 
 }  // namespace engram

@@ -6,17 +6,10 @@
 namespace engram {
 namespace {
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr float kLog2e = 1.44269504088896341f;
-
-__device__ __forceinline__ float load_f32(const void* x, int64_t i, int dtype) {
-  return dtype == ENGRAM_BF16 ? bf16_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
-}
-
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
-  return x;
-}
 
 __device__ __forceinline__ double wave_sum64(double x) {
 #pragma unroll
@@ -25,60 +18,307 @@ __device__ __forceinline__ double wave_sum64(double x) {
 }
 
 // ---- probabilities ----
-// One workgroup per row: largest logit, sum of exponentials, probabilities.
 // p_v = e^((l_v - max) / T) / sum; at T <= 0 the lowest index of the largest
 // logit has probability 1.  A row of -inf alone has probabilities 0; one with
 // a NaN has NaN throughout, and so has one with +inf at T > 0.
-__global__ void __launch_bounds__(256)
-probs_kernel(const void* __restrict__ logits, int dtype, int64_t V, int64_t ld, const float* __restrict__ temperature,
-             int64_t per, float* __restrict__ probs) {
-  __shared__ float red[4];
-  __shared__ int64_t first[4];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
-  const int64_t in = row * ld;
-  float* out = probs + row * V;
-  const float temp = temperature != nullptr ? temperature[row / per] : 1.0f;
-  float mx = -__builtin_inff();
-  bool nan = false;
-  for (int64_t v = tid; v < V; v += 256) {
-    const float l = load_f32(logits, in + v, dtype);
-    nan |= l != l;
-    mx = fmaxf(mx, l);
+//
+// Bound by memory: a row is read once and written once, by one workgroup that
+// keeps it in registers between its maximum, its sum and its output (N runs
+// of 4 values a thread, all loads in flight together).
+
+struct ProbsArgs {
+  const void* logits;
+  const float* temperature;
+  float* probs;
+  int64_t V;
+  int64_t ld;
+  int64_t per;
+};
+
+// Four logits from any element on, as stored; -inf past the row's end.
+template <int DT>
+struct Quad;
+template <>
+struct Quad<ENGRAM_F32> {
+  f32x4_t x;
+  __device__ __forceinline__ float at(int k) const { return x[k]; }
+};
+template <>
+struct Quad<ENGRAM_BF16> {
+  u32x2_t x;
+  __device__ __forceinline__ float at(int k) const { return __uint_as_float(k & 1 ? x[k >> 1] & 0xffff0000u : x[k >> 1] << 16); }
+};
+
+// Quad i of a row of `quads` whole ones, -inf past the last (no branch around
+// the load: it reads the row's first quad instead).
+template <int DT>
+__device__ __forceinline__ Quad<DT> load_quad(const void* row, int64_t i, int64_t quads) {
+  Quad<DT> q;
+  const bool in = i < quads;
+  const int64_t v = in ? i * 4 : 0;
+  if constexpr (DT == ENGRAM_F32) {
+    if (quads > 0) __builtin_memcpy(&q.x, static_cast<const float*>(row) + v, 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q.x[k] = in ? q.x[k] : -__builtin_inff();
+  } else {
+    if (quads > 0) __builtin_memcpy(&q.x, static_cast<const uint16_t*>(row) + v, 8);
+    q.x = in ? q.x : u32x2_t{0xff80ff80u, 0xff80ff80u};
   }
-  nan = __syncthreads_or(nan);
-  mx = wave_max(mx);
-  if ((tid & 63) == 0) red[tid >> 6] = mx;
+  return q;
+}
+
+__device__ __forceinline__ void store_quad(float* row, int64_t i, int64_t quads, f32x4_t y) {
+  if (i < quads) __builtin_memcpy(row + i * 4, &y, 16);
+}
+
+// The up to three entries behind the last quad are the first threads' own.
+template <int DT>
+__device__ __forceinline__ float load_tail(const void* row, int64_t v, int64_t V) {
+  if (v >= V) return -__builtin_inff();
+  if constexpr (DT == ENGRAM_F32) return static_cast<const float*>(row)[v];
+  else return bf16_to_f32(static_cast<const uint16_t*>(row)[v]);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
+  return x;
+}
+
+// Largest value over the workgroup, NaN if any thread saw one.
+template <int THREADS>
+__device__ __forceinline__ float group_max(float x, bool nan, float* red) {
+  x = wave_max(x);
+  if (__any(nan)) x = __builtin_nanf("");
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
   __syncthreads();
-  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float m = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) m = m != m || red[w] != red[w] ? __builtin_nanf("") : fmaxf(m, red[w]);
+  return m;
+}
+
+template <int THREADS>
+__device__ __forceinline__ float group_sum(float x, float* red) {
+  x = wave_sum(x);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
   __syncthreads();
-  if (nan || mx == -__builtin_inff() || (mx == __builtin_inff() && temp > 0.f)) {
-    const float fill = !nan && mx < 0.f ? 0.f : __builtin_nanf("");
-    for (int64_t v = tid; v < V; v += 256) out[v] = fill;
+  float s = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) s += red[w];
+  return s;
+}
+
+template <int THREADS>
+__device__ __forceinline__ int group_min(int x, int* red) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = min(x, __shfl_xor(x, off, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+  __syncthreads();
+  int m = red[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 64; ++w) m = min(m, red[w]);
+  return m;
+}
+
+template <int THREADS>
+struct ProbsShared {
+  float top[THREADS / 64], sum[THREADS / 64];
+  int first[THREADS / 64];
+};
+
+// What a row without a sum holds throughout, or nothing of the kind.
+__device__ __forceinline__ bool constant_row(float top, float temp, float* fill) {
+  *fill = top == -__builtin_inff() ? 0.f : __builtin_nanf("");
+  return top != top || top == -__builtin_inff() || (top == __builtin_inff() && temp > 0.f);
+}
+
+// bf16 pairs stay packed from pass to pass: without this the compiler keeps
+// every unpacked value, then every exponential, for the next pass, twice the
+// registers there are.  (float32 rows keep their exponentials in place.)
+template <int DT, int N>
+__device__ __forceinline__ void forget(Quad<DT> (&x)[N]) {
+  if constexpr (DT == ENGRAM_BF16)
+#pragma unroll
+    for (int n = 0; n < N; ++n) asm volatile("" : "+v"(x[n].x));
+}
+
+template <int DT, int THREADS, int N>
+__global__ void __launch_bounds__(THREADS)
+probs_kernel(ProbsArgs a) {
+  __shared__ ProbsShared<THREADS> sh;
+  const int64_t row = blockIdx.x, V = a.V;
+  constexpr int size = DT == ENGRAM_BF16 ? 2 : 4;
+  const void* in = static_cast<const char*>(a.logits) + row * a.ld * size;
+  float* out = a.probs + row * V;
+  const float temp = a.temperature != nullptr ? a.temperature[row / a.per] : 1.0f;
+  const int64_t quads = V / 4, vt = quads * 4 + threadIdx.x;   // vt: this thread's entry behind the quads
+  const int q0 = threadIdx.x;
+  Quad<DT> x[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) x[n] = load_quad<DT>(in, q0 + n * THREADS, quads);
+  const float xt = load_tail<DT>(in, vt, V);
+  float top = xt;
+  bool nan = xt != xt;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float l = x[n].at(k);
+      nan |= l != l;
+      top = fmaxf(top, l);
+    }
+  forget(x);
+  top = group_max<THREADS>(top, nan, sh.top);
+  float fill;
+  if (constant_row(top, temp, &fill)) {
+    for (int n = 0; n < N; ++n) store_quad(out, q0 + n * THREADS, quads, f32x4_t{fill, fill, fill, fill});
+    if (vt < V) out[vt] = fill;
     return;
   }
   if (!(temp > 0.f)) {
-    int64_t at = V;
-    for (int64_t v = tid; v < V && at == V; v += 256)
-      if (load_f32(logits, in + v, dtype) == mx) at = v;
+    int at = xt == top ? static_cast<int>(vt) : INT32_MAX;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) at = min(at, static_cast<int64_t>(__shfl_xor(static_cast<long long>(at), off, 64)));
-    if ((tid & 63) == 0) first[tid >> 6] = at;
-    __syncthreads();
-    at = min(min(first[0], first[1]), min(first[2], first[3]));
-    for (int64_t v = tid; v < V; v += 256) out[v] = v == at ? 1.f : 0.f;
+    for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+      for (int k = 3; k >= 0; --k) at = x[n].at(k) == top ? (q0 + n * THREADS) * 4 + k : at;
+    at = group_min<THREADS>(at, sh.first);
+    for (int n = 0; n < N; ++n) {
+      const int d = at - (q0 + n * THREADS) * 4;
+      store_quad(out, q0 + n * THREADS, quads, f32x4_t{d == 0 ? 1.f : 0.f, d == 1 ? 1.f : 0.f, d == 2 ? 1.f : 0.f, d == 3 ? 1.f : 0.f});
+    }
+    if (vt < V) out[vt] = at == vt ? 1.f : 0.f;
     return;
   }
-  const float k = kLog2e / temp;
-  float sum = 0.f;
-  for (int64_t v = tid; v < V; v += 256) sum += __builtin_amdgcn_exp2f((load_f32(logits, in + v, dtype) - mx) * k);
-  sum = wave_sum(sum);
-  if ((tid & 63) == 0) red[tid >> 6] = sum;
-  __syncthreads();
-  sum = (red[0] + red[1]) + (red[2] + red[3]);
-  const float inv = 1.0f / sum;
-  for (int64_t v = tid; v < V; v += 256) out[v] = __builtin_amdgcn_exp2f((load_f32(logits, in + v, dtype) - mx) * k) * inv;
+  const float f = kLog2e / temp;
+  const float et = __builtin_amdgcn_exp2f((xt - top) * f);
+  float sum = et;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float e[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f);
+    sum += (e[0] + e[1]) + (e[2] + e[3]);
+  }
+  forget(x);
+  const float inv = 1.0f / group_sum<THREADS>(sum, sh.sum);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    f32x4_t y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f) * inv;
+    store_quad(out, q0 + n * THREADS, quads, y);
+  }
+  if (vt < V) out[vt] = et * inv;
 }
+
+// Rows too long for the registers: one pass for the maximum and the sum (each
+// thread's sum is kept relative to its own maximum so far), a second one for
+// the output.
+template <int DT>
+__global__ void __launch_bounds__(1024)
+probs_long_kernel(ProbsArgs a) {
+  constexpr int THREADS = 1024, U = 8;
+  __shared__ ProbsShared<THREADS> sh;
+  const int64_t row = blockIdx.x, V = a.V;
+  constexpr int size = DT == ENGRAM_BF16 ? 2 : 4;
+  const void* in = static_cast<const char*>(a.logits) + row * a.ld * size;
+  float* out = a.probs + row * V;
+  const float temp = a.temperature != nullptr ? a.temperature[row / a.per] : 1.0f;
+  const float f = kLog2e / temp;
+  const int64_t quads = V / 4, vt = quads * 4 + threadIdx.x;
+  const float xt = load_tail<DT>(in, vt, V);
+  float top = -__builtin_inff(), sum = 0.f;
+  int at = INT32_MAX;
+  bool nan = xt != xt;
+  for (int64_t q = threadIdx.x; q < quads; q += U * THREADS) {
+    Quad<DT> x[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) x[i] = load_quad<DT>(in, q + i * THREADS, quads);
+    float m = top;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float l = x[i].at(k);
+        nan |= l != l;
+        if (l > m) at = (static_cast<int32_t>(q) + i * THREADS) * 4 + k;
+        m = fmaxf(m, l);
+      }
+    if (m > -__builtin_inff() && m < __builtin_inff()) {
+      sum = top > -__builtin_inff() ? sum * __builtin_amdgcn_exp2f((top - m) * f) : 0.f;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f((x[i].at(k) - m) * f);
+        sum += (e[0] + e[1]) + (e[2] + e[3]);
+      }
+    }
+    top = m;
+  }
+  const float own = top;
+  top = group_max<THREADS>(fmaxf(top, xt), nan, sh.top);
+  float fill;
+  if (constant_row(top, temp, &fill)) {
+    for (int64_t q = threadIdx.x; q < quads; q += THREADS) store_quad(out, q, quads, f32x4_t{fill, fill, fill, fill});
+    if (vt < V) out[vt] = fill;
+    return;
+  }
+  if (!(temp > 0.f)) {
+    at = group_min<THREADS>(own == top ? at : (xt == top ? static_cast<int32_t>(vt) : INT32_MAX), sh.first);
+    for (int64_t q = threadIdx.x; q < quads; q += THREADS) {
+      const int64_t d = at - q * 4;
+      store_quad(out, q, quads, f32x4_t{d == 0 ? 1.f : 0.f, d == 1 ? 1.f : 0.f, d == 2 ? 1.f : 0.f, d == 3 ? 1.f : 0.f});
+    }
+    if (vt < V) out[vt] = at == vt ? 1.f : 0.f;
+    return;
+  }
+  const float et = __builtin_amdgcn_exp2f((xt - top) * f);
+  const float part = own > -__builtin_inff() ? sum * __builtin_amdgcn_exp2f((own - top) * f) : 0.f;
+  const float inv = 1.0f / group_sum<THREADS>(part + et, sh.sum);
+  for (int64_t q = threadIdx.x; q < quads; q += U * THREADS) {
+    Quad<DT> x[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) x[i] = load_quad<DT>(in, q + i * THREADS, quads);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      f32x4_t y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_exp2f((x[i].at(k) - top) * f) * inv;
+      store_quad(out, q + i * THREADS, quads, y);
+    }
+  }
+  if (vt < V) out[vt] = et * inv;
+}
+
+template <int DT>
+void launch_probs_dt(const ProbsArgs& a, int64_t rows, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(rows));
+  // the fewest registers that hold a row
+  if (a.V <= 1024 * 2) launch_k((probs_kernel<DT, 256, 2>), grid, dim3(256), 0, s, a);
+  else if (a.V <= 1024 * 8) launch_k((probs_kernel<DT, 256, 8>), grid, dim3(256), 0, s, a);
+  else if (a.V <= 4096 * 4) launch_k((probs_kernel<DT, 1024, 4>), grid, dim3(1024), 0, s, a);
+  else if (a.V <= 4096 * 8) launch_k((probs_kernel<DT, 1024, 8>), grid, dim3(1024), 0, s, a);
+  else if (a.V <= 4096 * 16) launch_k((probs_kernel<DT, 1024, 16>), grid, dim3(1024), 0, s, a);
+  else if (DT == ENGRAM_BF16 && a.V <= 4096 * 32) launch_k((probs_kernel<ENGRAM_BF16, 1024, 32>), grid, dim3(1024), 0, s, a);
+  else launch_k(probs_long_kernel<DT>, grid, dim3(1024), 0, s, a);
+}
+
+}  // namespace
+
+size_t probs_workspace(int64_t, int64_t) { return 0; }
+
+hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
+                              int64_t per, float* probs, void*, hipStream_t s) {
+  if (rows == 0) return hipSuccess;
+  const ProbsArgs a{logits, temperature, probs, V, ld, per};
+  if (dtype == ENGRAM_BF16) launch_probs_dt<ENGRAM_BF16>(a, rows, s);
+  else launch_probs_dt<ENGRAM_F32>(a, rows, s);
+  return hipGetLastError();
+}
+
+namespace {
 
 // ---- verification ----
 // A draft x_i is accepted while u_i q_i(x_i) < p_i(x_i) (both sides exact in
@@ -87,6 +327,10 @@ probs_kernel(const void* __restrict__ logits, int dtype, int64_t V, int64_t ld, 
 // (and where p - q leaves nothing): the lowest index whose cumulative sum
 // passes u * total.  Sums are in double: a border between two tokens then
 // moves by about 2^-50 of the total rather than 2^-22.
+//
+// The row (and the draft's) is read once: every wavefront sums a contiguous
+// part of it.  The part in which the cumulative sum passes u * total is then
+// read again, by the whole workgroup, to find the token.
 
 struct VerifyArgs {
   const void* target;      // [S][G+1][V]
@@ -97,84 +341,113 @@ struct VerifyArgs {
   const float* u_sample;   // [S]
   int32_t* tokens;         // [S][G+1]
   int32_t* n_accepted;     // [S]
-  double2* part;           // [S][chunks]: sums of max(p - q, 0) and of p
+  double* part;            // [S][kParts], split form
   int64_t V;
   int G;
-  int dtype;
-  int chunks;
 };
 
-constexpr int kPerThread = 16;
-constexpr int kChunk = 256 * kPerThread;
+constexpr int kParts = 64;        // parts of a row in the split form
+constexpr int kVerifyWaves = 16;  // wavefronts of a workgroup; parts of a row in the one-workgroup form
 
-// Accepted drafts of sequence s, and whether one was refused.  Every
+template <int DT>
+__device__ __forceinline__ float prob(const void* p, int64_t i) {
+  if constexpr (DT == ENGRAM_BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
+}
+
+template <int DT>
+constexpr int vec_of() { return DT == ENGRAM_BF16 ? 8 : 4; }
+
+// 16 bytes of a row from any element on.
+template <int DT>
+__device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&f)[vec_of<DT>()]) {
+  if constexpr (DT == ENGRAM_BF16) {
+    uint4 w;
+    __builtin_memcpy(&w, static_cast<const uint16_t*>(p) + i, 16);
+    unpack8(w, f);
+  } else {
+    __builtin_memcpy(f, static_cast<const float*>(p) + i, 16);
+  }
+}
+
+// The row that the next token is drawn from.
+struct Rest {
+  const void* p;   // the target's row
+  const void* q;   // the draft's, or null
+  int32_t drop;    // token with draft probability 1, or -1
+};
+
+// An entry of it; a NaN counts as nothing.
+__device__ __forceinline__ double entry(double p, double q, bool dropped) {
+  const double d = p - q;
+  return dropped ? 0.0 : fmax(d, 0.0);
+}
+
+template <int DT>
+__device__ __forceinline__ double entry_at(const Rest& r, int64_t v) {
+  return entry(prob<DT>(r.p, v), r.q != nullptr ? prob<DT>(r.q, v) : 0.0f, v == r.drop);
+}
+
+// Accepted drafts of sequence s, and the row for the next token.  Every
 // wavefront of the workgroup computes it: lane i looks at draft i.
-__device__ __forceinline__ int accepted(const VerifyArgs& a, int64_t s, bool* refused) {
+template <int DT>
+__device__ __forceinline__ int accepted(const VerifyArgs& a, int64_t s, Rest* rest) {
   const int lane = threadIdx.x & 63;
+  const int32_t x = lane < a.G ? a.drafted[s * a.G + lane] : 0;
+  const float u = lane < a.G ? a.u_accept[s * a.G + lane] : 0.f;
   const int n = a.n_draft != nullptr ? min(max(a.n_draft[s], 0), a.G) : a.G;
-  bool ok = true;
-  if (lane < n) {
-    const int32_t x = a.drafted[s * a.G + lane];
-    ok = x >= 0 && x < a.V;
-    if (ok) {
-      const double p = load_f32(a.target, (s * (a.G + 1) + lane) * a.V + x, a.dtype);
-      const double q = a.draft != nullptr ? load_f32(a.draft, (s * a.G + lane) * a.V + x, a.dtype) : 1.0f;
-      ok = static_cast<double>(a.u_accept[s * a.G + lane]) * q < p;
-    }
+  bool ok = x >= 0 && x < a.V;
+  if (lane < a.G && ok) {
+    const double p = prob<DT>(a.target, (s * (a.G + 1) + lane) * a.V + x);
+    const double q = a.draft != nullptr ? prob<DT>(a.draft, (s * a.G + lane) * a.V + x) : 1.0f;
+    ok = static_cast<double>(u) * q < p;
   }
   const uint64_t bad = __ballot(lane < n && !ok);
-  *refused = bad != 0;
-  return bad != 0 ? __builtin_ctzll(bad) : n;
+  const int acc = bad != 0 ? __builtin_ctzll(bad) : n;
+  constexpr int size = DT == ENGRAM_BF16 ? 2 : 4;
+  rest->p = static_cast<const char*>(a.target) + (s * (a.G + 1) + acc) * a.V * size;
+  rest->q = bad != 0 && a.draft != nullptr ? static_cast<const char*>(a.draft) + (s * a.G + acc) * a.V * size : nullptr;
+  rest->drop = bad != 0 && a.draft == nullptr ? __shfl(x, acc, 64) : -1;
+  return acc;
 }
 
-// max(p_v - q_v, 0) and p_v of one entry; a NaN counts as nothing.
-struct Rest {
-  const void* p;
-  const void* q;    // null: none, or a draft without probabilities
-  int64_t p0, q0;   // first entry of the row
-  int64_t drop;     // token with draft probability 1, or -1
-  int dtype;
-  __device__ __forceinline__ double2 at(int64_t v) const {
-    const double pv = load_f32(p, p0 + v, dtype);
-    double d = pv;
-    if (q != nullptr) d -= static_cast<double>(load_f32(q, q0 + v, dtype));
-    if (v == drop) d = 0.0;
-    return make_double2(d > 0.0 ? d : 0.0, pv > 0.0 ? pv : 0.0);
-  }
-};
-
-__device__ __forceinline__ Rest rest_of(const VerifyArgs& a, int64_t s, int acc, bool refused) {
-  Rest r{a.target, refused ? a.draft : nullptr, (s * (a.G + 1) + acc) * a.V, (s * a.G + acc) * a.V, -1, a.dtype};
-  if (refused && a.draft == nullptr) r.drop = a.drafted[s * a.G + acc];
-  return r;
+// Length of a part: whole wavefront loads.
+template <int DT>
+__device__ __forceinline__ int64_t part_len(int64_t V, int parts) {
+  constexpr int64_t unit = 64 * vec_of<DT>();
+  return ((V + parts - 1) / parts + unit - 1) / unit * unit;
 }
 
-__global__ void __launch_bounds__(256)
-verify_sums_kernel(VerifyArgs a) {
-  __shared__ double2 red[4];
-  const int64_t s = blockIdx.y;
-  const int tid = threadIdx.x;
-  bool refused;
-  const int acc = accepted(a, s, &refused);
-  const Rest r = rest_of(a, s, acc, refused);
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kChunk;
-  double rest = 0.0, row = 0.0;
+// Sum of entries [v0, min(v0 + len, V)) by one wavefront, in every lane.
+template <int DT, bool Q>
+__device__ __forceinline__ double part_sum(const Rest& r, int64_t v0, int64_t len, int64_t V) {
+  constexpr int VEC = vec_of<DT>(), U = 16 / VEC;
+  const int lane = threadIdx.x & 63;
+  const int64_t end = min(v0 + len, V);
+  double s[2] = {0.0, 0.0};
+  int64_t v = v0 + lane * VEC;
+  for (; v + (U - 1) * 64 * VEC + VEC <= end; v += U * 64 * VEC) {
+    float p[U][VEC], q[U][VEC];
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int64_t v = v0 + i * 256 + tid;
-    if (v < a.V) {
-      const double2 d = r.at(v);
-      rest += d.x;
-      row += d.y;
+    for (int i = 0; i < U; ++i) {
+      load_vec<DT>(r.p, v + i * 64 * VEC, p[i]);
+      if constexpr (Q) load_vec<DT>(r.q, v + i * 64 * VEC, q[i]);
     }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) s[k & 1] += entry(p[i][k], Q ? q[i][k] : 0.0f, !Q && static_cast<int32_t>(v) + i * 64 * VEC + k == r.drop);
   }
-  rest = wave_sum64(rest);
-  row = wave_sum64(row);
-  if ((tid & 63) == 0) red[tid >> 6] = make_double2(rest, row);
-  __syncthreads();
-  if (tid == 0)
-    a.part[s * a.chunks + blockIdx.x] = make_double2((red[0].x + red[1].x) + (red[2].x + red[3].x),
-                                                     (red[0].y + red[1].y) + (red[2].y + red[3].y));
+  for (; v < end; v += 64 * VEC)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (v + k < end) s[k & 1] += entry_at<DT>(r, v + k);
+  return wave_sum64(s[0] + s[1]);
+}
+
+template <int DT>
+__device__ __forceinline__ double part_sum(const Rest& r, int64_t v0, int64_t len, int64_t V) {
+  return r.q != nullptr ? part_sum<DT, true>(r, v0, len, V) : part_sum<DT, false>(r, v0, len, V);
 }
 
 // Inclusive sum over the lanes of a wavefront.
@@ -188,127 +461,169 @@ __device__ __forceinline__ double wave_scan64(double x) {
   return x;
 }
 
-__global__ void __launch_bounds__(256)
-verify_pick_kernel(VerifyArgs a) {
-  __shared__ double wsum[4];
-  __shared__ int found[4], last[4];
-  __shared__ int chunk_s;
-  __shared__ double left_s;
-  __shared__ int use_row_s;
-  const int64_t s = blockIdx.x;
+struct PickShared {
+  double part[kParts];
+  double wave[kVerifyWaves];
+  int found[kVerifyWaves], last[kVerifyWaves];
+};
+
+// The next token of a row whose part sums are in sh.part (visible to the
+// workgroup), -1 where the row holds nothing.  *none: the parts sum to zero.
+template <int DT>
+__device__ __forceinline__ int64_t pick(const Rest& r, PickShared& sh, int parts, int64_t len, int64_t V, float u, bool* none) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  bool refused;
-  const int acc = accepted(a, s, &refused);
-  const Rest r = rest_of(a, s, acc, refused);
-  if (tid == 0) {
-    const double2* part = a.part + s * a.chunks;
-    double rest = 0.0, row = 0.0;
-    for (int c = 0; c < a.chunks; ++c) {
-      rest += part[c].x;
-      row += part[c].y;
-    }
-    const bool use_row = !(rest > 0.0);
-    const double total = use_row ? row : rest;
-    const double want = static_cast<double>(a.u_sample[s]) * total;
-    int chunk = -1, end = -1;
-    double before = 0.0, left = 0.0;
-    if (total > 0.0 && total < __builtin_inf()) {
-      for (int c = 0; c < a.chunks && chunk < 0; ++c) {
-        const double x = use_row ? part[c].y : part[c].x;
-        if (before + x > want) {
-          chunk = c;
-          left = before;
-        } else {
-          before += x;
-        }
-        if (x > 0.0) end = c;
+  const double x = lane < parts ? sh.part[lane] : 0.0;
+  const double scan = wave_scan64(x);
+  const double total = __shfl(scan, 63, 64), want = static_cast<double>(u) * total;
+  *none = !(total > 0.0);
+  if (*none || !(total < __builtin_inf())) return -1;
+  const uint64_t over = __ballot(x > 0.0 && scan > want), any = __ballot(x > 0.0);
+  const bool past = over == 0;   // u not below 1: the last token that has any probability
+  const int part = past ? 63 - __builtin_clzll(any) : __builtin_ctzll(over);
+  const double left = part > 0 ? __shfl(scan, part - 1, 64) : 0.0;
+  // this thread's run of the part
+  const int run = static_cast<int>((len + 64 * kVerifyWaves - 1) / (64 * kVerifyWaves));
+  const int64_t v0 = part * len + static_cast<int64_t>(tid) * run, v1 = min(min(v0 + run, (part + 1) * len), V);
+  constexpr int kKept = 8;
+  double e[kKept], sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) e[i] = i < run && v0 + i < v1 ? entry_at<DT>(r, v0 + i) : 0.0;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) sum += e[i];
+  for (int64_t v = v0 + kKept; v < v1; ++v) sum += entry_at<DT>(r, v);
+  const double inside = wave_scan64(sum);
+  if (lane == 63) sh.wave[wave] = inside;
+  __syncthreads();
+  double at = left;
+  for (int w = 0; w < wave; ++w) at += sh.wave[w];
+  const double prev = __shfl_up(inside, 1, 64);
+  if (lane > 0) at += prev;
+  // the first of this run that passes (in a chunk of its own kind: offsets
+  // within the part fit an int), and the last one that has any probability
+  int found = INT32_MAX, last = -1;
+  const int base = static_cast<int>(v0 - part * len);
+  if (sum > 0.0) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      at += e[i];
+      if (e[i] > 0.0) {
+        last = base + i;
+        if (found == INT32_MAX && !past && at > want) found = base + i;
       }
-      if (chunk < 0) {   // u not below 1: the last token that has any probability
-        chunk = end;
-        left = __builtin_inf();
+    }
+    for (int64_t v = v0 + kKept; v < v1; ++v) {
+      const double d = entry_at<DT>(r, v);
+      at += d;
+      if (d > 0.0) {
+        last = base + static_cast<int>(v - v0);
+        if (found == INT32_MAX && !past && at > want) found = last;
       }
     }
-    chunk_s = chunk;
-    left_s = left;
-    use_row_s = use_row;
-    wsum[0] = want;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    found = min(found, __shfl_xor(found, off, 64));
+    last = max(last, __shfl_xor(last, off, 64));
+  }
+  if (lane == 0) {
+    sh.found[wave] = found;
+    sh.last[wave] = last;
   }
   __syncthreads();
-  const int chunk = chunk_s;
-  const double want = wsum[0], left = left_s;
-  const bool use_row = use_row_s != 0;
+#pragma unroll
+  for (int w = 0; w < kVerifyWaves; ++w) {
+    found = min(found, sh.found[w]);
+    last = max(last, sh.last[w]);
+  }
+  // the part's sum was formed in another order: by a last bit the second one
+  // may not reach what the first reached
+  return part * len + (found != INT32_MAX ? found : last);
+}
+
+// Part sums of the whole row by this workgroup.
+template <int DT>
+__device__ __forceinline__ void sum_row(const Rest& r, PickShared& sh, int64_t len, int64_t V) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const double x = part_sum<DT>(r, wave * len, len, V);
+  if ((threadIdx.x & 63) == 0) sh.part[wave] = x;
   __syncthreads();
-  int32_t token = -1;
-  if (chunk >= 0) {
-    const int64_t v0 = static_cast<int64_t>(chunk) * kChunk + tid * kPerThread;
-    double x[kPerThread], sum = 0.0;
-    int end = -1;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      x[i] = 0.0;
-      if (v0 + i < a.V) {
-        const double2 d = r.at(v0 + i);
-        x[i] = use_row ? d.y : d.x;
-      }
-      if (x[i] > 0.0) end = tid * kPerThread + i;
-      sum += x[i];
-    }
-    const double scan = wave_scan64(sum);
-    if (lane == 63) wsum[wave] = scan;
+}
+
+// SPLIT: part sums from the workspace (verify_parts_kernel); otherwise this
+// workgroup reads the whole row.
+template <int DT, bool SPLIT>
+__global__ void __launch_bounds__(64 * kVerifyWaves)
+verify_kernel(VerifyArgs a) {
+  __shared__ PickShared sh;
+  const int64_t s = blockIdx.x;
+  const int tid = threadIdx.x;
+  Rest r;
+  const float u = a.u_sample[s];
+  const int acc = accepted<DT>(a, s, &r);
+  const int parts = SPLIT ? kParts : kVerifyWaves;
+  const int64_t len = part_len<DT>(a.V, parts);
+  if constexpr (SPLIT) {
+    if (tid < kParts) sh.part[tid] = a.part[s * kParts + tid];
     __syncthreads();
-    double run = left + (scan - sum);
-    for (int w = 0; w < wave; ++w) run += wsum[w];
-    int at = kChunk;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      run += x[i];
-      if (at == kChunk && x[i] > 0.0 && run > want && left < __builtin_inf()) at = tid * kPerThread + i;
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      at = min(at, __shfl_xor(at, off, 64));
-      end = max(end, __shfl_xor(end, off, 64));
-    }
-    if (lane == 0) {
-      found[wave] = at;
-      last[wave] = end;
-    }
+  } else {
+    sum_row<DT>(r, sh, len, a.V);
+  }
+  bool none;
+  int64_t token = pick<DT>(r, sh, parts, len, a.V, u, &none);
+  if (none && (r.q != nullptr || r.drop >= 0)) {   // the draft leaves nothing: from the target's row itself
     __syncthreads();
-    at = min(min(found[0], found[1]), min(found[2], found[3]));
-    end = max(max(last[0], last[1]), max(last[2], last[3]));
-    // the chunk's sum was formed in another order: by a last bit it may not
-    // reach what it reached there
-    token = static_cast<int32_t>(static_cast<int64_t>(chunk) * kChunk + (at < kChunk ? at : end));
+    r.q = nullptr;
+    r.drop = -1;
+    const int64_t own = part_len<DT>(a.V, kVerifyWaves);
+    sum_row<DT>(r, sh, own, a.V);
+    token = pick<DT>(r, sh, kVerifyWaves, own, a.V, u, &none);
   }
   if (tid == 0) a.n_accepted[s] = acc;
-  for (int i = tid; i <= a.G; i += 256) a.tokens[s * (a.G + 1) + i] = i < acc ? a.drafted[s * a.G + i] : (i == acc ? token : -1);
+  if (tid <= a.G)
+    a.tokens[s * (a.G + 1) + tid] = tid < acc ? a.drafted[s * a.G + tid] : (tid == acc ? static_cast<int32_t>(token) : -1);
+}
+
+// Split form, first launch: kParts part sums of each sequence's row, one
+// wavefront each.
+constexpr int kPartWaves = 4;
+template <int DT>
+__global__ void __launch_bounds__(64 * kPartWaves)
+verify_parts_kernel(VerifyArgs a) {
+  const int64_t s = blockIdx.x / (kParts / kPartWaves);
+  const int part = static_cast<int>(blockIdx.x % (kParts / kPartWaves)) * kPartWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Rest r;
+  accepted<DT>(a, s, &r);
+  const int64_t len = part_len<DT>(a.V, kParts);
+  const double x = part_sum<DT>(r, part * len, len, a.V);
+  if ((threadIdx.x & 63) == 0) a.part[s * kParts + part] = x;
+}
+
+// Few sequences with long rows: the sums are split over 16 workgroups a row.
+bool verify_splits(int64_t S, int64_t V) { return S <= 64 && V > 16384; }
+
+template <int DT>
+hipError_t launch_verify_dt(const VerifyArgs& a, int64_t S, hipStream_t s) {
+  if (verify_splits(S, a.V)) {
+    launch_k(verify_parts_kernel<DT>, dim3(static_cast<unsigned>(S * (kParts / kPartWaves))), dim3(64 * kPartWaves), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    launch_k((verify_kernel<DT, true>), dim3(static_cast<unsigned>(S)), dim3(64 * kVerifyWaves), 0, s, a);
+  } else {
+    launch_k((verify_kernel<DT, false>), dim3(static_cast<unsigned>(S)), dim3(64 * kVerifyWaves), 0, s, a);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t probs_workspace(int64_t, int64_t) { return 0; }
-
-hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
-                              int64_t per, float* probs, void*, hipStream_t s) {
-  if (rows == 0) return hipSuccess;
-  launch_k(probs_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, logits, dtype, V, ld, temperature, per, probs);
-  return hipGetLastError();
-}
-
-size_t verify_workspace(int64_t S, int64_t V) { return static_cast<size_t>(S) * ((V + kChunk - 1) / kChunk) * sizeof(double2); }
+size_t verify_workspace(int64_t S, int64_t V) { return verify_splits(S, V) ? static_cast<size_t>(S) * kParts * sizeof(double) : 0; }
 
 hipError_t launch_verify(const void* target, const void* draft, int dtype, const int32_t* drafted, const int32_t* n_draft,
                          const float* u_accept, const float* u_sample, int64_t S, int32_t G, int64_t V, int32_t* tokens,
                          int32_t* n_accepted, void* ws, hipStream_t s) {
   if (S == 0) return hipSuccess;
-  const int chunks = static_cast<int>((V + kChunk - 1) / kChunk);
-  const VerifyArgs a{target, draft, drafted, n_draft, u_accept, u_sample, tokens, n_accepted, static_cast<double2*>(ws),
-                     V, G, dtype, chunks};
-  launch_k(verify_sums_kernel, dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(S)), dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  launch_k(verify_pick_kernel, dim3(static_cast<unsigned>(S)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  const VerifyArgs a{target, draft, drafted, n_draft, u_accept, u_sample, tokens, n_accepted, static_cast<double*>(ws), V, G};
+  return dtype == ENGRAM_BF16 ? launch_verify_dt<ENGRAM_BF16>(a, S, s) : launch_verify_dt<ENGRAM_F32>(a, S, s);
 }
 
 }  // namespace engram

@@ -561,7 +561,7 @@ engram_status engram_commit_draft(const int32_t* tokens, int64_t B, int64_t T, c
  * -inf has probability 0 and a row of nothing else has none at all (zeros); a
  * row with a NaN, or with +inf at T > 0, is NaN throughout.  rows and V below
  * 2^31; rows = 0 is a no-op.  ws: engram_token_probs_workspace() bytes,
- * 256-byte aligned. */
+ * 256-byte aligned (NULL where that is 0). */
 size_t engram_token_probs_workspace(int64_t rows, int64_t V);
 engram_status engram_token_probs(const void* logits, engram_dtype dtype, int64_t rows, int64_t V, int64_t ld,
                                  const float* temperature, int64_t per, float* probs, void* ws, size_t ws_bytes,
@@ -586,7 +586,8 @@ engram_status engram_token_probs(const void* logits, engram_dtype dtype, int64_t
  *             -1; the next token is -1 where its row holds nothing (zeros, or
  *             a sum that is not finite; a NaN entry counts as 0)
  *   n_accepted device int32 [S]
- *   ws        engram_verify_drafts_workspace() bytes, 256-byte aligned
+ *   ws        engram_verify_drafts_workspace() bytes, 256-byte aligned (NULL where
+ *             that is 0)
  * 1 <= S <= 65535, 0 <= G <= ENGRAM_MAX_DRAFTS, 1 <= V < 2^31 (EUNSUPPORTED
  * otherwise); S = 0 is a no-op. */
 #define ENGRAM_MAX_DRAFTS 64

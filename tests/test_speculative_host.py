@@ -71,11 +71,11 @@ def test_project_i8_refusals():
     call(eg.EINVAL, "aligned", e_scale=ODD)
     call(eg.EINVAL, "aligned", out=ODD)
     call(eg.EINVAL, "aligned", w_scale=ODD)
-    need = eg.lib().engram_project_i8_workspace(4, 64, eg.BF16)
-    assert need >= 4 * 64 + 16 and eg.lib().engram_project_i8_workspace(4, 64, eg.I8) == 0
-    call(eg.EINVAL, "workspace", e_dtype=eg.BF16, e_scale=None)
-    call(eg.EINVAL, "workspace", e_dtype=eg.BF16, e_scale=None, ws=P, wsb=need - 1)
-    call(eg.EINVAL, "workspace", e_dtype=eg.BF16, e_scale=None, ws=ctypes.c_void_p(0x10010), wsb=need)
+    need = eg.lib().engram_project_i8_workspace(400, 64, eg.BF16)
+    assert need >= 400 * 64 + 1600 and eg.lib().engram_project_i8_workspace(400, 64, eg.I8) == 0
+    call(eg.EINVAL, "workspace", n=400, e_dtype=eg.BF16, e_scale=None)
+    call(eg.EINVAL, "workspace", n=400, e_dtype=eg.BF16, e_scale=None, ws=P, wsb=need - 1)
+    call(eg.EINVAL, "workspace", n=400, e_dtype=eg.BF16, e_scale=None, ws=ctypes.c_void_p(0x10010), wsb=need)
 
 
 def test_token_probs_refusals():
@@ -101,10 +101,10 @@ def test_token_probs_refusals():
 
 def test_verify_drafts_refusals():
     f = eg.lib().engram_verify_drafts
-    need = eg.lib().engram_verify_drafts_workspace(4, 1000)
-    assert need > 0 and eg.lib().engram_verify_drafts_workspace(0, 1000) == 0
+    need = eg.lib().engram_verify_drafts_workspace(4, 100000)
+    assert need > 0 and eg.lib().engram_verify_drafts_workspace(0, 100000) == 0
 
-    def call(status, text, target=P, draft=P, dtype=eg.F32, drafted=P, n=None, ua=P, us=P, S=4, G=2, V=1000, tok=P, acc=P,
+    def call(status, text, target=P, draft=P, dtype=eg.F32, drafted=P, n=None, ua=P, us=P, S=4, G=2, V=100000, tok=P, acc=P,
              ws=P, wsb=need):
         _expect(status, text, f, target, draft, dtype, drafted, n, ua, us, S, G, V, tok, acc, ws, wsb, None)
 
