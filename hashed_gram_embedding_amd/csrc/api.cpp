@@ -1448,7 +1448,7 @@ ENGRAM_API engram_status engram_commit_draft(const int32_t* tokens, int64_t B, i
 
 ENGRAM_API size_t engram_token_probs_workspace(int64_t rows, int64_t V) {
   if (rows < 1 || V < 1) return 0;
-  return engram::probs_workspace(rows, V);
+  return align_up(engram::probs_workspace(rows, V));
 }
 
 ENGRAM_API engram_status engram_token_probs(const void* logits, engram_dtype dtype, int64_t rows, int64_t V, int64_t ld,
@@ -1468,8 +1468,10 @@ ENGRAM_API engram_status engram_token_probs(const void* logits, engram_dtype dty
     return fail(ENGRAM_EINVAL, "token_probs: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
   prof_begin();
   prof_mark(stream, "token_probs_kernel");
-  return hip_status(engram::launch_token_probs(logits, dtype, rows, V, ld, temperature, per, probs, ws, stream),
-                    "token_probs launch");
+  const engram_status r = hip_status(engram::launch_token_probs(logits, dtype, rows, V, ld, temperature, per, probs, ws, stream),
+                                     "token_probs launch");
+  prof_mark(stream, nullptr);
+  return r;
 }
 
 ENGRAM_API size_t engram_verify_drafts_workspace(int64_t S, int64_t V) {

@@ -292,8 +292,142 @@ probs_long_kernel(ProbsArgs a) {
   if (vt < V) out[vt] = et * inv;
 }
 
+// Few rows, long ones: kSegment entries a workgroup.  A first launch leaves
+// each segment's maximum, its first place and the sum relative to it; a
+// second one joins them for its row and writes its segment (read again, from
+// the L2).
+constexpr int kSegThreads = 256, kSegQuads = 8, kSegment = kSegThreads * kSegQuads * 4;
+
+struct Segment {
+  float top, sum;   // NaN where the segment holds one
+  int32_t at;
+  int32_t pad;
+};
+
 template <int DT>
-void launch_probs_dt(const ProbsArgs& a, int64_t rows, hipStream_t s) {
+struct SegmentRow {
+  const void* in;
+  int64_t q0, quads, vt;   // first quad of this thread, whole quads of the row, its entry behind them (last segment)
+  __device__ __forceinline__ SegmentRow(const ProbsArgs& a, int64_t row, int seg, int segs) {
+    constexpr int size = DT == ENGRAM_BF16 ? 2 : 4;
+    in = static_cast<const char*>(a.logits) + row * a.ld * size;
+    quads = a.V / 4;
+    q0 = static_cast<int64_t>(seg) * (kSegment / 4) + threadIdx.x;
+    vt = seg == segs - 1 ? quads * 4 + threadIdx.x : a.V;
+  }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kSegThreads)
+probs_segments_kernel(ProbsArgs a, int segs, Segment* __restrict__ part) {
+  __shared__ ProbsShared<kSegThreads> sh;
+  const int64_t row = blockIdx.x / segs;
+  const int seg = static_cast<int>(blockIdx.x % segs);
+  const SegmentRow<DT> r(a, row, seg, segs);
+  Quad<DT> x[kSegQuads];
+#pragma unroll
+  for (int n = 0; n < kSegQuads; ++n) x[n] = load_quad<DT>(r.in, r.q0 + n * kSegThreads, r.quads);
+  const float temp = a.temperature != nullptr ? a.temperature[row / a.per] : 1.0f;
+  const float xt = load_tail<DT>(r.in, r.vt, a.V);
+  float top = xt;
+  bool nan = xt != xt;
+#pragma unroll
+  for (int n = 0; n < kSegQuads; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float l = x[n].at(k);
+      nan |= l != l;
+      top = fmaxf(top, l);
+    }
+  top = group_max<kSegThreads>(top, nan, sh.top);
+  int at = xt == top ? static_cast<int>(r.vt) : INT32_MAX;
+#pragma unroll
+  for (int n = kSegQuads - 1; n >= 0; --n)
+#pragma unroll
+    for (int k = 3; k >= 0; --k) at = x[n].at(k) == top ? (static_cast<int>(r.q0) + n * kSegThreads) * 4 + k : at;
+  at = group_min<kSegThreads>(at, sh.first);
+  float sum = 0.f;
+  if (top > -__builtin_inff() && top < __builtin_inff()) {
+    const float f = kLog2e / temp;
+    sum = __builtin_amdgcn_exp2f((xt - top) * f);
+#pragma unroll
+    for (int n = 0; n < kSegQuads; ++n) {
+      float e[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f);
+      sum += (e[0] + e[1]) + (e[2] + e[3]);
+    }
+  }
+  sum = group_sum<kSegThreads>(sum, sh.sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = Segment{top, sum, at, 0};
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kSegThreads)
+probs_join_kernel(ProbsArgs a, int segs, const Segment* __restrict__ part) {
+  __shared__ ProbsShared<kSegThreads> sh;
+  const int64_t row = blockIdx.x / segs;
+  const int seg = static_cast<int>(blockIdx.x % segs);
+  const SegmentRow<DT> r(a, row, seg, segs);
+  float* out = a.probs + row * a.V;
+  Quad<DT> x[kSegQuads];
+#pragma unroll
+  for (int n = 0; n < kSegQuads; ++n) x[n] = load_quad<DT>(r.in, r.q0 + n * kSegThreads, r.quads);
+  const float temp = a.temperature != nullptr ? a.temperature[row / a.per] : 1.0f;
+  const float xt = load_tail<DT>(r.in, r.vt, a.V);
+  const Segment* mine = part + row * segs;
+  float top = -__builtin_inff();
+  bool nan = false;
+  for (int i = threadIdx.x; i < segs; i += kSegThreads) {
+    const float t = mine[i].top;
+    nan |= t != t;
+    top = fmaxf(top, t);
+  }
+  top = group_max<kSegThreads>(top, nan, sh.top);
+  float fill;
+  const bool constant = constant_row(top, temp, &fill);
+  if (constant || !(temp > 0.f)) {
+    int at = INT32_MAX;
+    for (int i = threadIdx.x; i < segs; i += kSegThreads) at = mine[i].top == top ? min(at, mine[i].at) : at;
+    at = group_min<kSegThreads>(at, sh.first);
+    auto value = [&](int64_t v) { return constant ? fill : (v == at ? 1.f : 0.f); };
+    for (int n = 0; n < kSegQuads; ++n) {
+      const int64_t q = r.q0 + n * kSegThreads;
+      store_quad(out, q, r.quads, f32x4_t{value(q * 4), value(q * 4 + 1), value(q * 4 + 2), value(q * 4 + 3)});
+    }
+    if (r.vt < a.V) out[r.vt] = value(r.vt);
+    return;
+  }
+  const float f = kLog2e / temp;
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < segs; i += kSegThreads)
+    sum += mine[i].top > -__builtin_inff() ? mine[i].sum * __builtin_amdgcn_exp2f((mine[i].top - top) * f) : 0.f;
+  const float inv = 1.0f / group_sum<kSegThreads>(sum, sh.sum);
+#pragma unroll
+  for (int n = 0; n < kSegQuads; ++n) {
+    f32x4_t y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f) * inv;
+    store_quad(out, r.q0 + n * kSegThreads, r.quads, y);
+  }
+  if (r.vt < a.V) out[r.vt] = __builtin_amdgcn_exp2f((xt - top) * f) * inv;
+}
+
+bool probs_splits(int64_t rows, int64_t V) { return rows <= 64 && V > 32768; }
+
+int probs_segments(int64_t V) { return static_cast<int>((V + kSegment - 1) / kSegment); }
+
+template <int DT>
+hipError_t launch_probs_dt(const ProbsArgs& a, int64_t rows, void* ws, hipStream_t s) {
+  if (probs_splits(rows, a.V)) {
+    const int segs = probs_segments(a.V);
+    const dim3 wide(static_cast<unsigned>(rows * segs));
+    launch_k(probs_segments_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<Segment*>(ws));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    launch_k(probs_join_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<const Segment*>(ws));
+    return hipGetLastError();
+  }
   const dim3 grid(static_cast<unsigned>(rows));
   // the fewest registers that hold a row
   if (a.V <= 1024 * 2) launch_k((probs_kernel<DT, 256, 2>), grid, dim3(256), 0, s, a);
@@ -303,19 +437,20 @@ void launch_probs_dt(const ProbsArgs& a, int64_t rows, hipStream_t s) {
   else if (a.V <= 4096 * 16) launch_k((probs_kernel<DT, 1024, 16>), grid, dim3(1024), 0, s, a);
   else if (DT == ENGRAM_BF16 && a.V <= 4096 * 32) launch_k((probs_kernel<ENGRAM_BF16, 1024, 32>), grid, dim3(1024), 0, s, a);
   else launch_k(probs_long_kernel<DT>, grid, dim3(1024), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t probs_workspace(int64_t, int64_t) { return 0; }
+size_t probs_workspace(int64_t rows, int64_t V) {
+  return probs_splits(rows, V) ? static_cast<size_t>(rows) * probs_segments(V) * sizeof(Segment) : 0;
+}
 
 hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
-                              int64_t per, float* probs, void*, hipStream_t s) {
+                              int64_t per, float* probs, void* ws, hipStream_t s) {
   if (rows == 0) return hipSuccess;
   const ProbsArgs a{logits, temperature, probs, V, ld, per};
-  if (dtype == ENGRAM_BF16) launch_probs_dt<ENGRAM_BF16>(a, rows, s);
-  else launch_probs_dt<ENGRAM_F32>(a, rows, s);
-  return hipGetLastError();
+  return dtype == ENGRAM_BF16 ? launch_probs_dt<ENGRAM_BF16>(a, rows, ws, s) : launch_probs_dt<ENGRAM_F32>(a, rows, ws, s);
 }
 
 namespace {
@@ -599,7 +734,7 @@ verify_parts_kernel(VerifyArgs a) {
 }
 
 // Few sequences with long rows: the sums are split over 16 workgroups a row.
-bool verify_splits(int64_t S, int64_t V) { return S <= 64 && V > 16384; }
+bool verify_splits(int64_t S, int64_t V) { return S <= 96 && V > 40960; }
 
 template <int DT>
 hipError_t launch_verify_dt(const VerifyArgs& a, int64_t S, hipStream_t s) {

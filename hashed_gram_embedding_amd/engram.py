@@ -219,34 +219,37 @@ def _stream(stream=None):
 # (device, dtype, shape, contiguity) and launch on the tensors' own device.
 
 def _check_tensor(name: str, t: torch.Tensor, dtypes, shape, device, strided: bool = False):
+    if t.dtype in dtypes and t.shape == shape and t.device == device and (strided or t.is_contiguous()):
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not strided and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _launch(fn, device: torch.device, stream, *args, ws=None):
     """fn(*args, stream) with `device` current, on `stream` (default: the
     device's current one); ws is scratch allocated for this call."""
+    index = device.index
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a GPU, not on {device}")
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
-    if torch.cuda.current_device() == device.index:
-        cur = torch.cuda.current_stream()
-        s = cur if stream is None else stream
-        _check(fn(*args, s.cuda_stream))
+    # (the raw handle of the current stream, without building a Stream object: 0.1 instead of 2.9 us a call)
+    current = torch._C._cuda_getCurrentRawStream(index)
+    s = current if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, s)
     else:
-        with torch.cuda.device(device):
-            cur = torch.cuda.current_stream()
-            s = cur if stream is None else stream
-            _check(fn(*args, s.cuda_stream))
-    if ws is not None and s.cuda_stream != cur.cuda_stream:
-        ws.record_stream(s)   # allocated on the current stream, used on another
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    if status != OK:
+        raise EngramError(status, last_error())
+    if ws is not None and s != current:
+        ws.record_stream(stream)   # allocated on the current stream, used on another
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
@@ -878,12 +881,13 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], drafted: 
     tokens = torch.empty((S, G + 1), dtype=torch.int32, device=dev)
     n_accepted = torch.empty(S, dtype=torch.int32, device=dev)
     own = None
-    if ws is None:
-        ws = own = torch.empty(max(lib().engram_verify_drafts_workspace(S, V), 256), dtype=torch.uint8, device=dev)
+    nbytes = lib().engram_verify_drafts_workspace(S, V)
+    if ws is None and nbytes:
+        ws = own = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _launch(lib().engram_verify_drafts, dev, stream, target.data_ptr(), None if draft is None else draft.data_ptr(),
             _DT_OF[target.dtype], drafted.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
-            u_accept.data_ptr(), u_sample.data_ptr(), S, G, V, tokens.data_ptr(), n_accepted.data_ptr(), ws.data_ptr(),
-            ws.numel(), ws=own)
+            u_accept.data_ptr(), u_sample.data_ptr(), S, G, V, tokens.data_ptr(), n_accepted.data_ptr(),
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), ws=own)
     return tokens, n_accepted
 
 
