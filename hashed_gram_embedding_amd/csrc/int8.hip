@@ -18,6 +18,7 @@ namespace engram {
 namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes at any output
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
@@ -273,15 +274,21 @@ project_i8_kernel(ProjectI8Args a) {
 // multiplied and its outputs are scaled and stored.  (One workgroup per tile
 // left the matrix cores idle at both ends of every tile: with 1024 columns a
 // tile has 8 slices, and 32763 x 1024 x 5120 took 227 us instead of 195.)
-// Tiles go to the XCDs in contiguous shares, the operand with fewer bytes
-// fastest within a share, so that it is re-read from the XCD's L2 and the
-// larger one is read once.
+// Tiles go to the XCDs in contiguous shares of an order that walks bands of
+// kBand token tiles, tokens fastest: the 32 tiles that an XCD works on at one
+// time span 8 x 4, so both operands are re-read from its L2 (tokens fastest
+// over all of them, 128 x 1/4 at that size: 218 us, outputs fastest, 20 x
+// 1.6: 202, bands: 185).  Outputs of the large tiles are stored past the L2
+// (nontemporal): written through it they drive the operands out, 300 -> 265
+// us at 1795 x 1024 x 128000.
 //
 // DIRECT: slices go from memory straight into LDS (both operands 16-byte
 // aligned, whole chunks).  Otherwise through registers, at any alignment.
+constexpr int kBand = 8;
+
 template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
 __global__ void __launch_bounds__(64 * WF * WT) __attribute__((amdgpu_waves_per_eu(2, 2)))
-project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t, int f_fastest) {
+project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   constexpr int NT = 64 * WF * WT;
   constexpr int I = TF / WF / 32, J = TT / WT / 32;   // 32 x 32 blocks of a wavefront
   constexpr int WC = TF * 8, QC = TT * 8;             // chunks of a slice
@@ -304,8 +311,10 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t, int f_fastest)
   auto tile_of = [&](int local, Tile* t) {
     const int id = xcd * share + local;
     if (local >= share || id >= n_tiles) return false;
-    t->f0 = static_cast<int64_t>(f_fastest ? id % tiles_f : id / tiles_t) * TF;
-    t->t0 = static_cast<int64_t>(f_fastest ? id / tiles_f : id % tiles_t) * TT;
+    const int band = id / (kBand * tiles_f), b0 = band * kBand, rows = min(kBand, tiles_t - b0);
+    const int in = id - band * kBand * tiles_f;
+    t->t0 = static_cast<int64_t>(b0 + in % rows) * TT;
+    t->f0 = static_cast<int64_t>(in / rows) * TF;
     return true;
   };
 
@@ -414,19 +423,39 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t, int f_fastest)
       }
       const u32x4_t* Ws = lds + buf * (WC + QC);
       const u32x4_t* Qs = Ws + WC;
-      if constexpr (DIRECT) __builtin_amdgcn_iglp_opt(0);
+      // The operands of step ks + 1 are read while step ks multiplies: one
+      // LDS read behind each of the first products.
+      i32x4_t fa[2][I], fb[2][J];
+      auto operands = [&](int set, int ks) {
+        const int kc = (ks * 2 + lh) ^ ((lr >> 1) & 7);
+#pragma unroll
+        for (int i = 0; i < I; ++i) fa[set][i] = __builtin_bit_cast(i32x4_t, Ws[(wf * (TF / WF) + i * 32 + lr) * 8 + kc]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) fb[set][j] = __builtin_bit_cast(i32x4_t, Qs[(wt * (TT / WT) + j * 32 + lr) * 8 + kc]);
+      };
+      operands(0, 0);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        const int kc = (ks * 2 + lh) ^ ((lr >> 1) & 7);
-        i32x4_t fa[I], fb[J];
-#pragma unroll
-        for (int i = 0; i < I; ++i) fa[i] = __builtin_bit_cast(i32x4_t, Ws[(wf * (TF / WF) + i * 32 + lr) * 8 + kc]);
-#pragma unroll
-        for (int j = 0; j < J; ++j) fb[j] = __builtin_bit_cast(i32x4_t, Qs[(wt * (TT / WT) + j * 32 + lr) * 8 + kc]);
+        if (ks < 3) operands((ks + 1) & 1, ks + 1);
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
-          for (int j = 0; j < J; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < J; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
+      }
+      if constexpr (DIRECT && I * J >= I + J) {
+        constexpr int kMfma = 0x8, kLdsRead = 0x100;
+        __builtin_amdgcn_sched_group_barrier(kLdsRead, I + J, 0);
+#pragma unroll
+        for (int ks = 0; ks < 3; ++ks) {
+#pragma unroll
+          for (int z = 0; z < I + J; ++z) {
+            __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+          }
+          if constexpr (I * J > I + J) __builtin_amdgcn_sched_group_barrier(kMfma, I * J - I - J, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kMfma, I * J, 0);
       }
       if constexpr (!DIRECT) {
         if (same || more) store(buf ^ 1);
@@ -475,7 +504,10 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t, int f_fastest)
         if (tok < a.n_tok && o < a.n_out) {
           OutT* dst = static_cast<OutT*>(a.out) + tok * a.n_out + o;
           if (o + EPC <= a.n_out) {
-            __builtin_memcpy(dst, &v[it], 16);
+            if constexpr (TF * TT >= 65536)
+              __builtin_nontemporal_store(v[it], reinterpret_cast<u32x4_any_t*>(dst));
+            else
+              __builtin_memcpy(dst, &v[it], 16);
           } else {
             const int left = static_cast<int>(a.n_out - o);
 #pragma unroll
@@ -667,7 +699,7 @@ hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
   if (tf * tt > (1 << 30)) return hipErrorInvalidValue;
   // one workgroup of 8 wavefronts per CU, or two of 4
   const int grid = static_cast<int>(std::min<int64_t>(256 * 8 / (WF * WT), (tf * tt + 7) / 8 * 8));
-  launch_k(fn, dim3(grid), dim3(64 * WF * WT), kLds, s, a, static_cast<int>(tf), static_cast<int>(tt), a.n_out <= a.n_tok ? 1 : 0);
+  launch_k(fn, dim3(grid), dim3(64 * WF * WT), kLds, s, a, static_cast<int>(tf), static_cast<int>(tt));
   return hipGetLastError();
 }
 
