@@ -26,10 +26,6 @@ typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
 // ---- quantisation of rows ----
 
-__device__ __forceinline__ float load_f32(const void* x, int64_t i, int dtype) {
-  return dtype == ENGRAM_BF16 ? bf16_to_f32(static_cast<const uint16_t*>(x)[i]) : static_cast<const float*>(x)[i];
-}
-
 // What quantising a row needs: its largest magnitude, and 127 over it.  Both
 // and the values are scaled by g, a power of two that keeps 127 / top finite
 // for rows of the smallest numbers (exact: nothing is rounded by it).
@@ -73,21 +69,25 @@ __device__ __forceinline__ float row_scale(uint32_t top) {
 // row is zero or holds an infinity or a NaN.
 __device__ __forceinline__ bool row_has_codes(uint32_t top) { return top != 0u && top < 0x7f800000u; }
 
-// Eight values of a row, 16-byte aligned.
+// Eight values of a row from any element on.
 template <int DT>
 __device__ __forceinline__ void load8(const void* x, int64_t i, float* f) {
   if constexpr (DT == ENGRAM_BF16) {
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i), f);
+    uint4 v;
+    __builtin_memcpy(&v, static_cast<const uint16_t*>(x) + i, 16);
+    unpack8(v, f);
   } else {
-    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(x) + i);
-    const f32x4_t a = p[0], b = p[1];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[k] = a[k];
-      f[4 + k] = b[k];
-    }
+    __builtin_memcpy(f, static_cast<const float*>(x) + i, 32);
   }
 }
+
+template <int DT>
+__device__ __forceinline__ float load1(const void* x, int64_t i) {
+  if constexpr (DT == ENGRAM_BF16) return bf16_to_f32(static_cast<const uint16_t*>(x)[i]);
+  else return static_cast<const float*>(x)[i];
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 __device__ __forceinline__ u32x2_t quantize8(const float* f, const RowScale& r) {
   u32x2_t w{0, 0};
@@ -96,57 +96,79 @@ __device__ __forceinline__ u32x2_t quantize8(const float* f, const RowScale& r) 
   return w;
 }
 
-// Rows of up to 512 N columns in runs of 8 (aligned): one wavefront a row,
-// every value read once, all loads in flight together.  Zero rows have scale
-// 0, rows with an infinity or a NaN scale NaN and codes 0.
+// Where a row's codes go.  Plain rows keep their columns.  In the product's
+// own layout (tail) the last, incomplete run of 16 columns lies right-aligned
+// in its 16 bytes, zeros before it: the product reads W's last 16 columns
+// there, and the zeros leave out those that the run before holds.
+struct CodeRow {
+  int8_t* dst;
+  int whole, shift;
+  __device__ __forceinline__ CodeRow(int8_t* row, int cols, bool tail)
+      : dst(row), whole(cols / 16 * 16), shift(tail && cols % 16 != 0 ? 16 - cols % 16 : 0) {}
+  __device__ __forceinline__ int8_t* at(int c) const { return dst + (c < whole ? c : c + shift); }
+};
+
+// Rows of fewer than 512 N + 8 columns: one wavefront a row, runs of 8, every
+// value read once, all loads in flight together; up to 7 columns behind the
+// last run are the first lanes' own.  A row of zeros has scale 0, one holding
+// an infinity or a NaN codes 0 and scale NaN.
 template <int DT, int N>
 __global__ void __launch_bounds__(256)
-quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ q, int64_t ldq,
+quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ q, int64_t ldq, int tail,
                      float* __restrict__ scale) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), base = row * cols;
+  const int lane = threadIdx.x & 63, c8 = cols / 8 * 8, ct = c8 + lane;
   if (row >= rows) return;
   float f[N][8];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int c = (n * 64 + lane) * 8;
-    if (c < cols) {
-      load8<DT>(x, row * cols + c, f[n]);
+    if (c < c8) {
+      load8<DT>(x, base + c, f[n]);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[n][k] = 0.f;
     }
   }
-  uint32_t top = 0;
+  const float ft = ct < cols ? load1<DT>(x, base + ct) : 0.f;
+  uint32_t top = magnitude(ft);
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[n][k]) & 0x7fffffffu);
+    for (int k = 0; k < 8; ++k) top = max(top, magnitude(f[n][k]));
   top = wave_top(top);
   if (lane == 0) scale[row] = row_scale(top);
   const bool codes = row_has_codes(top);
   const RowScale rs = row_factors(__uint_as_float(top));
+  const CodeRow out(q + row * ldq, cols, tail != 0);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int c = (n * 64 + lane) * 8;
-    if (c < cols) *reinterpret_cast<u32x2_t*>(q + row * ldq + c) = codes ? quantize8(f[n], rs) : u32x2_t{0, 0};
+    const u32x2_t w = codes ? quantize8(f[n], rs) : u32x2_t{0, 0};
+    if (c < c8) __builtin_memcpy(out.at(c), &w, 8);
   }
+  if (ct < cols) *out.at(ct) = static_cast<int8_t>(codes ? quantize(ft, rs) : 0);
+  if (lane < out.shift) out.dst[out.whole + lane] = 0;
 }
 
-// Any columns and alignment, one row per workgroup, read twice (the second
-// time from the L2).  With `tail` the last, incomplete run of 16 columns is
-// stored right-aligned in its 16 bytes (zeros before it): the product reads
-// W's last 16 columns there (load_chunk) and the zeros leave out those
-// already counted.
+// Longer rows: one workgroup a row, which reads it twice (the second time
+// from the L2).
+template <int DT>
 __global__ void __launch_bounds__(256)
-quantize_any_kernel(const void* __restrict__ x, int dtype, int cols, int8_t* __restrict__ q, int64_t ldq, int tail,
-                    float* __restrict__ scale) {
+quantize_long_kernel(const void* __restrict__ x, int cols, int8_t* __restrict__ q, int64_t ldq, int tail,
+                     float* __restrict__ scale) {
   __shared__ uint32_t part[4];
   const int64_t row = blockIdx.x, base = row * cols;
-  const int t = threadIdx.x;
-  uint32_t top = 0;
+  const int t = threadIdx.x, c8 = cols / 8 * 8, ct = c8 + t;
+  const float ft = ct < cols ? load1<DT>(x, base + ct) : 0.f;
+  uint32_t top = magnitude(ft);
 #pragma unroll 4
-  for (int c = t; c < cols; c += 256) top = max(top, __float_as_uint(load_f32(x, base + c, dtype)) & 0x7fffffffu);
+  for (int c = t * 8; c < c8; c += 256 * 8) {
+    float f[8];
+    load8<DT>(x, base + c, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, magnitude(f[k]));
+  }
   top = wave_top(top);
   if ((t & 63) == 0) part[t >> 6] = top;
   __syncthreads();
@@ -154,13 +176,16 @@ quantize_any_kernel(const void* __restrict__ x, int dtype, int cols, int8_t* __r
   if (t == 0) scale[row] = row_scale(top);
   const bool codes = row_has_codes(top);
   const RowScale rs = row_factors(__uint_as_float(top));
-  const int whole = tail ? cols / 16 * 16 : cols;
-  const int shift = tail && whole < cols ? 16 - (cols - whole) : 0;
-  int8_t* dst = q + row * ldq;
+  const CodeRow out(q + row * ldq, cols, tail != 0);
 #pragma unroll 4
-  for (int c = t; c < cols; c += 256)
-    dst[c < whole ? c : c + shift] = static_cast<int8_t>(codes ? quantize(load_f32(x, base + c, dtype), rs) : 0);
-  if (t < shift) dst[whole + t] = 0;
+  for (int c = t * 8; c < c8; c += 256 * 8) {
+    float f[8];
+    load8<DT>(x, base + c, f);
+    const u32x2_t w = codes ? quantize8(f, rs) : u32x2_t{0, 0};
+    __builtin_memcpy(out.at(c), &w, 8);
+  }
+  if (ct < cols) *out.at(ct) = static_cast<int8_t>(codes ? quantize(ft, rs) : 0);
+  if (t < out.shift) out.dst[out.whole + t] = 0;
 }
 
 // ---- product ----
@@ -178,35 +203,25 @@ struct ProjectI8Args {
   int tailed;            // q's last run of 16 columns is right-aligned and zero-filled
 };
 
-// 16 columns of a row of K bytes, chunk c, from any alignment.  A last chunk
-// that is not whole reads the row's last 16 bytes instead (rows of fewer than
-// 16 are read byte by byte, right-aligned); the other operand holds zeros for
-// the columns that are then read twice.
-__device__ __forceinline__ u32x4_t load_chunk(const int8_t* row, int c, int K) {
-  u32x4_t v{0, 0, 0, 0};
-  if (K >= 16) {
-    __builtin_memcpy(&v, row + min(c * 16, K - 16), 16);
-  } else {
-    for (int i = 0; i < K; ++i) {
-      const int b = 16 - K + i;
-      v[b >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[i])) << (8 * (b & 3));
-    }
+// Which bytes of a row's last 16 belong to its last chunk: all of them, or
+// the K % 16 behind the ones that the chunk before holds.
+__device__ __forceinline__ u32x4_t tail_mask(int K) {
+  const int twice = (16 - K % 16) % 16;
+  u32x4_t m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = min(max(twice - 4 * i, 0), 4);
+    m[i] = n == 4 ? 0u : 0xffffffffu << (8 * n);
   }
-  return v;
+  return m;
 }
 
-// The same of a token row, with the columns counted before cleared.
-__device__ __forceinline__ u32x4_t load_chunk_once(const int8_t* row, int c, int K) {
-  u32x4_t v = load_chunk(row, c, K);
-  const int twice = c * 16 + 16 - K;   // leading bytes that an earlier chunk holds
-  if (twice > 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = min(max(twice - 4 * i, 0), 4);
-      v[i] = n == 4 ? 0u : v[i] & (0xffffffffu << (8 * n));
-    }
-  }
-  return v;
+// Chunk c (16 columns) of a row of K >= 16 codes at any alignment; the last
+// one right-aligned, zeros before it.
+__device__ __forceinline__ u32x4_t load_chunk(const int8_t* row, int c, int K) {
+  u32x4_t v;
+  __builtin_memcpy(&v, row + min(c * 16, K - 16), 16);
+  return c * 16 + 16 > K ? v & tail_mask(K) : v;
 }
 
 template <typename OutT>
@@ -214,52 +229,6 @@ __device__ __forceinline__ OutT to_out(float f) {
   if constexpr (sizeof(OutT) == 2) return f32_to_bf16(f);
   else return f;
 }
-
-// General product: any K and alignment.  64 tokens x 64 outputs per workgroup
-// of four wavefronts, 32 x 32 each on v_mfma_i32_32x32x32_i8; 64 columns a
-// step through registers into LDS.
-template <typename OutT>
-__global__ void __launch_bounds__(256)
-project_i8_kernel(ProjectI8Args a) {
-  __shared__ u32x4_t Ws[64 * 4], Qs[64 * 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tiles_n = static_cast<int>((a.n_out + 63) / 64);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x % tiles_n) * 64, t0 = static_cast<int64_t>(blockIdx.x / tiles_n) * 64;
-  const int chunks = (a.K + 15) / 16;
-  const int r = tid >> 2, cc = tid & 3;
-  const int8_t* wrow = a.w + min(n0 + r, a.n_out - 1) * a.K;
-  const int8_t* qrow = a.q + min(t0 + r, a.n_tok - 1) * a.ldq;
-  i32x16_t acc{};
-  for (int c0 = 0; c0 < chunks; c0 += 4) {
-    const int c = c0 + cc;
-    u32x4_t vw{0, 0, 0, 0}, vq{0, 0, 0, 0};
-    if (c < chunks) {
-      vw = load_chunk(wrow, c, a.K);
-      vq = a.tailed ? *reinterpret_cast<const u32x4_t*>(qrow + c * 16) : load_chunk_once(qrow, c, a.K);
-    }
-    __syncthreads();
-    Ws[r * 4 + (cc ^ (r & 3))] = vw;
-    Qs[r * 4 + (cc ^ (r & 3))] = vq;
-    __syncthreads();
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int kc = ks * 2 + (lane >> 5);
-      const int rw = (wave & 1) * 32 + (lane & 31), rq = (wave >> 1) * 32 + (lane & 31);
-      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, Ws[rw * 4 + (kc ^ (rw & 3))]),
-                                                  __builtin_bit_cast(i32x4_t, Qs[rq * 4 + (kc ^ (rq & 3))]), acc, 0, 0, 0);
-    }
-  }
-  const int64_t tok = t0 + (wave >> 1) * 32 + (lane & 31);
-  if (tok >= a.n_tok) return;
-  const float st = a.q_scale[tok];
-  OutT* out = static_cast<OutT*>(a.out) + tok * a.n_out;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t o = n0 + (wave & 1) * 32 + (i >> 2) * 8 + (lane >> 5) * 4 + (i & 3);
-    if (o < a.n_out) out[o] = to_out<OutT>(static_cast<float>(acc[i]) * st * a.w_scale[o]);
-  }
-}
-
 
 // Tiled product for the sizes that fill the chip.  A workgroup of WF x WT
 // wavefronts forms TF outputs x TT tokens; W rows are the A operand of
@@ -345,22 +314,33 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (__attribute__((address_space(3))) void*)(dst + WC + i * NT), 16,
                                                in ? qo + i * (NT / 8) * ldq : qo, kt * 128, 0, 0);
   };
-  // Through registers: load() early, store() once the buffer is free.
+  // Through registers: load() early, store() once the buffer is free.  A last
+  // chunk that is not whole reads the row's last 16 bytes; the token operand
+  // then gets zeros for the columns counted before (codes of this library's
+  // own quantisation hold them already) and for chunks past the last.
   u32x4_t vw[DIRECT ? 1 : NW], vq[DIRECT ? 1 : NQ];
   auto load = [&](const Tile& t, int kt) {
     const int c = kt * 8 + ch;
+    const int wc = min(c * 16, K - 16), qc = min(c * 16, a.tailed ? (chunks - 1) * 16 : K - 16);
+    const int w_last = static_cast<int>(min(static_cast<int64_t>(TF), a.n_out - t.f0)) - 1;
+    const int q_last = static_cast<int>(min(static_cast<int64_t>(TT), a.n_tok - t.t0)) - 1;
+    const int8_t* wb = a.w + t.f0 * K;
+    const int8_t* qb = a.q + t.t0 * ldq;
 #pragma unroll
     for (int i = 0; i < (DIRECT ? 0 : NW); ++i)
-      vw[i] = load_chunk(a.w + min(t.f0 + r0 + i * (NT / 8), a.n_out - 1) * K, min(c, chunks - 1), K);
+      __builtin_memcpy(&vw[i], wb + static_cast<uint32_t>(min(r0 + i * (NT / 8), w_last) * K + wc), 16);
 #pragma unroll
-    for (int i = 0; i < (DIRECT ? 0 : NQ); ++i) {
-      const int8_t* row = a.q + min(t.t0 + r0 + i * (NT / 8), a.n_tok - 1) * a.ldq;
-      vq[i] = u32x4_t{0, 0, 0, 0};
-      if (c < chunks) vq[i] = a.tailed ? *reinterpret_cast<const u32x4_t*>(row + c * 16) : load_chunk_once(row, c, K);
-    }
+    for (int i = 0; i < (DIRECT ? 0 : NQ); ++i)
+      __builtin_memcpy(&vq[i], qb + static_cast<uint32_t>(min(r0 + i * (NT / 8), q_last) * ldq + qc), 16);
   };
-  auto store = [&](int buf) {
+  auto store = [&](int kt, int buf) {
     u32x4_t* dst = lds + buf * (WC + QC) + tid;
+    const int c = kt * 8 + ch;
+    if (c >= chunks || (c == chunks - 1 && !a.tailed)) {
+      const u32x4_t keep = c < chunks ? tail_mask(K) : u32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < (DIRECT ? 0 : NQ); ++i) vq[i] &= keep;
+    }
 #pragma unroll
     for (int i = 0; i < (DIRECT ? 0 : NW); ++i) dst[i * NT] = vw[i];
 #pragma unroll
@@ -393,7 +373,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
     issue(cur, 0, 0);
   } else {
     load(cur, 0);
-    store(0);
+    store(0, 0);
   }
   for (;;) {
     i32x16_t acc[I][J];
@@ -420,6 +400,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       } else {
         if (same || more) load(same ? cur : next, same ? kt + 1 : 0);
         if (!same && more) scales(next, par ^ 1);
+        asm volatile("" ::: "memory");   // the loads go out here, not next to their use behind the products
       }
       const u32x4_t* Ws = lds + buf * (WC + QC);
       const u32x4_t* Qs = Ws + WC;
@@ -443,7 +424,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
           for (int j = 0; j < J; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
       }
-      if constexpr (DIRECT && I * J >= I + J) {
+      if constexpr (I * J >= I + J) {
         constexpr int kMfma = 0x8, kLdsRead = 0x100;
         __builtin_amdgcn_sched_group_barrier(kLdsRead, I + J, 0);
 #pragma unroll
@@ -458,7 +439,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
         __builtin_amdgcn_sched_group_barrier(kMfma, I * J, 0);
       }
       if constexpr (!DIRECT) {
-        if (same || more) store(buf ^ 1);
+        if (same || more) store(same ? kt + 1 : 0, buf ^ 1);
       }
       buf ^= 1;
     }
@@ -527,21 +508,84 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   }
 }
 
-// Few tokens: bound by reading W once.  Every wavefront streams 16 rows of W
-// from memory straight into the operand registers of v_mfma_i32_16x16x64_i8
-// (lane l: row l & 15, bytes 16 (l >> 4) of each run of 64), 16 loads (1024
-// columns) in flight, while the tokens' codes sit in LDS.  A row of codes
-// starts 16 bytes further round the banks than the one before (stride 16
-// modulo 256), so the 16 rows of an operand read are free of conflicts.
-// E_DT: type of e; up to kFewQuantized float rows are quantised here, one per
-// wavefront, which saves a launch, more are quantised beforehand.
-// NB: blocks of 16 tokens.
+// Fewer than 16 columns: one thread an output.
+template <typename OutT>
+__global__ void __launch_bounds__(256)
+project_i8_short_kernel(ProjectI8Args a) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= a.n_tok * a.n_out) return;
+  const int64_t t = id / a.n_out, o = id - t * a.n_out;
+  const int8_t* q = a.q + t * a.ldq + (a.tailed ? a.ldq - a.K : 0);   // right-aligned in its 16 bytes
+  const int8_t* w = a.w + o * a.K;
+  int sum = 0;
+  for (int c = 0; c < a.K; ++c) sum += static_cast<int>(q[c]) * static_cast<int>(w[c]);
+  static_cast<OutT*>(a.out)[id] = to_out<OutT>(static_cast<float>(sum) * a.q_scale[t] * a.w_scale[o]);
+}
+
+// Few tokens: bound by reading W once, or by latency.  Every wavefront streams 16 rows of W from memory straight into the operand
+// registers of v_mfma_i32_16x16x64_i8 (lane l: row l & 15, bytes 16 (l >> 4)
+// of each run of 64), 16 loads (1024 columns) in flight, while the codes of
+// up to 16 NB tokens sit in LDS.  A row of codes starts 16 bytes further
+// round the banks than the one before (stride 16 modulo 256), so the 16 rows
+// of an operand read are free of conflicts.
+// E_DT: type of e.  Up to 16 float rows are quantised here, by every
+// workgroup, behind the first loads of W: it saves a launch (9 x 1024 x 2048
+// 9.5 -> 8.7 us).  With 32 it takes longer than a launch of its own (13.4
+// against 11.3 us).
+// 1 x 1024 x 128000 takes 24.3 us (5.4 TB/s), 32 x 1024 x 128000 29.4; past 32
+// tokens the tiles are faster (64 tokens: 46 against 36 us).
 constexpr int kFewWaves = 8;
-constexpr int kFewQuantized = 8;
-constexpr int kFewTokens = 64;
 constexpr int kFewLds = 150 << 10;
 
 __host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 + 16; }
+
+// Rows wave, wave + 8, .. of e (R of them per wavefront) to codes and scales
+// in LDS; two passes over the rows, the loads of all of them together.
+template <int E_DT, int R>
+__device__ __forceinline__ void quantize_into(const void* e, int rows, int K, u32x4_t* lds, int stride, float* sq) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c8 = K / 8 * 8, ct = c8 + lane, chunks = (K + 15) / 16;
+  uint32_t top[R];
+  float ft[R];
+  int64_t base[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    base[i] = static_cast<int64_t>(min(wave + i * kFewWaves, rows - 1)) * K;   // rows past the last repeat it
+    ft[i] = ct < K ? load1<E_DT>(e, base[i] + ct) : 0.f;
+    top[i] = magnitude(ft[i]);
+  }
+#pragma unroll 2
+  for (int c = lane * 8; c < c8; c += 512) {
+    float f[R][8];
+#pragma unroll
+    for (int i = 0; i < R; ++i) load8<E_DT>(e, base[i] + c, f[i]);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top[i] = max(top[i], magnitude(f[i][k]));
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) top[i] = wave_top(top[i]);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int t = wave + i * kFewWaves;
+    if (t >= rows) break;
+    const bool codes = row_has_codes(top[i]);
+    const RowScale rs = row_factors(__uint_as_float(top[i]));
+    const CodeRow out(reinterpret_cast<int8_t*>(lds + t * stride), K, true);
+    if (lane == 0) sq[t] = row_scale(top[i]);
+#pragma unroll 2
+    for (int c = lane * 8; c < c8; c += 512) {
+      float f[8];
+      load8<E_DT>(e, base[i] + c, f);
+      const u32x2_t w = codes ? quantize8(f, rs) : u32x2_t{0, 0};
+      __builtin_memcpy(out.at(c), &w, 8);
+    }
+    if (ct < K) *out.at(ct) = static_cast<int8_t>(codes ? quantize(ft[i], rs) : 0);
+    if (lane < out.shift) out.dst[out.whole + lane] = 0;
+    for (int c = chunks + lane; c < (chunks + 3) / 4 * 4; c += 64) lds[t * stride + c] = u32x4_t{0, 0, 0, 0};
+  }
+}
 
 template <typename OutT, int E_DT, int NB>
 __global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(NB == 1 ? 4 : 2, NB == 1 ? 4 : 2)))
@@ -569,44 +613,14 @@ project_i8_few_kernel(ProjectI8Args a, const void* __restrict__ e) {
       const int t = i / (steps * 4), c = i % (steps * 4);
       const int8_t* row = a.q + t * a.ldq;
       u32x4_t v{0, 0, 0, 0};
-      if (c < chunks) v = a.tailed ? *reinterpret_cast<const u32x4_t*>(row + c * 16) : load_chunk_once(row, c, K);
+      if (c < chunks) v = a.tailed ? *reinterpret_cast<const u32x4_t*>(row + c * 16) : load_chunk(row, c, K);
       lds[t * stride + c] = v;
     }
     if (threadIdx.x < 16 * NB) sq[threadIdx.x] = a.q_scale[min(static_cast<int>(threadIdx.x), n_tok - 1)];
+  } else if (n_tok <= kFewWaves) {
+    quantize_into<E_DT, 1>(e, n_tok, K, lds, stride, sq);
   } else {
-    for (int t = wave; t < n_tok; t += kFewWaves) {
-      const int64_t base = static_cast<int64_t>(t) * K;
-      int8_t* dst = reinterpret_cast<int8_t*>(lds + t * stride);
-      const bool runs = K % 16 == 0 && reinterpret_cast<uintptr_t>(e) % 16 == 0;
-      uint32_t top = 0;
-      if (runs) {
-        for (int c = lane * 8; c < K; c += 512) {
-          float f[8];
-          load8<E_DT>(e, base + c, f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
-        }
-      } else {
-        for (int c = lane; c < K; c += 64) top = max(top, __float_as_uint(load_f32(e, base + c, E_DT)) & 0x7fffffffu);
-      }
-      top = wave_top(top);
-      if (lane == 0) sq[t] = row_scale(top);
-      const bool codes = row_has_codes(top);
-      const RowScale rs = row_factors(__uint_as_float(top));
-      if (runs) {
-        for (int c = lane * 8; c < K; c += 512) {
-          float f[8];
-          load8<E_DT>(e, base + c, f);
-          *reinterpret_cast<u32x2_t*>(dst + c) = codes ? quantize8(f, rs) : u32x2_t{0, 0};
-        }
-      } else {
-        const int whole = K / 16 * 16, shift = whole < K ? 16 - (K - whole) : 0;
-        for (int c = lane; c < K; c += 64)
-          dst[c < whole ? c : c + shift] = static_cast<int8_t>(codes ? quantize(load_f32(e, base + c, E_DT), rs) : 0);
-        if (lane < shift) dst[whole + lane] = 0;
-      }
-      for (int c = chunks + lane; c < steps * 4; c += 64) lds[t * stride + c] = u32x4_t{0, 0, 0, 0};
-    }
+    quantize_into<E_DT, 2>(e, n_tok, K, lds, stride, sq);
   }
   __syncthreads();
 
@@ -673,12 +687,10 @@ hipError_t launch_few(const ProjectI8Args& a, const void* e, hipStream_t s) {
 
 template <typename OutT, int E_DT>
 hipError_t launch_few_blocks(const ProjectI8Args& a, const void* e, hipStream_t s) {
-  if (a.n_tok <= 16) return launch_few<OutT, E_DT, 1>(a, e, s);
   if constexpr (E_DT == ENGRAM_I8) {
-    if (a.n_tok <= 32) return launch_few<OutT, E_DT, 2>(a, e, s);
-    return launch_few<OutT, E_DT, 4>(a, e, s);
+    if (a.n_tok > 16) return launch_few<OutT, E_DT, 2>(a, e, s);
   }
-  return hipErrorInvalidValue;
+  return launch_few<OutT, E_DT, 1>(a, e, s);
 }
 
 template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
@@ -714,33 +726,33 @@ hipError_t launch_tiles(const ProjectI8Args& a, hipStream_t s) {
 int64_t i8_row_stride(int64_t cols) { return (cols + 15) / 16 * 16; }
 
 template <int DT>
-void launch_quantize_rows(const void* x, int64_t rows, int cols, int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
-  if (cols <= 512) launch_k((quantize_rows_kernel<DT, 1>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
-  else if (cols <= 1024) launch_k((quantize_rows_kernel<DT, 2>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
-  else if (cols <= 2048) launch_k((quantize_rows_kernel<DT, 4>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
-  else launch_k((quantize_rows_kernel<DT, 8>), grid, dim3(256), 0, s, x, rows, cols, q, ldq, scale);
+void launch_quantize_dt(const void* x, int64_t rows, int cols, int8_t* q, int64_t ldq, int tail, float* scale, hipStream_t s) {
+  const dim3 wide(static_cast<unsigned>((rows + 3) / 4));
+  // the fewest registers that hold a row
+  if (cols < 512 + 8) launch_k((quantize_rows_kernel<DT, 1>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
+  else if (cols < 1024 + 8) launch_k((quantize_rows_kernel<DT, 2>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
+  else if (cols < 2048 + 8) launch_k((quantize_rows_kernel<DT, 4>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
+  else if (cols < 4096 + 8) launch_k((quantize_rows_kernel<DT, 8>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
+  else launch_k(quantize_long_kernel<DT>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, x, cols, q, ldq, tail, scale);
 }
 
 hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail,
                               float* scale, hipStream_t s) {
   if (rows == 0) return hipSuccess;
-  const int c = static_cast<int>(cols);
-  // runs of 8 with 16-byte loads (f32: two) and 8-byte stores; a whole number
-  // of 16-column runs has no tail to shift
-  const bool runs = c % 8 == 0 && c <= 4096 && ldq % 8 == 0 && (!tail || c % 16 == 0) && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-                    reinterpret_cast<uintptr_t>(q) % 8 == 0;
-  if (runs && dtype == ENGRAM_BF16) launch_quantize_rows<ENGRAM_BF16>(x, rows, c, q, ldq, scale, s);
-  else if (runs) launch_quantize_rows<ENGRAM_F32>(x, rows, c, q, ldq, scale, s);
-  else launch_k(quantize_any_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, x, dtype, c, q, ldq, tail ? 1 : 0, scale);
+  if (dtype == ENGRAM_BF16) launch_quantize_dt<ENGRAM_BF16>(x, rows, static_cast<int>(cols), q, ldq, tail ? 1 : 0, scale, s);
+  else launch_quantize_dt<ENGRAM_F32>(x, rows, static_cast<int>(cols), q, ldq, tail ? 1 : 0, scale, s);
   return hipGetLastError();
 }
 
+namespace {
+
 bool project_i8_few(int64_t n_tok, int64_t K) {
-  return n_tok <= kFewTokens && K >= 16 && n_tok * few_stride(static_cast<int>(K)) <= kFewLds;
+  return n_tok <= 32 && K >= 16 && n_tok * few_stride(static_cast<int>(K)) <= kFewLds;
 }
 
-bool project_i8_quantizes(int64_t n_tok, int64_t K) { return n_tok <= kFewQuantized && project_i8_few(n_tok, K); }
+}  // namespace
+
+bool project_i8_quantizes(int64_t n_tok, int64_t K) { return n_tok <= 16 && project_i8_few(n_tok, K); }
 
 namespace {
 
@@ -749,15 +761,15 @@ hipError_t launch_product(const ProjectI8Args& a, const void* e, int e_dtype, hi
   if (e_dtype == ENGRAM_BF16) return launch_few_blocks<OutT, ENGRAM_BF16>(a, e, s);
   if (e_dtype == ENGRAM_F32) return launch_few_blocks<OutT, ENGRAM_F32>(a, e, s);
   if (project_i8_few(a.n_tok, a.K)) return launch_few_blocks<OutT, ENGRAM_I8>(a, nullptr, s);
-  if (a.n_tok > 64 && a.n_out > 64) {
-    const bool direct = a.K % 16 == 0 && a.ldq % 16 == 0 &&
-                        (reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.w)) % 16 == 0;
-    return direct ? launch_tiles<OutT, true>(a, s) : launch_tiles<OutT, false>(a, s);
+  if (a.K < 16) {
+    const int64_t blocks = (a.n_tok * a.n_out + 255) / 256;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    launch_k(project_i8_short_kernel<OutT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+    return hipGetLastError();
   }
-  const int64_t tiles = ((a.n_out + 63) / 64) * ((a.n_tok + 63) / 64);
-  if (tiles > INT32_MAX) return hipErrorInvalidValue;
-  launch_k(project_i8_kernel<OutT>, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  const bool direct = a.K % 16 == 0 && a.ldq % 16 == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.w)) % 16 == 0;
+  return direct ? launch_tiles<OutT, true>(a, s) : launch_tiles<OutT, false>(a, s);
 }
 
 }  // namespace
