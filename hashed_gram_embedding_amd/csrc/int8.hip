@@ -10,6 +10,7 @@
 // them and results do not depend on it.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "device_util.h"
 #include "engram_internal.h"
@@ -277,7 +278,11 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   struct Tile {
     int64_t f0, t0;
   };
-  auto tile_of = [&](int local, Tile* t) {
+  // Round n of an XCD's share is `stride` tiles; a workgroup's place in it
+  // moves by one each round, so that no workgroup gets a band's ragged last
+  // tile (or a whole one) every time.
+  auto tile_of = [&](int round, Tile* t) {
+    const int local = round * stride + (static_cast<int>(blockIdx.x >> 3) + round) % stride;
     const int id = xcd * share + local;
     if (local >= share || id >= n_tiles) return false;
     const int band = id / (kBand * tiles_f), b0 = band * kBand, rows = min(kBand, tiles_t - b0);
@@ -365,8 +370,10 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   };
 
   Tile cur, next{0, 0};
-  int local = blockIdx.x >> 3;
-  if (!tile_of(local, &cur)) return;
+  int round = 0;
+  const int rounds = (share + stride - 1) / stride;
+  while (round < rounds && !tile_of(round, &cur)) ++round;   // a last round may leave a place empty
+  if (round >= rounds) return;
   int buf = 0, par = 0;
   scales(cur, 0);
   if constexpr (DIRECT) {
@@ -375,7 +382,13 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
     load(cur, 0);
     store(0, 0);
   }
-  for (;;) {
+  // One tile; `whole`: every block of this wavefront holds tokens.  (Two
+  // copies of the loop rather than a choice inside it, between whose sides the
+  // accumulators would have to move.)
+  bool more = false;
+  int jn = J;   // blocks of 32 tokens that this wavefront has in the tile
+  auto process = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
     i32x16_t acc[I][J];
 #pragma unroll
     for (int i = 0; i < I; ++i)
@@ -383,8 +396,6 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-    local += stride;
-    const bool more = tile_of(local, &next);
     for (int kt = 0; kt < ksteps; ++kt) {
       // this lane's part of the slice has landed and its reads of the other
       // buffer are done; after the barrier, every lane's
@@ -414,29 +425,42 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
 #pragma unroll
         for (int j = 0; j < J; ++j) fb[set][j] = __builtin_bit_cast(i32x4_t, Qs[(wt * (TT / WT) + j * 32 + lr) * 8 + kc]);
       };
-      operands(0, 0);
+      if constexpr (kWhole) {
+        operands(0, 0);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        if (ks < 3) operands((ks + 1) & 1, ks + 1);
+        for (int ks = 0; ks < 4; ++ks) {
+          if (ks < 3) operands((ks + 1) & 1, ks + 1);
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+          for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
+        }
+        if constexpr (I * J >= I + J) {
+          constexpr int kMfma = 0x8, kLdsRead = 0x100;
+          __builtin_amdgcn_sched_group_barrier(kLdsRead, I + J, 0);
+#pragma unroll
+          for (int ks = 0; ks < 3; ++ks) {
+#pragma unroll
+            for (int z = 0; z < I + J; ++z) {
+              __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+              __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+            }
+            if constexpr (I * J > I + J) __builtin_amdgcn_sched_group_barrier(kMfma, I * J - I - J, 0);
+          }
+          __builtin_amdgcn_sched_group_barrier(kMfma, I * J, 0);
+        }
+      } else {   // only the blocks that hold tokens
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          operands(0, ks);
 #pragma unroll
           for (int j = 0; j < J; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
-      }
-      if constexpr (I * J >= I + J) {
-        constexpr int kMfma = 0x8, kLdsRead = 0x100;
-        __builtin_amdgcn_sched_group_barrier(kLdsRead, I + J, 0);
+            if (j < jn)
 #pragma unroll
-        for (int ks = 0; ks < 3; ++ks) {
-#pragma unroll
-          for (int z = 0; z < I + J; ++z) {
-            __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-          }
-          if constexpr (I * J > I + J) __builtin_amdgcn_sched_group_barrier(kMfma, I * J - I - J, 0);
+              for (int i = 0; i < I; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(kMfma, I * J, 0);
       }
       if constexpr (!DIRECT) {
         if (same || more) store(same ? kt + 1 : 0, buf ^ 1);
@@ -455,6 +479,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
     const int64_t fw = cur.f0 + wf * (TF / WF);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
+      if (!kWhole && j >= jn) break;
       const float st = sq[j * 32 + lr];
 #pragma unroll
       for (int i = 0; i < I; ++i)
@@ -502,6 +527,15 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
         }
       }
     }
+  };
+  for (;;) {
+    more = false;
+    while (++round < rounds && !(more = tile_of(round, &next))) {
+    }
+    const int64_t left = a.n_tok - cur.t0 - wt * (TT / WT);
+    jn = static_cast<int>(min(max((left + 31) / 32, int64_t{0}), static_cast<int64_t>(J)));
+    if (jn == J) process(std::true_type{});
+    else process(std::false_type{});
     if (!more) break;
     cur = next;
     par ^= 1;
