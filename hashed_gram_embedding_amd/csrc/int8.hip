@@ -542,6 +542,122 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   }
 }
 
+// Small products of aligned operands, bound by latency: one tile of 64
+// outputs x 64 tokens a workgroup, four wavefronts of 32 x 32, and a ring of
+// kRing slices of 128 columns in LDS that are all in flight from the start
+// (the tiles' two buffers wait for each slice in turn: 256 x 1024 x 2048 8.5
+// us there, 5.9 here).  Only while every tile has its place on the chip at once:
+// with four tiles a CU at 1024 columns it is the slower (19.6 against 10.0 us).
+// kRingLoads memory instructions a wavefront and slice.
+constexpr int kRing = 8, kRingLoads = 4;
+
+// Waits until at most `slices` of this wavefront's younger slices are in flight.
+__device__ __forceinline__ void wait_for_slice(int slices) {
+  switch (slices) {
+    case 0: asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); break;
+    case 1: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kRingLoads) : "memory"); break;
+    case 2: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kRingLoads) : "memory"); break;
+    case 3: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * kRingLoads) : "memory"); break;
+    case 4: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * kRingLoads) : "memory"); break;
+    case 5: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * kRingLoads) : "memory"); break;
+    case 6: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(6 * kRingLoads) : "memory"); break;
+    default: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(7 * kRingLoads) : "memory"); break;
+  }
+}
+
+template <typename OutT>
+__global__ void __launch_bounds__(256)
+project_i8_ring_kernel(ProjectI8Args a, int tiles_f) {
+  extern __shared__ u32x4_t lds[];   // [kRing][64 W rows, 64 token rows][8 chunks]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 31, lh = lane >> 5, wf = wave & 1, wt = wave >> 1;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * 64, t0 = static_cast<int64_t>(blockIdx.x / tiles_f) * 64;
+  const int K = a.K, chunks = K / 16, ksteps = (chunks + 7) / 8, ldq = static_cast<int>(a.ldq);
+  const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
+  const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.w + f0 * K), 0,
+                                                    static_cast<int>(min(int64_t{64}, a.n_out - f0)) * K, 0x00020000);
+  const auto rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q + t0 * ldq), 0,
+                                                    static_cast<int>(min(int64_t{64}, a.n_tok - t0)) * ldq, 0x00020000);
+  // rows past the end and the chunks past the last one read zeros, as in the tiles
+  auto issue = [&](int kt) {
+    u32x4_t* dst = lds + (kt % kRing) * 1024 + wave * 64;
+    const bool in = kt * 8 + ch < chunks;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(dst + i * 256), 16,
+                                               (r0 + i * 32) * K + ch * 16, kt * 128, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (__attribute__((address_space(3))) void*)(dst + 512 + i * 256), 16,
+                                               in ? (r0 + i * 32) * ldq + ch * 16 : 0x7fff0000, kt * 128, 0, 0);
+  };
+  // the scales first: they have landed when the first slice has
+  float so[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) so[i] = a.w_scale[min(f0 + wf * 32 + (i >> 2) * 8 + lh * 4 + (i & 3), a.n_out - 1)];
+  const int64_t tok = t0 + wt * 32 + lr;
+  const float st = a.q_scale[min(tok, a.n_tok - 1)];
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int p = 0; p < kRing - 1; ++p)
+    if (p < ksteps) issue(p);
+  i32x16_t acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0;
+  for (int kt = 0; kt < ksteps; ++kt) {
+    wait_for_slice(min(kRing - 2, ksteps - 1 - kt));
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // everyone's part; slot kt - 1 has been read
+    if (kt + kRing - 1 < ksteps) issue(kt + kRing - 1);
+    const u32x4_t* Ws = lds + (kt % kRing) * 1024;
+    const u32x4_t* Qs = Ws + 512;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const int kc = (ks * 2 + lh) ^ ((lr >> 1) & 7);
+      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, Ws[(wf * 32 + lr) * 8 + kc]),
+                                                  __builtin_bit_cast(i32x4_t, Qs[(wt * 32 + lr) * 8 + kc]), acc, 0, 0, 0);
+    }
+  }
+  if (tok >= a.n_tok) return;
+  OutT* out = static_cast<OutT*>(a.out) + tok * a.n_out;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int64_t o = f0 + wf * 32 + g * 8 + lh * 4;
+    OutT x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = to_out<OutT>(static_cast<float>(acc[4 * g + e]) * st * so[4 * g + e]);
+    if (o + 4 <= a.n_out) {
+      __builtin_memcpy(out + o, x, sizeof(x));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (o + e < a.n_out) out[o + e] = x[e];
+    }
+  }
+}
+
+// LDS of a workgroup, and how many of them a CU holds.
+inline int ring_bytes(int K) { return std::min(kRing, (K + 127) / 128) * 1024 * 16; }
+inline int ring_places(int K) { return std::min(4, (160 << 10) / ring_bytes(K)); }
+
+template <typename OutT>
+hipError_t launch_ring(const ProjectI8Args& a, hipStream_t s) {
+  constexpr int kLds = kRing * 1024 * 16;
+  auto* const fn = project_i8_ring_kernel<OutT>;
+  static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if ((attr_set.load() & bit) == 0) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+    attr_set.fetch_or(bit);
+  }
+  const int64_t tf = (a.n_out + 63) / 64, tt = (a.n_tok + 63) / 64;
+  launch_k(fn, dim3(static_cast<unsigned>(tf * tt)), dim3(256), ring_bytes(a.K), s, a, static_cast<int>(tf));
+  return hipGetLastError();
+}
+
 // Fewer than 16 columns: one thread an output.
 template <typename OutT>
 __global__ void __launch_bounds__(256)
@@ -751,6 +867,9 @@ hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
 
 template <typename OutT, bool DIRECT>
 hipError_t launch_tiles(const ProjectI8Args& a, hipStream_t s) {
+  if constexpr (DIRECT) {
+    if (((a.n_out + 63) / 64) * ((a.n_tok + 63) / 64) <= 256 * ring_places(a.K)) return launch_ring<OutT>(a, s);
+  }
   if (((a.n_out + 255) / 256) * ((a.n_tok + 255) / 256) >= 256) return launch_tile<OutT, 256, 256, 4, 2, DIRECT>(a, s);
   return launch_tile<OutT, 128, 128, 2, 2, DIRECT>(a, s);
 }

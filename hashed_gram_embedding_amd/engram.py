@@ -765,11 +765,11 @@ def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, 
         _check_tensor("H", H, (_TORCH_DT[layer.hdtype],), H.shape, dev)
         if H.numel() != B * T * layer.M * layer.d:
             raise ValueError(f"H has {H.numel()} values, expected B*T*M*d = {B * T * layer.M * layer.d}")
-    if state is not None:
-        g, n1 = layer.li, layer.li.hash.max_n - 1
-        _check_tensor("state.ids", state.ids, _I32, (B, n1), dev)
-        _check_tensor("state.conv", state.conv, _F32, (B, layer.M, (g.kernel_w - 1) * g.dilation, layer.d), dev)
-        _check_tensor("state.pos", state.pos, _I32, (B,), dev)
+    if state is not None:   # (its three tensors were allocated together)
+        g = layer.li
+        _check_tensor("state.conv", state.conv, _F32, (B, g.branches, (g.kernel_w - 1) * g.dilation, g.d), dev)
+        if state.ids.shape[1] != g.hash.max_n - 1:
+            raise ValueError(f"the state holds {state.ids.shape[1]} ids a sequence, the layer needs {g.hash.max_n - 1}")
     return dev, B, T
 
 
