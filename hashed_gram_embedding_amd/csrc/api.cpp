@@ -579,46 +579,58 @@ engram_status run_retrieve(const int32_t* tokens, int64_t B, int64_t T, const en
                     "hash+gather launch");
 }
 
-// The 8-bit integer product; float rows are quantised into codes / scale first.
-engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, const int8_t* w, const float* w_scale,
-                             int64_t n_tok, int64_t d_mem, int64_t n_out, int out_dtype, void* out, int8_t* codes,
-                             float* scale, hipStream_t stream) {
-  int64_t ldq = d_mem;
-  const bool tailed = e_dtype != ENGRAM_I8 && !engram::project_i8_quantizes(n_tok, d_mem);
-  if (tailed) {
-    ldq = engram::i8_row_stride(d_mem);
-    prof_mark(stream, "quantize_i8_kernel");
-    const engram_status r = hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, codes, ldq, true, scale, stream),
-                                       "quantize_i8 launch");
-    if (r != ENGRAM_OK) return r;
-    e = codes;
-    e_dtype = ENGRAM_I8;
-    e_scale = scale;
-  }
-  prof_mark(stream, "project_i8_kernel");
-  return hip_status(engram::launch_project_i8(e, e_dtype, ldq, tailed, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out,
-                                              stream),
-                    "project_i8 launch");
-}
-
-// Codes and scales of quantised rows in a workspace.
+// What the 8-bit integer product keeps in a workspace: the codes and scales of
+// float rows, and aligned copies of rows whose length is no multiple of 16.
 struct CodeSpace {
-  int8_t* codes;
+  int8_t* codes;   // [n_tok] rows
   float* scale;
+  int8_t* w;       // [n_out] rows
 };
 
-CodeSpace carve_codes(Carve& c, int64_t n_tok, int64_t d_mem) {
-  CodeSpace s;
-  s.codes = c.take<int8_t>(static_cast<size_t>(n_tok) * engram::i8_row_stride(d_mem));
-  s.scale = c.take<float>(static_cast<size_t>(n_tok));
+CodeSpace carve_codes(Carve& c, int e_dtype, int64_t n_tok, int64_t d_mem, int64_t n_out) {
+  const int64_t ld = engram::i8_row_stride(d_mem);
+  const bool align = engram::project_i8_aligns(n_tok, d_mem);
+  const bool quantize = e_dtype != ENGRAM_I8 && !engram::project_i8_quantizes(n_tok, d_mem);
+  CodeSpace s{};
+  if (quantize || (e_dtype == ENGRAM_I8 && align)) s.codes = c.take<int8_t>(static_cast<size_t>(n_tok) * ld);
+  if (quantize) s.scale = c.take<float>(static_cast<size_t>(n_tok));
+  if (align) s.w = c.take<int8_t>(static_cast<size_t>(n_out) * ld);
   return s;
+}
+
+// The 8-bit integer product; cs carved for the same operands.
+engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, const int8_t* w, const float* w_scale,
+                             int64_t n_tok, int64_t d_mem, int64_t n_out, int out_dtype, void* out, const CodeSpace& cs,
+                             hipStream_t stream) {
+  engram_status r = ENGRAM_OK;
+  const bool quantize = cs.scale != nullptr;
+  if (quantize) {
+    prof_mark(stream, "quantize_i8_kernel");
+    r = hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, cs.codes, engram::i8_row_stride(d_mem), true, cs.scale, stream),
+                   "quantize_i8 launch");
+    if (r != ENGRAM_OK) return r;
+    e_dtype = ENGRAM_I8;
+    e_scale = cs.scale;
+  }
+  if (cs.w != nullptr) {
+    prof_mark(stream, "align_rows_kernel");
+    r = hip_status(engram::launch_align_i8(w, n_out, cs.w, static_cast<const int8_t*>(e), quantize ? 0 : n_tok, cs.codes, d_mem, stream),
+                   "align_rows launch");
+    if (r != ENGRAM_OK) return r;
+    w = cs.w;
+  }
+  if (cs.codes != nullptr) e = cs.codes;
+  const int64_t ldq = cs.codes != nullptr ? engram::i8_row_stride(d_mem) : d_mem;
+  prof_mark(stream, "project_i8_kernel");
+  return hip_status(engram::launch_project_i8(e, e_dtype, ldq, cs.codes != nullptr, e_scale, w, w_scale, n_tok, d_mem, n_out,
+                                              out_dtype, out, stream),
+                    "project_i8 launch");
 }
 
 // Step 5 in 8-bit integers: W and where the gathered rows' codes go.
 struct Int8Step {
   const engram_i8_weights* w;
-  int8_t* codes;
-  float* scale;
+  CodeSpace space;
 };
 
 // Steps 5-8 on gathered rows e.  i8: Step 5 as the 8-bit integer product, or
@@ -686,8 +698,8 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
   }
   // Step 5 into float32 projections, then whole-row gate statistics
   if (i8 != nullptr) {
-    r = run_project_i8(e, g.hdtype, nullptr, i8->w->w, i8->w->scale, n_tok, d_mem, n_out, ENGRAM_F32, f.kv, i8->codes,
-                       i8->scale, stream);
+    r = run_project_i8(e, g.hdtype, nullptr, i8->w->w, i8->w->scale, n_tok, d_mem, n_out, ENGRAM_F32, f.kv,
+                       i8->space, stream);
   } else {
     prof_mark(stream, "gemm_kernel");
     r = hip_status(engram::launch_project_kv(e, L->w, n_tok, d_mem, n_out, g.hdtype, ENGRAM_F32, f.kv, stream),
@@ -1260,10 +1272,10 @@ ENGRAM_API engram_status engram_quantize_i8(const void* x, engram_dtype dtype, i
   return hip_status(engram::launch_quantize_i8(x, dtype, rows, cols, q, cols, false, scale, stream), "quantize_i8 launch");
 }
 
-ENGRAM_API size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, engram_dtype e_dtype) {
-  if (n_tok < 1 || d_mem < 1 || e_dtype == ENGRAM_I8 || engram::project_i8_quantizes(n_tok, d_mem)) return 0;
+ENGRAM_API size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, int64_t n_out, engram_dtype e_dtype) {
+  if (n_tok < 1 || d_mem < 1 || d_mem > 131071 || n_out < 1) return 0;
   Carve c{nullptr};
-  carve_codes(c, n_tok, d_mem);
+  carve_codes(c, e_dtype, n_tok, d_mem, n_out);
   return c.used;
 }
 
@@ -1284,19 +1296,16 @@ ENGRAM_API engram_status engram_project_i8(const void* e, engram_dtype e_dtype, 
     return fail(ENGRAM_EINVAL, "project_i8: e, w, w_scale and out must be non-NULL");
   if ((e_dtype == ENGRAM_I8) != (e_scale != nullptr))
     return fail(ENGRAM_EINVAL, "project_i8: e_scale goes with int8 codes, and only with them");
-  if (!aligned(e, dtype_size(e_dtype)) || !aligned(out, dtype_size(out_dtype)) || !aligned(e_scale, 4) || !aligned(w_scale, 4))
-    return fail(ENGRAM_EINVAL, "project_i8: e, out and the scales must be aligned to their elements");
-  const size_t need = engram_project_i8_workspace(n_tok, d_mem, e_dtype);
+  if (!aligned(e, 16) || !aligned(w, 16)) return fail(ENGRAM_EINVAL, "project_i8: e and w must be 16-byte aligned");
+  if (!aligned(out, dtype_size(out_dtype)) || !aligned(e_scale, 4) || !aligned(w_scale, 4))
+    return fail(ENGRAM_EINVAL, "project_i8: out and the scales must be aligned to their elements");
+  const size_t need = engram_project_i8_workspace(n_tok, d_mem, n_out, e_dtype);
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
     return fail(ENGRAM_EINVAL, "project_i8: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
-  CodeSpace cs{};
-  if (need > 0) {
-    Carve c{static_cast<char*>(ws)};
-    cs = carve_codes(c, n_tok, d_mem);
-  }
+  Carve c{static_cast<char*>(ws)};
+  const CodeSpace cs = carve_codes(c, e_dtype, n_tok, d_mem, n_out);   // takes nothing where need is 0
   prof_begin();
-  const engram_status r = run_project_i8(e, e_dtype, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out, cs.codes,
-                                         cs.scale, stream);
+  const engram_status r = run_project_i8(e, e_dtype, e_scale, w, w_scale, n_tok, d_mem, n_out, out_dtype, out, cs, stream);
   prof_mark(stream, nullptr);
   return r;
 }
@@ -1324,7 +1333,8 @@ DraftWorkspace carve_draft(Carve& c, int64_t n_tok, const engram_layer* L, bool 
                                      : static_cast<size_t>(n_tok) * (1 + M));
     if (own_v) w.f.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
   }
-  if (i8) w.codes = carve_codes(c, n_tok, static_cast<int64_t>(L->tables.n_tables) * L->tables.dim);
+  const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim;
+  if (i8 && n_tok > 0) w.codes = carve_codes(c, L->gc.hdtype, n_tok, d_mem, static_cast<int64_t>(1 + M) * d);
   return w;
 }
 
@@ -1337,7 +1347,8 @@ size_t draft_ws_bytes(int64_t B, int64_t T, const engram_layer* L, bool i8, bool
 
 engram_status check_i8(const char* who, const engram_i8_weights* w) {
   if (w->w == nullptr || w->scale == nullptr) return fail(ENGRAM_EINVAL, "%s: int8 w and scale must be non-NULL", who);
-  if (!aligned(w->scale, 4)) return fail(ENGRAM_EINVAL, "%s: the int8 scales must be 4-byte aligned", who);
+  if (!aligned(w->w, 16) || !aligned(w->scale, 4))
+    return fail(ENGRAM_EINVAL, "%s: int8 w must be 16-byte and its scales 4-byte aligned", who);
   return ENGRAM_OK;
 }
 
@@ -1380,7 +1391,7 @@ engram_status forward_draft(const char* who, const int32_t* tokens, void* H, int
   // the int8 product reads the rows in hdtype, also where the layer has MXFP8 weights
   r = run_retrieve(tokens, B, T, L, ha, ta, g.hdtype, st, w.e, stream, w8 != nullptr ? static_cast<int>(g.hdtype) : -1);
   if (r != ENGRAM_OK) return r;
-  const Int8Step i8{w8, w.codes.codes, w.codes.scale};
+  const Int8Step i8{w8, w.codes};
   return run_compute(tokens, w.e, H, B, T, L, g, st, alpha_out, y_out, w.f, stream, nullptr, w8 != nullptr ? &i8 : nullptr,
                      draft == nullptr);
 }

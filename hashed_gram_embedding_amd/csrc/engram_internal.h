@@ -335,7 +335,13 @@ hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t co
 // Whether the product of float rows quantises them itself (few rows that fit
 // in LDS); otherwise launch_quantize_i8 comes first.
 bool project_i8_quantizes(int64_t n_tok, int64_t K);
-// Product with W of int8 codes [n_tok][ldq] (tailed: in the layout above; with
+// Whether W and token codes have to be brought into the layout above first
+// (launch_align_i8, rows of i8_row_stride(K) bytes): the tiles read whole
+// aligned chunks.
+bool project_i8_aligns(int64_t n_tok, int64_t K);
+hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
+                           hipStream_t s);   // q_rows = 0: W alone
+// Product with W (aligned if it has to be) of int8 codes [n_tok][ldq] (tailed: in the layout above; with
 // q_scale) or, where project_i8_quantizes, of float rows [n_tok][K].
 hipError_t launch_project_i8(const void* e, int e_dtype, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
                              const float* w_scale, int64_t n_tok, int64_t K, int64_t n_out, int out_dtype, void* out,

@@ -225,6 +225,28 @@ __device__ __forceinline__ u32x4_t load_chunk(const int8_t* row, int c, int K) {
   return c * 16 + 16 > K ? v & tail_mask(K) : v;
 }
 
+// Rows whose length is no multiple of 16 into the product's own layout: whole
+// aligned chunks, the last one right-aligned behind zeros.  One thread a
+// chunk.  (Reading such rows into the tiles through registers instead took
+// 1.2 to 2.7 times as long as the aligned tiles; the copy of W costs its bytes
+// twice, 30 against 45 us at 2000 x 4099 x 2000.)
+struct AlignJob {
+  const int8_t* x;   // [rows][K]
+  u32x4_t* y;        // [rows][chunks]
+  int64_t n;         // rows * chunks
+};
+
+__global__ void __launch_bounds__(256)
+align_rows_kernel(AlignJob a, AlignJob b, int K, int chunks) {
+  int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const bool first = id < a.n;
+  if (!first) id -= a.n;
+  const AlignJob& j = first ? a : b;
+  if (id >= j.n) return;
+  const int64_t r = id / chunks;
+  j.y[id] = load_chunk(j.x + r * K, static_cast<int>(id - r * chunks), K);
+}
+
 template <typename OutT>
 __device__ __forceinline__ OutT to_out(float f) {
   if constexpr (sizeof(OutT) == 2) return f32_to_bf16(f);
@@ -252,11 +274,11 @@ __device__ __forceinline__ OutT to_out(float f) {
 // (nontemporal): written through it they drive the operands out, 300 -> 265
 // us at 1795 x 1024 x 128000.
 //
-// DIRECT: slices go from memory straight into LDS (both operands 16-byte
-// aligned, whole chunks).  Otherwise through registers, at any alignment.
+// Slices go from memory straight into LDS, so both operands are 16-byte
+// aligned rows of whole chunks.
 constexpr int kBand = 8;
 
-template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
+template <typename OutT, int TF, int TT, int WF, int WT>
 __global__ void __launch_bounds__(64 * WF * WT) __attribute__((amdgpu_waves_per_eu(2, 2)))
 project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   constexpr int NT = 64 * WF * WT;
@@ -271,9 +293,13 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wf = wave % WF, wt = wave / WF, lr = lane & 31, lh = lane >> 5;
-  const int K = a.K, chunks = (K + 15) / 16, ksteps = (chunks + 7) / 8;
+  const int K = a.K, chunks = K / 16, ksteps = (chunks + 7) / 8;
   const int n_tiles = tiles_f * tiles_t, share = (n_tiles + 7) / 8;
   const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+
+  // whole 128-byte lines of the output leave past the L2; pieces of lines are
+  // put together there
+  const bool stream = a.n_out * static_cast<int64_t>(sizeof(OutT)) % 128 == 0 && reinterpret_cast<uintptr_t>(a.out) % 128 == 0;
 
   struct Tile {
     int64_t f0, t0;
@@ -299,9 +325,9 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
   const int ldq = static_cast<int>(a.ldq);
 
-  // Direct: rows past the operand's end and chunks past the last one are out
-  // of the buffer's range and read as zeros (a W chunk past the row's end may
-  // read the next row instead: the tokens' zeros leave it out).
+  // Rows past the operand's end and chunks past the last one are out of the
+  // buffer's range and read as zeros (a W chunk past the row's end may read
+  // the next row instead: the tokens' zeros leave it out).
   auto issue = [&](const Tile& t, int kt, int buf) {
     const int w_bytes = static_cast<int>(min(static_cast<int64_t>(TF), a.n_out - t.f0)) * K;
     const int q_bytes = static_cast<int>(min(static_cast<int64_t>(TT), a.n_tok - t.t0)) * ldq;
@@ -319,53 +345,16 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (__attribute__((address_space(3))) void*)(dst + WC + i * NT), 16,
                                                in ? qo + i * (NT / 8) * ldq : qo, kt * 128, 0, 0);
   };
-  // Through registers: load() early, store() once the buffer is free.  A last
-  // chunk that is not whole reads the row's last 16 bytes; the token operand
-  // then gets zeros for the columns counted before (codes of this library's
-  // own quantisation hold them already) and for chunks past the last.
-  u32x4_t vw[DIRECT ? 1 : NW], vq[DIRECT ? 1 : NQ];
-  auto load = [&](const Tile& t, int kt) {
-    const int c = kt * 8 + ch;
-    const int wc = min(c * 16, K - 16), qc = min(c * 16, a.tailed ? (chunks - 1) * 16 : K - 16);
-    const int w_last = static_cast<int>(min(static_cast<int64_t>(TF), a.n_out - t.f0)) - 1;
-    const int q_last = static_cast<int>(min(static_cast<int64_t>(TT), a.n_tok - t.t0)) - 1;
-    const int8_t* wb = a.w + t.f0 * K;
-    const int8_t* qb = a.q + t.t0 * ldq;
-#pragma unroll
-    for (int i = 0; i < (DIRECT ? 0 : NW); ++i)
-      __builtin_memcpy(&vw[i], wb + static_cast<uint32_t>(min(r0 + i * (NT / 8), w_last) * K + wc), 16);
-#pragma unroll
-    for (int i = 0; i < (DIRECT ? 0 : NQ); ++i)
-      __builtin_memcpy(&vq[i], qb + static_cast<uint32_t>(min(r0 + i * (NT / 8), q_last) * ldq + qc), 16);
-  };
-  auto store = [&](int kt, int buf) {
-    u32x4_t* dst = lds + buf * (WC + QC) + tid;
-    const int c = kt * 8 + ch;
-    if (c >= chunks || (c == chunks - 1 && !a.tailed)) {
-      const u32x4_t keep = c < chunks ? tail_mask(K) : u32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < (DIRECT ? 0 : NQ); ++i) vq[i] &= keep;
-    }
-#pragma unroll
-    for (int i = 0; i < (DIRECT ? 0 : NW); ++i) dst[i * NT] = vw[i];
-#pragma unroll
-    for (int i = 0; i < (DIRECT ? 0 : NQ); ++i) dst[WC + i * NT] = vq[i];
-  };
   auto scales = [&](const Tile& t, int par) {
-    if constexpr (DIRECT) {
 #pragma unroll
-      for (int b = 0; b < (TF + TT) / 64; b += WF * WT) {
-        const int seg = b + wave;   // 64 scales per wavefront instruction
-        if (seg < (TF + TT) / 64) {
-          const int r = seg * 64 + lane;
-          const float* src = seg < TF / 64 ? a.w_scale + min(t.f0 + r, a.n_out - 1) : a.q_scale + min(t.t0 + (r - TF), a.n_tok - 1);
-          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                           (__attribute__((address_space(3))) void*)(sc + par * (TF + TT) + seg * 64), 4, 0, 0);
-        }
+    for (int b = 0; b < (TF + TT) / 64; b += WF * WT) {
+      const int seg = b + wave;   // 64 scales per wavefront instruction
+      if (seg < (TF + TT) / 64) {
+        const int r = seg * 64 + lane;
+        const float* src = seg < TF / 64 ? a.w_scale + min(t.f0 + r, a.n_out - 1) : a.q_scale + min(t.t0 + (r - TF), a.n_tok - 1);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                         (__attribute__((address_space(3))) void*)(sc + par * (TF + TT) + seg * 64), 4, 0, 0);
       }
-    } else {
-      for (int r = tid; r < TF + TT; r += NT)
-        sc[par * (TF + TT) + r] = r < TF ? a.w_scale[min(t.f0 + r, a.n_out - 1)] : a.q_scale[min(t.t0 + (r - TF), a.n_tok - 1)];
     }
   };
 
@@ -376,12 +365,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   if (round >= rounds) return;
   int buf = 0, par = 0;
   scales(cur, 0);
-  if constexpr (DIRECT) {
-    issue(cur, 0, 0);
-  } else {
-    load(cur, 0);
-    store(0, 0);
-  }
+  issue(cur, 0, 0);
   // One tile; `whole`: every block of this wavefront holds tokens.  (Two
   // copies of the loop rather than a choice inside it, between whose sides the
   // accumulators would have to move.)
@@ -400,18 +384,11 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       // this lane's part of the slice has landed and its reads of the other
       // buffer are done; after the barrier, every lane's
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      const bool same = kt + 1 < ksteps;
-      if constexpr (DIRECT) {
-        if (same) {
-          issue(cur, kt + 1, buf ^ 1);
-        } else if (more) {
-          issue(next, 0, buf ^ 1);
-          scales(next, par ^ 1);
-        }
-      } else {
-        if (same || more) load(same ? cur : next, same ? kt + 1 : 0);
-        if (!same && more) scales(next, par ^ 1);
-        asm volatile("" ::: "memory");   // the loads go out here, not next to their use behind the products
+      if (kt + 1 < ksteps) {
+        issue(cur, kt + 1, buf ^ 1);
+      } else if (more) {
+        issue(next, 0, buf ^ 1);
+        scales(next, par ^ 1);
       }
       const u32x4_t* Ws = lds + buf * (WC + QC);
       const u32x4_t* Qs = Ws + WC;
@@ -462,9 +439,6 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
                 acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[0][i], fb[0][j], acc[i][j], 0, 0, 0);
         }
       }
-      if constexpr (!DIRECT) {
-        if (same || more) store(same ? kt + 1 : 0, buf ^ 1);
-      }
       buf ^= 1;
     }
     // Outputs: every wavefront turns a block of 32 tokens around in its part
@@ -510,7 +484,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
         if (tok < a.n_tok && o < a.n_out) {
           OutT* dst = static_cast<OutT*>(a.out) + tok * a.n_out + o;
           if (o + EPC <= a.n_out) {
-            if constexpr (TF * TT >= 65536)
+            if (TF * TT >= 65536 && stream)
               __builtin_nontemporal_store(v[it], reinterpret_cast<u32x4_any_t*>(dst));
             else
               __builtin_memcpy(dst, &v[it], 16);
@@ -685,7 +659,8 @@ project_i8_short_kernel(ProjectI8Args a) {
 // 1 x 1024 x 128000 takes 24.3 us (5.4 TB/s), 32 x 1024 x 128000 29.4; past 32
 // tokens the tiles are faster (64 tokens: 46 against 36 us).
 constexpr int kFewWaves = 8;
-constexpr int kFewLds = 150 << 10;
+constexpr int kFewLds = 140 << 10;
+constexpr int kFewShared = 512;   // groups up to which a workgroup shares each
 
 __host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 + 16; }
 
@@ -737,25 +712,65 @@ __device__ __forceinline__ void quantize_into(const void* e, int rows, int K, u3
   }
 }
 
-template <typename OutT, int E_DT, int NB>
-__global__ void __launch_bounds__(64 * kFewWaves) __attribute__((amdgpu_waves_per_eu(NB == 1 ? 4 : 2, NB == 1 ? 4 : 2)))
-project_i8_few_kernel(ProjectI8Args a, const void* __restrict__ e) {
+// SHIFT: rows of W that start at any byte.  A load from an address that is no
+// multiple of 4 takes the memory pipeline several times as long, so the 5
+// words around each chunk are read and shifted into place.
+// ks: wavefronts that share a group of 16 rows, taking every ks-th run of 64
+// columns: all kFewWaves where rows are longer than one wavefront's loads in
+// flight and groups too few to fill the chip (2 x 3840 x 219 17.3 -> 7.0 us, 8 x
+// 4096 x 8192 24.3 -> 19.8), else 1 (1 x 1024 x 16384 8.1 us, shared 18.5).
+template <typename OutT, int E_DT, int NB, bool SHIFT>
+__global__ void __launch_bounds__(64 * kFewWaves)
+__attribute__((amdgpu_waves_per_eu(NB == 1 && !SHIFT ? 4 : 2, NB == 1 && !SHIFT ? 4 : 2)))
+project_i8_few_kernel(ProjectI8Args a, const void* __restrict__ e, int ks) {
   extern __shared__ u32x4_t lds[];
   __shared__ float sq[16 * NB];
+  __shared__ i32x4_t part[kFewWaves][NB][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = a.K, chunks = (K + 15) / 16, steps = (chunks + 3) / 4;
   const int n_tok = static_cast<int>(a.n_tok), stride = few_stride(K) / 16;   // in chunks
   const int r = lane & 15, h = lane >> 4;
-  const int64_t groups = (a.n_out + 15) / 16, all = static_cast<int64_t>(gridDim.x) * kFewWaves;
-  int64_t g = static_cast<int64_t>(blockIdx.x) * kFewWaves + wave;
+  const int64_t groups = (a.n_out + 15) / 16, all = static_cast<int64_t>(gridDim.x) * (kFewWaves / ks);
+  int64_t g = ks == 1 ? static_cast<int64_t>(blockIdx.x) * kFewWaves + wave : blockIdx.x;
+  const int first = ks == 1 ? 0 : wave;
 
   u32x4_t w[16];
-  auto load = [&](int64_t grp, int s0) {
-    const int8_t* row = a.w + min(grp * 16 + r, a.n_out - 1) * K;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) __builtin_memcpy(&w[i], row + min(((s0 + i) * 4 + h) * 16, K - 16), 16);
+  uint32_t wx[SHIFT ? 16 : 1];   // the word behind each of them
+  const int8_t* const w_end = a.w + a.n_out * K;
+  // Bytes by which the chunk at p lies past a multiple of 4, or 0 where its
+  // five words are not all W's own (at W's ends): it is then read as it lies.
+  auto shift_of = [&](const int8_t* p) {
+    const int s4 = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+    return p - s4 < a.w || p - s4 + 20 > w_end ? 0 : s4;
   };
-  if (g < groups) load(g, 0);
+  auto chunk_of = [&](int64_t grp, int step) {
+    return a.w + min(grp * 16 + r, a.n_out - 1) * K + min((step * 4 + h) * 16, K - 16);
+  };
+  auto load = [&](int64_t grp, int s0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int8_t* p = chunk_of(grp, s0 + i * ks);
+      if constexpr (SHIFT) {
+        const int s4 = shift_of(p);
+        __builtin_memcpy(&w[i], p - s4, 16);
+        __builtin_memcpy(&wx[i], s4 != 0 ? p - s4 + 16 : p, 4);
+      } else {
+        __builtin_memcpy(&w[i], p, 16);
+      }
+    }
+  };
+  auto operand = [&](int64_t grp, int s0, int i) {
+    if constexpr (SHIFT) {
+      const uint32_t s4 = static_cast<uint32_t>(shift_of(chunk_of(grp, s0 + i * ks)));
+      return i32x4_t{static_cast<int>(__builtin_amdgcn_alignbyte(w[i][1], w[i][0], s4)),
+                     static_cast<int>(__builtin_amdgcn_alignbyte(w[i][2], w[i][1], s4)),
+                     static_cast<int>(__builtin_amdgcn_alignbyte(w[i][3], w[i][2], s4)),
+                     static_cast<int>(__builtin_amdgcn_alignbyte(wx[i], w[i][3], s4))};
+    } else {
+      return __builtin_bit_cast(i32x4_t, w[i]);
+    }
+  };
+  if (g < groups) load(g, first);
 
   // codes into LDS, in the layout of a chunked row with the tail right-aligned
   if constexpr (E_DT == ENGRAM_I8) {
@@ -782,20 +797,34 @@ project_i8_few_kernel(ProjectI8Args a, const void* __restrict__ e) {
     i32x4_t acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[b] = i32x4_t{0, 0, 0, 0};
-    for (int s0 = 0; s0 < steps; s0 += 16) {
-      if (s0 > 0) load(g, s0);
+    for (int s0 = first; s0 < steps; s0 += 16 * ks) {
+      if (s0 > first) load(g, s0);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (s0 + i < steps) {
+        if (s0 + i * ks < steps) {
+          const i32x4_t wi = operand(g, s0, i);
 #pragma unroll
           for (int b = 0; b < NB; ++b)   // tokens past the last read the first one's codes; not stored
             acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                __builtin_bit_cast(i32x4_t, w[i]),
-                __builtin_bit_cast(i32x4_t, lds[(b * 16 + r < n_tok ? b * 16 + r : 0) * stride + (s0 + i) * 4 + h]), acc[b], 0, 0, 0);
+                wi,
+                __builtin_bit_cast(i32x4_t, lds[(b * 16 + r < n_tok ? b * 16 + r : 0) * stride + (s0 + i * ks) * 4 + h]), acc[b], 0, 0, 0);
         }
       }
     }
-    if (g + all < groups) load(g + all, 0);
+    if (g + all < groups) load(g + all, first);
+    if (ks > 1) {   // the workgroup's wavefronts share the group: their sums join in the first one
+#pragma unroll
+      for (int b = 0; b < NB; ++b) part[wave][b][lane] = acc[b];
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll 1
+          for (int k = 1; k < kFewWaves; ++k) acc[b] += part[k][b][lane];
+      }
+      __syncthreads();
+      if (wave != 0) continue;
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if (b * 16 + r >= n_tok) continue;
@@ -815,9 +844,9 @@ project_i8_few_kernel(ProjectI8Args a, const void* __restrict__ e) {
   }
 }
 
-template <typename OutT, int E_DT, int NB>
+template <typename OutT, int E_DT, int NB, bool SHIFT>
 hipError_t launch_few(const ProjectI8Args& a, const void* e, hipStream_t s) {
-  auto* const fn = project_i8_few_kernel<OutT, E_DT, NB>;
+  auto* const fn = project_i8_few_kernel<OutT, E_DT, NB, SHIFT>;
   const int bytes = static_cast<int>(a.n_tok) * few_stride(a.K);
   static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
   int dev = 0;
@@ -830,23 +859,30 @@ hipError_t launch_few(const ProjectI8Args& a, const void* e, hipStream_t s) {
     attr_set.fetch_or(bit);
   }
   const int64_t groups = (a.n_out + 15) / 16;
-  const int64_t most = NB == 1 && bytes <= kFewLds / 2 ? 512 : 256;   // workgroups that are on the chip together
-  launch_k(fn, dim3(static_cast<unsigned>(std::min(most, (groups + kFewWaves - 1) / kFewWaves))), dim3(64 * kFewWaves), bytes, s, a, e);
+  const int64_t most = NB == 1 && !SHIFT && bytes <= kFewLds / 2 ? 512 : 256;   // workgroups that are on the chip together
+  const bool shared = a.K > 1024 && groups <= kFewShared;
+  const int64_t blocks = std::min(most, shared ? groups : (groups + kFewWaves - 1) / kFewWaves);
+  launch_k(fn, dim3(static_cast<unsigned>(blocks)), dim3(64 * kFewWaves), bytes, s, a, e, shared ? kFewWaves : 1);
   return hipGetLastError();
+}
+
+template <typename OutT, int E_DT, int NB>
+hipError_t launch_few_shift(const ProjectI8Args& a, const void* e, hipStream_t s) {
+  return a.K % 4 == 0 ? launch_few<OutT, E_DT, NB, false>(a, e, s) : launch_few<OutT, E_DT, NB, true>(a, e, s);
 }
 
 template <typename OutT, int E_DT>
 hipError_t launch_few_blocks(const ProjectI8Args& a, const void* e, hipStream_t s) {
   if constexpr (E_DT == ENGRAM_I8) {
-    if (a.n_tok > 16) return launch_few<OutT, E_DT, 2>(a, e, s);
+    if (a.n_tok > 16) return launch_few_shift<OutT, E_DT, 2>(a, e, s);
   }
-  return launch_few<OutT, E_DT, 1>(a, e, s);
+  return launch_few_shift<OutT, E_DT, 1>(a, e, s);
 }
 
-template <typename OutT, int TF, int TT, int WF, int WT, bool DIRECT>
+template <typename OutT, int TF, int TT, int WF, int WT>
 hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
   constexpr int kLds = 2 * (TF + TT) * 128 + 2 * (TF + TT) * 4;
-  auto* const fn = project_i8_tile_kernel<OutT, TF, TT, WF, WT, DIRECT>;
+  auto* const fn = project_i8_tile_kernel<OutT, TF, TT, WF, WT>;
   static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -865,13 +901,11 @@ hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename OutT, bool DIRECT>
+template <typename OutT>
 hipError_t launch_tiles(const ProjectI8Args& a, hipStream_t s) {
-  if constexpr (DIRECT) {
-    if (((a.n_out + 63) / 64) * ((a.n_tok + 63) / 64) <= 256 * ring_places(a.K)) return launch_ring<OutT>(a, s);
-  }
-  if (((a.n_out + 255) / 256) * ((a.n_tok + 255) / 256) >= 256) return launch_tile<OutT, 256, 256, 4, 2, DIRECT>(a, s);
-  return launch_tile<OutT, 128, 128, 2, 2, DIRECT>(a, s);
+  if (((a.n_out + 63) / 64) * ((a.n_tok + 63) / 64) <= 256 * ring_places(a.K)) return launch_ring<OutT>(a, s);
+  if (((a.n_out + 255) / 256) * ((a.n_tok + 255) / 256) >= 256) return launch_tile<OutT, 256, 256, 4, 2>(a, s);
+  return launch_tile<OutT, 128, 128, 2, 2>(a, s);
 }
 
 }  // namespace
@@ -907,10 +941,22 @@ bool project_i8_few(int64_t n_tok, int64_t K) {
 
 bool project_i8_quantizes(int64_t n_tok, int64_t K) { return n_tok <= 16 && project_i8_few(n_tok, K); }
 
+bool project_i8_aligns(int64_t n_tok, int64_t K) { return K >= 16 && K % 16 != 0 && !project_i8_few(n_tok, K); }
+
+hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
+                           hipStream_t s) {
+  const int64_t chunks = (K + 15) / 16, blocks = ((w_rows + q_rows) * chunks + 255) / 256;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  launch_k(align_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+           AlignJob{w, reinterpret_cast<u32x4_t*>(w_out), w_rows * chunks}, AlignJob{q, reinterpret_cast<u32x4_t*>(q_out), q_rows * chunks},
+           static_cast<int>(K), static_cast<int>(chunks));
+  return hipGetLastError();
+}
+
 namespace {
 
 template <typename OutT>
-hipError_t launch_product(const ProjectI8Args& a, const void* e, int e_dtype, hipStream_t s) {
+hipError_t launch_product(ProjectI8Args a, const void* e, int e_dtype, hipStream_t s) {
   if (e_dtype == ENGRAM_BF16) return launch_few_blocks<OutT, ENGRAM_BF16>(a, e, s);
   if (e_dtype == ENGRAM_F32) return launch_few_blocks<OutT, ENGRAM_F32>(a, e, s);
   if (project_i8_few(a.n_tok, a.K)) return launch_few_blocks<OutT, ENGRAM_I8>(a, nullptr, s);
@@ -920,9 +966,9 @@ hipError_t launch_product(const ProjectI8Args& a, const void* e, int e_dtype, hi
     launch_k(project_i8_short_kernel<OutT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  const bool direct = a.K % 16 == 0 && a.ldq % 16 == 0 &&
-                      (reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.w)) % 16 == 0;
-  return direct ? launch_tiles<OutT, true>(a, s) : launch_tiles<OutT, false>(a, s);
+  // whole chunks from here on: the rows are the product's own layout
+  a.K = static_cast<int>(i8_row_stride(a.K));
+  return launch_tiles<OutT>(a, s);
 }
 
 }  // namespace

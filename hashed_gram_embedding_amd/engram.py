@@ -152,7 +152,7 @@ def load_library(path: str) -> ctypes.CDLL:
         "engram_debug_read_errors": (i32, [ctypes.POINTER(ctypes.c_uint32)]),
         "engram_host_free": (i32, [vp]),
         "engram_quantize_i8": (i32, [vp, i32, i64, i64, vp, vp, vp]),
-        "engram_project_i8_workspace": (sz, [i64, i64, i32]),
+        "engram_project_i8_workspace": (sz, [i64, i64, i64, i32]),
         "engram_project_i8": (i32, [vp, i32, vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]),
         "engram_forward_i8_workspace": (sz, [i64, i64, ctypes.POINTER(LayerStruct)]),
         "engram_forward_i8": (i32, [vp, vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct),
@@ -716,7 +716,7 @@ def project_i8(e: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, e_scale:
     else:
         _check_tensor("out", out, (_TORCH_DT[odt],), (*lead, n_out), dev)
     own = None
-    nbytes = lib().engram_project_i8_workspace(n_tok, d_mem, dt)
+    nbytes = lib().engram_project_i8_workspace(n_tok, d_mem, n_out, dt)
     if ws is None and nbytes:
         ws = own = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _launch(lib().engram_project_i8, dev, stream, e.data_ptr(), dt, None if e_scale is None else e_scale.data_ptr(),

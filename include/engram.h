@@ -486,19 +486,19 @@ engram_status engram_quantize_i8(const void* x, engram_dtype dtype, int64_t rows
  * of W in 8-bit integers with one scale per token and one per output channel.
  * The sum is exact (int32); the two multiplications are in float32, and BF16
  * output rounds once more.
- *   e        device [n_tok][d_mem]: int8 codes with e_scale [n_tok] (e_dtype
- *            I8), or F32 or BF16 rows, quantised on the way as
- *            engram_quantize_i8 does (e_scale NULL)
- *   w        device int8 [n_out][d_mem], w_scale device [n_out] (the rows of W
- *            from engram_quantize_i8, or a checkpoint's)
+ *   e        device [n_tok][d_mem], 16-byte aligned: int8 codes with e_scale
+ *            [n_tok] (e_dtype I8), or F32 or BF16 rows, quantised on the way
+ *            as engram_quantize_i8 does (e_scale NULL)
+ *   w        device int8 [n_out][d_mem], 16-byte aligned, w_scale device
+ *            [n_out] (the rows of W from engram_quantize_i8, or a checkpoint's)
  *   out      device [n_tok][n_out], F32 or BF16, aligned to its elements
  *   ws       engram_project_i8_workspace() bytes, 256-byte aligned (NULL where
  *            that is 0)
  * 1 <= d_mem <= 131071 (so that the sum cannot leave int32), n_out < 2^31,
- * n_tok < 2^31 (EUNSUPPORTED otherwise).  Any d_mem, n_out and n_tok; 16-byte
- * aligned e and w with d_mem a multiple of 16 run fastest.  n_tok = 0 is a
- * no-op. */
-size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, engram_dtype e_dtype);
+ * n_tok < 2^31 (EUNSUPPORTED otherwise).  A d_mem that is no multiple of 16
+ * costs, past a few tokens, a copy of W into the workspace in each call.
+ * n_tok = 0 is a no-op. */
+size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, int64_t n_out, engram_dtype e_dtype);
 engram_status engram_project_i8(const void* e, engram_dtype e_dtype, const float* e_scale, const int8_t* w,
                                 const float* w_scale, int64_t n_tok, int64_t d_mem, int64_t n_out,
                                 engram_dtype out_dtype, void* out, void* ws, size_t ws_bytes, hipStream_t stream);

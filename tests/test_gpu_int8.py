@@ -116,24 +116,33 @@ def test_product_full_sums(n):
     assert (out.double() == float(np.float32(131071 * 16384))).all()
 
 
-@pytest.mark.parametrize("k", [64, 1024, 1000])
-def test_product_of_unaligned_views(k):
-    """Operands that start at any byte: views into larger buffers."""
-    log(f"project_i8 unaligned views k={k}")
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [17, 64, 1024, 1000, 1001, 1002])
+def test_product_into_a_view(k, out_dtype):
+    """Outputs that start at any element, operands that end with their
+    allocations' last byte: nothing beside the output is written."""
+    log(f"project_i8 views k={k} {out_dtype}")
     rng = np.random.default_rng(5)
-    for n, o, off in ((1, 70, 1), (40, 70, 3), (300, 130, 8)):
+    for n, o in ((1, 70), (20, 37), (40, 71), (300, 130), (4200, 4100)):
         q = rng.integers(-128, 128, (n, k), dtype=np.int8)
         w = rng.integers(-128, 128, (o, k), dtype=np.int8)
-        bq = torch.zeros(n * k + 16, dtype=torch.int8, device=DEV)
-        bw = torch.zeros(o * k + 16, dtype=torch.int8, device=DEV)
-        e, wt = bq[off:off + n * k].view(n, k), bw[off:off + o * k].view(o, k)
-        e.copy_(torch.from_numpy(q))
-        wt.copy_(torch.from_numpy(w))
-        buf = torch.full((n * o + 2,), 7.0, device=DEV)
+        buf = torch.full((n * o + 2,), 7.0, device=DEV, dtype=TYPES[out_dtype])
         out = buf[1:1 + n * o].view(n, o)
-        eg.project_i8(e, wt, torch.ones(o, device=DEV), e_scale=torch.ones(n, device=DEV), out_dtype="f32", out=out)
-        assert np.array_equal(to_f64(out), (q.astype(np.int64) @ w.astype(np.int64).T).astype(np.float32))
-        assert buf[0] == 7.0 and buf[-1] == 7.0      # nothing outside the output
+        eg.project_i8(torch.from_numpy(q).to(DEV), torch.from_numpy(w).to(DEV), torch.ones(o, device=DEV),
+                      e_scale=torch.ones(n, device=DEV), out_dtype=out_dtype, out=out)
+        ref = torch.from_numpy(q.astype(np.float32)).to(DEV).double() @ torch.from_numpy(w.astype(np.float32)).to(DEV).double().t()
+        assert torch.equal(out, ref.float().to(TYPES[out_dtype])), (n, o)
+        assert buf[0] == 7.0 and buf[-1] == 7.0
+
+
+def test_unaligned_operands_are_refused():
+    log("project_i8 unaligned operands")
+    b = torch.zeros(40 * 64 + 16, dtype=torch.int8, device=DEV)
+    one = torch.ones(40, device=DEV)
+    good, bad = b[:40 * 64].view(40, 64), b[8:8 + 40 * 64].view(40, 64)
+    for e, w in ((bad, good), (good, bad)):
+        with pytest.raises(eg.EngramError, match="16-byte"):
+            eg.project_i8(e, w, one, e_scale=one)
 
 
 @pytest.mark.parametrize("n", [1, 2, 40, 300])
@@ -208,7 +217,7 @@ def test_product_in_a_graph_and_on_another_stream():
         w = torch.randint(-127, 128, (515, 1000), dtype=torch.int8, device=DEV)
         s = torch.rand(515, device=DEV)
         out = torch.empty((n, 515), device=DEV)
-        ws = torch.empty(max(eg.lib().engram_project_i8_workspace(n, 1000, eg.BF16), 256), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(max(eg.lib().engram_project_i8_workspace(n, 1000, 515, eg.BF16), 256), dtype=torch.uint8, device=DEV)
         call = lambda: eg.project_i8(x, w, s, out_dtype="f32", out=out, ws=ws)   # noqa: E731
         call()
         g = torch.cuda.CUDAGraph()

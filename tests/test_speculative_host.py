@@ -71,8 +71,11 @@ def test_project_i8_refusals():
     call(eg.EINVAL, "aligned", e_scale=ODD)
     call(eg.EINVAL, "aligned", out=ODD)
     call(eg.EINVAL, "aligned", w_scale=ODD)
-    need = eg.lib().engram_project_i8_workspace(400, 64, eg.BF16)
-    assert need >= 400 * 64 + 1600 and eg.lib().engram_project_i8_workspace(400, 64, eg.I8) == 0
+    call(eg.EINVAL, "16-byte", e=ctypes.c_void_p(0x10008))
+    call(eg.EINVAL, "16-byte", w=ctypes.c_void_p(0x10008))
+    need = eg.lib().engram_project_i8_workspace(400, 64, 8, eg.BF16)
+    assert need >= 400 * 64 + 1600 and eg.lib().engram_project_i8_workspace(400, 64, 8, eg.I8) == 0
+    assert eg.lib().engram_project_i8_workspace(400, 70, 8, eg.I8) >= 400 * 80 + 8 * 80
     call(eg.EINVAL, "workspace", n=400, e_dtype=eg.BF16, e_scale=None)
     call(eg.EINVAL, "workspace", n=400, e_dtype=eg.BF16, e_scale=None, ws=P, wsb=need - 1)
     call(eg.EINVAL, "workspace", n=400, e_dtype=eg.BF16, e_scale=None, ws=ctypes.c_void_p(0x10010), wsb=need)
