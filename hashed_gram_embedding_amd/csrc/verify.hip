@@ -733,8 +733,11 @@ verify_parts_kernel(VerifyArgs a) {
   if ((threadIdx.x & 63) == 0) a.part[s * kParts + part] = x;
 }
 
-// Few sequences with long rows: the sums are split over 16 workgroups a row.
-bool verify_splits(int64_t S, int64_t V) { return S <= 96 && V > 40960; }
+// Long rows: the sums are split over 16 workgroups a row, in a launch of their
+// own.  One launch / two, in us: 1 x 32000 7.7 / 8.5, 1 x 65536 10.4 / 8.0, 1 x 128000
+// 15.0 / 8.6, 64 x 65536 10.9 / 10.4, 128 x 65536 15.9 / 16.7, 128 x 128000 28.0 /
+// 23.7, 256 x 128000 43.5 / 38.5.
+bool verify_splits(int64_t S, int64_t V) { return V > (S <= 64 ? 49152 : 81920); }
 
 template <int DT>
 hipError_t launch_verify_dt(const VerifyArgs& a, int64_t S, hipStream_t s) {
