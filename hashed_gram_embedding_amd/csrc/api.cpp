@@ -598,6 +598,13 @@ CodeSpace carve_codes(Carve& c, int e_dtype, int64_t n_tok, int64_t d_mem, int64
   return s;
 }
 
+// Codes of the rows e, in the aligned layout, into cs.
+engram_status run_quantize(const void* e, int e_dtype, int64_t n_tok, int64_t d_mem, const CodeSpace& cs, hipStream_t stream) {
+  prof_mark(stream, "quantize_i8_kernel");
+  return hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, cs.codes, engram::i8_row_stride(d_mem), true, cs.scale, stream),
+                    "quantize_i8 launch");
+}
+
 // The 8-bit integer product; cs carved for the same operands.
 engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, const int8_t* w, const float* w_scale,
                              int64_t n_tok, int64_t d_mem, int64_t n_out, int out_dtype, void* out, const CodeSpace& cs,
@@ -605,9 +612,7 @@ engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, c
   engram_status r = ENGRAM_OK;
   const bool quantize = cs.scale != nullptr;
   if (quantize) {
-    prof_mark(stream, "quantize_i8_kernel");
-    r = hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, cs.codes, engram::i8_row_stride(d_mem), true, cs.scale, stream),
-                   "quantize_i8 launch");
+    r = run_quantize(e, e_dtype, n_tok, d_mem, cs, stream);
     if (r != ENGRAM_OK) return r;
     e_dtype = ENGRAM_I8;
     e_scale = cs.scale;
@@ -644,6 +649,20 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
   const int M = g.branches, d = g.d;
   const int64_t n_out = static_cast<int64_t>(1 + M) * d;
   engram_status r;
+  // Decode step (T = 1, the strip conv): the state's ids and pos advance in the
+  // projection's launch and the conv writes the new ring row, so no commit
+  // kernel
+  auto folds = [&](int qv, int qk, bool mixed) {
+    if (!commit || st == nullptr || T != 1 || tokens == nullptr || st->ids == nullptr) return false;
+    engram::ConvArgs probe{};
+    probe.g = g;
+    probe.qv = qv;
+    probe.qk = qk;
+    probe.mixed = mixed;
+    probe.B = B;
+    probe.T = T;
+    return engram::conv_strip_ts(probe) == 1;
+  };
   if (i8 == nullptr && use_fused(L)) {
     // Step 5 with the gate's sums folded into the product's epilogue; only v is stored
     engram::ProjGateArgs pa{};
@@ -665,19 +684,7 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
     pa.M = M;
     const engram::ProjGateLayout pl =
         engram::proj_gate_layout(n_tok, static_cast<int>(n_out), d, static_cast<int>(d_mem), M, mx);
-    // Decode step (T = 1, the strip conv): the state's ids and pos advance in
-    // this launch and the conv writes the new ring row, so no commit kernel
-    bool fold = false;
-    if (commit && st != nullptr && T == 1 && tokens != nullptr && st->ids != nullptr) {
-      engram::ConvArgs probe{};
-      probe.g = g;
-      probe.qv = pl.qv;
-      probe.qk = pl.qk;
-      probe.mixed = pl.mixed;
-      probe.B = B;
-      probe.T = T;
-      fold = engram::conv_strip_ts(probe) == 1;
-    }
+    const bool fold = folds(pl.qv, pl.qk, pl.mixed);
     if (fold) {
       pa.st_ids = st->ids;
       pa.st_pos = st->pos;
@@ -695,6 +702,23 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
     return run_conv_commit(H, f.kv, d, ENGRAM_F32, f.stats, pl.qv, pl.qk, pl.mixed, B, T, g, st, tokens, L->hash.proj,
                            L->hash.max_n, static_cast<int32_t>(L->hash.vocab), alpha_out, f.gamma, y_out, stream, next, fold,
                            commit);
+  }
+  if (i8 != nullptr && use_fused(L)) {
+    r = run_quantize(e, g.hdtype, n_tok, d_mem, i8->space, stream);
+    if (r != ENGRAM_OK) return r;
+    const int q = d / engram::project_i8_gate_columns(n_tok, d_mem, d, M);
+    const bool fold = engram::project_i8_gate_advances(n_tok, d_mem, d, M) && folds(q, q, false);
+    engram::StateAdvance adv{};
+    if (fold)
+      adv = engram::StateAdvance{st->ids, st->pos, tokens, L->hash.proj, static_cast<int32_t>(L->hash.vocab), g_err_word.load(),
+                                 L->hash.max_n, static_cast<int32_t>(T), static_cast<int32_t>(B)};
+    prof_mark(stream, "project_i8_gate_kernel");
+    r = hip_status(engram::launch_project_i8_gate(i8->space.codes, i8->space.scale, i8->w->w, i8->w->scale, n_tok, d_mem, d, M, H, f.kv,
+                                                  f.stats, adv, stream),
+                   "int8 projection launch");
+    if (r != ENGRAM_OK) return r;
+    return run_conv_commit(H, f.kv, d, ENGRAM_F32, f.stats, q, q, false, B, T, g, st, tokens, L->hash.proj, L->hash.max_n,
+                           static_cast<int32_t>(L->hash.vocab), alpha_out, f.gamma, y_out, stream, next, fold, commit);
   }
   // Step 5 into float32 projections, then whole-row gate statistics
   if (i8 != nullptr) {
@@ -1322,24 +1346,31 @@ struct DraftWorkspace {
 
 DraftWorkspace carve_draft(Carve& c, int64_t n_tok, const engram_layer* L, bool i8, bool own_v) {
   const int M = L->gc.branches, d = L->gc.d;
+  const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim;
+  const bool fused = use_fused(L);
   DraftWorkspace w{};
   w.e = c.take<char>(rows_bytes(n_tok, L));
   if (own_v && !i8) {
     w.f = carve_compute(c, n_tok, L);
   } else {
-    const bool fused = !i8 && use_fused(L);
-    if (own_v) w.f.kv = c.take<float>(static_cast<size_t>(n_tok) * (1 + M) * d);
-    w.f.stats = c.take<float4>(fused ? static_cast<size_t>(n_tok) * (1 + M) * d / engram::kProjGateTileF
-                                     : static_cast<size_t>(n_tok) * (1 + M));
+    const int64_t columns = !fused ? d : i8 ? engram::project_i8_gate_columns(n_tok, d_mem, d, M) : engram::kProjGateTileF;
+    if (own_v) w.f.kv = c.take<float>(static_cast<size_t>(n_tok) * (fused ? 1 : 1 + M) * d);
+    w.f.stats = c.take<float4>(static_cast<size_t>(n_tok) * (1 + M) * (d / columns));
     if (own_v) w.f.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
   }
-  const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim;
-  if (i8 && n_tok > 0) w.codes = carve_codes(c, L->gc.hdtype, n_tok, d_mem, static_cast<int64_t>(1 + M) * d);
+  if (i8 && n_tok > 0) {
+    if (fused) {   // rows of codes, aligned as they are, at every size
+      w.codes.codes = c.take<int8_t>(static_cast<size_t>(n_tok) * d_mem);
+      w.codes.scale = c.take<float>(static_cast<size_t>(n_tok));
+    } else {
+      w.codes = carve_codes(c, L->gc.hdtype, n_tok, d_mem, static_cast<int64_t>(1 + M) * d);
+    }
+  }
   return w;
 }
 
 size_t draft_ws_bytes(int64_t B, int64_t T, const engram_layer* L, bool i8, bool own_v) {
-  if (L == nullptr || B < 0 || T < 0 || L->gc.branches < 1 || L->tables.n_tables < 1) return 0;
+  if (L == nullptr || B < 0 || T < 0 || L->gc.branches < 1 || L->gc.d < 1 || L->tables.n_tables < 1 || L->tables.dim < 1) return 0;
   Carve c{nullptr};
   carve_draft(c, B * T, L, i8, own_v);
   return c.used;
@@ -1411,7 +1442,7 @@ ENGRAM_API engram_status engram_forward_i8(const int32_t* tokens, void* H, int64
 
 ENGRAM_API int64_t engram_draft_stride(const engram_layer* L, const engram_i8_weights* w) {
   if (L == nullptr || L->gc.branches < 1) return 0;
-  return w == nullptr && use_fused(L) ? L->gc.d : static_cast<int64_t>(1 + L->gc.branches) * L->gc.d;
+  return use_fused(L) ? L->gc.d : static_cast<int64_t>(1 + L->gc.branches) * L->gc.d;
 }
 
 ENGRAM_API size_t engram_forward_draft_workspace(int64_t B, int64_t T, const engram_layer* L, const engram_i8_weights* w) {

@@ -346,6 +346,28 @@ hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const
 hipError_t launch_project_i8(const void* e, int e_dtype, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,
                              const float* w_scale, int64_t n_tok, int64_t K, int64_t n_out, int out_dtype, void* out,
                              hipStream_t s);
+// A decode state's advance in the launch of the int8 projection (adv_B > 0),
+// the fields and meaning as in ProjGateArgs.
+struct StateAdvance {
+  int32_t* st_ids;
+  int32_t* st_pos;
+  const int32_t* tokens;
+  const int32_t* proj;
+  int32_t vocab;
+  uint32_t* err;
+  int32_t max_n;
+  int32_t adv_T;
+  int32_t adv_B;
+};
+// Step 5 of a layer in 8-bit integers with Step 6's sums (codes q [n_tok][K],
+// K a multiple of 16, bf16 H, d a multiple of 128 up to 4096): v [n_tok][d]
+// and stats [n_tok][(1+M) d / columns], columns = project_i8_gate_columns():
+// v's runs of that many columns, then each branch's.  The launch takes a
+// decode state's advance along where project_i8_gate_advances() (few tokens).
+bool project_i8_gate_advances(int64_t n_tok, int64_t K, int d, int M);
+int project_i8_gate_columns(int64_t n_tok, int64_t K, int d, int M);
+hipError_t launch_project_i8_gate(const int8_t* q, const float* q_scale, const int8_t* w, const float* w_scale, int64_t n_tok, int64_t K,
+                                  int d, int M, const void* H, float* v, float4* stats, const StateAdvance& adv, hipStream_t s);
 hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
                               int64_t per, float* probs, void* ws, hipStream_t s);
 size_t probs_workspace(int64_t rows, int64_t V);

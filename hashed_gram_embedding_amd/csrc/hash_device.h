@@ -194,9 +194,10 @@ __device__ __forceinline__ int32_t hash_index(const int32_t* __restrict__ tokens
   return hash_of_ids(x, th);
 }
 
-// Decode-state advance (ProjGateArgs.adv_B > 0), by the threads of
-// workgroup 0: ids <- last N-1 of (ids ++ P(tokens)), pos += T.
-__device__ __forceinline__ void advance_state(const ProjGateArgs& a, uint32_t bid) {
+// Decode-state advance (ProjGateArgs.adv_B or StateAdvance.adv_B > 0), by the
+// threads of workgroup 0: ids <- last N-1 of (ids ++ P(tokens)), pos += T.
+template <typename Args>
+__device__ __forceinline__ void advance_state(const Args& a, uint32_t bid) {
   if (a.adv_B <= 0 || bid != 0) return;
   const int hl = a.max_n - 1;
   for (int b = threadIdx.x; b < a.adv_B; b += blockDim.x) {

@@ -14,6 +14,7 @@
 
 #include "device_util.h"
 #include "engram_internal.h"
+#include "hash_device.h"
 
 namespace engram {
 namespace {
@@ -202,6 +203,14 @@ struct ProjectI8Args {
   int64_t n_out;
   int K;
   int tailed;            // q's last run of 16 columns is right-aligned and zero-filled
+  // Step 5 of a layer with Step 6's sums instead of outputs (GATE forms): out
+  // is v [n_tok][d] float32, n_out = (1 + M) d
+  const uint16_t* H;     // [n_tok][M][d] bf16 (read only)
+  float4* stats;         // [n_tok][nq]
+  int d;
+  int M;
+  int nq;
+  StateAdvance adv;      // ring form only
 };
 
 // Which bytes of a row's last 16 belong to its last chunk: all of them, or
@@ -253,6 +262,33 @@ __device__ __forceinline__ OutT to_out(float f) {
   else return f;
 }
 
+// Sum over the 16 lanes of a DPP row, in all of them (rotations by 8, 4, 2, 1).
+__device__ __forceinline__ float row_sum(float x) {
+  auto turned = [](float v, auto by) {
+    constexpr int kRowRor = 0x120;
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), kRowRor + decltype(by)::value, 0xf, 0xf, false));
+  };
+  x += turned(x, std::integral_constant<int, 8>{});
+  x += turned(x, std::integral_constant<int, 4>{});
+  x += turned(x, std::integral_constant<int, 2>{});
+  x += turned(x, std::integral_constant<int, 1>{});
+  return x;
+}
+
+// What four columns of a projection row add to a token's gate sums (h.h, k.k,
+// h.k, v.v): value columns their squares, key columns those of h and k.
+__device__ __forceinline__ float4 gate_terms(const f32x4_t& x, bool is_v, uint2 h) {
+  const float xx = x[0] * x[0] + x[1] * x[1] + x[2] * x[2] + x[3] * x[3];
+  if (is_v) return make_float4(0.f, 0.f, 0.f, xx);
+  const float h0 = __uint_as_float(h.x << 16), h1 = __uint_as_float(h.x & 0xffff0000u);
+  const float h2 = __uint_as_float(h.y << 16), h3 = __uint_as_float(h.y & 0xffff0000u);
+  return make_float4(h0 * h0 + h1 * h1 + h2 * h2 + h3 * h3, xx, h0 * x[0] + h1 * x[1] + h2 * x[2] + h3 * x[3], 0.f);
+}
+
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // Tiled product for the sizes that fill the chip.  A workgroup of WF x WT
 // wavefronts forms TF outputs x TT tokens; W rows are the A operand of
 // v_mfma_i32_32x32x32_i8 and token rows the B operand, so a lane ends with
@@ -276,9 +312,16 @@ __device__ __forceinline__ OutT to_out(float f) {
 //
 // Slices go from memory straight into LDS, so both operands are 16-byte
 // aligned rows of whole chunks.
+//
+// GATE: Step 5 of a layer.  Value columns are stored, and instead of the keys
+// the sums that Step 6 takes of them and of h leave the kernel, one float4 per
+// token and run of 64 x (2 or 4) columns, so that the keys' float32 rows are
+// neither written nor read again (4096 tokens, one branch: 25.3 us for the
+// product and the sums apart, 18.1 together; 8192 tokens, 4 branches, with the
+// conv 148 against 116).
 constexpr int kBand = 8;
 
-template <typename OutT, int TF, int TT, int WF, int WT>
+template <typename OutT, int TF, int TT, int WF, int WT, bool GATE>
 __global__ void __launch_bounds__(64 * WF * WT) __attribute__((amdgpu_waves_per_eu(2, 2)))
 project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   constexpr int NT = 64 * WF * WT;
@@ -290,6 +333,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
   static_assert((TF + TT) % NT == 0 || NT % (TF + TT) == 0, "scales per thread");
   extern __shared__ u32x4_t lds[];
   float* const sc = reinterpret_cast<float*>(lds + 2 * (WC + QC));   // [2][TF + TT] scales: outputs, then tokens
+  float4* const red = reinterpret_cast<float4*>(sc + 2 * (TF + TT));  // GATE: [WF][TT] sums of the wavefronts' columns
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wf = wave % WF, wt = wave / WF, lr = lane & 31, lh = lane >> 5;
@@ -451,9 +495,23 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
     const float* sq = sc + par * (TF + TT) + TF + wt * (TT / WT);
     constexpr int EPC = 16 / static_cast<int>(sizeof(OutT));   // outputs of a chunk
     const int64_t fw = cur.f0 + wf * (TF / WF);
+    // GATE: this wavefront's columns are v's, or one branch's keys
+    const bool is_v = GATE && fw < a.d;
+    const int branch = GATE && !is_v ? static_cast<int>(fw / a.d) - 1 : 0;
+    const int64_t col = GATE ? fw - static_cast<int64_t>(is_v ? 0 : 1 + branch) * a.d : 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       if (!kWhole && j >= jn) break;
+      uint2 h[GATE ? 32 * RC / 64 : 1];
+      if constexpr (GATE) {
+#pragma unroll
+        for (int it = 0; it < 32 * RC / 64; ++it) {
+          h[it] = make_uint2(0u, 0u);
+          const int rr = (it * 64 + lane) / RC, c = (it * 64 + lane) % RC;
+          const int64_t tok = min(cur.t0 + wt * (TT / WT) + j * 32 + rr, a.n_tok - 1);
+          if (!is_v && fw < a.n_out) h[it] = *reinterpret_cast<const uint2*>(a.H + (tok * a.M + branch) * a.d + col + c * 4);
+        }
+      }
       const float st = sq[j * 32 + lr];
 #pragma unroll
       for (int i = 0; i < I; ++i)
@@ -481,7 +539,13 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       for (int it = 0; it < NIT; ++it) {
         const int rr = (it * 64 + lane) / RC, c = (it * 64 + lane) % RC;
         const int64_t tok = cur.t0 + wt * (TT / WT) + j * 32 + rr, o = fw + c * EPC;
-        if (tok < a.n_tok && o < a.n_out) {
+        if constexpr (GATE) {
+          const f32x4_t x = __builtin_bit_cast(f32x4_t, v[it]);
+          if (is_v && tok < a.n_tok) __builtin_memcpy(static_cast<float*>(a.out) + tok * a.d + o, &x, 16);
+          float4 p = gate_terms(x, is_v, h[it]);
+          p = make_float4(row_sum(p.x), row_sum(p.y), row_sum(p.z), row_sum(p.w));
+          if (c == 0) red[wf * TT + wt * (TT / WT) + j * 32 + rr] = p;
+        } else if (tok < a.n_tok && o < a.n_out) {
           OutT* dst = static_cast<OutT*>(a.out) + tok * a.n_out + o;
           if (o + EPC <= a.n_out) {
             if (TF * TT >= 65536 && stream)
@@ -498,6 +562,18 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
               if (e < left) dst[e] = x;
             }
           }
+        }
+      }
+    }
+    if constexpr (GATE) {
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const int join = static_cast<int>(a.n_out / (TF / WF)) / a.nq;   // wavefronts' sums in one: 2 or 4
+      for (int i = tid; i < TT * WF / join; i += NT) {
+        const int t = i % TT, g = i / TT * join;
+        if (cur.t0 + t < a.n_tok && cur.f0 + g * (TF / WF) < a.n_out) {
+          float4 p = add4(red[g * TT + t], red[(g + 1) * TT + t]);
+          if (join == 4) p = add4(p, add4(red[(g + 2) * TT + t], red[(g + 3) * TT + t]));
+          a.stats[(cur.t0 + t) * a.nq + (cur.f0 / (TF / WF) + g) / join] = p;
         }
       }
     }
@@ -539,12 +615,14 @@ __device__ __forceinline__ void wait_for_slice(int slices) {
   }
 }
 
-template <typename OutT>
+template <typename OutT, bool GATE>
 __global__ void __launch_bounds__(256)
 project_i8_ring_kernel(ProjectI8Args a, int tiles_f) {
   extern __shared__ u32x4_t lds[];   // [kRing][64 W rows, 64 token rows][8 chunks]
+  __shared__ float4 red[GATE ? 64 : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 31, lh = lane >> 5, wf = wave & 1, wt = wave >> 1;
+  if constexpr (GATE) advance_state(a.adv, blockIdx.x);
   const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * 64, t0 = static_cast<int64_t>(blockIdx.x / tiles_f) * 64;
   const int K = a.K, chunks = K / 16, ksteps = (chunks + 7) / 8, ldq = static_cast<int>(a.ldq);
   const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
@@ -591,6 +669,29 @@ project_i8_ring_kernel(ProjectI8Args a, int tiles_f) {
                                                   __builtin_bit_cast(i32x4_t, Qs[(wt * 32 + lr) * 8 + kc]), acc, 0, 0, 0);
     }
   }
+  if constexpr (GATE) {
+    // the tile's 64 columns are v's, or one branch's keys
+    const bool is_v = f0 < a.d;
+    const int branch = is_v ? 0 : static_cast<int>(f0 / a.d) - 1;
+    const int64_t row = min(tok, a.n_tok - 1);
+    const int64_t c0 = f0 - static_cast<int64_t>(is_v ? 0 : 1 + branch) * a.d + wf * 32 + lh * 4;
+    float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint2 h = make_uint2(0u, 0u);
+      if (!is_v) h = *reinterpret_cast<const uint2*>(a.H + (row * a.M + branch) * a.d + c0 + g * 8);
+      f32x4_t x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(acc[4 * g + e]) * st * so[4 * g + e];
+      if (is_v && tok < a.n_tok) __builtin_memcpy(static_cast<float*>(a.out) + tok * a.d + c0 + g * 8, &x, 16);
+      p = add4(p, gate_terms(x, is_v, h));
+    }
+    p = add4(p, make_float4(__shfl_xor(p.x, 32, 64), __shfl_xor(p.y, 32, 64), __shfl_xor(p.z, 32, 64), __shfl_xor(p.w, 32, 64)));
+    if (wf == 1 && lh == 0) red[wt * 32 + lr] = p;
+    __syncthreads();
+    if (wf == 0 && lh == 0 && tok < a.n_tok) a.stats[tok * a.nq + f0 / 64] = add4(p, red[wt * 32 + lr]);
+    return;
+  }
   if (tok >= a.n_tok) return;
   OutT* out = static_cast<OutT*>(a.out) + tok * a.n_out;
 #pragma unroll
@@ -613,10 +714,10 @@ project_i8_ring_kernel(ProjectI8Args a, int tiles_f) {
 inline int ring_bytes(int K) { return std::min(kRing, (K + 127) / 128) * 1024 * 16; }
 inline int ring_places(int K) { return std::min(4, (160 << 10) / ring_bytes(K)); }
 
-template <typename OutT>
+template <typename OutT, bool GATE = false>
 hipError_t launch_ring(const ProjectI8Args& a, hipStream_t s) {
   constexpr int kLds = kRing * 1024 * 16;
-  auto* const fn = project_i8_ring_kernel<OutT>;
+  auto* const fn = project_i8_ring_kernel<OutT, GATE>;
   static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -879,10 +980,11 @@ hipError_t launch_few_blocks(const ProjectI8Args& a, const void* e, hipStream_t 
   return launch_few_shift<OutT, E_DT, 1>(a, e, s);
 }
 
-template <typename OutT, int TF, int TT, int WF, int WT>
+template <typename OutT, int TF, int TT, int WF, int WT, bool GATE = false>
 hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
-  constexpr int kLds = 2 * (TF + TT) * 128 + 2 * (TF + TT) * 4;
-  auto* const fn = project_i8_tile_kernel<OutT, TF, TT, WF, WT>;
+  constexpr int kLds = 2 * (TF + TT) * 128 + 2 * (TF + TT) * 4 + (GATE ? WF * TT * 16 : 0);
+  static_assert(kLds * (8 / (WF * WT)) <= 160 << 10, "one workgroup of 8 wavefronts, or two of 4, on a CU");
+  auto* const fn = project_i8_tile_kernel<OutT, TF, TT, WF, WT, GATE>;
   static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -901,11 +1003,29 @@ hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which kernel a product of aligned operands takes.
+enum class Form { kRing, kTile128, kTile256 };
+
+Form product_form(int64_t n_tok, int64_t n_out, int64_t K) {
+  if (((n_out + 63) / 64) * ((n_tok + 63) / 64) <= 256 * ring_places(static_cast<int>(K))) return Form::kRing;
+  // a large tile for every CU
+  return ((n_out + 255) / 256) * ((n_tok + 255) / 256) >= 256 ? Form::kTile256 : Form::kTile128;
+}
+
 template <typename OutT>
 hipError_t launch_tiles(const ProjectI8Args& a, hipStream_t s) {
-  if (((a.n_out + 63) / 64) * ((a.n_tok + 63) / 64) <= 256 * ring_places(a.K)) return launch_ring<OutT>(a, s);
-  if (((a.n_out + 255) / 256) * ((a.n_tok + 255) / 256) >= 256) return launch_tile<OutT, 256, 256, 4, 2>(a, s);
-  return launch_tile<OutT, 128, 128, 2, 2>(a, s);
+  switch (product_form(a.n_tok, a.n_out, a.K)) {
+    case Form::kRing: return launch_ring<OutT>(a, s);
+    case Form::kTile256: return launch_tile<OutT, 256, 256, 4, 2>(a, s);
+    default: return launch_tile<OutT, 128, 128, 2, 2>(a, s);
+  }
+}
+
+// The GATE forms' sums come in runs of 64 columns (ring), 128 or 256; the conv
+// takes at most kConvMaxStats of them per row.
+Form gate_form(int64_t n_tok, int64_t n_out, int64_t K, int d) {
+  const Form f = product_form(n_tok, n_out, K);
+  return f == Form::kRing && 2 * d / 64 > kConvMaxStats ? Form::kTile128 : f;
 }
 
 }  // namespace
@@ -977,8 +1097,36 @@ hipError_t launch_project_i8(const void* e, int e_dtype, int64_t ldq, bool taile
                              const float* w_scale, int64_t n_tok, int64_t K, int64_t n_out, int out_dtype, void* out,
                              hipStream_t s) {
   if (n_tok == 0) return hipSuccess;
-  const ProjectI8Args a{static_cast<const int8_t*>(e), q_scale, w, w_scale, out, n_tok, ldq, n_out, static_cast<int>(K), tailed ? 1 : 0};
+  const ProjectI8Args a{static_cast<const int8_t*>(e), q_scale, w, w_scale, out, n_tok, ldq, n_out, static_cast<int>(K), tailed ? 1 : 0,
+                        nullptr, nullptr, 0, 0, 0, StateAdvance{}};
   return out_dtype == ENGRAM_BF16 ? launch_product<uint16_t>(a, e, e_dtype, s) : launch_product<float>(a, e, e_dtype, s);
+}
+
+bool project_i8_gate_advances(int64_t n_tok, int64_t K, int d, int M) {
+  return gate_form(n_tok, static_cast<int64_t>(1 + M) * d, K, d) == Form::kRing;
+}
+
+int project_i8_gate_columns(int64_t n_tok, int64_t K, int d, int M) {
+  switch (gate_form(n_tok, static_cast<int64_t>(1 + M) * d, K, d)) {
+    case Form::kRing: return 64;
+    case Form::kTile256: return d % 256 == 0 ? 256 : 128;
+    default: return 128;
+  }
+}
+
+hipError_t launch_project_i8_gate(const int8_t* q, const float* q_scale, const int8_t* w, const float* w_scale, int64_t n_tok, int64_t K,
+                                  int d, int M, const void* H, float* v, float4* stats, const StateAdvance& adv, hipStream_t s) {
+  if (n_tok == 0) return hipSuccess;
+  if (K % 16 != 0 || d % 128 != 0 || d > 4096) return hipErrorInvalidValue;
+  if (adv.adv_B > 0 && !project_i8_gate_advances(n_tok, K, d, M)) return hipErrorInvalidValue;
+  const int64_t n_out = static_cast<int64_t>(1 + M) * d;
+  const ProjectI8Args a{q, q_scale, w, w_scale, v, n_tok, K, n_out, static_cast<int>(K), 0, static_cast<const uint16_t*>(H), stats, d, M,
+                        static_cast<int>(n_out / project_i8_gate_columns(n_tok, K, d, M)), adv};
+  switch (gate_form(n_tok, n_out, K, d)) {
+    case Form::kRing: return launch_ring<float, true>(a, s);
+    case Form::kTile256: return launch_tile<float, 256, 256, 4, 2, true>(a, s);
+    default: return launch_tile<float, 128, 128, 2, 2, true>(a, s);
+  }
 }
 
 }  // namespace engram

@@ -189,6 +189,20 @@ def test_layer_matches_oracle(config, hdtype, kw):
     check(to_f64(alpha), ref["alpha"], to_f64(y), ref["Y"], to_f64(H), h_in, tag=f"int8 config {config}")
 
 
+@pytest.mark.parametrize("config,kw", [(1, dict(B=2, T=600)), (1, dict(B=3, T=7, table_dim=32, heads=1, d=128)),
+                                       (1, dict(B=2, T=40, d=192)), (1, dict(B=1, T=33, d=4096)),
+                                       (2, dict(B=1, T=3300)), (2, dict(B=1, T=8100, d=384)), (3, dict(B=600, T=1, layers=1))])
+def test_layer_forms(config, kw):
+    """Every form of the product with the gate's sums, ragged in tokens, at
+    widths that the sums' runs divide or not, and the unfused one."""
+    log(f"forward_i8 form {config} {kw}")
+    w, lay, L, w8 = _layer_case(config, "bf16", **kw)
+    H = eg.to_device(w.H, "bf16", DEV)
+    alpha, y = eg.forward_i8(torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV), H, L, w8, want_alpha=True, want_y=True)
+    ref = orc.forward(w.tokens, w.H, lay, "bf16", gemm="int8")
+    check_bf16_layer(to_f64(alpha), ref["alpha"], to_f64(y), ref["Y"], to_f64(H), orc.bf16_to_f64(w.H), tag=f"int8 {config} {kw}")
+
+
 def test_layer_decode_state():
     """A prefill and single-token steps with the int8 layer against the oracle run over the same chunks."""
     log("forward_i8 decode")
