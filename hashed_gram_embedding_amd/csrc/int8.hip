@@ -235,25 +235,57 @@ __device__ __forceinline__ u32x4_t load_chunk(const int8_t* row, int c, int K) {
 }
 
 // Rows whose length is no multiple of 16 into the product's own layout: whole
-// aligned chunks, the last one right-aligned behind zeros.  One thread a
-// chunk.  (Reading such rows into the tiles through registers instead took
-// 1.2 to 2.7 times as long as the aligned tiles; the copy of W costs its bytes
-// twice, 30 against 45 us at 2000 x 4099 x 2000.)
+// aligned chunks, the last one right-aligned behind zeros.  A thread takes
+// kAlignItems chunks, 256 apart.  A load from an address that is no multiple of
+// 4 takes the memory pipeline several times as long, so the 5 words around such
+// a chunk are read and shifted into place, except at the array's two ends.
+// (Reading odd rows into the tiles through registers instead took 46 us at
+// 2000 x 4099 x 2000, where the copy and the product take 38, and 94 against 87
+// at 1795 x 1001 x 32000; at 76 x 2823 x 70852, where the copy moves more than
+// the product, 113 against 149.)
+constexpr int kAlignItems = 4;
+
 struct AlignJob {
   const int8_t* x;   // [rows][K]
   u32x4_t* y;        // [rows][chunks]
-  int64_t n;         // rows * chunks
+  int64_t rows;
+  int64_t groups;    // workgroups: rows * chunks / (256 kAlignItems), rounded up
 };
 
 __global__ void __launch_bounds__(256)
 align_rows_kernel(AlignJob a, AlignJob b, int K, int chunks) {
-  int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const bool first = id < a.n;
-  if (!first) id -= a.n;
+  const bool first = blockIdx.x < a.groups;
   const AlignJob& j = first ? a : b;
-  if (id >= j.n) return;
-  const int64_t r = id / chunks;
-  j.y[id] = load_chunk(j.x + r * K, static_cast<int>(id - r * chunks), K);
+  const int64_t n = j.rows * chunks, base = (blockIdx.x - (first ? 0 : a.groups)) * 256 * kAlignItems;
+  const int64_t row0 = base / chunks, id0 = base + threadIdx.x;
+  const uint32_t c0 = static_cast<uint32_t>(base - row0 * chunks) + threadIdx.x, width = static_cast<uint32_t>(chunks);
+  const int8_t* const end = j.x + j.rows * K;
+  u32x4_t v[kAlignItems];
+  uint32_t behind[kAlignItems];
+  int past[kAlignItems];
+  int keep[kAlignItems];   // of the chunk: all, its last K % 16, nothing
+#pragma unroll
+  for (int i = 0; i < kAlignItems; ++i) {
+    const bool in = id0 + i * 256 < n;
+    const uint32_t down = (c0 + i * 256) / width;
+    const int64_t r = in ? row0 + down : 0;
+    const int c = in ? static_cast<int>(c0 + i * 256 - down * width) : 0;
+    const int8_t* p = j.x + r * K + min(c * 16, K - 16);
+    past[i] = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+    if (p - past[i] < j.x || p - past[i] + 20 > end) past[i] = 0;
+    keep[i] = c * 16 + 16 <= K ? 2 : c * 16 < K ? 1 : 0;
+    p -= past[i];
+    __builtin_memcpy(&v[i], p, 16);
+    __builtin_memcpy(&behind[i], past[i] != 0 ? p + 16 : p, 4);
+  }
+#pragma unroll
+  for (int i = 0; i < kAlignItems; ++i) {
+    const uint32_t by = static_cast<uint32_t>(past[i]);
+    const u32x4_t x{__builtin_amdgcn_alignbyte(v[i][1], v[i][0], by), __builtin_amdgcn_alignbyte(v[i][2], v[i][1], by),
+                    __builtin_amdgcn_alignbyte(v[i][3], v[i][2], by), __builtin_amdgcn_alignbyte(behind[i], v[i][3], by)};
+    const u32x4_t none{0, 0, 0, 0};
+    if (id0 + i * 256 < n) j.y[id0 + i * 256] = keep[i] == 2 ? x : keep[i] == 1 ? x & tail_mask(K) : none;
+  }
 }
 
 template <typename OutT>
@@ -1030,7 +1062,14 @@ Form gate_form(int64_t n_tok, int64_t n_out, int64_t K, int d) {
 
 }  // namespace
 
-int64_t i8_row_stride(int64_t cols) { return (cols + 15) / 16 * 16; }
+// Copied rows past 512 columns begin on whole 128-byte lines, like the slices
+// that the products read of them (2000 x 4112 x 2000 33 us, 2000 x 4224 x 2000
+// 27); shorter ones would grow by more than they gain (300 x 77 x 128000 moves
+// 60% more).
+int64_t i8_row_stride(int64_t cols) {
+  const int64_t whole = cols > 512 ? 128 : 16;
+  return cols % 16 == 0 ? cols : (cols + whole - 1) / whole * whole;
+}
 
 template <int DT>
 void launch_quantize_dt(const void* x, int64_t rows, int cols, int8_t* q, int64_t ldq, int tail, float* scale, hipStream_t s) {
@@ -1065,10 +1104,11 @@ bool project_i8_aligns(int64_t n_tok, int64_t K) { return K >= 16 && K % 16 != 0
 
 hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
                            hipStream_t s) {
-  const int64_t chunks = (K + 15) / 16, blocks = ((w_rows + q_rows) * chunks + 255) / 256;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  launch_k(align_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
-           AlignJob{w, reinterpret_cast<u32x4_t*>(w_out), w_rows * chunks}, AlignJob{q, reinterpret_cast<u32x4_t*>(q_out), q_rows * chunks},
+  const int64_t chunks = i8_row_stride(K) / 16, per = 256 * kAlignItems;
+  const int64_t wg = (w_rows * chunks + per - 1) / per, qg = (q_rows * chunks + per - 1) / per;
+  if (wg + qg > INT32_MAX) return hipErrorInvalidValue;
+  launch_k(align_rows_kernel, dim3(static_cast<unsigned>(wg + qg)), dim3(256), 0, s,
+           AlignJob{w, reinterpret_cast<u32x4_t*>(w_out), w_rows, wg}, AlignJob{q, reinterpret_cast<u32x4_t*>(q_out), q_rows, qg},
            static_cast<int>(K), static_cast<int>(chunks));
   return hipGetLastError();
 }

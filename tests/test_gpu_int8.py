@@ -76,7 +76,8 @@ def test_quantize_borders(dtype):
 
 SIZES = [(1, 16, 1), (1, 1024, 2000), (2, 64, 64), (3, 48, 65), (5, 17, 33), (16, 1024, 4100), (31, 15, 7), (33, 1, 5),
          (64, 1024, 256), (65, 128, 129), (130, 1000, 515), (200, 2823, 103), (257, 1024, 512), (300, 4096, 192),
-         (1000, 320, 1031), (513, 2048, 2048)]
+         (1000, 320, 1031), (513, 2048, 2048), (33, 513, 66),
+         (70, 601, 130), (300, 1001, 259), (40, 4099, 70), (18, 1009, 5)]
 
 
 @pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
