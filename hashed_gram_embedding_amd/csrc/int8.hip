@@ -743,8 +743,8 @@ project_i8_ring_kernel(ProjectI8Args a, int tiles_f) {
 }
 
 // LDS of a workgroup, and how many of them a CU holds.
-inline int ring_bytes(int K) { return std::min(kRing, (K + 127) / 128) * 1024 * 16; }
-inline int ring_places(int K) { return std::min(4, (160 << 10) / ring_bytes(K)); }
+inline int ring_bytes(int64_t K) { return static_cast<int>(std::min<int64_t>(kRing, (K + 127) / 128)) * 1024 * 16; }
+inline int ring_places(int64_t K) { return std::min(4, (160 << 10) / ring_bytes(K)); }
 
 template <typename OutT, bool GATE = false>
 hipError_t launch_ring(const ProjectI8Args& a, hipStream_t s) {
@@ -1039,7 +1039,7 @@ hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
 enum class Form { kRing, kTile128, kTile256 };
 
 Form product_form(int64_t n_tok, int64_t n_out, int64_t K) {
-  if (((n_out + 63) / 64) * ((n_tok + 63) / 64) <= 256 * ring_places(static_cast<int>(K))) return Form::kRing;
+  if (((n_out + 63) / 64) * ((n_tok + 63) / 64) <= 256 * ring_places(K)) return Form::kRing;
   // a large tile for every CU
   return ((n_out + 255) / 256) * ((n_tok + 255) / 256) >= 256 ? Form::kTile256 : Form::kTile128;
 }

@@ -133,6 +133,10 @@ __device__ __forceinline__ bool constant_row(float top, float temp, float* fill)
   return top != top || top == -__builtin_inff() || (top == __builtin_inff() && temp > 0.f);
 }
 
+// log2(e) / T, kept finite and above 0: the largest logit's exponent is then 0
+// and a masked one's -inf at the smallest and largest T too.
+__device__ __forceinline__ float exponent_factor(float temp) { return fminf(fmaxf(kLog2e / temp, 0x1p-126f), 0x1.fffffep127f); }
+
 // bf16 pairs stay packed from pass to pass: without this the compiler keeps
 // every unpacked value, then every exponential, for the next pass, twice the
 // registers there are.  (float32 rows keep their exponentials in place.)
@@ -190,7 +194,7 @@ probs_kernel(ProbsArgs a) {
     if (vt < V) out[vt] = at == vt ? 1.f : 0.f;
     return;
   }
-  const float f = kLog2e / temp;
+  const float f = exponent_factor(temp);
   const float et = __builtin_amdgcn_exp2f((xt - top) * f);
   float sum = et;
 #pragma unroll
@@ -225,7 +229,7 @@ probs_long_kernel(ProbsArgs a) {
   const void* in = static_cast<const char*>(a.logits) + row * a.ld * size;
   float* out = a.probs + row * V;
   const float temp = a.temperature != nullptr ? a.temperature[row / a.per] : 1.0f;
-  const float f = kLog2e / temp;
+  const float f = exponent_factor(temp);
   const int64_t quads = V / 4, vt = quads * 4 + threadIdx.x;
   const float xt = load_tail<DT>(in, vt, V);
   float top = -__builtin_inff(), sum = 0.f;
@@ -348,7 +352,7 @@ probs_segments_kernel(ProbsArgs a, int segs, Segment* __restrict__ part) {
   at = group_min<kSegThreads>(at, sh.first);
   float sum = 0.f;
   if (top > -__builtin_inff() && top < __builtin_inff()) {
-    const float f = kLog2e / temp;
+    const float f = exponent_factor(temp);
     sum = __builtin_amdgcn_exp2f((xt - top) * f);
 #pragma unroll
     for (int n = 0; n < kSegQuads; ++n) {
@@ -398,7 +402,7 @@ probs_join_kernel(ProbsArgs a, int segs, const Segment* __restrict__ part) {
     if (r.vt < a.V) out[r.vt] = value(r.vt);
     return;
   }
-  const float f = kLog2e / temp;
+  const float f = exponent_factor(temp);
   float sum = 0.f;
   for (int i = threadIdx.x; i < segs; i += kSegThreads)
     sum += mine[i].top > -__builtin_inff() ? mine[i].sum * __builtin_amdgcn_exp2f((mine[i].top - top) * f) : 0.f;

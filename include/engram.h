@@ -556,8 +556,8 @@ engram_status engram_commit_draft(const int32_t* tokens, int64_t B, int64_t T, c
 /* probs[r][v] = e^((l[r][v] - max_v l[r][v]) / T) / sum, float32 [rows][V].
  * logits: device, F32 or BF16, row r at element r * ld (ld >= V), aligned to
  * its elements.  temperature: device [ceil(rows / per)], T of rows i*per ..
- * i*per + per - 1 (per = the rows of one sequence), or NULL for 1.  T <= 0
- * puts probability 1 on the lowest index of the largest logit.  A logit of
+ * i*per + per - 1 (per = the rows of one sequence), or NULL for 1.  T <= 0 (or
+ * NaN) puts probability 1 on the lowest index of the largest logit.  A logit of
  * -inf has probability 0 and a row of nothing else has none at all (zeros); a
  * row with a NaN, or with +inf at T > 0, is NaN throughout.  rows and V below
  * 2^31; rows = 0 is a no-op.  ws: engram_token_probs_workspace() bytes,

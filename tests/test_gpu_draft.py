@@ -1,6 +1,8 @@
 """GPU: the layer over a drafted chunk with the state only read, the commit of
 the kept tokens, and a speculative decode loop of all the operators together
 against decoding token by token."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -118,6 +120,35 @@ def test_commit_in_a_graph():
         eg.forward_draft(tok, hr, L, ref, dr)
         eg.commit_draft(tok, L, dr, acc, ref)
         assert _same(h, hr) and torch.equal(st.ids, ref.ids) and torch.equal(st.pos, ref.pos) and _same(st.conv, ref.conv), i
+
+
+def test_int8_decode_in_a_graph():
+    """Single-token steps of the int8 layer, whose state advances in the
+    projection's launch: captured, replayed between eager work, against eager steps."""
+    log("int8 decode graph")
+    S = 5
+    w = inputs.make_config(3, B=S, T=6, layers=1, rows_per_table=997)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    h_all = eg.to_device(w.H, "bf16", DEV).view(S, 6, lay.branches, lay.d)
+    st, ref = (eg.DecodeState(S, 3, lay.branches, 9, lay.d, DEV) for _ in range(2))
+    one, h = tok[:, :1].contiguous(), h_all[:, :1].clone(memory_format=torch.contiguous_format)
+    ws = torch.empty(eg.lib().engram_forward_i8_workspace(S, 1, ctypes.byref(L.s)), dtype=torch.uint8, device=DEV)
+    eg.forward_i8(one, h.clone(), L, w8, state=_state_like(ref, S, 3, lay.branches, 9, lay.d), ws=ws)   # loads the code
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        eg.forward_i8(one, h, L, w8, state=st, ws=ws)
+    for t in range(6):
+        one.copy_(tok[:, t:t + 1])
+        h.copy_(h_all[:, t:t + 1])
+        g.replay()
+        torch.cuda.synchronize()
+        hr = h_all[:, t:t + 1].clone(memory_format=torch.contiguous_format)
+        eg.forward_i8(tok[:, t:t + 1].contiguous(), hr, L, w8, state=ref)
+        assert _same(h, hr) and torch.equal(st.ids, ref.ids) and torch.equal(st.pos, ref.pos) and _same(st.conv, ref.conv), t
+    assert (st.pos == 6).all()
 
 
 class _Decoder:

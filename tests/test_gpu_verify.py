@@ -85,6 +85,27 @@ def test_probs_of_masked_and_bad_rows(dtype, V):
     assert p[1, 4, 1] == 1 and p[1, 6, 0] == 1 and p[0, 1, V - 1] == 1
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [700, 40000, 200000])
+def test_probs_at_the_ends_of_the_temperature(dtype, V):
+    """The smallest temperatures (their reciprocal is past float32) leave the
+    largest logit, the largest ones every entry that is not masked; NaN counts as 0."""
+    log(f"token_probs temperatures {dtype} V={V}")
+    t = torch.tensor([2.0 ** -149, 1e-39, 1e-20, 1e30, 3e38, INF, NAN, -INF], device=DEV)
+    for rows in (1, 9):                      # 9: more rows than are split over workgroups
+        x = torch.randn(8, rows, V, device=DEV).to(TYPES[dtype])
+        x[:, :, V // 2] = 20.0
+        x[:, :, 5:9] = -INF
+        p = eg.token_probs(x, t).double().cpu().numpy()
+        one = np.zeros(V)
+        one[V // 2] = 1
+        flat = np.full(V, 1 / (V - 4))
+        flat[5:9] = 0
+        for s in range(8):
+            want = flat if 3 <= s <= 5 else one
+            assert np.all(np.abs(p[s] - want) <= want * 2.0 ** -24 * (V / 64 + 32 + 4)), (s, rows)
+
+
 def test_probs_of_padded_rows():
     """Rows of a padded vocabulary: the padding is not read, whatever it holds."""
     log("token_probs padded")
