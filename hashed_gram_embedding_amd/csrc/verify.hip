@@ -1,5 +1,7 @@
 // Token probabilities and the verification of drafted tokens: the end of a
 // speculative decode step whose layers ran over the drafted chunk.
+#include <type_traits>
+
 #include "device_util.h"
 #include "engram_internal.h"
 
@@ -11,10 +13,44 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-__device__ __forceinline__ double wave_sum64(double x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+// Cross-lane steps in the registers (DPP) rather than through LDS: every
+// reduction of these kernels is on the chain from a row's last load to its
+// result (verification of 1 x 4 drafts x 32001 7.8 -> 6.9 us).
+//
+// x of the lane that CTRL names, in the rows of 16 lanes that ROWS names; `old`
+// elsewhere and where there is no such lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float from_lane(float old, float x) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(old), __float_as_uint(x), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double from_lane(double old, double x) {
+  const uint64_t o = __double_as_longlong(old), b = __double_as_longlong(x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(static_cast<uint32_t>(o), static_cast<uint32_t>(b), CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(static_cast<uint32_t>(o >> 32), static_cast<uint32_t>(b >> 32), CTRL, ROWS, 0xf, false);
+  return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// lane - n of the row; lane - 1; the last lane of the row before; lane 31
+constexpr int kRowShr = 0x110, kWaveShr1 = 0x138, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+
+// Inclusive sum over the lanes of a wavefront.
+template <typename T>
+__device__ __forceinline__ T wave_scan(T x) {
+  x += from_lane<kRowShr + 1, 0xf>(T(0), x);
+  x += from_lane<kRowShr + 2, 0xf>(T(0), x);
+  x += from_lane<kRowShr + 4, 0xf>(T(0), x);
+  x += from_lane<kRowShr + 8, 0xf>(T(0), x);
+  x += from_lane<kRowBcast15, 0xa>(T(0), x);
+  x += from_lane<kRowBcast31, 0xc>(T(0), x);
   return x;
+}
+
+__device__ __forceinline__ float at_lane(float x, int lane) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane)); }
+__device__ __forceinline__ double at_lane(double x, int lane) {
+  const uint64_t b = __double_as_longlong(x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane), hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
+  return __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
 // ---- probabilities ----
@@ -80,9 +116,13 @@ __device__ __forceinline__ float load_tail(const void* row, int64_t v, int64_t V
 }
 
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
-  return x;
+  x = fmaxf(x, from_lane<kRowShr + 1, 0xf>(x, x));
+  x = fmaxf(x, from_lane<kRowShr + 2, 0xf>(x, x));
+  x = fmaxf(x, from_lane<kRowShr + 4, 0xf>(x, x));
+  x = fmaxf(x, from_lane<kRowShr + 8, 0xf>(x, x));
+  x = fmaxf(x, from_lane<kRowBcast15, 0xa>(x, x));
+  x = fmaxf(x, from_lane<kRowBcast31, 0xc>(x, x));
+  return at_lane(x, 63);
 }
 
 // Largest value over the workgroup, NaN if any thread saw one.
@@ -100,7 +140,7 @@ __device__ __forceinline__ float group_max(float x, bool nan, float* red) {
 
 template <int THREADS>
 __device__ __forceinline__ float group_sum(float x, float* red) {
-  x = wave_sum(x);
+  x = at_lane(wave_scan(x), 63);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
   __syncthreads();
   float s = red[0];
@@ -564,40 +604,45 @@ __device__ __forceinline__ double part_sum(const Rest& r, int64_t v0, int64_t le
   const int lane = threadIdx.x & 63;
   const int64_t end = min(v0 + len, V);
   double s[2] = {0.0, 0.0};
-  int64_t v = v0 + lane * VEC;
-  for (; v + (U - 1) * 64 * VEC + VEC <= end; v += U * 64 * VEC) {
+  // U runs of VEC entries a lane, all loads in flight; `whole`: all of them
+  // before `end`, else the runs that are not are read from end - VEC on and the
+  // entries that a run does not have itself left out
+  auto take = [&](int64_t at, auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
     float p[U][VEC], q[U][VEC];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      load_vec<DT>(r.p, v + i * 64 * VEC, p[i]);
-      if constexpr (Q) load_vec<DT>(r.q, v + i * 64 * VEC, q[i]);
+      const int64_t v = at + (i * 64 + lane) * VEC, from = kWhole ? v : min(v, end - VEC);
+      load_vec<DT>(r.p, from, p[i]);
+      if constexpr (Q) load_vec<DT>(r.q, from, q[i]);
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i) {
+      const int64_t v = at + (i * 64 + lane) * VEC, from = kWhole ? v : min(v, end - VEC);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) s[k & 1] += entry(p[i][k], Q ? q[i][k] : 0.0f, !Q && static_cast<int32_t>(v) + i * 64 * VEC + k == r.drop);
+      for (int k = 0; k < VEC; ++k) {
+        const double x = entry(p[i][k], Q ? q[i][k] : 0.0f, !Q && static_cast<int32_t>(from) + k == r.drop);
+        s[k & 1] += kWhole || from + k >= v ? x : 0.0;
+      }
+    }
+  };
+  constexpr int64_t step = U * 64 * VEC;
+  int64_t at = v0;
+  for (; at + step <= end; at += step) take(at, std::true_type{});
+  if (at < end) {
+    if (V >= VEC) {
+      take(at, std::false_type{});
+    } else {   // a row shorter than a run
+      const int64_t v = at + lane;
+      if (v < end) s[0] = entry_at<DT>(r, v);
+    }
   }
-  for (; v < end; v += 64 * VEC)
-#pragma unroll
-    for (int k = 0; k < VEC; ++k)
-      if (v + k < end) s[k & 1] += entry_at<DT>(r, v + k);
-  return wave_sum64(s[0] + s[1]);
+  return at_lane(wave_scan(s[0] + s[1]), 63);
 }
 
 template <int DT>
 __device__ __forceinline__ double part_sum(const Rest& r, int64_t v0, int64_t len, int64_t V) {
   return r.q != nullptr ? part_sum<DT, true>(r, v0, len, V) : part_sum<DT, false>(r, v0, len, V);
-}
-
-// Inclusive sum over the lanes of a wavefront.
-__device__ __forceinline__ double wave_scan64(double x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double y = __shfl_up(x, off, 64);
-    if (lane >= off) x += y;
-  }
-  return x;
 }
 
 struct PickShared {
@@ -612,14 +657,14 @@ template <int DT>
 __device__ __forceinline__ int64_t pick(const Rest& r, PickShared& sh, int parts, int64_t len, int64_t V, float u, bool* none) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const double x = lane < parts ? sh.part[lane] : 0.0;
-  const double scan = wave_scan64(x);
-  const double total = __shfl(scan, 63, 64), want = static_cast<double>(u) * total;
+  const double scan = wave_scan(x);
+  const double total = at_lane(scan, 63), want = static_cast<double>(u) * total;
   *none = !(total > 0.0);
   if (*none || !(total < __builtin_inf())) return -1;
   const uint64_t over = __ballot(x > 0.0 && scan > want), any = __ballot(x > 0.0);
   const bool past = over == 0;   // u not below 1: the last token that has any probability
   const int part = past ? 63 - __builtin_clzll(any) : __builtin_ctzll(over);
-  const double left = part > 0 ? __shfl(scan, part - 1, 64) : 0.0;
+  const double left = part > 0 ? at_lane(scan, part - 1) : 0.0;
   // this thread's run of the part
   const int run = static_cast<int>((len + 64 * kVerifyWaves - 1) / (64 * kVerifyWaves));
   const int64_t v0 = part * len + static_cast<int64_t>(tid) * run, v1 = min(min(v0 + run, (part + 1) * len), V);
@@ -630,13 +675,12 @@ __device__ __forceinline__ int64_t pick(const Rest& r, PickShared& sh, int parts
 #pragma unroll
   for (int i = 0; i < kKept; ++i) sum += e[i];
   for (int64_t v = v0 + kKept; v < v1; ++v) sum += entry_at<DT>(r, v);
-  const double inside = wave_scan64(sum);
+  const double inside = wave_scan(sum);
   if (lane == 63) sh.wave[wave] = inside;
   __syncthreads();
   double at = left;
   for (int w = 0; w < wave; ++w) at += sh.wave[w];
-  const double prev = __shfl_up(inside, 1, 64);
-  if (lane > 0) at += prev;
+  at += from_lane<kWaveShr1, 0xf>(0.0, inside);
   // the first of this run that passes (in a chunk of its own kind: offsets
   // within the part fit an int), and the last one that has any probability
   int found = INT32_MAX, last = -1;
@@ -659,11 +703,10 @@ __device__ __forceinline__ int64_t pick(const Rest& r, PickShared& sh, int parts
       }
     }
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    found = min(found, __shfl_xor(found, off, 64));
-    last = max(last, __shfl_xor(last, off, 64));
-  }
+  // (runs ascend with the lanes, and with the wavefronts)
+  const uint64_t founds = __ballot(found != INT32_MAX), lasts = __ballot(last >= 0);
+  found = founds != 0 ? __builtin_amdgcn_readlane(found, __builtin_ctzll(founds)) : INT32_MAX;
+  last = lasts != 0 ? __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(lasts)) : -1;
   if (lane == 0) {
     sh.found[wave] = found;
     sh.last[wave] = last;
@@ -738,9 +781,9 @@ verify_parts_kernel(VerifyArgs a) {
 }
 
 // Long rows: the sums are split over 16 workgroups a row, in a launch of their
-// own.  One launch / two, in us: 1 x 32000 7.7 / 8.5, 1 x 65536 10.4 / 8.0, 1 x 128000
-// 15.0 / 8.6, 64 x 65536 10.9 / 10.4, 128 x 65536 15.9 / 16.7, 128 x 128000 28.0 /
-// 23.7, 256 x 128000 43.5 / 38.5.
+// own.  One launch / two, in us: 1 x 32000 6.6 / 6.8, 1 x 65536 9.4 / 6.9, 1 x 128000
+// 15.3 / 7.5, 64 x 65536 10.0 / 9.6, 128 x 65536 15.2 / 16.3, 128 x 128000 28.7 /
+// 25.3, 256 x 128000 46.6 / 41.9.
 bool verify_splits(int64_t S, int64_t V) { return V > (S <= 64 ? 49152 : 81920); }
 
 template <int DT>
