@@ -58,9 +58,19 @@ __device__ __forceinline__ int quantize(float x, const RowScale& r) {
 // Largest magnitude of values held by a group of wavefronts, by its bits: an
 // infinity and a NaN order above every finite value.
 __device__ __forceinline__ uint32_t wave_top(uint32_t top) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off, 64)));
-  return top;
+  // in the registers (DPP): over each row of 16 lanes, then into the rows behind
+  auto join = [&](auto ctrl, auto rows) {
+    top = max(top, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(top), static_cast<int>(top), decltype(ctrl)::value,
+                                                                     decltype(rows)::value, 0xf, false)));
+  };
+  constexpr int kRowShr = 0x110, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+  join(std::integral_constant<int, kRowShr + 1>{}, std::integral_constant<int, 0xf>{});
+  join(std::integral_constant<int, kRowShr + 2>{}, std::integral_constant<int, 0xf>{});
+  join(std::integral_constant<int, kRowShr + 4>{}, std::integral_constant<int, 0xf>{});
+  join(std::integral_constant<int, kRowShr + 8>{}, std::integral_constant<int, 0xf>{});
+  join(std::integral_constant<int, kRowBcast15>{}, std::integral_constant<int, 0xa>{});
+  join(std::integral_constant<int, kRowBcast31>{}, std::integral_constant<int, 0xc>{});
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(top), 63));
 }
 
 __device__ __forceinline__ float row_scale(uint32_t top) {
@@ -785,10 +795,11 @@ project_i8_short_kernel(ProjectI8Args a) {
 // up to 16 NB tokens sit in LDS.  A row of codes starts 16 bytes further
 // round the banks than the one before (stride 16 modulo 256), so the 16 rows
 // of an operand read are free of conflicts.
-// E_DT: type of e.  Up to 16 float rows are quantised here, by every
-// workgroup, behind the first loads of W: it saves a launch (9 x 1024 x 2048
-// 9.5 -> 8.7 us).  With 32 it takes longer than a launch of its own (13.4
-// against 11.3 us).
+// E_DT: type of e.  Up to 16 float rows of together 32,768 columns are
+// quantised here, by every workgroup, behind the first loads of W: it saves a
+// launch (9 x 1024 x 2048 9.5 -> 8.7 us).  More take longer than a launch of
+// their own (32 x 1024 x 2048 13.4 against 11.3 us, 16 x 4096 x 2000 17.9 against
+// 16.1).
 // 1 x 1024 x 128000 takes 24.3 us (5.4 TB/s), 32 x 1024 x 128000 29.4; past 32
 // tokens the tiles are faster (64 tokens: 46 against 36 us).
 constexpr int kFewWaves = 8;
@@ -1098,7 +1109,7 @@ bool project_i8_few(int64_t n_tok, int64_t K) {
 
 }  // namespace
 
-bool project_i8_quantizes(int64_t n_tok, int64_t K) { return n_tok <= 16 && project_i8_few(n_tok, K); }
+bool project_i8_quantizes(int64_t n_tok, int64_t K) { return n_tok <= 16 && n_tok * K <= 32768 && project_i8_few(n_tok, K); }
 
 bool project_i8_aligns(int64_t n_tok, int64_t K) { return K >= 16 && K % 16 != 0 && !project_i8_few(n_tok, K); }
 
