@@ -230,26 +230,26 @@ def _check_tensor(name: str, t: torch.Tensor, dtypes, shape, device, strided: bo
     raise ValueError(f"{name} must be contiguous")
 
 
-def _empty(shape, dtype, device: torch.device, stream):
+def _empty(like: torch.Tensor, shape, dtype, stream):
     """Memory for a call on `stream` (default: the device's current one): from
     that stream's own pool, so that nothing still running elsewhere uses it."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None or like.device.type != "cuda":
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _launch(fn, device: torch.device, stream, *args):
     """fn(*args, stream) with `device` current, on `stream` (default: the
     device's current one)."""
     index = device.index
-    if device.type != "cuda":
+    if index is None:
         raise ValueError(f"the tensors must be on a GPU, not on {device}")
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
     # (the raw handle of the current stream, without building a Stream object: 0.1 instead of 2.9 us a call)
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, s)
     else:
         with torch.cuda.device(index):
@@ -694,8 +694,8 @@ def quantize_i8(x: torch.Tensor, stream=None):
     int8 [rows, cols], scales float32 [rows]), x about codes * scale."""
     rows, cols = x.shape
     _check_tensor("x", x, _FLOATS, (rows, cols), x.device)
-    q = _empty((rows, cols), torch.int8, x.device, stream)
-    scale = _empty(rows, torch.float32, x.device, stream)
+    q = _empty(x, (rows, cols), torch.int8, stream)
+    scale = _empty(x, rows, torch.float32, stream)
     _launch(lib().engram_quantize_i8, x.device, stream, x.data_ptr(), _DT_OF[x.dtype], rows, cols, q.data_ptr(),
             scale.data_ptr())
     return q, scale
@@ -718,12 +718,12 @@ def project_i8(e: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, e_scale:
         _check_tensor("e_scale", e_scale, _F32, lead, dev)
     odt = _DT[out_dtype]
     if out is None:
-        out = _empty((*lead, n_out), _TORCH_DT[odt], dev, stream)
+        out = _empty(e, (*lead, n_out), _TORCH_DT[odt], stream)
     else:
         _check_tensor("out", out, (_TORCH_DT[odt],), (*lead, n_out), dev)
     nbytes = lib().engram_project_i8_workspace(n_tok, d_mem, n_out, dt)
     if ws is None and nbytes:
-        ws = _empty(nbytes, torch.uint8, dev, stream)
+        ws = _empty(e, nbytes, torch.uint8, stream)
     _launch(lib().engram_project_i8, dev, stream, e.data_ptr(), dt, None if e_scale is None else e_scale.data_ptr(),
             w.data_ptr(), w_scale.data_ptr(), n_tok, d_mem, n_out, odt, out.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
@@ -778,9 +778,9 @@ def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, 
     return dev, B, T
 
 
-def _layer_outputs(B, T, layer, dev, want_alpha, want_y, stream):
-    alpha = _empty((B, T, layer.M), torch.float32, dev, stream) if want_alpha else None
-    y = _empty((B, T, layer.M, layer.d), torch.float32, dev, stream) if want_y else None
+def _layer_outputs(B, T, layer, H, want_alpha, want_y, stream):
+    alpha = _empty(H, (B, T, layer.M), torch.float32, stream) if want_alpha else None
+    y = _empty(H, (B, T, layer.M, layer.d), torch.float32, stream) if want_y else None
     return alpha, y
 
 
@@ -790,9 +790,9 @@ def forward_i8(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, w8: Int8Weig
     """forward() with Step 5 as the 8-bit integer product.  Returns (alpha, y)
     when asked."""
     dev, B, T = _check_chunk(tokens, H, layer, state)
-    alpha, y = _layer_outputs(B, T, layer, dev, want_alpha, want_y, stream)
+    alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
     if ws is None:
-        ws = _empty(max(lib().engram_forward_i8_workspace(B, T, ctypes.byref(layer.s)), 256), torch.uint8, dev, stream)
+        ws = _empty(H, max(lib().engram_forward_i8_workspace(B, T, ctypes.byref(layer.s)), 256), torch.uint8, stream)
     _launch(lib().engram_forward_i8, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s),
             ctypes.byref(w8.s), None if state is None else ctypes.byref(state.s), _ptr(alpha), _ptr(y), ws.data_ptr(),
             ws.numel())
@@ -807,10 +807,10 @@ def forward_draft(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, state: De
     dev, B, T = _check_chunk(tokens, H, layer, state)
     if (draft.B, draft.T) != (B, T):
         raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
-    alpha, y = _layer_outputs(B, T, layer, dev, want_alpha, want_y, stream)
+    alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
     p8 = None if w8 is None else ctypes.byref(w8.s)
     if ws is None:
-        ws = _empty(max(lib().engram_forward_draft_workspace(B, T, ctypes.byref(layer.s), p8), 256), torch.uint8, dev, stream)
+        ws = _empty(H, max(lib().engram_forward_draft_workspace(B, T, ctypes.byref(layer.s), p8), 256), torch.uint8, stream)
     _launch(lib().engram_forward_draft, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s), p8,
             ctypes.byref(state.s), ctypes.byref(draft.s), _ptr(alpha), _ptr(y), ws.data_ptr(), ws.numel())
     return alpha, y
@@ -848,12 +848,12 @@ def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None
     if temperature is not None:
         _check_tensor("temperature", temperature, _F32, (S,), dev)
     if probs is None:
-        probs = _empty(logits.shape, torch.float32, dev, stream)
+        probs = _empty(logits, logits.shape, torch.float32, stream)
     else:
         _check_tensor("probs", probs, _F32, logits.shape, dev)
     nbytes = lib().engram_token_probs_workspace(S * per, V)
     if ws is None and nbytes:
-        ws = _empty(nbytes, torch.uint8, dev, stream)
+        ws = _empty(logits, nbytes, torch.uint8, stream)
     _launch(lib().engram_token_probs, dev, stream, logits.data_ptr(), _DT_OF[logits.dtype], S * per, V, ld,
             None if temperature is None else temperature.data_ptr(), max(per, 1), probs.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
@@ -878,11 +878,11 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], drafted: 
     _check_tensor("u_sample", u_sample, _F32, (S,), dev)
     if n_draft is not None:
         _check_tensor("n_draft", n_draft, _I32, (S,), dev)
-    tokens = _empty((S, G + 1), torch.int32, dev, stream)
-    n_accepted = _empty(S, torch.int32, dev, stream)
+    tokens = _empty(drafted, (S, G + 1), torch.int32, stream)
+    n_accepted = _empty(drafted, S, torch.int32, stream)
     nbytes = lib().engram_verify_drafts_workspace(S, V)
     if ws is None and nbytes:
-        ws = _empty(nbytes, torch.uint8, dev, stream)
+        ws = _empty(drafted, nbytes, torch.uint8, stream)
     _launch(lib().engram_verify_drafts, dev, stream, target.data_ptr(), None if draft is None else draft.data_ptr(),
             _DT_OF[target.dtype], drafted.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
             u_accept.data_ptr(), u_sample.data_ptr(), S, G, V, tokens.data_ptr(), n_accepted.data_ptr(),
