@@ -239,6 +239,15 @@ def _empty(like: torch.Tensor, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _workspace(like: torch.Tensor, ws: Optional[torch.Tensor], nbytes: int, stream):
+    """The caller's workspace, checked, or one of this call's own (None for 0 bytes)."""
+    if ws is None:
+        return _empty(like, nbytes, torch.uint8, stream) if nbytes else None
+    if ws.device != like.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {like.device}, not {ws.dtype} on {ws.device}")
+    return ws
+
+
 def _launch(fn, device: torch.device, stream, *args):
     """fn(*args, stream) with `device` current, on `stream` (default: the
     device's current one)."""
@@ -722,8 +731,7 @@ def project_i8(e: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, e_scale:
     else:
         _check_tensor("out", out, (_TORCH_DT[odt],), (*lead, n_out), dev)
     nbytes = lib().engram_project_i8_workspace(n_tok, d_mem, n_out, dt)
-    if ws is None and nbytes:
-        ws = _empty(e, nbytes, torch.uint8, stream)
+    ws = _workspace(e, ws, nbytes, stream)
     _launch(lib().engram_project_i8, dev, stream, e.data_ptr(), dt, None if e_scale is None else e_scale.data_ptr(),
             w.data_ptr(), w_scale.data_ptr(), n_tok, d_mem, n_out, odt, out.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
@@ -766,6 +774,8 @@ def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, 
     dev = tokens.device
     B, T = tokens.shape
     _check_tensor("tokens", tokens, _I32, (B, T), dev)
+    if layer.w.device != dev:
+        raise ValueError(f"the layer is on {layer.w.device}, the tokens are on {dev}")
     if H is not None:
         _check_tensor("H", H, (_TORCH_DT[layer.hdtype],), H.shape, dev)
         if H.numel() != B * T * layer.M * layer.d:
@@ -776,6 +786,13 @@ def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, 
         if state.ids.shape[1] != g.hash.max_n - 1:
             raise ValueError(f"the state holds {state.ids.shape[1]} ids a sequence, the layer needs {g.hash.max_n - 1}")
     return dev, B, T
+
+
+def _check_draft(draft: Draft, B: int, T: int, dev):
+    if (draft.B, draft.T) != (B, T):
+        raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
+    if draft.v.device != dev:
+        raise ValueError(f"the draft is on {draft.v.device}, the tokens are on {dev}")
 
 
 def _layer_outputs(B, T, layer, H, want_alpha, want_y, stream):
@@ -791,8 +808,7 @@ def forward_i8(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, w8: Int8Weig
     when asked."""
     dev, B, T = _check_chunk(tokens, H, layer, state)
     alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
-    if ws is None:
-        ws = _empty(H, max(lib().engram_forward_i8_workspace(B, T, ctypes.byref(layer.s)), 256), torch.uint8, stream)
+    ws = _workspace(H, ws, max(lib().engram_forward_i8_workspace(B, T, ctypes.byref(layer.s)), 256), stream)
     _launch(lib().engram_forward_i8, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s),
             ctypes.byref(w8.s), None if state is None else ctypes.byref(state.s), _ptr(alpha), _ptr(y), ws.data_ptr(),
             ws.numel())
@@ -805,12 +821,10 @@ def forward_draft(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, state: De
     """One layer over a drafted chunk: H as forward() (or forward_i8() with w8)
     would leave it, `state` only read, the chunk's conv inputs in `draft`."""
     dev, B, T = _check_chunk(tokens, H, layer, state)
-    if (draft.B, draft.T) != (B, T):
-        raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
+    _check_draft(draft, B, T, dev)
     alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
     p8 = None if w8 is None else ctypes.byref(w8.s)
-    if ws is None:
-        ws = _empty(H, max(lib().engram_forward_draft_workspace(B, T, ctypes.byref(layer.s), p8), 256), torch.uint8, stream)
+    ws = _workspace(H, ws, max(lib().engram_forward_draft_workspace(B, T, ctypes.byref(layer.s), p8), 256), stream)
     _launch(lib().engram_forward_draft, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s), p8,
             ctypes.byref(state.s), ctypes.byref(draft.s), _ptr(alpha), _ptr(y), ws.data_ptr(), ws.numel())
     return alpha, y
@@ -821,8 +835,7 @@ def commit_draft(tokens: torch.Tensor, layer: Layer, draft: Draft, n_accepted: t
     """Advance `state` by the first n_accepted + 1 tokens of each sequence's
     chunk (n_accepted int32 [B] from verify_drafts; -1 keeps none)."""
     dev, B, T = _check_chunk(tokens, None, layer, state)
-    if (draft.B, draft.T) != (B, T):
-        raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
+    _check_draft(draft, B, T, dev)
     _check_tensor("n_accepted", n_accepted, _I32, (B,), dev)
     _launch(lib().engram_commit_draft, dev, stream, tokens.data_ptr(), B, T, ctypes.byref(layer.s),
             ctypes.byref(draft.s), n_accepted.data_ptr(), ctypes.byref(state.s))
@@ -852,8 +865,7 @@ def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None
     else:
         _check_tensor("probs", probs, _F32, logits.shape, dev)
     nbytes = lib().engram_token_probs_workspace(S * per, V)
-    if ws is None and nbytes:
-        ws = _empty(logits, nbytes, torch.uint8, stream)
+    ws = _workspace(logits, ws, nbytes, stream)
     _launch(lib().engram_token_probs, dev, stream, logits.data_ptr(), _DT_OF[logits.dtype], S * per, V, ld,
             None if temperature is None else temperature.data_ptr(), max(per, 1), probs.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
@@ -881,8 +893,7 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], drafted: 
     tokens = _empty(drafted, (S, G + 1), torch.int32, stream)
     n_accepted = _empty(drafted, S, torch.int32, stream)
     nbytes = lib().engram_verify_drafts_workspace(S, V)
-    if ws is None and nbytes:
-        ws = _empty(drafted, nbytes, torch.uint8, stream)
+    ws = _workspace(drafted, ws, nbytes, stream)
     _launch(lib().engram_verify_drafts, dev, stream, target.data_ptr(), None if draft is None else draft.data_ptr(),
             _DT_OF[target.dtype], drafted.data_ptr(), None if n_draft is None else n_draft.data_ptr(),
             u_accept.data_ptr(), u_sample.data_ptr(), S, G, V, tokens.data_ptr(), n_accepted.data_ptr(),

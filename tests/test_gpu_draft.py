@@ -122,6 +122,36 @@ def test_commit_in_a_graph():
         assert _same(h, hr) and torch.equal(st.ids, ref.ids) and torch.equal(st.pos, ref.pos) and _same(st.conv, ref.conv), i
 
 
+def test_operands_elsewhere_are_refused():
+    """Buffers in host memory, or for another batch, never reach a kernel."""
+    log("draft refusals")
+    w = inputs.make_config(3, B=2, T=4, layers=1, rows_per_table=997)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    H = eg.to_device(w.H, "bf16", DEV)
+    st = eg.DecodeState(2, 3, lay.branches, 9, lay.d, DEV)
+    acc = torch.zeros(2, dtype=torch.int32, device=DEV)
+    draft = eg.Draft(2, 4, L, DEV)
+    with pytest.raises(ValueError, match="draft is on cpu"):
+        eg.forward_draft(tok, H, L, st, eg.Draft(2, 4, L, "cpu"))
+    with pytest.raises(ValueError, match="draft is on cpu"):
+        eg.commit_draft(tok, L, eg.Draft(2, 4, L, "cpu"), acc, st)
+    with pytest.raises(ValueError, match="layer is on cuda"):
+        eg.forward_draft(tok.cpu(), H, L, st, draft)
+    with pytest.raises(ValueError, match="n_accepted is on cpu"):
+        eg.commit_draft(tok, L, draft, acc.cpu(), st)
+    with pytest.raises(ValueError, match="the draft is for"):
+        eg.commit_draft(tok[:, :3].contiguous(), L, draft, acc, st)
+    with pytest.raises(ValueError, match="ws must be"):
+        eg.forward_i8(tok, H, L, w8, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="state.conv has shape"):
+        eg.forward_i8(tok, H, L, w8, state=eg.DecodeState(1, 3, lay.branches, 9, lay.d, DEV))
+    with pytest.raises(eg.EngramError, match="workspace"):
+        eg.forward_i8(tok, H, L, w8, ws=torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
 def test_int8_decode_in_a_graph():
     """Single-token steps of the int8 layer, whose state advances in the
     projection's launch: captured, replayed between eager work, against eager steps."""

@@ -208,6 +208,10 @@ def test_binding_refuses_what_it_would_misread():
         eg.token_probs(l3.transpose(0, 1))
     with pytest.raises(ValueError, match="temperature has shape"):
         eg.token_probs(l3, torch.zeros(3))
+    with pytest.raises(ValueError, match="uint8 tensor on cpu, not torch.float32"):
+        eg.token_probs(torch.zeros(1, 40000), ws=torch.zeros(4096))
+    with pytest.raises(ValueError, match="uint8 tensor on cpu, not torch.uint8 on meta"):
+        eg.token_probs(torch.zeros(1, 40000), ws=torch.zeros(4096, dtype=torch.uint8, device="meta"))
     with pytest.raises(ValueError, match=r"\[S, R, V\]"):
         eg.token_probs(l3[0, 0])
     p, q, d, ua, us = torch.zeros(2, 4, 9), torch.zeros(2, 3, 9), torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, 3), torch.zeros(2)
