@@ -1476,7 +1476,6 @@ ENGRAM_API engram_status engram_commit_draft(const int32_t* tokens, int64_t B, i
   if ((r = check_draft("commit_draft", draft)) != ENGRAM_OK) return r;
   if (draft->v_stride < g.d || draft->v_stride % 4 != 0)
     return fail(ENGRAM_EINVAL, "commit_draft: v_stride must be a multiple of 4, at least d");
-  if (B > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "commit_draft: B above 2^31-1");
   if (B * T == 0) return ENGRAM_OK;
   if (tokens == nullptr || n_accepted == nullptr)
     return fail(ENGRAM_EINVAL, "commit_draft: tokens and n_accepted must be non-NULL");
