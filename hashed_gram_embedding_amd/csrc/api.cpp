@@ -632,11 +632,18 @@ engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, c
                     "project_i8 launch");
 }
 
-// Step 5 in 8-bit integers: W and where the gathered rows' codes go.
+// Step 5 in 8-bit integers: W and where the gathered rows' codes go, or
+// (in_rows) lie already, their scales behind them.
 struct Int8Step {
   const engram_i8_weights* w;
   CodeSpace space;
+  bool in_rows;
 };
+
+// Whether the gather writes the layer's rows as codes.
+bool gathers_i8(const engram_layer* L) {
+  return use_fused(L) && engram::gather_i8_rows(static_cast<int64_t>(L->tables.n_tables) * L->tables.dim);
+}
 
 // Steps 5-8 on gathered rows e.  i8: Step 5 as the 8-bit integer product, or
 // null.  commit = false leaves st as it is.
@@ -704,8 +711,12 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
                            commit);
   }
   if (i8 != nullptr && use_fused(L)) {
-    r = run_quantize(e, g.hdtype, n_tok, d_mem, i8->space, stream);
-    if (r != ENGRAM_OK) return r;
+    const int8_t* codes = i8->in_rows ? static_cast<const int8_t*>(e) : i8->space.codes;
+    const float* scale = i8->in_rows ? reinterpret_cast<const float*>(codes + n_tok * d_mem) : i8->space.scale;
+    if (!i8->in_rows) {
+      r = run_quantize(e, g.hdtype, n_tok, d_mem, i8->space, stream);
+      if (r != ENGRAM_OK) return r;
+    }
     const int q = d / engram::project_i8_gate_columns(n_tok, d_mem, d, M);
     const bool fold = engram::project_i8_gate_advances(n_tok, d_mem, d, M) && folds(q, q, false);
     engram::StateAdvance adv{};
@@ -713,7 +724,7 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
       adv = engram::StateAdvance{st->ids, st->pos, tokens, L->hash.proj, static_cast<int32_t>(L->hash.vocab), g_err_word.load(),
                                  L->hash.max_n, static_cast<int32_t>(T), static_cast<int32_t>(B)};
     prof_mark(stream, "project_i8_gate_kernel");
-    r = hip_status(engram::launch_project_i8_gate(i8->space.codes, i8->space.scale, i8->w->w, i8->w->scale, n_tok, d_mem, d, M, H, f.kv,
+    r = hip_status(engram::launch_project_i8_gate(codes, scale, i8->w->w, i8->w->scale, n_tok, d_mem, d, M, H, f.kv,
                                                   f.stats, adv, stream),
                    "int8 projection launch");
     if (r != ENGRAM_OK) return r;
@@ -1358,7 +1369,7 @@ DraftWorkspace carve_draft(Carve& c, int64_t n_tok, const engram_layer* L, bool 
     w.f.stats = c.take<float4>(static_cast<size_t>(n_tok) * (1 + M) * (d / columns));
     if (own_v) w.f.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
   }
-  if (i8 && n_tok > 0) {
+  if (i8 && n_tok > 0 && !gathers_i8(L)) {
     if (fused) {   // rows of codes, aligned as they are, at every size
       w.codes.codes = c.take<int8_t>(static_cast<size_t>(n_tok) * d_mem);
       w.codes.scale = c.take<float>(static_cast<size_t>(n_tok));
@@ -1419,10 +1430,11 @@ engram_status forward_draft(const char* who, const int32_t* tokens, void* H, int
     w.f.gamma = draft->gamma;
   }
   prof_begin();
-  // the int8 product reads the rows in hdtype, also where the layer has MXFP8 weights
-  r = run_retrieve(tokens, B, T, L, ha, ta, g.hdtype, st, w.e, stream, w8 != nullptr ? static_cast<int>(g.hdtype) : -1);
+  const bool in_rows = gathers_i8(L);
+  // the int8 product reads codes or rows in hdtype, also where the layer has MXFP8 weights
+  r = run_retrieve(tokens, B, T, L, ha, ta, g.hdtype, st, w.e, stream, w8 == nullptr ? -1 : in_rows ? engram::kGatherOutI8Rows : static_cast<int>(g.hdtype));
   if (r != ENGRAM_OK) return r;
-  const Int8Step i8{w8, w.codes};
+  const Int8Step i8{w8, w.codes, in_rows};
   return run_compute(tokens, w.e, H, B, T, L, g, st, alpha_out, y_out, w.f, stream, nullptr, w8 != nullptr ? &i8 : nullptr,
                      draft == nullptr);
 }

@@ -124,6 +124,11 @@ constexpr int kGatherOutMXFP8 = 3;
 // multiple of 32; the last block is whole, its rows past the last token left
 // unwritten.
 constexpr int kGatherOutFrag16 = 4;
+// Rows as 8-bit integers for the int8 product: codes [n_tok][d_mem], then the
+// row scales float32 [n_tok].  For rows that 64, 128 or 256 threads of the
+// gather hold (gather_i8_rows).
+constexpr int kGatherOutI8Rows = 5;
+inline bool gather_i8_rows(int64_t d_mem) { return d_mem == 512 || d_mem == 1024 || d_mem == 2048; }
 
 hipError_t launch_gather(const int32_t* z, int64_t n_tok, const TableArgs& ta, int out_dtype,
                          void* e, hipStream_t s);

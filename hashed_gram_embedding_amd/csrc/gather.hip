@@ -26,6 +26,12 @@
 // its order; on a hit it copies its 8 elements from the n-gram's hot row
 // (head k of order n covers columns k*dim .. k*dim+dim-1 of that row) and
 // reads no cold row.
+//
+// For the int8 product the rows leave as codes with one scale a token: where a
+// token's threads are whole wavefronts of one workgroup (d_mem 512, 1024 or
+// 2048) its largest magnitude is found in the registers and LDS, and no launch
+// reads the rows again to quantise them (4096 tokens: gather 4.9 and
+// quantisation 5.1 us, together here 6.3; 256 tokens: 4.1 and 4.1, here 4.2).
 #include "gather_device.h"
 
 namespace engram {
@@ -150,6 +156,10 @@ hipError_t launch_hashed(int64_t n_tok, const TableArgs& ta, int out, void* e, c
   if (n_tok == 0) return hipSuccess;
   if (out == kOutMXFP8) return launch_hashed_items<IN, kOutMXFP8, HOT>(n_tok, ta, e, hs, s);
   if (out == kOutFrag16) return launch_hashed_items<IN, kOutFrag16, HOT>(n_tok, ta, e, hs, s);
+  if (out == kOutI8Rows) {
+    if (!gather_i8_rows(static_cast<int64_t>(ta.n_tables) * ta.dim)) return hipErrorInvalidValue;
+    return launch_hashed_items<IN, kOutI8Rows, HOT>(n_tok, ta, e, hs, s);
+  }
   if (out == ENGRAM_BF16) return launch_hashed_items<IN, ENGRAM_BF16, HOT>(n_tok, ta, e, hs, s);
   return launch_hashed_items<IN, ENGRAM_F32, HOT>(n_tok, ta, e, hs, s);
 }

@@ -9,11 +9,13 @@
 #include "engram_internal.h"
 #include "hash_device.h"
 #include "hot_device.h"
+#include "int8_device.h"
 
 namespace engram {
 
 constexpr int kOutMXFP8 = kGatherOutMXFP8;
 constexpr int kOutFrag16 = kGatherOutFrag16;
+constexpr int kOutI8Rows = kGatherOutI8Rows;
 
 template <int IN>
 __device__ __forceinline__ void load8(const void* base, const float* scale, int64_t row, int dim,
@@ -86,6 +88,48 @@ __device__ __forceinline__ void store8(void* e, int64_t out, int64_t mx_scale_ba
   }
 }
 
+// Rows as 8-bit integers: the codes of the bf16 rows that the bf16 product
+// would read (as engram_quantize_i8 of them), then the scales.  `waves`
+// wavefronts hold a row, 8 of its values a thread; their maxima meet in LDS.
+template <int IN, int ITEMS>
+__device__ __forceinline__ void store_i8_rows(void* e, uint32_t g, uint32_t jc, uint32_t waves, uint32_t n_tok, int64_t dm,
+                                              const float (&f)[ITEMS][8], const bool (&live)[ITEMS]) {
+  __shared__ uint32_t part[ITEMS][4];
+  const uint32_t wave = threadIdx.x >> 6;
+  float x[ITEMS][8];
+#pragma unroll
+  for (int q = 0; q < ITEMS; ++q) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if constexpr (IN == ENGRAM_BF16) {
+        x[q][i] = f[q][i];
+        x[q][i + 1] = f[q][i + 1];
+      } else {
+        const uint32_t b = pack_bf16x2(f[q][i], f[q][i + 1]);
+        x[q][i] = __uint_as_float(b << 16);
+        x[q][i + 1] = __uint_as_float(b & 0xffff0000u);
+      }
+      top = max(top, max(magnitude(x[q][i]), magnitude(x[q][i + 1])));
+    }
+    part[q][wave] = wave_top(top);
+  }
+  __syncthreads();
+  const uint32_t first = wave & ~(waves - 1);   // 1, 2 or 4 wavefronts a row
+#pragma unroll
+  for (int q = 0; q < ITEMS; ++q) {
+    uint32_t top = part[q][first];
+    if (waves > 1) top = max(top, part[q][first + 1]);
+    if (waves > 2) top = max(top, max(part[q][2], part[q][3]));
+    const u32x2_t w = row_has_codes(top) ? quantize8(x[q], row_factors(__uint_as_float(top))) : u32x2_t{0, 0};
+    const int64_t tok = static_cast<int64_t>(g) * ITEMS + q;
+    if (live[q]) {
+      *reinterpret_cast<u32x2_t*>(static_cast<int8_t*>(e) + tok * dm + jc * 8) = w;
+      if (jc == 0) reinterpret_cast<float*>(static_cast<int8_t*>(e) + n_tok * dm)[tok] = row_scale(top);
+    }
+  }
+}
+
 // Steps 1-4 with in-thread hashing; ITEMS consecutive tokens per thread.
 // Thread gid serves tokens ITEMS*g .. ITEMS*g + ITEMS-1 of table j, chunk c,
 // with (g, j, c) = gid split as [groups][n_tables][chunks]; a wavefront's
@@ -119,7 +163,9 @@ __device__ __forceinline__ void hashed_gather_body(uint32_t gid, uint32_t n_tok,
   const uint32_t chunks = static_cast<uint32_t>(ta.dim) >> 3;
   const uint32_t per_group = nt * chunks;
   const uint32_t n_groups = (n_tok + ITEMS - 1) / ITEMS;
-  if (gid >= n_groups * per_group) return;
+  if constexpr (OUT != kOutI8Rows) {   // (there the workgroup meets at a barrier: no thread leaves, tokens past the last are not stored)
+    if (gid >= n_groups * per_group) return;
+  }
   const uint32_t g = gid / per_group;
   const uint32_t jc = gid - g * per_group;
   const int j = static_cast<int>(jc / chunks);
@@ -233,6 +279,11 @@ __device__ __forceinline__ void hashed_gather_body(uint32_t gid, uint32_t n_tok,
       if (live[q] && !(HOT && hot[q] >= 0)) atomicAdd(ta.counts + crow[q], 1u);
   }
   const int64_t dm = static_cast<int64_t>(nt) * ta.dim;
+  if constexpr (OUT == kOutI8Rows) {
+    // a token's threads are whole wavefronts of this workgroup (launcher)
+    store_i8_rows<IN, ITEMS>(e, g, jc, per_group >> 6, n_tok, dm, f, live);
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < ITEMS; ++q) {
     const int64_t tok = static_cast<int64_t>(g) * ITEMS + q;

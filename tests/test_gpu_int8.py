@@ -204,6 +204,26 @@ def test_layer_forms(config, kw):
     check_bf16_layer(to_f64(alpha), ref["alpha"], to_f64(y), ref["Y"], to_f64(H), orc.bf16_to_f64(w.H), tag=f"int8 {config} {kw}")
 
 
+@pytest.mark.parametrize("config,kw", [(1, dict(B=3, T=37)), (1, dict(B=1, T=700, heads=4)), (1, dict(B=2, T=5, heads=16)),
+                                       (1, dict(B=3, T=11, heads=5, table_dim=32)), (3, dict(B=9, T=1, layers=1)),
+                                       (3, dict(B=40, T=130, layers=1)), (1, dict(B=1, T=4097))])
+def test_layer_rows_are_quantised_exactly(config, kw):
+    """v of the int8 layer is engram_project_i8 of engram_quantize_i8 of the
+    gathered rows, bit for bit, where the gather writes the codes and where not."""
+    log(f"int8 rows {config} {kw}")
+    w, lay, L, w8 = _layer_case(config, "bf16", **kw)
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    B, T = tok.shape
+    e = torch.empty((B * T, L.d_mem), dtype=torch.bfloat16, device=DEV)
+    eg.retrieve(tok, L, e)
+    q, s = eg.quantize_i8(e)
+    want = eg.project_i8(q, w8.q[:lay.d], w8.scale[:lay.d], e_scale=s, out_dtype="f32")
+    draft = eg.Draft(B, T, L, DEV, w8=w8)
+    st = eg.DecodeState(B, 3, lay.branches, 9, lay.d, DEV)
+    eg.forward_draft(tok, eg.to_device(w.H, "bf16", DEV), L, st, draft, w8=w8)
+    assert torch.equal(draft.v[:, :lay.d], want)
+
+
 def test_layer_decode_state():
     """A prefill and single-token steps with the int8 layer against the oracle run over the same chunks."""
     log("forward_i8 decode")
