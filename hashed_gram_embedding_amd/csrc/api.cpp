@@ -1308,7 +1308,7 @@ ENGRAM_API engram_status engram_quantize_i8(const void* x, engram_dtype dtype, i
 }
 
 ENGRAM_API size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, int64_t n_out, engram_dtype e_dtype) {
-  if (n_tok < 1 || d_mem < 1 || d_mem > 131071 || n_out < 1) return 0;
+  if (n_tok < 1 || d_mem < 1 || d_mem > 131071 || n_out < 1 || n_tok > INT32_MAX || n_out > INT32_MAX) return 0;
   Carve c{nullptr};
   carve_codes(c, e_dtype, n_tok, d_mem, n_out);
   return c.used;
@@ -1382,6 +1382,7 @@ DraftWorkspace carve_draft(Carve& c, int64_t n_tok, const engram_layer* L, bool 
 
 size_t draft_ws_bytes(int64_t B, int64_t T, const engram_layer* L, bool i8, bool own_v) {
   if (L == nullptr || B < 0 || T < 0 || L->gc.branches < 1 || L->gc.d < 1 || L->tables.n_tables < 1 || L->tables.dim < 1) return 0;
+  if (B > 65535 || T > INT32_MAX) return 0;   // refused by the calls
   Carve c{nullptr};
   carve_draft(c, B * T, L, i8, own_v);
   return c.used;
@@ -1501,7 +1502,7 @@ ENGRAM_API engram_status engram_commit_draft(const int32_t* tokens, int64_t B, i
 }
 
 ENGRAM_API size_t engram_token_probs_workspace(int64_t rows, int64_t V) {
-  if (rows < 1 || V < 1) return 0;
+  if (rows < 1 || V < 1 || rows > INT32_MAX || V > INT32_MAX) return 0;
   return align_up(engram::probs_workspace(rows, V));
 }
 
@@ -1529,7 +1530,7 @@ ENGRAM_API engram_status engram_token_probs(const void* logits, engram_dtype dty
 }
 
 ENGRAM_API size_t engram_verify_drafts_workspace(int64_t S, int64_t V) {
-  if (S < 1 || V < 1) return 0;
+  if (S < 1 || V < 1 || S > 65535 || V > INT32_MAX) return 0;
   return align_up(engram::verify_workspace(S, V));
 }
 
