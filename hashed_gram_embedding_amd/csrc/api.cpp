@@ -598,10 +598,13 @@ CodeSpace carve_codes(Carve& c, int e_dtype, int64_t n_tok, int64_t d_mem, int64
   return s;
 }
 
-// Codes of the rows e, in the aligned layout, into cs.
-engram_status run_quantize(const void* e, int e_dtype, int64_t n_tok, int64_t d_mem, const CodeSpace& cs, hipStream_t stream) {
+// Codes of the rows e, in the aligned layout, into cs, and W's aligned copy
+// where cs has one.
+engram_status run_quantize(const void* e, int e_dtype, int64_t n_tok, int64_t d_mem, const CodeSpace& cs, const int8_t* w,
+                           int64_t n_out, hipStream_t stream) {
   prof_mark(stream, "quantize_i8_kernel");
-  return hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, cs.codes, engram::i8_row_stride(d_mem), true, cs.scale, stream),
+  return hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, cs.codes, engram::i8_row_stride(d_mem), true, cs.scale, w,
+                                               n_out, cs.w, stream),
                     "quantize_i8 launch");
 }
 
@@ -610,20 +613,18 @@ engram_status run_project_i8(const void* e, int e_dtype, const float* e_scale, c
                              int64_t n_tok, int64_t d_mem, int64_t n_out, int out_dtype, void* out, const CodeSpace& cs,
                              hipStream_t stream) {
   engram_status r = ENGRAM_OK;
-  const bool quantize = cs.scale != nullptr;
-  if (quantize) {
-    r = run_quantize(e, e_dtype, n_tok, d_mem, cs, stream);
+  if (cs.scale != nullptr) {
+    r = run_quantize(e, e_dtype, n_tok, d_mem, cs, w, n_out, stream);
     if (r != ENGRAM_OK) return r;
     e_dtype = ENGRAM_I8;
     e_scale = cs.scale;
-  }
-  if (cs.w != nullptr) {
+  } else if (cs.w != nullptr) {
     prof_mark(stream, "align_rows_kernel");
-    r = hip_status(engram::launch_align_i8(w, n_out, cs.w, static_cast<const int8_t*>(e), quantize ? 0 : n_tok, cs.codes, d_mem, stream),
+    r = hip_status(engram::launch_align_i8(w, n_out, cs.w, static_cast<const int8_t*>(e), n_tok, cs.codes, d_mem, stream),
                    "align_rows launch");
     if (r != ENGRAM_OK) return r;
-    w = cs.w;
   }
+  if (cs.w != nullptr) w = cs.w;
   if (cs.codes != nullptr) e = cs.codes;
   const int64_t ldq = cs.codes != nullptr ? engram::i8_row_stride(d_mem) : d_mem;
   prof_mark(stream, "project_i8_kernel");
@@ -714,7 +715,7 @@ engram_status run_compute(const int32_t* tokens, const void* e, void* H, int64_t
     const int8_t* codes = i8->in_rows ? static_cast<const int8_t*>(e) : i8->space.codes;
     const float* scale = i8->in_rows ? reinterpret_cast<const float*>(codes + n_tok * d_mem) : i8->space.scale;
     if (!i8->in_rows) {
-      r = run_quantize(e, g.hdtype, n_tok, d_mem, i8->space, stream);
+      r = run_quantize(e, g.hdtype, n_tok, d_mem, i8->space, nullptr, 0, stream);
       if (r != ENGRAM_OK) return r;
     }
     const int q = d / engram::project_i8_gate_columns(n_tok, d_mem, d, M);
@@ -1304,7 +1305,7 @@ ENGRAM_API engram_status engram_quantize_i8(const void* x, engram_dtype dtype, i
     return fail(ENGRAM_EINVAL, "quantize_i8: x and scale must be aligned to their elements");
   prof_begin();
   prof_mark(stream, "quantize_i8_kernel");
-  return hip_status(engram::launch_quantize_i8(x, dtype, rows, cols, q, cols, false, scale, stream), "quantize_i8 launch");
+  return hip_status(engram::launch_quantize_i8(x, dtype, rows, cols, q, cols, false, scale, nullptr, 0, nullptr, stream), "quantize_i8 launch");
 }
 
 ENGRAM_API size_t engram_project_i8_workspace(int64_t n_tok, int64_t d_mem, int64_t n_out, engram_dtype e_dtype) {

@@ -334,9 +334,10 @@ hipError_t launch_state_commit(const void* v, int64_t v_stride, int vdtype, int6
 int64_t i8_row_stride(int64_t cols);
 // Rows to int8 codes [rows][ldq] and scales.  tail: a last run of 16 columns
 // that is not whole is stored right-aligned in its 16 bytes, zeros before it
-// (ldq = i8_row_stride(cols)); otherwise the rows are plain.
-hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail,
-                              float* scale, hipStream_t s);
+// (ldq = i8_row_stride(cols)); otherwise the rows are plain.  w_out: W's rows
+// of `cols` into that layout in the same launch, or null.
+hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail, float* scale,
+                              const int8_t* w, int64_t w_rows, int8_t* w_out, hipStream_t s);
 // Whether the product of float rows quantises them itself (few rows that fit
 // in LDS); otherwise launch_quantize_i8 comes first.
 bool project_i8_quantizes(int64_t n_tok, int64_t K);
@@ -345,7 +346,7 @@ bool project_i8_quantizes(int64_t n_tok, int64_t K);
 // aligned chunks.
 bool project_i8_aligns(int64_t n_tok, int64_t K);
 hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
-                           hipStream_t s);   // q_rows = 0: W alone
+                           hipStream_t s);
 // Product with W (aligned if it has to be) of int8 codes [n_tok][ldq] (tailed: in the layout above; with
 // q_scale) or, where project_i8_quantizes, of float rows [n_tok][K].
 hipError_t launch_project_i8(const void* e, int e_dtype, int64_t ldq, bool tailed, const float* q_scale, const int8_t* w,

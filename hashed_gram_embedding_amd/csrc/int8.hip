@@ -63,10 +63,9 @@ struct CodeRow {
 // last run are the first lanes' own.  A row of zeros has scale 0, one holding
 // an infinity or a NaN codes 0 and scale NaN.
 template <int DT, int N>
-__global__ void __launch_bounds__(256)
-quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ q, int64_t ldq, int tail,
-                     float* __restrict__ scale) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), base = row * cols;
+__device__ __forceinline__ void quantize_rows(int64_t group, const void* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ q,
+                                              int64_t ldq, int tail, float* __restrict__ scale) {
+  const int64_t row = group * 4 + (threadIdx.x >> 6), base = row * cols;
   const int lane = threadIdx.x & 63, c8 = cols / 8 * 8, ct = c8 + lane;
   if (row >= rows) return;
   float f[N][8];
@@ -104,11 +103,10 @@ quantize_rows_kernel(const void* __restrict__ x, int64_t rows, int cols, int8_t*
 // Longer rows: one workgroup a row, which reads it twice (the second time
 // from the L2).
 template <int DT>
-__global__ void __launch_bounds__(256)
-quantize_long_kernel(const void* __restrict__ x, int cols, int8_t* __restrict__ q, int64_t ldq, int tail,
-                     float* __restrict__ scale) {
+__device__ __forceinline__ void quantize_long(int64_t row, const void* __restrict__ x, int cols, int8_t* __restrict__ q, int64_t ldq,
+                                              int tail, float* __restrict__ scale) {
   __shared__ uint32_t part[4];
-  const int64_t row = blockIdx.x, base = row * cols;
+  const int64_t base = row * cols;
   const int t = threadIdx.x, c8 = cols / 8 * 8, ct = c8 + t;
   const float ft = ct < cols ? load1<DT>(x, base + ct) : 0.f;
   uint32_t top = magnitude(ft);
@@ -200,11 +198,8 @@ struct AlignJob {
   int64_t groups;    // workgroups: rows * chunks / (256 kAlignItems), rounded up
 };
 
-__global__ void __launch_bounds__(256)
-align_rows_kernel(AlignJob a, AlignJob b, int K, int chunks) {
-  const bool first = blockIdx.x < a.groups;
-  const AlignJob& j = first ? a : b;
-  const int64_t n = j.rows * chunks, base = (blockIdx.x - (first ? 0 : a.groups)) * 256 * kAlignItems;
+__device__ __forceinline__ void align_rows(const AlignJob& j, int64_t group, int K, int chunks) {
+  const int64_t n = j.rows * chunks, base = group * 256 * kAlignItems;
   const int64_t row0 = base / chunks, id0 = base + threadIdx.x;
   const uint32_t c0 = static_cast<uint32_t>(base - row0 * chunks) + threadIdx.x, width = static_cast<uint32_t>(chunks);
   const int8_t* const end = j.x + j.rows * K;
@@ -234,6 +229,41 @@ align_rows_kernel(AlignJob a, AlignJob b, int K, int chunks) {
     const u32x4_t none{0, 0, 0, 0};
     if (id0 + i * 256 < n) j.y[id0 + i * 256] = keep[i] == 2 ? x : keep[i] == 1 ? x & tail_mask(K) : none;
   }
+}
+
+__global__ void __launch_bounds__(256)
+align_rows_kernel(AlignJob a, AlignJob b, int K, int chunks) {
+  const bool first = blockIdx.x < a.groups;
+  align_rows(first ? a : b, blockIdx.x - (first ? 0 : a.groups), K, chunks);
+}
+
+// Rows to codes, one wavefront a row (N > 0) or one workgroup (N = 0).  ALIGN:
+// the first workgroups copy W's odd rows, which nothing here reads, so the
+// product waits for one launch instead of two (55 x 2271 x 1676 18.0 -> 15.6 us, 2000 x
+// 4099 x 2000 44.6 -> 41.0).
+struct QuantizeArgs {
+  const void* x;
+  int64_t rows;
+  int8_t* q;
+  int64_t ldq;
+  float* scale;
+  int cols;
+  int tail;
+};
+
+template <int DT, int N, bool ALIGN>
+__global__ void __launch_bounds__(256)
+quantize_rows_kernel(QuantizeArgs a, AlignJob w, int chunks) {
+  int64_t group = blockIdx.x;
+  if constexpr (ALIGN) {
+    if (group < w.groups) {
+      align_rows(w, group, a.cols, chunks);
+      return;
+    }
+    group -= w.groups;
+  }
+  if constexpr (N > 0) quantize_rows<DT, N>(group, a.x, a.rows, a.cols, a.q, a.ldq, a.tail, a.scale);
+  else quantize_long<DT>(group, a.x, a.cols, a.q, a.ldq, a.tail, a.scale);
 }
 
 template <typename OutT>
@@ -1020,23 +1050,42 @@ int64_t i8_row_stride(int64_t cols) {
   return cols % 16 == 0 ? cols : (cols + whole - 1) / whole * whole;
 }
 
-template <int DT>
-void launch_quantize_dt(const void* x, int64_t rows, int cols, int8_t* q, int64_t ldq, int tail, float* scale, hipStream_t s) {
-  const dim3 wide(static_cast<unsigned>((rows + 3) / 4));
-  // the fewest registers that hold a row
-  if (cols < 512 + 8) launch_k((quantize_rows_kernel<DT, 1>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
-  else if (cols < 1024 + 8) launch_k((quantize_rows_kernel<DT, 2>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
-  else if (cols < 2048 + 8) launch_k((quantize_rows_kernel<DT, 4>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
-  else if (cols < 4096 + 8) launch_k((quantize_rows_kernel<DT, 8>), wide, dim3(256), 0, s, x, rows, cols, q, ldq, tail, scale);
-  else launch_k(quantize_long_kernel<DT>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, x, cols, q, ldq, tail, scale);
+namespace {
+
+AlignJob align_job(const int8_t* x, int8_t* y, int64_t rows, int64_t K) {
+  const int64_t per = 256 * kAlignItems;
+  return AlignJob{x, reinterpret_cast<u32x4_t*>(y), rows, (rows * (i8_row_stride(K) / 16) + per - 1) / per};
 }
 
-hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail,
-                              float* scale, hipStream_t s) {
-  if (rows == 0) return hipSuccess;
-  if (dtype == ENGRAM_BF16) launch_quantize_dt<ENGRAM_BF16>(x, rows, static_cast<int>(cols), q, ldq, tail ? 1 : 0, scale, s);
-  else launch_quantize_dt<ENGRAM_F32>(x, rows, static_cast<int>(cols), q, ldq, tail ? 1 : 0, scale, s);
+template <int DT, int N>
+hipError_t launch_quantize_n(const QuantizeArgs& a, const AlignJob& w, hipStream_t s) {
+  const int64_t groups = w.groups + (N > 0 ? (a.rows + 3) / 4 : a.rows);
+  if (groups > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(groups));
+  const int chunks = static_cast<int>(i8_row_stride(a.cols) / 16);
+  if (w.groups > 0) launch_k((quantize_rows_kernel<DT, N, true>), grid, dim3(256), 0, s, a, w, chunks);
+  else launch_k((quantize_rows_kernel<DT, N, false>), grid, dim3(256), 0, s, a, w, chunks);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_quantize_dt(const QuantizeArgs& a, const AlignJob& w, hipStream_t s) {
+  // the fewest registers that hold a row
+  if (a.cols < 512 + 8) return launch_quantize_n<DT, 1>(a, w, s);
+  if (a.cols < 1024 + 8) return launch_quantize_n<DT, 2>(a, w, s);
+  if (a.cols < 2048 + 8) return launch_quantize_n<DT, 4>(a, w, s);
+  if (a.cols < 4096 + 8) return launch_quantize_n<DT, 8>(a, w, s);
+  return launch_quantize_n<DT, 0>(a, w, s);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_i8(const void* x, int dtype, int64_t rows, int64_t cols, int8_t* q, int64_t ldq, bool tail, float* scale,
+                              const int8_t* w, int64_t w_rows, int8_t* w_out, hipStream_t s) {
+  if (rows == 0) return hipSuccess;
+  const QuantizeArgs a{x, rows, q, ldq, scale, static_cast<int>(cols), tail ? 1 : 0};
+  const AlignJob job = w_out != nullptr ? align_job(w, w_out, w_rows, cols) : AlignJob{};
+  return dtype == ENGRAM_BF16 ? launch_quantize_dt<ENGRAM_BF16>(a, job, s) : launch_quantize_dt<ENGRAM_F32>(a, job, s);
 }
 
 namespace {
@@ -1053,12 +1102,10 @@ bool project_i8_aligns(int64_t n_tok, int64_t K) { return K >= 16 && K % 16 != 0
 
 hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
                            hipStream_t s) {
-  const int64_t chunks = i8_row_stride(K) / 16, per = 256 * kAlignItems;
-  const int64_t wg = (w_rows * chunks + per - 1) / per, qg = (q_rows * chunks + per - 1) / per;
-  if (wg + qg > INT32_MAX) return hipErrorInvalidValue;
-  launch_k(align_rows_kernel, dim3(static_cast<unsigned>(wg + qg)), dim3(256), 0, s,
-           AlignJob{w, reinterpret_cast<u32x4_t*>(w_out), w_rows, wg}, AlignJob{q, reinterpret_cast<u32x4_t*>(q_out), q_rows, qg},
-           static_cast<int>(K), static_cast<int>(chunks));
+  const AlignJob a = align_job(w, w_out, w_rows, K), b = align_job(q, q_out, q_rows, K);
+  if (a.groups + b.groups > INT32_MAX) return hipErrorInvalidValue;
+  launch_k(align_rows_kernel, dim3(static_cast<unsigned>(a.groups + b.groups)), dim3(256), 0, s, a, b, static_cast<int>(K),
+           static_cast<int>(i8_row_stride(K) / 16));
   return hipGetLastError();
 }
 
