@@ -1454,7 +1454,7 @@ ENGRAM_API engram_status engram_forward_i8(const int32_t* tokens, void* H, int64
   return forward_draft("forward_i8", tokens, H, B, T, L, w, st, nullptr, alpha_out, y_out, ws, ws_bytes, stream);
 }
 
-ENGRAM_API int64_t engram_draft_stride(const engram_layer* L, const engram_i8_weights* w) {
+ENGRAM_API int64_t engram_draft_stride(const engram_layer* L) {
   if (L == nullptr || L->gc.branches < 1) return 0;
   return use_fused(L) ? L->gc.d : static_cast<int64_t>(1 + L->gc.branches) * L->gc.d;
 }
@@ -1471,9 +1471,9 @@ ENGRAM_API engram_status engram_forward_draft(const int32_t* tokens, void* H, in
   if (L == nullptr) return fail(ENGRAM_EINVAL, "layer is NULL");
   const engram_status r = check_draft("forward_draft", draft);
   if (r != ENGRAM_OK) return r;
-  if (draft->v_stride != engram_draft_stride(L, w))
+  if (draft->v_stride != engram_draft_stride(L))
     return fail(ENGRAM_EINVAL, "forward_draft: v_stride must be engram_draft_stride() = %lld",
-                static_cast<long long>(engram_draft_stride(L, w)));
+                static_cast<long long>(engram_draft_stride(L)));
   engram_decode_state view = *st;   // read only: no commit follows
   return forward_draft("forward_draft", tokens, H, B, T, L, w, &view, draft, alpha_out, y_out, ws, ws_bytes, stream);
 }

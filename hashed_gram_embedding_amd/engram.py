@@ -157,7 +157,7 @@ def load_library(path: str) -> ctypes.CDLL:
         "engram_forward_i8_workspace": (sz, [i64, i64, ctypes.POINTER(LayerStruct)]),
         "engram_forward_i8": (i32, [vp, vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct),
                                     ctypes.POINTER(DecodeStateStruct), vp, vp, vp, sz, vp]),
-        "engram_draft_stride": (i64, [ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct)]),
+        "engram_draft_stride": (i64, [ctypes.POINTER(LayerStruct)]),
         "engram_forward_draft_workspace": (sz, [i64, i64, ctypes.POINTER(LayerStruct),
                                                 ctypes.POINTER(I8WeightsStruct)]),
         "engram_forward_draft": (i32, [vp, vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(I8WeightsStruct),
@@ -756,9 +756,9 @@ class Draft:
     """The buffers that forward_draft fills and commit_draft reads (engram_draft):
     v float32 [B*T, stride] and gamma float32 [B*T, M], allocated unless given."""
 
-    def __init__(self, B: int, T: int, layer: Layer, device="cuda", w8: Optional[Int8Weights] = None,
-                 v: Optional[torch.Tensor] = None, gamma: Optional[torch.Tensor] = None):
-        stride = int(lib().engram_draft_stride(ctypes.byref(layer.s), None if w8 is None else ctypes.byref(w8.s)))
+    def __init__(self, B: int, T: int, layer: Layer, device="cuda", v: Optional[torch.Tensor] = None,
+                 gamma: Optional[torch.Tensor] = None):
+        stride = int(lib().engram_draft_stride(ctypes.byref(layer.s)))
         self.B, self.T = B, T
         self.v = torch.empty((B * T, stride), dtype=torch.float32, device=device) if v is None else v
         self.gamma = torch.empty((B * T, layer.M), dtype=torch.float32, device=device) if gamma is None else gamma

@@ -532,10 +532,10 @@ typedef struct engram_draft {
  * the sequences continue from st, which is only read.  H, alpha_out and y_out
  * are those of the forward call, bit for bit.  engram_commit_draft then
  * advances st by the tokens that are kept.
- * engram_draft_stride: columns of a row of draft->v (w NULL or not).
+ * engram_draft_stride: columns of a row of draft->v.
  * ws: engram_forward_draft_workspace() bytes, 256-byte aligned; it need not
  * outlive the call's kernels. */
-int64_t engram_draft_stride(const engram_layer* L, const engram_i8_weights* w);
+int64_t engram_draft_stride(const engram_layer* L);
 size_t engram_forward_draft_workspace(int64_t B, int64_t T, const engram_layer* L, const engram_i8_weights* w);
 engram_status engram_forward_draft(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
                                    const engram_i8_weights* w, const engram_decode_state* st,

@@ -65,7 +65,7 @@ def test_draft_then_commit_equals_forward(config, hdtype, S, T, int8):
     h_ref = H[:, 12:].clone(memory_format=torch.contiguous_format)
     a_ref, y_ref = run(chunk, h_ref, ref_st, want_alpha=True, want_y=True)
 
-    draft = eg.Draft(S, T, L, DEV, w8=w8)
+    draft = eg.Draft(S, T, L, DEV)
     h = H[:, 12:].clone(memory_format=torch.contiguous_format)
     a, y = eg.forward_draft(chunk, h, L, st, draft, w8=w8, want_alpha=True, want_y=True)
     assert _same(h, h_ref) and _same(a, a_ref) and _same(y, y_ref)
@@ -210,7 +210,7 @@ class _Decoder:
         H = self.emb[tok.long()].view(self.S, tok.shape[1], 1, self.d).contiguous()
         drafts = []
         for L, w8, st in zip(self.layers, self.w8, states):
-            drafts.append(eg.Draft(self.S, tok.shape[1], L, DEV, w8=w8))
+            drafts.append(eg.Draft(self.S, tok.shape[1], L, DEV))
             eg.forward_draft(tok, H, L, st, drafts[-1], w8=w8)
         return self.logits(H), drafts
 

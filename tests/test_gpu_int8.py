@@ -218,7 +218,7 @@ def test_layer_rows_are_quantised_exactly(config, kw):
     eg.retrieve(tok, L, e)
     q, s = eg.quantize_i8(e)
     want = eg.project_i8(q, w8.q[:lay.d], w8.scale[:lay.d], e_scale=s, out_dtype="f32")
-    draft = eg.Draft(B, T, L, DEV, w8=w8)
+    draft = eg.Draft(B, T, L, DEV)
     st = eg.DecodeState(B, 3, lay.branches, 9, lay.d, DEV)
     eg.forward_draft(tok, eg.to_device(w.H, "bf16", DEV), L, st, draft, w8=w8)
     assert torch.equal(draft.v[:, :lay.d], want)
