@@ -224,6 +224,39 @@ def test_layer_rows_are_quantised_exactly(config, kw):
     assert torch.equal(draft.v[:, :lay.d], want)
 
 
+@pytest.mark.parametrize("kw", [dict(B=3, T=50), dict(B=2, T=900)])
+def test_layer_rows_of_a_hot_tier_and_beside_mxfp8(kw):
+    """Rows from an Engram-Nine hot tier leave the gather as exact codes too, and
+    a layer that also has MXFP8 weights gives the same int8 results."""
+    log(f"int8 rows, hot tier {kw}")
+    from test_gpu_hot import hot_sets
+    w = inputs.make_config(1, rows_per_table=997, **kw)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV, mxfp8=True)
+    w8 = eg.Int8Weights(L)
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    B, T = tok.shape
+    plain = eg.Layer(lay, "bf16", DEV)
+    outs = []
+    for layer in (L, plain):
+        H = eg.to_device(w.H, "bf16", DEV)
+        eg.forward_i8(tok, H, layer, w8)
+        outs.append(H)
+    assert torch.equal(outs[0], outs[1])
+
+    _, hot = hot_sets(w, lay, 40, seed=3)
+    plain.set_hot(hot)
+    e = torch.empty((B * T, L.d_mem), dtype=torch.bfloat16, device=DEV)
+    eg.retrieve(tok, plain, e)
+    q, s = eg.quantize_i8(e)
+    draft = eg.Draft(B, T, plain, DEV)
+    st = eg.DecodeState(B, 3, lay.branches, 9, lay.d, DEV)
+    H = eg.to_device(w.H, "bf16", DEV)
+    eg.forward_draft(tok, H, plain, st, draft, w8=w8)
+    assert torch.equal(draft.v[:, :lay.d], eg.project_i8(q, w8.q[:lay.d], w8.scale[:lay.d], e_scale=s, out_dtype="f32"))
+    assert not torch.equal(H, outs[1])          # the tier's rows differ from the tables'
+
+
 def test_layer_decode_state():
     """A prefill and single-token steps with the int8 layer against the oracle run over the same chunks."""
     log("forward_i8 decode")
