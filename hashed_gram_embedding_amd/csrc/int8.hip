@@ -505,6 +505,10 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
     const float* sq = sc + par * (TF + TT) + TF + wt * (TT / WT);
     constexpr int EPC = 16 / static_cast<int>(sizeof(OutT));   // outputs of a chunk
     const int64_t fw = cur.f0 + wf * (TF / WF);
+    // every output of the wavefront is one of the product's: its first chunk
+    // of each block, rows apart by a stride that all lanes share
+    const bool inside = !GATE && fw + TF / WF <= a.n_out && cur.t0 + (wt + 1) * (TT / WT) <= a.n_tok;
+    OutT* const first = static_cast<OutT*>(a.out) + (cur.t0 + wt * (TT / WT) + lane / RC) * a.n_out + fw + lane % RC * EPC;
     // GATE: this wavefront's columns are v's, or one branch's keys
     const bool is_v = GATE && fw < a.d;
     const int branch = GATE && !is_v ? static_cast<int>(fw / a.d) - 1 : 0;
@@ -545,6 +549,19 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
         v[it] = E[rr * RC + (c ^ (rr & 7))];
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and read, before the next block's writes
+      if constexpr (!GATE) {
+        if (inside) {
+#pragma unroll
+          for (int it = 0; it < NIT; ++it) {
+            OutT* dst = first + (j * 32 + it * (64 / RC)) * a.n_out;
+            if (TF * TT >= 65536 && stream)
+              __builtin_nontemporal_store(v[it], reinterpret_cast<u32x4_any_t*>(dst));
+            else
+              __builtin_memcpy(dst, &v[it], 16);
+          }
+          continue;
+        }
+      }
 #pragma unroll
       for (int it = 0; it < NIT; ++it) {
         const int rr = (it * 64 + lane) / RC, c = (it * 64 + lane) % RC;
