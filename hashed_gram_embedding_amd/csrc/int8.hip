@@ -434,6 +434,13 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    i32x4_t fa[2][I], fb[2][J];   // operands of two steps of 32 columns
+    auto multiply = [&](int set) {
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[set][i], fb[set][j], acc[i][j], 0, 0, 0);
+    };
     for (int kt = 0; kt < ksteps; ++kt) {
       // this lane's part of the slice has landed and its reads of the other
       // buffer are done; after the barrier, every lane's
@@ -446,9 +453,6 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
       }
       const u32x4_t* Ws = lds + buf * (WC + QC);
       const u32x4_t* Qs = Ws + WC;
-      // The operands of step ks + 1 are read while step ks multiplies: one
-      // LDS read behind each of the first products.
-      i32x4_t fa[2][I], fb[2][J];
       auto operands = [&](int set, int ks) {
         const int kc = (ks * 2 + lh) ^ ((lr >> 1) & 7);
 #pragma unroll
@@ -457,19 +461,20 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
         for (int j = 0; j < J; ++j) fb[set][j] = __builtin_bit_cast(i32x4_t, Qs[(wt * (TT / WT) + j * 32 + lr) * 8 + kc]);
       };
       if constexpr (kWhole) {
+        // The operands of step ks + 1 are read while step ks multiplies, one
+        // LDS read behind each of the first products; those of a slice's first
+        // step while the last step of the slice before multiplies, which so
+        // waits behind the barrier (32763 x 1024 x 5120 191 -> 183 us, 32763 x 128 x
+        // 5120 82 -> 77).
         operands(0, 0);
+        if (kt > 0) multiply(1);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks < 3) operands((ks + 1) & 1, ks + 1);
-#pragma unroll
-          for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
+        for (int ks = 0; ks < 3; ++ks) {
+          operands((ks + 1) & 1, ks + 1);
+          multiply(ks & 1);
         }
         if constexpr (I * J >= I + J) {
           constexpr int kMfma = 0x8, kLdsRead = 0x100;
-          __builtin_amdgcn_sched_group_barrier(kLdsRead, I + J, 0);
 #pragma unroll
           for (int ks = 0; ks < 3; ++ks) {
 #pragma unroll
@@ -479,7 +484,6 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
             }
             if constexpr (I * J > I + J) __builtin_amdgcn_sched_group_barrier(kMfma, I * J - I - J, 0);
           }
-          __builtin_amdgcn_sched_group_barrier(kMfma, I * J, 0);
         }
       } else {   // only the blocks that hold tokens
 #pragma unroll
@@ -500,6 +504,7 @@ project_i8_tile_kernel(ProjectI8Args a, int tiles_f, int tiles_t) {
     // TF / WF outputs of one token.  acc[i][j][4g + e] is output 32i + 8g +
     // 4 lh + e of token 32j + lr.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the buffer's last reads are done
+    if constexpr (kWhole) multiply(1);
     u32x4_t* E = lds + (buf ^ 1) * (WC + QC) + wave * 32 * RC;
     const float* sw = sc + par * (TF + TT) + wf * (TF / WF);
     const float* sq = sc + par * (TF + TT) + TF + wt * (TT / WT);
