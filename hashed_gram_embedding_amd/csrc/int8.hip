@@ -55,7 +55,7 @@ struct CodeRow {
   int whole, shift;
   __device__ __forceinline__ CodeRow(int8_t* row, int cols, bool tail)
       : dst(row), whole(cols / 16 * 16), shift(tail && cols % 16 != 0 ? 16 - cols % 16 : 0) {}
-  __device__ __forceinline__ int8_t* at(int c) const { return dst + (c < whole ? c : c + shift); }
+  __device__ __forceinline__ int8_t* at(int64_t c) const { return dst + (c < whole ? c : c + shift); }
 };
 
 // Rows of fewer than 512 N + 8 columns: one wavefront a row, runs of 8, every
@@ -106,12 +106,12 @@ template <int DT>
 __device__ __forceinline__ void quantize_long(int64_t row, const void* __restrict__ x, int cols, int8_t* __restrict__ q, int64_t ldq,
                                               int tail, float* __restrict__ scale) {
   __shared__ uint32_t part[4];
-  const int64_t base = row * cols;
-  const int t = threadIdx.x, c8 = cols / 8 * 8, ct = c8 + t;
+  const int t = threadIdx.x;
+  const int64_t base = row * cols, c8 = cols / 8 * 8, ct = c8 + t;   // (rows up to 2^31 - 1 columns: no step past them in 32 bits)
   const float ft = ct < cols ? load1<DT>(x, base + ct) : 0.f;
   uint32_t top = magnitude(ft);
 #pragma unroll 4
-  for (int c = t * 8; c < c8; c += 256 * 8) {
+  for (int64_t c = t * 8; c < c8; c += 256 * 8) {
     float f[8];
     load8<DT>(x, base + c, f);
 #pragma unroll
@@ -126,7 +126,7 @@ __device__ __forceinline__ void quantize_long(int64_t row, const void* __restric
   const RowScale rs = row_factors(__uint_as_float(top));
   const CodeRow out(q + row * ldq, cols, tail != 0);
 #pragma unroll 4
-  for (int c = t * 8; c < c8; c += 256 * 8) {
+  for (int64_t c = t * 8; c < c8; c += 256 * 8) {
     float f[8];
     load8<DT>(x, base + c, f);
     const u32x2_t w = codes ? quantize8(f, rs) : u32x2_t{0, 0};
@@ -779,8 +779,8 @@ project_i8_short_kernel(ProjectI8Args a) {
   static_cast<OutT*>(a.out)[id] = to_out<OutT>(static_cast<float>(sum) * a.q_scale[t] * a.w_scale[o]);
 }
 
-// Few tokens: bound by reading W once, or by latency.  Every wavefront streams 16 rows of W from memory straight into the operand
-// registers of v_mfma_i32_16x16x64_i8 (lane l: row l & 15, bytes 16 (l >> 4)
+// Few tokens: bound by reading W once, or by latency.  Every wavefront streams
+// 16 rows of W from memory straight into the operand registers of v_mfma_i32_16x16x64_i8 (lane l: row l & 15, bytes 16 (l >> 4)
 // of each run of 64), 16 loads (1024 columns) in flight, while the codes of
 // up to 16 NB tokens sit in LDS.  A row of codes starts 16 bytes further
 // round the banks than the one before (stride 16 modulo 256), so the 16 rows

@@ -74,6 +74,22 @@ def test_quantize_borders(dtype):
     assert torch.isnan(s[7:10]).all() and (q[7:10] == 0).all() and s[4] == 0
 
 
+def test_quantize_the_longest_row():
+    """2^31 - 1 columns, the documented limit: the last ones are reached, nothing behind them."""
+    log("quantize_i8 longest row")
+    n = 2 ** 31 - 1
+    x = torch.zeros(1, n, dtype=torch.bfloat16, device=DEV)
+    at = [0, 5, 2 ** 30, n - 2049, n - 9, n - 8, n - 2, n - 1]
+    for i, c in enumerate(at):
+        x[0, c] = (i + 1) * (-1) ** i
+    x[0, n - 3] = 127.0
+    q, s = eg.quantize_i8(x)
+    assert float(s) == 1.0 and [int(q[0, c]) for c in at] == [(i + 1) * (-1) ** i for i in range(len(at))]
+    assert int(q[0, n - 3]) == 127
+    q[0, at + [n - 3]] = 0
+    assert not any(bool(p.any()) for p in q[0].split(1 << 28))
+
+
 SIZES = [(1, 16, 1), (1, 1024, 2000), (2, 64, 64), (3, 48, 65), (5, 17, 33), (16, 1024, 4100), (31, 15, 7), (33, 1, 5),
          (64, 1024, 256), (65, 128, 129), (130, 1000, 515), (200, 2823, 103), (257, 1024, 512), (300, 4096, 192),
          (1000, 320, 1031), (513, 2048, 2048), (33, 513, 66),
