@@ -152,6 +152,19 @@ def test_product_into_a_view(k, out_dtype):
         assert buf[0] == 7.0 and buf[-1] == 7.0
 
 
+@pytest.mark.parametrize("k,n_out,out_dtype", [(32, 120000, "bf16"), (40, 119999, "f32")])
+def test_outputs_past_32_bits(k, n_out, out_dtype):
+    """More than 2^31 outputs: rows at both ends against the same rows multiplied alone."""
+    log(f"project_i8 {k} x {n_out} past 32 bits")
+    n = 20001
+    q = torch.randint(-127, 128, (n, k), dtype=torch.int8, device=DEV)
+    w = torch.randint(-127, 128, (n_out, k), dtype=torch.int8, device=DEV)
+    qs, ws = torch.rand(n, device=DEV), torch.rand(n_out, device=DEV)
+    out = eg.project_i8(q, w, ws, e_scale=qs, out_dtype=out_dtype)
+    for a, b in ((0, 5), (17890, 17900), (n - 7, n)):
+        assert torch.equal(out[a:b], eg.project_i8(q[a:b].clone(), w, ws, e_scale=qs[a:b].clone(), out_dtype=out_dtype)), a
+
+
 def test_unaligned_operands_are_refused():
     log("project_i8 unaligned operands")
     b = torch.zeros(40 * 64 + 16, dtype=torch.int8, device=DEV)

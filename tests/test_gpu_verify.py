@@ -106,6 +106,36 @@ def test_probs_at_the_ends_of_the_temperature(dtype, V):
             assert np.all(np.abs(p[s] - want) <= want * 2.0 ** -24 * (V / 64 + 32 + 4)), (s, rows)
 
 
+def test_the_longest_rows():
+    """V = 2^31 - 1, the documented limit of both calls: entries at the very end
+    of a row, found through offsets past 32 bits."""
+    log("token_probs and verify_drafts longest rows")
+    n = 2 ** 31 - 1
+    x = torch.full((2, 1, n), -INF, dtype=torch.bfloat16, device=DEV)
+    x[:, 0, n - 1] = 1.0
+    x[:, 0, n - 2] = 1.0
+    x[:, 0, 11] = 0.0
+    p = eg.token_probs(x, torch.tensor([1.0, 0.0], device=DEV))
+    z = 2 * math.e + 1
+    got = [float(p[0, 0, c]) for c in (11, n - 2, n - 1)]
+    assert all(abs(g - w) <= w * 2.0 ** -20 for g, w in zip(got, (1 / z, math.e / z, math.e / z)))
+    assert float(p[1, 0, n - 2]) == 1.0
+    p[0, 0, 11] = p[0, 0, n - 2] = p[0, 0, n - 1] = p[1, 0, n - 2] = 0
+    assert not any(bool(c.any()) for r in p[:, 0] for c in r.split(1 << 28))
+    del x, p
+
+    t = torch.zeros((1, 3, n), dtype=torch.bfloat16, device=DEV)
+    t[0, 0, n - 1] = 1.0
+    t[0, 1, n - 3] = 0.25
+    t[0, 1, n - 1] = 0.5
+    t[0, 1, 3] = 0.25
+    drafted = torch.tensor([[n - 1, 5]], dtype=torch.int32, device=DEV)
+    ua = torch.zeros(1, 2, device=DEV)
+    for u, want in ((0.1, 3), (0.3, n - 3), (0.49, n - 3), (0.5, n - 1), (0.99, n - 1)):
+        tok, acc = eg.verify_drafts(t, None, drafted, ua, torch.tensor([u], device=DEV))
+        assert acc.tolist() == [1] and tok.tolist() == [[n - 1, want, -1]], u
+
+
 def test_probs_of_padded_rows():
     """Rows of a padded vocabulary: the padding is not read, whatever it holds."""
     log("token_probs padded")
