@@ -788,11 +788,21 @@ def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, 
     return dev, B, T
 
 
-def _check_draft(draft: Draft, B: int, T: int, dev):
+def _check_draft(draft: Draft, B: int, T: int, layer: Layer, dev):
     if (draft.B, draft.T) != (B, T):
         raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
     if draft.v.device != dev:
         raise ValueError(f"the draft is on {draft.v.device}, the tokens are on {dev}")
+    if draft.gamma.shape[1] != layer.M or draft.v.shape[1] < layer.d:
+        raise ValueError(f"the draft is for a layer of {draft.gamma.shape[1]} branches with rows of {draft.v.shape[1]}, "
+                         f"the layer has {layer.M} of d={layer.d}")
+
+
+def _check_w8(w8: Int8Weights, layer: Layer, dev):
+    if w8.q.device != dev:
+        raise ValueError(f"the int8 weights are on {w8.q.device}, the tokens are on {dev}")
+    if w8.q.shape != layer.w.shape:
+        raise ValueError(f"the int8 weights are {tuple(w8.q.shape)}, the layer's are {tuple(layer.w.shape)}")
 
 
 def _layer_outputs(B, T, layer, H, want_alpha, want_y, stream):
@@ -807,6 +817,7 @@ def forward_i8(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, w8: Int8Weig
     """forward() with Step 5 as the 8-bit integer product.  Returns (alpha, y)
     when asked."""
     dev, B, T = _check_chunk(tokens, H, layer, state)
+    _check_w8(w8, layer, dev)
     alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
     ws = _workspace(H, ws, max(lib().engram_forward_i8_workspace(B, T, ctypes.byref(layer.s)), 256), stream)
     _launch(lib().engram_forward_i8, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s),
@@ -821,7 +832,9 @@ def forward_draft(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, state: De
     """One layer over a drafted chunk: H as forward() (or forward_i8() with w8)
     would leave it, `state` only read, the chunk's conv inputs in `draft`."""
     dev, B, T = _check_chunk(tokens, H, layer, state)
-    _check_draft(draft, B, T, dev)
+    _check_draft(draft, B, T, layer, dev)
+    if w8 is not None:
+        _check_w8(w8, layer, dev)
     alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
     p8 = None if w8 is None else ctypes.byref(w8.s)
     ws = _workspace(H, ws, max(lib().engram_forward_draft_workspace(B, T, ctypes.byref(layer.s), p8), 256), stream)
@@ -835,7 +848,7 @@ def commit_draft(tokens: torch.Tensor, layer: Layer, draft: Draft, n_accepted: t
     """Advance `state` by the first n_accepted + 1 tokens of each sequence's
     chunk (n_accepted int32 [B] from verify_drafts; -1 keeps none)."""
     dev, B, T = _check_chunk(tokens, None, layer, state)
-    _check_draft(draft, B, T, dev)
+    _check_draft(draft, B, T, layer, dev)
     _check_tensor("n_accepted", n_accepted, _I32, (B,), dev)
     _launch(lib().engram_commit_draft, dev, stream, tokens.data_ptr(), B, T, ctypes.byref(layer.s),
             ctypes.byref(draft.s), n_accepted.data_ptr(), ctypes.byref(state.s))

@@ -226,6 +226,47 @@ def test_binding_refuses_what_it_would_misread():
         eg.verify_drafts(p, q, d, ua, us)
 
 
+def test_binding_refuses_drafts_and_weights_of_another_layer():
+    """A draft's gamma and int8 weights are sized by the layer they were made
+    for: with another layer's sizes the kernels would leave them.  (With d the
+    same, a fused layer's v rows are as long whatever its branches.)"""
+    from hashed_gram_embedding_amd import inputs
+    B, T, d = 2, 3, 128
+    layers = [inputs.make_shape(B, T, heads=2, dim=32, d=n, branches=m).layers[0] for n, m in ((d, 1), (d, 4), (2 * d, 1), (2 * d, 4))]
+    one, four, wide, wide4 = (eg.Layer(lay, "bf16", "cpu", bf16_packed=False) for lay in layers)
+    tok, acc = torch.zeros((B, T), dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+
+    def state(L):
+        return eg.DecodeState(B, 3, L.M, 9, L.d, "cpu")
+
+    def hidden(L):
+        return torch.zeros((B, T, L.M, L.d), dtype=torch.bfloat16)
+
+    def weights(L):
+        return eg.Int8Weights(L, torch.zeros(L.w.shape, dtype=torch.int8), torch.zeros(L.w.shape[0]))
+
+    for L, other in ((four, one), (one, four), (wide, one), (wide4, four)):
+        for draft in (eg.Draft(B, T, other, "cpu"), eg.Draft(B, T, other, "cpu", v=torch.zeros(B * T, d))):
+            with pytest.raises(ValueError, match="the draft is for a layer of"):
+                eg.forward_draft(tok, hidden(L), L, state(L), draft)
+            with pytest.raises(ValueError, match="the draft is for a layer of"):
+                eg.commit_draft(tok, L, draft, acc, state(L))
+        own = eg.Draft(B, T, L, "cpu")
+        with pytest.raises(ValueError, match="the int8 weights are"):
+            eg.forward_draft(tok, hidden(L), L, state(L), own, w8=weights(other))
+        with pytest.raises(ValueError, match="the int8 weights are"):
+            eg.forward_i8(tok, hidden(L), L, weights(other))
+        elsewhere = weights(L)
+        elsewhere.q = elsewhere.q.to("meta")
+        with pytest.raises(ValueError, match="the int8 weights are on meta"):
+            eg.forward_i8(tok, hidden(L), L, elsewhere)
+        # those of the layer itself pass these checks (and stop at the host tensors)
+        for call in (lambda: eg.forward_draft(tok, hidden(L), L, state(L), own, w8=weights(L)),
+                     lambda: eg.forward_i8(tok, hidden(L), L, weights(L)), lambda: eg.commit_draft(tok, L, own, acc, state(L))):
+            with pytest.raises(ValueError, match="on a GPU"):
+                call()
+
+
 def test_oracle_quantize_i8_by_hand():
     q, s = orc.quantize_i8(np.array([[254.0, 127.0, 1.0, -3.0, 0.5], [0.0] * 5, [np.inf, 1, 2, 3, 4]]))
     assert q[0].tolist() == [127, 64, 0, -2, 0]      # 63.5, 0.5, -1.5 to even, 0.25
