@@ -1,5 +1,6 @@
 // Token probabilities and the verification of drafted tokens: the end of a
 // speculative decode step whose layers ran over the drafted chunk.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_util.h"
@@ -457,13 +458,19 @@ probs_join_kernel(ProbsArgs a, int segs, const Segment* __restrict__ part) {
   if (r.vt < a.V) out[r.vt] = __builtin_amdgcn_exp2f((xt - top) * f) * inv;
 }
 
+// Rows of a launch: it has fewer than 2^32 work-items (HIP runs the low 32 bits
+// of a larger number, without an error).  More rows go in pieces of whole
+// sequences, or of a part of one: a piece's first row is at its first
+// temperature.
+constexpr int64_t kMostRows = 1 << 21;
+
 bool probs_splits(int64_t rows, int64_t V) { return rows <= 64 && V > 32768; }
 
 int probs_segments(int64_t V) { return static_cast<int>((V + kSegment - 1) / kSegment); }
 
 template <int DT>
-hipError_t launch_probs_dt(const ProbsArgs& a, int64_t rows, void* ws, hipStream_t s) {
-  if (probs_splits(rows, a.V)) {
+hipError_t launch_probs_dt(const ProbsArgs& a, int64_t rows, bool split, void* ws, hipStream_t s) {
+  if (split) {
     const int segs = probs_segments(a.V);
     const dim3 wide(static_cast<unsigned>(rows * segs));
     launch_k(probs_segments_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<Segment*>(ws));
@@ -492,9 +499,18 @@ size_t probs_workspace(int64_t rows, int64_t V) {
 
 hipError_t launch_token_probs(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
                               int64_t per, float* probs, void* ws, hipStream_t s) {
-  if (rows == 0) return hipSuccess;
-  const ProbsArgs a{logits, temperature, probs, V, ld, per};
-  return dtype == ENGRAM_BF16 ? launch_probs_dt<ENGRAM_BF16>(a, rows, ws, s) : launch_probs_dt<ENGRAM_F32>(a, rows, ws, s);
+  const int64_t size = dtype == ENGRAM_BF16 ? 2 : 4;
+  const bool split = probs_splits(rows, V);
+  for (int64_t r = 0; r < rows;) {
+    const int64_t n = std::min(rows - r, per <= kMostRows ? kMostRows / per * per : std::min(kMostRows, per - r % per));
+    const ProbsArgs a{static_cast<const char*>(logits) + r * ld * size, temperature != nullptr ? temperature + r / per : nullptr,
+                      probs + r * V, V, ld, per};
+    const hipError_t e = dtype == ENGRAM_BF16 ? launch_probs_dt<ENGRAM_BF16>(a, n, split, ws, s)
+                                              : launch_probs_dt<ENGRAM_F32>(a, n, split, ws, s);
+    if (e != hipSuccess) return e;
+    r += n;
+  }
+  return hipSuccess;
 }
 
 namespace {

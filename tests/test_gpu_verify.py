@@ -106,6 +106,27 @@ def test_probs_at_the_ends_of_the_temperature(dtype, V):
             assert np.all(np.abs(p[s] - want) <= want * 2.0 ** -24 * (V / 64 + 32 + 4)), (s, rows)
 
 
+@pytest.mark.parametrize("S,R,V", [(2 ** 24 + 3, 1, 3), (5, 2 ** 22 - 1, 4), (1, 2 ** 24 + 5, 3), (3, 2 ** 23 + 7, 2)])
+def test_probs_of_the_most_rows(S, R, V):
+    """More rows than one launch can have: each with its own sequence's temperature."""
+    log(f"token_probs {S} x {R} rows")
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(S, R, V, generator=g, device=DEV)
+    t = 0.25 + torch.rand(S, generator=g, device=DEV)
+    p = eg.token_probs(x, t)
+    worst = 0.0
+    for part in range(0, S * R, 1 << 22):
+        rows = slice(part, min(part + (1 << 22), S * R))
+        seq = torch.arange(rows.start, rows.stop, device=DEV) // R
+        a = x.view(S * R, V)[rows].double()
+        ref = torch.softmax(a / t.double()[seq, None], -1)
+        arg = (a.max(-1, keepdim=True).values - a) / t.double()[seq, None] / math.log(2)
+        own = 2.0 ** -24 * (4 * math.log(2) * arg + 4)
+        rel = own + (ref * own).sum(-1, keepdim=True) + 2.0 ** -24 * (32 + 2)
+        worst = max(worst, float(((p.view(S * R, V)[rows].double() - ref).abs() / (rel * ref)).max()))
+    assert worst <= 1.0, worst
+
+
 def test_the_longest_rows():
     """V = 2^31 - 1, the documented limit of both calls: entries at the very end
     of a row, found through offsets past 32 bits."""
