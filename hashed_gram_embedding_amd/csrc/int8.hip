@@ -1079,15 +1079,31 @@ AlignJob align_job(const int8_t* x, int8_t* y, int64_t rows, int64_t K) {
   return AlignJob{x, reinterpret_cast<u32x4_t*>(y), rows, (rows * (i8_row_stride(K) / 16) + per - 1) / per};
 }
 
+// Workgroups of 256 threads that a launch can have: it has fewer than 2^32
+// work-items (HIP runs the low 32 bits of a larger number, without an error).
+constexpr int64_t kMostGroups = (1 << 24) - 1;
+
+// More rows than a launch has workgroups for go in pieces; W's come with the first.
 template <int DT, int N>
-hipError_t launch_quantize_n(const QuantizeArgs& a, const AlignJob& w, hipStream_t s) {
-  const int64_t groups = w.groups + (N > 0 ? (a.rows + 3) / 4 : a.rows);
-  if (groups > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(groups));
+hipError_t launch_quantize_n(QuantizeArgs a, AlignJob w, hipStream_t s) {
+  constexpr int64_t per = N > 0 ? 4 : 1;   // rows of a workgroup
   const int chunks = static_cast<int>(i8_row_stride(a.cols) / 16);
-  if (w.groups > 0) launch_k((quantize_rows_kernel<DT, N, true>), grid, dim3(256), 0, s, a, w, chunks);
-  else launch_k((quantize_rows_kernel<DT, N, false>), grid, dim3(256), 0, s, a, w, chunks);
-  return hipGetLastError();
+  if (w.groups >= kMostGroups) return hipErrorInvalidValue;
+  for (int64_t left = a.rows; left > 0;) {
+    const int64_t n = std::min(left, (kMostGroups - w.groups) * per);
+    const dim3 grid(static_cast<unsigned>(w.groups + (n + per - 1) / per));
+    a.rows = n;
+    if (w.groups > 0) launch_k((quantize_rows_kernel<DT, N, true>), grid, dim3(256), 0, s, a, w, chunks);
+    else launch_k((quantize_rows_kernel<DT, N, false>), grid, dim3(256), 0, s, a, w, chunks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.x = static_cast<const char*>(a.x) + n * a.cols * (DT == ENGRAM_BF16 ? 2 : 4);
+    a.q += n * a.ldq;
+    a.scale += n;
+    w = AlignJob{};
+    left -= n;
+  }
+  return hipSuccess;
 }
 
 template <int DT>
@@ -1125,7 +1141,7 @@ bool project_i8_aligns(int64_t n_tok, int64_t K) { return K >= 16 && K % 16 != 0
 hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
                            hipStream_t s) {
   const AlignJob a = align_job(w, w_out, w_rows, K), b = align_job(q, q_out, q_rows, K);
-  if (a.groups + b.groups > INT32_MAX) return hipErrorInvalidValue;
+  if (a.groups + b.groups > kMostGroups) return hipErrorInvalidValue;   // (copies of 2^38 bytes)
   launch_k(align_rows_kernel, dim3(static_cast<unsigned>(a.groups + b.groups)), dim3(256), 0, s, a, b, static_cast<int>(K),
            static_cast<int>(i8_row_stride(K) / 16));
   return hipGetLastError();

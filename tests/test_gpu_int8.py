@@ -90,6 +90,23 @@ def test_quantize_the_longest_row():
     assert not any(bool(p.any()) for p in q[0].split(1 << 28))
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(2 ** 26 + 5, 4, "bf16"), (2 ** 26 + 5, 9, "f32")])
+def test_quantize_the_most_rows(rows, cols, dtype):
+    """More rows than one launch can have."""
+    log(f"quantize_i8 {rows} rows")
+    g = torch.Generator(device=DEV).manual_seed(6)
+    pattern = torch.randn(4099, cols, generator=g, device=DEV).to(TYPES[dtype])
+    times = -(-rows // 4099)
+    x = pattern.repeat(times, 1)[:rows].contiguous()
+    q, s = eg.quantize_i8(x)
+    del x
+    rq, rs = orc.quantize_i8(pattern.double().cpu().numpy())
+    rq, rs = torch.from_numpy(rq).to(DEV), torch.from_numpy(rs).to(DEV)
+    whole = rows // 4099 * 4099
+    assert (q[:whole].view(-1, 4099, cols) == rq).all() and (s[:whole].view(-1, 4099) == rs).all()
+    assert torch.equal(q[whole:], rq[:rows - whole]) and torch.equal(s[whole:], rs[:rows - whole])
+
+
 SIZES = [(1, 16, 1), (1, 1024, 2000), (2, 64, 64), (3, 48, 65), (5, 17, 33), (16, 1024, 4100), (31, 15, 7), (33, 1, 5),
          (64, 1024, 256), (65, 128, 129), (130, 1000, 515), (200, 2823, 103), (257, 1024, 512), (300, 4096, 192),
          (1000, 320, 1031), (513, 2048, 2048), (33, 513, 66),
