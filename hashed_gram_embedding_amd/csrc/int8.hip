@@ -1155,10 +1155,18 @@ hipError_t launch_product(ProjectI8Args a, const void* e, int e_dtype, hipStream
   if (e_dtype == ENGRAM_F32) return launch_few_blocks<OutT, ENGRAM_F32>(a, e, s);
   if (project_i8_few(a.n_tok, a.K)) return launch_few_blocks<OutT, ENGRAM_I8>(a, nullptr, s);
   if (a.K < 16) {
-    const int64_t blocks = (a.n_tok * a.n_out + 255) / 256;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    launch_k(project_i8_short_kernel<OutT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    // one thread an output, so tokens go in pieces of at most 2^31 outputs
+    const int64_t n_tok = a.n_tok, piece = std::max<int64_t>((int64_t{1} << 31) / a.n_out, 1);
+    for (int64_t t = 0; t < n_tok; t += piece) {
+      a.n_tok = std::min(piece, n_tok - t);
+      launch_k(project_i8_short_kernel<OutT>, dim3(static_cast<unsigned>((a.n_tok * a.n_out + 255) / 256)), dim3(256), 0, s, a);
+      const hipError_t err = hipGetLastError();
+      if (err != hipSuccess) return err;
+      a.q += piece * a.ldq;
+      a.q_scale += piece;
+      a.out = static_cast<OutT*>(a.out) + piece * a.n_out;
+    }
+    return hipSuccess;
   }
   // whole chunks from here on: the rows are the product's own layout
   a.K = static_cast<int>(i8_row_stride(a.K));

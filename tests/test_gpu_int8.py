@@ -107,6 +107,27 @@ def test_quantize_the_most_rows(rows, cols, dtype):
     assert torch.equal(q[whole:], rq[:rows - whole]) and torch.equal(s[whole:], rs[:rows - whole])
 
 
+@pytest.mark.parametrize("source", ["i8", "bf16"])
+def test_the_most_outputs_of_short_rows(source):
+    """Fewer than 16 columns and more outputs than one launch can have threads."""
+    log(f"project_i8 short rows, past 2^32 outputs, {source}")
+    n, k, o = 70001, 5, 61441
+    g = torch.Generator(device=DEV).manual_seed(8)
+    w = torch.randint(-127, 128, (o, k), generator=g, dtype=torch.int8, device=DEV)
+    ws = torch.rand(o, generator=g, device=DEV)
+    e, s = torch.randn(n, k, generator=g, device=DEV).to(torch.bfloat16), None
+    if source == "i8":
+        e, s = eg.quantize_i8(e)
+    out = eg.project_i8(e, w, ws, e_scale=s)
+    for a in [*range(0, n - 5, 7919), n - 5]:
+        part = eg.project_i8(e[a:a + 5].clone(), w, ws, e_scale=None if s is None else s[a:a + 5].clone())
+        assert torch.equal(out[a:a + 5], part), a
+    for a in range(0, n, 4096):   # every output, to the rounding of its type
+        qf, sf = (e[a:a + 4096], s[a:a + 4096]) if s is not None else eg.quantize_i8(e[a:a + 4096].clone())
+        ref = (qf.float() @ w.float().t()) * sf[:, None] * ws
+        assert ((out[a:a + 4096].float() - ref).abs() <= (2.0 ** -8 + 2.0 ** -20) * ref.abs() + 2 * TINY).all(), a
+
+
 SIZES = [(1, 16, 1), (1, 1024, 2000), (2, 64, 64), (3, 48, 65), (5, 17, 33), (16, 1024, 4100), (31, 15, 7), (33, 1, 5),
          (64, 1024, 256), (65, 128, 129), (130, 1000, 515), (200, 2823, 103), (257, 1024, 512), (300, 4096, 192),
          (1000, 320, 1031), (513, 2048, 2048), (33, 513, 66),
