@@ -230,6 +230,8 @@ bool prof_take(hipEvent_t* start, hipEvent_t* stop) {
   ++p.n;
   return true;
 }
+
+void prof_stage(const char* name) { prof_mark(nullptr, name); }
 }  // namespace engram
 
 namespace {
@@ -602,7 +604,6 @@ CodeSpace carve_codes(Carve& c, int e_dtype, int64_t n_tok, int64_t d_mem, int64
 // where cs has one.
 engram_status run_quantize(const void* e, int e_dtype, int64_t n_tok, int64_t d_mem, const CodeSpace& cs, const int8_t* w,
                            int64_t n_out, hipStream_t stream) {
-  prof_mark(stream, "quantize_i8_kernel");
   return hip_status(engram::launch_quantize_i8(e, e_dtype, n_tok, d_mem, cs.codes, engram::i8_row_stride(d_mem), true, cs.scale, w,
                                                n_out, cs.w, stream),
                     "quantize_i8 launch");
@@ -1304,7 +1305,6 @@ ENGRAM_API engram_status engram_quantize_i8(const void* x, engram_dtype dtype, i
   if (!aligned(x, dtype_size(dtype)) || !aligned(scale, 4))
     return fail(ENGRAM_EINVAL, "quantize_i8: x and scale must be aligned to their elements");
   prof_begin();
-  prof_mark(stream, "quantize_i8_kernel");
   return hip_status(engram::launch_quantize_i8(x, dtype, rows, cols, q, cols, false, scale, nullptr, 0, nullptr, stream), "quantize_i8 launch");
 }
 
@@ -1523,7 +1523,6 @@ ENGRAM_API engram_status engram_token_probs(const void* logits, engram_dtype dty
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
     return fail(ENGRAM_EINVAL, "token_probs: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
   prof_begin();
-  prof_mark(stream, "token_probs_kernel");
   const engram_status r = hip_status(engram::launch_token_probs(logits, dtype, rows, V, ld, temperature, per, probs, ws, stream),
                                      "token_probs launch");
   prof_mark(stream, nullptr);
@@ -1556,7 +1555,6 @@ ENGRAM_API engram_status engram_verify_drafts(const void* target, const void* dr
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
     return fail(ENGRAM_EINVAL, "verify_drafts: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
   prof_begin();
-  prof_mark(stream, "verify_drafts_kernel");
   const engram_status r = hip_status(engram::launch_verify(target, draft, dtype, drafted, n_draft, u_accept, u_sample, S, G, V, tokens,
                                                            n_accepted, ws, stream),
                                      "verify_drafts launch");

@@ -400,6 +400,10 @@ hipError_t launch_cache_build(const int32_t* tokens, int64_t B, int64_t T, const
 // execution and not the gaps around it.  prof_take hands out the open stage's
 // events (false when no stage is open).
 bool prof_take(hipEvent_t* start, hipEvent_t* stop);
+// Opens a stage: the next kernel launched on this thread is timed under `name`.
+// For launchers of more than one kernel (the others' stages are opened by the
+// entry points).
+void prof_stage(const char* name);
 
 template <typename F, typename... Args>
 inline void launch_k(F kernel, const dim3& grid, const dim3& block, uint32_t lds, hipStream_t s, Args... args) {

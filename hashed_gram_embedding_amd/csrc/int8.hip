@@ -1093,6 +1093,7 @@ hipError_t launch_quantize_n(QuantizeArgs a, AlignJob w, hipStream_t s) {
     const int64_t n = std::min(left, (kMostGroups - w.groups) * per);
     const dim3 grid(static_cast<unsigned>(w.groups + (n + per - 1) / per));
     a.rows = n;
+    prof_stage("quantize_i8_kernel");
     if (w.groups > 0) launch_k((quantize_rows_kernel<DT, N, true>), grid, dim3(256), 0, s, a, w, chunks);
     else launch_k((quantize_rows_kernel<DT, N, false>), grid, dim3(256), 0, s, a, w, chunks);
     const hipError_t e = hipGetLastError();
@@ -1159,6 +1160,7 @@ hipError_t launch_product(ProjectI8Args a, const void* e, int e_dtype, hipStream
     const int64_t n_tok = a.n_tok, piece = std::max<int64_t>((int64_t{1} << 31) / a.n_out, 1);
     for (int64_t t = 0; t < n_tok; t += piece) {
       a.n_tok = std::min(piece, n_tok - t);
+      prof_stage("project_i8_kernel");
       launch_k(project_i8_short_kernel<OutT>, dim3(static_cast<unsigned>((a.n_tok * a.n_out + 255) / 256)), dim3(256), 0, s, a);
       const hipError_t err = hipGetLastError();
       if (err != hipSuccess) return err;

@@ -473,13 +473,16 @@ hipError_t launch_probs_dt(const ProbsArgs& a, int64_t rows, bool split, void* w
   if (split) {
     const int segs = probs_segments(a.V);
     const dim3 wide(static_cast<unsigned>(rows * segs));
+    prof_stage("token_probs_segments_kernel");
     launch_k(probs_segments_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<Segment*>(ws));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    prof_stage("token_probs_join_kernel");
     launch_k(probs_join_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<const Segment*>(ws));
     return hipGetLastError();
   }
   const dim3 grid(static_cast<unsigned>(rows));
+  prof_stage("token_probs_kernel");
   // the fewest registers that hold a row
   if (a.V <= 1024 * 2) launch_k((probs_kernel<DT, 256, 2>), grid, dim3(256), 0, s, a);
   else if (a.V <= 1024 * 8) launch_k((probs_kernel<DT, 256, 8>), grid, dim3(256), 0, s, a);
@@ -805,11 +808,14 @@ bool verify_splits(int64_t S, int64_t V) { return V > (S <= 64 ? 49152 : 81920);
 template <int DT>
 hipError_t launch_verify_dt(const VerifyArgs& a, int64_t S, hipStream_t s) {
   if (verify_splits(S, a.V)) {
+    prof_stage("verify_parts_kernel");
     launch_k(verify_parts_kernel<DT>, dim3(static_cast<unsigned>(S * (kParts / kPartWaves))), dim3(64 * kPartWaves), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    prof_stage("verify_drafts_kernel");
     launch_k((verify_kernel<DT, true>), dim3(static_cast<unsigned>(S)), dim3(64 * kVerifyWaves), 0, s, a);
   } else {
+    prof_stage("verify_drafts_kernel");
     launch_k((verify_kernel<DT, false>), dim3(static_cast<unsigned>(S)), dim3(64 * kVerifyWaves), 0, s, a);
   }
   return hipGetLastError();

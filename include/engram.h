@@ -628,11 +628,12 @@ engram_status engram_hot_lookup(const int32_t* tokens, int64_t B, int64_t T, con
 /* Stage timing, for benchmarks.  While profiling is on, calls of
  * engram_forward (and engram_forward_noalloc, engram_forward_i8,
  * engram_forward_draft), engram_retrieve, engram_forward_retrieved(_prefetch),
- * engram_gate_conv_forward, engram_hot_lookup, engram_project_i8,
- * engram_token_probs, engram_verify_drafts and engram_commit_draft on the
- * calling thread time each kernel they launch: the start and stop events are
- * recorded by the kernel's own dispatch (hipExtLaunchKernel), so a stage is
- * the kernel's execution interval (events owned by the library and reused).
+ * engram_gate_conv_forward, engram_hot_lookup, engram_quantize_i8,
+ * engram_project_i8, engram_token_probs, engram_verify_drafts and
+ * engram_commit_draft on the calling thread time each kernel they launch: the
+ * start and stop events are recorded by the kernel's own dispatch
+ * (hipExtLaunchKernel), so a stage is the kernel's execution interval (events
+ * owned by the library and reused).
  *   on = 1: engram_profile_read returns the stages of the most recent call
  *           (at most 12).
  *   on = 2: stages accumulate over calls until engram_profile_read, which

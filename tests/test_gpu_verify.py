@@ -127,6 +127,29 @@ def test_probs_of_the_most_rows(S, R, V):
     assert worst <= 1.0, worst
 
 
+def test_every_launch_of_a_call_is_timed():
+    """Stage timing names each kernel that the calls launch, in order: one for
+    rows that a workgroup takes, two where they are split over workgroups."""
+    log("stages of token_probs and verify_drafts")
+    x = torch.randn(3, 2, 40000, device=DEV)
+    many = torch.randn(70, 1, 40000, device=DEV)
+    p, q, d, ua, us = _case(2, 1, 60000, "f32", True)
+    short = _case(2, 1, 6000, "f32", True)
+    calls = [(lambda: eg.quantize_i8(x.view(6, 40000)), ["quantize_i8_kernel"]),
+             (lambda: eg.token_probs(x), ["token_probs_segments_kernel", "token_probs_join_kernel"]),
+             (lambda: eg.token_probs(many), ["token_probs_kernel"]),
+             (lambda: eg.verify_drafts(p, q, d, ua, us), ["verify_parts_kernel", "verify_drafts_kernel"]),
+             (lambda: eg.verify_drafts(*short[:5]), ["verify_drafts_kernel"])]
+    try:
+        for call, names in calls:
+            eg.profile_enable(1)
+            call()
+            got = eg.profile_read()
+            assert [n for n, _ in got] == names and all(ms > 0 for _, ms in got), got
+    finally:
+        eg.profile_enable(False)
+
+
 def test_the_longest_rows():
     """V = 2^31 - 1, the documented limit of both calls: entries at the very end
     of a row, found through offsets past 32 bits."""
