@@ -174,9 +174,22 @@ __device__ __forceinline__ bool constant_row(float top, float temp, float* fill)
   return top != top || top == -__builtin_inff() || (top == __builtin_inff() && temp > 0.f);
 }
 
-// log2(e) / T, kept finite and above 0: the largest logit's exponent is then 0
-// and a masked one's -inf at the smallest and largest T too.
-__device__ __forceinline__ float exponent_factor(float temp) { return fminf(fmaxf(kLog2e / temp, 0x1p-126f), 0x1.fffffep127f); }
+// 2^((l - top) log2(e) / T) of the logits l <= top of a row.  The factor is kept
+// finite and above 0: the largest logit's exponent is then 0 and a masked one's
+// -inf at the smallest and largest T too.  Finite logits may lie further apart
+// than float32 reaches, which matters where T is large enough to bring them
+// together again: there the difference is formed of l / 16 and top / 16 (16
+// also keeps the factor a normal number up to the largest finite T).  At scale 1
+// the multiply-add is the difference itself.
+struct Exponent {
+  float scale, top, f;
+  __device__ __forceinline__ Exponent(float row_top, float temp) {
+    scale = temp > 0x1p64f ? 0x1p-4f : 1.0f;
+    top = row_top * scale;
+    f = fminf(fmaxf(kLog2e / (temp * scale), 0x1p-149f), 0x1.fffffep127f);
+  }
+  __device__ __forceinline__ float operator()(float l) const { return __builtin_amdgcn_exp2f(fmaf(l, scale, -top) * f); }
+};
 
 // bf16 pairs stay packed from pass to pass: without this the compiler keeps
 // every unpacked value, then every exponential, for the next pass, twice the
@@ -235,14 +248,14 @@ probs_kernel(ProbsArgs a) {
     if (vt < V) out[vt] = at == vt ? 1.f : 0.f;
     return;
   }
-  const float f = exponent_factor(temp);
-  const float et = __builtin_amdgcn_exp2f((xt - top) * f);
+  const Exponent of(top, temp);
+  const float et = of(xt);
   float sum = et;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     float e[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f);
+    for (int k = 0; k < 4; ++k) e[k] = of(x[n].at(k));
     sum += (e[0] + e[1]) + (e[2] + e[3]);
   }
   forget(x);
@@ -251,7 +264,7 @@ probs_kernel(ProbsArgs a) {
   for (int n = 0; n < N; ++n) {
     f32x4_t y;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f) * inv;
+    for (int k = 0; k < 4; ++k) y[k] = of(x[n].at(k)) * inv;
     store_quad(out, q0 + n * THREADS, quads, y);
   }
   if (vt < V) out[vt] = et * inv;
@@ -270,7 +283,6 @@ probs_long_kernel(ProbsArgs a) {
   const void* in = static_cast<const char*>(a.logits) + row * a.ld * size;
   float* out = a.probs + row * V;
   const float temp = a.temperature != nullptr ? a.temperature[row / a.per] : 1.0f;
-  const float f = exponent_factor(temp);
   const int64_t quads = V / 4, vt = quads * 4 + threadIdx.x;
   const float xt = load_tail<DT>(in, vt, V);
   float top = -__builtin_inff(), sum = 0.f;
@@ -291,12 +303,13 @@ probs_long_kernel(ProbsArgs a) {
         m = fmaxf(m, l);
       }
     if (m > -__builtin_inff() && m < __builtin_inff()) {
-      sum = top > -__builtin_inff() ? sum * __builtin_amdgcn_exp2f((top - m) * f) : 0.f;
+      const Exponent of(m, temp);
+      sum = top > -__builtin_inff() ? sum * of(top) : 0.f;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         float e[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f((x[i].at(k) - m) * f);
+        for (int k = 0; k < 4; ++k) e[k] = of(x[i].at(k));
         sum += (e[0] + e[1]) + (e[2] + e[3]);
       }
     }
@@ -319,8 +332,9 @@ probs_long_kernel(ProbsArgs a) {
     if (vt < V) out[vt] = at == vt ? 1.f : 0.f;
     return;
   }
-  const float et = __builtin_amdgcn_exp2f((xt - top) * f);
-  const float part = own > -__builtin_inff() ? sum * __builtin_amdgcn_exp2f((own - top) * f) : 0.f;
+  const Exponent of(top, temp);
+  const float et = of(xt);
+  const float part = own > -__builtin_inff() ? sum * of(own) : 0.f;
   const float inv = 1.0f / group_sum<THREADS>(part + et, sh.sum);
   for (int64_t q = threadIdx.x; q < quads; q += U * THREADS) {
     Quad<DT> x[U];
@@ -330,7 +344,7 @@ probs_long_kernel(ProbsArgs a) {
     for (int i = 0; i < U; ++i) {
       f32x4_t y;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_exp2f((x[i].at(k) - top) * f) * inv;
+      for (int k = 0; k < 4; ++k) y[k] = of(x[i].at(k)) * inv;
       store_quad(out, q + i * THREADS, quads, y);
     }
   }
@@ -393,13 +407,13 @@ probs_segments_kernel(ProbsArgs a, int segs, Segment* __restrict__ part) {
   at = group_min<kSegThreads>(at, sh.first);
   float sum = 0.f;
   if (top > -__builtin_inff() && top < __builtin_inff()) {
-    const float f = exponent_factor(temp);
-    sum = __builtin_amdgcn_exp2f((xt - top) * f);
+    const Exponent of(top, temp);
+    sum = of(xt);
 #pragma unroll
     for (int n = 0; n < kSegQuads; ++n) {
       float e[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f);
+      for (int k = 0; k < 4; ++k) e[k] = of(x[n].at(k));
       sum += (e[0] + e[1]) + (e[2] + e[3]);
     }
   }
@@ -443,19 +457,19 @@ probs_join_kernel(ProbsArgs a, int segs, const Segment* __restrict__ part) {
     if (r.vt < a.V) out[r.vt] = value(r.vt);
     return;
   }
-  const float f = exponent_factor(temp);
+  const Exponent of(top, temp);
   float sum = 0.f;
   for (int i = threadIdx.x; i < segs; i += kSegThreads)
-    sum += mine[i].top > -__builtin_inff() ? mine[i].sum * __builtin_amdgcn_exp2f((mine[i].top - top) * f) : 0.f;
+    sum += mine[i].top > -__builtin_inff() ? mine[i].sum * of(mine[i].top) : 0.f;
   const float inv = 1.0f / group_sum<kSegThreads>(sum, sh.sum);
 #pragma unroll
   for (int n = 0; n < kSegQuads; ++n) {
     f32x4_t y;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_exp2f((x[n].at(k) - top) * f) * inv;
+    for (int k = 0; k < 4; ++k) y[k] = of(x[n].at(k)) * inv;
     store_quad(out, r.q0 + n * kSegThreads, r.quads, y);
   }
-  if (r.vt < a.V) out[r.vt] = __builtin_amdgcn_exp2f((xt - top) * f) * inv;
+  if (r.vt < a.V) out[r.vt] = of(xt) * inv;
 }
 
 // Rows of a launch: it has fewer than 2^32 work-items (HIP runs the low 32 bits

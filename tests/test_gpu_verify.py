@@ -150,6 +150,41 @@ def test_every_launch_of_a_call_is_timed():
         eg.profile_enable(False)
 
 
+def _chain(V):
+    """Longest chain of additions in the sum of a row that one workgroup takes
+    (1024 threads, quads: up to V / 4096 of them a thread, three more in a quad
+    and for the tail, 6 over the wavefront and 15 over the workgroup), and for
+    rows past the registers the rescalings, one per 8 quads, of 4 units each."""
+    return V / 4096 + 1 + 3 + 6 + 15 + 4 * (V / 32768 + 2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(1, 700), (9, 40000), (12, 9000), (12, 200003)])
+def test_probs_of_logits_further_apart_than_their_type(dtype, rows, V):
+    """Logits at both ends of their type's range, whose difference leaves it: at
+    the largest temperatures they still have a share."""
+    log(f"token_probs far logits {dtype} {rows} x {V}")
+    t = torch.tensor([3.4e38, 1e38, 2.0 ** 120, 1e30, 0.5, INF], device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(7)
+    x = (torch.finfo(TYPES[dtype]).max * (2 * torch.rand(len(t), rows, V, generator=g, device=DEV, dtype=torch.float64) - 1)).to(TYPES[dtype])
+    x[..., 3] = torch.finfo(TYPES[dtype]).max
+    x[..., V - 1] = torch.finfo(TYPES[dtype]).min
+    x[..., 5] = -INF
+    p = eg.token_probs(x, t)
+    a, got, temps = x.double().cpu().numpy(), p.double().cpu().numpy(), t.double().cpu().numpy()
+    for s, temp in enumerate(temps):
+        for r in range(rows):
+            row = a[s, r]
+            arg = np.zeros(V)
+            arg[np.isfinite(row)] = (row.max() - row[np.isfinite(row)]) / temp / math.log(2)
+            ref = np.where(np.isfinite(row), np.exp2(-arg), 0.0)
+            ref /= ref.sum()
+            own = 2.0 ** -24 * (4 * math.log(2) * arg + 4)
+            rel = own + np.sum(ref * own) + 2.0 ** -24 * (_chain(V) + 2)
+            err = np.abs(got[s, r] - ref)
+            assert np.all(err <= rel * ref + 2.0 ** -125), (temp, r, float(np.max(err / np.maximum(rel * ref, 1e-300))))
+
+
 def test_the_longest_rows():
     """V = 2^31 - 1, the documented limit of both calls: entries at the very end
     of a row, found through offsets past 32 bits."""
