@@ -456,7 +456,7 @@ hipError_t launch_frag2(const ProjGateArgs& a, const ProjGateArgs& b, hipStream_
   if (e != hipSuccess) return e;
   const uint32_t na = static_cast<uint32_t>(a.tiles_f * a.tiles_t), nb = static_cast<uint32_t>(b.tiles_f * b.tiles_t);
   launch_k((proj_frag2_kernel<SPW>), dim3(na + nb), dim3(64 * kFragWaves), kFragLds, s, a, b, na);
-  return hipGetLastError();
+  return launch_error();
 }
 
 std::atomic<uint32_t> g_next_slot{0};
@@ -479,7 +479,7 @@ hipError_t launch_fused_t(AheadJob a, AheadJob b, hipStream_t s) {
   launch_k((ahead_fused_kernel<IN, SPW, HIST_ALL, GPT, TB>),
            dim3(static_cast<unsigned>(a.p.tiles_f), static_cast<unsigned>(a.p.tiles_t), nb > 0 ? 2 : 1),
            dim3(64 * kFragWaves), lds, s, a, b);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int IN, int SPW, bool HIST_ALL, int TB>

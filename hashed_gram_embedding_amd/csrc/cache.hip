@@ -368,7 +368,7 @@ hipError_t launch_cache_build(const int32_t* tokens, int64_t B, int64_t T, const
   launch_k(copy_rows_kernel, dim3(static_cast<unsigned>((work + 255) / 256)), dim3(256), 0, s, cache_slot,
                      total_rows, static_cast<const uint8_t*>(ta.rows), ta.scale, row_bytes,
                      static_cast<uint8_t*>(cache_rows), cache_scale);
-  return hipGetLastError();
+  return launch_error();
 }
 
 size_t cache_update_workspace(int64_t total_rows, int64_t cache_n) {
@@ -424,7 +424,7 @@ hipError_t launch_cache_update(const TableArgs& ta, int64_t total_rows, int row_
   }
   if (decay_shift > 0)
     launch_k(age_kernel, dim3(grid_for(total_rows, 256)), dim3(256), 0, s, counts, total_rows, decay_shift);
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace engram

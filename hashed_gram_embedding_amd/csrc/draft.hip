@@ -63,7 +63,7 @@ hipError_t launch_commit_draft(const float* v, int64_t v_stride, const float* ga
   if (B == 0 || T == 0) return hipSuccess;
   launch_k(commit_draft_kernel, dim3(static_cast<unsigned>(B)), dim3(kThreads), 0, s, v, v_stride, gamma, T, g, st, tokens, proj,
            max_n, vocab, n_accepted, err);
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace engram

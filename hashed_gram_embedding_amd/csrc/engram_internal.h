@@ -405,13 +405,34 @@ bool prof_take(hipEvent_t* start, hipEvent_t* stop);
 // entry points).
 void prof_stage(const char* name);
 
+// A launch has fewer than 2^32 work-items along each dimension: of a larger
+// number HIP runs the low 32 bits and reports no error, so such a launch is left
+// out here and launch_error() names it.
+inline bool& launch_refused() {
+  static thread_local bool refused = false;
+  return refused;
+}
+
 template <typename F, typename... Args>
 inline void launch_k(F kernel, const dim3& grid, const dim3& block, uint32_t lds, hipStream_t s, Args... args) {
+  constexpr uint64_t kMost = UINT32_MAX;
+  if (uint64_t{grid.x} * block.x > kMost || uint64_t{grid.y} * block.y > kMost || uint64_t{grid.z} * block.z > kMost) {
+    launch_refused() = true;
+    return;
+  }
   hipEvent_t e0, e1;
   if (prof_take(&e0, &e1))
     hipExtLaunchKernelGGL(kernel, grid, block, lds, s, e0, e1, 0, args...);
   else
     hipLaunchKernelGGL(kernel, grid, block, lds, s, args...);
+}
+
+// Error of the launches since the last call of this.
+inline hipError_t launch_error() {
+  const hipError_t e = hipGetLastError();
+  if (!launch_refused()) return e;
+  launch_refused() = false;
+  return hipErrorInvalidConfiguration;
 }
 
 }  // namespace engram

@@ -880,7 +880,7 @@ hipError_t launch_gate_stats(const void* H, const void* kv, int64_t n_tok, const
   else
     launch_k((gate_stats_kernel<ENGRAM_F32, ENGRAM_F32>), grid, dim3(256), 0, s, H, kv, n_tok,
                        g.branches, g.d, stats);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int CG>
@@ -907,7 +907,7 @@ hipError_t launch_conv_cg(const ConvArgs& a, int vdtype, hipStream_t s) {
     launch_k((conv_kernel<ENGRAM_BF16, ENGRAM_F32, CG>), grid, dim3(256), lds, s, a);
   else
     launch_k((conv_kernel<ENGRAM_F32, ENGRAM_F32, CG>), grid, dim3(256), lds, s, a);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int KW, int DIL, int TS, int CPT>
@@ -924,7 +924,7 @@ hipError_t launch_conv_strip(const ConvArgs& a, int vdtype, hipStream_t s) {
     launch_k((conv_strip_kernel<ENGRAM_BF16, ENGRAM_F32, KW, DIL, TS, CPT>), grid, dim3(256), 0, s, a, spx);
   else
     launch_k((conv_strip_kernel<ENGRAM_F32, ENGRAM_F32, KW, DIL, TS, CPT>), grid, dim3(256), 0, s, a, spx);
-  return hipGetLastError();
+  return launch_error();
 }
 
 // Strip shape of the pages' conv (w = 4, dilation 3): decode steps get
@@ -961,7 +961,7 @@ hipError_t launch_conv_gather_ts(const ConvArgs& a, const GatherJob& gj, hipStre
              gj);
   else
     launch_k((conv_gather_kernel<4, 3, TS, CPT, GIN, ENGRAM_BF16, items>), grid, dim3(256), 0, s, a, spx, nc, ux, gj);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int GIN>
@@ -1004,7 +1004,7 @@ hipError_t launch_conv(const ConvArgs& a, int vdtype, hipStream_t s) {
       launch_k(conv_decode_kernel<ENGRAM_BF16>, grid, dim3(256), 0, s, a);
     else
       launch_k(conv_decode_kernel<ENGRAM_F32>, grid, dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch_error();
   }
   // both conv kernels stage at most kConvMaxStats statistics per row (the
   // projection launchers never produce more)
@@ -1034,7 +1034,7 @@ hipError_t launch_state_commit(const void* v, int64_t v_stride, int vdtype, int6
   else
     launch_k(state_commit_kernel<ENGRAM_F32>, dim3(static_cast<unsigned>(B)), dim3(256), 0, s,
                        v, v_stride, T, g, gamma, st, tokens, proj, max_n, vocab, err);
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace engram

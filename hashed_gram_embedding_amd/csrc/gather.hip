@@ -117,7 +117,7 @@ hipError_t launch_gather2_t(const GatherJob& a, const GatherJob& b, hipStream_t 
     launch_k((hashed_gather2_kernel<IN, OUT, 2>), grid, dim3(256), 0, s, a, b, split);
   else
     launch_k((hashed_gather2_kernel<IN, OUT, 1>), grid, dim3(256), 0, s, a, b, split);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int IN>
@@ -130,7 +130,7 @@ hipError_t launch_in(const int32_t* z, int64_t n_tok, const TableArgs& ta, int o
     launch_k((gather_kernel<IN, ENGRAM_BF16>), grid, dim3(threads), 0, s, z, n_tok, ta, e);
   else
     launch_k((gather_kernel<IN, ENGRAM_F32>), grid, dim3(threads), 0, s, z, n_tok, ta, e);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int IN, int OUT, bool HOT>
@@ -148,7 +148,7 @@ hipError_t launch_hashed_items(int64_t n_tok, const TableArgs& ta, void* e, cons
     launch_k((hashed_gather_kernel<IN, OUT, HOT, 2>), grid, dim3(threads), 0, s, n, ta, e, hs);
   else
     launch_k((hashed_gather_kernel<IN, OUT, HOT, 1>), grid, dim3(threads), 0, s, n, ta, e, hs);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <int IN, bool HOT>

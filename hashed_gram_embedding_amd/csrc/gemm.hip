@@ -188,7 +188,7 @@ hipError_t launch_project_kv(const void* e, const void* w, int64_t n_tok, int64_
                        static_cast<const float*>(e), static_cast<const float*>(w),
                        static_cast<float*>(kv), n_tok, static_cast<int>(n_out), static_cast<int>(d_mem));
   }
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace engram

@@ -46,7 +46,7 @@ hipError_t launch_hot_lookup(const int32_t* tokens, int64_t B, int64_t T, const 
   const int64_t blocks = (total + threads - 1) / threads;
   launch_k(hot_lookup_kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, s, tokens, B, T, hist, proj,
            max_n, vocab, h, out, err);
-  return hipGetLastError();
+  return launch_error();
 }
 
 HotBuild hot_build(const int32_t* keys, int64_t n_hot, int n, uint64_t seed, uint32_t* pilots,

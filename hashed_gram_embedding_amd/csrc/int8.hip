@@ -762,7 +762,7 @@ hipError_t launch_ring(const ProjectI8Args& a, hipStream_t s) {
   }
   const int64_t tf = (a.n_out + 63) / 64, tt = (a.n_tok + 63) / 64;
   launch_k(fn, dim3(static_cast<unsigned>(tf * tt)), dim3(256), ring_bytes(a.K), s, a, static_cast<int>(tf));
-  return hipGetLastError();
+  return launch_error();
 }
 
 // Fewer than 16 columns: one thread an output.
@@ -997,7 +997,7 @@ hipError_t launch_few(const ProjectI8Args& a, const void* e, hipStream_t s) {
   const bool shared = a.K > 1024 && groups <= kFewShared;
   const int64_t blocks = std::min(most, shared ? groups : (groups + kFewWaves - 1) / kFewWaves);
   launch_k(fn, dim3(static_cast<unsigned>(blocks)), dim3(64 * kFewWaves), bytes, s, a, e, shared ? kFewWaves : 1);
-  return hipGetLastError();
+  return launch_error();
 }
 
 template <typename OutT, int E_DT, int NB>
@@ -1033,7 +1033,7 @@ hipError_t launch_tile(const ProjectI8Args& a, hipStream_t s) {
   // one workgroup of 8 wavefronts per CU, or two of 4
   const int grid = static_cast<int>(std::min<int64_t>(256 * 8 / (WF * WT), (tf * tt + 7) / 8 * 8));
   launch_k(fn, dim3(grid), dim3(64 * WF * WT), kLds, s, a, static_cast<int>(tf), static_cast<int>(tt));
-  return hipGetLastError();
+  return launch_error();
 }
 
 // Which kernel a product of aligned operands takes.
@@ -1080,7 +1080,7 @@ AlignJob align_job(const int8_t* x, int8_t* y, int64_t rows, int64_t K) {
 }
 
 // Workgroups of 256 threads that a launch can have: it has fewer than 2^32
-// work-items (HIP runs the low 32 bits of a larger number, without an error).
+// work-items (launch_k).
 constexpr int64_t kMostGroups = (1 << 24) - 1;
 
 // More rows than a launch has workgroups for go in pieces; W's come with the first.
@@ -1088,7 +1088,7 @@ template <int DT, int N>
 hipError_t launch_quantize_n(QuantizeArgs a, AlignJob w, hipStream_t s) {
   constexpr int64_t per = N > 0 ? 4 : 1;   // rows of a workgroup
   const int chunks = static_cast<int>(i8_row_stride(a.cols) / 16);
-  if (w.groups >= kMostGroups) return hipErrorInvalidValue;
+  if (w.groups >= kMostGroups) return hipErrorInvalidConfiguration;
   for (int64_t left = a.rows; left > 0;) {
     const int64_t n = std::min(left, (kMostGroups - w.groups) * per);
     const dim3 grid(static_cast<unsigned>(w.groups + (n + per - 1) / per));
@@ -1096,7 +1096,7 @@ hipError_t launch_quantize_n(QuantizeArgs a, AlignJob w, hipStream_t s) {
     prof_stage("quantize_i8_kernel");
     if (w.groups > 0) launch_k((quantize_rows_kernel<DT, N, true>), grid, dim3(256), 0, s, a, w, chunks);
     else launch_k((quantize_rows_kernel<DT, N, false>), grid, dim3(256), 0, s, a, w, chunks);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_error();
     if (e != hipSuccess) return e;
     a.x = static_cast<const char*>(a.x) + n * a.cols * (DT == ENGRAM_BF16 ? 2 : 4);
     a.q += n * a.ldq;
@@ -1142,10 +1142,10 @@ bool project_i8_aligns(int64_t n_tok, int64_t K) { return K >= 16 && K % 16 != 0
 hipError_t launch_align_i8(const int8_t* w, int64_t w_rows, int8_t* w_out, const int8_t* q, int64_t q_rows, int8_t* q_out, int64_t K,
                            hipStream_t s) {
   const AlignJob a = align_job(w, w_out, w_rows, K), b = align_job(q, q_out, q_rows, K);
-  if (a.groups + b.groups > kMostGroups) return hipErrorInvalidValue;   // (copies of 2^38 bytes)
+  if (a.groups + b.groups > kMostGroups) return hipErrorInvalidConfiguration;   // (copies of 2^38 bytes)
   launch_k(align_rows_kernel, dim3(static_cast<unsigned>(a.groups + b.groups)), dim3(256), 0, s, a, b, static_cast<int>(K),
            static_cast<int>(i8_row_stride(K) / 16));
-  return hipGetLastError();
+  return launch_error();
 }
 
 namespace {
@@ -1162,7 +1162,7 @@ hipError_t launch_product(ProjectI8Args a, const void* e, int e_dtype, hipStream
       a.n_tok = std::min(piece, n_tok - t);
       prof_stage("project_i8_kernel");
       launch_k(project_i8_short_kernel<OutT>, dim3(static_cast<unsigned>((a.n_tok * a.n_out + 255) / 256)), dim3(256), 0, s, a);
-      const hipError_t err = hipGetLastError();
+      const hipError_t err = launch_error();
       if (err != hipSuccess) return err;
       a.q += piece * a.ldq;
       a.q_scale += piece;

@@ -94,7 +94,7 @@ hipError_t launch_bf16_pack(const uint16_t* w, int64_t rows, int64_t cols, uint1
   if (n == 0) return hipSuccess;
   launch_k(bf16_pack_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, w, rows,
            static_cast<int>(cols), packed);
-  return hipGetLastError();
+  return launch_error();
 }
 
 hipError_t launch_mx_pack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, uint8_t* packed,
@@ -104,7 +104,7 @@ hipError_t launch_mx_pack(const uint8_t* q, const uint8_t* scale, int64_t rows, 
   if (n == 0) return hipSuccess;
   launch_k(mx_pack_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, q, scale, rows,
            static_cast<int>(cols), packed);
-  return hipGetLastError();
+  return launch_error();
 }
 
 hipError_t launch_mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* q, uint8_t* scale,
@@ -116,7 +116,7 @@ hipError_t launch_mx_quantize(const void* x, int dtype, int64_t rows, int64_t co
     launch_k(mx_quantize_kernel<ENGRAM_BF16>, grid, dim3(256), 0, s, x, n8, q, scale);
   else
     launch_k(mx_quantize_kernel<ENGRAM_F32>, grid, dim3(256), 0, s, x, n8, q, scale);
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace engram

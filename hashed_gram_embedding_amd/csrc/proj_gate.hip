@@ -1057,7 +1057,7 @@ hipError_t launch_resident_k(const ProjGateArgs& a, dim3 grid, size_t lds, hipSt
     attr_set.fetch_or(bit);
   }
   launch_k(proj_gate_mx_resident_kernel<KK>, grid, dim3(64 * kResWaves), lds, s, a);
-  return hipGetLastError();
+  return launch_error();
 }
 
 hipError_t launch_resident(const ProjGateArgs& in, int groups, hipStream_t s) {
@@ -1099,7 +1099,7 @@ hipError_t launch_tf(ProjGateArgs a, hipStream_t s) {
     attr_set.fetch_or(bit);
   }
   launch_k((proj_gate_kernel<TF, MX, WT, NBUF, MIXED>), dim3(a.tiles_f * a.tiles_t), dim3(64 * WF * WT), lds, s, a);
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace
@@ -1172,7 +1172,7 @@ hipError_t launch_small(const ProjGateArgs& in, hipStream_t s) {
   }
   launch_k(proj_gate_small_kernel<MX>, dim3(static_cast<unsigned>(a.tiles_f * a.tiles_t)), dim3(64 * kSmallWaves),
            small_lds_bytes<MX>(), s, a);
-  return hipGetLastError();
+  return launch_error();
 }
 
 // a and b shaped for STK-token tiles (tiles_t counted in STK)
@@ -1192,7 +1192,7 @@ hipError_t launch_small2(const ProjGateArgs& a, const ProjGateArgs& b, hipStream
   const uint32_t na = static_cast<uint32_t>(a.tiles_f * a.tiles_t), nb = static_cast<uint32_t>(b.tiles_f * b.tiles_t);
   launch_k((proj_gate_small2_kernel<MX, STK>), dim3(na + nb), dim3(64 * kSmallWaves), small_lds_bytes<MX, STK>(), s,
            a, b, na);
-  return hipGetLastError();
+  return launch_error();
 }
 
 hipError_t launch_project_layers(const ProjGateArgs& in_a, const ProjGateArgs* in_b, hipStream_t s) {

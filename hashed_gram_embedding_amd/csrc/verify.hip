@@ -472,10 +472,9 @@ probs_join_kernel(ProbsArgs a, int segs, const Segment* __restrict__ part) {
   if (r.vt < a.V) out[r.vt] = of(xt) * inv;
 }
 
-// Rows of a launch: it has fewer than 2^32 work-items (HIP runs the low 32 bits
-// of a larger number, without an error).  More rows go in pieces of whole
-// sequences, or of a part of one: a piece's first row is at its first
-// temperature.
+// Rows of a launch: it has fewer than 2^32 work-items (launch_k).  More rows go
+// in pieces of whole sequences, or of a part of one: a piece's first row is at
+// its first temperature.
 constexpr int64_t kMostRows = 1 << 21;
 
 bool probs_splits(int64_t rows, int64_t V) { return rows <= 64 && V > 32768; }
@@ -489,11 +488,11 @@ hipError_t launch_probs_dt(const ProbsArgs& a, int64_t rows, bool split, void* w
     const dim3 wide(static_cast<unsigned>(rows * segs));
     prof_stage("token_probs_segments_kernel");
     launch_k(probs_segments_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<Segment*>(ws));
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_error();
     if (e != hipSuccess) return e;
     prof_stage("token_probs_join_kernel");
     launch_k(probs_join_kernel<DT>, wide, dim3(kSegThreads), 0, s, a, segs, static_cast<const Segment*>(ws));
-    return hipGetLastError();
+    return launch_error();
   }
   const dim3 grid(static_cast<unsigned>(rows));
   prof_stage("token_probs_kernel");
@@ -505,7 +504,7 @@ hipError_t launch_probs_dt(const ProbsArgs& a, int64_t rows, bool split, void* w
   else if (a.V <= 4096 * 16) launch_k((probs_kernel<DT, 1024, 16>), grid, dim3(1024), 0, s, a);
   else if (DT == ENGRAM_BF16 && a.V <= 4096 * 32) launch_k((probs_kernel<ENGRAM_BF16, 1024, 32>), grid, dim3(1024), 0, s, a);
   else launch_k(probs_long_kernel<DT>, grid, dim3(1024), 0, s, a);
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace
@@ -824,7 +823,7 @@ hipError_t launch_verify_dt(const VerifyArgs& a, int64_t S, hipStream_t s) {
   if (verify_splits(S, a.V)) {
     prof_stage("verify_parts_kernel");
     launch_k(verify_parts_kernel<DT>, dim3(static_cast<unsigned>(S * (kParts / kPartWaves))), dim3(64 * kPartWaves), 0, s, a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_error();
     if (e != hipSuccess) return e;
     prof_stage("verify_drafts_kernel");
     launch_k((verify_kernel<DT, true>), dim3(static_cast<unsigned>(S)), dim3(64 * kVerifyWaves), 0, s, a);
@@ -832,7 +831,7 @@ hipError_t launch_verify_dt(const VerifyArgs& a, int64_t S, hipStream_t s) {
     prof_stage("verify_drafts_kernel");
     launch_k((verify_kernel<DT, false>), dim3(static_cast<unsigned>(S)), dim3(64 * kVerifyWaves), 0, s, a);
   }
-  return hipGetLastError();
+  return launch_error();
 }
 
 }  // namespace

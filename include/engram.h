@@ -36,7 +36,8 @@
  *  - Status codes: ENGRAM_OK, ENGRAM_EINVAL (null or misaligned pointer, bad
  *    size, inconsistent descriptors, workspace too small),
  *    ENGRAM_EUNSUPPORTED (dtype combination or shape outside the supported
- *    set), ENGRAM_EHIP (a HIP runtime or launch error; its text is in
+ *    set), ENGRAM_EHIP (a HIP runtime or launch error, also a size whose kernel
+ *    would need 2^32 work-items or more in one launch; its text is in
  *    engram_last_error()).
  *  - bf16 is IEEE bfloat16; every rounding to it is to nearest, ties to even.
  */

@@ -456,3 +456,22 @@ def test_project_ahead_and_forward_projected_are_checked():
     assert st == eg.EUNSUPPORTED and "decode state" in msg
     st, msg = _status(L.engram_forward_projected, p, p, 1, 2, ctypes.byref(lay), None, None, None, p, 0, None)
     assert st == eg.EINVAL and "workspace" in msg
+
+
+def test_launches_past_32_bits_of_work_items_are_refused():
+    """HIP takes the work-items of a launch modulo 2^32 and reports nothing, so
+    sizes whose launch would have more are refused by name and nothing runs."""
+    L = eg.lib()
+    p = ctypes.c_void_p(0x10000)
+    hp, keep = _hash_params()
+    t, keep2 = _tables()
+    calls = [lambda: L.engram_hash_indices(p, 1, 1 << 30, None, ctypes.byref(hp), p, None),      # 4 tables: 2^32 threads
+             lambda: L.engram_gather(p, 1 << 29, ctypes.byref(t), eg.F32, p, None),              # 8 threads a token
+             lambda: L.engram_project_kv(p, p, 1 << 20, 8, 1 << 12, eg.F32, p, None),            # one an output
+             lambda: L.engram_quantize_mxfp8(p, eg.BF16, 1 << 30, 32, p, p, None)]
+    for i, call in enumerate(calls):
+        st, msg = _status(call)
+        assert st == eg.EHIP and "invalid configuration" in msg, (i, st, msg)
+    # the refusal is that call's own: the next one does not see it
+    st, msg = _status(L.engram_hash_indices, p, 0, 5, None, ctypes.byref(hp), p, None)
+    assert st == eg.OK
