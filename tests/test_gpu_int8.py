@@ -128,6 +128,31 @@ def test_the_most_outputs_of_short_rows(source):
         assert ((out[a:a + 4096].float() - ref).abs() <= (2.0 ** -8 + 2.0 ** -20) * ref.abs() + 2 * TINY).all(), a
 
 
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 2823, 700), (3, 4099, 77), (9, 1025, 515), (15, 3001, 40), (20, 4097, 515), (8, 3842, 330),
+                                  (5, 4101, 8192), (32, 4349, 8193), (2, 9997, 21)])
+def test_few_tokens_of_long_odd_rows(size, out_dtype):
+    """Rows of W at every alignment, longer than a wavefront's loads in flight
+    and few enough for a workgroup's wavefronts to share each: every code is its
+    own, so a column out of place shows."""
+    n, k, o = size
+    log(f"project_i8 shared odd rows {size} {out_dtype}")
+    rng = np.random.default_rng(n * 7 + k * 3 + o)
+    w, q = rng.integers(-128, 128, (o, k), dtype=np.int8), rng.integers(-128, 128, (n, k), dtype=np.int8)
+    ws, s = np.exp2(rng.uniform(-9, 3, o)).astype(np.float32), np.exp2(rng.uniform(-9, 3, n)).astype(np.float32)
+    out = eg.project_i8(torch.from_numpy(q).to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV),
+                        e_scale=torch.from_numpy(s).to(DEV), out_dtype=out_dtype)
+    ref = orc.project_i8(q, s, w, ws)
+    err = np.abs(to_f64(out) - ref)
+    assert np.all(err <= _bound(ref, out_dtype)), float(np.max(err - _bound(ref, out_dtype)))
+    if n <= 8:                                # float rows, quantised by the product itself
+        x, x64 = _rows(rng, n, k, "bf16")
+        rq, rs = orc.quantize_i8(x64)
+        out = eg.project_i8(x, torch.from_numpy(w).to(DEV), torch.from_numpy(ws).to(DEV), out_dtype=out_dtype)
+        ref = orc.project_i8(rq, rs, w, ws)
+        assert np.all(np.abs(to_f64(out) - ref) <= _bound(ref, out_dtype))
+
+
 SIZES = [(1, 16, 1), (1, 1024, 2000), (2, 64, 64), (3, 48, 65), (5, 17, 33), (16, 1024, 4100), (31, 15, 7), (33, 1, 5),
          (64, 1024, 256), (65, 128, 129), (130, 1000, 515), (200, 2823, 103), (257, 1024, 512), (300, 4096, 192),
          (1000, 320, 1031), (513, 2048, 2048), (33, 513, 66),

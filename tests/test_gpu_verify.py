@@ -185,6 +185,55 @@ def test_probs_of_logits_further_apart_than_their_type(dtype, rows, V):
             assert np.all(err <= rel * ref + 2.0 ** -125), (temp, r, float(np.max(err / np.maximum(rel * ref, 1e-300))))
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 40001), ("bf16", 65536), ("bf16", 65537), ("bf16", 100003), ("bf16", 128000),
+                                     ("bf16", 131075), ("bf16", 262145), ("f32", 32770), ("f32", 65535), ("f32", 65539),
+                                     ("f32", 200003)])
+def test_probs_of_a_batch_of_long_rows(dtype, V):
+    """More rows than are split over workgroups, at ordinary temperatures: the
+    forms that hold a long row in registers and the one that reads it twice.
+    Rows of zeros, with NaN or +inf, masked and tied ones, greedy ones, and rows
+    whose weight lies in the entries behind the last four."""
+    log(f"token_probs batch {dtype} V={V}")
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = (3 * torch.randn(3, 25, V, generator=g, device=DEV)).to(TYPES[dtype])
+    low = torch.finfo(TYPES[dtype]).min
+    x[:, 0] = -INF
+    x[:, 1] = -INF
+    x[:, 1, V - 1] = -5.0
+    x[:, 2, 17] = NAN
+    x[:, 3, V - 1] = NAN
+    x[:, 4, V - 1] = INF
+    x[:, 5] = low
+    x[:, 6, V // 3:] = low
+    x[:, 7] = -2.5                           # all tied
+    x[:, 8] = x[:, 8].sort(dim=-1).values    # the running maximum moves all the way
+    x[:, 9] = x[:, 9].sort(dim=-1, descending=True).values
+    x[:, 10, V - V % 4 - 1:] = 24.0          # most of the weight at the very end
+    x[:, 11, V - 1] = 22.0
+    x[:, 12, :V - 1] = -INF
+    x[:, 13] = -INF
+    x[:, 13, ::4096] = 0.0
+    x[:, 14, V - 2:] = x[:, 14].max(dim=-1, keepdim=True).values
+    x[:, 15, 40:] = -INF
+    t = torch.tensor([0.7, 0.0, 1.9], device=DEV)
+    p = eg.token_probs(x, t)
+    a, got = x.double().cpu().numpy(), p.double().cpu().numpy()
+    for s in range(3):
+        temp = float(t[s])
+        for r in range(25):
+            ref, row = orc.token_probs(a[s, r], temp), a[s, r]
+            assert np.array_equal(np.isnan(ref), np.isnan(got[s, r])), (s, r)
+            if np.isnan(ref).any():
+                continue
+            rel = 0.0
+            if temp > 0 and np.isfinite(row.max()):
+                arg = np.where(np.isfinite(row), (row.max() - row) / temp / math.log(2), 0.0)
+                own = 2.0 ** -24 * (4 * math.log(2) * arg + 4)
+                rel = own + np.sum(ref * own) + 2.0 ** -24 * (_chain(V) + 2)
+            err = np.abs(got[s, r] - ref)
+            assert np.all(err <= rel * ref + 2.0 ** -125), (s, r, float(np.max(err - rel * ref)))
+
+
 def test_the_longest_rows():
     """V = 2^31 - 1, the documented limit of both calls: entries at the very end
     of a row, found through offsets past 32 bits."""
