@@ -1349,7 +1349,8 @@ ENGRAM_API engram_status engram_project_i8(const void* e, engram_dtype e_dtype, 
 namespace {
 
 // Workspace of a layer call with Step 5 in 8-bit integers or over a draft
-// (then v and gamma are the caller's): rows, projections, statistics, codes.
+// (then v and gamma are the caller's; own_v, the call without a draft, is
+// always with i8): rows, projections, statistics, codes.
 struct DraftWorkspace {
   void* e;
   ComputeWorkspace f;
@@ -1360,16 +1361,12 @@ DraftWorkspace carve_draft(Carve& c, int64_t n_tok, const engram_layer* L, bool 
   const int M = L->gc.branches, d = L->gc.d;
   const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim;
   const bool fused = use_fused(L);
+  const int64_t columns = !fused ? d : i8 ? engram::project_i8_gate_columns(n_tok, d_mem, d, M) : engram::kProjGateTileF;
   DraftWorkspace w{};
   w.e = c.take<char>(rows_bytes(n_tok, L));
-  if (own_v && !i8) {
-    w.f = carve_compute(c, n_tok, L);
-  } else {
-    const int64_t columns = !fused ? d : i8 ? engram::project_i8_gate_columns(n_tok, d_mem, d, M) : engram::kProjGateTileF;
-    if (own_v) w.f.kv = c.take<float>(static_cast<size_t>(n_tok) * (fused ? 1 : 1 + M) * d);
-    w.f.stats = c.take<float4>(static_cast<size_t>(n_tok) * (1 + M) * (d / columns));
-    if (own_v) w.f.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
-  }
+  if (own_v) w.f.kv = c.take<float>(static_cast<size_t>(n_tok) * (fused ? 1 : 1 + M) * d);
+  w.f.stats = c.take<float4>(static_cast<size_t>(n_tok) * (1 + M) * (d / columns));
+  if (own_v) w.f.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
   if (i8 && n_tok > 0 && !gathers_i8(L)) {
     if (fused) {   // rows of codes, aligned as they are, at every size
       w.codes.codes = c.take<int8_t>(static_cast<size_t>(n_tok) * d_mem);
