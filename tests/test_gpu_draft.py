@@ -2,6 +2,7 @@
 the kept tokens, and a speculative decode loop of all the operators together
 against decoding token by token."""
 import ctypes
+import dataclasses
 
 import numpy as np
 import pytest
@@ -92,6 +93,115 @@ def test_draft_then_commit_equals_forward(config, hdtype, S, T, int8):
             at = [(int(ref["pos"][s]) + r) % span for r in range(span)]
             got = part.conv[s][:, at].double().cpu().numpy()
             assert np.all(np.abs(got - ref["u"][s]) <= 2.0 ** -24 * np.abs(ref["u"][s]) + 2.0 ** -149), (k, s)
+
+
+def _odd_layer(w, kernel_w, dilation):
+    """The workload's layer with another short conv."""
+    lay = w.layers[0]
+    rng = np.random.default_rng(kernel_w * 10 + dilation)
+    conv = (0.1 * rng.standard_normal((lay.branches, lay.d, kernel_w))).astype(np.float32)
+    return dataclasses.replace(lay, conv_w=conv, kernel_w=kernel_w, dilation=dilation)
+
+
+SHAPES = [(dict(), 300, 8, (4, 3)), (dict(branches=4, d=256), 40, 60, (4, 3)), (dict(d=256), 3, 1, (4, 3)),
+          (dict(branches=2, d=384), 5, 7, (2, 1)), (dict(d=128), 4, 30, (8, 3)), (dict(max_n=4, heads=4, dim=32, d=256), 6, 5, (3, 5)),
+          (dict(max_n=2, heads=4, d=256), 6, 5, (4, 2)), (dict(d=4096), 3, 4, (4, 3)), (dict(branches=4, d=1024), 260, 5, (4, 3)),
+          (dict(d=192, heads=4), 5, 9, (4, 3))]
+
+
+# (MXFP8 layers have d a multiple of 128)
+@pytest.mark.parametrize("shape,S,T,conv,form", [(*c, f) for c in SHAPES for f in ("bf16", "mxfp8", "int8")
+                                                 if f != "mxfp8" or c[0].get("d", 1024) % 128 == 0])
+def test_draft_of_other_layers(shape, S, T, conv, form):
+    """Other branch counts, widths, orders, convs and forms of Step 5, over
+    chunks of one token to many: forward_draft and a commit of all tokens equal
+    the forward call bit for bit, and a commit of some the first of them."""
+    log(f"draft {shape} S={S} T={T} conv={conv} {form}")
+    pre = 5
+    w = inputs.make_shape(S, T + pre, **shape)
+    lay = _odd_layer(w, *conv)
+    L = eg.Layer(lay, "bf16", DEV, mxfp8=form == "mxfp8")
+    w8 = eg.Int8Weights(L) if form == "int8" else None
+    span, max_n, M = (lay.kernel_w - 1) * lay.dilation, lay.hash.max_n, lay.branches
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    H = eg.to_device(w.H, "bf16", DEV)
+    run = (lambda t, h, st, **k: eg.forward_i8(t, h, L, w8, state=st, **k)) if w8 is not None else \
+        (lambda t, h, st, **k: eg.forward(t, h, L, state=st, **k))
+    st = eg.DecodeState(S, max_n, M, span, lay.d, DEV)
+    run(tok[:, :pre].contiguous(), H[:, :pre].contiguous(), st)
+    before, ref = (_state_like(st, S, max_n, M, span, lay.d) for _ in range(2))
+    chunk = tok[:, pre:].contiguous()
+    hr, h = (H[:, pre:].clone(memory_format=torch.contiguous_format) for _ in range(2))
+    ar, yr = run(chunk, hr, ref, want_alpha=True, want_y=True)
+    draft = eg.Draft(S, T, L, DEV)
+    a, y = eg.forward_draft(chunk, h, L, st, draft, w8=w8, want_alpha=True, want_y=True)
+    assert _same(h, hr) and _same(a, ar) and _same(y, yr)
+    assert torch.equal(st.ids, before.ids) and torch.equal(st.pos, before.pos) and _same(st.conv, before.conv)
+    full = _state_like(st, S, max_n, M, span, lay.d)
+    eg.commit_draft(chunk, L, draft, torch.full((S,), T + 3, dtype=torch.int32, device=DEV), full)
+    assert torch.equal(full.ids, ref.ids) and torch.equal(full.pos, ref.pos) and _same(full.conv, ref.conv)
+
+    u = (draft.v[:, :lay.d].view(S, T, 1, lay.d) * draft.gamma.view(S, T, M, 1)).permute(0, 2, 1, 3)
+    acc = torch.arange(S, dtype=torch.int32, device=DEV) % (T + 1) - 1
+    eg.commit_draft(chunk, L, draft, acc, st)
+    k = acc.long() + 1
+    assert torch.equal(st.pos, before.pos + k.int())
+    ids = torch.cat([before.ids, torch.from_numpy(lay.hash.proj).to(DEV)[chunk.long()]], 1)
+    assert torch.equal(st.ids, ids.gather(1, k[:, None] + torch.arange(max_n - 1, device=DEV)))
+    for s in range(S):
+        want = before.conv[s].clone()
+        for t in range(int(k[s])):
+            want[:, (pre + t) % span] = u[s, :, t]
+        assert torch.equal(st.conv[s], want), s
+
+
+def test_speculative_calls_of_the_debug_build():
+    """Raw ids outside the vocabulary are clamped and reported by the debug
+    build's draft, commit and int8 calls; clean ones set no bit and give the
+    release build's results."""
+    log("debug build: speculative calls")
+    from hashed_gram_embedding_amd import build as bld
+    release = eg.lib()
+    S, T = 7, 4
+    w = inputs.make_config(3, B=S, T=T, layers=1, rows_per_table=997)
+    lay = w.layers[0]
+    V = lay.hash.vocab
+    bad = np.ascontiguousarray(w.tokens).copy()
+    bad[0, 1], bad[3, 3], bad[6, 0] = -5, V, V + 100
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    h0 = eg.to_device(w.H, "bf16", DEV)
+    acc = torch.full((S,), T - 1, dtype=torch.int32, device=DEV)
+
+    def chunk(tokens, read):
+        tok = torch.from_numpy(tokens).to(DEV)
+        st, h, draft, bits = eg.DecodeState(S, 3, 1, 9, lay.d, DEV), h0.clone(), eg.Draft(S, T, L, DEV), []
+        eg.forward_draft(tok, h, L, st, draft, w8=w8)
+        bits.append(read())
+        eg.commit_draft(tok, L, draft, acc, st)
+        bits.append(read())
+        one = h0[:, :1].clone(memory_format=torch.contiguous_format)
+        eg.forward_i8(tok[:, :1].contiguous(), one, L, w8, state=st)
+        bits.append(read())
+        return [h, one, st.ids, st.pos, st.conv], bits
+
+    clamped = np.clip(bad, 0, V - 1)
+    want, _ = chunk(clamped, lambda: 0)
+    got, _ = chunk(bad, lambda: 0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dbg = eg.load_library(bld.LIB_DEBUG)
+    eg._lib = dbg
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    try:
+        eg.debug_set_error_word(word)
+        clean, bits = chunk(clamped, eg.debug_read_errors)
+        assert bits == [0, 0, 0] and all(torch.equal(a, b) for a, b in zip(clean, want))
+        got, bits = chunk(bad, eg.debug_read_errors)
+        assert bits == [eg.ERR_TOKEN] * 3 and all(torch.equal(a, b) for a, b in zip(got, want))
+    finally:
+        torch.cuda.synchronize()
+        dbg.engram_debug_set_error_word(None)
+        eg._lib = release
 
 
 def test_commit_in_a_graph():

@@ -2,6 +2,8 @@
 product's sum is exact, so an output is off by the float32 conversion of the
 sum and two multiplications (3 * 2^-24, second-order terms within a fourth),
 and by half a bf16 step (2^-8) more where it is stored in bf16."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -90,9 +92,10 @@ def test_quantize_the_longest_row():
     assert not any(bool(p.any()) for p in q[0].split(1 << 28))
 
 
-@pytest.mark.parametrize("rows,cols,dtype", [(2 ** 26 + 5, 4, "bf16"), (2 ** 26 + 5, 9, "f32")])
+@pytest.mark.parametrize("rows,cols,dtype", [(2 ** 26 + 5, 4, "bf16"), (2 ** 26 + 5, 9, "f32"), (2 ** 20 + 3, 4097, "bf16"),
+                                             (2 ** 19 + 9, 8203, "bf16")])
 def test_quantize_the_most_rows(rows, cols, dtype):
-    """More rows than one launch can have."""
+    """More rows than one launch can have, more codes than 32 bits count."""
     log(f"quantize_i8 {rows} rows")
     g = torch.Generator(device=DEV).manual_seed(6)
     pattern = torch.randn(4099, cols, generator=g, device=DEV).to(TYPES[dtype])
@@ -228,6 +231,27 @@ def test_outputs_past_32_bits(k, n_out, out_dtype):
         assert torch.equal(out[a:b], eg.project_i8(q[a:b].clone(), w, ws, e_scale=qs[a:b].clone(), out_dtype=out_dtype)), a
 
 
+@pytest.mark.parametrize("n,k,o", [(3, 16384, 140001), (20, 16383, 140001), (300, 16384, 140001), (300, 16385, 140001), (140001, 16384, 70),
+                                   (140001, 16385, 70)])
+def test_operands_past_32_bits(n, k, o):
+    """Operands of more than 2^31 bytes: outputs at both ends and around the
+    border against the same rows multiplied alone."""
+    log(f"project_i8 {n} x {k} x {o}")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q = torch.randint(-127, 128, (n, k), generator=g, dtype=torch.int8, device=DEV)
+    w = torch.randint(-127, 128, (o, k), generator=g, dtype=torch.int8, device=DEV)
+    qs, ws = torch.rand(n, generator=g, device=DEV), torch.rand(o, generator=g, device=DEV)
+    out = eg.project_i8(q, w, ws, e_scale=qs, out_dtype="f32")
+    for t in {0, max(n - 40, 0)}:
+        for a in {0, min(131050, o - 64), o - 64}:
+            tt = slice(t, min(t + 40, n))
+            part = eg.project_i8(q[tt].clone(), w[a:a + 64].clone(), ws[a:a + 64].clone(), e_scale=qs[tt].clone(), out_dtype="f32")
+            assert torch.equal(out[tt, a:a + 64], part), (t, a)
+    if n > 131072:
+        a = slice(131060, 131090)
+        assert torch.equal(out[a], eg.project_i8(q[a].clone(), w, ws, e_scale=qs[a].clone(), out_dtype="f32"))
+
+
 def test_unaligned_operands_are_refused():
     log("project_i8 unaligned operands")
     b = torch.zeros(40 * 64 + 16, dtype=torch.int8, device=DEV)
@@ -347,6 +371,36 @@ def test_layer_rows_of_a_hot_tier_and_beside_mxfp8(kw):
     eg.forward_draft(tok, H, plain, st, draft, w8=w8)
     assert torch.equal(draft.v[:, :lay.d], eg.project_i8(q, w8.q[:lay.d], w8.scale[:lay.d], e_scale=s, out_dtype="f32"))
     assert not torch.equal(H, outs[1])          # the tier's rows differ from the tables'
+
+
+@pytest.mark.parametrize("table", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("B,T", [(3, 50), (2, 900)])
+def test_layer_rows_through_a_cache_are_quantised_exactly(table, B, T):
+    """Tables of every type behind an HBM row cache, accesses counted: the codes
+    are those of the rows that the bf16 gather gives, the counts those of it."""
+    log(f"int8 rows, cache, {table} {B}x{T}")
+    w = inputs.make_config(1, B=B, T=T, rows_per_table=997)
+    lay = w.layers[0]
+    hp, rng = lay.hash, np.random.default_rng(4)
+    shape = (lay.tables.total_rows, lay.tables.dim)
+    rows = {"f32": lambda: rng.standard_normal(shape).astype(np.float32), "bf16": lambda: lay.tables.rows,
+            "i8": lambda: rng.integers(-127, 128, shape, dtype=np.int8)}[table]()
+    scale = np.exp2(rng.uniform(-9, 0, shape[0])).astype(np.float32) if table == "i8" else None
+    lay = dataclasses.replace(lay, tables=dataclasses.replace(lay.tables, rows=rows, scale=scale, dtype=table))
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV)
+    L.set_cache(*eg.cache_build(tok[:, ::3].contiguous(), L, shape[0] // 20))
+    counts = [torch.zeros(shape[0], dtype=torch.int32, device=DEV) for _ in range(2)]
+    e = torch.empty((B * T, L.d_mem), dtype=torch.bfloat16, device=DEV)
+    L.set_access_counts(counts[0])
+    eg.retrieve(tok, L, e)
+    L.set_access_counts(counts[1])
+    draft = eg.Draft(B, T, L, DEV)
+    eg.forward_draft(tok, eg.to_device(w.H, "bf16", DEV), L, eg.DecodeState(B, hp.max_n, 1, 9, lay.d, DEV), draft, w8=w8)
+    q, s = eg.quantize_i8(e)
+    assert torch.equal(draft.v[:, :lay.d], eg.project_i8(q, w8.q[:lay.d], w8.scale[:lay.d], e_scale=s, out_dtype="f32"))
+    assert torch.equal(*counts) and int(counts[0].sum()) == B * T * hp.n_tables
 
 
 def test_layer_decode_state():

@@ -264,6 +264,35 @@ def test_the_longest_rows():
         assert acc.tolist() == [1] and tok.tolist() == [[n - 1, want, -1]], u
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_batches_past_32_bits(dtype):
+    """More than 2^31 (and 2^32) entries: the last rows and sequences as alone."""
+    log(f"token_probs and verify_drafts past 32 bits {dtype}")
+    V, G = 128000, 8
+    g = torch.Generator(device=DEV).manual_seed(11)
+    S = 3800 if dtype == "bf16" else 2000
+    x = torch.empty((S, G + 1, V), dtype=TYPES[dtype], device=DEV)
+    for part in x.split(200):
+        part.normal_(generator=g)
+    t = torch.rand(S, generator=g, device=DEV) + 0.5
+    p = eg.token_probs(x, t)
+    for a in (0, S // 2, S - 3):
+        assert torch.equal(p[a:a + 3], eg.token_probs(x[a:a + 3].repeat(3, 1, 1), t[a:a + 3].repeat(3))[:3]), a   # (81 rows: the same form)
+    d = torch.randint(0, V, (S, G), generator=g, device=DEV, dtype=torch.int32)
+    ua, us = 1e-7 * torch.rand(S, G, generator=g, device=DEV), torch.rand(S, generator=g, device=DEV)
+    for q in (None, x[:, :G].contiguous()):
+        tgt = x if q is None else p.to(TYPES[dtype])
+        if q is not None:
+            q.abs_()
+        tok, acc = eg.verify_drafts(tgt, q, d, ua, us)
+        for a in (0, S // 2, S - 3):
+            rows = slice(a, a + 3)
+            et, ea = eg.verify_drafts(tgt[rows].clone(), None if q is None else q[rows].clone(), d[rows].clone(), ua[rows].clone(),
+                                      us[rows].clone())
+            assert torch.equal(tok[rows], et) and torch.equal(acc[rows], ea), a
+        assert int(acc.max()) > 0
+
+
 def test_probs_of_padded_rows():
     """Rows of a padded vocabulary: the padding is not read, whatever it holds."""
     log("token_probs padded")
