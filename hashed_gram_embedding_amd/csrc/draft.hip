@@ -10,10 +10,12 @@ namespace {
 constexpr int kThreads = 1024;
 
 // One workgroup per sequence: pos and ids change when everyone has read them.
-// With k kept tokens the ring's slots hold the
-// conv inputs u_t = gamma_t v_t of the last min(k, span) of them, the
-// position p = pos + t in slot p % span (as after k steps of one token); ids
-// become the last N-1 compressed ids of (ids, kept tokens); pos grows by k.
+// With k kept tokens the ring's slots hold the conv inputs u_t = gamma_t v_t of
+// the last min(k, span) of them, the position p = pos + t in slot p % span (as
+// after k steps of one token); ids become the last N-1 compressed ids of (ids,
+// kept tokens); pos grows by k.  The launch lasts as long as the sequence that
+// keeps most: 256 sequences of 8 tokens, d = 1024, 4 branches 4.4 us where each
+// keeps one, 8.4 where each keeps all, 7.9 where they keep 1 to 8.
 __global__ void __launch_bounds__(kThreads)
 commit_draft_kernel(const float* __restrict__ v, int64_t v_stride, const float* __restrict__ gamma, int64_t T,
                     GateConvArgs g, StateArgs st, const int32_t* __restrict__ tokens, const int32_t* __restrict__ proj,

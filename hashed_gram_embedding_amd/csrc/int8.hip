@@ -61,7 +61,9 @@ struct CodeRow {
 // Rows of fewer than 512 N + 8 columns: one wavefront a row, runs of 8, every
 // value read once, all loads in flight together; up to 7 columns behind the
 // last run are the first lanes' own.  A row of zeros has scale 0, one holding
-// an infinity or a NaN codes 0 and scale NaN.
+// an infinity or a NaN codes 0 and scale NaN.  Bound by memory: bf16 rows of
+// 32768 x 1024 19.7 us (5.1 TB/s), 65536 x 4100 165 (4.9), float32 27.0 (6.2) and
+// 254 (5.3); 4096 x 1024 bf16 4.5, one chain of loads and the launch.
 template <int DT, int N>
 __device__ __forceinline__ void quantize_rows(int64_t group, const void* __restrict__ x, int64_t rows, int cols, int8_t* __restrict__ q,
                                               int64_t ldq, int tail, float* __restrict__ scale) {
@@ -101,7 +103,9 @@ __device__ __forceinline__ void quantize_rows(int64_t group, const void* __restr
 }
 
 // Longer rows: one workgroup a row, which reads it twice (the second time
-// from the L2).
+// from the L2, as far as the rows in work fit there: bf16 32768 x 8192 154 us
+// (5.2 TB/s by one read), 8192 x 16384 97 (4.2), 8192 x 16387 118 (3.4: runs of 8
+// at odd addresses), 4096 x 131071 621 (2.6)).
 template <int DT>
 __device__ __forceinline__ void quantize_long(int64_t row, const void* __restrict__ x, int cols, int8_t* __restrict__ q, int64_t ldq,
                                               int tail, float* __restrict__ scale) {
@@ -328,7 +332,8 @@ __device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
 // token and run of 64 x (2 or 4) columns, so that the keys' float32 rows are
 // neither written nor read again (4096 tokens, one branch: 25.3 us for the
 // product and the sums apart, 18.1 together; 8192 tokens, 4 branches, with the
-// conv 148 against 116).
+// conv 148 against 116).  These forms spill 52 (256 x 256) and 36 bytes a lane
+// around the epilogue.
 constexpr int kBand = 8;
 
 template <typename OutT, int TF, int TT, int WF, int WT, bool GATE>
@@ -791,7 +796,9 @@ project_i8_short_kernel(ProjectI8Args a) {
 // their own (32 x 1024 x 2048 13.4 against 11.3 us, 16 x 4096 x 2000 17.9 against
 // 16.1).
 // 1 x 1024 x 128000 takes 24.3 us (5.4 TB/s), 32 x 1024 x 128000 29.4; past 32
-// tokens the tiles are faster (64 tokens: 46 against 36 us).
+// tokens the tiles are faster (64 tokens: 46 against 36 us).  Held to 128
+// registers (4 wavefronts a SIMD) the aligned form of up to 16 tokens spills 20
+// bytes a lane.
 constexpr int kFewWaves = 8;
 constexpr int kFewLds = 140 << 10;
 constexpr int kFewShared = 512;   // groups up to which a workgroup shares each

@@ -61,7 +61,15 @@ __device__ __forceinline__ double at_lane(double x, int lane) {
 //
 // Bound by memory: a row is read once and written once, by one workgroup that
 // keeps it in registers between its maximum, its sum and its output (N runs
-// of 4 values a thread, all loads in flight together).
+// of 4 values a thread, all loads in flight together).  The longest bf16 rows
+// (N = 32) need more registers than the 128 a thread has: 84 bytes a lane are
+// spilled, 16% more bytes written (2048 x 128000: 340 us, 327 by the bytes of
+// the row and its outputs alone).
+//
+// The exponent (l - max) log2(e) / T has four roundings (the difference, the
+// constant, the division and the product; the formula itself two) and exp2 is the
+// hardware's, one unit off at most: a single probability of exponent x (in powers
+// of two) is within (4 ln 2 |x| + 4) 2^-24 of its value, beside the sum's error.
 
 struct ProbsArgs {
   const void* logits;
@@ -272,7 +280,8 @@ probs_kernel(ProbsArgs a) {
 
 // Rows too long for the registers: one pass for the maximum and the sum (each
 // thread's sum is kept relative to its own maximum so far), a second one for
-// the output.
+// the output, whose reads mostly meet the caches (2048 x 128000 float32 492 us,
+// 436 by the bytes of one read and one write; 2048 x 151936 bf16 413, 388).
 template <int DT>
 __global__ void __launch_bounds__(1024)
 probs_long_kernel(ProbsArgs a) {
@@ -477,6 +486,16 @@ probs_join_kernel(ProbsArgs a, int segs, const Segment* __restrict__ part) {
 // its first temperature.
 constexpr int64_t kMostRows = 1 << 21;
 
+// Few long rows are split.  One workgroup a row / split, in us (float32; bf16
+// changes sides within one column of it):
+//   V        1 row       16          64          96          128         200
+//   32001    6.1/8.0     6.5/8.4     7.3/9.3     8.0/10.5    8.9/11.4    10.5/15.0
+//   40000    8.3/7.9     8.8/8.5     10.0/10.1   11.0/11.2   11.8/13.0   15.0/17.2
+//   65536    9.1/8.0     9.7/8.7     11.6/11.4   14.2/14.5   17.0/17.2   21.7/27.4
+//   128000   22.8/8.1    23.7/9.3    27.4/17.6   30.5/25.4   34.8/31.8   48.0/49.0
+//   200000   36.4/8.1    37.5/10.7   43.4/27.3   46.9/38.5   53.4/48.9   77.6/74.6
+// (From 128000 on 65 to 128 rows would gain by it too; up to 64 every length past
+// 32768 does, 40000 by nothing at 64.)
 bool probs_splits(int64_t rows, int64_t V) { return rows <= 64 && V > 32768; }
 
 int probs_segments(int64_t V) { return static_cast<int>((V + kSegment - 1) / kSegment); }

@@ -485,8 +485,9 @@ engram_status engram_quantize_i8(const void* x, engram_dtype dtype, int64_t rows
 
 /* out[t][o] = (sum_c q[t][c] w[o][c]) * e_scale[t] * w_scale[o]: the product
  * of W in 8-bit integers with one scale per token and one per output channel.
- * The sum is exact (int32); the two multiplications are in float32, and BF16
- * output rounds once more.
+ * The sum is exact (int32); its conversion to float32 and the two
+ * multiplications, in this order, each round to float32, and BF16 output rounds
+ * once more.
  *   e        device [n_tok][d_mem], 16-byte aligned: int8 codes with e_scale
  *            [n_tok] (e_dtype I8), or F32 or BF16 rows, quantised on the way
  *            as engram_quantize_i8 does (e_scale NULL)
@@ -512,9 +513,9 @@ typedef struct engram_i8_weights {
 
 /* engram_forward with Step 5 as the 8-bit integer product: the gathered rows
  * (in the layer's hdtype) are quantised per token, the projections are
- * float32.  Arguments otherwise as engram_forward; L's own w, w_mx and
- * w_packed are not read.  ws: engram_forward_i8_workspace() bytes, 256-byte
- * aligned. */
+ * float32.  Arguments otherwise as engram_forward (L->w is checked as there);
+ * L's own w, w_mx and w_packed are not read.  ws:
+ * engram_forward_i8_workspace() bytes, 256-byte aligned. */
 size_t engram_forward_i8_workspace(int64_t B, int64_t T, const engram_layer* L);
 engram_status engram_forward_i8(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
                                 const engram_i8_weights* w, engram_decode_state* st, float* alpha_out,
