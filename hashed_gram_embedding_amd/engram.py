@@ -767,7 +767,8 @@ class Draft:
             raise ValueError(f"v must be [B*T, at least d={layer.d}]")
         _check_tensor("v", self.v, _F32, (B * T, self.v.shape[1]), dev)
         _check_tensor("gamma", self.gamma, _F32, (B * T, layer.M), dev)
-        self.s = DraftStruct(self.v.data_ptr(), self.v.shape[1], self.gamma.data_ptr())
+        self.M, self.columns = layer.M, self.v.shape[1]
+        self.s = DraftStruct(self.v.data_ptr(), self.columns, self.gamma.data_ptr())
 
 
 def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, state: Optional["DecodeState"]):
@@ -793,8 +794,8 @@ def _check_draft(draft: Draft, B: int, T: int, layer: Layer, dev):
         raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
     if draft.v.device != dev:
         raise ValueError(f"the draft is on {draft.v.device}, the tokens are on {dev}")
-    if draft.gamma.shape[1] != layer.M or draft.v.shape[1] < layer.d:
-        raise ValueError(f"the draft is for a layer of {draft.gamma.shape[1]} branches with rows of {draft.v.shape[1]}, "
+    if draft.M != layer.M or draft.columns < layer.d:
+        raise ValueError(f"the draft is for a layer of {draft.M} branches with rows of {draft.columns}, "
                          f"the layer has {layer.M} of d={layer.d}")
 
 
