@@ -790,13 +790,15 @@ def _check_chunk(tokens: torch.Tensor, H: Optional[torch.Tensor], layer: Layer, 
 
 
 def _check_draft(draft: Draft, B: int, T: int, layer: Layer, dev):
+    g = layer.li
+    if draft.B == B and draft.T == T and draft.M == g.branches and draft.columns >= g.d and draft.v.device == dev:
+        return
     if (draft.B, draft.T) != (B, T):
         raise ValueError(f"the draft is for {draft.B} x {draft.T} tokens, not {B} x {T}")
     if draft.v.device != dev:
         raise ValueError(f"the draft is on {draft.v.device}, the tokens are on {dev}")
-    if draft.M != layer.M or draft.columns < layer.d:
-        raise ValueError(f"the draft is for a layer of {draft.M} branches with rows of {draft.columns}, "
-                         f"the layer has {layer.M} of d={layer.d}")
+    raise ValueError(f"the draft is for a layer of {draft.M} branches with rows of {draft.columns}, "
+                     f"the layer has {g.branches} of d={g.d}")
 
 
 def _check_w8(w8: Int8Weights, layer: Layer, dev):
