@@ -1,6 +1,7 @@
 """GPU: the layer over a drafted chunk with the state only read, the commit of
 the kept tokens, and a speculative decode loop of all the operators together
 against decoding token by token."""
+import concurrent.futures
 import ctypes
 import dataclasses
 
@@ -377,3 +378,112 @@ def test_speculative_decode_loop():
                 # order in a one-token launch (up to 4 * 1024 roundings through the gate and the norm)
                 a, b = st[0].conv[s], ref[0].conv[s]
                 assert torch.all((a - b).abs() <= 4096 * 2.0 ** -24 * b.abs() + 2.0 ** -126), s
+
+
+def _guarded(shape, dtype, fill):
+    """A tensor in the middle of a larger allocation: (tensor, check that its surroundings still hold `fill`)."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 128,), fill, dtype=dtype, device=DEV)
+    return buf[64:64 + n].view(shape), lambda: bool((buf[:64] == fill).all() and (buf[64 + n:] == fill).all())
+
+
+@pytest.mark.parametrize("S,T,V", [(3, 4, 515), (2, 5, 40001), (70, 1, 40001), (5, 3, 100003), (1, 1, 3)])
+def test_nothing_beside_the_outputs_is_written(S, T, V):
+    """Outputs in the middle of larger buffers: what lies around them, states of
+    other sequences among it, stays."""
+    log(f"guarded outputs {S} x {T} x {V}")
+    lib, s = eg.lib(), torch.cuda.current_stream().cuda_stream
+    x = torch.randn(S, T, V, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        p, whole = _guarded((S, T, V), torch.float32, 7.0)
+        eg.token_probs(x.to(dtype), probs=p)
+        assert whole() and torch.allclose(p.sum(-1), torch.ones(S, T, device=DEV), atol=1e-4)
+        xq = x.to(dtype).view(S * T, V)
+        q, q_whole = _guarded((S * T, V), torch.int8, 99)
+        sc, sc_whole = _guarded((S * T,), torch.float32, 7.0)
+        assert lib.engram_quantize_i8(xq.data_ptr(), eg._DT_OF[dtype], S * T, V, q.data_ptr(), sc.data_ptr(), s) == eg.OK
+        want = eg.quantize_i8(xq)
+        assert q_whole() and sc_whole() and torch.equal(q, want[0]) and torch.equal(sc, want[1])
+    G = T - 1
+    d = torch.randint(0, V, (S, G), dtype=torch.int32, device=DEV)
+    ua, us = torch.rand(S, G, device=DEV), torch.rand(S, device=DEV)
+    want = eg.verify_drafts(p, None, d, ua, us)
+    tok, tok_whole = _guarded((S, T), torch.int32, -77)
+    acc, acc_whole = _guarded((S,), torch.int32, -77)
+    need = lib.engram_verify_drafts_workspace(S, V)
+    ws, ws_whole = _guarded((need + 256,), torch.uint8, 5)
+    base = (ws.data_ptr() + 255) // 256 * 256
+    assert lib.engram_verify_drafts(p.data_ptr(), None, eg.F32, d.data_ptr(), None, ua.data_ptr(), us.data_ptr(), S, G, V, tok.data_ptr(),
+                                    acc.data_ptr(), base if need else None, need, s) == eg.OK
+    assert tok_whole() and acc_whole() and ws_whole() and torch.equal(tok, want[0]) and torch.equal(acc, want[1])
+
+    w = inputs.make_shape(S, T, d=128, branches=2, heads=4)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    tk, h0 = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV), eg.to_device(w.H, "bf16", DEV)
+    v, v_whole = _guarded((S * T, 128), torch.float32, 7.0)
+    gm, gm_whole = _guarded((S * T, 2), torch.float32, 7.0)
+    h, h_whole = _guarded(tuple(h0.shape), torch.bfloat16, 7.0)
+    h.copy_(h0)
+    draft = eg.Draft(S, T, L, DEV, v=v, gamma=gm)
+    big = eg.DecodeState(S + 2, 3, 2, 9, 128, DEV)           # the calls' sequences lie between two others
+    big.ids.random_(0, 90000)
+    big.conv.normal_()
+    big.pos.fill_(11)
+    was = _state_like(big, S + 2, 3, 2, 9, 128)
+    part = eg.DecodeStateStruct(big.ids[1:].data_ptr(), big.conv[1:].data_ptr(), big.pos[1:].data_ptr())
+    need = lib.engram_forward_draft_workspace(S, T, ctypes.byref(L.s), ctypes.byref(w8.s))
+    ws, ws_whole = _guarded((need + 256,), torch.uint8, 5)
+    base = (ws.data_ptr() + 255) // 256 * 256
+    assert lib.engram_forward_draft(tk.data_ptr(), h.data_ptr(), S, T, ctypes.byref(L.s), ctypes.byref(w8.s), ctypes.byref(part),
+                                    ctypes.byref(draft.s), None, None, base, need, s) == eg.OK
+    assert v_whole() and gm_whole() and h_whole() and ws_whole() and not torch.equal(h, h0)
+    assert torch.equal(big.ids, was.ids) and torch.equal(big.pos, was.pos) and torch.equal(big.conv, was.conv)
+    n = torch.arange(S, dtype=torch.int32, device=DEV) % T
+    assert lib.engram_commit_draft(tk.data_ptr(), S, T, ctypes.byref(L.s), ctypes.byref(draft.s), n.data_ptr(), ctypes.byref(part), s) == eg.OK
+    for i in (0, S + 1):
+        assert torch.equal(big.ids[i], was.ids[i]) and torch.equal(big.conv[i], was.conv[i]) and int(big.pos[i]) == 11
+    assert torch.equal(big.pos[1:S + 1], 12 + n)
+
+
+def test_two_threads_on_two_streams():
+    """The operators called from two host threads at once, each with its own
+    stream, state and buffers, give what they give one after the other."""
+    log("two threads")
+    S, T, V = 6, 5, 40000
+    w = inputs.make_config(3, B=2 * S, T=T, layers=1, rows_per_table=997)
+    lay = w.layers[0]
+    L = eg.Layer(lay, "bf16", DEV)
+    w8 = eg.Int8Weights(L)
+    head = eg.quantize_i8(torch.randn(V, lay.d, device=DEV))
+    tok = torch.from_numpy(np.ascontiguousarray(w.tokens)).to(DEV).view(2, S, T)
+    h0 = eg.to_device(w.H, "bf16", DEV).view(2, S, T, 1, lay.d)
+    ua, us = torch.rand(2, S, T - 1, device=DEV), torch.rand(2, S, device=DEV)
+
+    def steps(i, stream):
+        out, st = [], states[i]
+        for _ in range(25):
+            with torch.cuda.stream(stream):
+                h, draft = h0[i].clone(), eg.Draft(S, T, L, DEV)
+            eg.forward_draft(tok[i], h, L, st, draft, w8=w8, stream=stream)
+            p = eg.token_probs(eg.project_i8(h.view(S, T, lay.d), *head, stream=stream), stream=stream)
+            t, a = eg.verify_drafts(p, None, drafted[i], ua[i], us[i], stream=stream)
+            eg.commit_draft(tok[i], L, draft, a, st, stream=stream)
+            out += [t, a, h]
+        stream.synchronize()
+        return out + [st.ids, st.conv, st.pos]
+
+    drafted = torch.randint(0, V, (2, S, T - 1), dtype=torch.int32, device=DEV)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    results = []
+    for parallel in (False, True):
+        states = [eg.DecodeState(S, 3, 1, 9, lay.d, DEV) for _ in range(2)]
+        torch.cuda.synchronize()
+        if parallel:
+            with concurrent.futures.ThreadPoolExecutor(2) as ex:
+                results.append([f.result() for f in [ex.submit(steps, i, streams[i]) for i in range(2)]])
+        else:
+            results.append([steps(i, streams[i]) for i in range(2)])
+    for a, b in zip(*results):
+        assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
