@@ -252,6 +252,26 @@ def test_operands_past_32_bits(n, k, o):
         assert torch.equal(out[a], eg.project_i8(q[a].clone(), w, ws, e_scale=qs[a].clone(), out_dtype="f32"))
 
 
+@pytest.mark.parametrize("k,o,source", [(17, 3, "bf16"), (32, 2, "bf16"), (17, 2, "i8"), (9, 2, "f32")])
+def test_product_of_the_most_tokens(k, o, source):
+    """More tokens than one launch quantises, W's odd rows copied beside the
+    first of them: every output against those of the pattern that repeats."""
+    log(f"project_i8 2^26 tokens x {k} x {o} {source}")
+    n, g = 2 ** 26 + 5, torch.Generator(device=DEV).manual_seed(12)
+    pattern = torch.randn(4099, k, generator=g, device=DEV).to(TYPES["f32" if source == "f32" else "bf16"])
+    w = torch.randint(-127, 128, (o, k), generator=g, dtype=torch.int8, device=DEV)
+    ws = torch.rand(o, generator=g, device=DEV)
+    times, e_scale = -(-n // 4099), None
+    want = eg.project_i8(pattern, w, ws, out_dtype="f32")
+    if source == "i8":
+        pattern, s = eg.quantize_i8(pattern)
+        e_scale = s.repeat(times)[:n].contiguous()
+    e = pattern.repeat(times, 1)[:n].contiguous()
+    out = eg.project_i8(e, w, ws, e_scale=e_scale, out_dtype="f32")
+    whole = n // 4099 * 4099
+    assert (out[:whole].view(-1, 4099, o) == want).all() and torch.equal(out[whole:], want[:n - whole])
+
+
 def test_unaligned_operands_are_refused():
     log("project_i8 unaligned operands")
     b = torch.zeros(40 * 64 + 16, dtype=torch.int8, device=DEV)
