@@ -1,0 +1,454 @@
+// Step 5 ("DeepSeek Engram series guide": v_t = W_V e_t, k_t = W_K e_t) for
+// many requests at once, each with a low-rank adapter of its own beside the
+// shared W:
+//   out_t = W e_t + s_a B_a (A_a e_t),   a = the adapter of token t's request
+//
+// Two launches.  The first leaves h_t = s_a A_a e_t for every token that has
+// an adapter; the second is the product with W, which adds B_a h_t to its
+// sums before they are rounded once and stored.  Tokens stay where they are:
+// a block of 32 tokens goes over the adapters that occur in it, with the rows
+// h of the other tokens read as zeros, so one adapter costs a few matrix
+// instructions and one read of its rows of B however its tokens are spread.
+//
+// bf16 layers keep h as the sum of two bf16 numbers (off by 2^-17 of h, beside
+// the 2^-8 of an output in bf16): one alone would be off by 2^-9, too much for
+// float32 outputs; A and B enter unrounded.  float32 layers run on
+// the float32 matrix instructions throughout.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "device_util.h"
+#include "engram_internal.h"
+
+namespace engram {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 64;   // columns of a step of the fragment loops
+
+// 16 bytes of a row are a lane's share of a step: 8 bf16 columns (one
+// v_mfma_f32_32x32x16_bf16) or 4 float32 ones (four v_mfma_f32_32x32x2_f32).
+template <int DT>
+struct Frag {
+  static constexpr int kSize = DT == ENGRAM_BF16 ? 2 : 4;
+  static constexpr int kVals = 16 / kSize;
+  static constexpr int kSteps = kChunk / 2 / kVals;   // of a chunk: lanes 0-31 take its first half, 32-63 its second
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16_t multiply(u32x4_t a, u32x4_t b, f32x16_t acc) {
+  if constexpr (DT == ENGRAM_BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+  } else {
+    const f32x4_t x = __builtin_bit_cast(f32x4_t, a), y = __builtin_bit_cast(f32x4_t, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[i], acc, 0, 0, 0);
+    return acc;
+  }
+}
+
+// Element i of an array of the layer's type.
+template <int DT>
+__device__ __forceinline__ const char* element(const void* p, int64_t i) { return static_cast<const char*>(p) + i * Frag<DT>::kSize; }
+
+__device__ __forceinline__ u32x4_t load16(const char* p) { return *reinterpret_cast<const u32x4_t*>(p); }
+
+struct AdaptArgs {
+  const void* e;          // [n_tok][K]
+  const void* w;          // [n_out][K]
+  const void* a;          // [adapters][rank][K]
+  const void* b;          // [adapters][n_out][rank]
+  const float* scale;     // [adapters] or null
+  const int32_t* which;   // [ceil(n_tok / per)]
+  void* h;                // bf16: [n_tok][2][padded rank], float32: [n_tok][rank]
+  void* out;              // [n_tok][n_out]
+  int64_t n_tok;
+  uint32_t per;
+  int32_t K;
+  int32_t n_out;
+  int32_t rank;
+  int32_t adapters;
+};
+
+// Columns of a row of h: whole matrix steps.
+__device__ __host__ __forceinline__ int h_columns(int dt, int rank) { return dt == ENGRAM_BF16 ? 2 * ((rank + 15) / 16 * 16) : rank; }
+
+// Token t's adapter, -1 for none.
+__device__ __forceinline__ int adapter_of(const AdaptArgs& a, int64_t t) {
+  if (t >= a.n_tok) return -1;
+  const int id = a.which[a.per == 1 ? static_cast<uint32_t>(t) : static_cast<uint32_t>(t) / a.per];
+  return static_cast<uint32_t>(id) < static_cast<uint32_t>(a.adapters) ? id : -1;
+}
+
+// f(adapter, its place among them) of the adapters that occur among a wavefront's ids.
+template <typename F>
+__device__ __forceinline__ void each_adapter(int id, F f) {
+  uint64_t left = __ballot(id >= 0);
+  for (int j = 0; left != 0; ++j) {
+    const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    left &= ~__ballot(id == one);
+    f(one, j);
+  }
+}
+
+// ---- h ----
+// A block of 32 tokens and one of the adapters in it a workgroup, whose four
+// wavefronts take every fourth 64 columns; 32 rows of A at a time.
+template <int DT>
+__global__ void __launch_bounds__(256)
+adapter_rows_kernel(AdaptArgs a) {
+  using Fr = Frag<DT>;
+  __shared__ f32x4_t part[4][4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 31, lh = lane >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lr;
+  const int id = adapter_of(a, t);
+  int mine = -1;
+  each_adapter(id, [&](int one, int j) { mine = j == static_cast<int>(blockIdx.y) ? one : mine; });
+  if (mine < 0) return;   // fewer adapters in this block
+  const float scale = a.scale != nullptr ? a.scale[mine] : 1.0f;
+  const char* e = element<DT>(a.e, min(t, a.n_tok - 1) * a.K + lh * (kChunk / 2));
+  const int hc = h_columns(DT, a.rank);
+  for (int r0 = 0; r0 < a.rank; r0 += 32) {
+    const bool row = r0 + lr < a.rank;
+    const char* ap = element<DT>(a.a, (static_cast<int64_t>(mine) * a.rank + (row ? r0 + lr : 0)) * a.K + lh * (kChunk / 2));
+    f32x16_t acc;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int c = wave * kChunk; c < a.K; c += 4 * kChunk) {
+      u32x4_t fa[Fr::kSteps], fe[Fr::kSteps];
+#pragma unroll
+      for (int s = 0; s < Fr::kSteps; ++s) {
+        fa[s] = load16(ap + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+        fe[s] = load16(e + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+      }
+#pragma unroll
+      for (int s = 0; s < Fr::kSteps; ++s) acc = multiply<DT>(row ? fa[s] : u32x4_t{0, 0, 0, 0}, fe[s], acc);
+    }
+    if (r0 > 0) __syncthreads();
+#pragma unroll
+    for (int g = 0; g < 4; ++g) part[wave][g][lane] = f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+    __syncthreads();
+    // rows r0 + 8 wave + 4 lh .. + 3 of the lane's token
+    f32x4_t x = part[0][wave][lane] + part[1][wave][lane] + part[2][wave][lane] + part[3][wave][lane];
+    const int r = r0 + wave * 8 + lh * 4;
+    if (id != mine) continue;
+    x *= scale;
+    if constexpr (DT == ENGRAM_BF16) {
+      if (r >= hc / 2) continue;
+      uint16_t* h = static_cast<uint16_t*>(a.h) + t * hc + r;
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        const float d0 = x[2 * i] - __uint_as_float(hi[i] << 16), d1 = x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
+        lo[i] = pack_bf16x2(d0 == d0 ? d0 : 0.f, d1 == d1 ? d1 : 0.f);   // (an infinity's second part is 0)
+      }
+      *reinterpret_cast<uint2*>(h) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(h + hc / 2) = make_uint2(lo[0], lo[1]);
+    } else {
+      if (r < a.rank) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.h) + t * hc + r) = x;
+    }
+  }
+}
+
+// Adds B_a h_t to the sums of FB blocks of 32 outputs (from f0 on; rows past
+// n_out read as output 0's) x one block of 32 tokens: every `of`-th of the
+// adapters in it, from `first` on.  id: of the lane's token t.  A lane's sums
+// are its own token's: where the block holds other tokens they keep what they
+// had, so that an infinity or a NaN in one request's adapter stays with it.
+template <int DT, int FB>
+__device__ __forceinline__ void add_adapters(const AdaptArgs& a, int id, int64_t t, int64_t f0, int first, int of, f32x16_t (&acc)[FB]) {
+  constexpr int kStep = 2 * Frag<DT>::kVals;   // columns of B of a step
+  const int lr = threadIdx.x & 31, lh = (threadIdx.x & 63) >> 5, hc = h_columns(DT, a.rank);
+  const char* h = static_cast<const char*>(a.h) + min(t, a.n_tok - 1) * hc * Frag<DT>::kSize + lh * 16;
+  each_adapter(id, [&](int one, int j) {
+    if (j % of != first) return;
+    const bool mine = id == one;
+    auto add = [&](auto from, auto n, f32x16_t* sums) {   // blocks from .. from + n - 1
+      const char* b[n];
+#pragma unroll
+      for (int f = 0; f < n; ++f) {
+        const int64_t o = f0 + (from + f) * 32 + lr;
+        b[f] = element<DT>(a.b, (static_cast<int64_t>(one) * a.n_out + (o < a.n_out ? o : 0)) * a.rank) + lh * 16;
+      }
+      for (int r = 0; r < a.rank; r += kStep) {
+        const bool in = r + lh * Frag<DT>::kVals < a.rank;   // (a rank of 8, 24, ..: the last step's second half has no columns)
+        const int at = r * Frag<DT>::kSize;
+        const u32x4_t zero = {0, 0, 0, 0};
+        u32x4_t fb[n];
+#pragma unroll
+        for (int f = 0; f < n; ++f) {
+          fb[f] = load16(b[f] + (in ? at : 0));
+          if (!in) fb[f] = zero;
+        }
+        u32x4_t h0 = load16(h + at), h1 = zero;
+        if constexpr (DT == ENGRAM_BF16) h1 = load16(h + at + hc);
+        if (!in) h0 = h1 = zero;
+#pragma unroll
+        for (int f = 0; f < n; ++f) {
+          sums[f] = multiply<DT>(fb[f], h0, sums[f]);
+          if constexpr (DT == ENGRAM_BF16) sums[f] = multiply<DT>(fb[f], h1, sums[f]);
+        }
+      }
+    };
+    if (__all(mine)) {
+      add(std::integral_constant<int, 0>{}, std::integral_constant<int, FB>{}, acc);
+    } else {
+#pragma unroll
+      for (int f = 0; f < FB; ++f) {
+        f32x16_t sum = acc[f];
+        add(f, std::integral_constant<int, 1>{}, &sum);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[f][i] = mine ? sum[i] : acc[f][i];
+      }
+    }
+  });
+}
+
+// ---- few tokens, and float32 ----
+// TB x FB blocks of 32 tokens x 32 outputs a workgroup.  Its four wavefronts
+// share the columns (every fourth 64) and the adapters, operands straight from
+// memory into registers; their sums meet in LDS.
+template <int DT, int TB, int FB, typename OutT>
+__global__ void __launch_bounds__(256)
+adapt_small_kernel(AdaptArgs a, int tiles_f) {
+  using Fr = Frag<DT>;
+  __shared__ f32x4_t part[4][TB * FB][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 31, lh = lane >> 5;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * FB * 32, t0 = static_cast<int64_t>(blockIdx.x / tiles_f) * TB * 32;
+  const char *w[FB], *e[TB];
+#pragma unroll
+  for (int f = 0; f < FB; ++f) w[f] = element<DT>(a.w, (f0 + f * 32 + lr) * a.K + lh * (kChunk / 2));
+#pragma unroll
+  for (int b = 0; b < TB; ++b) e[b] = element<DT>(a.e, min(t0 + b * 32 + lr, a.n_tok - 1) * a.K + lh * (kChunk / 2));
+  int id[TB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) id[b] = adapter_of(a, t0 + b * 32 + lr);
+  f32x16_t acc[TB][FB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b)
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[b][f][i] = 0.f;
+  for (int c = wave * kChunk; c < a.K; c += 4 * kChunk) {
+    u32x4_t fw[FB][Fr::kSteps], fe[TB][Fr::kSteps];
+#pragma unroll
+    for (int s = 0; s < Fr::kSteps; ++s) {
+#pragma unroll
+      for (int f = 0; f < FB; ++f) fw[f][s] = load16(w[f] + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+#pragma unroll
+      for (int b = 0; b < TB; ++b) fe[b][s] = load16(e[b] + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+    }
+#pragma unroll
+    for (int s = 0; s < Fr::kSteps; ++s)
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int f = 0; f < FB; ++f) acc[b][f] = multiply<DT>(fw[f][s], fe[b][s], acc[b][f]);
+  }
+#pragma unroll
+  for (int b = 0; b < TB; ++b) add_adapters<DT, FB>(a, id[b], t0 + b * 32 + lr, f0, wave, 4, acc[b]);
+#pragma unroll
+  for (int b = 0; b < TB; ++b)
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        part[wave][b * FB + f][g][lane] = f32x4_t{acc[b][f][4 * g], acc[b][f][4 * g + 1], acc[b][f][4 * g + 2], acc[b][f][4 * g + 3]};
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    const int64_t t = t0 + b * 32 + lr;
+    if (t >= a.n_tok) continue;
+#pragma unroll
+    for (int f = 0; f < FB; ++f) {
+      const int blk = b * FB + f;
+      const f32x4_t x = part[0][blk][wave][lane] + part[1][blk][wave][lane] + part[2][blk][wave][lane] + part[3][blk][wave][lane];
+      OutT* out = static_cast<OutT*>(a.out) + t * a.n_out + f0 + f * 32 + wave * 8 + lh * 4;
+      if constexpr (sizeof(OutT) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+      else *reinterpret_cast<f32x4_t*>(out) = x;
+    }
+  }
+}
+
+// ---- many tokens, bf16 ----
+// A tile of TF outputs x TT tokens a workgroup, WF x WT wavefronts; slices of
+// 64 columns of both go from memory straight into LDS, one in flight while the
+// other is multiplied.  A slice's row is 128 bytes, its 16-byte chunk c at
+// c ^ ((row >> 1) & 7), so that the rows a fragment read touches spread over
+// the banks.
+constexpr int kXcds = 8, kBand = 8;
+
+template <int TF, int TT, int WF, int WT, typename OutT>
+__global__ void __launch_bounds__(WF * WT * 64)
+adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
+  constexpr int NT = WF * WT * 64, FB = TF / WF / 32, TB = TT / WT / 32;
+  constexpr int kRowsAtOnce = NT / 8, kLoadsW = TF / kRowsAtOnce, kLoadsE = TT / kRowsAtOnce, kBuffer = (TF + TT) * 8;
+  extern __shared__ u32x4_t lds[];   // [2][TF + TT rows][8 chunks]; afterwards each wavefront's outputs
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 31, lh = lane >> 5;
+  const int wf = wave % WF, wt = wave / WF;
+  // Workgroup i runs on XCD i % 8: each XCD walks tiles of its own, band by
+  // band of token tiles, outputs outside, so that a band's rows stay in its L2
+  // while W streams past.
+  const int per_xcd = gridDim.x / kXcds, tile = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+  if (tile >= tiles_f * tiles_t) return;
+  const int band = tile / (tiles_f * kBand), in_band = tile - band * tiles_f * kBand, bt = min(kBand, tiles_t - band * kBand);
+  const int64_t f0 = static_cast<int64_t>(in_band / bt) * TF, t0 = (static_cast<int64_t>(band) * kBand + in_band % bt) * TT;
+  const int K = a.K;
+  const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
+  // rows past the end read zeros
+  const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<ENGRAM_BF16>(a.w, f0 * K)), 0,
+                                                    static_cast<int>(min(int64_t{TF}, a.n_out - f0)) * K * 2, 0x00020000);
+  const auto re = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<ENGRAM_BF16>(a.e, t0 * K)), 0,
+                                                    static_cast<int>(min(int64_t{TT}, a.n_tok - t0)) * K * 2, 0x00020000);
+  auto issue = [&](int kt) {
+    u32x4_t* dst = lds + (kt & 1) * kBuffer + wave * 64;
+#pragma unroll
+    for (int i = 0; i < kLoadsW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(dst + i * NT), 16,
+                                               ((r0 + i * kRowsAtOnce) * K + ch * 8) * 2, kt * 128, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kLoadsE; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (__attribute__((address_space(3))) void*)(dst + TF * 8 + i * NT), 16,
+                                               ((r0 + i * kRowsAtOnce) * K + ch * 8) * 2, kt * 128, 0, 0);
+  };
+  f32x16_t acc[TB][FB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b)
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[b][f][i] = 0.f;
+  const int ksteps = K / 64;
+  issue(0);
+  for (int kt = 0; kt < ksteps; ++kt) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the slice is there, the other buffer has been read
+    if (kt + 1 < ksteps) issue(kt + 1);
+    const u32x4_t* ws = lds + (kt & 1) * kBuffer + (wf * (TF / WF)) * 8;
+    const u32x4_t* es = lds + (kt & 1) * kBuffer + (TF + wt * (TT / WT)) * 8;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int kc = (s * 2 + lh) ^ ((lr >> 1) & 7);
+      u32x4_t fw[FB], fe[TB];
+#pragma unroll
+      for (int f = 0; f < FB; ++f) fw[f] = ws[(f * 32 + lr) * 8 + kc];
+#pragma unroll
+      for (int b = 0; b < TB; ++b) fe[b] = es[(b * 32 + lr) * 8 + kc];
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int f = 0; f < FB; ++f) acc[b][f] = multiply<ENGRAM_BF16>(fw[f], fe[b], acc[b][f]);
+    }
+  }
+  const int64_t fw0 = f0 + wf * (TF / WF), tw0 = t0 + wt * (TT / WT);
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    const int64_t t = tw0 + b * 32 + lr;
+    add_adapters<ENGRAM_BF16, FB>(a, adapter_of(a, t), t, fw0, 0, 1, acc[b]);
+  }
+  // outputs: a block of 32 tokens at a time through the wavefront's own LDS, whole rows of it to memory
+  __syncthreads();
+  constexpr int kRow = FB * 32 * static_cast<int>(sizeof(OutT)) + 16;   // bytes, 16 more than a row's: the rows' banks differ
+  constexpr int kRuns = FB * 32 * static_cast<int>(sizeof(OutT)) / 16;  // 16-byte runs of a row
+  constexpr int kEach = 16 / static_cast<int>(sizeof(OutT));
+  char* own = reinterpret_cast<char*>(lds) + wave * 32 * kRow;
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+#pragma unroll
+    for (int f = 0; f < FB; ++f)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        char* at = own + lr * kRow + (f * 32 + g * 8 + lh * 4) * static_cast<int>(sizeof(OutT));
+        const f32x16_t& x = acc[b][f];
+        if constexpr (sizeof(OutT) == 2)
+          *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(x[4 * g], x[4 * g + 1]), pack_bf16x2(x[4 * g + 2], x[4 * g + 3]));
+        else
+          *reinterpret_cast<f32x4_t*>(at) = f32x4_t{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wavefront's block is in LDS
+#pragma unroll
+    for (int i = 0; i < 32 * kRuns / 64; ++i) {
+      const int run = i * 64 + lane, row = run / kRuns, c = run % kRuns;
+      const int64_t t = tw0 + b * 32 + row, o = fw0 + c * kEach;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kRow + c * 16);
+      if (t < a.n_tok && o < a.n_out) *reinterpret_cast<u32x4_t*>(static_cast<OutT*>(a.out) + t * a.n_out + o) = v;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and read, before the next block's writes
+  }
+}
+
+template <int TF, int TT, int WF, int WT, typename OutT>
+hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
+  constexpr int kOut = WF * WT * 32 * (TF / WF * static_cast<int>(sizeof(OutT)) + 16);
+  constexpr int kLds = std::max(2 * (TF + TT) * 128, kOut);
+  auto* const fn = adapt_tile_kernel<TF, TT, WF, WT, OutT>;
+  static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if ((attr_set.load(std::memory_order_acquire) & bit) == 0) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+    attr_set.fetch_or(bit, std::memory_order_release);
+  }
+  const int tiles_f = (a.n_out + TF - 1) / TF, tiles_t = static_cast<int>((a.n_tok + TT - 1) / TT);
+  const int64_t tiles = static_cast<int64_t>(tiles_f) * tiles_t;
+  launch_k(fn, dim3(static_cast<unsigned>((tiles + kXcds - 1) / kXcds * kXcds)), dim3(WF * WT * 64), kLds, s, a, tiles_f, tiles_t);
+  return launch_error();
+}
+
+template <int DT, int TB, int FB, typename OutT>
+hipError_t launch_small(const AdaptArgs& a, hipStream_t s) {
+  const int tiles_f = a.n_out / (FB * 32);
+  const int64_t tiles = (a.n_tok + TB * 32 - 1) / (TB * 32) * tiles_f;
+  launch_k((adapt_small_kernel<DT, TB, FB, OutT>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a, tiles_f);
+  return launch_error();
+}
+
+template <typename OutT>
+hipError_t launch_product(const AdaptArgs& a, int dtype, hipStream_t s) {
+  if (dtype == ENGRAM_F32) {
+    if constexpr (sizeof(OutT) == 4) return a.n_tok <= 32 ? launch_small<ENGRAM_F32, 1, 1, float>(a, s) : launch_small<ENGRAM_F32, 2, 2, float>(a, s);
+    return hipErrorInvalidValue;
+  }
+  if (a.n_tok <= 32) return launch_small<ENGRAM_BF16, 1, 1, OutT>(a, s);
+  if (a.n_tok <= 512) return launch_small<ENGRAM_BF16, 2, 2, OutT>(a, s);
+  if (((a.n_tok + 255) / 256) * ((a.n_out + 255) / 256) >= 256) return launch_tile<256, 256, 2, 4, OutT>(a, s);
+  return launch_tile<128, 128, 2, 2, OutT>(a, s);
+}
+
+}  // namespace
+
+size_t adapt_workspace(int64_t n_tok, int dtype, int rank) {
+  return static_cast<size_t>(n_tok) * h_columns(dtype, rank) * (dtype == ENGRAM_BF16 ? 2 : 4);
+}
+
+hipError_t launch_project_adapted(const void* e, const void* w, int64_t n_tok, int64_t d_mem, int64_t n_out, int dtype, const void* lora_a,
+                                  const void* lora_b, const float* scale, int32_t rank, int32_t adapters, const int32_t* which, int64_t per,
+                                  int out_dtype, void* out, void* ws, hipStream_t s) {
+  if (n_tok == 0) return hipSuccess;
+  per = std::min(per, n_tok);
+  const AdaptArgs a{e, w, lora_a, lora_b, scale, which, ws, out, n_tok, static_cast<uint32_t>(per), static_cast<int32_t>(d_mem),
+                    static_cast<int32_t>(n_out), rank, adapters};
+  if (adapters > 0) {
+    // a block of 32 tokens meets at most so many requests, each with one adapter
+    const int64_t most = std::min<int64_t>({32, adapters, (30 + per) / per + 1});
+    const dim3 grid(static_cast<unsigned>((n_tok + 31) / 32), static_cast<unsigned>(most));
+    prof_stage("adapter_rows_kernel");
+    if (dtype == ENGRAM_BF16) launch_k(adapter_rows_kernel<ENGRAM_BF16>, grid, dim3(256), 0, s, a);
+    else launch_k(adapter_rows_kernel<ENGRAM_F32>, grid, dim3(256), 0, s, a);
+    const hipError_t r = launch_error();
+    if (r != hipSuccess) return r;
+  }
+  prof_stage("project_adapted_kernel");
+  return out_dtype == ENGRAM_BF16 ? launch_product<uint16_t>(a, dtype, s) : launch_product<float>(a, dtype, s);
+}
+
+}  // namespace engram

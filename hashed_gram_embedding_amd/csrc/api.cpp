@@ -1559,6 +1559,216 @@ ENGRAM_API engram_status engram_verify_drafts(const void* target, const void* dr
   return r;
 }
 
+// ---- around the layer ----
+
+namespace {
+
+bool float_dtype(int dt) { return dt == ENGRAM_F32 || dt == ENGRAM_BF16; }
+
+engram_status check_embed(const char* who, int64_t n, int64_t most, int dtype, int out_dtype, int64_t V, int64_t dim, int32_t branches) {
+  if (!float_dtype(dtype) || !float_dtype(out_dtype)) return fail(ENGRAM_EUNSUPPORTED, "%s: dtypes must be F32 or BF16", who);
+  if (n < 0 || V < 1 || dim < 1 || branches < 1)
+    return fail(ENGRAM_EINVAL, "%s: need n >= 0, V >= 1, dim >= 1 and branches >= 1", who);
+  if (n > most) return fail(ENGRAM_EUNSUPPORTED, "%s: n above %lld", who, static_cast<long long>(most));
+  if (V > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "%s: V must be below 2^31", who);
+  if (dim % 8 != 0 || dim > ENGRAM_MAX_D) return fail(ENGRAM_EUNSUPPORTED, "%s: dim must be a multiple of 8 up to %d", who, ENGRAM_MAX_D);
+  if (branches > ENGRAM_MAX_BRANCHES) return fail(ENGRAM_EUNSUPPORTED, "%s: branches above %d", who, ENGRAM_MAX_BRANCHES);
+  return ENGRAM_OK;
+}
+
+}  // namespace
+
+ENGRAM_API engram_status engram_embed(const int32_t* ids, int64_t n, const void* table, engram_dtype dtype, int64_t V, int64_t dim,
+                                      float scale, int32_t branches, engram_dtype out_dtype, void* out, hipStream_t stream) {
+  const engram_status r = check_embed("embed", n, INT32_MAX, dtype, out_dtype, V, dim, branches);
+  if (r != ENGRAM_OK) return r;
+  if (n == 0) return ENGRAM_OK;
+  if (ids == nullptr || table == nullptr || out == nullptr) return fail(ENGRAM_EINVAL, "embed: ids, table and out must be non-NULL");
+  if (!aligned(ids, 4) || !aligned(table, 16) || !aligned(out, 16))
+    return fail(ENGRAM_EINVAL, "embed: table and out must be 16-byte, ids 4-byte aligned");
+  prof_begin();
+  prof_mark(stream, "embed_kernel");
+  const engram_status e = hip_status(engram::launch_embed(ids, n, table, dtype, V, dim, scale, branches, out_dtype, out, stream), "embed launch");
+  prof_mark(stream, nullptr);
+  return e;
+}
+
+ENGRAM_API size_t engram_embed_backward_workspace(int64_t n, int64_t dim) {
+  if (n < 1 || n > ENGRAM_MAX_EMBED_GRAD_IDS || dim < 1 || dim > ENGRAM_MAX_D) return 0;
+  return engram::embed_backward_workspace(n, dim);
+}
+
+ENGRAM_API engram_status engram_embed_backward(const int32_t* ids, int64_t n, const void* dout, engram_dtype dtype, int64_t V,
+                                               int64_t dim, float scale, int32_t branches, int32_t accumulate,
+                                               engram_dtype out_dtype, void* dtable, void* ws, size_t ws_bytes,
+                                               hipStream_t stream) {
+  const engram_status r = check_embed("embed_backward", n, ENGRAM_MAX_EMBED_GRAD_IDS, dtype, out_dtype, V, dim, branches);
+  if (r != ENGRAM_OK) return r;
+  if (dtable == nullptr) return fail(ENGRAM_EINVAL, "embed_backward: dtable must be non-NULL");
+  if (!aligned(dtable, 16)) return fail(ENGRAM_EINVAL, "embed_backward: dtable must be 16-byte aligned");
+  if (n > 0) {
+    if (ids == nullptr || dout == nullptr) return fail(ENGRAM_EINVAL, "embed_backward: ids and dout must be non-NULL");
+    if (!aligned(ids, 4) || !aligned(dout, 16))
+      return fail(ENGRAM_EINVAL, "embed_backward: dout must be 16-byte, ids 4-byte aligned");
+  }
+  const size_t need = engram_embed_backward_workspace(n, dim);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256)))
+    return fail(ENGRAM_EINVAL, "embed_backward: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  prof_begin();
+  const engram_status e = hip_status(engram::launch_embed_backward(ids, n, dout, dtype, V, dim, scale, branches, accumulate != 0, out_dtype,
+                                                                   dtable, ws, stream),
+                                     "embed_backward launch");
+  prof_mark(stream, nullptr);
+  return e;
+}
+
+namespace {
+
+constexpr int32_t kMostAdapters = 1 << 20;
+
+engram_status check_adapters(const char* who, const engram_adapters* ad, const int32_t* which) {
+  if (ad == nullptr) return fail(ENGRAM_EINVAL, "%s: the adapters are NULL", who);
+  if (ad->n < 0) return fail(ENGRAM_EINVAL, "%s: need n >= 0 adapters", who);
+  if (ad->n > kMostAdapters) return fail(ENGRAM_EUNSUPPORTED, "%s: more than %d adapters", who, kMostAdapters);
+  if (ad->rank < 8 || ad->rank % 8 != 0 || ad->rank > ENGRAM_MAX_ADAPTER_RANK)
+    return fail(ENGRAM_EUNSUPPORTED, "%s: rank must be a multiple of 8 in [8, %d]", who, ENGRAM_MAX_ADAPTER_RANK);
+  if (ad->n > 0 && (ad->a == nullptr || ad->b == nullptr)) return fail(ENGRAM_EINVAL, "%s: the adapters' a and b must be non-NULL", who);
+  if (!aligned(ad->a, 16) || !aligned(ad->b, 16) || !aligned(ad->scale, 4))
+    return fail(ENGRAM_EINVAL, "%s: the adapters' a and b must be 16-byte, scale 4-byte aligned", who);
+  if (which == nullptr) return fail(ENGRAM_EINVAL, "%s: which must be non-NULL", who);
+  if (!aligned(which, 4)) return fail(ENGRAM_EINVAL, "%s: which must be 4-byte aligned", who);
+  return ENGRAM_OK;
+}
+
+}  // namespace
+
+ENGRAM_API size_t engram_project_adapted_workspace(int64_t n_tok, engram_dtype dtype, int32_t rank) {
+  if (n_tok < 1 || n_tok > INT32_MAX || !float_dtype(dtype) || rank < 8 || rank > ENGRAM_MAX_ADAPTER_RANK) return 0;
+  return align_up(engram::adapt_workspace(n_tok, dtype, rank));
+}
+
+ENGRAM_API engram_status engram_project_adapted(const void* e, const void* w, int64_t n_tok, int64_t d_mem, int64_t n_out,
+                                                engram_dtype dtype, const engram_adapters* ad, const int32_t* which,
+                                                int64_t per, engram_dtype out_dtype, void* out, void* ws, size_t ws_bytes,
+                                                hipStream_t stream) {
+  if (!float_dtype(dtype)) return fail(ENGRAM_EUNSUPPORTED, "project_adapted: dtype must be F32 or BF16");
+  if (!float_dtype(out_dtype) || (dtype == ENGRAM_F32 && out_dtype != ENGRAM_F32))
+    return fail(ENGRAM_EUNSUPPORTED, "project_adapted: out_dtype must be F32, or BF16 in a BF16 call");
+  if (n_tok < 0 || d_mem < 1 || n_out < 1 || per < 1)
+    return fail(ENGRAM_EINVAL, "project_adapted: need n_tok >= 0, d_mem >= 1, n_out >= 1 and per >= 1");
+  if (n_tok > INT32_MAX || n_out > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "project_adapted: n_tok and n_out must be below 2^31");
+  if (d_mem % 64 != 0 || n_out % 64 != 0 || d_mem > 65536)
+    return fail(ENGRAM_EUNSUPPORTED, "project_adapted: d_mem and n_out must be multiples of 64, d_mem up to 65536");
+  if (n_tok == 0) return ENGRAM_OK;
+  const engram_status r = check_adapters("project_adapted", ad, which);
+  if (r != ENGRAM_OK) return r;
+  if (e == nullptr || w == nullptr || out == nullptr) return fail(ENGRAM_EINVAL, "project_adapted: e, w and out must be non-NULL");
+  if (!aligned(e, 16) || !aligned(w, 16) || !aligned(out, 16))
+    return fail(ENGRAM_EINVAL, "project_adapted: e, w and out must be 16-byte aligned");
+  const size_t need = engram_project_adapted_workspace(n_tok, dtype, ad->rank);
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+    return fail(ENGRAM_EINVAL, "project_adapted: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  prof_begin();
+  const engram_status s = hip_status(engram::launch_project_adapted(e, w, n_tok, d_mem, n_out, dtype, ad->a, ad->b, ad->scale, ad->rank,
+                                                                    ad->n, which, per, out_dtype, out, ws, stream),
+                                     "project_adapted launch");
+  prof_mark(stream, nullptr);
+  return s;
+}
+
+namespace {
+
+struct AdaptedWorkspace {
+  void* e;
+  float* kv;
+  float4* stats;
+  float* gamma;
+  void* h;
+};
+
+AdaptedWorkspace carve_adapted(Carve& c, int64_t n_tok, const engram_layer* L, int32_t rank) {
+  const int M = L->gc.branches;
+  AdaptedWorkspace w;
+  w.e = c.take<char>(rows_bytes(n_tok, L));
+  w.kv = c.take<float>(static_cast<size_t>(n_tok) * (1 + M) * L->gc.d);
+  w.stats = c.take<float4>(static_cast<size_t>(n_tok) * (1 + M));
+  w.gamma = c.take<float>(static_cast<size_t>(n_tok) * M);
+  w.h = c.take<char>(engram::adapt_workspace(n_tok, L->gc.hdtype, rank));
+  return w;
+}
+
+}  // namespace
+
+ENGRAM_API size_t engram_forward_adapted_workspace(int64_t B, int64_t T, const engram_layer* L, const engram_adapters* ad) {
+  if (L == nullptr || ad == nullptr || B < 0 || T < 0 || B > 65535 || T > INT32_MAX || B * T > INT32_MAX) return 0;
+  if (L->gc.branches < 1 || L->gc.branches > ENGRAM_MAX_BRANCHES || L->gc.d < 1 || L->gc.d > ENGRAM_MAX_D || L->tables.n_tables < 1 ||
+      L->tables.n_tables > ENGRAM_MAX_TABLES || L->tables.dim < 1 || ad->rank < 8 || ad->rank > ENGRAM_MAX_ADAPTER_RANK)
+    return 0;   // refused by the call
+  Carve c{nullptr};
+  carve_adapted(c, B * T, L, ad->rank);
+  return c.used;
+}
+
+ENGRAM_API engram_status engram_forward_adapted(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                                                const engram_adapters* ad, const int32_t* which, engram_decode_state* st,
+                                                float* alpha_out, float* y_out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  engram::HashArgs ha;
+  engram::TableArgs ta;
+  engram::GateConvArgs g;
+  engram_status r = check_call("forward_adapted", L, st, true, B, T, &ha, &ta, &g);
+  if (r != ENGRAM_OK) return r;
+  const int64_t d_mem = static_cast<int64_t>(L->tables.n_tables) * L->tables.dim, n_out = static_cast<int64_t>(1 + g.branches) * g.d;
+  if (d_mem % 64 != 0 || d_mem > 65536)
+    return fail(ENGRAM_EUNSUPPORTED, "forward_adapted: n_tables*dim must be a multiple of 64 up to 65536");
+  const int64_t n_tok = B * T;
+  if (n_tok == 0) return ENGRAM_OK;
+  if (n_tok > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "forward_adapted: B*T above 2^31-1 tokens per call");
+  if ((r = check_adapters("forward_adapted", ad, which)) != ENGRAM_OK) return r;
+  if (tokens == nullptr || H == nullptr) return fail(ENGRAM_EINVAL, "forward_adapted: tokens and H must be non-NULL");
+  if (!aligned(H, 16)) return fail(ENGRAM_EINVAL, "forward_adapted: H must be 16-byte aligned");
+  if (y_out != nullptr && !aligned(y_out, 16)) return fail(ENGRAM_EINVAL, "forward_adapted: y_out must be 16-byte aligned");
+  const size_t need = engram_forward_adapted_workspace(B, T, L, ad);
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+    return fail(ENGRAM_EINVAL, "forward_adapted: workspace needs %zu bytes, 256-byte aligned (got %zu)", need, ws_bytes);
+  Carve c{static_cast<char*>(ws)};
+  const AdaptedWorkspace w = carve_adapted(c, n_tok, L, ad->rank);
+  prof_begin();
+  r = run_retrieve(tokens, B, T, L, ha, ta, g.hdtype, st, w.e, stream, static_cast<int>(g.hdtype));
+  if (r != ENGRAM_OK) return r;
+  r = hip_status(engram::launch_project_adapted(w.e, L->w, n_tok, d_mem, n_out, g.hdtype, ad->a, ad->b, ad->scale, ad->rank, ad->n, which,
+                                                T, ENGRAM_F32, w.kv, w.h, stream),
+                 "project_adapted launch");
+  if (r != ENGRAM_OK) return r;
+  g.kvdtype = ENGRAM_F32;
+  prof_mark(stream, "gate_stats_kernel");
+  r = hip_status(engram::launch_gate_stats(H, w.kv, n_tok, g, w.stats, stream), "gate statistics launch");
+  if (r != ENGRAM_OK) return r;
+  return run_conv_commit(H, w.kv, n_out, ENGRAM_F32, w.stats, 1, 1, false, B, T, g, st, tokens, L->hash.proj, L->hash.max_n,
+                         static_cast<int32_t>(L->hash.vocab), alpha_out, w.gamma, y_out, stream);
+}
+
+ENGRAM_API engram_status engram_sample_tokens(const void* logits, engram_dtype dtype, int64_t rows, int64_t V, int64_t ld,
+                                              const float* temperature, const int32_t* top_k, const float* top_p,
+                                              const float* min_p, int64_t per, const float* u, int32_t* tokens, float* logprob,
+                                              hipStream_t stream) {
+  if (!float_dtype(dtype)) return fail(ENGRAM_EUNSUPPORTED, "sample_tokens: dtype must be F32 or BF16");
+  if (rows < 0 || V < 1 || ld < V || per < 1)
+    return fail(ENGRAM_EINVAL, "sample_tokens: need rows >= 0, V >= 1, ld >= V and per >= 1");
+  if (rows > INT32_MAX || V > INT32_MAX) return fail(ENGRAM_EUNSUPPORTED, "sample_tokens: rows and V must be below 2^31");
+  if (rows == 0) return ENGRAM_OK;
+  if (logits == nullptr || u == nullptr || tokens == nullptr)
+    return fail(ENGRAM_EINVAL, "sample_tokens: logits, u and tokens must be non-NULL");
+  if (!aligned(logits, dtype_size(dtype)) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+      !aligned(min_p, 4) || !aligned(u, 4) || !aligned(tokens, 4) || !aligned(logprob, 4))
+    return fail(ENGRAM_EINVAL, "sample_tokens: every buffer must be aligned to its elements");
+  prof_begin();
+  const engram_status r = hip_status(engram::launch_sample_tokens(logits, dtype, rows, V, ld, temperature, top_k, top_p, min_p, per, u,
+                                                                  tokens, logprob, stream),
+                                     "sample_tokens launch");
+  prof_mark(stream, nullptr);
+  return r;
+}
+
 ENGRAM_API engram_status engram_quantize_mxfp8(const void* x, engram_dtype dtype, int64_t rows, int64_t cols,
                                                uint8_t* q, uint8_t* scale, hipStream_t stream) {
   if (dtype != ENGRAM_F32 && dtype != ENGRAM_BF16) return fail(ENGRAM_EUNSUPPORTED, "quantize_mxfp8: dtype F32 or BF16");

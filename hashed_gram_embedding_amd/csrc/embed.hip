@@ -1,0 +1,537 @@
+// Token embeddings beside the layer's own tables: the lookup with scaling that
+// makes the first hidden states, and its gradient.
+//
+//   H[i][m][:] = scale E[id_i][:]                                  (m < M)
+//   dE[v][:]   = scale sum_{i : id_i = v} sum_m dH[i][m][:]
+//
+// An id outside [0, V) (padding) has a row of zeros and no gradient.
+#include <algorithm>
+#include <type_traits>
+
+#include "device_util.h"
+#include "engram_internal.h"
+
+namespace engram {
+namespace {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+
+// A row's columns go to the lanes in chunks of 8: the lanes of a row are the
+// power of two that covers its chunks, at most a workgroup; longer rows take
+// more than one turn.
+int row_lanes_log2(int64_t dim) {
+  int log = 0;
+  while ((1 << log) < kThreads && (int64_t{8} << log) < dim) ++log;
+  return log;
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&f)[8]) {
+  if constexpr (DT == ENGRAM_BF16) {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), f);
+  } else {
+    const f32x4_t* q = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + i);
+    const f32x4_t a = q[0], b = q[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[k] = a[k];
+      f[k + 4] = b[k];
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
+  if constexpr (DT == ENGRAM_BF16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8(f);
+  } else {
+    f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i);
+    q[0] = f32x4_t{f[0], f[1], f[2], f[3]};
+    q[1] = f32x4_t{f[4], f[5], f[6], f[7]};
+  }
+}
+
+struct EmbedArgs {
+  const int32_t* ids;
+  const void* table;
+  void* out;
+  int64_t n;
+  int64_t V;
+  int64_t dim;
+  int32_t branches;
+  int32_t log_lanes;
+  float scale;
+};
+
+// One row of the table is read once and written M times.
+template <int IN, int OUT>
+__global__ void __launch_bounds__(kThreads)
+embed_kernel(EmbedArgs a) {
+  const int lanes = 1 << a.log_lanes;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
+  if (i >= a.n) return;
+  const int64_t id = a.ids[i];
+  const bool has = id >= 0 && id < a.V;
+  for (int64_t c = (threadIdx.x & (lanes - 1)) * 8; c < a.dim; c += lanes * 8) {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (has) {
+      load8<IN>(a.table, id * a.dim + c, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= a.scale;
+    }
+    for (int m = 0; m < a.branches; ++m) store8<OUT>(a.out, (i * a.branches + m) * a.dim + c, f);
+  }
+}
+
+// ---- the gradient ----
+// Tokens are sorted by id, equal ids by position, and the sums run over that
+// order: whichever workgroup adds them, every sum has the same terms in the
+// same order, so results are the same bits each time and no two workgroups
+// add to one row.
+
+// Zeros for the gradient's table, written by the workgroups behind a sorting
+// launch's own: the sort is a chain of small launches, and the table is the
+// larger part of what a call writes.
+struct Fill {
+  char* at;        // 16-byte aligned
+  int64_t bytes;   // a multiple of 16
+};
+constexpr int64_t kFillBytes = 256;   // of one thread
+
+__device__ __forceinline__ void fill_zeros(const Fill& f, int64_t group, int threads) {
+  const int64_t end = min(f.bytes, (group + 1) * threads * kFillBytes);
+  for (int64_t b = group * threads * kFillBytes + threadIdx.x * 16; b < end; b += threads * 16)
+    *reinterpret_cast<u32x4_t*>(f.at + b) = u32x4_t{0, 0, 0, 0};
+}
+
+// What the sort orders: an id, V for one without a row.
+__device__ __forceinline__ uint32_t key_of(int32_t id, uint32_t V) { return static_cast<uint32_t>(id) < V ? static_cast<uint32_t>(id) : V; }
+
+// Few ids: each one's place is the number of ids before it in the order,
+// counted over all of them (64 ids a workgroup, one a lane; 16 wavefronts
+// share the others, read as scalars).
+constexpr int kRankThreads = 1024;
+__global__ void __launch_bounds__(kRankThreads)
+rank_kernel(const int32_t* __restrict__ ids, int n, uint32_t V, uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out,
+            int groups, Fill fill) {
+  if (static_cast<int>(blockIdx.x) >= groups) return fill_zeros(fill, blockIdx.x - groups, kRankThreads);
+  __shared__ int part[kRankThreads / 64][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i0 = blockIdx.x * 64, i = i0 + lane;
+  const uint32_t key = i < n ? key_of(ids[i], V) : ~0u;
+  const int per = (n + kRankThreads / 64 - 1) / (kRankThreads / 64);
+  const int j0 = min(wave * per, n), j1 = min(j0 + per, n);
+  int before = 0;
+  // of the ids in front of this workgroup's equal ones count too, of those behind it they do not
+  const int front = min(max(i0, j0), j1), back = min(max(i0 + 64, j0), j1);
+  for (int j = j0; j < front; ++j) before += key_of(ids[j], V) <= key;
+  for (int j = front; j < back; ++j) {
+    const uint32_t other = key_of(ids[j], V);
+    before += other < key || (other == key && j < i);
+  }
+  for (int j = back; j < j1; ++j) before += key_of(ids[j], V) < key;
+  part[wave][lane] = before;
+  __syncthreads();
+  if (wave == 0 && i < n) {
+    int rank = 0;
+#pragma unroll
+    for (int w = 0; w < kRankThreads / 64; ++w) rank += part[w][lane];
+    key_out[rank] = key;
+    pos_out[rank] = i;
+  }
+}
+
+// More ids: stable passes over digits of the key, lowest first.  A pass counts
+// each block's digits, sums the counts (digit by digit, block by block) and
+// moves every id to its place.
+constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
+constexpr int kSortBlock = 4096;                       // ids of a workgroup
+constexpr int kSortRounds = kSortBlock / kSortThreads;
+constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
+
+struct SortPass {
+  const int32_t* ids;       // first pass: the caller's ids (pos is the index itself)
+  const uint32_t* key;      // later passes
+  const uint32_t* pos;
+  uint32_t* key_out;
+  uint32_t* pos_out;
+  uint32_t* counts;         // [kDigits][blocks]
+  int64_t n;
+  uint32_t V;
+  int32_t shift;
+  int32_t blocks;
+};
+
+__device__ __forceinline__ uint32_t sort_key(const SortPass& a, int64_t i) { return a.ids != nullptr ? key_of(a.ids[i], a.V) : a.key[i]; }
+
+__global__ void __launch_bounds__(kSortThreads)
+digit_count_kernel(SortPass a, Fill fill) {
+  if (static_cast<int>(blockIdx.x) >= a.blocks) return fill_zeros(fill, blockIdx.x - a.blocks, kSortThreads);
+  __shared__ uint32_t hist[kDigits];
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortBlock;
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t i = i0 + r * kSortThreads + threadIdx.x;
+    if (i < a.n) atomicAdd(&hist[(sort_key(a, i) >> a.shift) & (kDigits - 1)], 1u);
+  }
+  __syncthreads();
+  a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x] = hist[threadIdx.x];
+}
+
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x) {   // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const uint32_t y = __shfl_up(x, off, 64);
+    x += lane >= off ? y : 0;
+  }
+  return x;
+}
+
+// Exclusive sums of the counts, in place: one workgroup, each thread a run.
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads)
+digit_scan_kernel(uint32_t* __restrict__ counts, int64_t m, Fill fill) {
+  if (blockIdx.x > 0) return fill_zeros(fill, blockIdx.x - 1, kScanThreads);
+  __shared__ uint32_t part[kScanThreads / 64];
+  const int64_t run = (m + kScanThreads - 1) / kScanThreads;
+  const int64_t i0 = min(threadIdx.x * run, m), i1 = min(i0 + run, m);
+  uint32_t sum = 0;
+  for (int64_t i = i0; i < i1; ++i) sum += counts[i];
+  const uint32_t upto = wave_scan_u32(sum);
+  if ((threadIdx.x & 63) == 63) part[threadIdx.x >> 6] = upto;
+  __syncthreads();
+  uint32_t at = upto - sum;
+  for (int w = 0; w < static_cast<int>(threadIdx.x >> 6); ++w) at += part[w];
+  for (int64_t i = i0; i < i1; ++i) {
+    const uint32_t x = counts[i];
+    counts[i] = at;
+    at += x;
+  }
+}
+
+// Orders a wavefront's LDS accesses before this point and behind it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Each wavefront takes a contiguous quarter of the block's ids, 64 at a time;
+// lanes with the same digit find one another by a ballot for each digit bit.
+__global__ void __launch_bounds__(kSortThreads)
+digit_move_kernel(SortPass a, Fill fill) {
+  if (static_cast<int>(blockIdx.x) >= a.blocks) return fill_zeros(fill, blockIdx.x - a.blocks, kSortThreads);
+  __shared__ uint32_t at[kSortWaves][kDigits];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) at[w][threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortBlock + wave * (kSortBlock / kSortWaves);
+  uint32_t key[kSortRounds];
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t i = i0 + r * 64 + lane;
+    key[r] = i < a.n ? sort_key(a, i) : 0;
+    if (i < a.n) atomicAdd(&at[wave][(key[r] >> a.shift) & (kDigits - 1)], 1u);
+  }
+  __syncthreads();
+  {   // where each wavefront's ids of each digit begin
+    uint32_t from = a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t x = at[w][threadIdx.x];
+      at[w][threadIdx.x] = from;
+      from += x;
+    }
+  }
+  __syncthreads();
+  const uint64_t below = (uint64_t{1} << lane) - 1;
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t i = i0 + r * 64 + lane;
+    const uint32_t digit = (key[r] >> a.shift) & (kDigits - 1);
+    uint64_t same = __ballot(i < a.n);
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
+      const uint64_t set = __ballot((digit >> b) & 1);
+      same &= (digit >> b) & 1 ? set : ~set;
+    }
+    if (i < a.n) {
+      const uint32_t to = at[wave][digit] + __popcll(same & below);
+      a.key_out[to] = key[r];
+      a.pos_out[to] = a.ids != nullptr ? static_cast<uint32_t>(i) : a.pos[i];
+    }
+    wave_sync();   // every lane has read its digit's place before the digit's last lane moves it on
+    if (i < a.n && (same >> lane) == 1) at[wave][digit] += __popcll(same);
+    wave_sync();
+  }
+}
+
+struct SumArgs {
+  const uint32_t* key;    // [n] sorted
+  const uint32_t* pos;    // [n]
+  const void* dout;       // [n][M][dim]
+  void* dtable;           // [V][dim]
+  float* part;            // [tiles][2][dim]
+  int64_t n;
+  int64_t dim;
+  int64_t tiles;
+  uint32_t V;
+  int32_t branches;
+  int32_t log_lanes;
+  int32_t tile;           // sorted tokens of a tile
+  int32_t accumulate;
+  float scale;
+};
+
+template <int OUT>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int64_t c, float (&sum)[8]) {
+  const int64_t i = key * a.dim + c;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum[k] *= a.scale;
+  if (a.accumulate) {
+    float old[8];
+    load8<OUT>(a.dtable, i, old);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += old[k];
+  }
+  store8<OUT>(a.dtable, i, sum);
+}
+
+// Sums over tiles of the sorted tokens.  A run of equal ids inside a tile is
+// written to its row; one that came in from the tile before, or goes on in
+// the next, leaves its part sum (slot 0: came in, slot 1: begins here).
+template <int IN, int OUT>
+__global__ void __launch_bounds__(kThreads)
+tile_sum_kernel(SumArgs a) {
+  const int lanes = 1 << a.log_lanes;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
+  if (t >= a.tiles) return;
+  const int64_t p0 = t * a.tile, p1 = min(p0 + a.tile, a.n);
+  const int64_t c = (static_cast<int64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * 8;
+  if (c >= a.dim) return;
+  const int64_t step = a.branches * a.dim;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  uint32_t key = a.key[p0];
+  bool begun = p0 == 0 || a.key[p0 - 1] != key;   // the run begins in this tile
+  for (int64_t p = p0; p < p1; ++p) {
+    if (key >= a.V) return;   // ids without a row come last
+    const int64_t at = a.pos[p] * step + c;
+    for (int m = 0; m < a.branches; ++m) {
+      float f[8];
+      load8<IN>(a.dout, at + m * a.dim, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += f[k];
+    }
+    const uint32_t next = p + 1 < a.n ? a.key[p + 1] : ~0u;
+    const bool ends = next != key;
+    if (ends || p + 1 == p1) {
+      if (begun && ends) write_row<OUT>(a, key, c, sum);
+      else store8<ENGRAM_F32>(a.part, (t * 2 + (begun ? 1 : 0)) * a.dim + c, sum);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+      begun = true;
+    }
+    key = next;
+  }
+}
+
+// Runs over more than one tile: the tile in which one ends joins its parts,
+// kJoinGroups of them side by side (each a contiguous share, joined in order).
+constexpr int kJoinThreads = 256, kJoinLanes = 16, kJoinGroups = kJoinThreads / kJoinLanes;
+template <int OUT>
+__global__ void __launch_bounds__(kJoinThreads)
+tile_join_kernel(SumArgs a) {
+  __shared__ float share[kJoinGroups][kJoinLanes][9];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) + 1;
+  const int64_t p0 = t * a.tile, p1 = min(p0 + a.tile, a.n);
+  const uint32_t key = a.key[p0];
+  if (key >= a.V || a.key[p0 - 1] != key || (p1 < a.n && a.key[p1] == key && a.key[p1 - 1] == key)) return;
+  // the run's first token
+  int64_t lo = 0, hi = p0;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (a.key[mid] < key) lo = mid + 1;
+    else hi = mid;
+  }
+  const int64_t t0 = lo / a.tile, parts = t - t0 + 1, per = (parts + kJoinGroups - 1) / kJoinGroups;
+  const int lane = threadIdx.x % kJoinLanes, group = threadIdx.x / kJoinLanes;
+  const int64_t c = (static_cast<int64_t>(blockIdx.y) * kJoinLanes + lane) * 8;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < a.dim) {
+    const int64_t from = t0 + group * per, to = min(from + per, t + 1);
+#pragma unroll 4
+    for (int64_t q = from; q < to; ++q) {
+      float f[8];
+      load8<ENGRAM_F32>(a.part, (q * 2 + (q == t0 ? 1 : 0)) * a.dim + c, f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += f[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) share[group][lane][k] = sum[k];
+  __syncthreads();
+  if (group != 0 || c >= a.dim) return;
+  for (int g = 1; g < kJoinGroups; ++g)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] += share[g][lane][k];
+  write_row<OUT>(a, key, c, sum);
+}
+
+// Ids up to this number take rank_kernel.
+constexpr int64_t kMostRanked = 16384;
+
+int64_t sort_blocks(int64_t n) { return (n + kSortBlock - 1) / kSortBlock; }
+
+int sort_passes(int64_t V) {   // digits that hold the keys 0..V
+  int passes = 1;
+  while (passes < 4 && (V >> (passes * kDigitBits)) > 0) ++passes;
+  return passes;
+}
+
+// Sorted tokens of a tile: as many as leave enough tiles to fill the GPU.
+int tile_tokens(int64_t n) { return n <= 4096 ? 8 : 32; }
+
+size_t up256(size_t x) { return (x + 255) & ~size_t{255}; }
+
+struct GradSpace {
+  uint32_t *key[2], *pos[2], *counts;
+  float* part;
+  size_t bytes;
+};
+
+GradSpace carve_grad(void* ws, int64_t n, int64_t dim) {
+  GradSpace g{};
+  size_t used = 0;
+  auto take = [&](size_t bytes) {
+    char* p = ws == nullptr ? nullptr : static_cast<char*>(ws) + used;
+    used += up256(bytes);
+    return p;
+  };
+  const bool ranked = n <= kMostRanked;
+  for (int i = 0; i < (ranked ? 1 : 2); ++i) {
+    g.key[i] = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(n) * 4));
+    g.pos[i] = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(n) * 4));
+  }
+  if (!ranked) g.counts = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(sort_blocks(n)) * kDigits * 4));
+  const int64_t tile = tile_tokens(n), tiles = (n + tile - 1) / tile;
+  g.part = reinterpret_cast<float*>(take(static_cast<size_t>(tiles) * 2 * dim * 4));
+  g.bytes = used;
+  return g;
+}
+
+template <typename F>
+hipError_t by_types(int in, int out, F f) {
+  if (in == ENGRAM_BF16) return out == ENGRAM_BF16 ? f(std::integral_constant<int, ENGRAM_BF16>{}, std::integral_constant<int, ENGRAM_BF16>{})
+                                                   : f(std::integral_constant<int, ENGRAM_BF16>{}, std::integral_constant<int, ENGRAM_F32>{});
+  return out == ENGRAM_BF16 ? f(std::integral_constant<int, ENGRAM_F32>{}, std::integral_constant<int, ENGRAM_BF16>{})
+                            : f(std::integral_constant<int, ENGRAM_F32>{}, std::integral_constant<int, ENGRAM_F32>{});
+}
+
+// The next share of the zeros: of what is left, one part in `launches`.
+struct Zeros {
+  char* at;
+  int64_t bytes;
+  int64_t given = 0;
+  Fill next(int launches) {
+    const int64_t left = bytes - given, share = launches <= 1 ? left : left / launches / 16 * 16;
+    const Fill f{at + given, share};
+    given += f.bytes;
+    return f;
+  }
+};
+unsigned fill_groups(const Fill& f, int threads) { return static_cast<unsigned>((f.bytes + threads * kFillBytes - 1) / (threads * kFillBytes)); }
+
+__global__ void __launch_bounds__(kThreads)
+fill_kernel(Fill fill) { fill_zeros(fill, blockIdx.x, kThreads); }
+
+}  // namespace
+
+hipError_t launch_embed(const int32_t* ids, int64_t n, const void* table, int dtype, int64_t V, int64_t dim, float scale,
+                        int32_t branches, int out_dtype, void* out, hipStream_t s) {
+  const int log_lanes = row_lanes_log2(dim);
+  const int64_t per = kThreads >> log_lanes, most = (int64_t{1} << 23) * per;   // tokens of a launch (2^31 work-items)
+  const int64_t row = branches * dim * (out_dtype == ENGRAM_BF16 ? 2 : 4);
+  for (int64_t i = 0; i < n; i += most) {
+    const int64_t m = std::min(most, n - i);
+    const EmbedArgs a{ids + i, table, static_cast<char*>(out) + i * row, m, V, dim, branches, log_lanes, scale};
+    const hipError_t e = by_types(dtype, out_dtype, [&](auto in, auto to) {
+      launch_k((embed_kernel<decltype(in)::value, decltype(to)::value>), dim3(static_cast<unsigned>((m + per - 1) / per)), dim3(kThreads), 0, s, a);
+      return launch_error();
+    });
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+size_t embed_backward_workspace(int64_t n, int64_t dim) { return carve_grad(nullptr, n, dim).bytes; }
+
+hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout, int dtype, int64_t V, int64_t dim, float scale,
+                                 int32_t branches, bool accumulate, int out_dtype, void* dtable, void* ws, hipStream_t s) {
+  Zeros zeros{static_cast<char*>(dtable), accumulate ? 0 : V * dim * (out_dtype == ENGRAM_BF16 ? 2 : 4)};
+  hipError_t e;
+  if (n == 0) {
+    if (zeros.bytes == 0) return hipSuccess;
+    const Fill f = zeros.next(1);
+    prof_stage("fill_kernel");
+    launch_k(fill_kernel, dim3(fill_groups(f, kThreads)), dim3(kThreads), 0, s, f);
+    return launch_error();
+  }
+  const GradSpace g = carve_grad(ws, n, dim);
+  int sorted = 0;
+  if (n <= kMostRanked) {
+    const Fill f = zeros.next(1);
+    const int groups = static_cast<int>((n + 63) / 64);
+    prof_stage("rank_kernel");
+    launch_k(rank_kernel, dim3(groups + fill_groups(f, kRankThreads)), dim3(kRankThreads), 0, s, ids, static_cast<int>(n), static_cast<uint32_t>(V),
+             g.key[0], g.pos[0], groups, f);
+    if ((e = launch_error()) != hipSuccess) return e;
+  } else {
+    const int passes = sort_passes(V);
+    const int blocks = static_cast<int>(sort_blocks(n));
+    int left = passes * 3;
+    for (int p = 0; p < passes; ++p) {
+      const int from = sorted, to = p == 0 ? 0 : 1 - sorted;
+      const SortPass a{p == 0 ? ids : nullptr, g.key[from], g.pos[from], g.key[to], g.pos[to], g.counts, n, static_cast<uint32_t>(V),
+                       p * kDigitBits, blocks};
+      Fill f = zeros.next(left--);
+      prof_stage("digit_count_kernel");
+      launch_k(digit_count_kernel, dim3(blocks + fill_groups(f, kSortThreads)), dim3(kSortThreads), 0, s, a, f);
+      if ((e = launch_error()) != hipSuccess) return e;
+      f = zeros.next(left--);
+      prof_stage("digit_scan_kernel");
+      launch_k(digit_scan_kernel, dim3(1 + fill_groups(f, kScanThreads)), dim3(kScanThreads), 0, s, g.counts, int64_t{blocks} * kDigits, f);
+      if ((e = launch_error()) != hipSuccess) return e;
+      f = zeros.next(left--);
+      prof_stage("digit_move_kernel");
+      launch_k(digit_move_kernel, dim3(blocks + fill_groups(f, kSortThreads)), dim3(kSortThreads), 0, s, a, f);
+      if ((e = launch_error()) != hipSuccess) return e;
+      sorted = to;
+    }
+  }
+  const int log_lanes = row_lanes_log2(dim), lanes = 1 << log_lanes;
+  const int tile = tile_tokens(n);
+  const int64_t tiles = (n + tile - 1) / tile, per = kThreads / lanes;
+  const SumArgs a{g.key[sorted], g.pos[sorted], dout, dtable, g.part, n, dim, tiles, static_cast<uint32_t>(V), branches, log_lanes, tile,
+                  accumulate ? 1 : 0, scale};
+  prof_stage("tile_sum_kernel");
+  e = by_types(dtype, out_dtype, [&](auto in, auto to) {
+    launch_k((tile_sum_kernel<decltype(in)::value, decltype(to)::value>),
+             dim3(static_cast<unsigned>((tiles + per - 1) / per), static_cast<unsigned>((dim + lanes * 8 - 1) / (lanes * 8))), dim3(kThreads), 0, s, a);
+    return launch_error();
+  });
+  if (e != hipSuccess || tiles == 1) return e;
+  prof_stage("tile_join_kernel");
+  const dim3 grid(static_cast<unsigned>(tiles - 1), static_cast<unsigned>((dim + kJoinLanes * 8 - 1) / (kJoinLanes * 8)));
+  if (out_dtype == ENGRAM_BF16) launch_k(tile_join_kernel<ENGRAM_BF16>, grid, dim3(kJoinThreads), 0, s, a);
+  else launch_k(tile_join_kernel<ENGRAM_F32>, grid, dim3(kJoinThreads), 0, s, a);
+  return launch_error();
+}
+
+}  // namespace engram

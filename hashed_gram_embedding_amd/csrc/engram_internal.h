@@ -385,6 +385,20 @@ hipError_t launch_commit_draft(const float* v, int64_t v_stride, const float* ga
                                const GateConvArgs& g, const StateArgs& st, const int32_t* tokens, const int32_t* proj,
                                int32_t max_n, int32_t vocab, const int32_t* n_accepted, uint32_t* err, hipStream_t s);
 
+// ---- around the layer (embed.hip, adapt.hip, sample.hip) ----
+hipError_t launch_embed(const int32_t* ids, int64_t n, const void* table, int dtype, int64_t V, int64_t dim, float scale,
+                        int32_t branches, int out_dtype, void* out, hipStream_t s);
+size_t embed_backward_workspace(int64_t n, int64_t dim);
+hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout, int dtype, int64_t V, int64_t dim, float scale,
+                                 int32_t branches, bool accumulate, int out_dtype, void* dtable, void* ws, hipStream_t s);
+size_t adapt_workspace(int64_t n_tok, int dtype, int rank);
+hipError_t launch_project_adapted(const void* e, const void* w, int64_t n_tok, int64_t d_mem, int64_t n_out, int dtype, const void* lora_a,
+                                  const void* lora_b, const float* scale, int32_t rank, int32_t adapters, const int32_t* which, int64_t per,
+                                  int out_dtype, void* out, void* ws, hipStream_t s);
+hipError_t launch_sample_tokens(const void* logits, int dtype, int64_t rows, int64_t V, int64_t ld, const float* temperature,
+                                const int32_t* top_k, const float* top_p, const float* min_p, int64_t per, const float* u,
+                                int32_t* tokens, float* logprob, hipStream_t s);
+
 size_t cache_build_workspace(int64_t total_rows);
 size_t cache_update_workspace(int64_t total_rows, int64_t cache_n);
 hipError_t launch_cache_update(const TableArgs& ta, int64_t total_rows, int row_bytes, int64_t cache_n,

@@ -73,6 +73,11 @@ class I8WeightsStruct(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
+class AdaptersStruct(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("rank", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
 class DraftStruct(ctypes.Structure):
     _fields_ = [("v", ctypes.c_void_p), ("v_stride", ctypes.c_int64), ("gamma", ctypes.c_void_p)]
 
@@ -169,6 +174,16 @@ def load_library(path: str) -> ctypes.CDLL:
         "engram_token_probs": (i32, [vp, i32, i64, i64, i64, vp, i64, vp, vp, sz, vp]),
         "engram_verify_drafts_workspace": (sz, [i64, i64]),
         "engram_verify_drafts": (i32, [vp, vp, i32, vp, vp, vp, vp, i64, i32, i64, vp, vp, vp, sz, vp]),
+        "engram_embed": (i32, [vp, i64, vp, i32, i64, i64, ctypes.c_float, i32, i32, vp, vp]),
+        "engram_embed_backward_workspace": (sz, [i64, i64]),
+        "engram_embed_backward": (i32, [vp, i64, vp, i32, i64, i64, ctypes.c_float, i32, i32, i32, vp, vp, sz, vp]),
+        "engram_project_adapted_workspace": (sz, [i64, i32, i32]),
+        "engram_project_adapted": (i32, [vp, vp, i64, i64, i64, i32, ctypes.POINTER(AdaptersStruct), vp, i64, i32, vp, vp,
+                                         sz, vp]),
+        "engram_forward_adapted_workspace": (sz, [i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(AdaptersStruct)]),
+        "engram_forward_adapted": (i32, [vp, vp, i64, i64, ctypes.POINTER(LayerStruct), ctypes.POINTER(AdaptersStruct), vp,
+                                         ctypes.POINTER(DecodeStateStruct), vp, vp, vp, sz, vp]),
+        "engram_sample_tokens": (i32, [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -193,7 +208,10 @@ def exported_names():
             "engram_quantize_i8", "engram_project_i8_workspace", "engram_project_i8", "engram_forward_i8_workspace",
             "engram_forward_i8", "engram_draft_stride", "engram_forward_draft_workspace", "engram_forward_draft",
             "engram_commit_draft", "engram_token_probs_workspace", "engram_token_probs",
-            "engram_verify_drafts_workspace", "engram_verify_drafts"]
+            "engram_verify_drafts_workspace", "engram_verify_drafts",
+            "engram_embed", "engram_embed_backward_workspace", "engram_embed_backward",
+            "engram_project_adapted_workspace", "engram_project_adapted", "engram_forward_adapted_workspace",
+            "engram_forward_adapted", "engram_sample_tokens"]
 
 
 def last_error() -> str:
@@ -857,16 +875,13 @@ def commit_draft(tokens: torch.Tensor, layer: Layer, draft: Draft, n_accepted: t
             ctypes.byref(draft.s), n_accepted.data_ptr(), ctypes.byref(state.s))
 
 
-def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None,
-                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Probabilities float32 [S, R, V] of logits [S, R, V] (or [S, V]; float32
-    or bfloat16, rows may be padded: any uniform row stride) at a temperature
-    float32 [S] (default 1; 0 = all on the largest logit)."""
+def _check_logits(logits: torch.Tensor):
+    """(S, rows of a sequence, V, row stride) of logits [S, R, V] or [S, V]."""
     if logits.dim() not in (2, 3):
         raise ValueError("logits must be [S, R, V] or [S, V]")
-    dev, V, S = logits.device, logits.shape[-1], logits.shape[0]
+    V, S = logits.shape[-1], logits.shape[0]
     per = logits.shape[1] if logits.dim() == 3 else 1
-    _check_tensor("logits", logits, _FLOATS, logits.shape, dev, strided=True)
+    _check_tensor("logits", logits, _FLOATS, logits.shape, logits.device, strided=True)
     ld = logits.stride(-2)
     if S * per <= 1:
         ld = V
@@ -874,6 +889,16 @@ def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None
         ld = logits.stride(0)
     if (V > 1 and logits.stride(-1) != 1) or ld < V or (logits.dim() == 3 and S > 1 and per > 1 and logits.stride(0) != per * ld):
         raise ValueError("logits must have contiguous rows at one row stride")
+    return S, per, V, ld
+
+
+def token_probs(logits: torch.Tensor, temperature: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Probabilities float32 [S, R, V] of logits [S, R, V] (or [S, V]; float32
+    or bfloat16, rows may be padded: any uniform row stride) at a temperature
+    float32 [S] (default 1; 0 = all on the largest logit)."""
+    dev = logits.device
+    S, per, V, ld = _check_logits(logits)
     if temperature is not None:
         _check_tensor("temperature", temperature, _F32, (S,), dev)
     if probs is None:
@@ -915,6 +940,149 @@ def verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor], drafted: 
             u_accept.data_ptr(), u_sample.data_ptr(), S, G, V, tokens.data_ptr(), n_accepted.data_ptr(),
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return tokens, n_accepted
+
+
+def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, branches: int = 1, out_dtype: Optional[str] = None,
+          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Token embeddings [*ids.shape, branches, dim] = scale * table[ids] (int32
+    ids; one outside the table, such as a padding id of -1, gives zeros), in
+    the table's type or out_dtype."""
+    dev = ids.device
+    _check_tensor("ids", ids, _I32, ids.shape, dev)
+    if table.dim() != 2:
+        raise ValueError("table must be [V, dim]")
+    V, dim = table.shape
+    _check_tensor("table", table, _FLOATS, (V, dim), dev)
+    odt = _DT_OF[table.dtype] if out_dtype is None else _DT[out_dtype]
+    shape = (*ids.shape, branches, dim)
+    if out is None:
+        out = _empty(table, shape, _TORCH_DT[odt], stream)
+    else:
+        _check_tensor("out", out, (_TORCH_DT[odt],), shape, dev)
+    _launch(lib().engram_embed, dev, stream, ids.data_ptr(), ids.numel(), table.data_ptr(), _DT_OF[table.dtype], V, dim, scale,
+            branches, odt, out.data_ptr())
+    return out
+
+
+def embed_backward(ids: torch.Tensor, dout: torch.Tensor, vocab: int, scale: float = 1.0, out_dtype: str = "f32",
+                   dtable: Optional[torch.Tensor] = None, accumulate: bool = False, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The gradient [vocab, dim] of embed()'s table from dout [*ids.shape,
+    branches, dim]: the whole table, or added to dtable with accumulate."""
+    dev = ids.device
+    _check_tensor("ids", ids, _I32, ids.shape, dev)
+    if dout.dim() != ids.dim() + 2:
+        raise ValueError("dout must be [*ids.shape, branches, dim]")
+    branches, dim = dout.shape[-2:]
+    _check_tensor("dout", dout, _FLOATS, (*ids.shape, branches, dim), dev)
+    odt = _DT[out_dtype] if dtable is None else _DT_OF.get(dtable.dtype)
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dtable that is added to")
+        dtable = _empty(dout, (vocab, dim), _TORCH_DT[odt], stream)
+    else:
+        _check_tensor("dtable", dtable, _FLOATS, (vocab, dim), dev)
+    n = ids.numel()
+    ws = _workspace(dout, ws, lib().engram_embed_backward_workspace(n, dim), stream)
+    _launch(lib().engram_embed_backward, dev, stream, ids.data_ptr(), n, dout.data_ptr(), _DT_OF[dout.dtype], vocab, dim, scale,
+            branches, int(accumulate), odt, dtable.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
+    return dtable
+
+
+class Adapters:
+    """Low-rank adapters beside one W [n_out, d_mem] (engram_adapters): a [n,
+    rank, d_mem] and b [n, n_out, rank] of W's type, scale float32 [n] (default
+    1)."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        if a.dim() != 3 or b.dim() != 3:
+            raise ValueError("a must be [n, rank, d_mem] and b [n, n_out, rank]")
+        n, rank, d_mem = a.shape
+        _check_tensor("a", a, _FLOATS, (n, rank, d_mem), a.device)
+        _check_tensor("b", b, (a.dtype,), (n, b.shape[1], rank), a.device)
+        if scale is not None:
+            _check_tensor("scale", scale, _F32, (n,), a.device)
+        self.a, self.b, self.scale = a, b, scale
+        self.n, self.rank, self.d_mem, self.n_out = n, rank, d_mem, b.shape[1]
+        self.s = AdaptersStruct(n, rank, a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr())
+
+
+def _check_adapters(ad: Adapters, n_out: int, d_mem: int, dtype, which: torch.Tensor, ids: int, dev):
+    if ad.a.device != dev:
+        raise ValueError(f"the adapters are on {ad.a.device}, the tokens are on {dev}")
+    if ad.a.dtype != dtype or (ad.n_out, ad.d_mem) != (n_out, d_mem):
+        raise ValueError(f"the adapters are {ad.a.dtype} for a W of {(ad.n_out, ad.d_mem)}, W is {dtype} {(n_out, d_mem)}")
+    _check_tensor("which", which, _I32, (ids,), dev)
+
+
+def project_adapted(e: torch.Tensor, w: torch.Tensor, adapters: Adapters, which: torch.Tensor, per: int = 1,
+                    out_dtype: str = "f32", out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """e [..., d_mem] times W^T [n_out, d_mem] plus each request's adapter
+    (engram_project_adapted): which int32 [ceil(n_tok / per)], the adapter of
+    every `per` tokens, -1 for none."""
+    dev, d_mem, lead = e.device, e.shape[-1], e.shape[:-1]
+    n_tok = e.numel() // max(d_mem, 1)
+    _check_tensor("e", e, _FLOATS, e.shape, dev)
+    if w.dim() != 2:
+        raise ValueError("w must be [n_out, d_mem]")
+    n_out = w.shape[0]
+    _check_tensor("w", w, (e.dtype,), (n_out, d_mem), dev)
+    if per < 1:
+        raise ValueError("per must be at least 1")
+    _check_adapters(adapters, n_out, d_mem, e.dtype, which, -(-n_tok // per), dev)
+    odt = _DT[out_dtype]
+    if out is None:
+        out = _empty(e, (*lead, n_out), _TORCH_DT[odt], stream)
+    else:
+        _check_tensor("out", out, (_TORCH_DT[odt],), (*lead, n_out), dev)
+    dt = _DT_OF[e.dtype]
+    ws = _workspace(e, ws, lib().engram_project_adapted_workspace(n_tok, dt, adapters.rank), stream)
+    _launch(lib().engram_project_adapted, dev, stream, e.data_ptr(), w.data_ptr(), n_tok, d_mem, n_out, dt,
+            ctypes.byref(adapters.s), which.data_ptr(), per, odt, out.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
+    return out
+
+
+def forward_adapted(tokens: torch.Tensor, H: torch.Tensor, layer: Layer, adapters: Adapters, which: torch.Tensor,
+                    state: Optional[DecodeState] = None, want_alpha: bool = False, want_y: bool = False,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """forward() with adapter which[b] (int32 [B], -1 for none) beside the
+    layer's W in sequence b's Step 5.  Returns (alpha, y) when asked."""
+    dev, B, T = _check_chunk(tokens, H, layer, state)
+    _check_adapters(adapters, *layer.w.shape, layer.w.dtype, which, B, dev)
+    alpha, y = _layer_outputs(B, T, layer, H, want_alpha, want_y, stream)
+    nbytes = lib().engram_forward_adapted_workspace(B, T, ctypes.byref(layer.s), ctypes.byref(adapters.s))
+    ws = _workspace(H, ws, max(nbytes, 256), stream)
+    _launch(lib().engram_forward_adapted, dev, stream, tokens.data_ptr(), H.data_ptr(), B, T, ctypes.byref(layer.s),
+            ctypes.byref(adapters.s), which.data_ptr(), None if state is None else ctypes.byref(state.s), _ptr(alpha),
+            _ptr(y), ws.data_ptr(), ws.numel())
+    return alpha, y
+
+
+def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                  min_p: Optional[torch.Tensor] = None, want_logprob: bool = False, stream=None):
+    """Tokens int32 [S, R] (or [S]) drawn from logits [S, R, V] (or [S, V];
+    float32 or bfloat16, rows may be padded) with the random numbers u of the
+    same shape; temperature, top_p, min_p float32 and top_k int32 are one a
+    sequence [S] (engram_sample_tokens).  Returns (tokens, logprob or None)."""
+    dev = logits.device
+    S, per, V, ld = _check_logits(logits)
+    shape = logits.shape[:-1]
+    _check_tensor("u", u, _F32, shape, dev)
+    for name, t, kind in (("temperature", temperature, _F32), ("top_k", top_k, _I32), ("top_p", top_p, _F32),
+                          ("min_p", min_p, _F32)):
+        if t is not None:
+            _check_tensor(name, t, kind, (S,), dev)
+    tokens = _empty(logits, shape, torch.int32, stream)
+    logprob = _empty(logits, shape, torch.float32, stream) if want_logprob else None
+    _launch(lib().engram_sample_tokens, dev, stream, logits.data_ptr(), _DT_OF[logits.dtype], S * per, V, ld,
+            None if temperature is None else temperature.data_ptr(), None if top_k is None else top_k.data_ptr(),
+            None if top_p is None else top_p.data_ptr(), None if min_p is None else min_p.data_ptr(), max(per, 1),
+            u.data_ptr(), tokens.data_ptr(), None if logprob is None else logprob.data_ptr())
+    return tokens, logprob
 
 
 def hot_lookup(tokens: torch.Tensor, spec, hot: HotTier, hist: Optional[torch.Tensor] = None,

@@ -599,6 +599,116 @@ engram_status engram_verify_drafts(const void* target, const void* draft, engram
                                    int32_t G, int64_t V, int32_t* tokens, int32_t* n_accepted, void* ws,
                                    size_t ws_bytes, hipStream_t stream);
 
+/* ---- Around the layer: embeddings, adapters, sampling ----
+ * What a model that serves many requests does before, beside and behind its
+ * layers, and the gradient that fine-tuning its tables needs:
+ *   engram_embed             tokens to the first hidden states
+ *   engram_embed_backward    the gradient of that table (or of a hashed one)
+ *   engram_project_adapted   Step 5 with each request's low-rank adapter
+ *   engram_forward_adapted   the layer with them
+ *   engram_sample_tokens     the next tokens from logits
+ * None of these calls synchronises or allocates; all of them can be captured
+ * into a HIP graph.  Results are the same bits from call to call. */
+
+/* out[i][m][c] = scale * table[ids[i]][c] for m < branches (the hidden states
+ * [B][T][M][d] of a model with M residual branches): the product in float32,
+ * rounded once more for BF16 output.  An id outside [0, V) gives zeros.
+ *   ids      device int32 [n]
+ *   table    device [V][dim], F32 or BF16, 16-byte aligned
+ *   out      device [n][branches][dim], F32 or BF16, 16-byte aligned
+ * 0 <= n < 2^31, 1 <= V < 2^31, dim a multiple of 8 up to ENGRAM_MAX_D, 1 <=
+ * branches <= ENGRAM_MAX_BRANCHES (EUNSUPPORTED otherwise); n = 0 is a no-op. */
+engram_status engram_embed(const int32_t* ids, int64_t n, const void* table, engram_dtype dtype, int64_t V, int64_t dim,
+                           float scale, int32_t branches, engram_dtype out_dtype, void* out, hipStream_t stream);
+
+/* The gradient of engram_embed: dtable[v][c] = scale * sum of dout[i][m][c]
+ * over m and over the i with ids[i] = v, in float32 (ids sorted, equal ones in
+ * the order of their positions, so the sums' order is fixed) and rounded once
+ * for BF16 output.  The whole table is written, rows without an id with zeros;
+ * with accumulate != 0 the sum is added to what dtable holds and rows without
+ * an id are left alone (so scale = -rate takes a plain gradient step on a
+ * table itself, at the cost of the rows that were read).  With ids = row
+ * indices of a hashed table (engram_hash_indices plus row_offset) and dout =
+ * the columns of de it is the gradient of engram_gather.
+ *   dout     device [n][branches][dim], F32 or BF16, 16-byte aligned
+ *   dtable   device [V][dim], F32 or BF16, 16-byte aligned
+ *   ws       engram_embed_backward_workspace() bytes, 256-byte aligned (NULL
+ *            where that is 0)
+ * 0 <= n <= 2^28, otherwise as engram_embed.  n = 0 writes zeros (or, with
+ * accumulate, nothing). */
+#define ENGRAM_MAX_EMBED_GRAD_IDS (1 << 28)
+size_t engram_embed_backward_workspace(int64_t n, int64_t dim);
+engram_status engram_embed_backward(const int32_t* ids, int64_t n, const void* dout, engram_dtype dtype, int64_t V, int64_t dim,
+                                    float scale, int32_t branches, int32_t accumulate, engram_dtype out_dtype, void* dtable,
+                                    void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Low-rank adapters beside one W [n_out][d_mem].  An adapter of a smaller rank
+ * is padded with zeros. */
+typedef struct engram_adapters {
+  int32_t n;            /* adapters, 0..2^20                                            */
+  int32_t rank;         /* a multiple of 8, 8..ENGRAM_MAX_ADAPTER_RANK                  */
+  const void* a;        /* device [n][rank][d_mem], W's type, 16-byte aligned           */
+  const void* b;        /* device [n][n_out][rank], W's type, 16-byte aligned           */
+  const float* scale;   /* device [n], or NULL for 1                                    */
+} engram_adapters;
+#define ENGRAM_MAX_ADAPTER_RANK 128
+
+/* out[t] = W e[t] + scale[i] * b[i] (a[i] e[t]), i = which[t / per]: per is
+ * the tokens of one request (T of a [B][T] batch), or 1 with an id for every
+ * token.  An id outside [0, n) (-1) has no adapter.  Sums in float32; in BF16
+ * the adapter's inner product is carried with 16 significand bits; out is
+ * rounded once.  Nothing of one request's adapter reaches another's outputs.
+ *   e        device [n_tok][d_mem], w device [n_out][d_mem], both of dtype
+ *            (F32 or BF16), 16-byte aligned
+ *   which    device int32 [ceil(n_tok / per)]
+ *   out      device [n_tok][n_out], F32, or BF16 in a BF16 call; 16-byte aligned
+ *   ws       engram_project_adapted_workspace() bytes, 256-byte aligned (NULL
+ *            where that is 0)
+ * d_mem and n_out multiples of 64, d_mem up to 65536; n_tok and n_out below
+ * 2^31 (EUNSUPPORTED otherwise).  n_tok = 0 is a no-op. */
+size_t engram_project_adapted_workspace(int64_t n_tok, engram_dtype dtype, int32_t rank);
+engram_status engram_project_adapted(const void* e, const void* w, int64_t n_tok, int64_t d_mem, int64_t n_out,
+                                     engram_dtype dtype, const engram_adapters* ad, const int32_t* which, int64_t per,
+                                     engram_dtype out_dtype, void* out, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* engram_forward with Step 5 as engram_project_adapted in float32: sequence
+ * b's tokens take adapter which[b] (device int32 [B]).  The product reads L->w
+ * and the gathered rows in hdtype (L's w_mx and w_packed are not read); the
+ * layer's d_mem must be a multiple of 64.  Arguments otherwise as
+ * engram_forward; B*T < 2^31.  ws: engram_forward_adapted_workspace() bytes,
+ * 256-byte aligned. */
+size_t engram_forward_adapted_workspace(int64_t B, int64_t T, const engram_layer* L, const engram_adapters* ad);
+engram_status engram_forward_adapted(const int32_t* tokens, void* H, int64_t B, int64_t T, const engram_layer* L,
+                                     const engram_adapters* ad, const int32_t* which, engram_decode_state* st,
+                                     float* alpha_out, float* y_out, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* A token for each row of logits, drawn with the weights w_v = e^((l_v -
+ * max_v l_v) / T) of the entries that stay.  In the order of the logits,
+ * largest first and equal ones by index, stay
+ *   the first top_k (<= 0: all), of those
+ *   the shortest beginning whose weights reach top_p of theirs (>= 1 or NaN:
+ *   all; <= 0: the first), and
+ *   those with w_v >= min_p (<= 0 or NaN: all; above 1 counts as 1),
+ * so the first one always does.  The token is the lowest index whose running
+ * sum over the entries that stay passes u * (their total).  T <= 0 (or NaN)
+ * takes the lowest index of the largest logit.  A logit of -inf has weight 0;
+ * a row of nothing else, one with a NaN, or with +inf at T > 0, gives -1.
+ * Weights are multiples of 2^-F, F = min(50, 62 - ceil(log2 V)), rounded to
+ * nearest (one below half of that is 0), and every sum of them is exact.
+ *   logits   device, F32 or BF16, row r at element r * ld (ld >= V), aligned to
+ *            its elements
+ *   temperature, top_k, top_p, min_p   device [ceil(rows / per)], of rows i*per
+ *            .. i*per + per - 1; each may be NULL (1, all, all, all)
+ *   u        device [rows], random numbers in [0, 1) (outside: the first or the
+ *            last entry that stays)
+ *   tokens   device int32 [rows]
+ *   logprob  device [rows] or NULL: ln(w / total) of the token over the entries
+ *            that stay (0 at T <= 0, -inf with a token of -1)
+ * rows and V below 2^31, per >= 1; rows = 0 is a no-op. */
+engram_status engram_sample_tokens(const void* logits, engram_dtype dtype, int64_t rows, int64_t V, int64_t ld,
+                                   const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                                   int64_t per, const float* u, int32_t* tokens, float* logprob, hipStream_t stream);
+
 /* Engram-Nine hot tier set-up and lookup (see engram_hot_tier).
  *
  * engram_hot_buckets: pilots of a hot set of n_hot n-grams, ceil(n_hot / 4)
@@ -631,8 +741,10 @@ engram_status engram_hot_lookup(const int32_t* tokens, int64_t B, int64_t T, con
  * engram_forward (and engram_forward_noalloc, engram_forward_i8,
  * engram_forward_draft), engram_retrieve, engram_forward_retrieved(_prefetch),
  * engram_gate_conv_forward, engram_hot_lookup, engram_quantize_i8,
- * engram_project_i8, engram_token_probs, engram_verify_drafts and
- * engram_commit_draft on the calling thread time each kernel they launch: the
+ * engram_project_i8, engram_token_probs, engram_verify_drafts,
+ * engram_commit_draft, engram_embed, engram_embed_backward,
+ * engram_project_adapted, engram_forward_adapted and engram_sample_tokens on
+ * the calling thread time each kernel they launch: the
  * start and stop events are recorded by the kernel's own dispatch
  * (hipExtLaunchKernel), so a stage is the kernel's execution interval (events
  * owned by the library and reused).
