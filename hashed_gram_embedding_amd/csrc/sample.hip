@@ -55,30 +55,86 @@ constexpr int kTable = 128;
 
 __device__ __forceinline__ double table_entry(int j) { return exp2(j * (1.0 / kTable)); }
 
-// The weight of a logit and its exponent, in steps of 1 / kTable of a power of two.
+// Bins over the weights: 32 a power of two (8 in the small workgroup); the last
+// one, 60 powers below the largest weight, holds weights of 0.
+constexpr int kSteps = 60 * kTable;
+
+// bf16 logits take few values: the weights of those of kExponents powers of two,
+// up to the row's largest, lie in LDS (both signs), and an entry's weight is
+// one read.
+constexpr int kExponents = 15, kValues = kExponents << 7;
+
 struct Weight {
   double top, a;         // a: kTable log2(e) / T
   int fraction;
+  int bin_shift;
   const double* table;   // LDS
-  // <= 0; a masked logit's is far below every weight (and not the NaN that -inf at T = inf would give)
-  __device__ __forceinline__ double exponent(float l) const { return fmax((static_cast<double>(l) - top) * a, -60.0 * kTable); }
-  // the weight in units of 2^-F
-  __device__ __forceinline__ uint64_t units(double y) const {
+  uint64_t* values;      // LDS, [2][kValues], or null
+  uint32_t base;         // the first value's bits
+  // A logit's exponent in steps of 1 / kTable of a power of two, <= 0; a masked logit's is below every weight (and not
+  // the NaN that -inf at T = inf would give)
+  __device__ __forceinline__ double exponent(float l) const { return fmax((static_cast<double>(l) - top) * a, -static_cast<double>(kSteps)); }
+  // Its weight in units of 2^-F (below 2^52), its bin in the bits above.
+  __device__ __forceinline__ uint64_t formed(float l) const {
     constexpr double kWhole = 0x1.8p52;   // added, it leaves a whole number in the low bits
     constexpr double c1 = 0x1.62e42fefa39efp-8, c2 = 0x1.ebfbdff82c58fp-17, c3 = 0x1.c6b08d704a0c0p-26, c4 = 0x1.3b2ab6fba4e77p-35;   // (ln 2 / 128)^k / k!
-    const double t = y + kWhole, f = y - (t - kWhole);
+    const double y = exponent(l), t = y + kWhole, f = y - (t - kWhole);
     const int n = static_cast<int>(__double_as_longlong(t));
-    const double base = table[n & (kTable - 1)];
+    const double one = table[n & (kTable - 1)];
     const double q = f * fma(fma(fma(c4, f, c3), f, c2), f, c1);
-    const uint64_t w = __double_as_longlong(fma(base, q, base)) + (static_cast<uint64_t>(static_cast<uint32_t>((n >> 7) + fraction) << 20) << 32);
-    return __double_as_longlong(__longlong_as_double(w) + 0x1p52) - __double_as_longlong(0x1p52);
+    const uint64_t w = __double_as_longlong(fma(one, q, one)) + (static_cast<uint64_t>(static_cast<uint32_t>((n >> 7) + fraction) << 20) << 32);
+    const uint64_t whole = __double_as_longlong(__longlong_as_double(w) + 0x1p52);
+    return whole + (static_cast<uint64_t>((static_cast<uint32_t>(-n >> bin_shift) << 20) - 0x43300000u) << 32);
   }
-  __device__ __forceinline__ uint64_t operator()(float l) const { return units(exponent(l)); }
-  // ln of an exponent's weight over a sum of weights
-  __device__ __forceinline__ float log_share(double y, uint64_t total) const {
-    return static_cast<float>((y * (1.0 / kTable) - (log2(static_cast<double>(total)) - fraction)) * 0.69314718055994530942);
+  __device__ __forceinline__ int bin_formed(float l) const {
+    return -static_cast<int>(__double_as_longlong(exponent(l) + 0x1.8p52)) >> bin_shift;
+  }
+  static __device__ __forceinline__ uint64_t units(uint64_t formed) { return formed & ((uint64_t{1} << 52) - 1); }
+  static __device__ __forceinline__ int bin(uint64_t formed) { return static_cast<int>(formed >> 52); }
+  __device__ __forceinline__ uint64_t operator()(float l) const { return units(formed(l)); }
+  // the same, from the values
+  template <bool VALUES>
+  __device__ __forceinline__ uint64_t look(float l) const {
+    if constexpr (!VALUES) return formed(l);
+    const uint32_t bits = __float_as_uint(l) >> 16, at = (bits & 0x7fff) - base;
+    uint64_t w = values[min(at, kValues - 1u) + (bits >> 15) * kValues];
+    if (at >= kValues) w = l == -__builtin_inff() ? static_cast<uint64_t>(kSteps >> bin_shift) << 52 : formed(l);
+    return w;
+  }
+  template <int THREADS>
+  __device__ __forceinline__ void form_values(float row_top) {
+    base = max((__float_as_uint(row_top) >> 23 & 0xffu) + 1, 134u) * 128 - kValues;   // 134: magnitudes up to 128
+    for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) {
+      const uint32_t bits = (base + (i < kValues ? i : i - kValues)) | (i < kValues ? 0 : 0x8000);
+      const float l = __uint_as_float(bits << 16);
+      values[i] = l <= row_top ? formed(l) : 0;
+    }
+    __syncthreads();
+  }
+  // ln of a logit's weight over a sum of weights
+  __device__ __forceinline__ float log_share(float l, uint64_t total) const {
+    return static_cast<float>((exponent(l) * (1.0 / kTable) - (log2(static_cast<double>(total)) - fraction)) * 0.69314718055994530942);
   }
 };
+
+// The smallest float that `holds` (it does for larger ones, and for +inf), next to a guess of it.
+template <typename F>
+__device__ __forceinline__ float smallest(float guess, F holds) {
+  const int lane = threadIdx.x & 63;
+  uint32_t lo = order_key(-__builtin_inff()), hi = order_key(__builtin_inff());   // keys: lo .. hi hold at hi
+  uint32_t at = min(max(order_key(guess), lo + 32), hi - 32) - 32;
+  uint32_t stride = 1;
+  for (;;) {   // 64 keys at a time: around the guess, then over what is left
+    const uint32_t key = min(at + lane * stride, hi);
+    const uint64_t yes = __ballot(holds(of_key(key)));
+    const int first = yes != 0 ? __builtin_ctzll(yes) : 64;
+    if (first < 64) hi = min(hi, at + first * stride);
+    if (first > 0) lo = max(lo, min(at + (first - 1) * stride, hi) + 1);
+    if (lo >= hi) return of_key(hi);
+    stride = max((hi - lo) / 63, 1u);
+    at = lo;
+  }
+}
 
 // A row as its workgroup reads it: each wavefront a contiguous part, in runs
 // of 4 a lane.  Every pass reads it again, the first from memory, the others
@@ -138,13 +194,16 @@ struct Row {
 
 // What a workgroup of THREADS keeps in LDS: two of 512 fit a CU; a row of a
 // workgroup of 256 (4096 entries at most) always fits its list.
-template <int THREADS>
+template <int DT, int THREADS>
 struct SampleShared {
+  static constexpr bool kLooks = DT == ENGRAM_BF16 && THREADS > 256;   // weights of values
   static constexpr int kBinBits = THREADS <= 256 ? 9 : 11, kBins = 1 << kBinBits;
-  static constexpr int kListed = THREADS <= 256 ? 5120 : 7552;   // entries of the list
-  static constexpr int kOneBin = THREADS <= 256 ? 1024 : 2048;   // of them, at its end, those of the bin in which a cut lies
+  static constexpr int kBinShift = THREADS <= 256 ? 4 : 2, kLastBin = kSteps >> kBinShift;
+  static constexpr int kListed = THREADS <= 256 ? 5120 : kLooks ? 3584 : 7424;   // entries of the list
+  static constexpr int kOneBin = 1024;                                           // of them, at its end, those of the bin in which a cut lies
   uint64_t bins[kBins];
   uint64_t list[kListed];
+  uint64_t values[kLooks ? 2 * kValues : 1];
   double table[kTable];
   uint64_t few[64];
   uint64_t wave[THREADS / 64], wave2[THREADS / 64];
@@ -155,6 +214,7 @@ struct SampleShared {
   int listed;
   int few_n;
 };
+static_assert(kSteps >> 2 < 2048 && kSteps >> 4 < 512, "every bin has its place");
 
 // Sums of the threads before this one; *total: of all.
 template <int THREADS>
@@ -174,8 +234,8 @@ __device__ __forceinline__ uint64_t group_scan(uint64_t x, uint64_t* wave, uint6
 }
 
 // Smallest and largest of the workgroup's values.
-template <int THREADS>
-__device__ __forceinline__ void group_range(SampleShared<THREADS>& sh, uint64_t* lo, uint64_t* hi) {
+template <int THREADS, typename Sh>
+__device__ __forceinline__ void group_range(Sh& sh, uint64_t* lo, uint64_t* hi) {
   uint64_t a = *lo, b = *hi;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
@@ -198,9 +258,9 @@ __device__ __forceinline__ void group_range(SampleShared<THREADS>& sh, uint64_t*
 
 // The bin in which the bins' running sum (beginning at `before`) reaches `want`, into
 // sh.bin, and the sum in front of it into sh.before.  The bins' sums are complete.
-template <int THREADS>
-__device__ __forceinline__ void find_bin(SampleShared<THREADS>& sh, uint64_t before, uint64_t want) {
-  constexpr int kEach = SampleShared<THREADS>::kBins / THREADS;
+template <int THREADS, typename Sh>
+__device__ __forceinline__ void find_bin(Sh& sh, uint64_t before, uint64_t want) {
+  constexpr int kEach = Sh::kBins / THREADS;
   uint64_t b[kEach], sum = 0, all;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -219,10 +279,10 @@ __device__ __forceinline__ void find_bin(SampleShared<THREADS>& sh, uint64_t bef
   __syncthreads();
 }
 
-template <int THREADS>
-__device__ __forceinline__ void clear_bins(SampleShared<THREADS>& sh) {
+template <int THREADS, typename Sh>
+__device__ __forceinline__ void clear_bins(Sh& sh) {
 #pragma unroll
-  for (int i = 0; i < SampleShared<THREADS>::kBins / THREADS; ++i) sh.bins[i * THREADS + threadIdx.x] = 0;
+  for (int i = 0; i < Sh::kBins / THREADS; ++i) sh.bins[i * THREADS + threadIdx.x] = 0;
 }
 
 // An entry's place in the order: smaller comes first.
@@ -236,11 +296,11 @@ struct Place {
 // (it does), given the sum `before` of those in front of the ones that
 // `entries` visits (each once, as f(place), all in lo .. hi).  Rounds of kBins
 // bins over the places that are left; the last 64 of them in registers.
-template <int THREADS, typename Entries, typename Amount>
-__device__ __forceinline__ uint64_t find_place(SampleShared<THREADS>& sh, uint64_t lo, uint64_t hi, uint64_t before, uint64_t want,
+template <int THREADS, typename Sh, typename Entries, typename Amount>
+__device__ __forceinline__ uint64_t find_place(Sh& sh, uint64_t lo, uint64_t hi, uint64_t before, uint64_t want,
                                                Entries entries, Amount amount) {
   for (;;) {
-    const int shift = max(64 - __builtin_clzll((hi - lo) | 1) - SampleShared<THREADS>::kBinBits, 0);
+    const int shift = max(64 - __builtin_clzll((hi - lo) | 1) - Sh::kBinBits, 0);
     __syncthreads();
     clear_bins<THREADS>(sh);
     if (threadIdx.x == 0) sh.few_n = 0;
@@ -287,66 +347,76 @@ __device__ __forceinline__ uint64_t find_place(SampleShared<THREADS>& sh, uint64
   }
 }
 
-// What a row's passes know of it.
+// What a row's passes know of it.  The entries that stay are those up to a
+// place of the order; min_p ends at one too.
 template <int DT, int THREADS>
 struct Draw {
-  static constexpr int kBins = SampleShared<THREADS>::kBins, kListed = SampleShared<THREADS>::kListed;
-  SampleShared<THREADS>& sh;
+  using Sh = SampleShared<DT, THREADS>;
+  Sh& sh;
   Row<DT, THREADS> row;
   Weight weight;
   Place place;
-  float top, step;          // bins over the logits: their distance from the largest in steps
-  uint64_t cut;             // the last place that stays
-  float lcut;               // its logit
-  double least;             // min_p as an exponent
-  float floor_l;            // below it nothing stays by min_p
+  uint64_t cut;      // the last place that stays
+  float lcut;        // its logit
+  uint32_t vcut;     // its index
 
-  // (not decreasing in the distance)
-  __device__ __forceinline__ int bin_of(float l) const { return static_cast<int>(fminf((top - l) * step, kBins - 1.0f)); }
-  __device__ __forceinline__ bool in(float l, uint32_t v) const {
-    return l >= lcut && (l > lcut || v <= static_cast<uint32_t>(cut)) && l > -__builtin_inff();
-  }
-  // an entry's weight, 0 where it does not stay
-  __device__ __forceinline__ uint64_t kept(float l, uint32_t v) const {
-    const double y = weight.exponent(l);
-    const uint64_t w = weight.units(y);
-    return l >= lcut && (l > lcut || v <= static_cast<uint32_t>(cut)) && y >= least ? w : 0;
-  }
   __device__ __forceinline__ void set_cut(uint64_t c) {
     cut = c;
-    lcut = place.logit(c);
+    lcut = c == ~uint64_t{0} ? -__builtin_inff() : place.logit(c);
+    vcut = static_cast<uint32_t>(c);
   }
+  __device__ __forceinline__ bool in(float l, uint32_t v) const { return l >= lcut && (l > lcut || v <= vcut); }
+  // f(l, index, whether it is up to the cut) of the row's entries.  Equal logits
+  // matter only in the run in which the cut's index lies: in those before it
+  // entries equal to the cut's stay, in those behind it they do not.
+  template <int U, bool CUT, typename F>
+  __device__ __forceinline__ void each(F f) const {
+    if constexpr (!CUT) {
+      row.template each<U>([&](float l, uint32_t v) { f(l, v, true); });
+    } else {
+      const float above = lcut == __builtin_inff() ? lcut : of_key(order_key(lcut) + 1);
+      row.template each_quad<U>([&](const float (&l)[4], uint32_t v) {
+        const uint32_t v0 = __builtin_amdgcn_readfirstlane(v);   // 256 entries of a wavefront from here
+        const float from = v0 + 255 <= vcut ? lcut : above;
+        const bool mixed = v0 <= vcut && vcut < v0 + 255;
+        if (!__any(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= lcut)) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f(l[i], v + i, l[i] >= from || (mixed && in(l[i], v + i)));
+      });
+      if (row.vt < row.V) f(row.xt, static_cast<uint32_t>(row.vt), in(row.xt, static_cast<uint32_t>(row.vt)));
+    }
+  }
+  __device__ __forceinline__ uint64_t look(float l) const { return weight.template look<Sh::kLooks>(l); }
   __device__ __forceinline__ uint64_t share(float p, uint64_t all) const {
     return max(static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(all))), uint64_t{1});
   }
-  // All entries with a logit of `least_l` and more (any order) into the list; false: too many.
-  __device__ __forceinline__ bool collect(float least_l, int* n) {
+  // All entries with a logit of `from` and more (any order) into the list; false: too many.
+  __device__ __forceinline__ bool collect(float from, int* n) {
     __syncthreads();
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
-    row.template each_quad<4>([&](const float (&l)[4], uint32_t v) {
-      if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= least_l)) return;
+    auto take = [&](float l, uint32_t v) {
+      if (l >= from && l > -__builtin_inff()) {
+        const int at = atomicAdd(&sh.listed, 1);
+        if (at < Sh::kListed) sh.list[at] = place(l, v);
+      }
+    };
+    row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
+      if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= from)) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (l[k] >= least_l && l[k] > -__builtin_inff()) {
-          const int at = atomicAdd(&sh.listed, 1);
-          if (at < kListed) sh.list[at] = place(l[k], v + k);
-        }
+      for (int k = 0; k < 4; ++k) take(l[k], v + k);
     });
-    if (row.vt < row.V && row.xt >= least_l && row.xt > -__builtin_inff()) {
-      const int at = atomicAdd(&sh.listed, 1);
-      if (at < kListed) sh.list[at] = place(row.xt, static_cast<uint32_t>(row.vt));
-    }
+    if (row.vt < row.V) take(row.xt, static_cast<uint32_t>(row.vt));
     __syncthreads();
     *n = sh.listed;
-    return *n <= kListed;
+    return *n <= Sh::kListed;
   }
 };
 
 // f(place) of the list's entries up to a cut.
-template <int THREADS>
+template <int THREADS, typename Sh>
 struct Listed {
-  const SampleShared<THREADS>& sh;
+  const Sh& sh;
   int n;
   uint64_t cut;
   template <typename F>
@@ -356,37 +426,26 @@ struct Listed {
   }
 };
 
-// The cut of a row: SUM ? where the weights reach top_p of all up to the cut
-// so far : where the first top_k end.  Bins over the logits, then the places in
-// the one bin in which it ends.  The entries up to that bin come into the list,
-// its own entries at the list's end; *listed: how many there are, -1 where
-// they do not fit.
-template <bool SUM, int DT, int THREADS>
+// The cut of a row whose entries that stay are not few: SUM ? where the weights
+// reach top_p of all up to the cut so far : where the first top_k end.  Bins
+// over the weights, then the places in the one bin in which it ends.  The
+// entries up to that bin come into the list, its own at the list's end;
+// *listed: how many there are, -1 where they do not fit.
+template <bool SUM, bool CUT, int DT, int THREADS>
 __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float p, int* listed) {
-  SampleShared<THREADS>& sh = d.sh;
-  using Sh = SampleShared<THREADS>;
+  using Sh = SampleShared<DT, THREADS>;
+  Sh& sh = d.sh;
   constexpr int kBins = Sh::kBins, kOneBin = Sh::kOneBin, kFront = Sh::kListed - kOneBin;
   *listed = -1;
   __syncthreads();
   clear_bins<THREADS>(sh);
   if (threadIdx.x == 0) sh.listed = sh.few_n = 0;
   __syncthreads();
-  uint64_t rest = 0;   // the last bin takes whatever lies far from the largest: not by atomics
-  auto count = [&](float l, uint32_t v, uint64_t w) {
-    const int b = d.bin_of(l);
-    const bool in = d.in(l, v);
-    rest += in && b == kBins - 1 ? w : 0;
-    if (in && b < kBins - 1) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[b]), w);
-  };
-  d.row.template each_quad<2>([&](const float (&l)[4], uint32_t v) {
-    uint64_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = SUM ? d.weight(l[i]) : 1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) count(l[i], v + i, w[i]);
+  d.template each<2, CUT>([&](float l, uint32_t, bool in) {
+    const uint64_t w = d.look(l);
+    if (in && d.weight.bin(w) < Sh::kLastBin)   // (entries of weight 0 count for nothing)
+      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) : 1);
   });
-  if (d.row.vt < d.row.V) count(d.row.xt, static_cast<uint32_t>(d.row.vt), SUM ? d.weight(d.row.xt) : 1);
-  if (rest > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[kBins - 1]), rest);
   __syncthreads();
   uint64_t want = k;
   {
@@ -395,16 +454,21 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     for (int i = 0; i < kBins / THREADS; ++i) sum += sh.bins[i * THREADS + threadIdx.x];
     group_scan<THREADS>(sum, sh.wave, &all);
     if constexpr (SUM) want = d.share(p, all);
-    if (want >= all) return;   // everything stays
+    if (want >= all) return;   // everything of any weight stays
   }
   find_bin<THREADS>(sh, 0, want);
   const int bin = sh.bin;
   const uint64_t before = sh.before;
+  // the smallest logits of the bin and of the one before
+  auto first_of = [&](int b) {
+    return smallest(static_cast<float>(d.weight.top - (((b + 1) << Sh::kBinShift) - 0.5) / d.weight.a), [&](float l) { return l >= d.weight.top || d.weight.bin_formed(l) <= b; });
+  };
+  const float from = first_of(bin), front_from = bin > 0 ? first_of(bin - 1) : __builtin_inff();
   uint64_t lo = ~uint64_t{0}, hi = 0;
-  d.row.template each<4>([&](float l, uint32_t v) {
-    if (!d.in(l, v) || d.bin_of(l) > bin) return;
+  auto take = [&](float l, uint32_t v) {
+    if (!(l >= from) || (CUT && !d.in(l, v))) return;
     const uint64_t q = d.place(l, v);
-    if (d.bin_of(l) < bin) {
+    if (l >= front_from) {
       const int at = atomicAdd(&sh.listed, 1);
       if (at < kFront) sh.list[at] = q;
     } else {
@@ -413,7 +477,13 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
       const int at = atomicAdd(&sh.few_n, 1);
       if (at < kOneBin) sh.list[kFront + at] = q;
     }
+  };
+  d.row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
+    if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= from)) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) take(l[i], v + i);
   });
+  if (d.row.vt < d.row.V) take(d.row.xt, static_cast<uint32_t>(d.row.vt));
   group_range<THREADS>(sh, &lo, &hi);   // (its barrier: the list is complete)
   const int front = sh.listed, one = sh.few_n;
   auto amount = [&](uint64_t at) { return SUM ? d.weight(d.place.logit(at)) : uint64_t{1}; };
@@ -423,12 +493,13 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     }, amount));
     if (front > kFront) return;
     // the bin's entries behind the others
-    uint64_t q[kOneBin / THREADS];
+    constexpr int kEach = (kOneBin + THREADS - 1) / THREADS;
+    uint64_t q[kEach];
 #pragma unroll
-    for (int i = 0; i < kOneBin / THREADS; ++i) q[i] = sh.list[kFront + i * THREADS + threadIdx.x];
+    for (int i = 0; i < kEach; ++i) q[i] = sh.list[kFront + i * THREADS + threadIdx.x];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kOneBin / THREADS; ++i) {
+    for (int i = 0; i < kEach; ++i) {
       const int at = i * THREADS + threadIdx.x;
       if (at < one) sh.list[front + at] = q[i];
     }
@@ -438,7 +509,7 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
   }
   d.set_cut(find_place<THREADS>(sh, lo, hi, before, want, [&](auto f) {   // (many equal logits)
     d.row.template each<2>([&](float l, uint32_t v) {
-      if (d.in(l, v) && d.bin_of(l) == bin) f(d.place(l, v));
+      if (l >= from && !(l >= front_from) && (!CUT || d.in(l, v))) f(d.place(l, v));
     });
   }, amount));
 }
@@ -446,7 +517,8 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
 template <int DT, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 4)   // (four wavefronts a SIMD: two workgroups of 512 a CU)
 sample_kernel(SampleArgs a) {
-  __shared__ SampleShared<THREADS> sh;
+  using Sh = SampleShared<DT, THREADS>;
+  __shared__ Sh sh;
   const int64_t row_at = blockIdx.x, seq = row_at / a.per, V = a.V;
   constexpr int size = DT == ENGRAM_BF16 ? 2 : 4;
   Row<DT, THREADS> row;
@@ -458,15 +530,18 @@ sample_kernel(SampleArgs a) {
   const float u = a.u[row_at];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
-  float own = row.xt;   // this thread's largest
-  bool nan = own != own;
-  row.template each_quad<8>([&](const float (&l)[4], uint32_t) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      nan |= l[k] != l[k];
-      own = fmaxf(own, l[k]);
-    }
+  // this thread's largest, and the first run of four that holds it
+  float own = -__builtin_inff();
+  uint32_t own_v = 0;
+  bool nan = row.xt != row.xt;
+  row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
+    nan |= __builtin_isunordered(l[0], l[1]) | __builtin_isunordered(l[2], l[3]);
+    const float x = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+    own_v = x > own ? v : own_v;
+    own = fmaxf(own, x);
   });
+  const float quads_own = own;
+  own = fmaxf(own, row.xt);
   const float top = group_max<THREADS>(own, nan, sh.red);
   if (top != top || top == -__builtin_inff() || (top == __builtin_inff() && temp > 0.f)) {
     if (threadIdx.x == 0) {
@@ -475,12 +550,19 @@ sample_kernel(SampleArgs a) {
     }
     return;
   }
+  auto at_index = [&](int64_t v) {
+    if constexpr (DT == ENGRAM_BF16) return bf16_to_f32(static_cast<const uint16_t*>(row.in)[v]);
+    else return static_cast<const float*>(row.in)[v];
+  };
   if (!(temp > 0.f)) {
-    uint32_t at = ~0u;
-    if (own == top) row.template each<4>([&](float l, uint32_t v) { at = l == top ? min(at, v) : at; });
     if (threadIdx.x == 0) sh.bin = INT32_MAX;
     __syncthreads();
-    if (at != ~0u) atomicMin(&sh.bin, static_cast<int>(at));
+    if (quads_own == top) {
+      while (at_index(own_v) != top) ++own_v;
+      atomicMin(&sh.bin, static_cast<int>(own_v));
+    } else if (own == top) {
+      atomicMin(&sh.bin, static_cast<int>(row.vt));
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
       a.tokens[row_at] = sh.bin;
@@ -491,15 +573,11 @@ sample_kernel(SampleArgs a) {
 
   if (threadIdx.x < kTable) sh.table[threadIdx.x] = table_entry(threadIdx.x);   // (a barrier follows before its first use)
   constexpr double kLog2e = 1.4426950408889634074;
-  // bins over 48 powers of two
-  Draw<DT, THREADS> d{sh, row, Weight{top, kTable * kLog2e / temp, a.fraction, sh.table}, Place{order_key(top)}, top, 0.f, ~uint64_t{0},
-                      -__builtin_inff(), m > 0.f ? kTable * log2(static_cast<double>(fminf(m, 1.0f))) : -__builtin_inf(), -__builtin_inff()};
-  d.step = fminf(fmaxf(static_cast<float>(d.weight.a) * (d.kBins / 48.0f / kTable), 0x1p-126f), 0x1p126f);
-  if (m > 0.f && d.weight.a > 0.0) {   // the logit at which min_p ends, and a margin for the roundings
-    const double at = top + d.least / d.weight.a;
-    d.floor_l = static_cast<float>(at - 1e-6 * (fabs(at) + fabs(static_cast<double>(top))));
-  }
-  const bool by_k = top_k > 0 && top_k < V, by_p = p < 1.0f;
+  Draw<DT, THREADS> d{sh, row, Weight{top, kTable * kLog2e / temp, a.fraction, Sh::kBinShift, sh.table, sh.values, 0u}, Place{order_key(top)},
+                      ~uint64_t{0}, -__builtin_inff(), ~0u};
+  const bool by_k = top_k > 0 && top_k < V, by_p = p < 1.0f, by_m = m > 0.f;
+  const auto one = [](uint64_t) { return uint64_t{1}; };
+  const auto weight_of = [&](uint64_t q) { return d.weight(d.place.logit(q)); };
 
   // Few entries stay (a small top_k): then a list holds them, and the rest is done on
   // the list.  The threads' largest logits bound the top_k-th from below.
@@ -509,69 +587,75 @@ sample_kernel(SampleArgs a) {
     const uint64_t mine = own > -__builtin_inff() ? d.place(own, threadIdx.x) : ~uint64_t{0};
     uint64_t lo = mine, hi = mine;
     group_range<THREADS>(sh, &lo, &hi);
-    const uint64_t kth = find_place<THREADS>(sh, lo, hi, 0, top_k, [&](auto f) { f(mine); }, [](uint64_t) { return uint64_t{1}; });
-    const float least_l = kth == ~uint64_t{0} ? -__builtin_inff() : d.place.logit(kth);
+    const uint64_t kth = find_place<THREADS>(sh, lo, hi, 0, top_k, [&](auto f) { f(mine); }, one);
+    const float from = kth == ~uint64_t{0} ? -__builtin_inff() : d.place.logit(kth);
     int n;
-    if (d.collect(least_l, &n)) {
+    if (d.collect(from, &n)) {
       listed = n;
-      if (n > top_k) {
-        d.set_cut(find_place<THREADS>(sh, 0, d.place(least_l, ~0u), 0, top_k, Listed<THREADS>{sh, n, ~uint64_t{0}},
-                                      [](uint64_t) { return uint64_t{1}; }));
-      }
+      if (n > top_k) d.set_cut(find_place<THREADS>(sh, 0, d.place(from, ~0u), 0, top_k, Listed<THREADS, Sh>{sh, n, ~uint64_t{0}}, one));
     }
   }
-  if (by_k && listed < 0) cut_row<false>(d, top_k, 0.f, &listed);
-  bool p_left = by_p;
-  if (by_p && listed < 0) {
-    cut_row<true>(d, 0, p, &listed);
-    p_left = false;
+  float least = -__builtin_inff();   // where min_p ends
+  if (by_m) {
+    __syncthreads();                 // the table
+    const double y = kTable * log2(static_cast<double>(fminf(m, 1.0f)));
+    least = smallest(static_cast<float>(top + y / d.weight.a), [&](float l) { return l >= top || d.weight.exponent(l) >= y; });
   }
-  if (m > 0.f && !by_k && !by_p) {   // few entries stay by min_p alone
+  if (by_m && !by_k && !by_p) {      // few entries stay by min_p alone
     int n;
-    if (d.collect(d.floor_l, &n)) listed = n;
+    if (d.collect(least, &n)) listed = n;
+  }
+  bool p_left = by_p;
+  if (listed < 0) {
+    __syncthreads();
+    if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
+    if (by_k) cut_row<false, false>(d, top_k, 0.f, &listed);
+    if (by_p && listed < 0) {
+      if (d.cut == ~uint64_t{0}) cut_row<true, false>(d, 0, p, &listed);
+      else cut_row<true, true>(d, 0, p, &listed);
+      p_left = false;
+    }
   }
   __syncthreads();
+  if (listed >= 0 && p_left) {
+    uint64_t sum = 0, all;
+    Listed<THREADS, Sh>{sh, listed, d.cut}([&](uint64_t q) { sum += weight_of(q); });
+    group_scan<THREADS>(sum, sh.wave, &all);
+    d.set_cut(find_place<THREADS>(sh, 0, d.lcut > -__builtin_inff() ? d.place(d.lcut, ~0u) : ~uint64_t{0}, 0, d.share(p, all),
+                                  Listed<THREADS, Sh>{sh, listed, d.cut}, weight_of));
+  }
+  if (by_m && least > d.lcut) d.set_cut(d.place(least, ~0u));
+  auto wanted = [&](uint64_t total) {   // the token is the first whose running sum is above this
+    return min(static_cast<uint64_t>(fmin(fmax(static_cast<double>(u), 0.0), 1.0) * static_cast<double>(total)), total - 1);
+  };
+  auto write = [&](uint32_t v, float l, uint64_t total) {
+    a.tokens[row_at] = static_cast<int32_t>(v);
+    if (a.logprob != nullptr) a.logprob[row_at] = d.weight.log_share(l, total);
+  };
   if (listed >= 0) {
-    auto weight_of = [&](uint64_t q) { return d.weight(d.place.logit(q)); };
-    const uint64_t last = d.lcut > -__builtin_inff() ? d.place(d.lcut, ~0u) : ~uint64_t{0};
-    if (p_left) {
-      uint64_t sum = 0, all;
-      Listed<THREADS>{sh, listed, d.cut}([&](uint64_t q) { sum += weight_of(q); });
-      group_scan<THREADS>(sum, sh.wave, &all);
-      d.set_cut(find_place<THREADS>(sh, 0, last, 0, d.share(p, all),
-                                    Listed<THREADS>{sh, listed, d.cut}, weight_of));
-    }
-    auto stays = [&](uint64_t q) {
-      const double y = d.weight.exponent(d.place.logit(q));
-      return y >= d.least ? d.weight.units(y) : 0;
-    };
-    const Listed<THREADS> entries{sh, listed, d.cut};
+    const Listed<THREADS, Sh> entries{sh, listed, d.cut};
     uint64_t sum = 0, total;
-    entries([&](uint64_t q) { sum += stays(q); });
+    entries([&](uint64_t q) { sum += weight_of(q); });
     group_scan<THREADS>(sum, sh.wave, &total);
-    const uint64_t want = min(static_cast<uint64_t>(fmin(fmax(static_cast<double>(u), 0.0), 1.0) * static_cast<double>(total)), total - 1);
     // by index: the entry's place with its halves exchanged
-    const uint64_t found = find_place<THREADS>(sh, 0, static_cast<uint64_t>(V) << 32 | ~0u, 0, want + 1, [&](auto f) {
+    const uint64_t found = find_place<THREADS>(sh, 0, static_cast<uint64_t>(V) << 32 | ~0u, 0, wanted(total) + 1, [&](auto f) {
       entries([&](uint64_t q) { f(q << 32 | q >> 32); });
-    }, [&](uint64_t q) { return stays(q << 32 | q >> 32); });
-    if (threadIdx.x == 0) {
-      a.tokens[row_at] = static_cast<int32_t>(found >> 32);
-      if (a.logprob != nullptr)
-        a.logprob[row_at] = d.weight.log_share(d.weight.exponent(d.place.logit(found << 32)), total);
-    }
+    }, [&](uint64_t q) { return weight_of(q << 32 | q >> 32); });
+    if (threadIdx.x == 0) write(static_cast<uint32_t>(found >> 32), d.place.logit(found << 32), total);
     return;
   }
 
   // a wavefront's part of the row each, and the entries behind the quads
-  const float lowest = fmaxf(d.lcut, d.floor_l);
-  uint64_t sum = 0;
-  row.template each_quad<2>([&](const float (&l)[4], uint32_t v) {
-    if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= lowest)) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum += d.kept(l[i], v + i);
-  });
+  auto kept = [&](float l, uint32_t v) -> uint64_t { return d.in(l, v) ? d.weight.units(d.look(l)) : 0; };
+  uint64_t sum = 0, tail = 0;
+  auto add = [&](float l, uint32_t v, bool in) {
+    const uint64_t w = d.weight.units(d.look(l));
+    (v < row.quads * 4 ? sum : tail) += in ? w : 0;
+  };
+  if (d.cut == ~uint64_t{0}) d.template each<2, false>(add);
+  else d.template each<2, true>(add);
   sum = wave_scan(sum);
-  uint64_t tail = wave == 0 ? wave_scan(row.vt < V ? d.kept(row.xt, static_cast<uint32_t>(row.vt)) : uint64_t{0}) : 0;
+  tail = wave_scan(tail);
   __syncthreads();
   if (lane == 63) sh.part[wave] = sum;
   if (threadIdx.x == 63) sh.part[THREADS / 64] = tail;
@@ -579,8 +663,7 @@ sample_kernel(SampleArgs a) {
   uint64_t total = 0;
 #pragma unroll
   for (int w = 0; w <= THREADS / 64; ++w) total += sh.part[w];
-  // the token is the first whose running sum is above `want`
-  const uint64_t want = min(static_cast<uint64_t>(fmin(fmax(static_cast<double>(u), 0.0), 1.0) * static_cast<double>(total)), total - 1);
+  const uint64_t want = wanted(total);
   uint64_t at = 0;
   int part = 0;
   while (at + sh.part[part] <= want) at += sh.part[part++];
@@ -590,23 +673,16 @@ sample_kernel(SampleArgs a) {
   const int64_t v1 = behind ? V : min(v0 + row.part * 256, row.quads * 4);
   const int64_t run = (v1 - v0 + THREADS - 1) / THREADS;
   const int64_t b = min(v0 + threadIdx.x * run, v1), e = min(b + run, v1);
-  auto at_index = [&](int64_t v) {
-    if constexpr (DT == ENGRAM_BF16) return bf16_to_f32(static_cast<const uint16_t*>(row.in)[v]);
-    else return static_cast<const float*>(row.in)[v];
-  };
   uint64_t mine = 0, all;
 #pragma unroll 4
-  for (int64_t v = b; v < e; ++v) mine += d.kept(at_index(v), static_cast<uint32_t>(v));
+  for (int64_t v = b; v < e; ++v) mine += kept(at_index(v), static_cast<uint32_t>(v));
   at += group_scan<THREADS>(mine, sh.wave, &all);
   if (at <= want && want < at + mine) {   // one thread's
     for (int64_t v = b; v < e; ++v) {
       const float l = at_index(v);
-      const uint64_t w = d.kept(l, static_cast<uint32_t>(v));
-      at += w;
-      if (w > 0 && at > want) {
-        a.tokens[row_at] = static_cast<int32_t>(v);
-        if (a.logprob != nullptr)
-          a.logprob[row_at] = d.weight.log_share(d.weight.exponent(l), total);
+      at += kept(l, static_cast<uint32_t>(v));
+      if (at > want) {
+        write(static_cast<uint32_t>(v), l, total);
         break;
       }
     }
