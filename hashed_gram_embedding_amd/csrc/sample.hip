@@ -181,6 +181,29 @@ struct Row {
       for (int i = 0; i < U; ++i) x[i] = next[i];
     }
   }
+  // f(l[4], index of the first) in the order of the row (the workgroup's runs side by side): for the
+  // pass from memory, which streams a row faster so than in a part for each wavefront.
+  template <int U, typename F>
+  __device__ __forceinline__ void stream(F f) const {
+    Quad<DT> x[U], next[U];
+    auto load = [&](Quad<DT> (&y)[U], int64_t q) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) y[i] = load_quad<DT>(in, q + i * THREADS, quads);
+    };
+    load(x, threadIdx.x);
+    for (int64_t q = threadIdx.x; q < quads; q += U * THREADS) {
+      load(next, q + U * THREADS);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float l[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l[k] = x[i].at(k);
+        f(l, static_cast<uint32_t>(q + i * THREADS) * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) x[i] = next[i];
+    }
+  }
   // f(l, index), the entries behind the quads among them
   template <int U, typename F>
   __device__ __forceinline__ void each(F f) const {
@@ -200,7 +223,6 @@ struct SampleShared {
   static constexpr int kBinBits = THREADS <= 256 ? 9 : 11, kBins = 1 << kBinBits;
   static constexpr int kBinShift = THREADS <= 256 ? 4 : 2, kLastBin = kSteps >> kBinShift;
   static constexpr int kListed = THREADS <= 256 ? 5120 : kLooks ? 3584 : 7424;   // entries of the list
-  static constexpr int kOneBin = 1024;                                           // of them, at its end, those of the bin in which a cut lies
   uint64_t bins[kBins];
   uint64_t list[kListed];
   uint64_t values[kLooks ? 2 * kValues : 1];
@@ -390,23 +412,41 @@ struct Draw {
   __device__ __forceinline__ uint64_t share(float p, uint64_t all) const {
     return max(static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(all))), uint64_t{1});
   }
+  // Those of a run whose bit of `which` is set into the list from `at` on, which holds `most` of them; *n counts them.
+  // One LDS atomic a wavefront and run.
+  __device__ __forceinline__ void append(const float (&l)[4], uint32_t v, uint32_t which, int at, int most, int* n) const {
+    if (!__any(which != 0)) return;
+    const uint64_t below = (uint64_t{1} << (threadIdx.x & 63)) - 1;
+    int mine = 0, all = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t b = __ballot(which >> k & 1);
+      mine += __popcll(b & below);
+      all += __popcll(b);
+    }
+    int first = 0;
+    if ((threadIdx.x & 63) == 0) first = atomicAdd(n, all);
+    mine += __builtin_amdgcn_readfirstlane(first);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (which >> k & 1) {
+        if (mine < most) sh.list[at + mine] = place(l[k], v + k);
+        ++mine;
+      }
+  }
   // All entries with a logit of `from` and more (any order) into the list; false: too many.
   __device__ __forceinline__ bool collect(float from, int* n) {
     __syncthreads();
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
-    auto take = [&](float l, uint32_t v) {
-      if (l >= from && l > -__builtin_inff()) {
-        const int at = atomicAdd(&sh.listed, 1);
-        if (at < Sh::kListed) sh.list[at] = place(l, v);
-      }
-    };
+    auto which = [&](float l, int k) { return l >= from && l > -__builtin_inff() ? 1u << k : 0u; };
     row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
-      if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= from)) return;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) take(l[k], v + k);
+      append(l, v, which(l[0], 0) | which(l[1], 1) | which(l[2], 2) | which(l[3], 3), 0, Sh::kListed, &sh.listed);
     });
-    if (row.vt < row.V) take(row.xt, static_cast<uint32_t>(row.vt));
+    if (row.vt < row.V && which(row.xt, 0)) {
+      const int at = atomicAdd(&sh.listed, 1);
+      if (at < Sh::kListed) sh.list[at] = place(row.xt, static_cast<uint32_t>(row.vt));
+    }
     __syncthreads();
     *n = sh.listed;
     return *n <= Sh::kListed;
@@ -428,18 +468,19 @@ struct Listed {
 
 // The cut of a row whose entries that stay are not few: SUM ? where the weights
 // reach top_p of all up to the cut so far : where the first top_k end.  Bins
-// over the weights, then the places in the one bin in which it ends.  The
-// entries up to that bin come into the list, its own at the list's end;
-// *listed: how many there are, -1 where they do not fit.
+// over the weights; then the places in the one bin in which it ends, in the
+// list (at most kListed of them), and, where SUM, in the same pass the sums of
+// the weights in front of that bin (*sum, each wavefront's part; *tail, the
+// entries behind the quads), to which those of the bin that stay are added in
+// sh.part.  False: everything stays.
 template <bool SUM, bool CUT, int DT, int THREADS>
-__device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float p, int* listed) {
+__device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float p) {
   using Sh = SampleShared<DT, THREADS>;
   Sh& sh = d.sh;
-  constexpr int kBins = Sh::kBins, kOneBin = Sh::kOneBin, kFront = Sh::kListed - kOneBin;
-  *listed = -1;
+  constexpr int kBins = Sh::kBins, kWaves = THREADS / 64;
   __syncthreads();
   clear_bins<THREADS>(sh);
-  if (threadIdx.x == 0) sh.listed = sh.few_n = 0;
+  if (threadIdx.x == 0) sh.listed = 0;
   __syncthreads();
   d.template each<2, CUT>([&](float l, uint32_t, bool in) {
     const uint64_t w = d.look(l);
@@ -454,7 +495,7 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     for (int i = 0; i < kBins / THREADS; ++i) sum += sh.bins[i * THREADS + threadIdx.x];
     group_scan<THREADS>(sum, sh.wave, &all);
     if constexpr (SUM) want = d.share(p, all);
-    if (want >= all) return;   // everything of any weight stays
+    if (want >= all) return false;   // everything of any weight stays
   }
   find_bin<THREADS>(sh, 0, want);
   const int bin = sh.bin;
@@ -464,54 +505,121 @@ __device__ __forceinline__ void cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     return smallest(static_cast<float>(d.weight.top - (((b + 1) << Sh::kBinShift) - 0.5) / d.weight.a), [&](float l) { return l >= d.weight.top || d.weight.bin_formed(l) <= b; });
   };
   const float from = first_of(bin), front_from = bin > 0 ? first_of(bin - 1) : __builtin_inff();
-  uint64_t lo = ~uint64_t{0}, hi = 0;
-  auto take = [&](float l, uint32_t v) {
-    if (!(l >= from) || (CUT && !d.in(l, v))) return;
-    const uint64_t q = d.place(l, v);
-    if (l >= front_from) {
-      const int at = atomicAdd(&sh.listed, 1);
-      if (at < kFront) sh.list[at] = q;
-    } else {
-      lo = min(lo, q);
-      hi = max(hi, q);
-      const int at = atomicAdd(&sh.few_n, 1);
-      if (at < kOneBin) sh.list[kFront + at] = q;
-    }
+  uint64_t lo = ~uint64_t{0}, hi = 0, sum = 0, tail = 0;
+  auto in_bin = [&](float l, uint32_t v) { return l >= from && !(l >= front_from) && (!CUT || d.in(l, v)); };
+  auto range = [&](uint64_t q) {
+    lo = min(lo, q);
+    hi = max(hi, q);
   };
-  d.row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
-    if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= from)) return;
+  d.row.template each_quad<4>([&](const float (&l)[4], uint32_t v) {
+    const float x = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+    if (!__any(x >= from)) return;
+    uint32_t which = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) take(l[i], v + i);
-  });
-  if (d.row.vt < d.row.V) take(d.row.xt, static_cast<uint32_t>(d.row.vt));
-  group_range<THREADS>(sh, &lo, &hi);   // (its barrier: the list is complete)
-  const int front = sh.listed, one = sh.few_n;
-  auto amount = [&](uint64_t at) { return SUM ? d.weight(d.place.logit(at)) : uint64_t{1}; };
-  if (one <= kOneBin) {
-    d.set_cut(find_place<THREADS>(sh, lo, hi, before, want, [&](auto f) {
-      for (int i = threadIdx.x; i < one; i += THREADS) f(sh.list[kFront + i]);
-    }, amount));
-    if (front > kFront) return;
-    // the bin's entries behind the others
-    constexpr int kEach = (kOneBin + THREADS - 1) / THREADS;
-    uint64_t q[kEach];
+    for (int i = 0; i < 4; ++i) which |= in_bin(l[i], v + i) ? 1u << i : 0;
+    if (which != 0)
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) q[i] = sh.list[kFront + i * THREADS + threadIdx.x];
-    __syncthreads();
+      for (int i = 0; i < 4; ++i)
+        if (which >> i & 1) range(d.place(l[i], v + i));
+    d.append(l, v, which, 0, Sh::kListed, &sh.listed);
+    if constexpr (SUM) {   // (a cut before this one lies behind every entry in front of the bin)
+      if (!__any(x >= front_from)) return;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int at = i * THREADS + threadIdx.x;
-      if (at < one) sh.list[front + at] = q[i];
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t w = d.weight.units(d.look(l[i]));
+        sum += l[i] >= front_from ? w : 0;
+      }
     }
-    __syncthreads();
-    *listed = front + one;
-    return;
+  });
+  if (d.row.vt < d.row.V) {
+    const float l = d.row.xt;
+    const uint32_t v = static_cast<uint32_t>(d.row.vt);
+    if (in_bin(l, v)) {
+      range(d.place(l, v));
+      const int at = atomicAdd(&sh.listed, 1);
+      if (at < Sh::kListed) sh.list[at] = d.place(l, v);
+    }
+    if (SUM && l >= front_from) tail = d.weight(l);
   }
-  d.set_cut(find_place<THREADS>(sh, lo, hi, before, want, [&](auto f) {   // (many equal logits)
+  group_range<THREADS>(sh, &lo, &hi);   // (its barrier: the list is complete)
+  const int listed = sh.listed;
+  auto amount = [&](uint64_t at) { return SUM ? d.weight(d.place.logit(at)) : uint64_t{1}; };
+  const bool fits = listed <= Sh::kListed;
+  const Listed<THREADS, Sh> entries{sh, listed, ~uint64_t{0}};
+  auto of_row = [&](auto f) {   // (many equal logits)
     d.row.template each<2>([&](float l, uint32_t v) {
-      if (l >= from && !(l >= front_from) && (!CUT || d.in(l, v))) f(d.place(l, v));
+      if (in_bin(l, v)) f(d.place(l, v));
     });
-  }, amount));
+  };
+  const uint64_t cut = fits ? find_place<THREADS>(sh, lo, hi, before, want, entries, amount) : find_place<THREADS>(sh, lo, hi, before, want, of_row, amount);
+  if constexpr (SUM) {
+    sum = wave_scan(sum);
+    tail = wave_scan(tail);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63) sh.part[threadIdx.x >> 6] = sum;
+    if (threadIdx.x == 63) sh.part[kWaves] = tail;
+    __syncthreads();
+    auto add = [&](uint64_t q) {
+      const uint32_t v = static_cast<uint32_t>(q);
+      if (q <= cut) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.part[v < d.row.quads * 4 ? v / (static_cast<uint32_t>(d.row.part) * 256) : kWaves]), amount(q));
+    };
+    if (fits) entries(add);
+    else of_row(add);
+    __syncthreads();
+  }
+  d.set_cut(cut);
+  return true;
+}
+
+// The n-th largest of the lanes' values (1 <= n <= 64).
+__device__ __forceinline__ float wave_nth(float x, int n) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int size = 2; size <= 64; size *= 2) {
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2) {
+      const float other = __shfl_xor(x, step, 64);
+      const bool up = (lane & size) == 0, lower = (lane & step) == 0;
+      x = up == lower ? fmaxf(x, other) : fminf(x, other);   // descending
+    }
+  }
+  return __shfl(x, n - 1, 64);
+}
+
+// Orders a wavefront's LDS accesses before this point and behind it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Sorts a wavefront's 256 places, lane i's four at 4 i .. 4 i + 3, ascending.
+__device__ __forceinline__ void sort_places(uint64_t (&x)[4]) {
+  const int lane = threadIdx.x & 63;
+  auto order = [](uint64_t& a, uint64_t& b, bool up) {
+    const bool swap = (a > b) == up;
+    const uint64_t t = a;
+    a = swap ? b : a;
+    b = swap ? t : b;
+  };
+#pragma unroll
+  for (int size = 2; size <= 256; size *= 2) {
+#pragma unroll
+    for (int step = size / 2; step > 0; step /= 2) {
+      if (step >= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t other = __shfl_xor(static_cast<unsigned long long>(x[i]), step / 4, 64);
+          const bool up = (lane * 4 & size) == 0, lower = (lane & (step / 4)) == 0;
+          x[i] = (other < x[i]) == (up == lower) ? other : x[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((i & step) == 0) order(x[i], x[i + step], ((lane * 4 + i) & size) == 0);
+      }
+    }
+  }
 }
 
 template <int DT, int THREADS>
@@ -534,7 +642,7 @@ sample_kernel(SampleArgs a) {
   float own = -__builtin_inff();
   uint32_t own_v = 0;
   bool nan = row.xt != row.xt;
-  row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
+  row.template stream<8>([&](const float (&l)[4], uint32_t v) {
     nan |= __builtin_isunordered(l[0], l[1]) | __builtin_isunordered(l[2], l[3]);
     const float x = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
     own_v = x > own ? v : own_v;
@@ -580,20 +688,21 @@ sample_kernel(SampleArgs a) {
   const auto weight_of = [&](uint64_t q) { return d.weight(d.place.logit(q)); };
 
   // Few entries stay (a small top_k): then a list holds them, and the rest is done on
-  // the list.  The threads' largest logits bound the top_k-th from below.
+  // the list.  Every wavefront has `each` lanes whose largest logits reach the
+  // smallest of their `each`-th largest ones, so top_k entries reach it.
   int listed = -1;
-  if (by_k && top_k <= THREADS / 2 && V >= 4 * THREADS) {
-    // (a thread without a finite entry counts as the last place)
-    const uint64_t mine = own > -__builtin_inff() ? d.place(own, threadIdx.x) : ~uint64_t{0};
-    uint64_t lo = mine, hi = mine;
-    group_range<THREADS>(sh, &lo, &hi);
-    const uint64_t kth = find_place<THREADS>(sh, lo, hi, 0, top_k, [&](auto f) { f(mine); }, one);
-    const float from = kth == ~uint64_t{0} ? -__builtin_inff() : d.place.logit(kth);
+  constexpr int kWaves = THREADS / 64;
+  if (by_k && top_k <= 32 * kWaves && V >= 4 * THREADS) {
+    const int each = (top_k + kWaves - 1) / kWaves;
+    const float nth = wave_nth(own, each);
+    __syncthreads();
+    if (lane == 0) sh.red[wave] = nth;
+    __syncthreads();
+    float from = sh.red[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) from = fminf(from, sh.red[w]);
     int n;
-    if (d.collect(from, &n)) {
-      listed = n;
-      if (n > top_k) d.set_cut(find_place<THREADS>(sh, 0, d.place(from, ~0u), 0, top_k, Listed<THREADS, Sh>{sh, n, ~uint64_t{0}}, one));
-    }
+    if (d.collect(from, &n)) listed = n;
   }
   float least = -__builtin_inff();   // where min_p ends
   if (by_m) {
@@ -605,26 +714,7 @@ sample_kernel(SampleArgs a) {
     int n;
     if (d.collect(least, &n)) listed = n;
   }
-  bool p_left = by_p;
-  if (listed < 0) {
-    __syncthreads();
-    if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
-    if (by_k) cut_row<false, false>(d, top_k, 0.f, &listed);
-    if (by_p && listed < 0) {
-      if (d.cut == ~uint64_t{0}) cut_row<true, false>(d, 0, p, &listed);
-      else cut_row<true, true>(d, 0, p, &listed);
-      p_left = false;
-    }
-  }
-  __syncthreads();
-  if (listed >= 0 && p_left) {
-    uint64_t sum = 0, all;
-    Listed<THREADS, Sh>{sh, listed, d.cut}([&](uint64_t q) { sum += weight_of(q); });
-    group_scan<THREADS>(sum, sh.wave, &all);
-    d.set_cut(find_place<THREADS>(sh, 0, d.lcut > -__builtin_inff() ? d.place(d.lcut, ~0u) : ~uint64_t{0}, 0, d.share(p, all),
-                                  Listed<THREADS, Sh>{sh, listed, d.cut}, weight_of));
-  }
-  if (by_m && least > d.lcut) d.set_cut(d.place(least, ~0u));
+  __syncthreads();                   // the table, the list
   auto wanted = [&](uint64_t total) {   // the token is the first whose running sum is above this
     return min(static_cast<uint64_t>(fmin(fmax(static_cast<double>(u), 0.0), 1.0) * static_cast<double>(total)), total - 1);
   };
@@ -632,7 +722,75 @@ sample_kernel(SampleArgs a) {
     a.tokens[row_at] = static_cast<int32_t>(v);
     if (a.logprob != nullptr) a.logprob[row_at] = d.weight.log_share(l, total);
   };
-  if (listed >= 0) {
+  if (listed >= 0 && listed <= 256) {   // one wavefront does it without a barrier
+    if (wave != 0) return;
+    uint64_t x[4], w[4], before[4], kept[4], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = lane * 4 + i < listed ? sh.list[lane * 4 + i] : ~uint64_t{0};
+    sort_places(x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rank = lane * 4 + i;
+      w[i] = rank < listed && !(by_k && rank >= top_k) ? weight_of(x[i]) : 0;
+      before[i] = sum;
+      sum += w[i];
+    }
+    const uint64_t scan = wave_scan(sum);
+    const uint64_t front = scan - sum;
+    all = at_lane(scan, 63);
+    const uint64_t share = by_p ? d.share(p, all) : all;
+    sum = 0;
+    int stay = 0;   // they are the first of the order
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool stays = w[i] > 0 && before[i] + front < share && d.place.logit(x[i]) >= least;
+      kept[i] = stays ? w[i] : 0;
+      sum += kept[i];
+      stay += __popcll(__ballot(stays));
+    }
+    const uint64_t total = at_lane(wave_scan(sum), 63), want = wanted(total);
+    if (stay <= 64) {   // one a lane: what lies in front of it by index, from the other lanes
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lane * 4 + i < stay) {
+          sh.few[lane * 4 + i] = x[i];
+          sh.list[lane * 4 + i] = kept[i];
+        }
+      wave_sync();
+      const uint64_t mine = lane < stay ? sh.few[lane] : 0, own_w = lane < stay ? sh.list[lane] : 0;
+      uint64_t at = 0;
+      for (int i = 0; i < stay; ++i) {
+        const uint64_t q = at_lane(mine, i), y = at_lane(own_w, i);
+        at += static_cast<uint32_t>(q) < static_cast<uint32_t>(mine) ? y : 0;
+      }
+      if (own_w > 0 && at <= want && want < at + own_w) write(static_cast<uint32_t>(mine), d.place.logit(mine), total);
+      return;
+    }
+    // bit by bit: the first index up to which the weights pass `want`
+    uint32_t found = 0;
+    for (int b = 31 - __builtin_clz(static_cast<uint32_t>(V - 1) | 1); b >= 0; --b) {
+      const uint32_t upto = found + (1u << b) - 1;
+      uint64_t s = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += static_cast<uint32_t>(x[i]) <= upto ? kept[i] : 0;
+      if (at_lane(wave_scan(s), 63) <= want) found += 1u << b;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (kept[i] > 0 && static_cast<uint32_t>(x[i]) == found) write(found, d.place.logit(x[i]), total);
+    return;
+  }
+
+  if (listed >= 0) {   // a longer list
+    if (by_k && listed > top_k) d.set_cut(find_place<THREADS>(sh, 0, ~uint64_t{0}, 0, top_k, Listed<THREADS, Sh>{sh, listed, ~uint64_t{0}}, one));
+    if (by_p) {
+      uint64_t sum = 0, all;
+      Listed<THREADS, Sh>{sh, listed, d.cut}([&](uint64_t q) { sum += weight_of(q); });
+      group_scan<THREADS>(sum, sh.wave, &all);
+      d.set_cut(find_place<THREADS>(sh, 0, d.lcut > -__builtin_inff() ? d.place(d.lcut, ~0u) : ~uint64_t{0}, 0, d.share(p, all),
+                                    Listed<THREADS, Sh>{sh, listed, d.cut}, weight_of));
+    }
+    if (least > d.lcut) d.set_cut(d.place(least, ~0u));
     const Listed<THREADS, Sh> entries{sh, listed, d.cut};
     uint64_t sum = 0, total;
     entries([&](uint64_t q) { sum += weight_of(q); });
@@ -645,47 +803,67 @@ sample_kernel(SampleArgs a) {
     return;
   }
 
-  // a wavefront's part of the row each, and the entries behind the quads
-  auto kept = [&](float l, uint32_t v) -> uint64_t { return d.in(l, v) ? d.weight.units(d.look(l)) : 0; };
-  uint64_t sum = 0, tail = 0;
-  auto add = [&](float l, uint32_t v, bool in) {
-    const uint64_t w = d.weight.units(d.look(l));
-    (v < row.quads * 4 ? sum : tail) += in ? w : 0;
-  };
-  if (d.cut == ~uint64_t{0}) d.template each<2, false>(add);
-  else d.template each<2, true>(add);
-  sum = wave_scan(sum);
-  tail = wave_scan(tail);
-  __syncthreads();
-  if (lane == 63) sh.part[wave] = sum;
-  if (threadIdx.x == 63) sh.part[THREADS / 64] = tail;
-  __syncthreads();
+  // Sums of a wavefront's part of the row each, and of the entries behind the quads.
+  if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
+  bool summed = false;
+  if (by_k) cut_row<false, false>(d, top_k, 0.f);
+  if (by_p) summed = d.cut == ~uint64_t{0} ? cut_row<true, false>(d, 0, p) : cut_row<true, true>(d, 0, p);
+  if (least > d.lcut) {
+    d.set_cut(d.place(least, ~0u));
+    summed = false;
+  }
+  if (!summed) {
+    uint64_t sum = 0, tail = 0;
+    auto add = [&](float l, uint32_t v, bool in) {
+      const uint64_t w = d.weight.units(d.look(l));
+      (v < row.quads * 4 ? sum : tail) += in ? w : 0;
+    };
+    if (d.cut == ~uint64_t{0}) d.template each<2, false>(add);
+    else d.template each<2, true>(add);
+    sum = wave_scan(sum);
+    tail = wave_scan(tail);
+    __syncthreads();
+    if (lane == 63) sh.part[wave] = sum;
+    if (threadIdx.x == 63) sh.part[kWaves] = tail;
+    __syncthreads();
+  }
   uint64_t total = 0;
 #pragma unroll
-  for (int w = 0; w <= THREADS / 64; ++w) total += sh.part[w];
+  for (int w = 0; w <= kWaves; ++w) total += sh.part[w];
   const uint64_t want = wanted(total);
   uint64_t at = 0;
   int part = 0;
   while (at + sh.part[part] <= want) at += sh.part[part++];
-  // that part again, by the whole workgroup
-  const bool behind = part == THREADS / 64;
+  // that part again, by the whole workgroup, kRun entries a thread at a time
+  constexpr int kRun = 8;
+  const bool behind = part == kWaves;
   const int64_t v0 = behind ? row.quads * 4 : min(part * row.part * 256, row.quads * 4);
   const int64_t v1 = behind ? V : min(v0 + row.part * 256, row.quads * 4);
-  const int64_t run = (v1 - v0 + THREADS - 1) / THREADS;
-  const int64_t b = min(v0 + threadIdx.x * run, v1), e = min(b + run, v1);
-  uint64_t mine = 0, all;
-#pragma unroll 4
-  for (int64_t v = b; v < e; ++v) mine += kept(at_index(v), static_cast<uint32_t>(v));
-  at += group_scan<THREADS>(mine, sh.wave, &all);
-  if (at <= want && want < at + mine) {   // one thread's
-    for (int64_t v = b; v < e; ++v) {
-      const float l = at_index(v);
-      at += kept(l, static_cast<uint32_t>(v));
-      if (at > want) {
-        write(static_cast<uint32_t>(v), l, total);
-        break;
+  for (int64_t from = v0; from < v1; from += THREADS * kRun) {
+    const int64_t b = from + threadIdx.x * kRun;
+    float l[kRun];
+    uint64_t w[kRun], mine = 0, all;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) l[i] = b + i < v1 ? at_index(b + i) : -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      w[i] = d.in(l[i], static_cast<uint32_t>(b + i)) ? d.weight.units(d.look(l[i])) : 0;
+      mine += w[i];
+    }
+    uint64_t sum = at + group_scan<THREADS>(mine, sh.wave, &all);
+    if (sum <= want && want < sum + mine) {   // one thread's
+      bool done = false;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        sum += w[i];
+        if (!done && sum > want) {
+          write(static_cast<uint32_t>(b + i), l[i], total);
+          done = true;
+        }
       }
     }
+    at += all;
+    if (at > want) break;
   }
 }
 
