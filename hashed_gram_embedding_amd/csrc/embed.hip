@@ -10,11 +10,11 @@
 
 #include "device_util.h"
 #include "engram_internal.h"
+#include "lanes_device.h"
 
 namespace engram {
 namespace {
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
@@ -213,13 +213,6 @@ digit_scan_kernel(uint32_t* __restrict__ counts, int64_t m, Fill fill) {
     counts[i] = at;
     at += x;
   }
-}
-
-// Orders a wavefront's LDS accesses before this point and behind it.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Each wavefront takes a contiguous quarter of the block's ids, 64 at a time;

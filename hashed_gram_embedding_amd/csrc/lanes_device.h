@@ -127,6 +127,13 @@ __device__ __forceinline__ float group_max(float x, bool nan, float* red) {
   return m;
 }
 
+// Orders a wavefront's LDS accesses before this point and behind it.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // bf16 pairs stay packed from pass to pass: without this the compiler keeps
 // every unpacked value, then every exponential, for the next pass, twice the
 // registers there are.  (float32 rows keep their exponentials in place.)

@@ -181,6 +181,47 @@ struct Row {
       for (int i = 0; i < U; ++i) x[i] = next[i];
     }
   }
+  // The runs that `mark` marks are read a second time for f, which the whole wavefront calls (with -inf in lanes
+  // that have none left): few runs, so that the pass itself is a short loop.
+  template <int U, typename M, typename F>
+  __device__ __forceinline__ void marked(M mark, F f) const {
+    const int64_t q0 = static_cast<int64_t>(threadIdx.x >> 6) * part * 64 + (threadIdx.x & 63);
+    auto load = [&](Quad<DT> (&x)[U], int64_t n) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) x[i] = load_quad<DT>(in, n + i < part ? q0 + (n + i) * 64 : quads, quads);
+    };
+    auto values = [](const Quad<DT>& x, float (&l)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) l[k] = x.at(k);
+    };
+    Quad<DT> x[U], next[U];
+    load(x, 0);
+    for (int64_t n0 = 0; n0 < part; n0 += 32) {
+      uint32_t marks = 0;
+#pragma unroll 1
+      for (int n = 0; n < 32 && n0 + n < part; n += U) {
+        load(next, n0 + n + U);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          float l[4];
+          values(x[i], l);
+          marks |= mark(l) ? 1u << (n + i) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) x[i] = next[i];
+      }
+      if (part - n0 < 32) marks &= (1u << (part - n0)) - 1;   // (behind the part -inf was read, which may be marked)
+#pragma unroll 1
+      while (__any(marks != 0)) {
+        const int64_t q = marks != 0 ? q0 + (n0 + __builtin_ctz(marks)) * 64 : quads;
+        const Quad<DT> y = load_quad<DT>(in, q, quads);
+        float l[4];
+        values(y, l);
+        f(l, static_cast<uint32_t>(q) * 4);
+        marks &= marks - 1;
+      }
+    }
+  }
   // f(l[4], index of the first) in the order of the row (the workgroup's runs side by side): for the
   // pass from memory, which streams a row faster so than in a part for each wavefront.
   template <int U, typename F>
@@ -227,7 +268,7 @@ struct SampleShared {
   uint64_t list[kListed];
   uint64_t values[kLooks ? 2 * kValues : 1];
   double table[kTable];
-  uint64_t few[64];
+  uint64_t few[512];
   uint64_t wave[THREADS / 64], wave2[THREADS / 64];
   uint64_t part[THREADS / 64 + 1];
   uint64_t before;
@@ -440,7 +481,8 @@ struct Draw {
     if (threadIdx.x == 0) sh.listed = 0;
     __syncthreads();
     auto which = [&](float l, int k) { return l >= from && l > -__builtin_inff() ? 1u << k : 0u; };
-    row.template each_quad<8>([&](const float (&l)[4], uint32_t v) {
+    row.template marked<8>([&](const float (&l)[4]) { return fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= from; },
+                           [&](const float (&l)[4], uint32_t v) {
       append(l, v, which(l[0], 0) | which(l[1], 1) | which(l[2], 2) | which(l[3], 3), 0, Sh::kListed, &sh.listed);
     });
     if (row.vt < row.V && which(row.xt, 0)) {
@@ -482,11 +524,35 @@ __device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
   clear_bins<THREADS>(sh);
   if (threadIdx.x == 0) sh.listed = 0;
   __syncthreads();
-  d.template each<2, CUT>([&](float l, uint32_t, bool in) {
-    const uint64_t w = d.look(l);
-    if (in && d.weight.bin(w) < Sh::kLastBin)   // (entries of weight 0 count for nothing)
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) : 1);
-  });
+  if constexpr (Sh::kLooks && !CUT) {
+    // entries counted by value (half the LDS work of adding up their weights), the values binned afterwards
+    uint32_t* counts = reinterpret_cast<uint32_t*>(sh.list);
+    static_assert(sizeof(sh.list) >= 2 * kValues * 4, "the counts fit");
+    for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) counts[i] = 0;
+    __syncthreads();
+    const uint32_t base = d.weight.base;
+    d.template each<4, CUT>([&](float l, uint32_t, bool) {
+      const uint32_t bits = __float_as_uint(l) >> 16, at = (bits & 0x7fff) - base;
+      if (at < kValues) {
+        atomicAdd(&counts[at + (bits >> 15) * kValues], 1u);
+      } else if (l > -__builtin_inff()) {
+        const uint64_t w = d.weight.formed(l);
+        if (d.weight.bin(w) < Sh::kLastBin) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) : 1);
+      }
+    });
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) {
+      const uint64_t n = counts[i], w = sh.values[i];
+      if (n > 0 && d.weight.bin(w) < Sh::kLastBin)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) * n : n);
+    }
+  } else {
+    d.template each<2, CUT>([&](float l, uint32_t, bool in) {
+      const uint64_t w = d.look(l);
+      if (in && d.weight.bin(w) < Sh::kLastBin)   // (entries of weight 0 count for nothing)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) : 1);
+    });
+  }
   __syncthreads();
   uint64_t want = k;
   {
@@ -511,25 +577,30 @@ __device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     lo = min(lo, q);
     hi = max(hi, q);
   };
-  d.row.template each_quad<4>([&](const float (&l)[4], uint32_t v) {
-    const float x = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
-    if (!__any(x >= from)) return;
-    uint32_t which = 0;
+  d.row.template marked<4>([&](const float (&l)[4]) {
+    float x = -__builtin_inff();   // the largest behind those in front of the bin
+    if (!SUM || !__any(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= front_from)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) which |= in_bin(l[i], v + i) ? 1u << i : 0;
-    if (which != 0)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (which >> i & 1) range(d.place(l[i], v + i));
-    d.append(l, v, which, 0, Sh::kListed, &sh.listed);
-    if constexpr (SUM) {   // (a cut before this one lies behind every entry in front of the bin)
-      if (!__any(x >= front_from)) return;
+      for (int i = 0; i < 4; ++i) x = fmaxf(x, l[i] >= front_from ? x : l[i]);
+    } else {   // (a cut before this one lies behind every entry in front of the bin)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t w = d.weight.units(d.look(l[i]));
-        sum += l[i] >= front_from ? w : 0;
+        const bool front = l[i] >= front_from;
+        sum += front ? w : 0;
+        x = fmaxf(x, front ? x : l[i]);
       }
     }
+    return x >= from;
+  }, [&](const float (&l)[4], uint32_t v) {
+    uint32_t which = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (in_bin(l[i], v + i)) {
+        which |= 1u << i;
+        range(d.place(l[i], v + i));
+      }
+    d.append(l, v, which, 0, Sh::kListed, &sh.listed);
   });
   if (d.row.vt < d.row.V) {
     const float l = d.row.xt;
@@ -586,40 +657,28 @@ __device__ __forceinline__ float wave_nth(float x, int n) {
   return __shfl(x, n - 1, 64);
 }
 
-// Orders a wavefront's LDS accesses before this point and behind it.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
+constexpr int kShort = 512;   // places of a list that one wavefront finishes
 
-// Sorts a wavefront's 256 places, lane i's four at 4 i .. 4 i + 3, ascending.
-__device__ __forceinline__ void sort_places(uint64_t (&x)[4]) {
+// The list's n <= kShort places in ascending order, into sh.few: a wavefront
+// counts, for every kWaves-th place, those before it.  (What a workgroup runs
+// once is fetched from the L2 as it goes, at some 5 cycles a byte: a sorting
+// network over 256 places took 8000 cycles, this loop 2500.)
+template <int THREADS, typename Sh>
+__device__ __forceinline__ void order_list(Sh& sh, int n) {
   const int lane = threadIdx.x & 63;
-  auto order = [](uint64_t& a, uint64_t& b, bool up) {
-    const bool swap = (a > b) == up;
-    const uint64_t t = a;
-    a = swap ? b : a;
-    b = swap ? t : b;
-  };
+  uint64_t x[kShort / 64];
 #pragma unroll
-  for (int size = 2; size <= 256; size *= 2) {
+  for (int i = 0; i < kShort / 64; ++i) x[i] = i * 64 + lane < n ? sh.list[i * 64 + lane] : ~uint64_t{0};
+#pragma unroll 1
+  for (int e = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); e < n; e += THREADS / 64) {
+    const uint64_t p = sh.list[e];
+    int before = 0;
 #pragma unroll
-    for (int step = size / 2; step > 0; step /= 2) {
-      if (step >= 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t other = __shfl_xor(static_cast<unsigned long long>(x[i]), step / 4, 64);
-          const bool up = (lane * 4 & size) == 0, lower = (lane & (step / 4)) == 0;
-          x[i] = (other < x[i]) == (up == lower) ? other : x[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((i & step) == 0) order(x[i], x[i + step], ((lane * 4 + i) & size) == 0);
-      }
-    }
+    for (int i = 0; i < kShort / 64; ++i)
+      if (i * 64 < n) before += __popcll(__ballot(x[i] < p));
+    if (lane == 0) sh.few[before] = p;
   }
+  __syncthreads();
 }
 
 template <int DT, int THREADS>
@@ -718,70 +777,67 @@ sample_kernel(SampleArgs a) {
   auto wanted = [&](uint64_t total) {   // the token is the first whose running sum is above this
     return min(static_cast<uint64_t>(fmin(fmax(static_cast<double>(u), 0.0), 1.0) * static_cast<double>(total)), total - 1);
   };
+  // the thread that finds the token keeps it for the end
+  bool found_it = false;
+  uint32_t token = 0;
+  float logit = 0.f;
+  uint64_t weights = 1;
   auto write = [&](uint32_t v, float l, uint64_t total) {
-    a.tokens[row_at] = static_cast<int32_t>(v);
-    if (a.logprob != nullptr) a.logprob[row_at] = d.weight.log_share(l, total);
+    found_it = true;
+    token = v;
+    logit = l;
+    weights = total;
   };
-  if (listed >= 0 && listed <= 256) {   // one wavefront does it without a barrier
-    if (wave != 0) return;
-    uint64_t x[4], w[4], before[4], kept[4], sum = 0, all;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lane * 4 + i < listed ? sh.list[lane * 4 + i] : ~uint64_t{0};
-    sort_places(x);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int rank = lane * 4 + i;
-      w[i] = rank < listed && !(by_k && rank >= top_k) ? weight_of(x[i]) : 0;
-      before[i] = sum;
-      sum += w[i];
-    }
-    const uint64_t scan = wave_scan(sum);
-    const uint64_t front = scan - sum;
-    all = at_lane(scan, 63);
-    const uint64_t share = by_p ? d.share(p, all) : all;
-    sum = 0;
-    int stay = 0;   // they are the first of the order
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool stays = w[i] > 0 && before[i] + front < share && d.place.logit(x[i]) >= least;
-      kept[i] = stays ? w[i] : 0;
-      sum += kept[i];
-      stay += __popcll(__ballot(stays));
-    }
-    const uint64_t total = at_lane(wave_scan(sum), 63), want = wanted(total);
-    if (stay <= 64) {   // one a lane: what lies in front of it by index, from the other lanes
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane * 4 + i < stay) {
-          sh.few[lane * 4 + i] = x[i];
-          sh.list[lane * 4 + i] = kept[i];
-        }
-      wave_sync();
-      const uint64_t mine = lane < stay ? sh.few[lane] : 0, own_w = lane < stay ? sh.list[lane] : 0;
-      uint64_t at = 0;
-      for (int i = 0; i < stay; ++i) {
-        const uint64_t q = at_lane(mine, i), y = at_lane(own_w, i);
-        at += static_cast<uint32_t>(q) < static_cast<uint32_t>(mine) ? y : 0;
+  if (listed >= 0 && listed <= kShort) {   // one wavefront does it without a barrier, lane i the order's i-th, i + 64-th, ..
+    order_list<THREADS>(sh, listed);
+    if (wave == 0) {
+      const int rounds = (listed + 63) / 64;
+      auto round_place = [&](int i) { return i * 64 + lane < listed ? sh.few[i * 64 + lane] : ~uint64_t{0}; };
+      uint64_t all = 0;
+#pragma unroll 1
+      for (int i = 0; i < rounds; ++i) {
+        const int rank = i * 64 + lane;
+        const uint64_t w = rank < listed && !(by_k && rank >= top_k) ? weight_of(sh.few[rank]) : 0;
+        sh.list[rank] = w;
+        all += at_lane(wave_scan(w), 63);
       }
-      if (own_w > 0 && at <= want && want < at + own_w) write(static_cast<uint32_t>(mine), d.place.logit(mine), total);
-      return;
+      wave_sync();
+      const uint64_t share = by_p ? d.share(p, all) : all;
+      uint64_t sum = 0, total = 0;
+      int stay = 0;   // they are the first of the order
+#pragma unroll 1
+      for (int i = 0; i < rounds; ++i) {
+        const uint64_t w = sh.list[i * 64 + lane], upto = wave_scan(w);
+        const bool stays = w > 0 && sum + upto - w < share && d.place.logit(round_place(i)) >= least;
+        sum += at_lane(upto, 63);
+        total += at_lane(wave_scan(stays ? w : uint64_t{0}), 63);
+        stay += __popcll(__ballot(stays));
+      }
+      const uint64_t want = wanted(total);
+      if (stay <= 64) {   // what lies in front of each by index, from the other lanes
+        const uint64_t mine = round_place(0), own_w = lane < stay ? sh.list[lane] : 0;
+        uint64_t before = 0;
+#pragma unroll 1
+        for (int j = 0; j < stay; ++j) {
+          const uint64_t q = at_lane(mine, j), y = at_lane(own_w, j);
+          before += static_cast<uint32_t>(q) < static_cast<uint32_t>(mine) ? y : 0;
+        }
+        if (own_w > 0 && before <= want && want < before + own_w) write(static_cast<uint32_t>(mine), d.place.logit(mine), total);
+      } else {            // bit by bit: the first index up to which the weights pass `want`
+        uint32_t found = 0;
+#pragma unroll 1
+        for (int b = 31 - __builtin_clz(static_cast<uint32_t>(V - 1) | 1); b >= 0; --b) {
+          const uint32_t upto = found + (1u << b) - 1;
+          uint64_t part = 0;
+#pragma unroll 2
+          for (int i = lane; i < stay; i += 64) part += static_cast<uint32_t>(sh.few[i]) <= upto ? sh.list[i] : 0;
+          if (at_lane(wave_scan(part), 63) <= want) found += 1u << b;
+        }
+        for (int i = lane; i < stay; i += 64)
+          if (static_cast<uint32_t>(sh.few[i]) == found) write(found, d.place.logit(sh.few[i]), total);
+      }
     }
-    // bit by bit: the first index up to which the weights pass `want`
-    uint32_t found = 0;
-    for (int b = 31 - __builtin_clz(static_cast<uint32_t>(V - 1) | 1); b >= 0; --b) {
-      const uint32_t upto = found + (1u << b) - 1;
-      uint64_t s = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s += static_cast<uint32_t>(x[i]) <= upto ? kept[i] : 0;
-      if (at_lane(wave_scan(s), 63) <= want) found += 1u << b;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (kept[i] > 0 && static_cast<uint32_t>(x[i]) == found) write(found, d.place.logit(x[i]), total);
-    return;
-  }
-
-  if (listed >= 0) {   // a longer list
+  } else if (listed >= 0) {   // a longer list
     if (by_k && listed > top_k) d.set_cut(find_place<THREADS>(sh, 0, ~uint64_t{0}, 0, top_k, Listed<THREADS, Sh>{sh, listed, ~uint64_t{0}}, one));
     if (by_p) {
       uint64_t sum = 0, all;
@@ -800,70 +856,76 @@ sample_kernel(SampleArgs a) {
       entries([&](uint64_t q) { f(q << 32 | q >> 32); });
     }, [&](uint64_t q) { return weight_of(q << 32 | q >> 32); });
     if (threadIdx.x == 0) write(static_cast<uint32_t>(found >> 32), d.place.logit(found << 32), total);
-    return;
-  }
-
-  // Sums of a wavefront's part of the row each, and of the entries behind the quads.
-  if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
-  bool summed = false;
-  if (by_k) cut_row<false, false>(d, top_k, 0.f);
-  if (by_p) summed = d.cut == ~uint64_t{0} ? cut_row<true, false>(d, 0, p) : cut_row<true, true>(d, 0, p);
-  if (least > d.lcut) {
-    d.set_cut(d.place(least, ~0u));
-    summed = false;
-  }
-  if (!summed) {
-    uint64_t sum = 0, tail = 0;
-    auto add = [&](float l, uint32_t v, bool in) {
-      const uint64_t w = d.weight.units(d.look(l));
-      (v < row.quads * 4 ? sum : tail) += in ? w : 0;
-    };
-    if (d.cut == ~uint64_t{0}) d.template each<2, false>(add);
-    else d.template each<2, true>(add);
-    sum = wave_scan(sum);
-    tail = wave_scan(tail);
-    __syncthreads();
-    if (lane == 63) sh.part[wave] = sum;
-    if (threadIdx.x == 63) sh.part[kWaves] = tail;
-    __syncthreads();
-  }
-  uint64_t total = 0;
-#pragma unroll
-  for (int w = 0; w <= kWaves; ++w) total += sh.part[w];
-  const uint64_t want = wanted(total);
-  uint64_t at = 0;
-  int part = 0;
-  while (at + sh.part[part] <= want) at += sh.part[part++];
-  // that part again, by the whole workgroup, kRun entries a thread at a time
-  constexpr int kRun = 8;
-  const bool behind = part == kWaves;
-  const int64_t v0 = behind ? row.quads * 4 : min(part * row.part * 256, row.quads * 4);
-  const int64_t v1 = behind ? V : min(v0 + row.part * 256, row.quads * 4);
-  for (int64_t from = v0; from < v1; from += THREADS * kRun) {
-    const int64_t b = from + threadIdx.x * kRun;
-    float l[kRun];
-    uint64_t w[kRun], mine = 0, all;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) l[i] = b + i < v1 ? at_index(b + i) : -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      w[i] = d.in(l[i], static_cast<uint32_t>(b + i)) ? d.weight.units(d.look(l[i])) : 0;
-      mine += w[i];
+  } else {
+    // Sums of a wavefront's part of the row each, and of the entries behind the quads.
+    if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
+    bool summed = false;
+    if (by_k) cut_row<false, false>(d, top_k, 0.f);
+    if (by_p) summed = d.cut == ~uint64_t{0} ? cut_row<true, false>(d, 0, p) : cut_row<true, true>(d, 0, p);
+    if (least > d.lcut) {
+      d.set_cut(d.place(least, ~0u));
+      summed = false;
     }
-    uint64_t sum = at + group_scan<THREADS>(mine, sh.wave, &all);
-    if (sum <= want && want < sum + mine) {   // one thread's
-      bool done = false;
+    if (!summed) {
+      uint64_t sum = 0, tail = 0;
+      auto add = [&](float l, uint32_t v, bool in) {
+        const uint64_t w = d.weight.units(d.look(l));
+        (v < row.quads * 4 ? sum : tail) += in ? w : 0;
+      };
+      constexpr int U = Sh::kLooks ? 4 : 2;
+      if (d.cut == ~uint64_t{0}) d.template each<U, false>(add);
+      else d.template each<U, true>(add);
+      sum = wave_scan(sum);
+      tail = wave_scan(tail);
+      __syncthreads();
+      if (lane == 63) sh.part[wave] = sum;
+      if (threadIdx.x == 63) sh.part[kWaves] = tail;
+      __syncthreads();
+    }
+    uint64_t total = 0;
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        sum += w[i];
-        if (!done && sum > want) {
-          write(static_cast<uint32_t>(b + i), l[i], total);
-          done = true;
+    for (int w = 0; w <= kWaves; ++w) total += sh.part[w];
+    const uint64_t want = wanted(total);
+    uint64_t at = 0;
+    int part = 0;
+    while (at + sh.part[part] <= want) at += sh.part[part++];
+    // that part again, by the whole workgroup, kRun runs a thread at a time
+    constexpr int kRun = 2;
+    if (part == kWaves) {
+      const uint64_t w = row.vt < V && d.in(row.xt, static_cast<uint32_t>(row.vt)) ? d.weight(row.xt) : 0;
+      uint64_t all;
+      const uint64_t before = at + group_scan<THREADS>(w, sh.wave, &all);
+      if (before <= want && want < before + w) write(static_cast<uint32_t>(row.vt), row.xt, total);
+    } else {
+      const int64_t q0 = part * row.part * 64, q1 = min(q0 + row.part * 64, row.quads);
+      for (int64_t from = q0; from < q1; from += THREADS * kRun) {
+        const int64_t q = from + threadIdx.x * kRun;
+        Quad<DT> x[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) x[i] = load_quad<DT>(row.in, q + i, q1);
+        uint64_t w[kRun * 4], mine = 0, all;
+#pragma unroll
+        for (int i = 0; i < kRun * 4; ++i) {
+          const float l = x[i >> 2].at(i & 3);
+          w[i] = d.in(l, static_cast<uint32_t>(q * 4 + i)) ? d.weight.units(d.look(l)) : 0;
+          mine += w[i];
         }
+        uint64_t sum = at + group_scan<THREADS>(mine, sh.wave, &all);
+        if (sum <= want && want < sum + mine) {   // one thread's
+#pragma unroll
+          for (int i = 0; i < kRun * 4; ++i) {
+            sum += w[i];
+            if (!found_it && sum > want) write(static_cast<uint32_t>(q * 4 + i), x[i >> 2].at(i & 3), total);
+          }
+        }
+        at += all;
+        if (at > want) break;
       }
     }
-    at += all;
-    if (at > want) break;
+  }
+  if (found_it) {
+    a.tokens[row_at] = static_cast<int32_t>(token);
+    if (a.logprob != nullptr) a.logprob[row_at] = d.weight.log_share(logit, weights);
   }
 }
 
