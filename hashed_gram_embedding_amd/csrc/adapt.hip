@@ -277,20 +277,46 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
   }
 }
 
-// ---- many tokens, bf16 ----
+// ---- more tokens, bf16 ----
 // A tile of TF outputs x TT tokens a workgroup, WF x WT wavefronts; slices of
-// 64 columns of both go from memory straight into LDS, one in flight while the
-// other is multiplied.  A slice's row is 128 bytes, its 16-byte chunk c at
-// c ^ ((row >> 1) & 7), so that the rows a fragment read touches spread over
-// the banks.
+// 64 columns of both operands go from memory straight into LDS, RING - 1 in
+// flight while one is multiplied.  A slice's row is 128 bytes, its 16-byte
+// chunk c at c ^ ((row >> 1) & 7), so that the rows a fragment read touches
+// spread over the banks.
+//
+// The adapters are more slices of the same loop: behind the columns of W come
+// 16 columns of B of every adapter that occurs among a wavefront's tokens, four
+// to a slice, kPer = 4 / WT for each row of wavefronts, multiplied with the
+// tokens' rows of h from registers.  Read from memory by the wavefronts
+// themselves, one adapter after another, they took 25 of 34 us at 256 tokens of
+// 64 adapters (1024 x 5120); in slices that one row of wavefronts filled after
+// the other, 31 of 41.
 constexpr int kXcds = 8, kBand = 8;
 
-template <int TF, int TT, int WF, int WT, typename OutT>
+// Waits until at most `younger` slices of LOADS instructions are in flight.
+template <int LOADS, int MOST>
+__device__ __forceinline__ void wait_slices(int younger) {
+  static_assert(LOADS * MOST < 64, "the counter's range");
+  if constexpr (MOST > 0) {
+    if (younger >= MOST) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS * MOST) : "memory");
+      return;
+    }
+    wait_slices<LOADS, MOST - 1>(younger);
+  } else {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+}
+
+template <int TF, int TT, int WF, int WT, int RING, typename OutT>
 __global__ void __launch_bounds__(WF * WT * 64)
 adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   constexpr int NT = WF * WT * 64, FB = TF / WF / 32, TB = TT / WT / 32;
   constexpr int kRowsAtOnce = NT / 8, kLoadsW = TF / kRowsAtOnce, kLoadsE = TT / kRowsAtOnce, kBuffer = (TF + TT) * 8;
-  extern __shared__ u32x4_t lds[];   // [2][TF + TT rows][8 chunks]; afterwards each wavefront's outputs
+  extern __shared__ u32x4_t lds[];   // [RING][TF + TT rows][8 chunks]; afterwards each wavefront's outputs
+  constexpr int kPer = 4 / WT, kTokens = TT / WT;
+  static_assert(TB <= 2 && WT * kPer == 4, "a lane of the wavefront for each of its tokens, four adapters a slice");
+  __shared__ int adapters[WT][kTokens], counts[WT];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lr = lane & 31, lh = lane >> 5;
   const int wf = wave % WF, wt = wave / WF;
   // Workgroup i runs on XCD i % 8: each XCD walks tiles of its own, band by
@@ -300,7 +326,7 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   if (tile >= tiles_f * tiles_t) return;
   const int band = tile / (tiles_f * kBand), in_band = tile - band * tiles_f * kBand, bt = min(kBand, tiles_t - band * kBand);
   const int64_t f0 = static_cast<int64_t>(in_band / bt) * TF, t0 = (static_cast<int64_t>(band) * kBand + in_band % bt) * TT;
-  const int K = a.K;
+  const int K = a.K, ksteps = K / 64;
   const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
   // rows past the end read zeros
   const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<ENGRAM_BF16>(a.w, f0 * K)), 0,
@@ -308,7 +334,7 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   const auto re = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<ENGRAM_BF16>(a.e, t0 * K)), 0,
                                                     static_cast<int>(min(int64_t{TT}, a.n_tok - t0)) * K * 2, 0x00020000);
   auto issue = [&](int kt) {
-    u32x4_t* dst = lds + (kt & 1) * kBuffer + wave * 64;
+    u32x4_t* dst = lds + (kt % RING) * kBuffer + wave * 64;
 #pragma unroll
     for (int i = 0; i < kLoadsW; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(dst + i * NT), 16,
@@ -318,6 +344,63 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (__attribute__((address_space(3))) void*)(dst + TF * 8 + i * NT), 16,
                                                ((r0 + i * kRowsAtOnce) * K + ch * 8) * 2, kt * 128, 0, 0);
   };
+  const int64_t tw0 = t0 + wt * (TT / WT);
+  int id[TB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) id[b] = adapter_of(a, tw0 + b * 32 + lr);
+#pragma unroll
+  for (int p = 0; p < RING - 1; ++p)
+    if (p < ksteps) issue(p);
+  // the adapters among each row of wavefronts' tokens
+  const int token = TB == 2 && lh == 1 ? id[TB - 1] : TB == 1 && lh == 1 ? -1 : id[0];   // a lane's own of them
+  int own = 0;
+  each_adapter(token, [&](int one, int j) {
+    if (wf == 0 && lane == 0) adapters[wt][j] = one;
+    own = j + 1;
+  });
+  if (wf == 0 && lane == 0) counts[wt] = own;
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  int most = 0;
+#pragma unroll
+  for (int g = 0; g < WT; ++g) most = max(most, counts[g]);
+  // The slices: 16 columns of B after 16 columns, each of kPer adapters of every row of wavefronts after kPer.
+  const int turns = (most + kPer - 1) / kPer, slices = ksteps + turns * ((a.rank + 15) / 16);
+  // This lane loads a half of one entry a slice (chunk ch), the `load_j`-th adapter of its row, columns load_r .. + 7.
+  // Where there is none something valid is loaded and not used.  An entry's place is found a slice ahead.
+  const int row_of = (ch >> 1) / kPer, in_row = counts[row_of];
+  int load_j = (ch >> 1) % kPer, load_r = (ch & 1) * 8;
+  auto entry = [&]() {
+    const bool has = load_j < in_row && load_r < a.rank;
+    const int64_t from = has ? static_cast<int64_t>(adapters[row_of][load_j]) * a.n_out : 0;
+    const char* src = element<ENGRAM_BF16>(a.b, from * a.rank + (has ? load_r : 0));
+    load_j += kPer;
+    if (load_j >= turns * kPer) {
+      load_j -= turns * kPer;
+      load_r += 16;
+    }
+    return src;
+  };
+  int rows[kLoadsW];   // the rows of B that this lane loads
+#pragma unroll
+  for (int l = 0; l < kLoadsW; ++l) {
+    const int64_t o = f0 + r0 + l * kRowsAtOnce;
+    rows[l] = static_cast<int>(o < a.n_out ? o : 0);
+  }
+  const char* from = slices > ksteps ? entry() : nullptr;
+  auto issue_adapters = [&](int kt) {
+    u32x4_t* dst = lds + (kt % RING) * kBuffer + wave * 64;
+#pragma unroll
+    for (int l = 0; l < kLoadsW; ++l)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)element<ENGRAM_BF16>(from, static_cast<int64_t>(rows[l]) * a.rank),
+                                       (__attribute__((address_space(3))) void*)(dst + l * NT), 16, 0, 0);
+#pragma unroll
+    for (int l = 0; l < kLoadsE; ++l)   // (no rows: a slice has its number of loads all the same)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (__attribute__((address_space(3))) void*)(dst + TF * 8 + l * NT), 16, 0x7fff0000, 0, 0, 0);
+    from = entry();
+  };
+#pragma unroll
+  for (int p = 0; p < RING - 1; ++p)
+    if (p >= ksteps && p < slices) issue_adapters(p);
   f32x16_t acc[TB][FB];
 #pragma unroll
   for (int b = 0; b < TB; ++b)
@@ -325,13 +408,17 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
     for (int f = 0; f < FB; ++f)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][f][i] = 0.f;
-  const int ksteps = K / 64;
-  issue(0);
+  // (the wait: slice kt is there, and slice kt - 1, whose buffer is filled next, has been read)
+  auto begin = [&](int kt) {
+    wait_slices<kLoadsW + kLoadsE, RING - 2>(slices - 1 - kt);
+    const int next = kt + RING - 1;
+    if (next < ksteps) issue(next);
+    else if (next < slices) issue_adapters(next);
+  };
   for (int kt = 0; kt < ksteps; ++kt) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the slice is there, the other buffer has been read
-    if (kt + 1 < ksteps) issue(kt + 1);
-    const u32x4_t* ws = lds + (kt & 1) * kBuffer + (wf * (TF / WF)) * 8;
-    const u32x4_t* es = lds + (kt & 1) * kBuffer + (TF + wt * (TT / WT)) * 8;
+    begin(kt);
+    const u32x4_t* ws = lds + (kt % RING) * kBuffer + (wf * (TF / WF)) * 8;
+    const u32x4_t* es = lds + (kt % RING) * kBuffer + (TF + wt * (TT / WT)) * 8;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int kc = (s * 2 + lh) ^ ((lr >> 1) & 7);
@@ -346,48 +433,109 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
         for (int f = 0; f < FB; ++f) acc[b][f] = multiply<ENGRAM_BF16>(fw[f], fe[b], acc[b][f]);
     }
   }
-  const int64_t fw0 = f0 + wf * (TF / WF), tw0 = t0 + wt * (TT / WT);
+  const u32x4_t zero = {0, 0, 0, 0};
+  const int hc = h_columns(ENGRAM_BF16, a.rank);
+  f32x16_t none;
 #pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    const int64_t t = tw0 + b * 32 + lr;
-    add_adapters<ENGRAM_BF16, FB>(a, adapter_of(a, t), t, fw0, 0, 1, acc[b]);
+  for (int i = 0; i < 16; ++i) none[i] = 0.f;
+  u32x4_t h0[TB], h1[TB];
+  int j = 0, r = -16;   // this wavefront's next adapter, its columns
+  bool in = false;
+  for (int kt = ksteps; kt < slices; ++kt) {
+    begin(kt);
+    if (j == 0) {
+      r += 16;
+      in = r + lh * 8 < a.rank;   // (a rank of 8, 24, ..: the last columns' second half is none)
+#pragma unroll
+      for (int b = 0; b < TB; ++b) {
+        const char* h = static_cast<const char*>(a.h) + (min(tw0 + b * 32 + lr, a.n_tok - 1) * hc + r + lh * 8) * 2;
+        h0[b] = load16(h);
+        h1[b] = load16(h + hc);
+        if (!in) h0[b] = h1[b] = zero;
+      }
+    }
+    const u32x4_t* ws = lds + (kt % RING) * kBuffer + (wf * (TF / WF)) * 8;
+    int one[kPer];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) one[p] = j + p < own ? adapters[wt][j + p] : -2;
+    j += kPer;
+    if (j >= turns * kPer) j = 0;
+    bool mine[TB][kPer], all[TB], any[TB];
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      bool some = false;
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) some |= mine[b][p] = id[b] == one[p];
+      any[b] = __any(some);
+      all[b] = __all(mine[b][0]);
+    }
+#pragma unroll
+    for (int f = 0; f < FB; ++f) {
+      u32x4_t fw[kPer];
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) {
+        fw[p] = ws[(f * 32 + lr) * 8 + (((wt * kPer + p) * 2 + lh) ^ ((lr >> 1) & 7))];
+        if (!in) fw[p] = zero;
+      }
+#pragma unroll
+      for (int b = 0; b < TB; ++b) {
+        if (all[b]) {
+          acc[b][f] = multiply<ENGRAM_BF16>(fw[0], h1[b], multiply<ENGRAM_BF16>(fw[0], h0[b], acc[b][f]));
+        } else if (any[b]) {
+          // a lane's sums are its own token's: it takes its adapter's product and no other's, so that an infinity or a
+          // NaN in one request's adapter stays with it
+          f32x16_t sum[kPer];
+#pragma unroll
+          for (int p = 0; p < kPer; ++p)
+            sum[p] = multiply<ENGRAM_BF16>(fw[p], h1[b], multiply<ENGRAM_BF16>(fw[p], h0[b], p == 0 ? acc[b][f] : none));
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float y = acc[b][f][x];
+#pragma unroll
+            for (int p = kPer - 1; p > 0; --p) y = mine[b][p] ? acc[b][f][x] + sum[p][x] : y;
+            acc[b][f][x] = mine[b][0] ? sum[0][x] : y;
+          }
+        }
+      }
+    }
   }
+  const int64_t fw0 = f0 + wf * (TF / WF);
   // outputs: a block of 32 tokens at a time through the wavefront's own LDS, whole rows of it to memory
   __syncthreads();
   constexpr int kRow = FB * 32 * static_cast<int>(sizeof(OutT)) + 16;   // bytes, 16 more than a row's: the rows' banks differ
   constexpr int kRuns = FB * 32 * static_cast<int>(sizeof(OutT)) / 16;  // 16-byte runs of a row
   constexpr int kEach = 16 / static_cast<int>(sizeof(OutT));
-  char* own = reinterpret_cast<char*>(lds) + wave * 32 * kRow;
+  char* mem = reinterpret_cast<char*>(lds) + wave * 32 * kRow;
 #pragma unroll
   for (int b = 0; b < TB; ++b) {
 #pragma unroll
     for (int f = 0; f < FB; ++f)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        char* at = own + lr * kRow + (f * 32 + g * 8 + lh * 4) * static_cast<int>(sizeof(OutT));
+        char* to = mem + lr * kRow + (f * 32 + g * 8 + lh * 4) * static_cast<int>(sizeof(OutT));
         const f32x16_t& x = acc[b][f];
         if constexpr (sizeof(OutT) == 2)
-          *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(x[4 * g], x[4 * g + 1]), pack_bf16x2(x[4 * g + 2], x[4 * g + 3]));
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(x[4 * g], x[4 * g + 1]), pack_bf16x2(x[4 * g + 2], x[4 * g + 3]));
         else
-          *reinterpret_cast<f32x4_t*>(at) = f32x4_t{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+          *reinterpret_cast<f32x4_t*>(to) = f32x4_t{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wavefront's block is in LDS
 #pragma unroll
     for (int i = 0; i < 32 * kRuns / 64; ++i) {
       const int run = i * 64 + lane, row = run / kRuns, c = run % kRuns;
       const int64_t t = tw0 + b * 32 + row, o = fw0 + c * kEach;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * kRow + c * 16);
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mem + row * kRow + c * 16);
       if (t < a.n_tok && o < a.n_out) *reinterpret_cast<u32x4_t*>(static_cast<OutT*>(a.out) + t * a.n_out + o) = v;
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // and read, before the next block's writes
   }
 }
 
-template <int TF, int TT, int WF, int WT, typename OutT>
+template <int TF, int TT, int WF, int WT, int RING, typename OutT>
 hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
   constexpr int kOut = WF * WT * 32 * (TF / WF * static_cast<int>(sizeof(OutT)) + 16);
-  constexpr int kLds = std::max(2 * (TF + TT) * 128, kOut);
-  auto* const fn = adapt_tile_kernel<TF, TT, WF, WT, OutT>;
+  constexpr int kLds = std::max(RING * (TF + TT) * 128, kOut);
+  auto* const fn = adapt_tile_kernel<TF, TT, WF, WT, RING, OutT>;
   static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -419,9 +567,10 @@ hipError_t launch_product(const AdaptArgs& a, int dtype, hipStream_t s) {
     return hipErrorInvalidValue;
   }
   if (a.n_tok <= 32) return launch_small<ENGRAM_BF16, 1, 1, OutT>(a, s);
-  if (a.n_tok <= 512) return launch_small<ENGRAM_BF16, 2, 2, OutT>(a, s);
-  if (((a.n_tok + 255) / 256) * ((a.n_out + 255) / 256) >= 256) return launch_tile<256, 256, 2, 4, OutT>(a, s);
-  return launch_tile<128, 128, 2, 2, OutT>(a, s);
+  const int64_t t = a.n_tok, o = a.n_out;
+  if (((t + 255) / 256) * ((o + 255) / 256) >= 256) return launch_tile<256, 256, 2, 4, 2, OutT>(a, s);
+  if (((t + 127) / 128) * ((o + 127) / 128) >= 256) return launch_tile<128, 128, 2, 2, 2, OutT>(a, s);
+  return launch_tile<64, 64, 2, 2, 4, OutT>(a, s);
 }
 
 }  // namespace
