@@ -351,14 +351,23 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
 #pragma unroll
   for (int p = 0; p < RING - 1; ++p)
     if (p < ksteps) issue(p);
-  // the adapters among each row of wavefronts' tokens
+  // the adapters among each row of wavefronts' tokens, in the order of their first ones
   const int token = TB == 2 && lh == 1 ? id[TB - 1] : TB == 1 && lh == 1 ? -1 : id[0];   // a lane's own of them
-  int own = 0;
-  each_adapter(token, [&](int one, int j) {
-    if (wf == 0 && lane == 0) adapters[wt][j] = one;
-    own = j + 1;
-  });
-  if (wf == 0 && lane == 0) counts[wt] = own;
+  bool opens = token >= 0;
+  if (!__all(token == __builtin_amdgcn_readfirstlane(token)))
+#pragma unroll 4
+    for (int l = 0; l < kTokens - 1; ++l) {
+      const int earlier = __builtin_amdgcn_readlane(token, l);   // (every lane active)
+      opens &= (l >= lane) | (earlier != token);
+    }
+  else
+    opens &= lane == 0;
+  const uint64_t openers = __ballot(opens);
+  const int own = __popcll(openers);
+  if (wf == 0) {
+    if (opens) adapters[wt][__popcll(openers & ((uint64_t{1} << lane) - 1))] = token;
+    if (lane == 0) counts[wt] = own;
+  }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   int most = 0;
 #pragma unroll
@@ -460,14 +469,13 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
     for (int p = 0; p < kPer; ++p) one[p] = j + p < own ? adapters[wt][j + p] : -2;
     j += kPer;
     if (j >= turns * kPer) j = 0;
-    bool mine[TB][kPer], all[TB], any[TB];
+    bool mine[TB][kPer], any[TB];
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
       bool some = false;
 #pragma unroll
       for (int p = 0; p < kPer; ++p) some |= mine[b][p] = id[b] == one[p];
       any[b] = __any(some);
-      all[b] = __all(mine[b][0]);
     }
 #pragma unroll
     for (int f = 0; f < FB; ++f) {
@@ -477,13 +485,21 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
         fw[p] = ws[(f * 32 + lr) * 8 + (((wt * kPer + p) * 2 + lh) ^ ((lr >> 1) & 7))];
         if (!in) fw[p] = zero;
       }
+      uint32_t top = 0;   // an exponent of ones carries into the sign's place
+#pragma unroll
+      for (int p = 0; p < kPer; ++p)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top |= (fw[p][x] & 0x7f807f80u) + 0x00800080u;
+      const bool odd = __any((top & 0x80008000u) != 0);
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        if (all[b]) {
-          acc[b][f] = multiply<ENGRAM_BF16>(fw[0], h1[b], multiply<ENGRAM_BF16>(fw[0], h0[b], acc[b][f]));
+        if (!odd) {        // the other tokens' rows of h as zeros
+#pragma unroll
+          for (int p = 0; p < kPer; ++p)
+            acc[b][f] = multiply<ENGRAM_BF16>(fw[p], mine[b][p] ? h1[b] : zero, multiply<ENGRAM_BF16>(fw[p], mine[b][p] ? h0[b] : zero, acc[b][f]));
         } else if (any[b]) {
-          // a lane's sums are its own token's: it takes its adapter's product and no other's, so that an infinity or a
-          // NaN in one request's adapter stays with it
+          // an infinity or a NaN in B: a lane's sums are its own token's, it takes its adapter's product and no other's,
+          // so that one request's bad adapter stays with it
           f32x16_t sum[kPer];
 #pragma unroll
           for (int p = 0; p < kPer; ++p)
