@@ -148,9 +148,10 @@ rank_kernel(const int32_t* __restrict__ ids, int n, uint32_t V, uint32_t* __rest
 // each block's digits, sums the counts (digit by digit, block by block) and
 // moves every id to its place.
 constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
-constexpr int kSortBlock = 4096;                       // ids of a workgroup
-constexpr int kSortRounds = kSortBlock / kSortThreads;
-constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits, kDigitsEach = kDigits / kSortThreads;
+// ROUNDS * kSortThreads ids a workgroup: 4 rounds up to kShortSort ids, 16 above
+// (more workgroups for the one, fewer counts to sum for the other).
+constexpr int64_t kShortSort = 1 << 18;
 
 struct SortPass {
   const int32_t* ids;       // first pass: the caller's ids (pos is the index itself)
@@ -167,20 +168,26 @@ struct SortPass {
 
 __device__ __forceinline__ uint32_t sort_key(const SortPass& a, int64_t i) { return a.ids != nullptr ? key_of(a.ids[i], a.V) : a.key[i]; }
 
+template <int ROUNDS>
 __global__ void __launch_bounds__(kSortThreads)
 digit_count_kernel(SortPass a, Fill fill) {
   if (static_cast<int>(blockIdx.x) >= a.blocks) return fill_zeros(fill, blockIdx.x - a.blocks, kSortThreads);
   __shared__ uint32_t hist[kDigits];
-  hist[threadIdx.x] = 0;
-  __syncthreads();
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortBlock;
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
+  for (int k = 0; k < kDigitsEach; ++k) hist[k * kSortThreads + threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * ROUNDS * kSortThreads;
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
     const int64_t i = i0 + r * kSortThreads + threadIdx.x;
     if (i < a.n) atomicAdd(&hist[(sort_key(a, i) >> a.shift) & (kDigits - 1)], 1u);
   }
   __syncthreads();
-  a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x] = hist[threadIdx.x];
+#pragma unroll
+  for (int k = 0; k < kDigitsEach; ++k) {
+    const int digit = k * kSortThreads + threadIdx.x;
+    a.counts[static_cast<int64_t>(digit) * a.blocks + blockIdx.x] = hist[digit];
+  }
 }
 
 __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x) {   // inclusive
@@ -217,36 +224,42 @@ digit_scan_kernel(uint32_t* __restrict__ counts, int64_t m, Fill fill) {
 
 // Each wavefront takes a contiguous quarter of the block's ids, 64 at a time;
 // lanes with the same digit find one another by a ballot for each digit bit.
+template <int ROUNDS>
 __global__ void __launch_bounds__(kSortThreads)
 digit_move_kernel(SortPass a, Fill fill) {
   if (static_cast<int>(blockIdx.x) >= a.blocks) return fill_zeros(fill, blockIdx.x - a.blocks, kSortThreads);
   __shared__ uint32_t at[kSortWaves][kDigits];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int w = 0; w < kSortWaves; ++w) at[w][threadIdx.x] = 0;
-  __syncthreads();
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortBlock + wave * (kSortBlock / kSortWaves);
-  uint32_t key[kSortRounds];
+  for (int w = 0; w < kSortWaves; ++w)
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
+    for (int k = 0; k < kDigitsEach; ++k) at[w][k * kSortThreads + threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kSortWaves + wave) * ROUNDS * 64;
+  uint32_t key[ROUNDS], pos[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
     const int64_t i = i0 + r * 64 + lane;
     key[r] = i < a.n ? sort_key(a, i) : 0;
+    pos[r] = a.ids != nullptr || i >= a.n ? static_cast<uint32_t>(i) : a.pos[i];
     if (i < a.n) atomicAdd(&at[wave][(key[r] >> a.shift) & (kDigits - 1)], 1u);
   }
   __syncthreads();
-  {   // where each wavefront's ids of each digit begin
-    uint32_t from = a.counts[static_cast<int64_t>(threadIdx.x) * a.blocks + blockIdx.x];
+#pragma unroll
+  for (int k = 0; k < kDigitsEach; ++k) {   // where each wavefront's ids of each digit begin
+    const int digit = k * kSortThreads + threadIdx.x;
+    uint32_t from = a.counts[static_cast<int64_t>(digit) * a.blocks + blockIdx.x];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t x = at[w][threadIdx.x];
-      at[w][threadIdx.x] = from;
+      const uint32_t x = at[w][digit];
+      at[w][digit] = from;
       from += x;
     }
   }
   __syncthreads();
   const uint64_t below = (uint64_t{1} << lane) - 1;
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
+  for (int r = 0; r < ROUNDS; ++r) {
     const int64_t i = i0 + r * 64 + lane;
     const uint32_t digit = (key[r] >> a.shift) & (kDigits - 1);
     uint64_t same = __ballot(i < a.n);
@@ -258,7 +271,7 @@ digit_move_kernel(SortPass a, Fill fill) {
     if (i < a.n) {
       const uint32_t to = at[wave][digit] + __popcll(same & below);
       a.key_out[to] = key[r];
-      a.pos_out[to] = a.ids != nullptr ? static_cast<uint32_t>(i) : a.pos[i];
+      a.pos_out[to] = pos[r];
     }
     wave_sync();   // every lane has read its digit's place before the digit's last lane moves it on
     if (i < a.n && (same >> lane) == 1) at[wave][digit] += __popcll(same);
@@ -299,39 +312,79 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int64_
 
 // Sums over tiles of the sorted tokens.  A run of equal ids inside a tile is
 // written to its row; one that came in from the tile before, or goes on in
-// the next, leaves its part sum (slot 0: came in, slot 1: begins here).
-template <int IN, int OUT>
+// the next, leaves its part sum (slot 0: came in, slot 1: begins here).  Bound
+// by memory: kAhead rows of dout are in flight for every chunk of columns (one
+// at a time, 32763 x 4 x 1024 bf16 148 us).
+constexpr int kAhead = 8;
+constexpr int kLeastLanes = 2;   // log2: of a tile
+template <int IN>
+struct Chunk {   // 8 columns as stored
+  u32x4_t x[IN == ENGRAM_BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + i * (IN == ENGRAM_BF16 ? 2 : 4));
+    x[0] = q[0];
+    if constexpr (IN == ENGRAM_F32) x[1] = q[1];
+  }
+  __device__ __forceinline__ float at(int k) const {
+    if constexpr (IN == ENGRAM_BF16) return __uint_as_float(k & 1 ? x[0][k >> 1] & 0xffff0000u : x[0][k >> 1] << 16);
+    else return __uint_as_float(x[k >> 2][k & 3]);
+  }
+};
+
+template <int IN, int OUT, int TILE>
 __global__ void __launch_bounds__(kThreads)
 tile_sum_kernel(SumArgs a) {
-  const int lanes = 1 << a.log_lanes;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
-  if (t >= a.tiles) return;
-  const int64_t p0 = t * a.tile, p1 = min(p0 + a.tile, a.n);
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * 8;
-  if (c >= a.dim) return;
+  constexpr int kMost = (kThreads >> kLeastLanes) * TILE;   // sorted tokens of a workgroup
+  __shared__ uint32_t keys[kMost + 2], pos[kMost];           // keys[0]: of the token before
+  const int tiles = kThreads >> a.log_lanes, mine = threadIdx.x >> a.log_lanes;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * tiles * TILE;
+  const int here = static_cast<int>(min(static_cast<int64_t>(tiles) * TILE, a.n - first));
+  for (int i = threadIdx.x; i < here + 2; i += kThreads) {
+    const int64_t p = first + i - 1;
+    keys[i] = p >= 0 && p < a.n ? a.key[p] : ~0u;
+    if (i < here) pos[i] = a.pos[first + i];
+  }
+  __syncthreads();
+  const int p0 = mine * TILE, p1 = min(p0 + TILE, here);
+  const int64_t c = ((static_cast<int64_t>(blockIdx.y) << a.log_lanes) + (threadIdx.x & ((1 << a.log_lanes) - 1))) * 8;
+  if (p0 >= here || c >= a.dim) return;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * tiles + mine;
+  int end = p1;   // ids without a row come last
+  while (end > p0 && keys[end] >= a.V) --end;
   const int64_t step = a.branches * a.dim;
+  const int items = (end - p0) * a.branches;   // (token, branch) pairs
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  uint32_t key = a.key[p0];
-  bool begun = p0 == 0 || a.key[p0 - 1] != key;   // the run begins in this tile
-  for (int64_t p = p0; p < p1; ++p) {
-    if (key >= a.V) return;   // ids without a row come last
-    const int64_t at = a.pos[p] * step + c;
-    for (int m = 0; m < a.branches; ++m) {
-      float f[8];
-      load8<IN>(a.dout, at + m * a.dim, f);
+  bool begun = keys[p0] != keys[p0 + 1];       // the run begins in this tile
+  int p = p0, m = 0;                           // of the next to be added
+  int q = p0, b = 0;                           // of the next to be loaded
+  for (int i0 = 0; i0 < items; i0 += kAhead) {
+    Chunk<IN> x[kAhead];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += f[k];
+    for (int i = 0; i < kAhead; ++i) {
+      x[i].load(a.dout, pos[q] * step + b * a.dim + c);
+      if (i0 + i + 1 < items && ++b == a.branches) {   // (behind the last one it is loaded again)
+        b = 0;
+        ++q;
+      }
     }
-    const uint32_t next = p + 1 < a.n ? a.key[p + 1] : ~0u;
-    const bool ends = next != key;
-    if (ends || p + 1 == p1) {
-      if (begun && ends) write_row<OUT>(a, key, c, sum);
-      else store8<ENGRAM_F32>(a.part, (t * 2 + (begun ? 1 : 0)) * a.dim + c, sum);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] = 0.f;
-      begun = true;
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= items) break;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += x[i].at(k);
+      if (++m < a.branches) continue;
+      m = 0;
+      const uint32_t key = keys[p + 1];
+      const bool ends = keys[p + 2] != key;
+      if (ends || p + 1 == p1) {
+        if (begun && ends) write_row<OUT>(a, key, c, sum);
+        else store8<ENGRAM_F32>(a.part, (tile * 2 + (begun ? 1 : 0)) * a.dim + c, sum);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+        begun = true;
+      }
+      ++p;
     }
-    key = next;
   }
 }
 
@@ -342,18 +395,29 @@ template <int OUT>
 __global__ void __launch_bounds__(kJoinThreads)
 tile_join_kernel(SumArgs a) {
   __shared__ float share[kJoinGroups][kJoinLanes][9];
+  __shared__ int back[kJoinThreads / 64];
   const int64_t t = static_cast<int64_t>(blockIdx.x) + 1;
   const int64_t p0 = t * a.tile, p1 = min(p0 + a.tile, a.n);
   const uint32_t key = a.key[p0];
   if (key >= a.V || a.key[p0 - 1] != key || (p1 < a.n && a.key[p1] == key && a.key[p1 - 1] == key)) return;
-  // the run's first token
-  int64_t lo = 0, hi = p0;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.key[mid] < key) lo = mid + 1;
-    else hi = mid;
+  // the tiles before this one that begin inside the run, kJoinThreads of them a turn
+  int64_t begin = t;
+  for (;;) {
+    const int64_t u = begin - 1 - threadIdx.x;
+    const uint64_t other = __ballot(u < 0 || a.key[u * a.tile] != key);
+    if ((threadIdx.x & 63) == 0) back[threadIdx.x >> 6] = other != 0 ? __builtin_ctzll(other) : 64;
+    __syncthreads();
+    int n = 0;
+    for (int w = 0; w < kJoinThreads / 64; ++w) {
+      n += back[w];
+      if (back[w] < 64) break;
+    }
+    __syncthreads();
+    begin -= n;
+    if (n < kJoinThreads) break;
   }
-  const int64_t t0 = lo / a.tile, parts = t - t0 + 1, per = (parts + kJoinGroups - 1) / kJoinGroups;
+  const int64_t t0 = begin > 0 && a.key[begin * a.tile - 1] == key ? begin - 1 : begin;
+  const int64_t parts = t - t0 + 1, per = (parts + kJoinGroups - 1) / kJoinGroups;
   const int lane = threadIdx.x % kJoinLanes, group = threadIdx.x / kJoinLanes;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * kJoinLanes + lane) * 8;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -380,16 +444,20 @@ tile_join_kernel(SumArgs a) {
 // Ids up to this number take rank_kernel.
 constexpr int64_t kMostRanked = 16384;
 
-int64_t sort_blocks(int64_t n) { return (n + kSortBlock - 1) / kSortBlock; }
+int64_t sort_blocks(int64_t n) {
+  const int64_t block = kSortThreads * (n <= kShortSort ? 4 : 16);
+  return (n + block - 1) / block;
+}
 
 int sort_passes(int64_t V) {   // digits that hold the keys 0..V
   int passes = 1;
-  while (passes < 4 && (V >> (passes * kDigitBits)) > 0) ++passes;
+  while (passes * kDigitBits < 32 && (V >> (passes * kDigitBits)) > 0) ++passes;
   return passes;
 }
 
 // Sorted tokens of a tile: as many as leave enough tiles to fill the GPU.
-int tile_tokens(int64_t n) { return n <= 4096 ? 8 : 32; }
+constexpr int kShortTile = 8, kLongTile = 32;
+int tile_tokens(int64_t n) { return n <= 4096 ? kShortTile : kLongTile; }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t{255}; }
 
@@ -495,7 +563,7 @@ hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout
                        p * kDigitBits, blocks};
       Fill f = zeros.next(left--);
       prof_stage("digit_count_kernel");
-      launch_k(digit_count_kernel, dim3(blocks + fill_groups(f, kSortThreads)), dim3(kSortThreads), 0, s, a, f);
+      launch_k(n <= kShortSort ? digit_count_kernel<4> : digit_count_kernel<16>, dim3(blocks + fill_groups(f, kSortThreads)), dim3(kSortThreads), 0, s, a, f);
       if ((e = launch_error()) != hipSuccess) return e;
       f = zeros.next(left--);
       prof_stage("digit_scan_kernel");
@@ -503,19 +571,20 @@ hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout
       if ((e = launch_error()) != hipSuccess) return e;
       f = zeros.next(left--);
       prof_stage("digit_move_kernel");
-      launch_k(digit_move_kernel, dim3(blocks + fill_groups(f, kSortThreads)), dim3(kSortThreads), 0, s, a, f);
+      launch_k(n <= kShortSort ? digit_move_kernel<4> : digit_move_kernel<16>, dim3(blocks + fill_groups(f, kSortThreads)), dim3(kSortThreads), 0, s, a, f);
       if ((e = launch_error()) != hipSuccess) return e;
       sorted = to;
     }
   }
-  const int log_lanes = row_lanes_log2(dim), lanes = 1 << log_lanes;
+  const int log_lanes = std::max(row_lanes_log2(dim), kLeastLanes), lanes = 1 << log_lanes;
   const int tile = tile_tokens(n);
   const int64_t tiles = (n + tile - 1) / tile, per = kThreads / lanes;
   const SumArgs a{g.key[sorted], g.pos[sorted], dout, dtable, g.part, n, dim, tiles, static_cast<uint32_t>(V), branches, log_lanes, tile,
                   accumulate ? 1 : 0, scale};
   prof_stage("tile_sum_kernel");
   e = by_types(dtype, out_dtype, [&](auto in, auto to) {
-    launch_k((tile_sum_kernel<decltype(in)::value, decltype(to)::value>),
+    launch_k(tile == kShortTile ? tile_sum_kernel<decltype(in)::value, decltype(to)::value, kShortTile>
+                                : tile_sum_kernel<decltype(in)::value, decltype(to)::value, kLongTile>,
              dim3(static_cast<unsigned>((tiles + per - 1) / per), static_cast<unsigned>((dim + lanes * 8 - 1) / (lanes * 8))), dim3(kThreads), 0, s, a);
     return launch_error();
   });
