@@ -97,13 +97,13 @@ __device__ __forceinline__ void each_adapter(int id, F f) {
 }
 
 // ---- h ----
-// A block of 32 tokens and one of the adapters in it a workgroup, whose four
-// wavefronts take every fourth 64 columns; 32 rows of A at a time.
-template <int DT>
-__global__ void __launch_bounds__(256)
+// A block of 32 tokens and one of the adapters in it a workgroup, whose NW
+// wavefronts take every NW-th 64 columns; 32 rows of A at a time.
+template <int DT, int NW>
+__global__ void __launch_bounds__(NW * 64)
 adapter_rows_kernel(AdaptArgs a) {
   using Fr = Frag<DT>;
-  __shared__ f32x4_t part[4][4][64];
+  __shared__ f32x4_t part[NW][4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 31, lh = lane >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lr;
   const int id = adapter_of(a, t);
@@ -119,7 +119,7 @@ adapter_rows_kernel(AdaptArgs a) {
     f32x16_t acc;
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int c = wave * kChunk; c < a.K; c += 4 * kChunk) {
+    for (int c = wave * kChunk; c < a.K; c += NW * kChunk) {
       u32x4_t fa[Fr::kSteps], fe[Fr::kSteps];
 #pragma unroll
       for (int s = 0; s < Fr::kSteps; ++s) {
@@ -134,9 +134,11 @@ adapter_rows_kernel(AdaptArgs a) {
     for (int g = 0; g < 4; ++g) part[wave][g][lane] = f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
     __syncthreads();
     // rows r0 + 8 wave + 4 lh .. + 3 of the lane's token
-    f32x4_t x = part[0][wave][lane] + part[1][wave][lane] + part[2][wave][lane] + part[3][wave][lane];
+    if (wave >= 4 || id != mine) continue;
+    f32x4_t x = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) x += part[w][wave][lane];
     const int r = r0 + wave * 8 + lh * 4;
-    if (id != mine) continue;
     x *= scale;
     if constexpr (DT == ENGRAM_BF16) {
       if (r >= hc / 2) continue;
@@ -211,14 +213,14 @@ __device__ __forceinline__ void add_adapters(const AdaptArgs& a, int id, int64_t
 }
 
 // ---- few tokens, and float32 ----
-// TB x FB blocks of 32 tokens x 32 outputs a workgroup.  Its four wavefronts
-// share the columns (every fourth 64) and the adapters, operands straight from
+// TB x FB blocks of 32 tokens x 32 outputs a workgroup.  Its NW wavefronts
+// share the columns (every NW-th 64) and the adapters, operands straight from
 // memory into registers; their sums meet in LDS.
-template <int DT, int TB, int FB, typename OutT>
-__global__ void __launch_bounds__(256)
+template <int DT, int TB, int FB, int NW, typename OutT>
+__global__ void __launch_bounds__(NW * 64)
 adapt_small_kernel(AdaptArgs a, int tiles_f) {
   using Fr = Frag<DT>;
-  __shared__ f32x4_t part[4][TB * FB][4][64];
+  __shared__ f32x4_t part[NW][TB * FB][4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 31, lh = lane >> 5;
   const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * FB * 32, t0 = static_cast<int64_t>(blockIdx.x / tiles_f) * TB * 32;
   const char *w[FB], *e[TB];
@@ -236,7 +238,7 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
     for (int f = 0; f < FB; ++f)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[b][f][i] = 0.f;
-  for (int c = wave * kChunk; c < a.K; c += 4 * kChunk) {
+  for (int c = wave * kChunk; c < a.K; c += NW * kChunk) {
     u32x4_t fw[FB][Fr::kSteps], fe[TB][Fr::kSteps];
 #pragma unroll
     for (int s = 0; s < Fr::kSteps; ++s) {
@@ -253,7 +255,7 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
         for (int f = 0; f < FB; ++f) acc[b][f] = multiply<DT>(fw[f][s], fe[b][s], acc[b][f]);
   }
 #pragma unroll
-  for (int b = 0; b < TB; ++b) add_adapters<DT, FB>(a, id[b], t0 + b * 32 + lr, f0, wave, 4, acc[b]);
+  for (int b = 0; b < TB; ++b) add_adapters<DT, FB>(a, id[b], t0 + b * 32 + lr, f0, wave, NW, acc[b]);
 #pragma unroll
   for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -262,6 +264,7 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
       for (int g = 0; g < 4; ++g)
         part[wave][b * FB + f][g][lane] = f32x4_t{acc[b][f][4 * g], acc[b][f][4 * g + 1], acc[b][f][4 * g + 2], acc[b][f][4 * g + 3]};
   __syncthreads();
+  if (wave >= 4) return;
 #pragma unroll
   for (int b = 0; b < TB; ++b) {
     const int64_t t = t0 + b * 32 + lr;
@@ -269,7 +272,9 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
 #pragma unroll
     for (int f = 0; f < FB; ++f) {
       const int blk = b * FB + f;
-      const f32x4_t x = part[0][blk][wave][lane] + part[1][blk][wave][lane] + part[2][blk][wave][lane] + part[3][blk][wave][lane];
+      f32x4_t x = part[0][blk][wave][lane];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) x += part[w][blk][wave][lane];
       OutT* out = static_cast<OutT*>(a.out) + t * a.n_out + f0 + f * 32 + wave * 8 + lh * 4;
       if constexpr (sizeof(OutT) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
       else *reinterpret_cast<f32x4_t*>(out) = x;
@@ -568,22 +573,23 @@ hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
   return launch_error();
 }
 
-template <int DT, int TB, int FB, typename OutT>
+template <int DT, int TB, int FB, int NW, typename OutT>
 hipError_t launch_small(const AdaptArgs& a, hipStream_t s) {
   const int tiles_f = a.n_out / (FB * 32);
   const int64_t tiles = (a.n_tok + TB * 32 - 1) / (TB * 32) * tiles_f;
-  launch_k((adapt_small_kernel<DT, TB, FB, OutT>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a, tiles_f);
+  launch_k((adapt_small_kernel<DT, TB, FB, NW, OutT>), dim3(static_cast<unsigned>(tiles)), dim3(NW * 64), 0, s, a, tiles_f);
   return launch_error();
 }
 
 template <typename OutT>
 hipError_t launch_product(const AdaptArgs& a, int dtype, hipStream_t s) {
+  const int64_t t = a.n_tok, o = a.n_out;
   if (dtype == ENGRAM_F32) {
-    if constexpr (sizeof(OutT) == 4) return a.n_tok <= 32 ? launch_small<ENGRAM_F32, 1, 1, float>(a, s) : launch_small<ENGRAM_F32, 2, 2, float>(a, s);
+    if constexpr (sizeof(OutT) == 4)
+      return ((t + 63) / 64) * (o / 64) < 512 ? launch_small<ENGRAM_F32, 1, 1, 8, float>(a, s) : launch_small<ENGRAM_F32, 2, 2, 4, float>(a, s);
     return hipErrorInvalidValue;
   }
-  if (a.n_tok <= 32) return launch_small<ENGRAM_BF16, 1, 1, OutT>(a, s);
-  const int64_t t = a.n_tok, o = a.n_out;
+  if (t <= 32) return launch_small<ENGRAM_BF16, 1, 1, 16, OutT>(a, s);
   if (((t + 255) / 256) * ((o + 255) / 256) >= 256) return launch_tile<256, 256, 2, 4, 2, OutT>(a, s);
   if (((t + 127) / 128) * ((o + 127) / 128) >= 256) return launch_tile<128, 128, 2, 2, 2, OutT>(a, s);
   return launch_tile<64, 64, 2, 2, 4, OutT>(a, s);
@@ -607,8 +613,10 @@ hipError_t launch_project_adapted(const void* e, const void* w, int64_t n_tok, i
     const int64_t most = std::min<int64_t>({32, adapters, (30 + per) / per + 1});
     const dim3 grid(static_cast<unsigned>((n_tok + 31) / 32), static_cast<unsigned>(most));
     prof_stage("adapter_rows_kernel");
-    if (dtype == ENGRAM_BF16) launch_k(adapter_rows_kernel<ENGRAM_BF16>, grid, dim3(256), 0, s, a);
-    else launch_k(adapter_rows_kernel<ENGRAM_F32>, grid, dim3(256), 0, s, a);
+    // few workgroups: more wavefronts for the columns of each
+    const bool few = n_tok <= 512;
+    if (dtype == ENGRAM_F32) launch_k(few ? adapter_rows_kernel<ENGRAM_F32, 8> : adapter_rows_kernel<ENGRAM_F32, 4>, grid, dim3(few ? 512 : 256), 0, s, a);
+    else launch_k(few ? adapter_rows_kernel<ENGRAM_BF16, 16> : adapter_rows_kernel<ENGRAM_BF16, 4>, grid, dim3(few ? 1024 : 256), 0, s, a);
     const hipError_t r = launch_error();
     if (r != hipSuccess) return r;
   }
