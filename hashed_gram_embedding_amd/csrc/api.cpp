@@ -181,7 +181,7 @@ engram_status check_state(const engram_decode_state* st, bool need_ids) {
 // Mode 1 keeps the stages of the last call (kCallStages); mode 2 keeps every
 // stage since the last read, up to kMaxStages (later ones are dropped and
 // counted).
-constexpr int kCallStages = 12;
+constexpr int kCallStages = 16;
 constexpr int kMaxStages = 2048;
 
 struct Profiler {

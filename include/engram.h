@@ -749,7 +749,7 @@ engram_status engram_hot_lookup(const int32_t* tokens, int64_t B, int64_t T, con
  * (hipExtLaunchKernel), so a stage is the kernel's execution interval (events
  * owned by the library and reused).
  *   on = 1: engram_profile_read returns the stages of the most recent call
- *           (at most 12).
+ *           (at most 16).
  *   on = 2: stages accumulate over calls until engram_profile_read, which
  *           returns all of them (at most 2048) and starts a new series, so
  *           calls can run back to back without a host wait between them.
