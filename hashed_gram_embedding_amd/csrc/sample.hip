@@ -63,6 +63,7 @@ constexpr int kSteps = 60 * kTable;
 // up to the row's largest, lie in LDS (both signs), and an entry's weight is
 // one read.
 constexpr int kExponents = 15, kValues = kExponents << 7;
+constexpr uint32_t kFirstBase = (127 + 7) * 128 - kValues;   // of rows whose largest logit is below 128 in magnitude
 
 struct Weight {
   double top, a;         // a: kTable log2(e) / T
@@ -101,9 +102,16 @@ struct Weight {
     if (at >= kValues) w = l == -__builtin_inff() ? static_cast<uint64_t>(kSteps >> bin_shift) << 52 : formed(l);
     return w;
   }
+  // An entry counted by value; f(l) for one of another magnitude.
+  template <typename F>
+  static __device__ __forceinline__ void count(uint32_t* counts, uint32_t from, float l, F f) {
+    const uint32_t bits = __float_as_uint(l) >> 16, at = (bits & 0x7fff) - from;
+    if (at < kValues) atomicAdd(&counts[at + (bits >> 15) * kValues], 1u);
+    else if (l > -__builtin_inff()) f(l);
+  }
   template <int THREADS>
   __device__ __forceinline__ void form_values(float row_top) {
-    base = max((__float_as_uint(row_top) >> 23 & 0xffu) + 1, 134u) * 128 - kValues;   // 134: magnitudes up to 128
+    base = max((__float_as_uint(row_top) >> 23 & 0xffu) * 128 + 128 - kValues, kFirstBase);
     for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) {
       const uint32_t bits = (base + (i < kValues ? i : i - kValues)) | (i < kValues ? 0 : 0x8000);
       const float l = __uint_as_float(bits << 16);
@@ -263,12 +271,13 @@ struct SampleShared {
   static constexpr bool kLooks = DT == ENGRAM_BF16 && THREADS > 256;   // weights of values
   static constexpr int kBinBits = THREADS <= 256 ? 9 : 11, kBins = 1 << kBinBits;
   static constexpr int kBinShift = THREADS <= 256 ? 4 : 2, kLastBin = kSteps >> kBinShift;
-  static constexpr int kListed = THREADS <= 256 ? 5120 : kLooks ? 3584 : 7424;   // entries of the list
+  static constexpr int kListed = THREADS <= 256 ? 5120 : kLooks ? 2560 : 6400;   // entries of the list
   uint64_t bins[kBins];
   uint64_t list[kListed];
   uint64_t values[kLooks ? 2 * kValues : 1];
   double table[kTable];
   uint64_t few[512];
+  float queue[THREADS / 64][128];
   uint64_t wave[THREADS / 64], wave2[THREADS / 64];
   uint64_t part[THREADS / 64 + 1];
   uint64_t before;
@@ -514,9 +523,10 @@ struct Listed {
 // list (at most kListed of them), and, where SUM, in the same pass the sums of
 // the weights in front of that bin (*sum, each wavefront's part; *tail, the
 // entries behind the quads), to which those of the bin that stay are added in
-// sh.part.  False: everything stays.
+// sh.part.  False: everything stays.  counted: the entries' values are counted
+// already (in the list's place), those of other magnitudes in sh.few.
 template <bool SUM, bool CUT, int DT, int THREADS>
-__device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float p) {
+__device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float p, bool counted = false) {
   using Sh = SampleShared<DT, THREADS>;
   Sh& sh = d.sh;
   constexpr int kBins = Sh::kBins, kWaves = THREADS / 64;
@@ -528,19 +538,19 @@ __device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     // entries counted by value (half the LDS work of adding up their weights), the values binned afterwards
     uint32_t* counts = reinterpret_cast<uint32_t*>(sh.list);
     static_assert(sizeof(sh.list) >= 2 * kValues * 4, "the counts fit");
-    for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) counts[i] = 0;
-    __syncthreads();
-    const uint32_t base = d.weight.base;
-    d.template each<4, CUT>([&](float l, uint32_t, bool) {
-      const uint32_t bits = __float_as_uint(l) >> 16, at = (bits & 0x7fff) - base;
-      if (at < kValues) {
-        atomicAdd(&counts[at + (bits >> 15) * kValues], 1u);
-      } else if (l > -__builtin_inff()) {
-        const uint64_t w = d.weight.formed(l);
-        if (d.weight.bin(w) < Sh::kLastBin) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) : 1);
-      }
-    });
-    __syncthreads();
+    auto other = [&](float l) {
+      const uint64_t w = d.weight.formed(l);
+      if (d.weight.bin(w) < Sh::kLastBin) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[d.weight.bin(w)]), SUM ? d.weight.units(w) : 1);
+    };
+    if (counted) {
+      for (int i = threadIdx.x; i < sh.few_n; i += THREADS) other(reinterpret_cast<const float*>(sh.few)[i]);
+    } else {
+      for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) counts[i] = 0;
+      __syncthreads();
+      const uint32_t base = d.weight.base;
+      d.template each<4, CUT>([&](float l, uint32_t, bool) { Weight::count(counts, base, l, other); });
+      __syncthreads();
+    }
     for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) {
       const uint64_t n = counts[i], w = sh.values[i];
       if (n > 0 && d.weight.bin(w) < Sh::kLastBin)
@@ -572,6 +582,19 @@ __device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
   };
   const float from = first_of(bin), front_from = bin > 0 ? first_of(bin - 1) : __builtin_inff();
   uint64_t lo = ~uint64_t{0}, hi = 0, sum = 0, tail = 0;
+  // (the entries in front of the bin are queued, so that their weights are formed or looked up 64 at a time)
+  float* queue = sh.queue[threadIdx.x >> 6];
+  int queued = 0;
+  auto take_queue = [&]() {   // 64 of them, or what is there
+    const int lane = threadIdx.x & 63;
+    wave_sync();
+    const float l = queue[lane], later = queue[64 + lane];
+    if (lane < queued) sum += d.weight.units(d.look(l));
+    wave_sync();
+    if (lane < queued - 64) queue[lane] = later;
+    queued = max(queued - 64, 0);
+    wave_sync();
+  };
   auto in_bin = [&](float l, uint32_t v) { return l >= from && !(l >= front_from) && (!CUT || d.in(l, v)); };
   auto range = [&](uint64_t q) {
     lo = min(lo, q);
@@ -585,9 +608,11 @@ __device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
     } else {   // (a cut before this one lies behind every entry in front of the bin)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t w = d.weight.units(d.look(l[i]));
         const bool front = l[i] >= front_from;
-        sum += front ? w : 0;
+        const uint64_t b = __ballot(front);
+        if (front) queue[queued + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(b >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(b), 0))] = l[i];
+        queued += __popcll(b);
+        if (queued >= 64) take_queue();
         x = fmaxf(x, front ? x : l[i]);
       }
     }
@@ -602,6 +627,7 @@ __device__ __forceinline__ bool cut_row(Draw<DT, THREADS>& d, uint64_t k, float 
       }
     d.append(l, v, which, 0, Sh::kListed, &sh.listed);
   });
+  if (SUM && queued > 0) take_queue();
   if (d.row.vt < d.row.V) {
     const float l = d.row.xt;
     const uint32_t v = static_cast<uint32_t>(d.row.vt);
@@ -657,7 +683,8 @@ __device__ __forceinline__ float wave_nth(float x, int n) {
   return __shfl(x, n - 1, 64);
 }
 
-constexpr int kShort = 512;   // places of a list that one wavefront finishes
+constexpr int kShort = 512;     // places of a list that one wavefront finishes
+constexpr int kOthers = 1024;   // entries of a counted row that are no value of the table: sh.few holds so many floats
 
 // The list's n <= kShort places in ascending order, into sh.few: a wavefront
 // counts, for every kWaves-th place, those before it.  (What a workgroup runs
@@ -701,12 +728,36 @@ sample_kernel(SampleArgs a) {
   float own = -__builtin_inff();
   uint32_t own_v = 0;
   bool nan = row.xt != row.xt;
-  row.template stream<8>([&](const float (&l)[4], uint32_t v) {
+  auto seen = [&](const float (&l)[4], uint32_t v) {
     nan |= __builtin_isunordered(l[0], l[1]) | __builtin_isunordered(l[2], l[3]);
     const float x = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
     own_v = x > own ? v : own_v;
     own = fmaxf(own, x);
-  });
+  };
+  // a bf16 row that is going to be cut by top_p alone: its values are counted on the way
+  bool counted = Sh::kLooks && p < 1.0f && temp > 0.f && !(top_k > 0 && top_k < V);
+  if constexpr (Sh::kLooks) {
+    if (counted) {
+      uint32_t* counts = reinterpret_cast<uint32_t*>(sh.list);
+      for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) counts[i] = 0;
+      if (threadIdx.x == 0) sh.few_n = 0;
+      __syncthreads();
+      auto other = [&](float l) {
+        const int at = atomicAdd(&sh.few_n, 1);
+        if (at < kOthers) reinterpret_cast<float*>(sh.few)[at] = l;
+      };
+      row.template stream<4>([&](const float (&l)[4], uint32_t v) {
+        seen(l, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Weight::count(counts, kFirstBase, l[i], other);
+      });
+      if (row.vt < V) Weight::count(counts, kFirstBase, row.xt, other);
+    } else {
+      row.template stream<8>(seen);
+    }
+  } else {
+    row.template stream<8>(seen);
+  }
   const float quads_own = own;
   own = fmaxf(own, row.xt);
   const float top = group_max<THREADS>(own, nan, sh.red);
@@ -861,7 +912,8 @@ sample_kernel(SampleArgs a) {
     if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
     bool summed = false;
     if (by_k) cut_row<false, false>(d, top_k, 0.f);
-    if (by_p) summed = d.cut == ~uint64_t{0} ? cut_row<true, false>(d, 0, p) : cut_row<true, true>(d, 0, p);
+    counted = counted && d.weight.base == kFirstBase && sh.few_n <= kOthers;
+    if (by_p) summed = d.cut == ~uint64_t{0} ? cut_row<true, false>(d, 0, p, counted) : cut_row<true, true>(d, 0, p);
     if (least > d.lcut) {
       d.set_cut(d.place(least, ~0u));
       summed = false;
