@@ -66,7 +66,9 @@ struct EmbedArgs {
   float scale;
 };
 
-// One row of the table is read once and written M times.
+// One row of the table is read once and written M times.  Bound by memory: 32763
+// tokens x 4 x 1024 in bf16 50 us (5.8 TB/s); 256 x 1 x 1024 4 us, a launch
+// and two loads in a chain.
 template <int IN, int OUT>
 __global__ void __launch_bounds__(kThreads)
 embed_kernel(EmbedArgs a) {
@@ -111,34 +113,48 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t group, int thr
 __device__ __forceinline__ uint32_t key_of(int32_t id, uint32_t V) { return static_cast<uint32_t>(id) < V ? static_cast<uint32_t>(id) : V; }
 
 // Few ids: each one's place is the number of ids before it in the order,
-// counted over all of them (64 ids a workgroup, one a lane; 16 wavefronts
-// share the others, read as scalars).
-constexpr int kRankThreads = 1024;
+// counted over all of them.  16 ids a workgroup, so that few ids still fill the
+// GPU; its other 64 lanes to an id take every 64th 4 of the ids, kRankAhead loads
+// of 16 bytes in flight.  Bound by the comparisons, 3 instructions each.  (64
+// ids a workgroup, the others read as scalars: 17.8 us at 4096 ids, 65 at 16384.)
+constexpr int kRankThreads = 1024, kRankIds = 16, kRankParts = kRankThreads / kRankIds, kRankAhead = 8;
 __global__ void __launch_bounds__(kRankThreads)
 rank_kernel(const int32_t* __restrict__ ids, int n, uint32_t V, uint32_t* __restrict__ key_out, uint32_t* __restrict__ pos_out,
             int groups, Fill fill) {
   if (static_cast<int>(blockIdx.x) >= groups) return fill_zeros(fill, blockIdx.x - groups, kRankThreads);
-  __shared__ int part[kRankThreads / 64][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int i0 = blockIdx.x * 64, i = i0 + lane;
-  const uint32_t key = i < n ? key_of(ids[i], V) : ~0u;
-  const int per = (n + kRankThreads / 64 - 1) / (kRankThreads / 64);
-  const int j0 = min(wave * per, n), j1 = min(j0 + per, n);
+  __shared__ int share[kRankThreads / 64][kRankIds];
+  const int at = threadIdx.x % kRankIds, part = threadIdx.x / kRankIds;
+  const int i = blockIdx.x * kRankIds + at, own = i & ~3;
+  const uint32_t key = i < n ? key_of(ids[i], V) : 0;
+  const int whole = n / 4;
   int before = 0;
-  // of the ids in front of this workgroup's equal ones count too, of those behind it they do not
-  const int front = min(max(i0, j0), j1), back = min(max(i0 + 64, j0), j1);
-  for (int j = j0; j < front; ++j) before += key_of(ids[j], V) <= key;
-  for (int j = front; j < back; ++j) {
-    const uint32_t other = key_of(ids[j], V);
-    before += other < key || (other == key && j < i);
+  // equal ids count where they are in front; of i's own four only smaller ones do here
+  auto four = [&](int j, u32x4_t x) {
+    const uint32_t bound = key + (j < own ? 1 : 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) before += min(x[k], V) < bound;
+  };
+  for (int c0 = part; c0 < whole; c0 += kRankParts * kRankAhead) {
+    u32x4_t x[kRankAhead];
+#pragma unroll
+    for (int u = 0; u < kRankAhead; ++u) {
+      const int c = min(c0 + u * kRankParts, whole - 1);
+      __builtin_memcpy(&x[u], ids + c * 4, 16);   // (ids are aligned to 4 bytes)
+    }
+#pragma unroll
+    for (int u = 0; u < kRankAhead; ++u)
+      if (c0 + u * kRankParts < whole) four((c0 + u * kRankParts) * 4, x[u]);
   }
-  for (int j = back; j < j1; ++j) before += key_of(ids[j], V) < key;
-  part[wave][lane] = before;
+  before += __shfl_xor(before, 16, 64);
+  before += __shfl_xor(before, 32, 64);
+  if ((threadIdx.x & 63) < kRankIds) share[threadIdx.x / 64][at] = before;
   __syncthreads();
-  if (wave == 0 && i < n) {
+  if (threadIdx.x < kRankIds && i < n) {
     int rank = 0;
 #pragma unroll
-    for (int w = 0; w < kRankThreads / 64; ++w) rank += part[w][lane];
+    for (int w = 0; w < kRankThreads / 64; ++w) rank += share[w][at];
+    for (int j = whole * 4; j < n; ++j) rank += key_of(ids[j], V) < key;
+    for (int j = own; j < i; ++j) rank += key_of(ids[j], V) == key;
     key_out[rank] = key;
     pos_out[rank] = i;
   }
@@ -149,9 +165,10 @@ rank_kernel(const int32_t* __restrict__ ids, int n, uint32_t V, uint32_t* __rest
 // moves every id to its place.
 constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits, kDigitsEach = kDigits / kSortThreads;
-// ROUNDS * kSortThreads ids a workgroup: 4 rounds up to kShortSort ids, 16 above
-// (more workgroups for the one, fewer counts to sum for the other).
-constexpr int64_t kShortSort = 1 << 18;
+// ROUNDS * kSortThreads ids a workgroup: 4 rounds up to kShortSort ids (more
+// workgroups), 16 above (fewer counts to sum).  A pass of 131072 ids takes 26 us
+// with 4 and 23 with 16, one of 1048576 ids 160 and 60; 32768 ids take 13 with 4.
+constexpr int64_t kShortSort = 1 << 16;
 
 struct SortPass {
   const int32_t* ids;       // first pass: the caller's ids (pos is the index itself)
@@ -330,8 +347,10 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int64_
 // Sums over tiles of the sorted tokens.  A run of equal ids inside a tile is
 // written to its row; one that came in from the tile before, or goes on in
 // the next, leaves its part sum (slot 0: came in, slot 1: begins here).  Bound
-// by memory: kAhead rows of dout are in flight for every chunk of columns (one
-// at a time, 32763 x 4 x 1024 bf16 148 us).
+// by memory: kAhead rows of dout are in flight for every chunk of columns: 32763
+// x 4 x 1024 bf16 112 us, 2.4 TB/s while the lines of the table's zeros are
+// still written back (one row at a time 148; 4 or 16 rows, tiles of 16 tokens or
+// two buffers of rows 107-119, no different).
 constexpr int kAhead = 8;
 constexpr int kLeastLanes = 2;   // log2: of a tile
 template <int IN>
@@ -458,8 +477,10 @@ tile_join_kernel(SumArgs a) {
   write_row<OUT>(a, key, c, sum);
 }
 
-// Ids up to this number take rank_kernel.
-constexpr int64_t kMostRanked = 16384;
+// Ids up to this number take rank_kernel: 8192 ids 13.8 us against 13 a pass of
+// the sort (two passes of a table of 32001 rows, three of 646400), 12288 25, 16384
+// 43.
+constexpr int64_t kMostRanked = 12288;
 
 int64_t sort_blocks(int64_t n) {
   const int64_t block = kSortThreads * (n <= kShortSort ? 4 : 16);
@@ -472,9 +493,12 @@ int sort_passes(int64_t V) {   // digits that hold the keys 0..V
   return passes;
 }
 
-// Sorted tokens of a tile: as many as leave enough tiles to fill the GPU.
+// Sorted tokens of a tile: long ones leave fewer part sums, short ones more
+// tiles to fill the GPU.  At 16384 tokens x 4 x 1024 columns, where the rule
+// changes, sums and joins take 45.6 us short and 44.4 long; at 8192 x 4 x 1024 26
+// and 42, at 16384 x 4 x 64 14 and 34.
 constexpr int kShortTile = 8, kLongTile = 32;
-int tile_tokens(int64_t n) { return n <= 4096 ? kShortTile : kLongTile; }
+int tile_tokens(int64_t n, int64_t dim) { return n * ((dim + 7) / 8) <= int64_t{1} << 21 ? kShortTile : kLongTile; }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t{255}; }
 
@@ -498,7 +522,7 @@ GradSpace carve_grad(void* ws, int64_t n, int64_t dim) {
     g.pos[i] = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(n) * 4));
   }
   if (!ranked) g.counts = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(sort_blocks(n)) * kDigits * 4));
-  const int64_t tile = tile_tokens(n), tiles = (n + tile - 1) / tile;
+  const int64_t tile = tile_tokens(n, dim), tiles = (n + tile - 1) / tile;
   g.part = reinterpret_cast<float*>(take(static_cast<size_t>(tiles) * 2 * dim * 4));
   g.bytes = used;
   return g;
@@ -565,7 +589,7 @@ hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout
   int sorted = 0;
   if (n <= kMostRanked) {
     const Fill f = zeros.next(1);
-    const int groups = static_cast<int>((n + 63) / 64);
+    const int groups = static_cast<int>((n + kRankIds - 1) / kRankIds);
     prof_stage("rank_kernel");
     launch_k(rank_kernel, dim3(groups + fill_groups(f, kRankThreads)), dim3(kRankThreads), 0, s, ids, static_cast<int>(n), static_cast<uint32_t>(V),
              g.key[0], g.pos[0], groups, f);
@@ -594,7 +618,7 @@ hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout
     }
   }
   const int log_lanes = std::max(row_lanes_log2(dim), kLeastLanes), lanes = 1 << log_lanes;
-  const int tile = tile_tokens(n);
+  const int tile = tile_tokens(n, dim);
   const int64_t tiles = (n + tile - 1) / tile, per = kThreads / lanes;
   const SumArgs a{g.key[sorted], g.pos[sorted], dout, dtable, g.part, n, dim, tiles, static_cast<uint32_t>(V), branches, log_lanes, tile,
                   accumulate ? 1 : 0, scale};
