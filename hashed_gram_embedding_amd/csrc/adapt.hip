@@ -97,8 +97,13 @@ __device__ __forceinline__ void each_adapter(int id, F f) {
 }
 
 // ---- h ----
-// A block of 32 tokens and one of the adapters in it a workgroup, whose NW
-// wavefronts take every NW-th 64 columns; 32 rows of A at a time.
+// The rows of A of all adapters in a block of 32 tokens, one adapter after
+// another, are taken 32 a workgroup (small ranks share one, large ones take
+// several), each with all of the block's tokens; what is stored is each token's
+// products with its own adapter.  NW wavefronts take every NW-th 64 columns.  A
+// chain of loads where tokens are few (256 tokens of 64 adapters of rank 16, 1024
+// columns: 7 us), the operands' way from the L2 where they are many (4096: 31 us;
+// with a workgroup for every adapter, whatever its rank, 46).
 template <int DT, int NW>
 __global__ void __launch_bounds__(NW * 64)
 adapter_rows_kernel(AdaptArgs a) {
@@ -107,195 +112,142 @@ adapter_rows_kernel(AdaptArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 31, lh = lane >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lr;
   const int id = adapter_of(a, t);
+  const int v = static_cast<int>(blockIdx.y) * 32 + lr, which = v / a.rank, r = v - which * a.rank;   // this lane's row
   int mine = -1;
-  each_adapter(id, [&](int one, int j) { mine = j == static_cast<int>(blockIdx.y) ? one : mine; });
-  if (mine < 0) return;   // fewer adapters in this block
-  const float scale = a.scale != nullptr ? a.scale[mine] : 1.0f;
+  each_adapter(id, [&](int one, int j) { mine = j == which ? one : mine; });
+  if (!__any(mine >= 0)) return;   // fewer rows in this block
+  const bool row = mine >= 0;
   const char* e = element<DT>(a.e, min(t, a.n_tok - 1) * a.K + lh * (kChunk / 2));
+  const char* ap = element<DT>(a.a, (static_cast<int64_t>(row ? mine : 0) * a.rank + r) * a.K + lh * (kChunk / 2));
+  f32x16_t acc;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int c = wave * kChunk; c < a.K; c += NW * kChunk) {
+    u32x4_t fa[Fr::kSteps], fe[Fr::kSteps];
+#pragma unroll
+    for (int s = 0; s < Fr::kSteps; ++s) {
+      fa[s] = load16(ap + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+      fe[s] = load16(e + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+    }
+#pragma unroll
+    for (int s = 0; s < Fr::kSteps; ++s) acc = multiply<DT>(row ? fa[s] : u32x4_t{0, 0, 0, 0}, fe[s], acc);
+  }
+#pragma unroll
+  for (int g = 0; g < 4; ++g) part[wave][g][lane] = f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+  __syncthreads();
+  // rows 8 wave + 4 lh .. + 3 of these 32, of the lane's token (of one adapter: a rank is a multiple of 8)
+  if (wave >= 4) return;
+  const int owner = __shfl(mine, wave * 8 + lh * 4, 64), column = __shfl(r, wave * 8 + lh * 4, 64);
+  if (owner < 0 || owner != id) return;
+  f32x4_t x = part[0][wave][lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) x += part[w][wave][lane];
+  x *= a.scale != nullptr ? a.scale[owner] : 1.0f;
   const int hc = h_columns(DT, a.rank);
-  for (int r0 = 0; r0 < a.rank; r0 += 32) {
-    const bool row = r0 + lr < a.rank;
-    const char* ap = element<DT>(a.a, (static_cast<int64_t>(mine) * a.rank + (row ? r0 + lr : 0)) * a.K + lh * (kChunk / 2));
-    f32x16_t acc;
+  if constexpr (DT == ENGRAM_BF16) {
+    uint16_t* h = static_cast<uint16_t*>(a.h) + t * hc + column;
+    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int c = wave * kChunk; c < a.K; c += NW * kChunk) {
-      u32x4_t fa[Fr::kSteps], fe[Fr::kSteps];
-#pragma unroll
-      for (int s = 0; s < Fr::kSteps; ++s) {
-        fa[s] = load16(ap + static_cast<int64_t>(c) * Fr::kSize + s * 16);
-        fe[s] = load16(e + static_cast<int64_t>(c) * Fr::kSize + s * 16);
-      }
-#pragma unroll
-      for (int s = 0; s < Fr::kSteps; ++s) acc = multiply<DT>(row ? fa[s] : u32x4_t{0, 0, 0, 0}, fe[s], acc);
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      const float d0 = x[2 * i] - __uint_as_float(hi[i] << 16), d1 = x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
+      lo[i] = pack_bf16x2(d0 == d0 ? d0 : 0.f, d1 == d1 ? d1 : 0.f);   // (an infinity's second part is 0)
     }
-    if (r0 > 0) __syncthreads();
-#pragma unroll
-    for (int g = 0; g < 4; ++g) part[wave][g][lane] = f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
-    __syncthreads();
-    // rows r0 + 8 wave + 4 lh .. + 3 of the lane's token
-    if (wave >= 4 || id != mine) continue;
-    f32x4_t x = part[0][wave][lane];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) x += part[w][wave][lane];
-    const int r = r0 + wave * 8 + lh * 4;
-    x *= scale;
-    if constexpr (DT == ENGRAM_BF16) {
-      if (r >= hc / 2) continue;
-      uint16_t* h = static_cast<uint16_t*>(a.h) + t * hc + r;
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        const float d0 = x[2 * i] - __uint_as_float(hi[i] << 16), d1 = x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
-        lo[i] = pack_bf16x2(d0 == d0 ? d0 : 0.f, d1 == d1 ? d1 : 0.f);   // (an infinity's second part is 0)
-      }
-      *reinterpret_cast<uint2*>(h) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(h + hc / 2) = make_uint2(lo[0], lo[1]);
-    } else {
-      if (r < a.rank) *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.h) + t * hc + r) = x;
-    }
+    *reinterpret_cast<uint2*>(h) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(h + hc / 2) = make_uint2(lo[0], lo[1]);
+  } else {
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.h) + t * hc + column) = x;
   }
 }
 
-// Adds B_a h_t to the sums of FB blocks of 32 outputs (from f0 on; rows past
-// n_out read as output 0's) x one block of 32 tokens: every `of`-th of the
-// adapters in it, from `first` on.  id: of the lane's token t.  A lane's sums
-// are its own token's: where the block holds other tokens they keep what they
-// had, so that an infinity or a NaN in one request's adapter stays with it.
-template <int DT, int FB>
-__device__ __forceinline__ void add_adapters(const AdaptArgs& a, int id, int64_t t, int64_t f0, int first, int of, f32x16_t (&acc)[FB]) {
+// Adds B_a h_t to the sums of a block of 32 outputs (from f0 on) x one of 32
+// tokens: every `of`-th of the adapters in it, from `first` on.  id: of the
+// lane's token t.  A lane's sums are its own token's: where the block holds other
+// tokens they keep what they had, so that an infinity or a NaN in one request's
+// adapter stays with it.
+template <int DT>
+__device__ __forceinline__ void add_adapters(const AdaptArgs& a, int id, int64_t t, int64_t f0, int first, int of, f32x16_t& acc) {
   constexpr int kStep = 2 * Frag<DT>::kVals;   // columns of B of a step
   const int lr = threadIdx.x & 31, lh = (threadIdx.x & 63) >> 5, hc = h_columns(DT, a.rank);
   const char* h = static_cast<const char*>(a.h) + min(t, a.n_tok - 1) * hc * Frag<DT>::kSize + lh * 16;
   each_adapter(id, [&](int one, int j) {
     if (j % of != first) return;
-    const bool mine = id == one;
-    auto add = [&](auto from, auto n, f32x16_t* sums) {   // blocks from .. from + n - 1
-      const char* b[n];
-#pragma unroll
-      for (int f = 0; f < n; ++f) {
-        const int64_t o = f0 + (from + f) * 32 + lr;
-        b[f] = element<DT>(a.b, (static_cast<int64_t>(one) * a.n_out + (o < a.n_out ? o : 0)) * a.rank) + lh * 16;
-      }
-      for (int r = 0; r < a.rank; r += kStep) {
-        const bool in = r + lh * Frag<DT>::kVals < a.rank;   // (a rank of 8, 24, ..: the last step's second half has no columns)
-        const int at = r * Frag<DT>::kSize;
-        const u32x4_t zero = {0, 0, 0, 0};
-        u32x4_t fb[n];
-#pragma unroll
-        for (int f = 0; f < n; ++f) {
-          fb[f] = load16(b[f] + (in ? at : 0));
-          if (!in) fb[f] = zero;
-        }
-        u32x4_t h0 = load16(h + at), h1 = zero;
-        if constexpr (DT == ENGRAM_BF16) h1 = load16(h + at + hc);
-        if (!in) h0 = h1 = zero;
-#pragma unroll
-        for (int f = 0; f < n; ++f) {
-          sums[f] = multiply<DT>(fb[f], h0, sums[f]);
-          if constexpr (DT == ENGRAM_BF16) sums[f] = multiply<DT>(fb[f], h1, sums[f]);
-        }
-      }
-    };
-    if (__all(mine)) {
-      add(std::integral_constant<int, 0>{}, std::integral_constant<int, FB>{}, acc);
-    } else {
-#pragma unroll
-      for (int f = 0; f < FB; ++f) {
-        f32x16_t sum = acc[f];
-        add(f, std::integral_constant<int, 1>{}, &sum);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[f][i] = mine ? sum[i] : acc[f][i];
-      }
+    const char* b = element<DT>(a.b, (static_cast<int64_t>(one) * a.n_out + f0 + lr) * a.rank) + lh * 16;
+    f32x16_t sum = acc;
+    for (int r = 0; r < a.rank; r += kStep) {
+      const bool in = r + lh * Frag<DT>::kVals < a.rank;   // (a rank of 8, 24, ..: the last step's second half has no columns)
+      const int at = r * Frag<DT>::kSize;
+      const u32x4_t zero = {0, 0, 0, 0};
+      u32x4_t fb = load16(b + (in ? at : 0)), h0 = load16(h + at), h1 = zero;
+      if constexpr (DT == ENGRAM_BF16) h1 = load16(h + at + hc);
+      if (!in) fb = h0 = h1 = zero;
+      sum = multiply<DT>(fb, h0, sum);
+      if constexpr (DT == ENGRAM_BF16) sum = multiply<DT>(fb, h1, sum);
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = id == one ? sum[i] : acc[i];
   });
 }
 
-// ---- few tokens, and float32 ----
-// TB x FB blocks of 32 tokens x 32 outputs a workgroup.  Its NW wavefronts
-// share the columns (every NW-th 64) and the adapters, operands straight from
-// memory into registers; their sums meet in LDS.
-template <int DT, int TB, int FB, int NW, typename OutT>
+// ---- few tokens ----
+// A block of 32 tokens x 32 outputs a workgroup.  Its NW wavefronts share the
+// columns (every NW-th 64) and the adapters, operands straight from memory into
+// registers; their sums meet in LDS.  One token, 1024 x 2048 in bf16: 4.8 us, a
+// chain of loads.
+template <int DT, int NW, typename OutT>
 __global__ void __launch_bounds__(NW * 64)
 adapt_small_kernel(AdaptArgs a, int tiles_f) {
   using Fr = Frag<DT>;
-  __shared__ f32x4_t part[NW][TB * FB][4][64];
+  __shared__ f32x4_t part[NW][4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 31, lh = lane >> 5;
-  const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * FB * 32, t0 = static_cast<int64_t>(blockIdx.x / tiles_f) * TB * 32;
-  const char *w[FB], *e[TB];
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * 32, t = static_cast<int64_t>(blockIdx.x / tiles_f) * 32 + lr;
+  const char* w = element<DT>(a.w, (f0 + lr) * a.K + lh * (kChunk / 2));
+  const char* e = element<DT>(a.e, min(t, a.n_tok - 1) * a.K + lh * (kChunk / 2));
+  const int id = adapter_of(a, t);
+  f32x16_t acc;
 #pragma unroll
-  for (int f = 0; f < FB; ++f) w[f] = element<DT>(a.w, (f0 + f * 32 + lr) * a.K + lh * (kChunk / 2));
-#pragma unroll
-  for (int b = 0; b < TB; ++b) e[b] = element<DT>(a.e, min(t0 + b * 32 + lr, a.n_tok - 1) * a.K + lh * (kChunk / 2));
-  int id[TB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b) id[b] = adapter_of(a, t0 + b * 32 + lr);
-  f32x16_t acc[TB][FB];
-#pragma unroll
-  for (int b = 0; b < TB; ++b)
-#pragma unroll
-    for (int f = 0; f < FB; ++f)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[b][f][i] = 0.f;
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
   for (int c = wave * kChunk; c < a.K; c += NW * kChunk) {
-    u32x4_t fw[FB][Fr::kSteps], fe[TB][Fr::kSteps];
+    u32x4_t fw[Fr::kSteps], fe[Fr::kSteps];
 #pragma unroll
     for (int s = 0; s < Fr::kSteps; ++s) {
-#pragma unroll
-      for (int f = 0; f < FB; ++f) fw[f][s] = load16(w[f] + static_cast<int64_t>(c) * Fr::kSize + s * 16);
-#pragma unroll
-      for (int b = 0; b < TB; ++b) fe[b][s] = load16(e[b] + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+      fw[s] = load16(w + static_cast<int64_t>(c) * Fr::kSize + s * 16);
+      fe[s] = load16(e + static_cast<int64_t>(c) * Fr::kSize + s * 16);
     }
 #pragma unroll
-    for (int s = 0; s < Fr::kSteps; ++s)
-#pragma unroll
-      for (int b = 0; b < TB; ++b)
-#pragma unroll
-        for (int f = 0; f < FB; ++f) acc[b][f] = multiply<DT>(fw[f][s], fe[b][s], acc[b][f]);
+    for (int s = 0; s < Fr::kSteps; ++s) acc = multiply<DT>(fw[s], fe[s], acc);
   }
+  add_adapters<DT>(a, id, t, f0, wave, NW, acc);
 #pragma unroll
-  for (int b = 0; b < TB; ++b) add_adapters<DT, FB>(a, id[b], t0 + b * 32 + lr, f0, wave, NW, acc[b]);
-#pragma unroll
-  for (int b = 0; b < TB; ++b)
-#pragma unroll
-    for (int f = 0; f < FB; ++f)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        part[wave][b * FB + f][g][lane] = f32x4_t{acc[b][f][4 * g], acc[b][f][4 * g + 1], acc[b][f][4 * g + 2], acc[b][f][4 * g + 3]};
+  for (int g = 0; g < 4; ++g) part[wave][g][lane] = f32x4_t{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
   __syncthreads();
-  if (wave >= 4) return;
+  if (wave >= 4 || t >= a.n_tok) return;
+  f32x4_t x = part[0][wave][lane];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) {
-    const int64_t t = t0 + b * 32 + lr;
-    if (t >= a.n_tok) continue;
-#pragma unroll
-    for (int f = 0; f < FB; ++f) {
-      const int blk = b * FB + f;
-      f32x4_t x = part[0][blk][wave][lane];
-#pragma unroll
-      for (int w = 1; w < NW; ++w) x += part[w][blk][wave][lane];
-      OutT* out = static_cast<OutT*>(a.out) + t * a.n_out + f0 + f * 32 + wave * 8 + lh * 4;
-      if constexpr (sizeof(OutT) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-      else *reinterpret_cast<f32x4_t*>(out) = x;
-    }
-  }
+  for (int w = 1; w < NW; ++w) x += part[w][wave][lane];
+  OutT* out = static_cast<OutT*>(a.out) + t * a.n_out + f0 + wave * 8 + lh * 4;
+  if constexpr (sizeof(OutT) == 2) *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  else *reinterpret_cast<f32x4_t*>(out) = x;
 }
 
-// ---- more tokens, bf16 ----
+// ---- more tokens ----
 // A tile of TF outputs x TT tokens a workgroup, WF x WT wavefronts; slices of
-// 64 columns of both operands go from memory straight into LDS, RING - 1 in
+// 128 bytes of both operands' rows go from memory straight into LDS, RING - 1 in
 // flight while one is multiplied.  A slice's row is 128 bytes, its 16-byte
 // chunk c at c ^ ((row >> 1) & 7), so that the rows a fragment read touches
 // spread over the banks.
 //
 // The adapters are more slices of the same loop: behind the columns of W come
-// 16 columns of B of every adapter that occurs among a wavefront's tokens, four
+// kColumns columns of B of every adapter that occurs among a wavefront's tokens, four
 // to a slice, kPer = 4 / WT for each row of wavefronts, multiplied with the
 // tokens' rows of h from registers.  Read from memory by the wavefronts
 // themselves, one adapter after another, they took 25 of 34 us at 256 tokens of
 // 64 adapters (1024 x 5120); in slices that one row of wavefronts filled after
-// the other, 31 of 41.
+// the other, 31 of 41.  Bound by the LDS reads of the operands: 32763 x 1024 x 5120
+// with 16 adapters 346-411 us (0.9-1.0 PFLOP/s), float32 8192 x 1024 x 5120 658 (the
+// matrix cores: 131 TFLOP/s).  Two workgroups of 128 x 128 share a CU, which
+// needs no more than 256 registers a lane: with 268, as the compiler chose by
+// itself, bf16 outputs took 44 us instead of 32 at 2048 tokens x 5120.
 constexpr int kXcds = 8, kBand = 8;
 
 // Waits until at most `younger` slices of LOADS instructions are in flight.
@@ -313,10 +265,11 @@ __device__ __forceinline__ void wait_slices(int younger) {
   }
 }
 
-template <int TF, int TT, int WF, int WT, int RING, typename OutT>
-__global__ void __launch_bounds__(WF * WT * 64)
+template <int DT, int TF, int TT, int WF, int WT, int RING, typename OutT>
+__global__ void __launch_bounds__(WF * WT * 64, 2)
 adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   constexpr int NT = WF * WT * 64, FB = TF / WF / 32, TB = TT / WT / 32;
+  constexpr int kSize = Frag<DT>::kSize, kVals = Frag<DT>::kVals, kColumns = 2 * kVals;   // kColumns of B: a part of a slice
   constexpr int kRowsAtOnce = NT / 8, kLoadsW = TF / kRowsAtOnce, kLoadsE = TT / kRowsAtOnce, kBuffer = (TF + TT) * 8;
   extern __shared__ u32x4_t lds[];   // [RING][TF + TT rows][8 chunks]; afterwards each wavefront's outputs
   constexpr int kPer = 4 / WT, kTokens = TT / WT;
@@ -331,23 +284,23 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   if (tile >= tiles_f * tiles_t) return;
   const int band = tile / (tiles_f * kBand), in_band = tile - band * tiles_f * kBand, bt = min(kBand, tiles_t - band * kBand);
   const int64_t f0 = static_cast<int64_t>(in_band / bt) * TF, t0 = (static_cast<int64_t>(band) * kBand + in_band % bt) * TT;
-  const int K = a.K, ksteps = K / 64;
+  const int K = a.K, ksteps = K * kSize / 128;
   const int r0 = tid >> 3, ch = (tid & 7) ^ ((r0 >> 1) & 7);
   // rows past the end read zeros
-  const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<ENGRAM_BF16>(a.w, f0 * K)), 0,
-                                                    static_cast<int>(min(int64_t{TF}, a.n_out - f0)) * K * 2, 0x00020000);
-  const auto re = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<ENGRAM_BF16>(a.e, t0 * K)), 0,
-                                                    static_cast<int>(min(int64_t{TT}, a.n_tok - t0)) * K * 2, 0x00020000);
+  const auto rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<DT>(a.w, f0 * K)), 0,
+                                                    static_cast<int>(min(int64_t{TF}, a.n_out - f0)) * K * kSize, 0x00020000);
+  const auto re = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(element<DT>(a.e, t0 * K)), 0,
+                                                    static_cast<int>(min(int64_t{TT}, a.n_tok - t0)) * K * kSize, 0x00020000);
   auto issue = [&](int kt) {
     u32x4_t* dst = lds + (kt % RING) * kBuffer + wave * 64;
 #pragma unroll
     for (int i = 0; i < kLoadsW; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(dst + i * NT), 16,
-                                               ((r0 + i * kRowsAtOnce) * K + ch * 8) * 2, kt * 128, 0, 0);
+                                               ((r0 + i * kRowsAtOnce) * K + ch * kVals) * kSize, kt * 128, 0, 0);
 #pragma unroll
     for (int i = 0; i < kLoadsE; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (__attribute__((address_space(3))) void*)(dst + TF * 8 + i * NT), 16,
-                                               ((r0 + i * kRowsAtOnce) * K + ch * 8) * 2, kt * 128, 0, 0);
+                                               ((r0 + i * kRowsAtOnce) * K + ch * kVals) * kSize, kt * 128, 0, 0);
   };
   const int64_t tw0 = t0 + wt * (TT / WT);
   int id[TB];
@@ -377,20 +330,20 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   int most = 0;
 #pragma unroll
   for (int g = 0; g < WT; ++g) most = max(most, counts[g]);
-  // The slices: 16 columns of B after 16 columns, each of kPer adapters of every row of wavefronts after kPer.
-  const int turns = (most + kPer - 1) / kPer, slices = ksteps + turns * ((a.rank + 15) / 16);
-  // This lane loads a half of one entry a slice (chunk ch), the `load_j`-th adapter of its row, columns load_r .. + 7.
+  // The slices: kColumns columns of B after kColumns columns, each of kPer adapters of every row of wavefronts after kPer.
+  const int turns = (most + kPer - 1) / kPer, slices = ksteps + turns * ((a.rank + kColumns - 1) / kColumns);
+  // This lane loads a half of one entry a slice (chunk ch), the `load_j`-th adapter of its row, columns load_r .. + kVals - 1.
   // Where there is none something valid is loaded and not used.  An entry's place is found a slice ahead.
   const int row_of = (ch >> 1) / kPer, in_row = counts[row_of];
-  int load_j = (ch >> 1) % kPer, load_r = (ch & 1) * 8;
+  int load_j = (ch >> 1) % kPer, load_r = (ch & 1) * kVals;
   auto entry = [&]() {
     const bool has = load_j < in_row && load_r < a.rank;
     const int64_t from = has ? static_cast<int64_t>(adapters[row_of][load_j]) * a.n_out : 0;
-    const char* src = element<ENGRAM_BF16>(a.b, from * a.rank + (has ? load_r : 0));
+    const char* src = element<DT>(a.b, from * a.rank + (has ? load_r : 0));
     load_j += kPer;
     if (load_j >= turns * kPer) {
       load_j -= turns * kPer;
-      load_r += 16;
+      load_r += kColumns;
     }
     return src;
   };
@@ -405,7 +358,7 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
     u32x4_t* dst = lds + (kt % RING) * kBuffer + wave * 64;
 #pragma unroll
     for (int l = 0; l < kLoadsW; ++l)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)element<ENGRAM_BF16>(from, static_cast<int64_t>(rows[l]) * a.rank),
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)element<DT>(from, static_cast<int64_t>(rows[l]) * a.rank),
                                        (__attribute__((address_space(3))) void*)(dst + l * NT), 16, 0, 0);
 #pragma unroll
     for (int l = 0; l < kLoadsE; ++l)   // (no rows: a slice has its number of loads all the same)
@@ -444,27 +397,32 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
 #pragma unroll
       for (int b = 0; b < TB; ++b)
 #pragma unroll
-        for (int f = 0; f < FB; ++f) acc[b][f] = multiply<ENGRAM_BF16>(fw[f], fe[b], acc[b][f]);
+        for (int f = 0; f < FB; ++f) acc[b][f] = multiply<DT>(fw[f], fe[b], acc[b][f]);
     }
   }
   const u32x4_t zero = {0, 0, 0, 0};
-  const int hc = h_columns(ENGRAM_BF16, a.rank);
+  const int hc = h_columns(DT, a.rank);
   f32x16_t none;
 #pragma unroll
   for (int i = 0; i < 16; ++i) none[i] = 0.f;
-  u32x4_t h0[TB], h1[TB];
-  int j = 0, r = -16;   // this wavefront's next adapter, its columns
+  auto both = [&](u32x4_t b, u32x4_t first, u32x4_t second, f32x16_t sums) {   // a block's sums and B with both parts of h
+    sums = multiply<DT>(b, first, sums);
+    if constexpr (DT == ENGRAM_BF16) sums = multiply<DT>(b, second, sums);
+    return sums;
+  };
+  u32x4_t h0[TB], h1[TB];   // (float32: h0 alone)
+  int j = 0, r = -kColumns;   // this wavefront's next adapter, its columns
   bool in = false;
   for (int kt = ksteps; kt < slices; ++kt) {
     begin(kt);
     if (j == 0) {
-      r += 16;
-      in = r + lh * 8 < a.rank;   // (a rank of 8, 24, ..: the last columns' second half is none)
+      r += kColumns;
+      in = r + lh * kVals < a.rank;   // (a rank of 8, 24, ..: the last columns' second half is none)
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        const char* h = static_cast<const char*>(a.h) + (min(tw0 + b * 32 + lr, a.n_tok - 1) * hc + r + lh * 8) * 2;
+        const char* h = static_cast<const char*>(a.h) + (min(tw0 + b * 32 + lr, a.n_tok - 1) * hc + r + lh * kVals) * kSize;
         h0[b] = load16(h);
-        h1[b] = load16(h + hc);
+        h1[b] = DT == ENGRAM_BF16 ? load16(h + hc) : zero;
         if (!in) h0[b] = h1[b] = zero;
       }
     }
@@ -491,24 +449,25 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
         if (!in) fw[p] = zero;
       }
       uint32_t top = 0;   // an exponent of ones carries into the sign's place
+      constexpr uint32_t kExponent = DT == ENGRAM_BF16 ? 0x7f807f80u : 0x7f800000u, kOne = DT == ENGRAM_BF16 ? 0x00800080u : 0x00800000u;
 #pragma unroll
       for (int p = 0; p < kPer; ++p)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) top |= (fw[p][x] & 0x7f807f80u) + 0x00800080u;
-      const bool odd = __any((top & 0x80008000u) != 0);
+        for (int x = 0; x < 4; ++x) top |= (fw[p][x] & kExponent) + kOne;
+      const bool odd = __any((top & (~kExponent & (kExponent + kOne))) != 0);
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
         if (!odd) {        // the other tokens' rows of h as zeros
 #pragma unroll
           for (int p = 0; p < kPer; ++p)
-            acc[b][f] = multiply<ENGRAM_BF16>(fw[p], mine[b][p] ? h1[b] : zero, multiply<ENGRAM_BF16>(fw[p], mine[b][p] ? h0[b] : zero, acc[b][f]));
+            acc[b][f] = both(fw[p], mine[b][p] ? h0[b] : zero, mine[b][p] ? h1[b] : zero, acc[b][f]);
         } else if (any[b]) {
           // an infinity or a NaN in B: a lane's sums are its own token's, it takes its adapter's product and no other's,
           // so that one request's bad adapter stays with it
           f32x16_t sum[kPer];
 #pragma unroll
           for (int p = 0; p < kPer; ++p)
-            sum[p] = multiply<ENGRAM_BF16>(fw[p], h1[b], multiply<ENGRAM_BF16>(fw[p], h0[b], p == 0 ? acc[b][f] : none));
+            sum[p] = both(fw[p], h0[b], h1[b], p == 0 ? acc[b][f] : none);
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float y = acc[b][f][x];
@@ -552,11 +511,11 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   }
 }
 
-template <int TF, int TT, int WF, int WT, int RING, typename OutT>
+template <int DT, int TF, int TT, int WF, int WT, int RING, typename OutT>
 hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
   constexpr int kOut = WF * WT * 32 * (TF / WF * static_cast<int>(sizeof(OutT)) + 16);
   constexpr int kLds = std::max(RING * (TF + TT) * 128, kOut);
-  auto* const fn = adapt_tile_kernel<TF, TT, WF, WT, RING, OutT>;
+  auto* const fn = adapt_tile_kernel<DT, TF, TT, WF, WT, RING, OutT>;
   static std::atomic<uint64_t> attr_set{0};   // > 64 KiB of dynamic LDS, raised once per device
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -573,26 +532,43 @@ hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
   return launch_error();
 }
 
-template <int DT, int TB, int FB, int NW, typename OutT>
+template <int DT, int NW, typename OutT>
 hipError_t launch_small(const AdaptArgs& a, hipStream_t s) {
-  const int tiles_f = a.n_out / (FB * 32);
-  const int64_t tiles = (a.n_tok + TB * 32 - 1) / (TB * 32) * tiles_f;
-  launch_k((adapt_small_kernel<DT, TB, FB, NW, OutT>), dim3(static_cast<unsigned>(tiles)), dim3(NW * 64), 0, s, a, tiles_f);
+  const int tiles_f = a.n_out / 32;
+  launch_k((adapt_small_kernel<DT, NW, OutT>), dim3(static_cast<unsigned>((a.n_tok + 31) / 32 * tiles_f)), dim3(NW * 64), 0, s, a, tiles_f);
   return launch_error();
 }
 
 template <typename OutT>
 hipError_t launch_product(const AdaptArgs& a, int dtype, hipStream_t s) {
   const int64_t t = a.n_tok, o = a.n_out;
+  // The adapters that 64 tokens may meet.  Each one's B is more columns for a tile, so many favour small tiles.
+  const int64_t spread = std::min<int64_t>({a.adapters, 64, (62 + a.per) / a.per + 1});
+  auto tiles = [&](int64_t side) { return (t + side - 1) / side * ((o + side - 1) / side); };
+  // workgroups of a tile by turns on the GPU's 256 CUs
+  auto rounds = [&](int64_t side) { return (tiles(side) + 255) / 256; };
   if (dtype == ENGRAM_F32) {
-    if constexpr (sizeof(OutT) == 4)
-      return ((t + 63) / 64) * (o / 64) < 512 ? launch_small<ENGRAM_F32, 1, 1, 8, float>(a, s) : launch_small<ENGRAM_F32, 2, 2, 4, float>(a, s);
+    if constexpr (sizeof(OutT) == 4) {
+      // Too few tiles of 64: 256 x 1024 x 1024 23 us so and 25 in tiles (64 adapters: 27 and 47), 64 x 1024 x 5120 36 and 25.
+      if (tiles(32) <= 256) return launch_small<ENGRAM_F32, 8, float>(a, s);
+      // A tile of 128 takes as long as three of 64: 512 x 1024 x 5120 66 us in tiles of 64, 74 of 128; 1024 x 1024 x 2048 44
+      // and 73, x 5120 108 and 134; 4096 x 1024 x 2048 163 and 136.
+      if (rounds(64) < 3 * rounds(128)) return launch_tile<ENGRAM_F32, 64, 64, 2, 2, 4, float>(a, s);
+      return launch_tile<ENGRAM_F32, 128, 128, 2, 2, 2, float>(a, s);
+    }
     return hipErrorInvalidValue;
   }
-  if (t <= 32) return launch_small<ENGRAM_BF16, 1, 1, 16, OutT>(a, s);
-  if (((t + 255) / 256) * ((o + 255) / 256) >= 256) return launch_tile<256, 256, 2, 4, 2, OutT>(a, s);
-  if (((t + 127) / 128) * ((o + 127) / 128) >= 256) return launch_tile<128, 128, 2, 2, 2, OutT>(a, s);
-  return launch_tile<64, 64, 2, 2, 4, OutT>(a, s);
+  const bool many = spread > 8;
+  // At 32 x 1024 x 20480 15 us so and 18 in tiles of 64; 64 adapters: 256 x 1024 x 2048 13 and 16.5, 128 x 1024 x 5120 18.4
+  // and 17.1; 4 adapters: 256 x 1024 x 1024 6 and 9, x 2048 10.1 and 9.4.
+  if (t <= 32 || tiles(32) <= (many ? 512 : 256)) return launch_small<ENGRAM_BF16, 16, OutT>(a, s);
+  // While the tiles of 64 all have their place on the chip: 1024 x 1024 x 2048 12 us (128: 16.5), 512 x 1024 x 5120 18 (15);
+  // 64 adapters: 512 x 1024 x 5120 34 (43), 2048 x 1024 x 5120 94 (90).
+  if (tiles(64) <= (many ? 1024 : 512)) return launch_tile<ENGRAM_BF16, 64, 64, 2, 2, 4, OutT>(a, s);
+  // Tiles of 256 where the last turn is mostly filled: 8192 x 1024 x 2048 37 us (128: 43), 32763 x 1024 x 5120 346 (409), 5120 x
+  // 1024 x 5120 68 (71), but 3584 x 1024 x 5120 61 (51); 64 adapters: 371 (268) at 8192 x 1024 x 5120.
+  if (many || tiles(256) * 4 < rounds(256) * 256 * 3) return launch_tile<ENGRAM_BF16, 128, 128, 2, 2, 2, OutT>(a, s);
+  return launch_tile<ENGRAM_BF16, 256, 256, 2, 4, 2, OutT>(a, s);
 }
 
 }  // namespace
@@ -611,9 +587,10 @@ hipError_t launch_project_adapted(const void* e, const void* w, int64_t n_tok, i
   if (adapters > 0) {
     // a block of 32 tokens meets at most so many requests, each with one adapter
     const int64_t most = std::min<int64_t>({32, adapters, (30 + per) / per + 1});
-    const dim3 grid(static_cast<unsigned>((n_tok + 31) / 32), static_cast<unsigned>(most));
+    const dim3 grid(static_cast<unsigned>((n_tok + 31) / 32), static_cast<unsigned>((most * rank + 31) / 32));
     prof_stage("adapter_rows_kernel");
-    // few workgroups: more wavefronts for the columns of each
+    // few workgroups: more wavefronts for the columns of each (bf16, 256 tokens of 16 adapters: 5.4 us with 16, 6.4 with 4;
+    // 2048: 18 and 14; float32, one wavefront's share longer: 64 tokens 10 with 8, 12.6 with 4)
     const bool few = n_tok <= 512;
     if (dtype == ENGRAM_F32) launch_k(few ? adapter_rows_kernel<ENGRAM_F32, 8> : adapter_rows_kernel<ENGRAM_F32, 4>, grid, dim3(few ? 512 : 256), 0, s, a);
     else launch_k(few ? adapter_rows_kernel<ENGRAM_BF16, 16> : adapter_rows_kernel<ENGRAM_BF16, 4>, grid, dim3(few ? 1024 : 256), 0, s, a);
