@@ -799,7 +799,8 @@ sample_kernel(SampleArgs a) {
 
   // Few entries stay (a small top_k): then a list holds them, and the rest is done on
   // the list.  Every wavefront has `each` lanes whose largest logits reach the
-  // smallest of their `each`-th largest ones, so top_k entries reach it.
+  // smallest of their `each`-th largest ones, so top_k entries reach it.  (top_k of 20 in a row of 32001: 14.2 us, 29.8
+  // by bins; of 100 in 2048 rows of 128000: 206 and 384.)
   int listed = -1;
   constexpr int kWaves = THREADS / 64;
   if (by_k && top_k <= 32 * kWaves && V >= 4 * THREADS) {
@@ -988,8 +989,12 @@ template <int DT>
 hipError_t launch_sample_dt(const SampleArgs& a, int64_t rows, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(rows));
   prof_stage("sample_tokens_kernel");
-  if (a.V <= 1024 * 4) launch_k((sample_kernel<DT, 256>), grid, dim3(256), 0, s, a);
-  else if (rows <= 256) launch_k((sample_kernel<DT, 1024>), grid, dim3(1024), 0, s, a);
+  // Threads: the passes over a row want many, the steps between them few, and several rows a CU hide each other's steps.
+  // us for 256 / 512 / 1024 threads, no filters and top_p: 2048 x 8192 33 / 51 / 117 and 63 / 84 / 179, x 32001 bf16 101 / 92 / 152
+  // and 169 / 142 / 244; 1 x 8192 7.6 / 9.6 / 14.3 and 17.4 / 17.3 / 21.8, x 32001 18.9 / 15.5 / 17.4 and 43 / 26 / 27; 256 x 65536
+  // - / 27 / 27 and - / 54 / 50, x 128000 - / 49 / 44 and - / 87 / 73; 1024 x 128000 - / 139 / 168 and - / 190 / 249.
+  if (a.V <= (rows > 256 ? 8192 : 4096)) launch_k((sample_kernel<DT, 256>), grid, dim3(256), 0, s, a);
+  else if (a.V > 65536 && rows <= 256) launch_k((sample_kernel<DT, 1024>), grid, dim3(1024), 0, s, a);
   else launch_k((sample_kernel<DT, 512>), grid, dim3(512), 0, s, a);
   return launch_error();
 }
