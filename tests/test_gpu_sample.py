@@ -172,3 +172,18 @@ def test_row_past_32_bits():
     assert torch.equal(tokens.long(), torch.minimum(at, V - 1 - at)) and torch.allclose(lp, torch.full_like(lp, -0.6931472))
     tokens, _ = eg.sample_tokens(x, u + 0.5, top_p=torch.full((260,), 0.75, device=DEV))
     assert torch.equal(tokens.long(), torch.maximum(at, V - 1 - at))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [4095, 4097, 8189, 8192, 8193])
+def test_many_rows(V, dtype):
+    """More rows than the GPU has places for, each with settings of its own."""
+    log(f"sample_tokens many rows {V} {dtype}")
+    S = 300
+    x, u = _logits(S, 1, V, dtype, V, masked=0.2)
+    g = np.random.default_rng(V)
+    t = np.where(g.random(S) < 0.1, 0.0, 0.3 + g.random(S)).astype(np.float32)
+    k = np.where(g.random(S) < 0.5, 0, g.integers(1, 400, S))
+    p = np.where(g.random(S) < 0.4, 1.0, g.random(S)).astype(np.float32)
+    m = np.where(g.random(S) < 0.6, 0.0, 0.3 * g.random(S)).astype(np.float32)
+    _check(x, u, t.tolist(), k.tolist(), p.tolist(), m.tolist())
