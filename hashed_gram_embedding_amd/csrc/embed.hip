@@ -18,6 +18,7 @@ namespace {
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+constexpr int64_t kL2Bytes = 32 << 20;   // 8 XCDs x 4 MiB
 
 // A row's columns go to the lanes in chunks of 8: the lanes of a row are the
 // power of two that covers its chunks, at most a workgroup; longer rows take
@@ -43,14 +44,19 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float (&f)[8]) {
   }
 }
 
-template <int DT>
+// PAST: lines that are not to stay in the L2.
+template <int DT, bool PAST = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&f)[8]) {
+  auto store = [](auto v, auto* q) {
+    if constexpr (PAST) __builtin_nontemporal_store(v, q);
+    else *q = v;
+  };
   if constexpr (DT == ENGRAM_BF16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack8(f);
+    store(__builtin_bit_cast(u32x4_t, pack8(f)), reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i));
   } else {
     f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i);
-    q[0] = f32x4_t{f[0], f[1], f[2], f[3]};
-    q[1] = f32x4_t{f[4], f[5], f[6], f[7]};
+    store(f32x4_t{f[0], f[1], f[2], f[3]}, q);
+    store(f32x4_t{f[4], f[5], f[6], f[7]}, q + 1);
   }
 }
 
@@ -67,9 +73,9 @@ struct EmbedArgs {
 };
 
 // One row of the table is read once and written M times.  Bound by memory: 32763
-// tokens x 4 x 1024 in bf16 50 us (5.8 TB/s); 256 x 1 x 1024 4 us, a launch
-// and two loads in a chain.
-template <int IN, int OUT>
+// tokens x 4 x 1024 in bf16 43 us (6.8 TB/s) with outputs stored past the L2 (PAST),
+// 51 through it; 256 x 1 x 1024 2.5 us, a launch and two loads in a chain, either way.
+template <int IN, int OUT, bool PAST>
 __global__ void __launch_bounds__(kThreads)
 embed_kernel(EmbedArgs a) {
   const int lanes = 1 << a.log_lanes;
@@ -84,7 +90,7 @@ embed_kernel(EmbedArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] *= a.scale;
     }
-    for (int m = 0; m < a.branches; ++m) store8<OUT>(a.out, (i * a.branches + m) * a.dim + c, f);
+    for (int m = 0; m < a.branches; ++m) store8<OUT, PAST>(a.out, (i * a.branches + m) * a.dim + c, f);
   }
 }
 
@@ -347,19 +353,23 @@ __device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int64_
 // Sums over tiles of the sorted tokens.  A run of equal ids inside a tile is
 // written to its row; one that came in from the tile before, or goes on in
 // the next, leaves its part sum (slot 0: came in, slot 1: begins here).  Bound
-// by memory: kAhead rows of dout are in flight for every chunk of columns: 32763
-// x 4 x 1024 bf16 112 us, 2.4 TB/s while the lines of the table's zeros are
-// still written back (one row at a time 148; 4 or 16 rows, tiles of 16 tokens or
-// two buffers of rows 107-119, no different).
+// by memory: kAhead rows of dout are in flight for every chunk of columns, and
+// where they are more than the L2 holds they are read past it (PAST), so that
+// the lines of the table's zeros, which the sorting launches have just written,
+// need not make room for them: 32763 x 4 x 1024 bf16 68 us (4.6 TB/s), through the
+// L2 112 (then one row at a time 148; 4 or 16 rows, tiles of 16 tokens or two
+// buffers of rows 107-119, no different).  The 0.5 MB of 509 x 256 float32 take
+// 5.9 us past the L2 and 4.8 through it.
 constexpr int kAhead = 8;
 constexpr int kLeastLanes = 2;   // log2: of a tile
 template <int IN>
 struct Chunk {   // 8 columns as stored
   u32x4_t x[IN == ENGRAM_BF16 ? 1 : 2];
+  template <bool PAST>
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + i * (IN == ENGRAM_BF16 ? 2 : 4));
-    x[0] = q[0];
-    if constexpr (IN == ENGRAM_F32) x[1] = q[1];
+    x[0] = PAST ? __builtin_nontemporal_load(q) : q[0];
+    if constexpr (IN == ENGRAM_F32) x[1] = PAST ? __builtin_nontemporal_load(q + 1) : q[1];
   }
   __device__ __forceinline__ float at(int k) const {
     if constexpr (IN == ENGRAM_BF16) return __uint_as_float(k & 1 ? x[0][k >> 1] & 0xffff0000u : x[0][k >> 1] << 16);
@@ -367,7 +377,7 @@ struct Chunk {   // 8 columns as stored
   }
 };
 
-template <int IN, int OUT, int TILE>
+template <int IN, int OUT, int TILE, bool PAST>
 __global__ void __launch_bounds__(kThreads)
 tile_sum_kernel(SumArgs a) {
   constexpr int kMost = (kThreads >> kLeastLanes) * TILE;   // sorted tokens of a workgroup
@@ -397,7 +407,7 @@ tile_sum_kernel(SumArgs a) {
     Chunk<IN> x[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      x[i].load(a.dout, pos[q] * step + b * a.dim + c);
+      x[i].template load<PAST>(a.dout, pos[q] * step + b * a.dim + c);
       if (i0 + i + 1 < items && ++b == a.branches) {   // (behind the last one it is loaded again)
         b = 0;
         ++q;
@@ -560,11 +570,12 @@ hipError_t launch_embed(const int32_t* ids, int64_t n, const void* table, int dt
   const int log_lanes = row_lanes_log2(dim);
   const int64_t per = kThreads >> log_lanes, most = (int64_t{1} << 23) * per;   // tokens of a launch (2^31 work-items)
   const int64_t row = branches * dim * (out_dtype == ENGRAM_BF16 ? 2 : 4);
+  const bool past = n * row > kL2Bytes;   // the next kernel will not find them there anyway
   for (int64_t i = 0; i < n; i += most) {
     const int64_t m = std::min(most, n - i);
     const EmbedArgs a{ids + i, table, static_cast<char*>(out) + i * row, m, V, dim, branches, log_lanes, scale};
     const hipError_t e = by_types(dtype, out_dtype, [&](auto in, auto to) {
-      launch_k((embed_kernel<decltype(in)::value, decltype(to)::value>), dim3(static_cast<unsigned>((m + per - 1) / per)), dim3(kThreads), 0, s, a);
+      launch_k(past ? embed_kernel<decltype(in)::value, decltype(to)::value, true> : embed_kernel<decltype(in)::value, decltype(to)::value, false>, dim3(static_cast<unsigned>((m + per - 1) / per)), dim3(kThreads), 0, s, a);
       return launch_error();
     });
     if (e != hipSuccess) return e;
@@ -623,9 +634,11 @@ hipError_t launch_embed_backward(const int32_t* ids, int64_t n, const void* dout
   const SumArgs a{g.key[sorted], g.pos[sorted], dout, dtable, g.part, n, dim, tiles, static_cast<uint32_t>(V), branches, log_lanes, tile,
                   accumulate ? 1 : 0, scale};
   prof_stage("tile_sum_kernel");
+  const bool past = n * branches * dim * (dtype == ENGRAM_BF16 ? 2 : 4) > kL2Bytes;
   e = by_types(dtype, out_dtype, [&](auto in, auto to) {
-    launch_k(tile == kShortTile ? tile_sum_kernel<decltype(in)::value, decltype(to)::value, kShortTile>
-                                : tile_sum_kernel<decltype(in)::value, decltype(to)::value, kLongTile>,
+    constexpr int I = decltype(in)::value, O = decltype(to)::value;
+    launch_k(tile == kShortTile ? (past ? tile_sum_kernel<I, O, kShortTile, true> : tile_sum_kernel<I, O, kShortTile, false>)
+                                : (past ? tile_sum_kernel<I, O, kLongTile, true> : tile_sum_kernel<I, O, kLongTile, false>),
              dim3(static_cast<unsigned>((tiles + per - 1) / per), static_cast<unsigned>((dim + lanes * 8 - 1) / (lanes * 8))), dim3(kThreads), 0, s, a);
     return launch_error();
   });
