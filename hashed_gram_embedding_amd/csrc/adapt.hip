@@ -402,9 +402,6 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   }
   const u32x4_t zero = {0, 0, 0, 0};
   const int hc = h_columns(DT, a.rank);
-  f32x16_t none;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) none[i] = 0.f;
   auto both = [&](u32x4_t b, u32x4_t first, u32x4_t second, f32x16_t sums) {   // a block's sums and B with both parts of h
     sums = multiply<DT>(b, first, sums);
     if constexpr (DT == ENGRAM_BF16) sums = multiply<DT>(b, second, sums);
@@ -464,16 +461,11 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
         } else if (any[b]) {
           // an infinity or a NaN in B: a lane's sums are its own token's, it takes its adapter's product and no other's,
           // so that one request's bad adapter stays with it
-          f32x16_t sum[kPer];
 #pragma unroll
-          for (int p = 0; p < kPer; ++p)
-            sum[p] = both(fw[p], h0[b], h1[b], p == 0 ? acc[b][f] : none);
+          for (int p = 0; p < kPer; ++p) {
+            const f32x16_t sum = both(fw[p], h0[b], h1[b], acc[b][f]);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float y = acc[b][f][x];
-#pragma unroll
-            for (int p = kPer - 1; p > 0; --p) y = mine[b][p] ? acc[b][f][x] + sum[p][x] : y;
-            acc[b][f][x] = mine[b][0] ? sum[0][x] : y;
+            for (int x = 0; x < 16; ++x) acc[b][f][x] = mine[b][p] ? sum[x] : acc[b][f][x];
           }
         }
       }

@@ -114,6 +114,50 @@ def test_bad_adapters_stay_with_their_requests(dtype, n):
     assert not torch.isfinite(got[which == 3]).any()
 
 
+# The smallest calls, ragged in tokens and outputs, that each kernel takes with few adapters or many.
+KERNELS = [("bf16", 257, 256, 100), ("bf16", 1001, 320, 200), ("bf16", 1701, 320, 1), ("bf16", 3001, 1088, 700), ("bf16", 4097, 1088, 1),
+           ("bf16", 3001, 5184, 1024), ("f32", 257, 256, 100), ("f32", 1001, 320, 1), ("f32", 1003, 320, 300), ("f32", 5001, 2112, 1),
+           ("f32", 5001, 2112, 900)]
+
+
+@pytest.mark.parametrize("K,rank", [(64, 8), (192, 24), (320, 128)])
+@pytest.mark.parametrize("dtype,n,out,per", KERNELS)
+def test_every_kernel(dtype, n, out, per, K, rank):
+    log(f"project_adapted kernels {dtype} {n} {out} {per} {K} {rank}")
+    e, w, ad, which = _inputs(n, K, out, rank, 30, per, dtype)
+    rows = np.unique(np.concatenate([np.arange(0, n, 61), np.arange(n - 40, n), np.arange(125, 135)]))
+    for out_t in ("f32", "bf16") if dtype == "bf16" else ("f32",):
+        whole = torch.full((n + 2, out), 7.0, device=DEV, dtype=TYPES[out_t])
+        got = eg.project_adapted(e, w, ad, which, per=per, out_dtype=out_t, out=whole[1:n + 1])
+        _check(got, e, w, ad, which, per, dtype, out_t, rows)
+        assert (whole[0] == 7).all() and (whole[-1] == 7).all()
+
+
+@pytest.mark.parametrize("adapters", [6, 40])
+@pytest.mark.parametrize("dtype,n,out", sorted({k[:3] for k in KERNELS}))
+def test_bad_adapters_in_every_kernel(dtype, n, out, adapters):
+    log(f"project_adapted isolation {dtype} {n} {out} {adapters}")
+    e, w, ad, which = _inputs(n, 128, out, 24, adapters, 1, dtype)
+    which.copy_(torch.arange(n, device=DEV) % (adapters + 1) - 1)
+    good = eg.project_adapted(e, w, ad, which)
+    ad.a[2, 3, 5] = float("nan")
+    ad.b[3] = float("inf")
+    ad.b[5, 7, 23] = float("nan")
+    ad.scale[4] = float("nan")
+    e[8] = float("inf")
+    got = eg.project_adapted(e, w, ad, which)
+    same = (which < 2) | (which > 5)
+    same[8] = False
+    assert torch.equal(got[same], good[same]) and torch.isfinite(good).all()
+    assert torch.isnan(got[which == 2]).all() and torch.isnan(got[which == 4]).all()
+    assert not torch.isfinite(got[which == 3]).any()
+    one = which == 5
+    one[8] = False
+    assert torch.isnan(got[one][:, 7]).all()
+    others = torch.arange(out, device=DEV) != 7
+    assert torch.equal(got[one][:, others], good[one][:, others])
+
+
 def test_scale_defaults_to_one():
     log("project_adapted scale")
     e, w, ad, which = _inputs(50, 64, 64, 8, 3, 1, "bf16")
