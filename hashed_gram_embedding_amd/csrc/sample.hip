@@ -708,6 +708,12 @@ __device__ __forceinline__ void order_list(Sh& sh, int n) {
   __syncthreads();
 }
 
+// Bound by the arithmetic of the weights in double precision and by the passes
+// over the row, the first from memory, the others from the L2: 2048 x 128000 bf16
+// 93 us greedy (5.6 TB/s), 272 without filters, 217 with top_k, 345 with top_p (one
+// or two passes more); a row of 32001 float32 9, 17, 21 and 25 us, a chain of
+// passes by one workgroup.  (1024 threads have 128 registers: 53 spilled, 60 bytes a
+// lane.)
 template <int DT, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 4)   // (four wavefronts a SIMD: two workgroups of 512 a CU)
 sample_kernel(SampleArgs a) {
