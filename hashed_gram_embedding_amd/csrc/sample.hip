@@ -459,8 +459,10 @@ struct Draw {
     }
   }
   __device__ __forceinline__ uint64_t look(float l) const { return weight.template look<Sh::kLooks>(l); }
+  // What the weights have to reach for top_p, at least one unit: a negative top_p keeps the first entry, as 0 does (and a
+  // negative number has no value as an unsigned one).
   __device__ __forceinline__ uint64_t share(float p, uint64_t all) const {
-    return max(static_cast<uint64_t>(ceil(static_cast<double>(p) * static_cast<double>(all))), uint64_t{1});
+    return static_cast<uint64_t>(fmax(ceil(static_cast<double>(p) * static_cast<double>(all)), 1.0));
   }
   // Those of a run whose bit of `which` is set into the list from `at` on, which holds `most` of them; *n counts them.
   // One LDS atomic a wavefront and run.

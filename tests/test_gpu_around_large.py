@@ -89,3 +89,15 @@ def test_sample_in_several_launches(per):
     assert torch.equal(tokens.view(-1).long(), last)
     weight = torch.where(last == top, torch.e, 1.0).double() / (torch.e + k - 1)
     assert (lp.view(-1).double() - weight.log()).abs().max() <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("top_p", [-0.125, -0.25, -1.0, -3e38, float("-inf"), 0.0])
+def test_sample_negative_top_p_in_a_long_row(top_p):
+    """Weights of more than 2^30 entries are multiples of 2^-31, so the largest is 2^31 units: a top_p of 0 and less keeps
+    the first entry, whatever the low bits of top_p times the total are."""
+    log(f"sample_tokens long row, top_p {top_p}")
+    V = (1 << 30) + 8
+    x = torch.full((1, V), float("-inf"), dtype=torch.bfloat16, device=DEV)
+    x[0, torch.tensor([5, 77, 1 << 20, V - 1], device=DEV)] = 1.0
+    tokens, lp = eg.sample_tokens(x, torch.tensor([0.9], device=DEV), top_p=torch.tensor([top_p], device=DEV), want_logprob=True)
+    assert tokens.tolist() == [5] and lp.tolist() == [0.0]
