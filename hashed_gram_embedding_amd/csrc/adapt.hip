@@ -147,9 +147,11 @@ adapter_rows_kernel(AdaptArgs a) {
   if constexpr (DT == ENGRAM_BF16) {
     uint16_t* h = static_cast<uint16_t*>(a.h) + t * hc + column;
     uint32_t hi[2], lo[2];
+    constexpr float kMost = 0x1.fep127f;   // bf16's largest: what lies behind it would round to an infinity, and is left to the second part
+    auto finite = [](float y) { return fabsf(y) > kMost && fabsf(y) < __builtin_inff() ? copysignf(kMost, y) : y; };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      hi[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      hi[i] = pack_bf16x2(finite(x[2 * i]), finite(x[2 * i + 1]));
       const float d0 = x[2 * i] - __uint_as_float(hi[i] << 16), d1 = x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
       lo[i] = pack_bf16x2(d0 == d0 ? d0 : 0.f, d1 == d1 ? d1 : 0.f);   // (an infinity's second part is 0)
     }

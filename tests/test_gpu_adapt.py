@@ -158,6 +158,24 @@ def test_bad_adapters_in_every_kernel(dtype, n, out, adapters):
     assert torch.equal(got[one][:, others], good[one][:, others])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 40, 600, 3001])
+def test_inner_products_past_the_largest_bf16(dtype, n):
+    """h = s A e between bf16's largest number and float32's: finite, and so is B h."""
+    log(f"project_adapted large h {dtype} {n}")
+    e, w, ad, which = _inputs(n, 64, 128, 8, 2, 1, dtype)
+    which.copy_(torch.arange(n, device=DEV) % 3 % 2)
+    e[:, 0], ad.a[:] = 1.0, 0.0
+    most = torch.finfo(torch.bfloat16).max
+    ad.a[0, 0, 0], ad.a[0, 7, 0], ad.a[1, 3, 0] = most, -most, -most
+    ad.b[:] = 0.0
+    ad.b[0, :, 0], ad.b[0, ::2, 7], ad.b[1, 1::2, 3] = 2.0 ** -120, 2.0 ** -121, 2.0 ** -120
+    ad.scale.copy_(torch.tensor([1.003, 1.0039]))   # bf16's halfway point to infinity is 1.00195 of its largest, float32's end 1.0039
+    got = eg.project_adapted(e, w, ad, which)
+    assert torch.isfinite(got).all()
+    _check(got, e, w, ad, which, 1, dtype, "f32")
+
+
 def test_scale_defaults_to_one():
     log("project_adapted scale")
     e, w, ad, which = _inputs(50, 64, 64, 8, 3, 1, "bf16")
