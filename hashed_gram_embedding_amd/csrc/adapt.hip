@@ -147,13 +147,13 @@ adapter_rows_kernel(AdaptArgs a) {
   if constexpr (DT == ENGRAM_BF16) {
     uint16_t* h = static_cast<uint16_t*>(a.h) + t * hc + column;
     uint32_t hi[2], lo[2];
-    constexpr float kMost = 0x1.fep127f;   // bf16's largest: what lies behind it would round to an infinity, and is left to the second part
-    auto finite = [](float y) { return fabsf(y) > kMost && fabsf(y) < __builtin_inff() ? copysignf(kMost, y) : y; };
+    // The first part stops at bf16's largest number: what is larger goes on in the second one, an infinity or a NaN too.
+    constexpr float kMost = 0x1.fep127f;
+    auto first_part = [](float y) { return __builtin_amdgcn_fmed3f(y, -kMost, kMost); };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      hi[i] = pack_bf16x2(finite(x[2 * i]), finite(x[2 * i + 1]));
-      const float d0 = x[2 * i] - __uint_as_float(hi[i] << 16), d1 = x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
-      lo[i] = pack_bf16x2(d0 == d0 ? d0 : 0.f, d1 == d1 ? d1 : 0.f);   // (an infinity's second part is 0)
+      hi[i] = pack_bf16x2(first_part(x[2 * i]), first_part(x[2 * i + 1]));
+      lo[i] = pack_bf16x2(x[2 * i] - __uint_as_float(hi[i] << 16), x[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
     }
     *reinterpret_cast<uint2*>(h) = make_uint2(hi[0], hi[1]);
     *reinterpret_cast<uint2*>(h + hc / 2) = make_uint2(lo[0], lo[1]);
