@@ -73,7 +73,12 @@ struct AdaptArgs {
   int32_t n_out;
   int32_t rank;
   int32_t adapters;
+  uint32_t first;         // workgroup of this launch
 };
+
+// A launch has fewer than 2^32 work-items (launch_k): workgroups, of up to 1024
+// threads, are launched so many at a time.
+constexpr int64_t kMostGroups = 1 << 21;
 
 // Columns of a row of h: whole matrix steps.
 __device__ __host__ __forceinline__ int h_columns(int dt, int rank) { return dt == ENGRAM_BF16 ? 2 * ((rank + 15) / 16 * 16) : rank; }
@@ -110,7 +115,7 @@ adapter_rows_kernel(AdaptArgs a) {
   using Fr = Frag<DT>;
   __shared__ f32x4_t part[NW][4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 31, lh = lane >> 5;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lr;
+  const int64_t t = static_cast<int64_t>(a.first + blockIdx.x) * 32 + lr;
   const int id = adapter_of(a, t);
   const int v = static_cast<int>(blockIdx.y) * 32 + lr, which = v / a.rank, r = v - which * a.rank;   // this lane's row
   int mine = -1;
@@ -202,7 +207,8 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
   using Fr = Frag<DT>;
   __shared__ f32x4_t part[NW][4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lr = lane & 31, lh = lane >> 5;
-  const int64_t f0 = static_cast<int64_t>(blockIdx.x % tiles_f) * 32, t = static_cast<int64_t>(blockIdx.x / tiles_f) * 32 + lr;
+  const unsigned block = a.first + blockIdx.x;
+  const int64_t f0 = static_cast<int64_t>(block % tiles_f) * 32, t = static_cast<int64_t>(block / tiles_f) * 32 + lr;
   const char* w = element<DT>(a.w, (f0 + lr) * a.K + lh * (kChunk / 2));
   const char* e = element<DT>(a.e, min(t, a.n_tok - 1) * a.K + lh * (kChunk / 2));
   const int id = adapter_of(a, t);
@@ -282,7 +288,7 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   // Workgroup i runs on XCD i % 8: each XCD walks tiles of its own, band by
   // band of token tiles, outputs outside, so that a band's rows stay in its L2
   // while W streams past.
-  const int per_xcd = gridDim.x / kXcds, tile = (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
+  const int per_xcd = gridDim.x / kXcds, tile = a.first + (blockIdx.x % kXcds) * per_xcd + blockIdx.x / kXcds;
   if (tile >= tiles_f * tiles_t) return;
   const int band = tile / (tiles_f * kBand), in_band = tile - band * tiles_f * kBand, bt = min(kBand, tiles_t - band * kBand);
   const int64_t f0 = static_cast<int64_t>(in_band / bt) * TF, t0 = (static_cast<int64_t>(band) * kBand + in_band % bt) * TT;
@@ -505,6 +511,20 @@ adapt_tile_kernel(AdaptArgs a, int tiles_f, int tiles_t) {
   }
 }
 
+// launch(arguments, number of workgroups) for all of them, each launch a stage.
+template <typename F>
+hipError_t launch_groups(AdaptArgs a, int64_t groups, const char* stage, F launch) {
+  if (groups > INT32_MAX) return hipErrorInvalidConfiguration;
+  for (int64_t first = 0; first < groups; first += kMostGroups) {
+    prof_stage(stage);
+    a.first = static_cast<uint32_t>(first);
+    launch(a, std::min(kMostGroups, groups - first));
+    const hipError_t e = launch_error();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int DT, int TF, int TT, int WF, int WT, int RING, typename OutT>
 hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
   constexpr int kOut = WF * WT * 32 * (TF / WF * static_cast<int>(sizeof(OutT)) + 16);
@@ -520,17 +540,18 @@ hipError_t launch_tile(const AdaptArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_release);
   }
-  const int tiles_f = (a.n_out + TF - 1) / TF, tiles_t = static_cast<int>((a.n_tok + TT - 1) / TT);
-  const int64_t tiles = static_cast<int64_t>(tiles_f) * tiles_t;
-  launch_k(fn, dim3(static_cast<unsigned>((tiles + kXcds - 1) / kXcds * kXcds)), dim3(WF * WT * 64), kLds, s, a, tiles_f, tiles_t);
-  return launch_error();
+  const int tiles_f = static_cast<int>((int64_t{a.n_out} + TF - 1) / TF), tiles_t = static_cast<int>((a.n_tok + TT - 1) / TT);
+  return launch_groups(a, static_cast<int64_t>(tiles_f) * tiles_t, "project_adapted_kernel", [&](const AdaptArgs& b, int64_t groups) {
+    launch_k(fn, dim3(static_cast<unsigned>((groups + kXcds - 1) / kXcds * kXcds)), dim3(WF * WT * 64), kLds, s, b, tiles_f, tiles_t);
+  });
 }
 
 template <int DT, int NW, typename OutT>
 hipError_t launch_small(const AdaptArgs& a, hipStream_t s) {
   const int tiles_f = a.n_out / 32;
-  launch_k((adapt_small_kernel<DT, NW, OutT>), dim3(static_cast<unsigned>((a.n_tok + 31) / 32 * tiles_f)), dim3(NW * 64), 0, s, a, tiles_f);
-  return launch_error();
+  return launch_groups(a, (a.n_tok + 31) / 32 * tiles_f, "project_adapted_kernel", [&](const AdaptArgs& b, int64_t groups) {
+    launch_k((adapt_small_kernel<DT, NW, OutT>), dim3(static_cast<unsigned>(groups)), dim3(NW * 64), 0, s, b, tiles_f);
+  });
 }
 
 template <typename OutT>
@@ -577,21 +598,21 @@ hipError_t launch_project_adapted(const void* e, const void* w, int64_t n_tok, i
   if (n_tok == 0) return hipSuccess;
   per = std::min(per, n_tok);
   const AdaptArgs a{e, w, lora_a, lora_b, scale, which, ws, out, n_tok, static_cast<uint32_t>(per), static_cast<int32_t>(d_mem),
-                    static_cast<int32_t>(n_out), rank, adapters};
+                    static_cast<int32_t>(n_out), rank, adapters, 0};
   if (adapters > 0) {
     // a block of 32 tokens meets at most so many requests, each with one adapter
     const int64_t most = std::min<int64_t>({32, adapters, (30 + per) / per + 1});
-    const dim3 grid(static_cast<unsigned>((n_tok + 31) / 32), static_cast<unsigned>((most * rank + 31) / 32));
-    prof_stage("adapter_rows_kernel");
+    const unsigned rows = static_cast<unsigned>((most * rank + 31) / 32);
     // few workgroups: more wavefronts for the columns of each (bf16, 256 tokens of 16 adapters: 5.4 us with 16, 6.4 with 4;
     // 2048: 18 and 14; float32, one wavefront's share longer: 64 tokens 10 with 8, 12.6 with 4)
     const bool few = n_tok <= 512;
-    if (dtype == ENGRAM_F32) launch_k(few ? adapter_rows_kernel<ENGRAM_F32, 8> : adapter_rows_kernel<ENGRAM_F32, 4>, grid, dim3(few ? 512 : 256), 0, s, a);
-    else launch_k(few ? adapter_rows_kernel<ENGRAM_BF16, 16> : adapter_rows_kernel<ENGRAM_BF16, 4>, grid, dim3(few ? 1024 : 256), 0, s, a);
-    const hipError_t r = launch_error();
+    const hipError_t r = launch_groups(a, (n_tok + 31) / 32, "adapter_rows_kernel", [&](const AdaptArgs& b, int64_t groups) {
+      const dim3 grid(static_cast<unsigned>(groups), rows);
+      if (dtype == ENGRAM_F32) launch_k(few ? adapter_rows_kernel<ENGRAM_F32, 8> : adapter_rows_kernel<ENGRAM_F32, 4>, grid, dim3(few ? 512 : 256), 0, s, b);
+      else launch_k(few ? adapter_rows_kernel<ENGRAM_BF16, 16> : adapter_rows_kernel<ENGRAM_BF16, 4>, grid, dim3(few ? 1024 : 256), 0, s, b);
+    });
     if (r != hipSuccess) return r;
   }
-  prof_stage("project_adapted_kernel");
   return out_dtype == ENGRAM_BF16 ? launch_product<uint16_t>(a, dtype, s) : launch_product<float>(a, dtype, s);
 }
 

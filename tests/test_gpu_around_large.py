@@ -71,6 +71,61 @@ def test_project_adapted_past_32_bits(dtype, n, K, out, out_t):
     assert (np.abs(_f64(got[rows]) - ref) <= tol).all()
 
 
+def _check_rows(got, e, w, ad, which, out_t):
+    K = e.shape[1]
+    ref, size, carried = plain.project_adapted(_f64(e), _f64(w), _f64(ad.a), _f64(ad.b), None, which.cpu().numpy())
+    tol = (K + ad.rank + 2) * UNIT * size + 2.0 ** -17 * carried + (2.0 ** -8 * np.abs(ref) if out_t == "bf16" else 0.0)
+    assert (np.abs(_f64(got) - ref) <= tol).all()
+
+
+def test_project_adapted_of_many_tokens():
+    """More workgroups than one launch has work-items for: 2^20 tokens again and again, and the first ones once more."""
+    log("project_adapted of 2^29 tokens")
+    torch.cuda.empty_cache()
+    n, again, turns, K = 33, 1 << 20, 512, 64
+    g = torch.Generator(device=DEV).manual_seed(29)
+    bf16 = torch.bfloat16
+    e = torch.empty(turns * again + n, K, dtype=bf16, device=DEV)
+    which = torch.empty(turns * again + n, dtype=torch.int32, device=DEV)
+    e[:again] = torch.randn(again, K, generator=g, device=DEV)
+    which[:again] = torch.randint(-1, 3, (again,), generator=g, device=DEV)
+    for t in (e, which):
+        t[again:turns * again].view(turns - 1, again, *t.shape[1:]).copy_(t[None, :again])
+        t[turns * again:] = t[:n]
+    w = (torch.randn(64, K, generator=g, device=DEV) / 8).to(bf16)
+    ad = eg.Adapters((torch.randn(3, 8, K, generator=g, device=DEV) / 8).to(bf16), torch.randn(3, 64, 8, generator=g, device=DEV).to(bf16))
+    got = eg.project_adapted(e, w, ad, which, out_dtype="bf16")
+    rows = torch.arange(0, again, 4099, device=DEV)
+    _check_rows(got[rows], e[rows], w, ad, which[rows], "bf16")
+    for i in range(1, turns):
+        assert torch.equal(got[i * again:(i + 1) * again], got[:again]), i
+    assert torch.equal(got[turns * again:], got[:n])
+
+
+@pytest.mark.parametrize("out_t", ["f32", "bf16"])
+def test_project_adapted_of_many_outputs(out_t):
+    """2^27 outputs and more of few tokens: rows of W and B again and again."""
+    log(f"project_adapted of 2^27 outputs {out_t}")
+    torch.cuda.empty_cache()
+    more, again, turns, K, n = 64, 1 << 20, 128, 64, 3
+    g = torch.Generator(device=DEV).manual_seed(27)
+    bf16 = torch.bfloat16
+    out = turns * again + more
+    w, b = torch.empty(out, K, dtype=bf16, device=DEV), torch.empty(1, out, 8, dtype=bf16, device=DEV)
+    for t in (w, b[0]):
+        t[:again] = torch.randn(again, t.shape[1], generator=g, device=DEV) / 8
+        t[again:turns * again].view(turns - 1, again, -1).copy_(t[None, :again])
+        t[turns * again:] = t[:more]
+    ad = eg.Adapters((torch.randn(1, 8, K, generator=g, device=DEV) / 8).to(bf16), b)
+    e = torch.randn(n, K, generator=g, device=DEV).to(bf16)
+    which = torch.tensor([0, -1, 0], dtype=torch.int32, device=DEV)
+    got = eg.project_adapted(e, w, ad, which, out_dtype=out_t)
+    _check_rows(got[:, :again:4099], e, w[:again:4099], eg.Adapters(ad.a, b[:, :again:4099].contiguous()), which, out_t)
+    for i in range(1, turns):
+        assert torch.equal(got[:, i * again:(i + 1) * again], got[:, :again]), i
+    assert torch.equal(got[:, turns * again:], got[:, :more])
+
+
 @pytest.mark.parametrize("per", [1, 5, 1 << 20, (1 << 21) + 9])
 def test_sample_in_several_launches(per):
     """A launch takes 2^21 rows: more of them, with settings of one row, of a few, and of more rows than a launch's."""
