@@ -20,6 +20,7 @@
 #include "device_util.h"
 #include "engram_internal.h"
 #include "lanes_device.h"
+#include "sample_values.h"
 
 namespace engram {
 namespace {
@@ -59,11 +60,8 @@ __device__ __forceinline__ double table_entry(int j) { return exp2(j * (1.0 / kT
 // one, 60 powers below the largest weight, holds weights of 0.
 constexpr int kSteps = 60 * kTable;
 
-// bf16 logits take few values: the weights of those of kExponents powers of two,
-// up to the row's largest, lie in LDS (both signs), and an entry's weight is
-// one read.
-constexpr int kExponents = 15, kValues = kExponents << 7;
-constexpr uint32_t kFirstBase = (127 + 7) * 128 - kValues;   // of rows whose largest logit is below 128 in magnitude
+// The weights of a bf16 row's table of values (sample_values.h) lie in LDS, and
+// an entry's weight is one read.
 
 struct Weight {
   double top, a;         // a: kTable log2(e) / T
@@ -109,9 +107,10 @@ struct Weight {
     if (at < kValues) atomicAdd(&counts[at + (bits >> 15) * kValues], 1u);
     else if (l > -__builtin_inff()) f(l);
   }
+  // zeros: the largest logit is 0, and so are most others.
   template <int THREADS>
-  __device__ __forceinline__ void form_values(float row_top) {
-    base = max((__float_as_uint(row_top) >> 23 & 0xffu) * 128 + 128 - kValues, kFirstBase);
+  __device__ __forceinline__ void form_values(float row_top, bool zeros) {
+    base = first_value(__float_as_uint(row_top) >> 23 & 0xffu, zeros);
     for (int i = threadIdx.x; i < 2 * kValues; i += THREADS) {
       const uint32_t bits = (base + (i < kValues ? i : i - kValues)) | (i < kValues ? 0 : 0x8000);
       const float l = __uint_as_float(bits << 16);
@@ -920,7 +919,14 @@ sample_kernel(SampleArgs a) {
     if (threadIdx.x == 0) write(static_cast<uint32_t>(found >> 32), d.place.logit(found << 32), total);
   } else {
     // Sums of a wavefront's part of the row each, and of the entries behind the quads.
-    if constexpr (Sh::kLooks) d.weight.template form_values<THREADS>(top);
+    if constexpr (Sh::kLooks) {
+      // A row whose largest is 0 holds logits less their largest, or little but zeros, which are in the table of the
+      // smallest magnitudes alone; its first entries tell (it is longer than THREADS).  2048 x 128000 without filters,
+      // logits less their largest and zeros: 252 us and 430 by the table up to 128, 435 and 251 by the other.
+      bool zeros = false;
+      if (top == 0.f) zeros = 2 * __syncthreads_count(at_index(threadIdx.x) == 0.f) > THREADS;
+      d.weight.template form_values<THREADS>(top, zeros);
+    }
     bool summed = false;
     if (by_k) cut_row<false, false>(d, top_k, 0.f);
     counted = counted && d.weight.base == kFirstBase && sh.few_n <= kOthers;

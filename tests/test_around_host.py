@@ -3,6 +3,8 @@ pointers that never reach a GPU), workspace sizes, refusals of the binding, and
 pins of the tests' own plain forms."""
 import ctypes
 import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -255,3 +257,16 @@ def test_plain_gradient_and_adapters_by_hand():
     out, _, _ = plain.project_adapted(np.array([[1.0, 2.0], [1.0, 2.0]]), np.array([[1.0, 1.0]]), np.array([[[3.0, 0.0]]]),
                                       np.array([[[5.0]]]), [2.0], [0, -1])
     assert out.tolist() == [[3.0 + 2 * 5 * 3], [3.0]]
+
+
+def test_values_of_a_row_on_the_host(tmp_path):
+    """Which bf16 values a row's table of weights holds, for every exponent of its largest logit."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = tmp_path / "sample_values_host"
+    subprocess.run([cxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I", os.path.join(os.path.dirname(here), "hashed_gram_embedding_amd", "csrc"),
+                    os.path.join(here, "native", "sample_values_host.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "all passed" in r.stdout, r.stdout + r.stderr

@@ -187,3 +187,30 @@ def test_many_rows(V, dtype):
     p = np.where(g.random(S) < 0.4, 1.0, g.random(S)).astype(np.float32)
     m = np.where(g.random(S) < 0.6, 0.0, 0.3 * g.random(S)).astype(np.float32)
     _check(x, u, t.tolist(), k.tolist(), p.tolist(), m.tolist())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5003, 70001])
+def test_rows_up_to_zero(V, dtype):
+    """Logits less their largest, rows of zeros of both signs (all of the row, more and less than half of it), and rows
+    whose largest is tiny, below the smallest normal number or far below zero."""
+    log(f"sample_tokens rows up to zero {dtype} {V}")
+    x, u = _logits(12, 1, V, dtype, V, spread=2.0, masked=0.05)
+    x = (x.float() - x.float().amax(-1, keepdim=True)).to(TYPES[dtype])
+    at = torch.arange(V, device=DEV)
+    x[1] = 0.0
+    x[2] = -0.0
+    x[3, 0, at % 3 > 0] = 0.0
+    x[4, 0, at % 3 == 0] = -0.0
+    x[5] = torch.where(at % 2 == 0, 0.0, -0.0)
+    x[6, 0, 17] = 2.0 ** -126
+    x[7] = torch.where(x[7] == 0, 2.0 ** -115, x[7].float())
+    x[8] = torch.where(at % 5 == 0, 0.0, -(at % 7).float() * 2.0 ** -112)
+    x[9] -= 300.0
+    x[10] = torch.where(at % 3 == 0, 0.0, 2.0 ** -9)
+    x[11] = torch.where(at == V - 2, 0.0, float("-inf"))
+    S = x.shape[0]
+    _check(x, u)
+    _check(x, u, p=[0.9] * S)
+    _check(x, u, k=[1500] * S)
+    _check(x, u, t=[0.7] * S, k=[3000] * S, p=[0.83] * S, m=[0.01] * S)
