@@ -263,8 +263,9 @@ struct Row {
   }
 };
 
-// What a workgroup of THREADS keeps in LDS: two of 512 fit a CU; a row of a
-// workgroup of 256 (4096 entries at most) always fits its list.
+// What a workgroup of THREADS keeps in LDS: two of 512 fit a CU.  A list need
+// not hold a whole row, in no workgroup (one of 256 takes rows of up to 8192
+// entries, its list 5120): entries that do not fit are read from the row again.
 template <int DT, int THREADS>
 struct SampleShared {
   static constexpr bool kLooks = DT == ENGRAM_BF16 && THREADS > 256;   // weights of values

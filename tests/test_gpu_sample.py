@@ -214,3 +214,27 @@ def test_rows_up_to_zero(V, dtype):
     _check(x, u, p=[0.9] * S)
     _check(x, u, k=[1500] * S)
     _check(x, u, t=[0.7] * S, k=[3000] * S, p=[0.83] * S, m=[0.01] * S)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [8192, 7001])
+def test_equal_logits_of_many_rows(V, dtype):
+    """More than 256 rows of few different logits, up to 8192 entries each: more equal ones than the smallest workgroup's
+    list holds, cut by a top_k that is collected and one that is binned, by top_p, and by both."""
+    log(f"sample_tokens equal logits of many rows {dtype} {V}")
+    S = 260
+    g = torch.Generator(device=DEV).manual_seed(V)
+    often = torch.rand(S, 1, 1, generator=g, device=DEV)             # of the largest: few of a row to all of it
+    x = torch.where(torch.rand(S, 1, V, generator=g, device=DEV) < often, 1.5,
+                    torch.randint(0, 2, (S, 1, V), generator=g, device=DEV).float()).to(TYPES[dtype])
+    x[7] = 0.75
+    assert int((x == 1.5).sum(-1).max()) > 5120
+    u = torch.rand(S, 1, generator=g, device=DEV)
+    r = np.random.default_rng(V)
+    small, large = 2 * r.integers(0, 60, S) + 1, 2 * r.integers(100, V // 2, S) + 1
+    p = (0.05 + 0.9 * r.random(S)).tolist()
+    _check(x, u, k=small.tolist())
+    _check(x, u, k=large.tolist())
+    _check(x, u, p=p)
+    _check(x, u, k=large.tolist(), p=p)
+    _check(x, u, m=[0.3, 0.7] * (S // 2))
