@@ -190,3 +190,40 @@ def test_hashed_table_gradient():
     table = L.rows.view(total, dim)
     e = eg.gather(z, L).view(*z.shape, 1, dim)
     assert torch.equal(eg.embed(rows, table), e)
+
+
+@pytest.mark.parametrize("n", [17000, 70001])
+@pytest.mark.parametrize("V", [511, 512, (1 << 18) - 1, 1 << 18, (1 << 27) - 1, 1 << 27])
+def test_gradient_ends_of_digits(V, n):
+    """Tables at the ends of the sort's 9-bit digits, where the padding's key takes one more, for both lengths of its
+    workgroups' shares: every row, in whole numbers."""
+    log(f"embed_backward ends of digits V={V} n={n}")
+    g = torch.Generator(device=DEV).manual_seed(V + n)
+    ids = torch.randint(0, V, (n,), generator=g, device=DEV, dtype=torch.int32)
+    ids[::5] = V - 1 - ids[::5] % 3
+    ids[:6] = torch.tensor([V - 1, 0, V, -1, 2 ** 31 - 1, V - 1], dtype=torch.int32)
+    ids[-2:] = torch.tensor([V, V - 1], dtype=torch.int32)
+    dout = torch.randint(-8, 9, (n, 1, 8), generator=g, device=DEV).float()
+    at = torch.where((ids >= 0) & (ids < V), ids, V).long()
+    ref = torch.zeros(V + 1, 8, device=DEV).index_add_(0, at, dout[:, 0])
+    assert torch.equal(eg.embed_backward(ids, dout, V), ref[:V])
+
+
+@pytest.mark.parametrize("n", [12284, 12288, 12292, 65536, 65540, 131076])
+@pytest.mark.parametrize("V", [40000, 1 << 18, 1 << 27])
+def test_gradient_adds_in_the_order_of_positions(n, V):
+    """Every id four times, anywhere: the bits of their sum in the order of their positions, on both sides of the numbers
+    of ids at which the sort changes."""
+    log(f"embed_backward order n={n} V={V}")
+    g = torch.Generator(device=DEV).manual_seed(n)
+    different = n // 4
+    rows = torch.arange(different, device=DEV) * (V // different)
+    ids = rows.repeat_interleave(4)[torch.randperm(n, generator=g, device=DEV)]
+    dout = torch.randn(n, 1, 8, generator=g, device=DEV) * torch.exp2(torch.randint(-12, 13, (n, 1, 1), generator=g, device=DEV).float())
+    d = dout[torch.argsort(ids, stable=True), 0].view(different, 4, 8)
+    ref = torch.zeros(V, 8, device=DEV)
+    ref[rows] = ((d[:, 0] + d[:, 1]) + d[:, 2]) + d[:, 3]
+    other = torch.zeros(V, 8, device=DEV)
+    other[rows] = ((d[:, 3] + d[:, 2]) + d[:, 1]) + d[:, 0]
+    assert not torch.equal(ref, other)
+    assert torch.equal(eg.embed_backward(ids.int(), dout, V), ref)
