@@ -108,7 +108,10 @@ __device__ __forceinline__ void each_adapter(int id, F f) {
 // products with its own adapter.  NW wavefronts take every NW-th 64 columns.  A
 // chain of loads where tokens are few (256 tokens of 64 adapters of rank 16, 1024
 // columns: 7 us), the operands' way from the L2 where they are many (4096: 31 us;
-// with a workgroup for every adapter, whatever its rank, 46).
+// with a workgroup for every adapter, whatever its rank, 46).  A block's tokens meet
+// all of its adapters' rows, one share of the products is kept: 32763 tokens of 64
+// adapters take 197 us at rank 16 and 739 at rank 64 with an adapter a token, 16 and
+// 36 with one for every 256.
 template <int DT, int NW>
 __global__ void __launch_bounds__(NW * 64)
 adapter_rows_kernel(AdaptArgs a) {
@@ -252,8 +255,14 @@ adapt_small_kernel(AdaptArgs a, int tiles_f) {
 // themselves, one adapter after another, they took 25 of 34 us at 256 tokens of
 // 64 adapters (1024 x 5120); in slices that one row of wavefronts filled after
 // the other, 31 of 41.  Bound by the LDS reads of the operands: 32763 x 1024 x 5120
-// with 16 adapters 346-411 us (0.9-1.0 PFLOP/s), float32 8192 x 1024 x 5120 658 (the
-// matrix cores: 131 TFLOP/s).  Two workgroups of 128 x 128 share a CU, which
+// with 16 adapters, bf16 outputs, 420 us (median of 60 calls in three series, 380 to
+// 526 as the clock goes; the library's product without adapters, in turn with it, 285
+// and 273 to 394), float32 8192 x 1024 x 5120 658 (the matrix cores: 131 TFLOP/s).
+// Every adapter that occurs among a wavefront's tokens costs as many matrix
+// instructions as if all of them had it, so spread ones cost by their number and
+// rank: 32763 x 1024 x 2048 with 64 adapters, an adapter a token and one for every 256,
+// rank 16 444 and 166 us, rank 64 1736 and 195; float32, 4096 tokens, rank 64, 787 and
+// 158.  Two workgroups of 128 x 128 share a CU, which
 // needs no more than 256 registers a lane: with 268, as the compiler chose by
 // itself, bf16 outputs took 44 us instead of 32 at 2048 tokens x 5120.
 constexpr int kXcds = 8, kBand = 8;

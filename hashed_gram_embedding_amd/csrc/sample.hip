@@ -62,7 +62,6 @@ constexpr int kSteps = 60 * kTable;
 
 // The weights of a bf16 row's table of values (sample_values.h) lie in LDS, and
 // an entry's weight is one read.
-
 struct Weight {
   double top, a;         // a: kTable log2(e) / T
   int fraction;
@@ -100,7 +99,9 @@ struct Weight {
     if (at >= kValues) w = l == -__builtin_inff() ? static_cast<uint64_t>(kSteps >> bin_shift) << 52 : formed(l);
     return w;
   }
-  // An entry counted by value; f(l) for one of another magnitude.
+  // An entry counted by value; f(l) for one of another magnitude.  Lanes that count one value wait for one another: 2048 x
+  // 128000 with top_p take 318 us of spread logits, 2500 where half of them are zeros, 3060 of zeros alone (a row with more
+  // than kOthers entries below the table's magnitudes is counted a second time).
   template <typename F>
   static __device__ __forceinline__ void count(uint32_t* counts, uint32_t from, float l, F f) {
     const uint32_t bits = __float_as_uint(l) >> 16, at = (bits & 0x7fff) - from;
@@ -710,12 +711,15 @@ __device__ __forceinline__ void order_list(Sh& sh, int n) {
   __syncthreads();
 }
 
-// Bound by the arithmetic of the weights in double precision and by the passes
-// over the row, the first from memory, the others from the L2: 2048 x 128000 bf16
-// 93 us greedy (5.6 TB/s), 272 without filters, 217 with top_k, 345 with top_p (one
-// or two passes more); a row of 32001 float32 9, 17, 21 and 25 us, a chain of
-// passes by one workgroup.  (1024 threads have 128 registers: 53 spilled, 60 bytes a
-// lane.)
+// Bound by the vector instructions of the passes over a row, where there are many
+// (the first pass from memory, the others from the L2: a row is fetched once).  2048 x
+// 128000 bf16 takes 93 us greedy (memory: 5.6 TB/s), 272 without filters, 217 with
+// top_k, 340 with top_p, in 7, 35, 17 and 37 instructions to 64 entries; at 4 cycles
+// each the issue of 35 is 235 us, and LDS conflicts keep a CU's LDS busy for 35 to 40
+// more.  Double precision is 1.1 of those 35 and 0.5 of the 37, since weights come
+// from the table of values.  A row of 32001 float32 takes 9, 17, 21 and 25 us, a
+// chain of passes by one workgroup, each weight formed in double.  (1024 threads
+// have 128 registers: 53 spilled, 60 bytes a lane.)
 template <int DT, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 4)   // (four wavefronts a SIMD: two workgroups of 512 a CU)
 sample_kernel(SampleArgs a) {
@@ -1009,7 +1013,9 @@ hipError_t launch_sample_dt(const SampleArgs& a, int64_t rows, hipStream_t s) {
   // Threads: the passes over a row want many, the steps between them few, and several rows a CU hide each other's steps.
   // us for 256 / 512 / 1024 threads, no filters and top_p: 2048 x 8192 33 / 51 / 117 and 63 / 84 / 179, x 32001 bf16 101 / 92 / 152
   // and 169 / 142 / 244; 1 x 8192 7.6 / 9.6 / 14.3 and 17.4 / 17.3 / 21.8, x 32001 18.9 / 15.5 / 17.4 and 43 / 26 / 27; 256 x 65536
-  // - / 27 / 27 and - / 54 / 50, x 128000 - / 49 / 44 and - / 87 / 73; 1024 x 128000 - / 139 / 168 and - / 190 / 249.
+  // - / 27 / 27 and - / 54 / 50.  512 / 1024 threads at 128000 bf16 entries, no filters, top_p of 0.9 and top_k of 100: 256 rows
+  // 51 / 44, 69 / 56 and 41 / 43; 320 rows 70 / 78, 88 / 105 and 54 / 70; 512 rows 77 / 83, 90 / 108 and 57 / 78; 1024 rows
+  // 139 / 163, 169 / 213 and 105 / 148.
   if (a.V <= (rows > 256 ? 8192 : 4096)) launch_k((sample_kernel<DT, 256>), grid, dim3(256), 0, s, a);
   else if (a.V > 65536 && rows <= 256) launch_k((sample_kernel<DT, 1024>), grid, dim3(1024), 0, s, a);
   else launch_k((sample_kernel<DT, 512>), grid, dim3(512), 0, s, a);

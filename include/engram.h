@@ -627,7 +627,8 @@ engram_status engram_embed(const int32_t* ids, int64_t n, const void* table, eng
  * for BF16 output.  The whole table is written, rows without an id with zeros;
  * with accumulate != 0 the sum is added to what dtable holds and rows without
  * an id are left alone (so scale = -rate takes a plain gradient step on a
- * table itself, at the cost of the rows that were read).  With ids = row
+ * table itself, at the cost of the rows that were read).  dout comes from the
+ * caller's backward pass: no call here computes it.  With ids = row
  * indices of a hashed table (engram_hash_indices plus row_offset) and dout =
  * the columns of de it is the gradient of engram_gather.
  *   dout     device [n][branches][dim], F32 or BF16, 16-byte aligned
